@@ -22,6 +22,9 @@ SITU_ACT_BF16, SITU_ACT_MXFP8, SITU_ACT_NVFP4 = 0, 1, 2
 SITU_ACT_FN_SITU, SITU_ACT_FN_SWIGLU_BIAS = 0, 1
 SITU_W_MXFP4, SITU_W_NVFP4 = 0, 1
 
+SITU_DT_BF16, SITU_DT_F16, SITU_DT_F32 = 0, 1, 2
+SITU_GROUPED_FORWARD, SITU_GROUPED_DGRAD, SITU_GROUPED_WGRAD = 0, 1, 2
+
 _lib = None
 _lock = threading.Lock()
 
@@ -42,6 +45,23 @@ class SituMoeArgs(ctypes.Structure):
             "w2_gscale", "gemm1_alpha", "gemm1_beta", "g1_alphas", "g1_alphas_up", "g2_alphas",
             "out", "scales_packed")] + [(n, ctypes.c_int32) for n in (
                 "fuse_combine", "activation", "apply_topk_in_fc1", "h1_nvfp4")] + [("tactic", ctypes.c_int32 * 2)]
+
+
+class SituGroupedGemmArgs(ctypes.Structure):
+    """Mirror of ``situ_grouped_gemm_args``."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("direction", "dtype", "out_dtype", "S", "N", "K", "E", "accumulate",
+                                              "keep_rest")] + [
+        ("a", ctypes.c_void_p), ("lda", ctypes.c_int64), ("b", ctypes.c_void_p), ("ldb", ctypes.c_int64),
+        ("offsets", ctypes.c_void_p), ("out", ctypes.c_void_p), ("ldo", ctypes.c_int64),
+        ("device_status", ctypes.c_void_p)]
+
+
+class SituFp8GemmArgs(ctypes.Structure):
+    """Mirror of ``situ_fp8_gemm_args``."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("out_dtype", "S", "N", "K", "E", "keep_rest")] + [
+        ("x_q", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("x_scale", ctypes.c_void_p), ("w_q", ctypes.c_void_p),
+        ("w_scale", ctypes.c_void_p), ("offsets", ctypes.c_void_p), ("out", ctypes.c_void_p),
+        ("ldo", ctypes.c_int64), ("device_status", ctypes.c_void_p)]
 
 
 def library_path() -> str:
@@ -96,6 +116,12 @@ def lib() -> ctypes.CDLL:
             l.situ_moe_forward_wait_test.argtypes = [ctypes.POINTER(SituMoeArgs), vp, sz, vp, i32, i32]
             l.situ_tc_peak.restype = ctypes.c_int
             l.situ_tc_peak.argtypes = [i32, i32, vp, ctypes.POINTER(ctypes.c_double), vp]
+            l.situ_moe_grouped_gemm.restype = ctypes.c_int
+            l.situ_moe_grouped_gemm.argtypes = [ctypes.POINTER(SituGroupedGemmArgs), vp]
+            l.situ_moe_quant_fp8.restype = ctypes.c_int
+            l.situ_moe_quant_fp8.argtypes = [vp, i32, i32, i32, i32, ctypes.c_int64, i32, vp, vp, vp]
+            l.situ_moe_fp8_gemm.restype = ctypes.c_int
+            l.situ_moe_fp8_gemm.argtypes = [ctypes.POINTER(SituFp8GemmArgs), vp]
             _lib = l
     return _lib
 
@@ -324,6 +350,259 @@ def situ_moe_forward_profiled(args: SituMoeArgs, workspace: torch.Tensor, events
     _check("situ_moe_forward_profiled", lib().situ_moe_forward_profiled(
         ctypes.byref(args), _p(workspace), workspace.numel() * workspace.element_size(),
         _stream(stream), arr))
+
+
+# ---------------------------------------------------------------------------
+# expert products with 16-bit and with E4M3 weights
+# ---------------------------------------------------------------------------
+
+_DTYPES = {torch.bfloat16: SITU_DT_BF16, torch.float16: SITU_DT_F16, torch.float32: SITU_DT_F32}
+_E4M3 = (torch.uint8, torch.float8_e4m3fn)
+_gemm_status = {}
+
+
+def _status(device: torch.device) -> torch.Tensor:
+    """The status word that this process's products on ``device`` share."""
+    t = _gemm_status.get(device)
+    if t is None:
+        with torch.cuda.device(device):
+            t = torch.zeros(1, dtype=torch.int32, device=device)
+            torch.cuda.synchronize()   # once per device: zero before any stream uses it
+        t = _gemm_status.setdefault(device, t)
+    return t
+
+
+def situ_moe_gemm_status(device=None, reset: bool = False) -> int:
+    """0, or the code of the first bounded wait that a product
+    (situ_moe_grouped_gemm*, situ_moe_fp8*_gemm) on ``device`` gave up; until
+    it is reset the products there do no work.  Waits for the device."""
+    device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    torch.cuda.synchronize(device)
+    t = _status(device)
+    code = int(t.item())
+    if reset and code:
+        t.zero_()
+        torch.cuda.synchronize(device)
+    return code
+
+
+def _rows(t: torch.Tensor, what: str, unit: int) -> torch.Tensor:
+    """``t`` as rows that the kernels can read in place: columns packed, rows
+    a multiple of ``unit`` elements apart and 16-byte aligned; else a copy."""
+    if t.dim() != 2:
+        raise ValueError(f"{what} must be 2-dimensional")
+    if t.shape[0] > 1 and (t.stride(0) < t.shape[1] or t.stride(0) % unit) or \
+            (t.shape[1] > 1 and t.stride(1) != 1) or t.data_ptr() % 16:
+        return t.clone(memory_format=torch.contiguous_format)
+    return t
+
+
+def _pitch(t: torch.Tensor) -> int:
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _packed(t: torch.Tensor) -> torch.Tensor:
+    """``t`` contiguous and 16-byte aligned."""
+    t = t.contiguous()
+    return t.clone() if t.data_ptr() % 16 else t
+
+
+def _groups(offsets: torch.Tensor, dev) -> torch.Tensor:
+    if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.shape[0] < 2:
+        raise TypeError("offsets must be int32 [E + 1]")
+    _same_device(dev, offsets)
+    return offsets.contiguous()
+
+
+def _same_device(dev, *ts) -> None:
+    if dev.type != "cuda":
+        raise ValueError("the operands must be CUDA tensors")
+    for t in ts:
+        if t.device != dev:
+            raise ValueError(f"operands on {t.device} and {dev}")
+
+
+def _result(out, shape, dtype, dev, what: str, unit: int) -> torch.Tensor:
+    """The tensor to write: a new one, or ``out`` after its checks."""
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    if tuple(out.shape) != tuple(shape) or out.dtype != dtype or out.device != dev:
+        raise ValueError(f"{what}: needs {dtype} {tuple(shape)} on {dev}")
+    packed = out.is_contiguous() if len(shape) != 2 else \
+        (shape[1] <= 1 or out.stride(1) == 1) and (shape[0] <= 1 or (out.stride(0) >= shape[1] and out.stride(0) % unit == 0))
+    if not packed or out.data_ptr() % 16:
+        raise ValueError(f"{what}: needs 16-byte aligned rows, packed along the last dimension")
+    return out
+
+
+def _grouped(direction, a, b, offsets, N, K, out, out_shape, out_dtype, accumulate, zero_rest, stream):
+    dev = a.device
+    _same_device(dev, b)
+    if a.dtype not in (torch.bfloat16, torch.float16) or b.dtype != a.dtype:
+        raise TypeError("the operands must be both bf16 or both f16")
+    if out_dtype is None:
+        out_dtype = out.dtype if out is not None else a.dtype
+    if out_dtype not in (a.dtype, torch.float32):
+        raise TypeError("the output must be of the operands' type or fp32")
+    offsets = _groups(offsets, dev)
+    wgrad = direction == SITU_GROUPED_WGRAD
+    out = _result(out, out_shape, out_dtype, dev, "out", 8)
+    a = _rows(a, "rows", 8)
+    b = _rows(b, "rows", 8) if wgrad else _packed(b)
+    with torch.cuda.device(dev):
+        args = SituGroupedGemmArgs(
+            direction, _DTYPES[a.dtype], _DTYPES[out_dtype], a.shape[0], N, K, offsets.shape[0] - 1, int(accumulate),
+            0 if wgrad or zero_rest else 1, a.data_ptr(), _pitch(a), b.data_ptr(), _pitch(b) if wgrad else 0,
+            offsets.data_ptr(), out.data_ptr(), 0 if wgrad else _pitch(out), _status(dev).data_ptr())
+        _check("situ_moe_grouped_gemm", lib().situ_moe_grouped_gemm(ctypes.byref(args), _stream(stream)))
+    return out
+
+
+def _experts(w: torch.Tensor, offsets: torch.Tensor):
+    """w [E, N, K] (or one expert's [N, K]) against its offsets."""
+    if w.dim() == 2:
+        w = w.unsqueeze(0)
+    if w.dim() != 3 or w.shape[0] != offsets.shape[0] - 1:
+        raise ValueError("weights must be [E, N, K] with offsets [E + 1]")
+    return w
+
+
+def situ_moe_grouped_gemm(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, *, out=None, out_dtype=None,
+                          zero_rest: bool = True, stream=None) -> torch.Tensor:
+    """y[r] = x[r] @ w[e].T for the rows r of each expert e: x [S, K] sorted by
+    expert, w [E, N, K] of the same 16-bit type, offsets int32 [E + 1] (as
+    situ_moe_permute returns them).  Rows of no expert give zeros, or are left
+    unwritten with ``zero_rest=False``."""
+    w = _experts(w, offsets)
+    if x.dim() != 2 or x.shape[1] != w.shape[2]:
+        raise ValueError("x must be [S, K]")
+    return _grouped(SITU_GROUPED_FORWARD, x, w, offsets, w.shape[1], w.shape[2], out, (x.shape[0], w.shape[1]),
+                    out_dtype, False, zero_rest, stream)
+
+
+def situ_moe_grouped_gemm_dgrad(dy: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, *, out=None,
+                                out_dtype=None, zero_rest: bool = True, stream=None) -> torch.Tensor:
+    """The gradient of situ_moe_grouped_gemm's x: dx[r] = dy[r] @ w[e], [S, K]."""
+    w = _experts(w, offsets)
+    if dy.dim() != 2 or dy.shape[1] != w.shape[1]:
+        raise ValueError("dy must be [S, N]")
+    return _grouped(SITU_GROUPED_DGRAD, dy, w, offsets, w.shape[1], w.shape[2], out, (dy.shape[0], w.shape[2]),
+                    out_dtype, False, zero_rest, stream)
+
+
+def situ_moe_grouped_gemm_wgrad(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor, *, out=None,
+                                out_dtype=None, accumulate: bool = False, stream=None) -> torch.Tensor:
+    """The gradient of its w: dw[e] = dy[rows of e].T @ x[rows of e], [E, N, K];
+    zeros for an expert without rows.  ``accumulate`` adds to ``out``."""
+    if dy.dim() != 2 or x.dim() != 2 or dy.shape[0] != x.shape[0]:
+        raise ValueError("dy must be [S, N] and x [S, K]")
+    if accumulate and out is None:
+        raise ValueError("accumulate adds to out: none given")
+    return _grouped(SITU_GROUPED_WGRAD, dy, x, offsets, dy.shape[1], x.shape[1], out,
+                    (offsets.shape[0] - 1, dy.shape[1], x.shape[1]), out_dtype, accumulate, True, stream)
+
+
+class _GroupedLinear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, offsets):
+        ctx.save_for_backward(x, w, offsets)
+        return situ_moe_grouped_gemm(x, w, offsets)
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, w, offsets = ctx.saved_tensors
+        dx = situ_moe_grouped_gemm_dgrad(dy, w, offsets) if ctx.needs_input_grad[0] else None
+        dw = situ_moe_grouped_gemm_wgrad(dy, x, offsets) if ctx.needs_input_grad[1] else None
+        return dx, dw, None
+
+
+def grouped_linear(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor) -> torch.Tensor:
+    """situ_moe_grouped_gemm for training: differentiable in x [S, K] and
+    w [E, N, K]."""
+    if w.dim() != 3:
+        raise ValueError("w must be [E, N, K]")
+    return _GroupedLinear.apply(x, w, offsets)
+
+
+def situ_moe_quant_fp8(x: torch.Tensor, block_rows: int = 1, *, out=None, stream=None):
+    """bf16, f16 or fp32 [R, K] or [E, R, K] -> (E4M3 uint8 of x's shape, fp32
+    scales per block of 128): block_rows 1, a scale per row and 128 columns
+    (activations); 128, one per 128 x 128 block (weights)."""
+    if x.dtype not in _DTYPES:
+        raise TypeError("x must be bf16, f16 or fp32")
+    if x.dim() not in (2, 3):
+        raise ValueError("x must be [R, K] or [E, R, K]")
+    if block_rows not in (1, 128):
+        raise ValueError("block_rows must be 1 or 128")
+    _same_device(x.device)
+    x = _rows(x, "x", 4 if x.dtype == torch.float32 else 8) if x.dim() == 2 else _packed(x)
+    R, K = x.shape[-2:]
+    E = x.shape[0] if x.dim() == 3 else 1
+    dims = (*x.shape[:-2], -(-R // block_rows), -(-K // 128))
+    if out is None:
+        q = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
+        scale = torch.empty(dims, dtype=torch.float32, device=x.device)
+    else:
+        q, scale = out
+        for t, shape, dts, what in ((q, x.shape, _E4M3, "q"), (scale, dims, (torch.float32,), "scale")):
+            if tuple(t.shape) != tuple(shape) or t.dtype not in dts or t.device != x.device or not t.is_contiguous():
+                raise ValueError(f"{what}: needs a contiguous {dts[0]} tensor {tuple(shape)} on {x.device}")
+    with torch.cuda.device(x.device):
+        _check("situ_moe_quant_fp8", lib().situ_moe_quant_fp8(
+            _p(x), _DTYPES[x.dtype], E, R, K, _pitch(x) if x.dim() == 2 else K, block_rows, _p(q), _p(scale),
+            _stream(stream)))
+    return q, scale
+
+
+def _fp8_gemm(x_q, x_scale, w_q, w_scale, offsets, out, out_dtype, zero_rest, stream):
+    dev = x_q.device
+    _same_device(dev, x_scale, w_q, w_scale)
+    if x_q.dtype not in _E4M3 or w_q.dtype not in _E4M3:
+        raise TypeError("x_q and w_q must hold E4M3 codes (uint8 or float8_e4m3fn)")
+    if x_scale.dtype != torch.float32 or w_scale.dtype != torch.float32:
+        raise TypeError("the scales must be fp32")
+    if out_dtype is None:
+        out_dtype = out.dtype if out is not None else torch.bfloat16
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("the output must be bf16 or fp32")
+    E, N, K = w_q.shape
+    S, nkb = x_q.shape[0], -(-K // 128)
+    if x_q.dim() != 2 or x_q.shape[1] != K:
+        raise ValueError("x_q must be [S, K]")
+    if tuple(x_scale.shape) != (S, nkb) or tuple(w_scale.shape) != (E, -(-N // 128), nkb):
+        raise ValueError(f"needs x_scale {(S, nkb)} and w_scale {(E, -(-N // 128), nkb)}")
+    out = _result(out, (S, N), out_dtype, dev, "out", 8)
+    x_q, w_q = _rows(x_q, "x_q", 16), _packed(w_q)
+    x_scale, w_scale = x_scale.contiguous(), w_scale.contiguous()
+    with torch.cuda.device(dev):
+        args = SituFp8GemmArgs(
+            _DTYPES[out_dtype], S, N, K, E, 0 if zero_rest else 1, x_q.data_ptr(), _pitch(x_q), x_scale.data_ptr(),
+            w_q.data_ptr(), w_scale.data_ptr(), None if offsets is None else offsets.data_ptr(), out.data_ptr(),
+            _pitch(out), _status(dev).data_ptr())
+        _check("situ_moe_fp8_gemm", lib().situ_moe_fp8_gemm(ctypes.byref(args), _stream(stream)))
+    return out
+
+
+def situ_moe_fp8_gemm(x_q: torch.Tensor, x_scale: torch.Tensor, w_q: torch.Tensor, w_scale: torch.Tensor, *,
+                      out=None, out_dtype=None, stream=None) -> torch.Tensor:
+    """x @ w.T of operands quantised by situ_moe_quant_fp8: x_q [S, K] with a
+    scale per row and 128 columns, w_q [N, K] with one per 128 x 128 block;
+    bf16 (default) or fp32 [S, N]."""
+    if w_q.dim() != 2 or w_scale.dim() != 2:
+        raise ValueError("w_q must be [N, K] and w_scale [ceil(N/128), ceil(K/128)]")
+    return _fp8_gemm(x_q, x_scale, w_q.unsqueeze(0), w_scale.unsqueeze(0), None, out, out_dtype, True, stream)
+
+
+def situ_moe_fp8_grouped_gemm(x_q: torch.Tensor, x_scale: torch.Tensor, w_q: torch.Tensor, w_scale: torch.Tensor,
+                              offsets: torch.Tensor, *, out=None, out_dtype=None, zero_rest: bool = True,
+                              stream=None) -> torch.Tensor:
+    """The same per expert: rows of x_q sorted by expert, w_q [E, N, K],
+    offsets int32 [E + 1].  Rows of no expert give zeros, or are left
+    unwritten with ``zero_rest=False``."""
+    offsets = _groups(offsets, x_q.device)
+    w_q = _experts(w_q, offsets)
+    w_scale = w_scale.unsqueeze(0) if w_scale.dim() == 2 else w_scale
+    return _fp8_gemm(x_q, x_scale, w_q, w_scale, offsets, out, out_dtype, zero_rest, stream)
 
 
 class Layer:

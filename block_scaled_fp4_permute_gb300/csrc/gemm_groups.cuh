@@ -1,0 +1,365 @@
+// gemm_groups.cuh -- what the products over ragged expert groups share: the
+// groups' row ranges and their token tiles, the tile walk, the CTA-pair forms
+// of the tcgen05 and mbarrier instructions, and the tensor-map encoders.
+//
+// Rows are sorted by expert: group e holds rows [offsets[e], offsets[e + 1]).
+// The offsets live on the device (the permute writes them), so the host never
+// sees them: grids are sized for the GPU, and every CTA scans the groups'
+// tile counts into shared memory once and walks its share of the tiles.
+// Offsets are clamped to [0, S] and to ascending order before use, so that no
+// content of the array can address outside the operands.
+#pragma once
+#include "situ_internal.h"
+#include "tc_common.cuh"
+
+namespace situ {
+namespace gg {
+
+using namespace tc;
+
+constexpr int kMaxGroups = 1024;   // tile prefix in shared memory, 4 KB
+
+__device__ __forceinline__ int2 group_rows(const int32_t* off, int e, int S) {
+  if (off == nullptr) return make_int2(0, S);   // one dense group
+  const int b = min(max(__ldg(off + e), 0), S);
+  return make_int2(b, min(max(__ldg(off + e + 1), b), S) - b);   // (first row, rows)
+}
+
+// tp[e] = token tiles of the groups before e, tp[E] = all of them (E <=
+// kMaxGroups).  Called by all `threads` threads of the block; ends synced.
+__device__ __forceinline__ void scan_tiles(const int32_t* off, int E, int S, int tile, int* tp, int threads) {
+  __shared__ int warp_sum[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (E + threads - 1) / threads;
+  int cnt[(kMaxGroups + 255) / 256], sum = 0;   // blocks here have at least 256 threads
+#pragma unroll
+  for (int j = 0; j < (kMaxGroups + 255) / 256; ++j) {
+    const int e = tid * per + j;
+    cnt[j] = (j < per && e < E) ? (group_rows(off, e, S).y + tile - 1) / tile : 0;
+    sum += cnt[j];
+  }
+  int inc = sum;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, inc, d);
+    if (lane >= d) inc += o;
+  }
+  if (lane == 31) warp_sum[warp] = inc;
+  __syncthreads();
+  int base = 0;
+  for (int w = 0; w < warp; ++w) base += warp_sum[w];
+  int run = base + inc - sum;
+#pragma unroll
+  for (int j = 0; j < (kMaxGroups + 255) / 256; ++j) {
+    const int e = tid * per + j;
+    if (j < per && e < E) tp[e] = run;
+    run += cnt[j];
+  }
+  if (tid == threads - 1) tp[E] = base + inc;
+  __syncthreads();
+}
+
+// the group of token tile v: the largest e with tp[e] <= v (v < tp[E])
+__device__ __forceinline__ int find_group(const int* tp, int E, int v) {
+  int lo = 0, hi = E;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (tp[mid] <= v) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// ---------------------------------------------------------------------------
+// CTA pairs
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// the shared::cluster address of `a` in the pair's even CTA
+__device__ __forceinline__ uint32_t leader_addr(uint32_t a) { return a & 0xFEFFFFFFu; }
+// one arrival on a barrier of CTA `rank` of the cluster
+__device__ __forceinline__ void mbar_arrive_at(uint32_t a, uint32_t rank) {
+  asm volatile(
+      "{\n .reg .b32 r;\n mapa.shared::cluster.u32 r, %0, %1;\n"
+      " mbarrier.arrive.release.cluster.shared::cluster.b64 _, [r];\n}" ::"r"(a),
+      "r"(rank)
+      : "memory");
+}
+
+template <int CG>
+__device__ __forceinline__ void tmem_alloc(uint32_t dst, uint32_t cols) {
+  if (CG == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "r"(cols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "r"(cols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+}
+template <int CG>
+__device__ __forceinline__ void tmem_free(uint32_t tmem, uint32_t cols) {
+  if (CG == 1)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols) : "memory");
+  else
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols) : "memory");
+}
+// one arrival on `bar` of every CTA of the group once the MMAs issued so far are done
+template <int CG>
+__device__ __forceinline__ void commit(uint32_t bar) {
+  if (CG == 1) {
+    mma_commit(bar);
+  } else {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
+  }
+}
+template <int CG>
+__device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  if (CG == 1)
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  if (CG == 1)
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+// Tile copies.  In a pair both CTAs' copies complete on the even CTA's
+// barrier (it alone issues the MMAs).
+template <int CG>
+__device__ __forceinline__ void copy_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  if (CG == 1)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+        "[%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(leader_addr(bar))
+        : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void copy_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  if (CG == 1)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+            dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
+        "%4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(leader_addr(bar))
+        : "memory");
+}
+// four rows named by index (a map whose box is one row high); an index past
+// the map's last row gives zeros
+template <int CG>
+__device__ __forceinline__ void copy_rows4(uint32_t dst, const CUtensorMap* map, int x, int r0, int r1, int r2, int r3,
+                                           uint32_t bar) {
+  if (CG == 1)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
+        "%4, %5, %6}], [%7];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], "
+        "[%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(leader_addr(bar))
+        : "memory");
+}
+
+// tcgen05 descriptor of an operand whose M or N elements are contiguous
+// (MN-major, 128-byte swizzle): chunks of 64 elements x `rows` contraction
+// rows of 128 bytes, `chunk` bytes apart; 8-row groups are 1,024 bytes apart.
+__device__ __forceinline__ uint64_t sdesc_mn(uint32_t a, uint32_t chunk) {
+  uint64_t d = 0;
+  d |= (uint64_t)((a >> 4) & 0x3FFFu);
+  d |= (uint64_t)(chunk >> 4) << 16;   // leading byte offset: the next 64 elements
+  d |= (uint64_t)(1024u >> 4) << 32;   // stride byte offset: the next 8 contraction rows
+  d |= (uint64_t)1u << 46;
+  d |= (uint64_t)2u << 61;
+  return d;
+}
+
+// A place in a ring of N and the parity of its current round.
+template <int N>
+struct Ring {
+  int s = 0;
+  uint32_t ph = 0;
+  int used = 0;   // steps taken, up to N
+  __device__ __forceinline__ void next() {
+    if (used < N) ++used;
+    if (++s == N) {
+      s = 0;
+      ph ^= 1;
+    }
+  }
+};
+
+// Bounded wait (kWaitNs) for what this CTA itself put in flight, on the way
+// out after a failure; unlike mbar_wait it does not give up on another CTA's
+// error.
+__device__ __forceinline__ void drain_wait(uint32_t a, uint32_t parity) {
+  const unsigned long long t0 = globaltimer();
+  while (!mbar_try(a, parity))
+    if (globaltimer() - t0 > kWaitNs) return;
+}
+
+// barrier `id` over `threads` threads; the AND of every thread's v
+__device__ __forceinline__ bool bar_and(int id, int threads, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %3, 0;\n barrier.cta.red.and.pred q, %1, %2, p;\n selp.u32 %0, 1, 0, q;\n}"
+      : "=r"(r)
+      : "r"(id), "r"(threads), "r"((uint32_t)v)
+      : "memory");
+  return r != 0;
+}
+
+// tcgen05.ld of 32 columns, without the wait
+__device__ __forceinline__ void tmem_ld32_nowait(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld16_nowait(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+// waits for the loads above and ties their registers to the wait, so that no
+// use of them moves ahead of it
+template <int N>
+__device__ __forceinline__ void tmem_ld_wait(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+// zeros to rows [from, to) of a row-major output (width and pitch in bytes,
+// multiples of 16), spread over `n` threads of which this is number `t`
+__device__ __forceinline__ void zero_rows(uint8_t* out, long from, long to, size_t width, size_t pitch, long t, long n) {
+  const long per = (long)(width / 16);
+  for (long i = t; i < (to - from) * per; i += n)
+    *reinterpret_cast<uint4*>(out + (size_t)(from + i / per) * pitch + (size_t)(i % per) * 16) = make_uint4(0, 0, 0, 0);
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+
+// The map encoder needs a current context, which a host thread that has made
+// no runtime call yet (autograd's backward threads) does not have: binds the
+// thread to its device's primary context, once.
+inline bool bind_thread() {
+  static thread_local bool bound = false;
+  if (!bound) {
+    int dev = 0;
+    bound = cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess;
+  }
+  return bound;
+}
+
+// dims[i] elements, stride[i - 1] bytes between elements of dims[i] (i >= 1)
+inline bool make_map_nd(CUtensorMap* m, CUtensorMapDataType dt, const void* base, int nd, const uint64_t* dims,
+                        const uint64_t* strides, const uint32_t* box) {
+  PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+  if (!fn || !bind_thread()) return false;
+  const cuuint32_t estr[3] = {1, 1, 1};
+  cuuint64_t d[3], st[2];
+  cuuint32_t b[3];
+  for (int i = 0; i < nd; ++i) {
+    d[i] = dims[i];
+    b[i] = box[i];
+    if (i > 0) st[i - 1] = strides[i - 1];
+  }
+  return fn(m, dt, (cuuint32_t)nd, const_cast<void*>(base), d, st, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// SMs of the current device (looked up once per device)
+inline int sm_count() {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  int n = dev < 64 ? known[dev].load() : 0;
+  if (n == 0) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    if (dev < 64) known[dev].store(n);
+  }
+  return n;
+}
+
+// Raises a kernel's dynamic shared memory limit once per device, then
+// launches it in clusters of `cluster` CTAs.
+template <class Kernel, class... Args>
+cudaError_t launch_cluster(Kernel k, std::atomic<uint64_t>* raised, int cluster, int grid, int threads, size_t smem,
+                           cudaStream_t st, Args&&... args) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (bit == 0 || !(raised->load() & bit)) {
+    std::lock_guard<std::mutex> lock(attr_mutex());
+    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    raised->fetch_or(bit);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)cluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, k, args...);
+}
+
+}  // namespace gg
+}  // namespace situ

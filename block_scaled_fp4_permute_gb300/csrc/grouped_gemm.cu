@@ -1,0 +1,478 @@
+// grouped_gemm.cu -- 16-bit products over ragged expert groups and their
+// gradients on tcgen05 (kind::f16, fp32 accumulation in TMEM).
+//
+// Rows r of x [S, K] are sorted by expert, e(r) is the group that holds r:
+//   forward   y[r, n]     = sum_k  x[r, k]  w[e(r), n, k]
+//   dgrad     dx[r, k]    = sum_n  dy[r, n] w[e(r), n, k]
+//   wgrad     dw[e, n, k] = sum_{r in e} dy[r, n] x[r, k]
+// The weights take the MMA's M side (128 per CTA) in all three and the
+// tokens its N side (dw: n and k), so that a ragged group's last tile costs
+// an N rounded up to 16, not a whole tile of rows, and a group of few tokens
+// streams its weights once.  Operands whose contraction index is contiguous
+// are K-major (x, w in the forward, dy in dgrad), the others MN-major (w in
+// dgrad; dy and x in wgrad), both as 128-byte-swizzled TMA tiles.
+//
+// Per CTA: warp 0 copies stages of 64 contraction elements into a ring,
+// warp 1 issues the MMAs into two TMEM accumulators in turn, warps 4..7 read
+// the accumulator of the previous tile and store it meanwhile.  CTAs are
+// persistent and walk the tiles with a fixed stride.
+//
+// The contraction's end: k and n past the weight's extent read as zeros (the
+// maps end there; w is a 3D map, so that rows past n = N do not run into the
+// next expert).  In wgrad the contraction runs over a group's rows and ends
+// anywhere: a last stage of fewer than 64 rows is fetched row by row (gather
+// of four), with the rows past the group's end named out of bounds, so that
+// the MMA sees zeros in both operands there (a zero in one of them would not
+// do: the neighbour's rows may hold infinities).
+#include "../../include/situ_moe.h"
+#include "gemm_groups.cuh"
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+namespace situ {
+
+using namespace gg;
+
+namespace {
+
+constexpr int kFwd = SITU_GROUPED_FORWARD, kDgrad = SITU_GROUPED_DGRAD, kWgrad = SITU_GROUPED_WGRAD;
+constexpr int kBK = 64;             // contraction elements per stage
+constexpr int kABytes = 128 * 128;  // 128 weights (or n) x 64 elements
+constexpr int kThreads = 256;
+constexpr int kEpiWarp = 4;         // first epilogue warp
+
+struct GgParams {
+  const int32_t* offsets;
+  int E, S;
+  int M, L, Ncol;   // M side extent; contraction (fwd, dgrad); N side extent (wgrad)
+  int n_mt, n_nt;   // M tiles; N tiles (wgrad)
+  void* out;
+  long ld_out;      // elements
+  int bf16, out_f32, accumulate, zero_rest;
+  int* err;
+};
+
+template <int CG, int TN>
+struct Cfg {
+  static constexpr int kTNB = TN / CG;                // N-side rows of one CTA
+  static constexpr int kBBytes = kTNB * 128;
+  static constexpr int kStageBytes = kABytes + kBBytes;
+  static constexpr int kMaxBytes = 232448 - 1024 - 4 * (kMaxGroups + 1) - 512;
+  static constexpr int kStages = kMaxBytes / kStageBytes;
+  static constexpr int kOffB = kStages * kABytes;
+  static constexpr int kOffTp = kOffB + kStages * kBBytes;
+  static constexpr int kOffBar = (kOffTp + 4 * (kMaxGroups + 1) + 15) / 16 * 16;
+  static constexpr int kNumBars = 2 * kStages + 5;    // full, empty; acc_full[2], acc_empty[2]; drain
+  static constexpr int kOffTm = kOffBar + 8 * kNumBars;
+  static constexpr int kSmem = kOffTm + 16 + 1024;
+  static constexpr int kTmemCols = 2 * TN;
+  static_assert(kSmem <= 232448 && kTmemCols <= 512 && kTmemCols >= 32, "shared memory and TMEM");
+};
+
+__device__ __forceinline__ uint16_t to_16(float v, int bf16) {
+  if (bf16) return __bfloat16_as_ushort(__float2bfloat16_rn(v));
+  return __half_as_ushort(__float2half_rn(v));
+}
+__device__ __forceinline__ uint32_t to_16x2(float a, float b, int bf16) {
+  return bf16 ? f32x2_to_bf16x2(a, b) : pack_f16x2(a, b);
+}
+__device__ __forceinline__ float from_16(uint32_t v, int bf16) {
+  return bf16 ? __uint_as_float(v << 16) : f16_to_f32(v);
+}
+
+// What one tile is: the group's rows, the tile's corner and its N extent.
+struct Tile {
+  int e, row0, rows;   // group and its rows
+  int m0, c0, cols;    // M-side start, N-side start (row in the group; k in wgrad) and extent
+  int nk;              // stages
+};
+
+template <int CG, int MODE, int TN>
+__device__ __forceinline__ Tile tile_of(const GgParams& p, const int* tp, int idx) {
+  Tile t;
+  int mt;
+  if (MODE == kWgrad) {
+    const int per = p.n_mt * p.n_nt;
+    t.e = idx / per;
+    const int r = idx - t.e * per;
+    mt = r / p.n_nt;
+    t.c0 = (r - mt * p.n_nt) * TN;
+    const int2 g = group_rows(p.offsets, t.e, p.S);
+    t.row0 = g.x;
+    t.rows = g.y;
+    t.cols = min(TN, p.Ncol - t.c0);
+    t.nk = (t.rows + kBK - 1) / kBK;
+  } else {
+    t.e = find_group(tp, p.E, idx / p.n_mt);
+    const int r = idx - tp[t.e] * p.n_mt, tt = tp[t.e + 1] - tp[t.e];
+    mt = r / tt;   // a group's token tiles run side by side: they read the same weights
+    t.c0 = (r - mt * tt) * TN;
+    const int2 g = group_rows(p.offsets, t.e, p.S);
+    t.row0 = g.x;
+    t.rows = g.y;
+    t.cols = min(TN, t.rows - t.c0);
+    t.nk = (p.L + kBK - 1) / kBK;
+  }
+  t.m0 = mt * 128 * CG;
+  return t;
+}
+
+template <int CG, int MODE, int TN>
+__global__ void __launch_bounds__(kThreads, 1)
+gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
+          const __grid_constant__ CUtensorMap mapA1, const __grid_constant__ CUtensorMap mapB1, const GgParams p) {
+  using C = Cfg<CG, TN>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = CG == 2 ? cluster_rank() : 0;
+  const uint32_t sbase = saddr(smem);
+  int* tp = reinterpret_cast<int*>(smem + C::kOffTp);
+  const uint32_t bar0 = sbase + C::kOffBar;
+  auto full = [&](int s) { return bar0 + 8 * s; };
+  auto empty = [&](int s) { return bar0 + 8 * (C::kStages + s); };
+  auto acc_full = [&](int b) { return bar0 + 8 * (2 * C::kStages + b); };
+  auto acc_empty = [&](int b) { return bar0 + 8 * (2 * C::kStages + 2 + b); };
+  const uint32_t drain = bar0 + 8 * (2 * C::kStages + 4);
+  uint32_t* tm_holder = reinterpret_cast<uint32_t*>(smem + C::kOffTm);
+
+  if (tid == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(acc_full(b), 1);
+      mbar_init(acc_empty(b), 4 * CG);
+    }
+    mbar_init(drain, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) tmem_alloc<CG>(saddr(tm_holder), C::kTmemCols);
+  if (MODE != kWgrad) scan_tiles(p.offsets, p.E, p.S, TN, tp, kThreads);
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  if (CG == 2) cluster_sync();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const uint32_t tmem = *tm_holder;
+
+  // an earlier launch that gave up a wait leaves its code in *err: no work then
+  int total = MODE == kWgrad ? p.E * p.n_mt * p.n_nt : tp[p.E] * p.n_mt;
+  if (*reinterpret_cast<volatile int*>(p.err) != 0) total = 0;
+  const int first = blockIdx.x / CG, stride = gridDim.x / CG;
+
+  if (warp == 0) {
+    // ---------------- copies ----------------
+    const bool leader = elect_one();
+    Ring<C::kStages> r;
+    bool ok = true;
+    for (int idx = first; idx < total && ok; idx += stride) {
+      const Tile t = tile_of<CG, MODE, TN>(p, tp, idx);
+      const int nact = (t.cols + 16 * CG - 1) / (16 * CG) * (16 * CG);   // the MMA's N
+      const int half = nact / CG;                                       // this CTA's part of it
+      const int ma = t.m0 + 128 * (int)rank, cb = t.c0 + half * (int)rank;
+      const int nchunk = (half + 63) / 64;
+      for (int kk = 0; kk < t.nk; ++kk, r.next()) {
+        const int s = r.s;
+        if (r.used == C::kStages && !mbar_wait_warp(empty(s), r.ph ^ 1, p.err, 71)) {
+          ok = false;
+          break;
+        }
+        if (leader) {
+          const uint32_t a = sbase + s * kABytes, b = sbase + C::kOffB + s * C::kBBytes;
+          const int k0 = kk * kBK;
+          if (MODE != kWgrad) {
+            if (CG == 1 || rank == 0) mbar_expect_tx(full(s), CG * C::kStageBytes);
+            if (MODE == kFwd) {
+              copy_3d<CG>(a, &mapA, k0, ma, t.e, full(s));
+            } else {   // w as [n, k], k contiguous: two chunks of 64 k
+              copy_3d<CG>(a, &mapA, ma, k0, t.e, full(s));
+              copy_3d<CG>(a + kABytes / 2, &mapA, ma + 64, k0, t.e, full(s));
+            }
+            copy_2d<CG>(b, &mapB, k0, t.row0 + cb, full(s));
+          } else {
+            const int rows = t.rows - k0;
+            if (rows >= kBK) {
+              if (CG == 1 || rank == 0) mbar_expect_tx(full(s), CG * (kABytes + nchunk * 8192));
+              for (int c = 0; c < 2; ++c) copy_2d<CG>(a + 8192 * c, &mapA, ma + 64 * c, t.row0 + k0, full(s));
+              for (int c = 0; c < nchunk; ++c) copy_2d<CG>(b + 8192 * c, &mapB, cb + 64 * c, t.row0 + k0, full(s));
+            } else {
+              const int r16 = (rows + 15) & ~15;
+              if (CG == 1 || rank == 0) mbar_expect_tx(full(s), CG * (2 + nchunk) * r16 * 128);
+              for (int i = 0; i < r16; i += 4) {
+                int q[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) q[j] = i + j < rows ? t.row0 + k0 + i + j : p.S;   // S: out of bounds, zeros
+                for (int c = 0; c < 2; ++c)
+                  copy_rows4<CG>(a + 8192 * c + i * 128, &mapA1, ma + 64 * c, q[0], q[1], q[2], q[3], full(s));
+                for (int c = 0; c < nchunk; ++c)
+                  copy_rows4<CG>(b + 8192 * c + i * 128, &mapB1, cb + 64 * c, q[0], q[1], q[2], q[3], full(s));
+              }
+            }
+          }
+        }
+        __syncwarp();
+      }
+    }
+    if (ok) {   // the last arrivals on this CTA's barriers, before it may leave
+      for (int j = 0; j < r.used; ++j) mbar_wait_warp(empty(j), j < r.s ? r.ph : r.ph ^ 1, p.err, 72);
+    } else if (rank == 0) {   // copies in flight
+      for (int j = 0; j < r.used; ++j) drain_wait(full(j), j < r.s ? r.ph : r.ph ^ 1);
+    } else {
+      const unsigned long long t0 = globaltimer();   // they complete on the other CTA's barriers
+      while (globaltimer() - t0 < 2000000ull) {
+      }
+    }
+  } else if (warp == 1 && rank == 0) {
+    // ---------------- MMAs ----------------
+    const bool leader = elect_one();
+    Ring<C::kStages> r;
+    Ring<2> ab;
+    bool ok = true;
+    const uint32_t id0 = (1u << 4) | (p.bf16 ? (1u << 7) | (1u << 10) : 0u) | (MODE != kFwd ? 1u << 15 : 0u) |
+                         (MODE == kWgrad ? 1u << 16 : 0u) | ((uint32_t)(128 * CG >> 4) << 24);
+    for (int idx = first; idx < total && ok; idx += stride) {
+      const Tile t = tile_of<CG, MODE, TN>(p, tp, idx);
+      if (t.nk == 0) continue;
+      const int nact = (t.cols + 16 * CG - 1) / (16 * CG) * (16 * CG);
+      const uint32_t idesc = id0 | ((uint32_t)(nact >> 3) << 17);
+      const int buf = ab.s;
+      if (ab.used == 2 && !mbar_wait_warp(acc_empty(buf), ab.ph ^ 1, p.err, 73)) {
+        ok = false;
+        break;
+      }
+      ab.next();
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      const int len = MODE == kWgrad ? t.rows : p.L;
+      for (int kk = 0; kk < t.nk; ++kk, r.next()) {
+        const int s = r.s;
+        if (!mbar_wait_warp(full(s), r.ph, p.err, 74)) {
+          ok = false;
+          break;
+        }
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        if (leader) {
+          const uint32_t a = sbase + s * kABytes, b = sbase + C::kOffB + s * C::kBBytes;
+          const uint64_t ad = MODE == kFwd ? sdesc(a) : sdesc_mn(a, 8192);
+          const uint64_t bd = MODE != kWgrad ? sdesc(b) : sdesc_mn(b, 8192);
+          const int steps = min(4, (len - kk * kBK + 15) >> 4);
+          // per 16 contraction elements: 32 bytes along a K-major row, 16 rows of 128 bytes else
+          for (int k = 0; k < steps; ++k)
+            mma_f16<CG>(tmem + buf * TN, ad + (MODE == kFwd ? 2 : 128) * k, bd + (MODE != kWgrad ? 2 : 128) * k, idesc,
+                        (kk | k) != 0);
+          commit<CG>(empty(s));
+        }
+        __syncwarp();
+      }
+      if (ok) {
+        if (leader) commit<CG>(acc_full(buf));
+        __syncwarp();
+      }
+    }
+    if (!ok) {   // MMAs in flight
+      if (leader) commit<CG>(drain);
+      __syncwarp();
+      drain_wait(drain, 0);
+    }
+  } else if (warp >= kEpiWarp) {
+    // ---------------- epilogue ----------------
+    const int q = warp - kEpiWarp;
+    Ring<2> ab;
+    for (int idx = first; idx < total; idx += stride) {
+      const Tile t = tile_of<CG, MODE, TN>(p, tp, idx);
+      const int m = t.m0 + 128 * (int)rank + 32 * q + lane;
+      const bool vm = m < p.M;
+      if (MODE == kWgrad && t.nk == 0) {   // an expert without rows
+        if (!p.accumulate && vm) {
+          const size_t at = ((size_t)t.e * p.M + m) * (size_t)p.ld_out + t.c0;
+          uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(p.out) + at * (p.out_f32 ? 4 : 2));
+          for (int c = 0; c < t.cols * (p.out_f32 ? 4 : 2) / 16; ++c) dst[c] = make_uint4(0, 0, 0, 0);
+        }
+        continue;
+      }
+      const int buf = ab.s;
+      if (!mbar_wait_warp(acc_full(buf), ab.ph, p.err, 75)) break;
+      ab.next();
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      const uint32_t trow = tmem + buf * TN + ((uint32_t)(32 * q) << 16);
+      for (int c0 = 0; c0 < t.cols; c0 += 16) {
+        float v[16];
+        __syncwarp();
+        tmem_ld16(trow + c0, v);
+        if (!vm) continue;
+        if (MODE == kWgrad) {
+          const size_t at = ((size_t)t.e * p.M + m) * (size_t)p.ld_out + t.c0 + c0;
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {   // columns come in eights
+            if (c0 + 8 * g >= t.cols) continue;
+            float* w = v + 8 * g;
+            if (p.out_f32) {
+              float4* dst = reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + at + 8 * g);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                float4 f = make_float4(w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3]);
+                if (p.accumulate) {
+                  const float4 o = dst[h];
+                  f = make_float4(f.x + o.x, f.y + o.y, f.z + o.z, f.w + o.w);
+                }
+                dst[h] = f;
+              }
+            } else {
+              uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + at + 8 * g);
+              if (p.accumulate) {
+                const uint4 o = *dst;
+                const uint32_t ow[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+                for (int h = 0; h < 8; ++h) w[h] += from_16((ow[h >> 1] >> (16 * (h & 1))) & 0xFFFFu, p.bf16);
+              }
+              *dst = make_uint4(to_16x2(w[0], w[1], p.bf16), to_16x2(w[2], w[3], p.bf16), to_16x2(w[4], w[5], p.bf16),
+                                to_16x2(w[6], w[7], p.bf16));
+            }
+          }
+        } else {   // column c is token row c; the warp's lanes are 32 neighbouring elements of it
+          const size_t at = (size_t)(t.row0 + t.c0 + c0) * (size_t)p.ld_out + m;
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            if (c0 + c >= t.cols) break;
+            if (p.out_f32) reinterpret_cast<float*>(p.out)[at + (size_t)c * p.ld_out] = v[c];
+            else reinterpret_cast<uint16_t*>(p.out)[at + (size_t)c * p.ld_out] = to_16(v[c], p.bf16);
+          }
+        }
+      }
+      __syncwarp();
+      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) {
+        if (CG == 1) mbar_arrive(acc_empty(buf));
+        else mbar_arrive_at(acc_empty(buf), 0);
+      }
+    }
+    // rows of no group
+    if (MODE != kWgrad && p.zero_rest && *reinterpret_cast<volatile int*>(p.err) == 0) {
+      const long t = (long)blockIdx.x * 128 + tid - 32 * kEpiWarp, n = (long)gridDim.x * 128;
+      const int el = p.out_f32 ? 4 : 2;
+      uint8_t* out = reinterpret_cast<uint8_t*>(p.out);
+      const int2 last = group_rows(p.offsets, p.E - 1, p.S);
+      zero_rows(out, 0, group_rows(p.offsets, 0, p.S).x, (size_t)p.M * el, (size_t)p.ld_out * el, t, n);
+      zero_rows(out, last.x + last.y, p.S, (size_t)p.M * el, (size_t)p.ld_out * el, t, n);
+    }
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  if (CG == 2) cluster_sync();   // no CTA leaves while the other may still signal it
+  if (warp == 1) {
+    __syncwarp();
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    tmem_free<CG>(tmem, C::kTmemCols);
+  }
+}
+
+template <int CG, int MODE, int TN>
+cudaError_t launch_t(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& a1, const CUtensorMap& b1,
+                     const GgParams& p, long max_items, cudaStream_t st) {
+  static std::atomic<uint64_t> raised{0};
+  const long sms = sm_count();
+  if (sms <= 0) return cudaErrorInvalidDevice;
+  const long ctas = max_items < sms / CG ? max_items * CG : sms / CG * CG;
+  return launch_cluster(gg_kernel<CG, MODE, TN>, &raised, CG, (int)(ctas < CG ? CG : ctas), kThreads, Cfg<CG, TN>::kSmem,
+                        st, a, b, a1, b1, p);
+}
+
+bool fits16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+}  // namespace
+}  // namespace situ
+
+extern "C" situ_status situ_moe_grouped_gemm(const situ_grouped_gemm_args* g, void* stream) {
+  using namespace situ;
+  if (!g) return SITU_ERR_NULL_ARG;
+  const int mode = g->direction;
+  if (mode != kFwd && mode != kDgrad && mode != kWgrad) return SITU_ERR_UNSUPPORTED;
+  if (g->dtype != SITU_DT_BF16 && g->dtype != SITU_DT_F16) return SITU_ERR_UNSUPPORTED;
+  if (g->out_dtype != g->dtype && g->out_dtype != SITU_DT_F32) return SITU_ERR_UNSUPPORTED;
+  if (g->accumulate != 0 && (g->accumulate != 1 || mode != kWgrad)) return SITU_ERR_UNSUPPORTED;
+  if (g->keep_rest != 0 && (g->keep_rest != 1 || mode == kWgrad)) return SITU_ERR_UNSUPPORTED;
+  if (g->S < 0 || g->N < 8 || g->K < 8 || g->N % 8 != 0 || g->K % 8 != 0 || g->E < 1 || g->E > kMaxGroups ||
+      g->N > SITU_GEMM_MAX_DIM || g->K > SITU_GEMM_MAX_DIM || g->S > SITU_GEMM_MAX_ROWS)
+    return SITU_ERR_BAD_SHAPE;
+  const int64_t ca = mode == kFwd ? g->K : g->N;                         // columns of the first operand's rows
+  const int64_t cb = mode == kFwd ? 0 : mode == kDgrad ? 0 : g->K;       // of the second's (wgrad: x)
+  const int64_t co = mode == kFwd ? g->N : g->K;
+  if (g->lda < ca || g->lda % 8 != 0 || (mode == kWgrad && (g->ldb < cb || g->ldb % 8 != 0)) ||
+      (mode != kWgrad && (g->ldo < co || g->ldo % 8 != 0)))
+    return SITU_ERR_BAD_SHAPE;
+  if (g->S == 0 && mode != kWgrad) return SITU_OK;
+  if (!g->out || !g->offsets || !g->device_status || (g->S > 0 && (!g->a || !g->b)) || (mode != kWgrad && !g->b))
+    return SITU_ERR_NULL_ARG;
+  if (!fits16(g->a) || !fits16(g->b) || !fits16(g->out) || (reinterpret_cast<uintptr_t>(g->offsets) & 3) ||
+      (reinterpret_cast<uintptr_t>(g->device_status) & 3))
+    return SITU_ERR_MISALIGNED;
+  cudaStream_t st = (cudaStream_t)stream;
+  const size_t out_el = g->out_dtype == SITU_DT_F32 ? 4 : 2;
+  if (mode == kWgrad && g->S == 0) {
+    if (g->accumulate) return SITU_OK;
+    return cudaMemsetAsync(g->out, 0, (size_t)g->E * g->N * g->K * out_el, st) == cudaSuccess ? SITU_OK : SITU_ERR_CUDA;
+  }
+
+  GgParams p = {};
+  p.offsets = g->offsets;
+  p.E = g->E;
+  p.S = g->S;
+  p.out = g->out;
+  p.ld_out = mode == kWgrad ? g->K : g->ldo;
+  p.bf16 = g->dtype == SITU_DT_BF16;
+  p.out_f32 = g->out_dtype == SITU_DT_F32;
+  p.accumulate = g->accumulate;
+  p.zero_rest = !g->keep_rest;
+  p.err = g->device_status;
+  p.M = mode == kDgrad ? g->K : g->N;
+  p.L = mode == kDgrad ? g->N : g->K;
+  p.Ncol = g->K;
+
+  // tokens per tile by the average group: a group of few rows is bound by its
+  // weights' bytes, and a narrow tile leaves the ring more stages
+  const double per = (double)g->S / g->E;
+  const int tn = mode == kWgrad ? 256 : per <= 32 ? 32 : per <= 64 ? 64 : per <= 128 ? 128 : 256;
+  constexpr int cg = 1;
+  p.n_mt = (p.M + 128 * cg - 1) / (128 * cg);
+  p.n_nt = (p.Ncol + tn - 1) / tn;
+  const double items = mode == kWgrad ? (double)p.E * p.n_mt * p.n_nt : ((double)g->S / tn + p.E) * p.n_mt;
+  if (items > 2.0e9) return SITU_ERR_BAD_SHAPE;
+
+  const CUtensorMapDataType dt = p.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  CUtensorMap ma, mb, ma1, mb1;
+  bool ok;
+  const uint64_t S = (uint64_t)g->S, N = (uint64_t)g->N, K = (uint64_t)g->K, E = (uint64_t)g->E;
+  if (mode == kWgrad) {
+    const uint64_t da[2] = {N, S}, sa[1] = {(uint64_t)g->lda * 2}, db[2] = {K, S}, sb[1] = {(uint64_t)g->ldb * 2};
+    const uint32_t box[2] = {64, 64}, box1[2] = {64, 1};
+    ok = make_map_nd(&ma, dt, g->a, 2, da, sa, box) && make_map_nd(&mb, dt, g->b, 2, db, sb, box) &&
+         make_map_nd(&ma1, dt, g->a, 2, da, sa, box1) && make_map_nd(&mb1, dt, g->b, 2, db, sb, box1);
+  } else {
+    const uint64_t dw[3] = {K, N, E}, sw[2] = {K * 2, N * K * 2};
+    const uint32_t boxw[3] = {64, mode == kFwd ? 128u : 64u, 1};
+    const uint64_t dx[2] = {(uint64_t)p.L, S}, sx[1] = {(uint64_t)g->lda * 2};
+    const uint32_t boxx[2] = {64, (uint32_t)(tn / cg)};
+    ok = make_map_nd(&ma, dt, g->b, 3, dw, sw, boxw) && make_map_nd(&mb, dt, g->a, 2, dx, sx, boxx);
+    ma1 = ma;
+    mb1 = mb;
+  }
+  if (!ok) return SITU_ERR_CUDA;
+  const long cap = items > 1e6 ? 1000000 : (long)items + 1;
+  cudaError_t e;
+  if (mode == kWgrad) {
+    e = launch_t<cg, kWgrad, 256>(ma, mb, ma1, mb1, p, cap, st);
+  } else if (mode == kFwd) {
+    e = tn == 32    ? launch_t<cg, kFwd, 32>(ma, mb, ma1, mb1, p, cap, st)
+        : tn == 64  ? launch_t<cg, kFwd, 64>(ma, mb, ma1, mb1, p, cap, st)
+        : tn == 128 ? launch_t<cg, kFwd, 128>(ma, mb, ma1, mb1, p, cap, st)
+                    : launch_t<cg, kFwd, 256>(ma, mb, ma1, mb1, p, cap, st);
+  } else {
+    e = tn == 32    ? launch_t<cg, kDgrad, 32>(ma, mb, ma1, mb1, p, cap, st)
+        : tn == 64  ? launch_t<cg, kDgrad, 64>(ma, mb, ma1, mb1, p, cap, st)
+        : tn == 128 ? launch_t<cg, kDgrad, 128>(ma, mb, ma1, mb1, p, cap, st)
+                    : launch_t<cg, kDgrad, 256>(ma, mb, ma1, mb1, p, cap, st);
+  }
+  return e == cudaSuccess ? SITU_OK : SITU_ERR_CUDA;
+}

@@ -498,6 +498,102 @@ size_t situ_moe_packed_scales_size(const situ_moe_args* args);
 situ_status situ_moe_pack_scales(const situ_moe_args* args, void* packed, size_t packed_bytes,
                                  void* stream);
 
+/* ------------------------------------------------------------------------
+ * Expert products with 16-bit and with E4M3 weights.
+ *
+ * Beside the FP4 layer: products over the rows that situ_moe_permute sorts
+ * by expert, for experts that are trained (16-bit weights, with gradients)
+ * or whose checkpoint holds E4M3 weights with one fp32 scale per block of
+ * 128.  Rows of local expert e are [offsets[e], offsets[e + 1]), offsets an
+ * int32 [E + 1] device array in ascending order (situ_moe_permute's
+ * expert_offsets); entries are clamped to [0, S] on the device.  Rows before
+ * offsets[0] and from offsets[E] on belong to no expert: their output rows
+ * are set to zero, unless keep_rest = 1 leaves them as they are.
+ *
+ * Each of these kernels bounds its waits as the layer's do; one that gives
+ * up records a nonzero code in *device_status (one int32 in device memory,
+ * which the caller sets to 0 once and reads when it likes).  While it is
+ * nonzero, later calls with it do no work, so that a failed result is not
+ * built upon.  These operators have no counterpart in the pages.
+ * --------------------------------------------------------------------- */
+typedef enum situ_dtype { SITU_DT_BF16 = 0, SITU_DT_F16 = 1, SITU_DT_F32 = 2 } situ_dtype;
+typedef enum situ_grouped_direction {
+  SITU_GROUPED_FORWARD = 0,   /* a = x [S, K],  b = w [E, N, K], out = y [S, N]     */
+  SITU_GROUPED_DGRAD = 1,     /* a = dy [S, N], b = w [E, N, K], out = dx [S, K]    */
+  SITU_GROUPED_WGRAD = 2      /* a = dy [S, N], b = x [S, K],    out = dw [E, N, K] */
+} situ_grouped_direction;
+#define SITU_GEMM_MAX_GROUPS 1024
+#define SITU_GEMM_MAX_DIM (1 << 20)    /* N, K */
+#define SITU_GEMM_MAX_ROWS (1 << 30)   /* S */
+
+/* situ_moe_grouped_gemm -- y = x w_e^T and its gradients, per expert:
+ *   FORWARD  y[r, n]     = sum_k x[r, k] w[e, n, k]      (r a row of e)
+ *   DGRAD    dx[r, k]    = sum_n dy[r, n] w[e, n, k]
+ *   WGRAD    dw[e, n, k] = sum_{rows r of e} dy[r, n] x[r, k]; zeros for an
+ *            expert without rows, or added to dw with accumulate = 1
+ * a and b are of one 16-bit type; sums are fp32, rounded once to out_dtype
+ * (the operands' type or fp32; an accumulating bf16 / f16 dw is rounded once
+ * per call).  N and K are multiples of 8, rows may be strided (lda, ldb, ldo
+ * in elements, multiples of 8; ldb is wgrad's x, ldo y or dx; weights and dw
+ * are contiguous).  a, b, out are 16-byte aligned.  S == 0 launches nothing,
+ * or sets dw to zeros.  Results do not depend on the order of execution.
+ * Errors: NULL_ARG, BAD_SHAPE, UNSUPPORTED, MISALIGNED, CUDA. */
+typedef struct situ_grouped_gemm_args {
+  int32_t direction;              /* situ_grouped_direction */
+  int32_t dtype, out_dtype;       /* situ_dtype */
+  int32_t S, N, K, E;
+  int32_t accumulate;             /* WGRAD only */
+  int32_t keep_rest;              /* FORWARD, DGRAD: 1 leaves the rows of no expert unwritten */
+  const void* a;
+  int64_t lda;
+  const void* b;
+  int64_t ldb;
+  const int32_t* offsets;         /* int32 [E + 1] */
+  void* out;
+  int64_t ldo;
+  int32_t* device_status;
+} situ_grouped_gemm_args;
+situ_status situ_moe_grouped_gemm(const situ_grouped_gemm_args* args, void* stream);
+
+/* situ_moe_quant_fp8 -- x [E, R, K] (bf16, f16 or fp32; rows ldx elements
+ * apart, matrices R * ldx) to E4M3 codes q [E, R, K] and fp32 scales:
+ * block_rows = 1, one per row and 128 columns, [E, R, ceil(K/128)]
+ * (activations); block_rows = 128, one per 128 x 128 block,
+ * [E, ceil(R/128), ceil(K/128)] (weights).  The last blocks may be partial.
+ *   scale = max(amax / 448, 2^-126),  q = nearest E4M3 of x / scale, ties to
+ * even, both divisions in fp32; a NaN or an infinity in a block makes its
+ * scale non-finite.  K a multiple of 8, ldx of 8 (fp32: 4); x 16-byte
+ * aligned, q 8-byte.  Errors: NULL_ARG, BAD_SHAPE, UNSUPPORTED (dtype,
+ * block_rows), MISALIGNED, CUDA. */
+situ_status situ_moe_quant_fp8(const void* x, int32_t dtype, int32_t E, int32_t R, int32_t K, int64_t ldx,
+                               int32_t block_rows, uint8_t* q, float* scale, void* stream);
+
+/* situ_moe_fp8_gemm -- the product of operands in that form, per expert, or
+ * dense (offsets NULL, E = 1: a shared expert or any linear layer):
+ *   y[r, n] = sum_b x_scale[r, b] w_scale[e, n / 128, b]
+ *                   sum_{k in block b} x_q[r, k] w_q[e, n, k]
+ * x_q [S, K] with x_scale [S, ceil(K/128)], w_q [E, N, K] with w_scale
+ * [E, ceil(N/128), ceil(K/128)] (contiguous); out bf16 or fp32 [S, N].  A
+ * block's products are summed in the tensor cores, the scaled blocks in
+ * fp32.  K is a multiple of 16, N of 8; x_q rows may be ldx bytes apart (a
+ * multiple of 16), out rows ldo elements (a multiple of 8).
+ * Errors: NULL_ARG, BAD_SHAPE, UNSUPPORTED, MISALIGNED, CUDA. */
+typedef struct situ_fp8_gemm_args {
+  int32_t out_dtype;              /* SITU_DT_BF16 or SITU_DT_F32 */
+  int32_t S, N, K, E;
+  int32_t keep_rest;
+  const uint8_t* x_q;
+  int64_t ldx;
+  const float* x_scale;
+  const uint8_t* w_q;
+  const float* w_scale;
+  const int32_t* offsets;         /* int32 [E + 1], or NULL: dense */
+  void* out;
+  int64_t ldo;
+  int32_t* device_status;
+} situ_fp8_gemm_args;
+situ_status situ_moe_fp8_gemm(const situ_fp8_gemm_args* args, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
