@@ -68,10 +68,8 @@ struct Cfg {
   static constexpr int kTmemCols = kBufs * TN;
   static constexpr int kCh = TN >= 64 ? 32 : 16;               // columns per TMEM load
   static constexpr int kNch = TN / (2 * kCh);                  // loads per promoting warp and block
-  static constexpr bool kSplitRegs = TN >= 256;
   static_assert(kSmem <= 232448 && kTmemCols <= 512, "shared memory and TMEM");
 };
-constexpr int kLaunchRegs = 168;   // per thread, what kSplitRegs shares out
 
 struct Tile {
   int e, row0, mt, c0, cols;
@@ -102,6 +100,18 @@ __device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
   asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(v));
   lo = __uint_as_float(a);
   hi = __uint_as_float(b);
+}
+
+// zeros to the rows of no group; et: this thread's number among the CTA's
+// per_cta promoting threads
+__device__ __forceinline__ void zero_rest(const F8Params& p, int et, int per_cta) {
+  if (!p.offsets || !p.zero_rest || *reinterpret_cast<volatile int*>(p.err) != 0) return;
+  const long t = (long)blockIdx.x * per_cta + et, n = (long)gridDim.x * per_cta;
+  const int el = p.out_f32 ? 4 : 2;
+  uint8_t* out = reinterpret_cast<uint8_t*>(p.out);
+  const int2 last = group_rows(p.offsets, p.E - 1, p.S);
+  zero_rows(out, 0, group_rows(p.offsets, 0, p.S).x, (size_t)p.N * el, (size_t)p.ld_out * el, t, n);
+  zero_rows(out, last.x + last.y, p.S, (size_t)p.N * el, (size_t)p.ld_out * el, t, n);
 }
 
 template <int CG, int TN>
@@ -148,8 +158,7 @@ f8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
   const int first = blockIdx.x / CG, stride = gridDim.x / CG;
 
   if (warp < kEpiWarp) {
-    if (C::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    if (warp == 0) {
+      if (warp == 0) {
       // ---------------- copies ----------------
       const bool leader = elect_one();
       Ring<C::kStages> r;
@@ -219,7 +228,6 @@ f8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
     }
   } else {
     // ---------------- promotion and store ----------------
-    if (C::kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
     const int q = warp & 3, h = (warp - kEpiWarp) >> 2, et = tid - 32 * kEpiWarp;
     float* stage = reinterpret_cast<float*>(smem + C::kOffS);
     constexpr int kPer = kSG * TN / kEpiThreads > 0 ? kSG * TN / kEpiThreads : 1;   // factors per thread and group
@@ -334,15 +342,7 @@ f8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
       }
       __syncwarp();
     }
-    // rows of no group
-    if (p.offsets && p.zero_rest && *reinterpret_cast<volatile int*>(p.err) == 0) {
-      const long t = (long)blockIdx.x * kEpiThreads + et, n = (long)gridDim.x * kEpiThreads;
-      const int el = p.out_f32 ? 4 : 2;
-      uint8_t* out = reinterpret_cast<uint8_t*>(p.out);
-      const int2 last = group_rows(p.offsets, p.E - 1, p.S);
-      zero_rows(out, 0, group_rows(p.offsets, 0, p.S).x, (size_t)p.N * el, (size_t)p.ld_out * el, t, n);
-      zero_rows(out, last.x + last.y, p.S, (size_t)p.N * el, (size_t)p.ld_out * el, t, n);
-    }
+    zero_rest(p, et, kEpiThreads);
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
@@ -354,20 +354,391 @@ f8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
   }
 }
 
+// ---------------------------------------------------------------------------
+// Wide tiles: tokens on the MMA's M side
+// ---------------------------------------------------------------------------
+
+constexpr int kWideN = 256;
+constexpr int kWideParts = 2;                          // halves of a tile: an MMA and a promoting warpgroup each
+constexpr int kWideThreads = 128 + 128 * kWideParts;
+
+template <int CG>
+struct WCfg {
+  static constexpr int kTM = 128 * CG;                 // tokens per tile
+  static constexpr int kTN = kWideN;                     // weight rows per tile
+  static constexpr int kCols = kTN / kWideParts;       // of one half
+  static constexpr int kBBytes = kTN / CG * 128;
+  static constexpr int kStageBytes = kABytes + kBBytes;
+  // scales: slots of four blocks, 128 tokens' and two weight blocks' factors
+  static constexpr int kSlots = 4;
+  static constexpr int kSlotBytes = (128 + 2) * 16;
+  static constexpr int kOutBytes = 2048;               // output staging of a promoting warp
+  static constexpr int kMaxBytes = 232448 - 1024 - 4 * (kMaxGroups + 1) - 512 - kSlots * kSlotBytes - 4 * kWideParts * kOutBytes;
+  static constexpr int kStages = kMaxBytes / kStageBytes;
+  static constexpr int kOffB = kStages * kABytes;
+  static constexpr int kOffS = kOffB + kStages * kBBytes;
+  static constexpr int kOffOut = kOffS + kSlots * kSlotBytes;
+  static constexpr int kOffTp = kOffOut + 4 * kWideParts * kOutBytes;
+  static constexpr int kOffBar = (kOffTp + 4 * (kMaxGroups + 1) + 15) / 16 * 16;
+  // full, done[2] per stage; acc_empty[2][2]; drain[2]; scale slots full, empty
+  static constexpr int kNumBars = 3 * kStages + 6 + 2 * kSlots;
+  static constexpr int kOffTm = kOffBar + 8 * kNumBars;
+  static constexpr int kSmem = kOffTm + 16 + 1024;
+  static_assert(kSmem <= 232448, "shared memory");
+};
+
+constexpr int kLaunchRegs = 168;   // per thread of a launch, what the warps share out
+
+struct WTile {
+  int e, row0, rows, t0, n0, cols;
+};
+template <int CG>
+__device__ __forceinline__ WTile wide_tile_of(const F8Params& p, const int* tp, int idx) {
+  using C = WCfg<CG>;
+  WTile t;
+  t.e = find_group(tp, p.E, idx / p.n_mt);
+  const int r = idx - tp[t.e] * p.n_mt, tt = tp[t.e + 1] - tp[t.e], nt = r / tt;
+  t.t0 = (r - nt * tt) * C::kTM;   // a group's token tiles run side by side: they read the same weights
+  t.n0 = nt * C::kTN;
+  const int2 g = group_rows(p.offsets, t.e, p.S);
+  t.row0 = g.x;
+  t.rows = g.y;
+  t.cols = min(C::kTN, p.N - t.n0);
+  return t;
+}
+
+// src[i..i + 3] of n to 16 bytes of shared memory, zeros past the end; vec:
+// src is 16-byte aligned and n a multiple of 4
+__device__ __forceinline__ void copy_scales(uint32_t dst, const float* src, int i, int n, bool vec) {
+  if (vec) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src + i) : "memory");
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst + 4 * j), "l"(src + (i + j < n ? i + j : i)),
+                 "r"(i + j < n ? 4 : 0)
+                 : "memory");
+}
+
+__device__ __forceinline__ float4 lds_f32x4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
+  return v;
+}
+// A box of 32 rows x 64 bytes, 16-byte chunks exchanged within row pairs so
+// that neither a column of chunks nor whole rows conflict.
+__device__ __forceinline__ void stage16(uint8_t* box, int row, int chunk, uint4 v) {
+  *reinterpret_cast<uint4*>(box + row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4)) = v;
+}
+// the box to rows [row, row + min(rows, 32)) of the output from column n on
+// (el bytes per element), as far as N goes
+__device__ __forceinline__ void store_box(const F8Params& p, const uint8_t* box, int lane, int row, int rows, int n, int el) {
+  const int chunk = lane & 3, col = n + chunk * (16 / el);
+  if (col >= p.N) return;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = (lane >> 2) + 8 * i;
+    if (r < rows)
+      *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + ((size_t)(row + r) * (size_t)p.ld_out + col) * el) =
+          *reinterpret_cast<const uint4*>(box + r * 64 + ((chunk ^ ((r >> 1) & 3)) << 4));
+  }
+}
+// acc += d * f, kept in its place between the TMEM loads and the arrivals
+__device__ __forceinline__ void fma_in_order(float& acc, uint32_t d, float f) {
+  asm volatile("fma.rn.f32 %0, %1, %2, %0;" : "+f"(acc) : "f"(__uint_as_float(d)), "f"(f));
+}
+
+// the MMA's N of half h of a tile
+template <int CG>
+__device__ __forceinline__ int half_cols(const WTile& t, int h) {
+  const int c = min(max(t.cols - 128 * h, 0), 128);
+  return (c + 16 * CG - 1) / (16 * CG) * (16 * CG);
+}
+
+template <int CG>
+__global__ void __launch_bounds__(kWideThreads, 1)
+f8w_kernel(const __grid_constant__ CUtensorMap mapX, const __grid_constant__ CUtensorMap mapW, const F8Params p) {
+  using C = WCfg<CG>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = CG == 2 ? cluster_rank() : 0;
+  const uint32_t sbase = saddr(smem);
+  int* tp = reinterpret_cast<int*>(smem + C::kOffTp);
+  const uint32_t bar0 = sbase + C::kOffBar;
+  auto full = [&](int s) { return bar0 + 8 * s; };
+  auto done = [&](int h, int s) { return bar0 + 8 * (C::kStages * (1 + h) + s); };
+  auto acc_empty = [&](int h, int b) { return bar0 + 8 * (3 * C::kStages + 2 * h + b); };
+  auto drain = [&](int h) { return bar0 + 8 * (3 * C::kStages + 4 + h); };
+  auto sc_full = [&](int i) { return bar0 + 8 * (3 * C::kStages + 6 + i); };
+  auto sc_empty = [&](int i) { return bar0 + 8 * (3 * C::kStages + 6 + C::kSlots + i); };
+  uint32_t* tm_holder = reinterpret_cast<uint32_t*>(smem + C::kOffTm);
+
+  if (tid == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(done(0, s), 1);
+      mbar_init(done(1, s), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(acc_empty(0, b), 4 * CG);
+      mbar_init(acc_empty(1, b), 4 * CG);
+    }
+    mbar_init(drain(0), 1);
+    mbar_init(drain(1), 1);
+    for (int i = 0; i < C::kSlots; ++i) {
+      mbar_init(sc_full(i), 32);
+      mbar_init(sc_empty(i), 4 * kWideParts);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) tmem_alloc<CG>(saddr(tm_holder), 512);
+  scan_tiles(p.offsets, p.E, p.S, C::kTM, tp, kWideThreads);
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  if (CG == 2) cluster_sync();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const uint32_t tmem = *tm_holder;
+
+  int total = tp[p.E] * p.n_mt;
+  if (*reinterpret_cast<volatile int*>(p.err) != 0) total = 0;
+  const int first = blockIdx.x / CG, stride = gridDim.x / CG;
+
+  const bool xvec = (p.nkb & 3) == 0 && ((reinterpret_cast<uintptr_t>(p.xs) | reinterpret_cast<uintptr_t>(p.ws)) & 15) == 0;
+  if (warp < kEpiWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if (warp == 0) {
+      // ---------------- copies ----------------
+      const bool leader = elect_one();
+      Ring<C::kStages> r;
+      bool ok = true;
+      for (int idx = first; idx < total && ok; idx += stride) {
+        const WTile t = wide_tile_of<CG>(p, tp, idx);
+        int n[2];   // this CTA's first weight row of each half's product
+#pragma unroll
+        for (int h = 0; h < 2; ++h) n[h] = t.n0 + C::kCols * h + half_cols<CG>(t, h) / CG * (int)rank;
+        const int row = t.row0 + t.t0 + 128 * (int)rank;
+        for (int kb = 0; kb < p.nkb; ++kb, r.next()) {
+          const int s = r.s;
+          if (r.used == C::kStages && !(mbar_wait_warp(done(0, s), r.ph ^ 1, p.err, 91) && mbar_wait_warp(done(1, s), r.ph ^ 1, p.err, 91))) {
+            ok = false;
+            break;
+          }
+          if (leader) {
+            if (CG == 1 || rank == 0) mbar_expect_tx(full(s), CG * C::kStageBytes);
+            copy_2d<CG>(sbase + s * kABytes, &mapX, kb * 128, row, full(s));
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              copy_3d<CG>(sbase + C::kOffB + s * C::kBBytes + h * (C::kBBytes / 2), &mapW, kb * 128, n[h], t.e, full(s));
+          }
+          __syncwarp();
+        }
+      }
+      if (ok) {   // the last arrivals on this CTA's barriers, before it may leave
+        for (int j = 0; j < r.used; ++j) {
+          mbar_wait_warp(done(0, j), j < r.s ? r.ph : r.ph ^ 1, p.err, 92);
+          mbar_wait_warp(done(1, j), j < r.s ? r.ph : r.ph ^ 1, p.err, 92);
+        }
+      } else if (rank == 0) {   // copies in flight
+        for (int j = 0; j < r.used; ++j) drain_wait(full(j), j < r.s ? r.ph : r.ph ^ 1);
+      } else {
+        const unsigned long long t0 = globaltimer();   // they complete on the other CTA's barriers
+        while (globaltimer() - t0 < 2000000ull) {
+        }
+      }
+    } else if (warp <= 2) {
+      // ---------------- MMAs ----------------
+      // A warp per half: the waits and the commit of a product take an issuer
+      // about as long as its MMAs run.
+      if (rank == 0) {
+        const int h = warp - 1;
+        const bool leader = elect_one();
+        Ring<C::kStages> r;
+        Ring<2> ab;
+        bool ok = true;
+        for (int idx = first; idx < total && ok; idx += stride) {
+          const WTile t = wide_tile_of<CG>(p, tp, idx);
+          const int nact = half_cols<CG>(t, h);
+          // E4M3 x E4M3 -> fp32, K-major
+          const uint32_t idesc = (1u << 4) | ((uint32_t)(128 * CG >> 4) << 24) | ((uint32_t)(nact >> 3) << 17);
+          for (int kb = 0; kb < p.nkb; ++kb, r.next(), ab.next()) {
+            if ((ab.used == 2 && !mbar_wait_warp(acc_empty(h, ab.s), ab.ph ^ 1, p.err, 93)) ||
+                !mbar_wait_warp(full(r.s), r.ph, p.err, 94)) {
+              ok = false;
+              break;
+            }
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            if (leader) {
+              const uint64_t ad = sdesc(sbase + r.s * kABytes),
+                             bd = sdesc(sbase + C::kOffB + r.s * C::kBBytes + h * (C::kBBytes / 2));
+              if (nact > 0) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  mma_f8<CG>(tmem + ab.s * C::kTN + h * C::kCols, ad + 2 * k, bd + 2 * k, idesc, k != 0);
+              }
+              // this half is done with the stage, and its product is there
+              commit<CG>(done(h, r.s));
+            }
+            __syncwarp();
+          }
+        }
+        if (!ok) {   // MMAs in flight
+          if (leader) commit<CG>(drain(h));
+          __syncwarp();
+          drain_wait(drain(h), 0);
+        }
+      }
+    } else {
+      // ---------------- scales ----------------
+      // Copied ahead of the promotion, up to four slots (16 blocks): read
+      // when they are needed, from an L2 busy with the tiles, they would
+      // stall every block.
+      const int st = tid - 96;
+      Ring<C::kSlots> sr;
+      bool ok = true;
+      for (int idx = first; idx < total && ok; idx += stride) {
+        const WTile t = wide_tile_of<CG>(p, tp, idx);
+        const int row = t.t0 + 128 * (int)rank, wb = t.n0 >> 7;
+        for (int kb = 0; kb < p.nkb; kb += 4, sr.next()) {
+          if (sr.used == C::kSlots && !mbar_wait_warp(sc_empty(sr.s), sr.ph ^ 1, p.err, 96)) {
+            ok = false;
+            break;
+          }
+          const uint32_t slot = sbase + C::kOffS + sr.s * C::kSlotBytes;
+          for (int i = st; i < 128 + 2; i += 32) {   // tokens, then weight blocks
+            const bool tok = i < 128;
+            const float* src = tok ? p.xs + (size_t)(t.row0 + min(row + i, t.rows - 1)) * p.nkb
+                                   : p.ws + ((size_t)t.e * p.nrb + min(wb + i - 128, p.nrb - 1)) * p.nkb;
+            copy_scales(slot + 16 * i, src, kb, p.nkb, xvec);
+          }
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(sc_full(sr.s)) : "memory");
+        }
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+    }
+  } else {
+    // ---------------- promotion and store ----------------
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+    const int q = warp & 3, h = (warp - kEpiWarp) >> 2, et = tid - 32 * kEpiWarp;
+    Ring<C::kSlots> sr;
+    Ring<2> ab;
+    Ring<C::kStages> r;
+    bool ok = true;
+    const uint32_t tbase = tmem + C::kCols * h + ((uint32_t)(32 * q) << 16);
+    for (int idx = first; idx < total && ok; idx += stride) {
+      // a half's 128 columns lie in one block of weight rows
+      float acc[C::kCols];
+#pragma unroll
+      for (int c = 0; c < C::kCols; ++c) acc[c] = 0.f;
+      for (int k0 = 0; k0 < p.nkb && ok; k0 += 4) {
+        if (!mbar_wait_warp(sc_full(sr.s), sr.ph, p.err, 97)) {
+          ok = false;
+          break;
+        }
+        const uint32_t slot = sbase + C::kOffS + sr.s * C::kSlotBytes;
+        float f[4];
+        {
+          const float4 x = lds_f32x4(slot + 16 * (32 * q + lane)), w = lds_f32x4(slot + 16 * (128 + h));
+          f[0] = x.x * w.x;
+          f[1] = x.y * w.y;
+          f[2] = x.z * w.z;
+          f[3] = x.w * w.w;
+        }
+        __syncwarp();
+        mbar_arrive_if(sc_empty(sr.s), lane == 0);
+        sr.next();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (k0 + j >= p.nkb) break;
+          if (!mbar_wait_warp(done(h, r.s), r.ph, p.err, 95)) {
+            ok = false;
+            break;
+          }
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          // 64 columns at a time
+          uint32_t d[64];
+#pragma unroll
+          for (int l = 0; l < C::kCols; l += 64) {
+            tmem_ld32_nowait(tbase + ab.s * C::kTN + l, d);
+            tmem_ld32_nowait(tbase + ab.s * C::kTN + l + 32, d + 32);
+            tmem_ld_wait<64>(d);
+            if (l + 64 == C::kCols) {   // read: the accumulator may be written again
+              asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+              if (CG == 1) mbar_arrive_if(acc_empty(h, ab.s), lane == 0);
+              else mbar_arrive_at_if(acc_empty(h, ab.s), 0, lane == 0);
+            }
+#pragma unroll
+            for (int c = 0; c < 64; ++c) fma_in_order(acc[l + c], d[c], f[j]);
+          }
+          ab.next();
+          r.next();
+        }
+      }
+      if (!ok) break;
+      const WTile t = wide_tile_of<CG>(p, tp, idx);
+      // through shared memory, 64 bytes of each of the warp's 32 rows at a time:
+      // a warp's store then covers 8 rows' whole sectors, not 32 rows' halves
+      const int row0 = t.t0 + 128 * (int)rank + 32 * q, n0 = t.n0 + C::kCols * h;
+      uint8_t* box = smem + C::kOffOut + (warp - kEpiWarp) * C::kOutBytes;
+      if (p.out_f32) {
+#pragma unroll
+        for (int i = 0; i < C::kCols / 16; ++i) {
+          const float* v = acc + 16 * i;
+          __syncwarp();
+#pragma unroll
+          for (int c = 0; c < 4; ++c) stage16(box, lane, c, make_uint4(__float_as_uint(v[4 * c]), __float_as_uint(v[4 * c + 1]),
+                                                                       __float_as_uint(v[4 * c + 2]), __float_as_uint(v[4 * c + 3])));
+          __syncwarp();
+          store_box(p, box, lane, t.row0 + row0, t.rows - row0, n0 + 16 * i, 4);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < C::kCols / 32; ++i) {
+          const float* v = acc + 32 * i;
+          __syncwarp();
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            stage16(box, lane, c, make_uint4(f32x2_to_bf16x2(v[8 * c], v[8 * c + 1]), f32x2_to_bf16x2(v[8 * c + 2], v[8 * c + 3]),
+                                             f32x2_to_bf16x2(v[8 * c + 4], v[8 * c + 5]), f32x2_to_bf16x2(v[8 * c + 6], v[8 * c + 7])));
+          __syncwarp();
+          store_box(p, box, lane, t.row0 + row0, t.rows - row0, n0 + 32 * i, 2);
+        }
+      }
+    }
+    zero_rest(p, et, 128 * kWideParts);
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  if (CG == 2) cluster_sync();   // no CTA leaves while the other may still signal it
+  if (warp == 1) {
+    __syncwarp();
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    tmem_free<CG>(tmem, 512);
+  }
+}
+
 template <int CG, int TN>
 cudaError_t launch_t(const CUtensorMap& a, const CUtensorMap& b, const F8Params& p, long max_items, cudaStream_t st) {
   static std::atomic<uint64_t> raised{0};
   const long sms = sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
-  if (Cfg<CG, TN>::kSplitRegs) {   // the shares need the launch to hold their sum
-    static const int regs = [] {
-      cudaFuncAttributes fa;
-      return cudaFuncGetAttributes(&fa, f8_kernel<CG, TN>) == cudaSuccess ? fa.numRegs : 0;
-    }();
-    if (regs < kLaunchRegs) return cudaErrorInvalidConfiguration;
-  }
   const long ctas = max_items < sms / CG ? max_items * CG : sms / CG * CG;
   return launch_cluster(f8_kernel<CG, TN>, &raised, CG, (int)(ctas < CG ? CG : ctas), kThreads, Cfg<CG, TN>::kSmem, st, a, b, p);
+}
+
+template <int CG>
+cudaError_t launch_wide(const CUtensorMap& x, const CUtensorMap& w, const F8Params& p, long max_items, cudaStream_t st) {
+  static std::atomic<uint64_t> raised{0};
+  // the register shares need the launch to hold their sum
+  static const int regs = [] {
+    cudaFuncAttributes fa;
+    return cudaFuncGetAttributes(&fa, f8w_kernel<CG>) == cudaSuccess ? fa.numRegs : 0;
+  }();
+  const long sms = sm_count();
+  if (sms <= 0 || regs < kLaunchRegs) return cudaErrorInvalidConfiguration;
+  const long ctas = max_items < sms / CG ? max_items * CG : sms / CG * CG;
+  return launch_cluster(f8w_kernel<CG>, &raised, CG, (int)(ctas < CG ? CG : ctas), kWideThreads, WCfg<CG>::kSmem, st, x, w, p);
 }
 
 }  // namespace
@@ -406,23 +777,24 @@ extern "C" situ_status situ_moe_fp8_gemm(const situ_fp8_gemm_args* g, void* stre
   p.err = g->device_status;
 
   const double per = (double)g->S / g->E;
-  const int tn = per <= 32 ? 32 : per <= 64 ? 64 : per <= 128 ? 128 : 256;
-  constexpr int cg = 1;
-  p.n_mt = (p.N + 128 * cg - 1) / (128 * cg);
-  const double items = ((double)g->S / tn + p.E) * p.n_mt;
+  const int tn = per <= 20 ? 32 : per <= 64 ? 64 : 256;
+  const int cg = tn < 256 || per < 200 ? 1 : 2;
+  const int tm = tn < 256 ? tn : 128 * cg;        // tokens per tile
+  p.n_mt = tn < 256 ? (p.N + 127) / 128 : (p.N + kWideN - 1) / kWideN;
+  const double items = ((double)g->S / tm + p.E) * p.n_mt;
   if (items > 2.0e9) return SITU_ERR_BAD_SHAPE;
-  CUtensorMap ma, mb;
+  CUtensorMap mw, mx;
   const uint64_t S = (uint64_t)g->S, N = (uint64_t)g->N, K = (uint64_t)g->K, E = (uint64_t)g->E;
   const uint64_t dw[3] = {K, N, E}, sw[2] = {K, N * K}, dx[2] = {K, S}, sx[1] = {(uint64_t)g->ldx};
-  const uint32_t boxw[3] = {128, 128, 1}, boxx[2] = {128, (uint32_t)(tn / cg)};
-  if (!make_map_nd(&ma, CU_TENSOR_MAP_DATA_TYPE_UINT8, g->w_q, 3, dw, sw, boxw) ||
-      !make_map_nd(&mb, CU_TENSOR_MAP_DATA_TYPE_UINT8, g->x_q, 2, dx, sx, boxx))
+  const uint32_t boxw[3] = {128, tn < 256 ? 128u : (uint32_t)(kWideN / 2 / cg), 1}, boxx[2] = {128, tn < 256 ? (uint32_t)tn : 128u};
+  if (!make_map_nd(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, g->w_q, 3, dw, sw, boxw) ||
+      !make_map_nd(&mx, CU_TENSOR_MAP_DATA_TYPE_UINT8, g->x_q, 2, dx, sx, boxx))
     return SITU_ERR_CUDA;
   cudaStream_t st = (cudaStream_t)stream;
   const long cap = items > 1e6 ? 1000000 : (long)items + 1;
-  const cudaError_t e = tn == 32    ? launch_t<cg, 32>(ma, mb, p, cap, st)
-                        : tn == 64  ? launch_t<cg, 64>(ma, mb, p, cap, st)
-                        : tn == 128 ? launch_t<cg, 128>(ma, mb, p, cap, st)
-                                    : launch_t<cg, 256>(ma, mb, p, cap, st);
+  const cudaError_t e = tn == 32    ? launch_t<1, 32>(mw, mx, p, cap, st)
+                        : tn == 64  ? launch_t<1, 64>(mw, mx, p, cap, st)
+                        : cg == 1   ? launch_wide<1>(mx, mw, p, cap, st)
+                                    : launch_wide<2>(mx, mw, p, cap, st);
   return e == cudaSuccess ? SITU_OK : SITU_ERR_CUDA;
 }

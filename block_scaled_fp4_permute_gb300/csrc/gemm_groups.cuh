@@ -83,12 +83,29 @@ __device__ __forceinline__ void cluster_sync() {
 }
 // the shared::cluster address of `a` in the pair's even CTA
 __device__ __forceinline__ uint32_t leader_addr(uint32_t a) { return a & 0xFEFFFFFFu; }
-// one arrival on a barrier of CTA `rank` of the cluster
+// One arrival on a barrier of CTA `rank` of the cluster.  It orders tensor
+// memory reads (with the tcgen05 fences around it) and nothing in global
+// memory: with release at cluster scope it would wait for the thread's
+// output stores, about 1 us each time.
 __device__ __forceinline__ void mbar_arrive_at(uint32_t a, uint32_t rank) {
   asm volatile(
       "{\n .reg .b32 r;\n mapa.shared::cluster.u32 r, %0, %1;\n"
-      " mbarrier.arrive.release.cluster.shared::cluster.b64 _, [r];\n}" ::"r"(a),
+      " mbarrier.arrive.shared::cluster.b64 _, [r];\n}" ::"r"(a),
       "r"(rank)
+      : "memory");
+}
+
+// the same as predicated instructions, without a branch
+__device__ __forceinline__ void mbar_arrive_if(uint32_t a, bool p) {
+  asm volatile("{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n @q mbarrier.arrive.shared::cta.b64 _, [%0];\n}" ::"r"(a),
+               "r"((uint32_t)p)
+               : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_at_if(uint32_t a, uint32_t rank, bool p) {
+  asm volatile(
+      "{\n .reg .pred q;\n .reg .b32 r;\n setp.ne.b32 q, %2, 0;\n mapa.shared::cluster.u32 r, %0, %1;\n"
+      " @q mbarrier.arrive.shared::cluster.b64 _, [r];\n}" ::"r"(a),
+      "r"(rank), "r"((uint32_t)p)
       : "memory");
 }
 

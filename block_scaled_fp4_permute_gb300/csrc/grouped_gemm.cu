@@ -39,6 +39,7 @@ namespace {
 constexpr int kFwd = SITU_GROUPED_FORWARD, kDgrad = SITU_GROUPED_DGRAD, kWgrad = SITU_GROUPED_WGRAD;
 constexpr int kBK = 64;             // contraction elements per stage
 constexpr int kABytes = 128 * 128;  // 128 weights (or n) x 64 elements
+constexpr int kBoxRows = 32;        // token rows per copy (forward, dgrad)
 constexpr int kThreads = 256;
 constexpr int kEpiWarp = 4;         // first epilogue warp
 
@@ -53,16 +54,20 @@ struct GgParams {
   int* err;
 };
 
-template <int CG, int TN>
+template <int CG, int MODE, int TN>
 struct Cfg {
   static constexpr int kTNB = TN / CG;                // N-side rows of one CTA
   static constexpr int kBBytes = kTNB * 128;
   static constexpr int kStageBytes = kABytes + kBBytes;
-  static constexpr int kMaxBytes = 232448 - 1024 - 4 * (kMaxGroups + 1) - 512;
+  // wgrad: output staging, two 4 KB boxes per epilogue warp (and no tile prefix)
+  static constexpr int kOutBytes = MODE == kWgrad ? 4 * 2 * 4096 : 0;
+  static constexpr int kTpBytes = MODE == kWgrad ? 0 : 4 * (kMaxGroups + 1);
+  static constexpr int kMaxBytes = 232448 - 1024 - kTpBytes - kOutBytes - 512;
   static constexpr int kStages = kMaxBytes / kStageBytes;
   static constexpr int kOffB = kStages * kABytes;
-  static constexpr int kOffTp = kOffB + kStages * kBBytes;
-  static constexpr int kOffBar = (kOffTp + 4 * (kMaxGroups + 1) + 15) / 16 * 16;
+  static constexpr int kOffOut = kOffB + kStages * kBBytes;
+  static constexpr int kOffTp = kOffOut + kOutBytes;
+  static constexpr int kOffBar = (kOffTp + kTpBytes + 15) / 16 * 16;
   static constexpr int kNumBars = 2 * kStages + 5;    // full, empty; acc_full[2], acc_empty[2]; drain
   static constexpr int kOffTm = kOffBar + 8 * kNumBars;
   static constexpr int kSmem = kOffTm + 16 + 1024;
@@ -121,8 +126,10 @@ __device__ __forceinline__ Tile tile_of(const GgParams& p, const int* tp, int id
 template <int CG, int MODE, int TN>
 __global__ void __launch_bounds__(kThreads, 1)
 gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
-          const __grid_constant__ CUtensorMap mapA1, const __grid_constant__ CUtensorMap mapB1, const GgParams p) {
-  using C = Cfg<CG, TN>;
+          const __grid_constant__ CUtensorMap mapA1, const __grid_constant__ CUtensorMap mapB1,
+          const __grid_constant__ CUtensorMap mapA16, const __grid_constant__ CUtensorMap mapB16,
+          const __grid_constant__ CUtensorMap mapO, const GgParams p) {
+  using C = Cfg<CG, MODE, TN>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -183,14 +190,16 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
           const uint32_t a = sbase + s * kABytes, b = sbase + C::kOffB + s * C::kBBytes;
           const int k0 = kk * kBK;
           if (MODE != kWgrad) {
-            if (CG == 1 || rank == 0) mbar_expect_tx(full(s), CG * C::kStageBytes);
+            const int nbox = (half + kBoxRows - 1) / kBoxRows;   // token rows in boxes of 32: a short tile reads few
+            if (CG == 1 || rank == 0) mbar_expect_tx(full(s), CG * (kABytes + nbox * kBoxRows * 128));
             if (MODE == kFwd) {
               copy_3d<CG>(a, &mapA, k0, ma, t.e, full(s));
             } else {   // w as [n, k], k contiguous: two chunks of 64 k
               copy_3d<CG>(a, &mapA, ma, k0, t.e, full(s));
               copy_3d<CG>(a + kABytes / 2, &mapA, ma + 64, k0, t.e, full(s));
             }
-            copy_2d<CG>(b, &mapB, k0, t.row0 + cb, full(s));
+            for (int i = 0; i < nbox; ++i)
+              copy_2d<CG>(b + i * kBoxRows * 128, &mapB, k0, t.row0 + cb + i * kBoxRows, full(s));
           } else {
             const int rows = t.rows - k0;
             if (rows >= kBK) {
@@ -198,19 +207,29 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
               for (int c = 0; c < 2; ++c) copy_2d<CG>(a + 8192 * c, &mapA, ma + 64 * c, t.row0 + k0, full(s));
               for (int c = 0; c < nchunk; ++c) copy_2d<CG>(b + 8192 * c, &mapB, cb + 64 * c, t.row0 + k0, full(s));
             } else {
-              const int r16 = (rows + 15) & ~15;
-              if (CG == 1 || rank == 0) mbar_expect_tx(full(s), CG * (2 + nchunk) * r16 * 128);
-              for (int i = 0; i < r16; i += 4) {
-                int q[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) q[j] = i + j < rows ? t.row0 + k0 + i + j : p.S;   // S: out of bounds, zeros
-                for (int c = 0; c < 2; ++c)
-                  copy_rows4<CG>(a + 8192 * c + i * 128, &mapA1, ma + 64 * c, q[0], q[1], q[2], q[3], full(s));
+              // whole sixteens in boxes, the rest row by row below
+              const int whole = rows & ~15;
+              if (CG == 1 || rank == 0) mbar_expect_tx(full(s), CG * (2 + nchunk) * ((rows + 15) & ~15) * 128);
+              for (int i = 0; i < whole; i += 16) {
+                for (int c = 0; c < 2; ++c) copy_2d<CG>(a + 8192 * c + i * 128, &mapA16, ma + 64 * c, t.row0 + k0 + i, full(s));
                 for (int c = 0; c < nchunk; ++c)
-                  copy_rows4<CG>(b + 8192 * c + i * 128, &mapB1, cb + 64 * c, q[0], q[1], q[2], q[3], full(s));
+                  copy_2d<CG>(b + 8192 * c + i * 128, &mapB16, cb + 64 * c, t.row0 + k0 + i, full(s));
               }
             }
           }
+        }
+        __syncwarp();
+        if (MODE == kWgrad && t.rows - kk * kBK < kBK && (t.rows & 15) != 0 && lane < 4 * (2 + nchunk)) {
+          // the last, partial sixteen: a lane per chunk and four rows; rows past
+          // the group's end are named S, out of bounds, and read as zeros
+          const int c = lane >> 2, i = (t.rows & ~15) - kk * kBK + 4 * (lane & 3), r0 = kk * kBK + i;
+          int row[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) row[j] = r0 + j < t.rows ? t.row0 + r0 + j : p.S;
+          const bool is_a = c < 2;
+          copy_rows4<CG>(sbase + (is_a ? s * kABytes + 8192 * c : C::kOffB + s * C::kBBytes + 8192 * (c - 2)) + i * 128,
+                         is_a ? &mapA1 : &mapB1, is_a ? ma + 64 * c : cb + 64 * (c - 2), row[0], row[1], row[2], row[3],
+                         full(s));
         }
         __syncwarp();
       }
@@ -279,16 +298,61 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
     // ---------------- epilogue ----------------
     const int q = warp - kEpiWarp;
     Ring<2> ab;
+    auto release = [&](int buf) {   // the accumulator may be written again
+      __syncwarp();
+      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) {
+        if (CG == 1) mbar_arrive(acc_empty(buf));
+        else mbar_arrive_at(acc_empty(buf), 0);
+      }
+    };
+    // 32 rows of dw from row n0: boxes of 128 bytes x 32 rows through shared
+    // memory (128-byte swizzle), two in flight; the map ends at N and K
+    uint32_t obuf = 0;
+    auto store_dw = [&](const Tile& t, int n0, uint32_t trow, bool sums) {
+      const int per = p.out_f32 ? 32 : 64;
+      if (n0 >= p.M) return;
+      for (int c0 = 0; c0 < t.cols; c0 += per) {
+        uint32_t v[64];
+        if (sums) {
+          tmem_ld32_nowait(trow + c0, v);
+          if (!p.out_f32) tmem_ld32_nowait(trow + c0 + 32, v + 32);
+          tmem_ld_wait<64>(v);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 64; ++i) v[i] = 0u;
+        }
+        if (!p.out_f32) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = to_16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]), p.bf16);
+        }
+        // the box written two steps ago has been read
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+        __syncwarp();
+        uint8_t* box = smem + C::kOffOut + (2 * q + obuf) * 4096;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          *reinterpret_cast<uint4*>(box + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+              make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+          asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                           reinterpret_cast<uint64_t>(&mapO)),
+                       "r"(t.c0 + c0), "r"(n0), "r"(t.e), "r"(saddr(box))
+                       : "memory");
+          asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        }
+        obuf ^= 1;
+      }
+    };
     for (int idx = first; idx < total; idx += stride) {
       const Tile t = tile_of<CG, MODE, TN>(p, tp, idx);
       const int m = t.m0 + 128 * (int)rank + 32 * q + lane;
       const bool vm = m < p.M;
       if (MODE == kWgrad && t.nk == 0) {   // an expert without rows
-        if (!p.accumulate && vm) {
-          const size_t at = ((size_t)t.e * p.M + m) * (size_t)p.ld_out + t.c0;
-          uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(p.out) + at * (p.out_f32 ? 4 : 2));
-          for (int c = 0; c < t.cols * (p.out_f32 ? 4 : 2) / 16; ++c) dst[c] = make_uint4(0, 0, 0, 0);
-        }
+        if (!p.accumulate) store_dw(t, m - lane, 0, false);
         continue;
       }
       const int buf = ab.s;
@@ -296,6 +360,11 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
       ab.next();
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const uint32_t trow = tmem + buf * TN + ((uint32_t)(32 * q) << 16);
+      if (MODE == kWgrad && !p.accumulate) {
+        store_dw(t, m - lane, trow, true);
+        release(buf);
+        continue;
+      }
       for (int c0 = 0; c0 < t.cols; c0 += 16) {
         float v[16];
         __syncwarp();
@@ -340,14 +409,9 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
           }
         }
       }
-      __syncwarp();
-      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) {
-        if (CG == 1) mbar_arrive(acc_empty(buf));
-        else mbar_arrive_at(acc_empty(buf), 0);
-      }
+      release(buf);
     }
+    if (MODE == kWgrad && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     // rows of no group
     if (MODE != kWgrad && p.zero_rest && *reinterpret_cast<volatile int*>(p.err) == 0) {
       const long t = (long)blockIdx.x * 128 + tid - 32 * kEpiWarp, n = (long)gridDim.x * 128;
@@ -368,15 +432,19 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
   }
 }
 
+// operands; wgrad: their rows four by index and in sixteens, and the output
+struct Maps {
+  CUtensorMap a, b, a1, b1, a16, b16, out;
+};
+
 template <int CG, int MODE, int TN>
-cudaError_t launch_t(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& a1, const CUtensorMap& b1,
-                     const GgParams& p, long max_items, cudaStream_t st) {
+cudaError_t launch_t(const Maps& m, const GgParams& p, long max_items, cudaStream_t st) {
   static std::atomic<uint64_t> raised{0};
   const long sms = sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
   const long ctas = max_items < sms / CG ? max_items * CG : sms / CG * CG;
-  return launch_cluster(gg_kernel<CG, MODE, TN>, &raised, CG, (int)(ctas < CG ? CG : ctas), kThreads, Cfg<CG, TN>::kSmem,
-                        st, a, b, a1, b1, p);
+  return launch_cluster(gg_kernel<CG, MODE, TN>, &raised, CG, (int)(ctas < CG ? CG : ctas), kThreads, Cfg<CG, MODE, TN>::kSmem,
+                        st, m.a, m.b, m.a1, m.b1, m.a16, m.b16, m.out, p);
 }
 
 bool fits16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -433,46 +501,50 @@ extern "C" situ_status situ_moe_grouped_gemm(const situ_grouped_gemm_args* g, vo
   // tokens per tile by the average group: a group of few rows is bound by its
   // weights' bytes, and a narrow tile leaves the ring more stages
   const double per = (double)g->S / g->E;
-  const int tn = mode == kWgrad ? 256 : per <= 32 ? 32 : per <= 64 ? 64 : per <= 128 ? 128 : 256;
-  constexpr int cg = 1;
+  const int tn = mode == kWgrad ? 256 : per <= 20 ? 32 : per <= 44 ? 64 : per <= 98 ? 128 : 256;
+  const int cg = tn == 256 && p.M > 128 ? 2 : 1;
   p.n_mt = (p.M + 128 * cg - 1) / (128 * cg);
   p.n_nt = (p.Ncol + tn - 1) / tn;
   const double items = mode == kWgrad ? (double)p.E * p.n_mt * p.n_nt : ((double)g->S / tn + p.E) * p.n_mt;
   if (items > 2.0e9) return SITU_ERR_BAD_SHAPE;
 
   const CUtensorMapDataType dt = p.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  CUtensorMap ma, mb, ma1, mb1;
+  Maps m = {};
   bool ok;
   const uint64_t S = (uint64_t)g->S, N = (uint64_t)g->N, K = (uint64_t)g->K, E = (uint64_t)g->E;
   if (mode == kWgrad) {
     const uint64_t da[2] = {N, S}, sa[1] = {(uint64_t)g->lda * 2}, db[2] = {K, S}, sb[1] = {(uint64_t)g->ldb * 2};
-    const uint32_t box[2] = {64, 64}, box1[2] = {64, 1};
-    ok = make_map_nd(&ma, dt, g->a, 2, da, sa, box) && make_map_nd(&mb, dt, g->b, 2, db, sb, box) &&
-         make_map_nd(&ma1, dt, g->a, 2, da, sa, box1) && make_map_nd(&mb1, dt, g->b, 2, db, sb, box1);
+    const uint32_t box[2] = {64, 64}, box1[2] = {64, 1}, box16[2] = {64, 16};
+    const uint64_t dout[3] = {K, N, E}, sout[2] = {K * out_el, N * K * out_el};
+    const uint32_t boxo[3] = {(uint32_t)(128 / out_el), 32, 1};
+    ok = make_map_nd(&m.a, dt, g->a, 2, da, sa, box) && make_map_nd(&m.b, dt, g->b, 2, db, sb, box) &&
+         make_map_nd(&m.a1, dt, g->a, 2, da, sa, box1) && make_map_nd(&m.b1, dt, g->b, 2, db, sb, box1) &&
+         make_map_nd(&m.a16, dt, g->a, 2, da, sa, box16) && make_map_nd(&m.b16, dt, g->b, 2, db, sb, box16) &&
+         make_map_nd(&m.out, p.out_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : dt, g->out, 3, dout, sout, boxo);
   } else {
     const uint64_t dw[3] = {K, N, E}, sw[2] = {K * 2, N * K * 2};
     const uint32_t boxw[3] = {64, mode == kFwd ? 128u : 64u, 1};
     const uint64_t dx[2] = {(uint64_t)p.L, S}, sx[1] = {(uint64_t)g->lda * 2};
-    const uint32_t boxx[2] = {64, (uint32_t)(tn / cg)};
-    ok = make_map_nd(&ma, dt, g->b, 3, dw, sw, boxw) && make_map_nd(&mb, dt, g->a, 2, dx, sx, boxx);
-    ma1 = ma;
-    mb1 = mb;
+    const uint32_t boxx[2] = {64, (uint32_t)kBoxRows};
+    ok = make_map_nd(&m.a, dt, g->b, 3, dw, sw, boxw) && make_map_nd(&m.b, dt, g->a, 2, dx, sx, boxx);
   }
   if (!ok) return SITU_ERR_CUDA;
   const long cap = items > 1e6 ? 1000000 : (long)items + 1;
   cudaError_t e;
   if (mode == kWgrad) {
-    e = launch_t<cg, kWgrad, 256>(ma, mb, ma1, mb1, p, cap, st);
+    e = cg == 2 ? launch_t<2, kWgrad, 256>(m, p, cap, st) : launch_t<1, kWgrad, 256>(m, p, cap, st);
   } else if (mode == kFwd) {
-    e = tn == 32    ? launch_t<cg, kFwd, 32>(ma, mb, ma1, mb1, p, cap, st)
-        : tn == 64  ? launch_t<cg, kFwd, 64>(ma, mb, ma1, mb1, p, cap, st)
-        : tn == 128 ? launch_t<cg, kFwd, 128>(ma, mb, ma1, mb1, p, cap, st)
-                    : launch_t<cg, kFwd, 256>(ma, mb, ma1, mb1, p, cap, st);
+    e = tn == 32    ? launch_t<1, kFwd, 32>(m, p, cap, st)
+        : tn == 64  ? launch_t<1, kFwd, 64>(m, p, cap, st)
+        : tn == 128 ? launch_t<1, kFwd, 128>(m, p, cap, st)
+        : cg == 2   ? launch_t<2, kFwd, 256>(m, p, cap, st)
+                    : launch_t<1, kFwd, 256>(m, p, cap, st);
   } else {
-    e = tn == 32    ? launch_t<cg, kDgrad, 32>(ma, mb, ma1, mb1, p, cap, st)
-        : tn == 64  ? launch_t<cg, kDgrad, 64>(ma, mb, ma1, mb1, p, cap, st)
-        : tn == 128 ? launch_t<cg, kDgrad, 128>(ma, mb, ma1, mb1, p, cap, st)
-                    : launch_t<cg, kDgrad, 256>(ma, mb, ma1, mb1, p, cap, st);
+    e = tn == 32    ? launch_t<1, kDgrad, 32>(m, p, cap, st)
+        : tn == 64  ? launch_t<1, kDgrad, 64>(m, p, cap, st)
+        : tn == 128 ? launch_t<1, kDgrad, 128>(m, p, cap, st)
+        : cg == 2   ? launch_t<2, kDgrad, 256>(m, p, cap, st)
+                    : launch_t<1, kDgrad, 256>(m, p, cap, st);
   }
   return e == cudaSuccess ? SITU_OK : SITU_ERR_CUDA;
 }
