@@ -361,14 +361,14 @@ _E4M3 = (torch.uint8, torch.float8_e4m3fn)
 _gemm_status = {}
 
 
-def _status(device: torch.device) -> torch.Tensor:
-    """The status word that this process's products on ``device`` share."""
-    t = _gemm_status.get(device)
+def _status_word(index: int) -> torch.Tensor:
+    """The status word that this process's products on GPU ``index`` share."""
+    t = _gemm_status.get(index)
     if t is None:
-        with torch.cuda.device(device):
-            t = torch.zeros(1, dtype=torch.int32, device=device)
+        with torch.cuda.device(index):
+            t = torch.zeros(1, dtype=torch.int32, device=f"cuda:{index}")
             torch.cuda.synchronize()   # once per device: zero before any stream uses it
-        t = _gemm_status.setdefault(device, t)
+        t = _gemm_status.setdefault(index, t)
     return t
 
 
@@ -376,85 +376,98 @@ def situ_moe_gemm_status(device=None, reset: bool = False) -> int:
     """0, or the code of the first bounded wait that a product
     (situ_moe_grouped_gemm*, situ_moe_fp8*_gemm) on ``device`` gave up; until
     it is reset the products there do no work.  Waits for the device."""
-    device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-    torch.cuda.synchronize(device)
-    t = _status(device)
+    device = torch.device("cuda" if device is None else device)
+    index = torch.cuda.current_device() if device.index is None else device.index
+    torch.cuda.synchronize(index)
+    t = _status_word(index)
     code = int(t.item())
     if reset and code:
         t.zero_()
-        torch.cuda.synchronize(device)
+        torch.cuda.synchronize(index)
     return code
 
 
-def _rows(t: torch.Tensor, what: str, unit: int) -> torch.Tensor:
-    """``t`` as rows that the kernels can read in place: columns packed, rows
-    a multiple of ``unit`` elements apart and 16-byte aligned; else a copy."""
-    if t.dim() != 2:
-        raise ValueError(f"{what} must be 2-dimensional")
-    if t.shape[0] > 1 and (t.stride(0) < t.shape[1] or t.stride(0) % unit) or \
-            (t.shape[1] > 1 and t.stride(1) != 1) or t.data_ptr() % 16:
-        return t.clone(memory_format=torch.contiguous_format)
-    return t
+def _enqueue(name: str, *args, dev: torch.device, stream) -> None:
+    """Calls the C entry point ``name`` on ``dev``, its stream last."""
+    index = dev.index
+    raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    fn = getattr(_lib or lib(), name)
+    if torch._C._cuda_getDevice() == index:
+        status = fn(*args, raw)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, raw)
+    if status:
+        _check(name, status)
 
 
-def _pitch(t: torch.Tensor) -> int:
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+def _rows(t: torch.Tensor, unit: int):
+    """(tensor, pointer, elements between rows) of ``t`` [R, C]: itself where
+    the kernels can read it in place (columns packed, rows a multiple of
+    ``unit`` elements apart, 16-byte aligned), else a copy."""
+    R, C = t.shape
+    s0, s1 = t.stride()
+    p = t.data_ptr()
+    if s1 == 1 and p & 15 == 0:
+        if R <= 1:
+            return t, p, C
+        if s0 >= C and s0 % unit == 0:
+            return t, p, s0
+    t = t.clone(memory_format=torch.contiguous_format)
+    return t, t.data_ptr(), C
 
 
 def _packed(t: torch.Tensor) -> torch.Tensor:
     """``t`` contiguous and 16-byte aligned."""
     t = t.contiguous()
-    return t.clone() if t.data_ptr() % 16 else t
+    return t.clone() if t.data_ptr() & 15 else t
+
+
+def _result(out, shape, dtype, dev, unit: int):
+    """(tensor to write, elements between rows): a new one, or ``out`` after
+    its checks."""
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=dev), shape[-1]
+    if tuple(out.shape) != shape or out.dtype != dtype or out.device != dev:
+        raise ValueError(f"out: needs {dtype} {shape} on {dev}")
+    if out.data_ptr() & 15 == 0:
+        if out.is_contiguous():
+            return out, shape[-1]
+        if len(shape) == 2 and out.stride(1) == 1 and out.stride(0) >= shape[1] and out.stride(0) % unit == 0:
+            return out, out.stride(0)
+    raise ValueError("out: needs 16-byte aligned rows, packed along the last dimension")
 
 
 def _groups(offsets: torch.Tensor, dev) -> torch.Tensor:
     if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.shape[0] < 2:
         raise TypeError("offsets must be int32 [E + 1]")
-    _same_device(dev, offsets)
+    if offsets.device != dev:
+        raise ValueError(f"operands on {offsets.device} and {dev}")
     return offsets.contiguous()
 
 
-def _same_device(dev, *ts) -> None:
-    if dev.type != "cuda":
-        raise ValueError("the operands must be CUDA tensors")
-    for t in ts:
-        if t.device != dev:
-            raise ValueError(f"operands on {t.device} and {dev}")
-
-
-def _result(out, shape, dtype, dev, what: str, unit: int) -> torch.Tensor:
-    """The tensor to write: a new one, or ``out`` after its checks."""
-    if out is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    if tuple(out.shape) != tuple(shape) or out.dtype != dtype or out.device != dev:
-        raise ValueError(f"{what}: needs {dtype} {tuple(shape)} on {dev}")
-    packed = out.is_contiguous() if len(shape) != 2 else \
-        (shape[1] <= 1 or out.stride(1) == 1) and (shape[0] <= 1 or (out.stride(0) >= shape[1] and out.stride(0) % unit == 0))
-    if not packed or out.data_ptr() % 16:
-        raise ValueError(f"{what}: needs 16-byte aligned rows, packed along the last dimension")
-    return out
-
-
 def _grouped(direction, a, b, offsets, N, K, out, out_shape, out_dtype, accumulate, zero_rest, stream):
-    dev = a.device
-    _same_device(dev, b)
-    if a.dtype not in (torch.bfloat16, torch.float16) or b.dtype != a.dtype:
+    dev, dtype = a.device, a.dtype
+    if dev.type != "cuda" or b.device != dev:
+        raise ValueError(f"the operands must be on one CUDA device, not on {dev} and {b.device}")
+    if dtype is not torch.bfloat16 and dtype is not torch.float16 or b.dtype is not dtype:
         raise TypeError("the operands must be both bf16 or both f16")
     if out_dtype is None:
-        out_dtype = out.dtype if out is not None else a.dtype
-    if out_dtype not in (a.dtype, torch.float32):
+        out_dtype = out.dtype if out is not None else dtype
+    if out_dtype is not dtype and out_dtype is not torch.float32:
         raise TypeError("the output must be of the operands' type or fp32")
     offsets = _groups(offsets, dev)
-    wgrad = direction == SITU_GROUPED_WGRAD
-    out = _result(out, out_shape, out_dtype, dev, "out", 8)
-    a = _rows(a, "rows", 8)
-    b = _rows(b, "rows", 8) if wgrad else _packed(b)
-    with torch.cuda.device(dev):
-        args = SituGroupedGemmArgs(
-            direction, _DTYPES[a.dtype], _DTYPES[out_dtype], a.shape[0], N, K, offsets.shape[0] - 1, int(accumulate),
-            0 if wgrad or zero_rest else 1, a.data_ptr(), _pitch(a), b.data_ptr(), _pitch(b) if wgrad else 0,
-            offsets.data_ptr(), out.data_ptr(), 0 if wgrad else _pitch(out), _status(dev).data_ptr())
-        _check("situ_moe_grouped_gemm", lib().situ_moe_grouped_gemm(ctypes.byref(args), _stream(stream)))
+    out, ldo = _result(out, out_shape, out_dtype, dev, 8)
+    a, pa, lda = _rows(a, 8)
+    if direction == SITU_GROUPED_WGRAD:
+        b, pb, ldb = _rows(b, 8)
+    else:
+        b = _packed(b)
+        pb, ldb = b.data_ptr(), 0
+    args = SituGroupedGemmArgs(direction, _DTYPES[dtype], _DTYPES[out_dtype], a.shape[0], N, K, offsets.shape[0] - 1,
+                               1 if accumulate else 0, 0 if zero_rest else 1, pa, lda, pb, ldb, offsets.data_ptr(),
+                               out.data_ptr(), ldo, _status_word(dev.index).data_ptr())
+    _enqueue("situ_moe_grouped_gemm", ctypes.byref(args), dev=dev, stream=stream)
     return out
 
 
@@ -474,20 +487,20 @@ def situ_moe_grouped_gemm(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tenso
     situ_moe_permute returns them).  Rows of no expert give zeros, or are left
     unwritten with ``zero_rest=False``."""
     w = _experts(w, offsets)
-    if x.dim() != 2 or x.shape[1] != w.shape[2]:
+    _, N, K = w.shape
+    if x.dim() != 2 or x.shape[1] != K:
         raise ValueError("x must be [S, K]")
-    return _grouped(SITU_GROUPED_FORWARD, x, w, offsets, w.shape[1], w.shape[2], out, (x.shape[0], w.shape[1]),
-                    out_dtype, False, zero_rest, stream)
+    return _grouped(SITU_GROUPED_FORWARD, x, w, offsets, N, K, out, (x.shape[0], N), out_dtype, False, zero_rest, stream)
 
 
 def situ_moe_grouped_gemm_dgrad(dy: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, *, out=None,
                                 out_dtype=None, zero_rest: bool = True, stream=None) -> torch.Tensor:
     """The gradient of situ_moe_grouped_gemm's x: dx[r] = dy[r] @ w[e], [S, K]."""
     w = _experts(w, offsets)
-    if dy.dim() != 2 or dy.shape[1] != w.shape[1]:
+    _, N, K = w.shape
+    if dy.dim() != 2 or dy.shape[1] != N:
         raise ValueError("dy must be [S, N]")
-    return _grouped(SITU_GROUPED_DGRAD, dy, w, offsets, w.shape[1], w.shape[2], out, (dy.shape[0], w.shape[2]),
-                    out_dtype, False, zero_rest, stream)
+    return _grouped(SITU_GROUPED_DGRAD, dy, w, offsets, N, K, out, (dy.shape[0], K), out_dtype, False, zero_rest, stream)
 
 
 def situ_moe_grouped_gemm_wgrad(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor, *, out=None,
@@ -534,52 +547,55 @@ def situ_moe_quant_fp8(x: torch.Tensor, block_rows: int = 1, *, out=None, stream
         raise ValueError("x must be [R, K] or [E, R, K]")
     if block_rows not in (1, 128):
         raise ValueError("block_rows must be 1 or 128")
-    _same_device(x.device)
-    x = _rows(x, "x", 4 if x.dtype == torch.float32 else 8) if x.dim() == 2 else _packed(x)
-    R, K = x.shape[-2:]
-    E = x.shape[0] if x.dim() == 3 else 1
-    dims = (*x.shape[:-2], -(-R // block_rows), -(-K // 128))
+    dev = x.device
+    if dev.type != "cuda":
+        raise ValueError("x must be a CUDA tensor")
+    if x.dim() == 2:
+        E, (R, K) = 1, x.shape
+        x, px, ldx = _rows(x, 4 if x.dtype is torch.float32 else 8)
+        dims = (-(-R // block_rows), -(-K // 128))
+    else:
+        E, R, K = x.shape
+        x = _packed(x)
+        px, ldx = x.data_ptr(), K
+        dims = (E, -(-R // block_rows), -(-K // 128))
     if out is None:
-        q = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
-        scale = torch.empty(dims, dtype=torch.float32, device=x.device)
+        q = torch.empty(x.shape, dtype=torch.uint8, device=dev)
+        scale = torch.empty(dims, dtype=torch.float32, device=dev)
     else:
         q, scale = out
         for t, shape, dts, what in ((q, x.shape, _E4M3, "q"), (scale, dims, (torch.float32,), "scale")):
-            if tuple(t.shape) != tuple(shape) or t.dtype not in dts or t.device != x.device or not t.is_contiguous():
-                raise ValueError(f"{what}: needs a contiguous {dts[0]} tensor {tuple(shape)} on {x.device}")
-    with torch.cuda.device(x.device):
-        _check("situ_moe_quant_fp8", lib().situ_moe_quant_fp8(
-            _p(x), _DTYPES[x.dtype], E, R, K, _pitch(x) if x.dim() == 2 else K, block_rows, _p(q), _p(scale),
-            _stream(stream)))
+            if tuple(t.shape) != tuple(shape) or t.dtype not in dts or t.device != dev or not t.is_contiguous():
+                raise ValueError(f"{what}: needs a contiguous {dts[0]} tensor {tuple(shape)} on {dev}")
+    _enqueue("situ_moe_quant_fp8", px, _DTYPES[x.dtype], E, R, K, ldx, block_rows, q.data_ptr(), scale.data_ptr(),
+             dev=dev, stream=stream)
     return q, scale
 
 
-def _fp8_gemm(x_q, x_scale, w_q, w_scale, offsets, out, out_dtype, zero_rest, stream):
+def _fp8_gemm(x_q, x_scale, w_q, w_scale, E, N, K, offsets, out, out_dtype, zero_rest, stream):
     dev = x_q.device
-    _same_device(dev, x_scale, w_q, w_scale)
+    if dev.type != "cuda" or x_scale.device != dev or w_q.device != dev or w_scale.device != dev:
+        raise ValueError("the operands must be on one CUDA device")
     if x_q.dtype not in _E4M3 or w_q.dtype not in _E4M3:
         raise TypeError("x_q and w_q must hold E4M3 codes (uint8 or float8_e4m3fn)")
-    if x_scale.dtype != torch.float32 or w_scale.dtype != torch.float32:
+    if x_scale.dtype is not torch.float32 or w_scale.dtype is not torch.float32:
         raise TypeError("the scales must be fp32")
     if out_dtype is None:
         out_dtype = out.dtype if out is not None else torch.bfloat16
-    if out_dtype not in (torch.bfloat16, torch.float32):
+    if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
         raise TypeError("the output must be bf16 or fp32")
-    E, N, K = w_q.shape
-    S, nkb = x_q.shape[0], -(-K // 128)
     if x_q.dim() != 2 or x_q.shape[1] != K:
         raise ValueError("x_q must be [S, K]")
-    if tuple(x_scale.shape) != (S, nkb) or tuple(w_scale.shape) != (E, -(-N // 128), nkb):
-        raise ValueError(f"needs x_scale {(S, nkb)} and w_scale {(E, -(-N // 128), nkb)}")
-    out = _result(out, (S, N), out_dtype, dev, "out", 8)
-    x_q, w_q = _rows(x_q, "x_q", 16), _packed(w_q)
-    x_scale, w_scale = x_scale.contiguous(), w_scale.contiguous()
-    with torch.cuda.device(dev):
-        args = SituFp8GemmArgs(
-            _DTYPES[out_dtype], S, N, K, E, 0 if zero_rest else 1, x_q.data_ptr(), _pitch(x_q), x_scale.data_ptr(),
-            w_q.data_ptr(), w_scale.data_ptr(), None if offsets is None else offsets.data_ptr(), out.data_ptr(),
-            _pitch(out), _status(dev).data_ptr())
-        _check("situ_moe_fp8_gemm", lib().situ_moe_fp8_gemm(ctypes.byref(args), _stream(stream)))
+    S, nkb, nrb = x_q.shape[0], -(-K // 128), -(-N // 128)
+    if x_scale.shape != (S, nkb) or w_scale.shape != ((nrb, nkb) if w_scale.dim() == 2 and E == 1 else (E, nrb, nkb)):
+        raise ValueError(f"needs x_scale {(S, nkb)} and w_scale {(E, nrb, nkb)}")
+    out, ldo = _result(out, (S, N), out_dtype, dev, 8)
+    x_q, px, ldx = _rows(x_q, 16)
+    w_q, x_scale, w_scale = _packed(w_q), x_scale.contiguous(), w_scale.contiguous()
+    args = SituFp8GemmArgs(_DTYPES[out_dtype], S, N, K, E, 0 if zero_rest else 1, px, ldx, x_scale.data_ptr(),
+                           w_q.data_ptr(), w_scale.data_ptr(), None if offsets is None else offsets.data_ptr(),
+                           out.data_ptr(), ldo, _status_word(dev.index).data_ptr())
+    _enqueue("situ_moe_fp8_gemm", ctypes.byref(args), dev=dev, stream=stream)
     return out
 
 
@@ -590,7 +606,8 @@ def situ_moe_fp8_gemm(x_q: torch.Tensor, x_scale: torch.Tensor, w_q: torch.Tenso
     bf16 (default) or fp32 [S, N]."""
     if w_q.dim() != 2 or w_scale.dim() != 2:
         raise ValueError("w_q must be [N, K] and w_scale [ceil(N/128), ceil(K/128)]")
-    return _fp8_gemm(x_q, x_scale, w_q.unsqueeze(0), w_scale.unsqueeze(0), None, out, out_dtype, True, stream)
+    N, K = w_q.shape
+    return _fp8_gemm(x_q, x_scale, w_q, w_scale, 1, N, K, None, out, out_dtype, True, stream)
 
 
 def situ_moe_fp8_grouped_gemm(x_q: torch.Tensor, x_scale: torch.Tensor, w_q: torch.Tensor, w_scale: torch.Tensor,
@@ -601,8 +618,7 @@ def situ_moe_fp8_grouped_gemm(x_q: torch.Tensor, x_scale: torch.Tensor, w_q: tor
     unwritten with ``zero_rest=False``."""
     offsets = _groups(offsets, x_q.device)
     w_q = _experts(w_q, offsets)
-    w_scale = w_scale.unsqueeze(0) if w_scale.dim() == 2 else w_scale
-    return _fp8_gemm(x_q, x_scale, w_q, w_scale, offsets, out, out_dtype, zero_rest, stream)
+    return _fp8_gemm(x_q, x_scale, w_q, w_scale, *w_q.shape, offsets, out, out_dtype, zero_rest, stream)
 
 
 class Layer:

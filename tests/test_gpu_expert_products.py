@@ -561,7 +561,7 @@ def test_a_given_up_wait_stops_later_products():
     x = torch.ones(4, 64, dtype=torch.bfloat16, device="cuda")
     w = torch.ones(1, 64, 64, dtype=torch.bfloat16, device="cuda")
     off = offsets_of([4])
-    B._status(x.device).fill_(74)
+    B._status_word(x.device.index).fill_(74)
     out = torch.full((4, 64), 5.0, dtype=torch.bfloat16, device="cuda")
     B.situ_moe_grouped_gemm(x, w, off, out=out)
     assert (out == 5).all()
