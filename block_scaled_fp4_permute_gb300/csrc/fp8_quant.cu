@@ -34,77 +34,157 @@ struct In {
 #pragma unroll
     for (int i = 0; i < kVec; ++i) v[i] = __ldg(q + i);
   }
-  __device__ __forceinline__ void get(float* f) const {
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) {
-      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (DT == SITU_DT_F32) {
-          f[4 * i + j] = __uint_as_float(w[j]);
-        } else if (DT == SITU_DT_BF16) {
-          f[2 * j] = bf16_lo(w[j]);
-          f[2 * j + 1] = bf16_hi(w[j]);
-        } else {
-          f[2 * j] = f16_to_f32(w[j] & 0xFFFFu);
-          f[2 * j + 1] = f16_to_f32(w[j] >> 16);
-        }
-      }
+  // elements 2j and 2j + 1
+  __device__ __forceinline__ void pair(int j, float& a, float& b) const {
+    const uint4& u = v[DT == SITU_DT_F32 ? j >> 1 : 0];
+    if (DT == SITU_DT_F32) {
+      a = __uint_as_float(j & 1 ? u.z : u.x);
+      b = __uint_as_float(j & 1 ? u.w : u.y);
+    } else {
+      const uint32_t w = j == 0 ? u.x : j == 1 ? u.y : j == 2 ? u.z : u.w;
+      a = DT == SITU_DT_BF16 ? bf16_lo(w) : f16_to_f32(w & 0xFFFFu);
+      b = DT == SITU_DT_BF16 ? bf16_hi(w) : f16_to_f32(w >> 16);
     }
   }
 };
 
-// the largest magnitude as a bit pattern: ordered as the values are, with
-// infinity above every finite value and NaN above infinity
-__device__ __forceinline__ uint32_t amax_bits(const float* f) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(f[i]) & 0x7FFFFFFFu);
-  return m;
+// Magnitudes are compared as bit patterns, which are ordered as the values
+// are, with infinity above every finite value and NaN above infinity: for
+// 16-bit types two at a time.
+template <int DT>
+__device__ __forceinline__ uint32_t amax_word(uint32_t m, const uint4& v) {
+  if (DT == SITU_DT_F32)
+    return max(max(max(m, v.x & 0x7FFFFFFFu), max(v.y & 0x7FFFFFFFu, v.z & 0x7FFFFFFFu)), v.w & 0x7FFFFFFFu);
+  return __vmaxu2(__vmaxu2(__vmaxu2(m, v.x & 0x7FFF7FFFu), __vmaxu2(v.y & 0x7FFF7FFFu, v.z & 0x7FFF7FFFu)),
+                  v.w & 0x7FFF7FFFu);
 }
-__device__ __forceinline__ float scale_of(uint32_t bits) {
-  const float s = __fdiv_rn(__uint_as_float(bits), 448.f);
-  return s < kMinScale ? kMinScale : s;   // a NaN stays
+template <int DT>
+__device__ __forceinline__ uint32_t amax_join(uint32_t a, uint32_t b) {
+  return DT == SITU_DT_F32 ? max(a, b) : __vmaxu2(a, b);
 }
-__device__ __forceinline__ uint2 codes(const float* f, float s) {
+template <int DT>
+__device__ __forceinline__ float amax_value(uint32_t m) {
+  if (DT == SITU_DT_F32) return __uint_as_float(m);
+  const uint32_t h = max(m & 0xFFFFu, m >> 16);
+  return DT == SITU_DT_BF16 ? __uint_as_float(h << 16) : f16_to_f32(h);
+}
+// x / s correctly rounded, from r = 1 / s correctly rounded: a product, one
+// residual step that makes it faithful and a second that rounds it correctly
+// (Markstein, "Computation of elementary functions on the IBM RISC
+// System/6000 processor", 1990).  Needs s in [2^-80, inf): the residuals of
+// any quotient of at least 2^-20 are then exact, and a smaller one becomes
+// the code 0 all the same.  As packed pairs that is 2.5 instructions an
+// element; with divisions the kernels were bound by issue slots.
+__device__ __forceinline__ float quotient(float x, float s, float r) {
+  float q = x * r;
+  q = fmaf(fmaf(-q, s, x), r, q);
+  return fmaf(fmaf(-q, s, x), r, q);
+}
+__device__ __forceinline__ uint64_t pair64(float a, float b) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul_pair(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+// A block's scale, its negative and its reciprocal in pairs, fast = whether
+// quotient() holds for it.
+struct Scale {
+  float s;
+  bool fast;
+  uint64_t ns2, r2;
+};
+__device__ __forceinline__ Scale scale_of(float amax) {
+  Scale o;
+  // 1 / 448 correctly rounded; outside these bounds the residuals may underflow or be NaN
+  const float s = amax > 0x1p-90f && amax < INFINITY ? quotient(amax, 448.f, 1.f / 448.f) : __fdiv_rn(amax, 448.f);
+  o.s = s < kMinScale ? kMinScale : s;   // a NaN stays
+  o.fast = o.s >= 0x1p-80f && o.s < INFINITY;
+  const float r = __frcp_rn(o.s);
+  o.ns2 = pair64(-o.s, -o.s);
+  o.r2 = pair64(r, r);
+  return o;
+}
+// eight codes
+template <int DT>
+__device__ __forceinline__ uint2 codes(const In<DT>& in, const Scale& sc) {
   uint32_t c[4];
+  if (sc.fast) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) c[i] = f32x2_to_e4m3x2(__fdiv_rn(f[2 * i], s), __fdiv_rn(f[2 * i + 1], s));
+    for (int i = 0; i < 4; ++i) {
+      float a, b;
+      in.pair(i, a, b);
+      const uint64_t x = pair64(a, b);
+      uint64_t q = mul_pair(x, sc.r2);
+      q = fma_pair(fma_pair(q, sc.ns2, x), sc.r2, q);
+      q = fma_pair(fma_pair(q, sc.ns2, x), sc.r2, q);
+      asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(q));
+      c[i] = f32x2_to_e4m3x2(a, b);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float a, b;
+      in.pair(i, a, b);
+      c[i] = f32x2_to_e4m3x2(__fdiv_rn(a, sc.s), __fdiv_rn(b, sc.s));
+    }
+  }
   return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
-// A scale per 128 columns of a row: a half warp per block, kUnroll blocks in
-// flight per half warp.
-constexpr int kUnroll = 4;
+// A scale per 128 columns of a row: eight lanes per block, each with eight
+// elements of its first half and eight of its second, kUnroll blocks in
+// flight per lane.
+constexpr int kUnroll = 2;
 template <int DT>
 __global__ void __launch_bounds__(256)
 quant_fp8_rows_kernel(const void* __restrict__ x, long ldx, long R, int K, int nkb, uint8_t* __restrict__ q,
                       float* __restrict__ scale) {
-  const long hw = ((long)blockIdx.x * 256 + threadIdx.x) >> 4;
-  const int l = threadIdx.x & 15;
-  const long blocks = R * nkb, b0 = hw * kUnroll;
-  In<DT> in[kUnroll];
+  const int l = threadIdx.x & 7;
+  const long blocks = R * nkb, b0 = (((long)blockIdx.x * 256 + threadIdx.x) >> 3) * kUnroll;
+  // one division for the first block's row, 32 bits wide where that holds it
+  const long row0 = blocks <= 0xFFFFFFFFl ? (long)((uint32_t)b0 / (uint32_t)nkb) : b0 / nkb;
   long row[kUnroll];
   int col[kUnroll];
+  In<DT> in[kUnroll][2];
+  long r = row0;
+  int kb = (int)(b0 - row0 * nkb);
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) {
-    const long b = b0 + u;
-    row[u] = b / nkb;
-    col[u] = (int)(b - row[u] * nkb) * kBlk + 8 * l;
-    in[u].zero();
-    if (b < blocks && col[u] < K) in[u].load(x, (size_t)row[u] * (size_t)ldx + col[u]);
+    row[u] = r;
+    col[u] = kb * kBlk + 8 * l;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      in[u][h].zero();
+      if (r < R && col[u] + 64 * h < K) in[u][h].load(x, (size_t)r * (size_t)ldx + col[u] + 64 * h);
+    }
+    if (++kb == nkb) {
+      kb = 0;
+      ++r;
+    }
   }
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) {
-    float f[8];
-    in[u].get(f);
-    uint32_t m = amax_bits(f);
+    uint32_t m = 0;
 #pragma unroll
-    for (int d = 8; d >= 1; d >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
-    const float s = scale_of(m);
-    if (b0 + u >= blocks) continue;
-    if (col[u] < K) *reinterpret_cast<uint2*>(q + (size_t)row[u] * K + col[u]) = codes(f, s);
-    if (l == 0) scale[b0 + u] = s;
+    for (int i = 0; i < 2 * In<DT>::kVec; ++i) m = amax_word<DT>(m, in[u][i / In<DT>::kVec].v[i % In<DT>::kVec]);
+#pragma unroll
+    for (int d = 4; d >= 1; d >>= 1) m = amax_join<DT>(m, __shfl_xor_sync(0xffffffffu, m, d));
+    const Scale sc = scale_of(amax_value<DT>(m));
+    if (row[u] >= R) continue;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (col[u] + 64 * h < K)
+        *reinterpret_cast<uint2*>(q + (size_t)row[u] * K + col[u] + 64 * h) = codes<DT>(in[u][h], sc);
+    if (l == 0) scale[b0 + u] = sc.s;
   }
 }
 
@@ -129,25 +209,21 @@ quant_fp8_tiles_kernel(const void* __restrict__ x, long ldx, long lde, int R, in
     if (r + 16 * u < R && col < K) in[u].load(x, (size_t)e * lde + (size_t)(r + 16 * u) * ldx + col);
   }
 #pragma unroll
-  for (int u = 0; u < 8; ++u) {
-    float f[8];
-    in[u].get(f);
-    m = max(m, amax_bits(f));
-  }
+  for (int u = 0; u < 8; ++u)
 #pragma unroll
-  for (int d = 16; d >= 1; d >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
+    for (int i = 0; i < In<DT>::kVec; ++i) m = amax_word<DT>(m, in[u].v[i]);
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) m = amax_join<DT>(m, __shfl_xor_sync(0xffffffffu, m, d));
   if ((threadIdx.x & 31) == 0) wmax[threadIdx.x >> 5] = m;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < 8; ++w) m = max(m, wmax[w]);
-  const float s = scale_of(m);
-  if (threadIdx.x == 0) scale[b] = s;
+  for (int w = 0; w < 8; ++w) m = amax_join<DT>(m, wmax[w]);
+  const Scale sc = scale_of(amax_value<DT>(m));
+  if (threadIdx.x == 0) scale[b] = sc.s;
 #pragma unroll
   for (int u = 0; u < 8; ++u) {
     if (r + 16 * u >= R || col >= K) continue;
-    float f[8];
-    in[u].get(f);
-    *reinterpret_cast<uint2*>(q + ((size_t)e * R + r + 16 * u) * (size_t)K + col) = codes(f, s);
+    *reinterpret_cast<uint2*>(q + ((size_t)e * R + r + 16 * u) * (size_t)K + col) = codes<DT>(in[u], sc);
   }
 }
 
@@ -156,7 +232,7 @@ cudaError_t launch_dt(const void* x, long ldx, long lde, int E, int R, int K, in
                       cudaStream_t st) {
   const int nkb = (K + kBlk - 1) / kBlk;
   if (block_rows == 1) {
-    const long per = 16 * kUnroll, blocks = (long)E * R * nkb;
+    const long per = 32 * kUnroll, blocks = (long)E * R * nkb;
     quant_fp8_rows_kernel<DT><<<(unsigned)((blocks + per - 1) / per), 256, 0, st>>>(x, ldx, (long)E * R, K, nkb, q, scale);
   } else {
     const int nrb = (R + kBlk - 1) / kBlk;

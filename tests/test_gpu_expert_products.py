@@ -394,6 +394,28 @@ def test_quant_extremes(rows):
     assert (v[:rows] == 0).all() and (s[0] == 2.0 ** -126).all()
 
 
+def test_quant_codes_are_those_of_a_correct_division():
+    # blocks whose scales have random mantissas, with values at, just below
+    # and just above the midpoints between neighbouring codes: a quotient off
+    # by one unit in the last place changes a code here
+    g = gen(33)
+    R = 4096
+    grid = torch.arange(0, 127, dtype=torch.uint8).view(torch.float8_e4m3fn).float()
+    mid = ((grid[1:] + grid[:-1]) / 2).cuda()
+    x = torch.zeros(R, 128, device="cuda")
+    x[:, 0] = (1 + torch.rand(R, generator=g, device="cuda")) * torch.exp2(
+        torch.randint(-70, 100, (R,), generator=g, device="cuda").float())
+    scale = x[:, 0].cpu() / 448.0
+    v = (mid[:, None] * scale.cuda()).T                  # rounded products: within an ulp of the midpoints
+    v = (v.view(torch.int32) + torch.randint(-1, 2, v.shape, generator=g, device="cuda", dtype=torch.int32)).view(
+        torch.float32)
+    x[:, 1:127] = v
+    q, s = B.situ_moe_quant_fp8(x)
+    rq, rs = plain_quant(x, 1)
+    assert torch.equal(s.cpu(), rs)
+    assert torch.equal(q.cpu(), rq.view(torch.uint8))
+
+
 def test_quant_strided_and_out():
     g = gen(31)
     big = normal(g, 40, 400)
