@@ -169,7 +169,7 @@ f8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
         const int m0 = (t.mt * CG + (int)rank) * 128, row = t.row0 + t.c0 + half * (int)rank;
         for (int kb = 0; kb < p.nkb; ++kb, r.next()) {
           const int s = r.s;
-          if (r.used == C::kStages && !mbar_wait_warp(empty(s), r.ph ^ 1, p.err, 81)) {
+          if (r.used == C::kStages && !warp_wait(empty(s), r.ph ^ 1, p.err, 81)) {
             ok = false;
             break;
           }
@@ -182,7 +182,7 @@ f8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
         }
       }
       if (ok) {   // the last arrivals on this CTA's barriers, before it may leave
-        for (int j = 0; j < r.used; ++j) mbar_wait_warp(empty(j), j < r.s ? r.ph : r.ph ^ 1, p.err, 82);
+        for (int j = 0; j < r.used; ++j) warp_wait(empty(j), j < r.s ? r.ph : r.ph ^ 1, p.err, 82);
       } else if (rank == 0) {   // copies in flight
         for (int j = 0; j < r.used; ++j) drain_wait(full(j), j < r.s ? r.ph : r.ph ^ 1);
       } else {
@@ -203,8 +203,8 @@ f8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
         const uint32_t idesc = id0 | ((uint32_t)(nact >> 3) << 17);
         for (int kb = 0; kb < p.nkb; ++kb, r.next(), ab.next()) {
           const int s = r.s, buf = ab.s;
-          if ((ab.used == C::kBufs && !mbar_wait_warp(acc_empty(buf), ab.ph ^ 1, p.err, 83)) ||
-              !mbar_wait_warp(full(s), r.ph, p.err, 84)) {
+          if ((ab.used == C::kBufs && !warp_wait(acc_empty(buf), ab.ph ^ 1, p.err, 83)) ||
+              !warp_wait(full(s), r.ph, p.err, 84)) {
             ok = false;
             break;
           }
@@ -271,7 +271,7 @@ f8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
         const int g = kb / kSG;
         if (kb % kSG == 0 && kb + kSG < p.nkb) fetch(g + 1);
         const int buf = ab.s;
-        ok = ok && mbar_wait_warp(acc_full(buf), ab.ph, p.err, 85);
+        ok = ok && warp_wait(acc_full(buf), ab.ph, p.err, 85);
         if (!ok) {
           if (kb % kSG == kSG - 1 && kb + 1 < p.nkb) {
             bar_and(1, kEpiThreads, false);
@@ -521,7 +521,7 @@ f8w_kernel(const __grid_constant__ CUtensorMap mapX, const __grid_constant__ CUt
         const int row = t.row0 + t.t0 + 128 * (int)rank;
         for (int kb = 0; kb < p.nkb; ++kb, r.next()) {
           const int s = r.s;
-          if (r.used == C::kStages && !(mbar_wait_warp(done(0, s), r.ph ^ 1, p.err, 91) && mbar_wait_warp(done(1, s), r.ph ^ 1, p.err, 91))) {
+          if (r.used == C::kStages && !warp_wait2(done(0, s), r.ph ^ 1, done(1, s), r.ph ^ 1, p.err, 91)) {
             ok = false;
             break;
           }
@@ -537,8 +537,8 @@ f8w_kernel(const __grid_constant__ CUtensorMap mapX, const __grid_constant__ CUt
       }
       if (ok) {   // the last arrivals on this CTA's barriers, before it may leave
         for (int j = 0; j < r.used; ++j) {
-          mbar_wait_warp(done(0, j), j < r.s ? r.ph : r.ph ^ 1, p.err, 92);
-          mbar_wait_warp(done(1, j), j < r.s ? r.ph : r.ph ^ 1, p.err, 92);
+          warp_wait(done(0, j), j < r.s ? r.ph : r.ph ^ 1, p.err, 92);
+          warp_wait(done(1, j), j < r.s ? r.ph : r.ph ^ 1, p.err, 92);
         }
       } else if (rank == 0) {   // copies in flight
         for (int j = 0; j < r.used; ++j) drain_wait(full(j), j < r.s ? r.ph : r.ph ^ 1);
@@ -563,8 +563,8 @@ f8w_kernel(const __grid_constant__ CUtensorMap mapX, const __grid_constant__ CUt
           // E4M3 x E4M3 -> fp32, K-major
           const uint32_t idesc = (1u << 4) | ((uint32_t)(128 * CG >> 4) << 24) | ((uint32_t)(nact >> 3) << 17);
           for (int kb = 0; kb < p.nkb; ++kb, r.next(), ab.next()) {
-            if ((ab.used == 2 && !mbar_wait_warp(acc_empty(h, ab.s), ab.ph ^ 1, p.err, 93)) ||
-                !mbar_wait_warp(full(r.s), r.ph, p.err, 94)) {
+            // the first two blocks find their accumulators empty: any completed phase will do
+            if (!warp_wait2(acc_empty(h, ab.s), ab.ph ^ 1, full(r.s), r.ph, p.err, 93)) {
               ok = false;
               break;
             }
@@ -601,7 +601,7 @@ f8w_kernel(const __grid_constant__ CUtensorMap mapX, const __grid_constant__ CUt
         const WTile t = wide_tile_of<CG>(p, tp, idx);
         const int row = t.t0 + 128 * (int)rank, wb = t.n0 >> 7;
         for (int kb = 0; kb < p.nkb; kb += 4, sr.next()) {
-          if (sr.used == C::kSlots && !mbar_wait_warp(sc_empty(sr.s), sr.ph ^ 1, p.err, 96)) {
+          if (sr.used == C::kSlots && !warp_wait(sc_empty(sr.s), sr.ph ^ 1, p.err, 96)) {
             ok = false;
             break;
           }
@@ -632,7 +632,7 @@ f8w_kernel(const __grid_constant__ CUtensorMap mapX, const __grid_constant__ CUt
 #pragma unroll
       for (int c = 0; c < C::kCols; ++c) acc[c] = 0.f;
       for (int k0 = 0; k0 < p.nkb && ok; k0 += 4) {
-        if (!mbar_wait_warp(sc_full(sr.s), sr.ph, p.err, 97)) {
+        if (!warp_wait(sc_full(sr.s), sr.ph, p.err, 97)) {
           ok = false;
           break;
         }
@@ -651,7 +651,7 @@ f8w_kernel(const __grid_constant__ CUtensorMap mapX, const __grid_constant__ CUt
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           if (k0 + j >= p.nkb) break;
-          if (!mbar_wait_warp(done(h, r.s), r.ph, p.err, 95)) {
+          if (!warp_wait(done(h, r.s), r.ph, p.err, 95)) {
             ok = false;
             break;
           }

@@ -182,7 +182,7 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
       const int nchunk = (half + 63) / 64;
       for (int kk = 0; kk < t.nk; ++kk, r.next()) {
         const int s = r.s;
-        if (r.used == C::kStages && !mbar_wait_warp(empty(s), r.ph ^ 1, p.err, 71)) {
+        if (r.used == C::kStages && !warp_wait(empty(s), r.ph ^ 1, p.err, 71)) {
           ok = false;
           break;
         }
@@ -235,7 +235,7 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
       }
     }
     if (ok) {   // the last arrivals on this CTA's barriers, before it may leave
-      for (int j = 0; j < r.used; ++j) mbar_wait_warp(empty(j), j < r.s ? r.ph : r.ph ^ 1, p.err, 72);
+      for (int j = 0; j < r.used; ++j) warp_wait(empty(j), j < r.s ? r.ph : r.ph ^ 1, p.err, 72);
     } else if (rank == 0) {   // copies in flight
       for (int j = 0; j < r.used; ++j) drain_wait(full(j), j < r.s ? r.ph : r.ph ^ 1);
     } else {
@@ -257,7 +257,7 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
       const int nact = (t.cols + 16 * CG - 1) / (16 * CG) * (16 * CG);
       const uint32_t idesc = id0 | ((uint32_t)(nact >> 3) << 17);
       const int buf = ab.s;
-      if (ab.used == 2 && !mbar_wait_warp(acc_empty(buf), ab.ph ^ 1, p.err, 73)) {
+      if (ab.used == 2 && !warp_wait(acc_empty(buf), ab.ph ^ 1, p.err, 73)) {
         ok = false;
         break;
       }
@@ -266,7 +266,7 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
       const int len = MODE == kWgrad ? t.rows : p.L;
       for (int kk = 0; kk < t.nk; ++kk, r.next()) {
         const int s = r.s;
-        if (!mbar_wait_warp(full(s), r.ph, p.err, 74)) {
+        if (!warp_wait(full(s), r.ph, p.err, 74)) {
           ok = false;
           break;
         }
@@ -356,7 +356,7 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
         continue;
       }
       const int buf = ab.s;
-      if (!mbar_wait_warp(acc_full(buf), ab.ph, p.err, 75)) break;
+      if (!warp_wait(acc_full(buf), ab.ph, p.err, 75)) break;
       ab.next();
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const uint32_t trow = tmem + buf * TN + ((uint32_t)(32 * q) << 16);
