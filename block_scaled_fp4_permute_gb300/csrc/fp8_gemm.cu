@@ -34,6 +34,7 @@ constexpr int kThreads = 384;
 constexpr int kEpiWarp = 4;
 constexpr int kEpiThreads = 256;
 constexpr int kSG = 4;   // blocks per group of staged factors
+constexpr int kSplitLeast = 4;   // blocks that a CTA of a split tile takes at least
 
 struct F8Params {
   const int32_t* offsets;   // null: one dense group of S rows
@@ -114,7 +115,7 @@ __device__ __forceinline__ void zero_rest(const F8Params& p, int et, int per_cta
   zero_rows(out, last.x + last.y, p.S, (size_t)p.N * el, (size_t)p.ld_out * el, t, n);
 }
 
-template <int CG, int TN>
+template <int CG, int TN, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
 f8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB, const F8Params p) {
   using C = Cfg<CG, TN>;
@@ -122,6 +123,9 @@ f8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = CG == 2 ? cluster_rank() : 0;
+  const int part = SPLIT ? (int)cluster_rank() : 0, parts = SPLIT ? (int)cluster_size() : 1;
+  // a split tile's CTAs take neighbouring ranges of its blocks
+  const int kb0 = p.nkb * part / parts, kb1 = p.nkb * (part + 1) / parts;
   const uint32_t sbase = saddr(smem);
   int* tp = reinterpret_cast<int*>(smem + C::kOffTp);
   const uint32_t bar0 = sbase + C::kOffBar;
@@ -155,7 +159,7 @@ f8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
   // an earlier launch that gave up a wait leaves its code in *err: no work then
   int total = tp[p.E] * p.n_mt;
   if (*reinterpret_cast<volatile int*>(p.err) != 0) total = 0;
-  const int first = blockIdx.x / CG, stride = gridDim.x / CG;
+  const int first = blockIdx.x / (CG * parts), stride = gridDim.x / (CG * parts);
 
   if (warp < kEpiWarp) {
       if (warp == 0) {
@@ -167,7 +171,7 @@ f8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
         const Tile t = tile_of<CG, TN>(p, tp, idx);
         const int half = (t.cols + 16 * CG - 1) / (16 * CG) * 16;
         const int m0 = (t.mt * CG + (int)rank) * 128, row = t.row0 + t.c0 + half * (int)rank;
-        for (int kb = 0; kb < p.nkb; ++kb, r.next()) {
+        for (int kb = kb0; kb < kb1; ++kb, r.next()) {
           const int s = r.s;
           if (r.used == C::kStages && !warp_wait(empty(s), r.ph ^ 1, p.err, 81)) {
             ok = false;
@@ -201,7 +205,7 @@ f8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
         const Tile t = tile_of<CG, TN>(p, tp, idx);
         const int nact = (t.cols + 16 * CG - 1) / (16 * CG) * (16 * CG);
         const uint32_t idesc = id0 | ((uint32_t)(nact >> 3) << 17);
-        for (int kb = 0; kb < p.nkb; ++kb, r.next(), ab.next()) {
+        for (int kb = kb0; kb < kb1; ++kb, r.next(), ab.next()) {
           const int s = r.s, buf = ab.s;
           if ((ab.used == C::kBufs && !warp_wait(acc_empty(buf), ab.ph ^ 1, p.err, 83)) ||
               !warp_wait(full(s), r.ph, p.err, 84)) {
@@ -241,12 +245,12 @@ f8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
       const float* ws = p.ws + ((size_t)t.e * p.nrb + min(mtile, p.nrb - 1)) * p.nkb;
       float f[kPer], fw;
       auto fetch = [&](int g) {   // the factors of blocks [kSG * g, ...)
-        const int kb = kSG * g + j;
-        fw = kb < p.nkb ? __ldg(ws + kb) : 0.f;
+        const int kb = kb0 + kSG * g + j;
+        fw = kb < kb1 ? __ldg(ws + kb) : 0.f;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
           const int r = (et >> 2) + i * (kEpiThreads / kSG);
-          f[i] = (kb < p.nkb && r < t.cols) ? __ldg(xs + (size_t)r * p.nkb + kb) : 0.f;
+          f[i] = (kb < kb1 && r < t.cols) ? __ldg(xs + (size_t)r * p.nkb + kb) : 0.f;
         }
       };
       auto put = [&](int g) {
@@ -267,13 +271,13 @@ f8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
       if (!bar_and(1, kEpiThreads, ok)) break;
       put(0);
       bar_and(1, kEpiThreads, true);
-      for (int kb = 0; kb < p.nkb; ++kb, ab.next()) {
+      for (int kb = 0, n = kb1 - kb0; kb < n; ++kb, ab.next()) {
         const int g = kb / kSG;
-        if (kb % kSG == 0 && kb + kSG < p.nkb) fetch(g + 1);
+        if (kb % kSG == 0 && kb + kSG < n) fetch(g + 1);
         const int buf = ab.s;
         ok = ok && warp_wait(acc_full(buf), ab.ph, p.err, 85);
         if (!ok) {
-          if (kb % kSG == kSG - 1 && kb + 1 < p.nkb) {
+          if (kb % kSG == kSG - 1 && kb + 1 < n) {
             bar_and(1, kEpiThreads, false);
             left = true;
             break;
@@ -308,7 +312,7 @@ f8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
             fma2(acc[i][2 * c + 1], pack2(d[i & 1][4 * c + 2], d[i & 1][4 * c + 3]), s.y);
           }
         }
-        if (kb % kSG == kSG - 1 && kb + 1 < p.nkb) {
+        if (kb % kSG == kSG - 1 && kb + 1 < n) {
           put(g + 1);   // the buffer of group g - 1, which every warp left before the last barrier
           if (!bar_and(1, kEpiThreads, true)) {
             ok = false;
@@ -321,7 +325,18 @@ f8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
       if (!ok) continue;
       // column c is token row c; the warp's lanes are 32 neighbouring outputs of it
       const int m = mtile * 128 + 32 * q + lane;
-      if (m < p.N) {
+      if (SPLIT) {   // this CTA's part, [token][128], over the ring: its copies and MMAs are done
+        float* dst = reinterpret_cast<float*>(smem) + 32 * q + lane;
+#pragma unroll
+        for (int i = 0; i < C::kNch; ++i)
+#pragma unroll
+          for (int c = 0; c < C::kCh / 2; ++c) {
+            float v[2];
+            unpack2(acc[i][c], v[0], v[1]);
+            dst[((2 * i + h) * C::kCh + 2 * c) * 128] = v[0];
+            dst[((2 * i + h) * C::kCh + 2 * c + 1) * 128] = v[1];
+          }
+      } else if (m < p.N) {
 #pragma unroll
         for (int i = 0; i < C::kNch; ++i) {
           const int c0 = (2 * i + h) * C::kCh;
@@ -347,6 +362,19 @@ f8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   if (CG == 2) cluster_sync();   // no CTA leaves while the other may still signal it
+  if (SPLIT) {
+    cluster_sync();              // every part is there
+    if (first < total && *reinterpret_cast<volatile int*>(p.err) == 0) {
+      const Tile t = tile_of<CG, TN>(p, tp, first);
+      join_parts(sbase, t.cols, tid, kThreads, [&](int col, int m, float2 v) {
+        if (t.mt * 128 + m >= p.N) return;   // N is even
+        const size_t at = (size_t)(t.row0 + t.c0 + col) * (size_t)p.ld_out + t.mt * 128 + m;
+        if (p.out_f32) *reinterpret_cast<float2*>(reinterpret_cast<float*>(p.out) + at) = v;
+        else *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(p.out) + at) = f32x2_to_bf16x2(v.x, v.y);
+      });
+    }
+    cluster_sync();              // and read
+  }
   if (warp == 1) {
     __syncwarp();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -718,13 +746,17 @@ f8w_kernel(const __grid_constant__ CUtensorMap mapX, const __grid_constant__ CUt
   }
 }
 
-template <int CG, int TN>
-cudaError_t launch_t(const CUtensorMap& a, const CUtensorMap& b, const F8Params& p, long max_items, cudaStream_t st) {
+// split: CTAs per tile (SPLIT), with one tile per cluster
+template <int CG, int TN, bool SPLIT>
+cudaError_t launch_t(const CUtensorMap& a, const CUtensorMap& b, const F8Params& p, long max_items, cudaStream_t st,
+                     int split = 1) {
   static std::atomic<uint64_t> raised{0};
   const long sms = sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
-  const long ctas = max_items < sms / CG ? max_items * CG : sms / CG * CG;
-  return launch_cluster(f8_kernel<CG, TN>, &raised, CG, (int)(ctas < CG ? CG : ctas), kThreads, Cfg<CG, TN>::kSmem, st, a, b, p);
+  const int cluster = SPLIT ? split : CG;
+  const long tiles = SPLIT || max_items < sms / CG ? max_items : sms / CG;
+  return launch_cluster(f8_kernel<CG, TN, SPLIT>, &raised, cluster, (int)(tiles < 1 ? 1 : tiles) * cluster, kThreads,
+                        Cfg<CG, TN>::kSmem, st, a, b, p);
 }
 
 template <int CG>
@@ -791,10 +823,18 @@ extern "C" situ_status situ_moe_fp8_gemm(const situ_fp8_gemm_args* g, void* stre
       !make_map_nd(&mx, CU_TENSOR_MAP_DATA_TYPE_UINT8, g->x_q, 2, dx, sx, boxx))
     return SITU_ERR_CUDA;
   cudaStream_t st = (cudaStream_t)stream;
-  const long cap = items > 1e6 ? 1000000 : (long)items + 1;
-  const cudaError_t e = tn == 32    ? launch_t<1, 32>(mw, mx, p, cap, st)
-                        : tn == 64  ? launch_t<1, 64>(mw, mx, p, cap, st)
-                        : cg == 1   ? launch_wide<1>(mx, mw, p, cap, st)
-                                    : launch_wide<2>(mx, mw, p, cap, st);
+  // at most so many tiles have rows: a group of r rows has at most r, and at
+  // most (r - 1) / tm + 1
+  const double most = ((double)(g->S < g->E ? g->S : g->E) + (double)g->S / tm) * p.n_mt;
+  const long cap = most > 1e6 ? 1000000 : (long)most + 1;
+  const int split = tn < 256 ? split_of((double)cap, sm_count(), p.nkb, kSplitLeast) : 1;
+  cudaError_t e;
+  if (split > 1)
+    e = tn == 32 ? launch_t<1, 32, true>(mw, mx, p, cap, st, split) : launch_t<1, 64, true>(mw, mx, p, cap, st, split);
+  else
+    e = tn == 32   ? launch_t<1, 32, false>(mw, mx, p, cap, st)
+        : tn == 64 ? launch_t<1, 64, false>(mw, mx, p, cap, st)
+        : cg == 1  ? launch_wide<1>(mx, mw, p, cap, st)
+                   : launch_wide<2>(mx, mw, p, cap, st);
   return e == cudaSuccess ? SITU_OK : SITU_ERR_CUDA;
 }

@@ -317,6 +317,66 @@ __device__ __forceinline__ void tmem_ld_wait(uint32_t* r) {
   for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
 }
 
+// tcgen05.ld of 16 lanes x 32 columns as 8 x 8 fragments: thread t gets, of
+// eight columns i, elements (t / 4, 2 (t % 4)), (.., + 1) in r[4 i], r[4 i + 1]
+// and those of row t / 4 + 8 in r[4 i + 2], r[4 i + 3]
+__device__ __forceinline__ void tmem_ld_frag_nowait(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+// four 8 x 8 matrices of 16-bit elements stored transposed; lane l names the
+// 16 bytes of row l % 8 of matrix l / 8
+__device__ __forceinline__ void store_transposed(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
+               "r"(c), "r"(d)
+               : "memory");
+}
+
+// ---------------------------------------------------------------------------
+// Split contractions: a cluster of up to 8 CTAs takes one tile, each a part of
+// the contraction, and adds the parts up through distributed shared memory in
+// the order of the ranks (so the result does not depend on timing).  For
+// launches whose tiles alone would leave most of the GPU idle.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ float2 peer_f32x2(uint32_t addr, uint32_t rank) {
+  float2 v;
+  asm volatile("{\n .reg .b32 r;\n mapa.shared::cluster.u32 r, %2, %3;\n ld.shared::cluster.v2.f32 {%0, %1}, [r];\n}"
+               : "=f"(v.x), "=f"(v.y)
+               : "r"(addr), "r"(rank));
+  return v;
+}
+// The parts [cols][128] at `part` of every CTA, summed; emit(col, m, sums of m
+// and m + 1) for this CTA's share, over n threads of which this is number t.
+template <class Emit>
+__device__ __forceinline__ void join_parts(uint32_t part, int cols, int t, int n, Emit&& emit) {
+  const uint32_t ranks = cluster_size();
+  for (int i = (int)cluster_rank() * n + t; i < cols * 64; i += (int)ranks * n) {
+    const int col = i >> 6, m = 2 * (i & 63);
+    float2 s = make_float2(0.f, 0.f);
+    for (uint32_t r = 0; r < ranks; ++r) {
+      const float2 v = peer_f32x2(part + (uint32_t)(col * 128 + m) * 4, r);
+      s.x += v.x;
+      s.y += v.y;
+    }
+    emit(col, m, s);
+  }
+}
+// CTAs per tile: as many as fit the GPU's SMs once for `tiles` tiles and leave
+// each at least `least` of the `steps` contraction steps
+inline int split_of(double tiles, int sms, int steps, int least) {
+  int c = tiles >= 1.0 ? (int)(sms / tiles) : 1;
+  if (c > steps / least) c = steps / least;
+  return c > 8 ? 8 : c < 1 ? 1 : c;
+}
+
 // zeros to rows [from, to) of a row-major output (width and pitch in bytes,
 // multiples of 16), spread over `n` threads of which this is number `t`
 __device__ __forceinline__ void zero_rows(uint8_t* out, long from, long to, size_t width, size_t pitch, long t, long n) {

@@ -42,6 +42,8 @@ constexpr int kABytes = 128 * 128;  // 128 weights (or n) x 64 elements
 constexpr int kBoxRows = 32;        // token rows per copy (forward, dgrad)
 constexpr int kThreads = 256;
 constexpr int kEpiWarp = 4;         // first epilogue warp
+constexpr int kSplitLeast = 8;      // stages that a CTA of a split tile takes at least
+constexpr int kOutPitch = 80;       // bytes of a staged token row: 32 elements and 16 bytes
 
 struct GgParams {
   const int32_t* offsets;
@@ -59,8 +61,9 @@ struct Cfg {
   static constexpr int kTNB = TN / CG;                // N-side rows of one CTA
   static constexpr int kBBytes = kTNB * 128;
   static constexpr int kStageBytes = kABytes + kBBytes;
-  // wgrad: output staging, two 4 KB boxes per epilogue warp (and no tile prefix)
-  static constexpr int kOutBytes = MODE == kWgrad ? 4 * 2 * 4096 : 0;
+  // output staging of the four epilogue warps: wgrad two 4 KB boxes each (and
+  // no tile prefix), else 32 tokens x 32 elements at a pitch without conflicts
+  static constexpr int kOutBytes = MODE == kWgrad ? 4 * 2 * 4096 : 4 * 32 * kOutPitch;
   static constexpr int kTpBytes = MODE == kWgrad ? 0 : 4 * (kMaxGroups + 1);
   static constexpr int kMaxBytes = 232448 - 1024 - kTpBytes - kOutBytes - 512;
   static constexpr int kStages = kMaxBytes / kStageBytes;
@@ -123,7 +126,7 @@ __device__ __forceinline__ Tile tile_of(const GgParams& p, const int* tp, int id
   return t;
 }
 
-template <int CG, int MODE, int TN>
+template <int CG, int MODE, int TN, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
 gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
           const __grid_constant__ CUtensorMap mapA1, const __grid_constant__ CUtensorMap mapB1,
@@ -134,6 +137,8 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = CG == 2 ? cluster_rank() : 0;
+  static_assert(!SPLIT || (CG == 1 && MODE != kWgrad), "split tiles");
+  const int part = SPLIT ? (int)cluster_rank() : 0, parts = SPLIT ? (int)cluster_size() : 1;
   const uint32_t sbase = saddr(smem);
   int* tp = reinterpret_cast<int*>(smem + C::kOffTp);
   const uint32_t bar0 = sbase + C::kOffBar;
@@ -167,7 +172,10 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
   // an earlier launch that gave up a wait leaves its code in *err: no work then
   int total = MODE == kWgrad ? p.E * p.n_mt * p.n_nt : tp[p.E] * p.n_mt;
   if (*reinterpret_cast<volatile int*>(p.err) != 0) total = 0;
-  const int first = blockIdx.x / CG, stride = gridDim.x / CG;
+  const int first = blockIdx.x / (CG * parts), stride = gridDim.x / (CG * parts);
+  // a split tile's CTAs take neighbouring ranges of its stages
+  auto stage_from = [&](const Tile& t) { return SPLIT ? t.nk * part / parts : 0; };
+  auto stage_to = [&](const Tile& t) { return SPLIT ? t.nk * (part + 1) / parts : t.nk; };
 
   if (warp == 0) {
     // ---------------- copies ----------------
@@ -180,7 +188,7 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
       const int half = nact / CG;                                       // this CTA's part of it
       const int ma = t.m0 + 128 * (int)rank, cb = t.c0 + half * (int)rank;
       const int nchunk = (half + 63) / 64;
-      for (int kk = 0; kk < t.nk; ++kk, r.next()) {
+      for (int kk = stage_from(t), to = stage_to(t); kk < to; ++kk, r.next()) {
         const int s = r.s;
         if (r.used == C::kStages && !warp_wait(empty(s), r.ph ^ 1, p.err, 71)) {
           ok = false;
@@ -264,7 +272,8 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
       ab.next();
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const int len = MODE == kWgrad ? t.rows : p.L;
-      for (int kk = 0; kk < t.nk; ++kk, r.next()) {
+      const int from = stage_from(t);
+      for (int kk = from, to = stage_to(t); kk < to; ++kk, r.next()) {
         const int s = r.s;
         if (!warp_wait(full(s), r.ph, p.err, 74)) {
           ok = false;
@@ -279,7 +288,7 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
           // per 16 contraction elements: 32 bytes along a K-major row, 16 rows of 128 bytes else
           for (int k = 0; k < steps; ++k)
             mma_f16<CG>(tmem + buf * TN, ad + (MODE == kFwd ? 2 : 128) * k, bd + (MODE != kWgrad ? 2 : 128) * k, idesc,
-                        (kk | k) != 0);
+                        ((kk - from) | k) != 0);
           commit<CG>(empty(s));
         }
         __syncwarp();
@@ -365,12 +374,12 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
         release(buf);
         continue;
       }
-      for (int c0 = 0; c0 < t.cols; c0 += 16) {
-        float v[16];
-        __syncwarp();
-        tmem_ld16(trow + c0, v);
-        if (!vm) continue;
-        if (MODE == kWgrad) {
+      if (MODE == kWgrad) {   // dw += sums
+        for (int c0 = 0; c0 < t.cols; c0 += 16) {
+          float v[16];
+          __syncwarp();
+          tmem_ld16(trow + c0, v);
+          if (!vm) continue;
           const size_t at = ((size_t)t.e * p.M + m) * (size_t)p.ld_out + t.c0 + c0;
 #pragma unroll
           for (int g = 0; g < 2; ++g) {   // columns come in eights
@@ -399,13 +408,55 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
                                 to_16x2(w[6], w[7], p.bf16));
             }
           }
-        } else {   // column c is token row c; the warp's lanes are 32 neighbouring elements of it
-          const size_t at = (size_t)(t.row0 + t.c0 + c0) * (size_t)p.ld_out + m;
+        }
+      } else if (SPLIT) {   // this CTA's part, [token][128], over the ring: its copies and MMAs are done
+        float* dst = reinterpret_cast<float*>(smem) + 32 * q + lane;
+        for (int c0 = 0; c0 < t.cols; c0 += 16) {
+          float v[16];
+          __syncwarp();
+          tmem_ld16(trow + c0, v);
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            if (c0 + c >= t.cols) break;
-            if (p.out_f32) reinterpret_cast<float*>(p.out)[at + (size_t)c * p.ld_out] = v[c];
-            else reinterpret_cast<uint16_t*>(p.out)[at + (size_t)c * p.ld_out] = to_16(v[c], p.bf16);
+          for (int c = 0; c < 16; ++c) dst[(c0 + c) * 128] = v[c];
+        }
+      } else if (p.out_f32) {   // column c is token c; a warp's lanes are 128 bytes of its row
+        for (int c0 = 0; c0 < t.cols; c0 += 16) {
+          float v[16];
+          __syncwarp();
+          tmem_ld16(trow + c0, v);
+          if (!vm) continue;
+          float* dst = reinterpret_cast<float*>(p.out) + (size_t)(t.row0 + t.c0 + c0) * (size_t)p.ld_out + m;
+#pragma unroll
+          for (int c = 0; c < 16; ++c)
+            if (c0 + c < t.cols) dst[(size_t)c * p.ld_out] = v[c];
+        }
+      } else {
+        // transposed through shared memory, 32 tokens at a time: a store
+        // instruction is then 64 bytes of 8 token rows, where storing straight
+        // from the accumulator's layout takes 2 bytes a lane
+        const uint32_t box = sbase + C::kOffOut + q * 32 * kOutPitch;
+        const int chunk = lane & 3, n = m - lane + 8 * chunk;
+        for (int c0 = 0; c0 < t.cols; c0 += 32) {
+          uint32_t v[32];
+          __syncwarp();
+          tmem_ld_frag_nowait(trow + c0, v);
+          tmem_ld_frag_nowait(trow + (16u << 16) + c0, v + 16);
+          tmem_ld_wait<32>(v);
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            auto two = [&](int i) { return to_16x2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]), p.bf16); };
+            store_transposed(box + (8 * g + (lane & 7)) * kOutPitch + (lane >> 3) * 16, two(4 * g), two(4 * g + 2),
+                             two(16 + 4 * g), two(16 + 4 * g + 2));
+          }
+          __syncwarp();
+          if (n < p.M) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int tok = (lane >> 2) + 8 * i;
+              if (c0 + tok < t.cols)
+                *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) +
+                                          (size_t)(t.row0 + t.c0 + c0 + tok) * (size_t)p.ld_out + n) =
+                    *reinterpret_cast<const uint4*>(smem + C::kOffOut + q * 32 * kOutPitch + tok * kOutPitch + chunk * 16);
+            }
           }
         }
       }
@@ -425,6 +476,19 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   if (CG == 2) cluster_sync();   // no CTA leaves while the other may still signal it
+  if (SPLIT) {
+    cluster_sync();              // every part is there
+    if (first < total && *reinterpret_cast<volatile int*>(p.err) == 0) {
+      const Tile t = tile_of<CG, MODE, TN>(p, tp, first);
+      join_parts(sbase, t.cols, tid, kThreads, [&](int col, int m, float2 v) {
+        if (t.m0 + m >= p.M) return;   // M is even
+        const size_t at = (size_t)(t.row0 + t.c0 + col) * (size_t)p.ld_out + t.m0 + m;
+        if (p.out_f32) *reinterpret_cast<float2*>(reinterpret_cast<float*>(p.out) + at) = v;
+        else *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(p.out) + at) = to_16x2(v.x, v.y, p.bf16);
+      });
+    }
+    cluster_sync();              // and read
+  }
   if (warp == 1) {
     __syncwarp();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -437,14 +501,16 @@ struct Maps {
   CUtensorMap a, b, a1, b1, a16, b16, out;
 };
 
-template <int CG, int MODE, int TN>
-cudaError_t launch_t(const Maps& m, const GgParams& p, long max_items, cudaStream_t st) {
+// split: CTAs per tile (SPLIT), with one tile per cluster
+template <int CG, int MODE, int TN, bool SPLIT = false>
+cudaError_t launch_t(const Maps& m, const GgParams& p, long max_items, cudaStream_t st, int split = 1) {
   static std::atomic<uint64_t> raised{0};
   const long sms = sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
-  const long ctas = max_items < sms / CG ? max_items * CG : sms / CG * CG;
-  return launch_cluster(gg_kernel<CG, MODE, TN>, &raised, CG, (int)(ctas < CG ? CG : ctas), kThreads, Cfg<CG, MODE, TN>::kSmem,
-                        st, m.a, m.b, m.a1, m.b1, m.a16, m.b16, m.out, p);
+  const int cluster = SPLIT ? split : CG;
+  const long tiles = SPLIT || max_items < sms / CG ? max_items : sms / CG;
+  return launch_cluster(gg_kernel<CG, MODE, TN, SPLIT>, &raised, cluster, (int)(tiles < 1 ? 1 : tiles) * cluster, kThreads,
+                        Cfg<CG, MODE, TN>::kSmem, st, m.a, m.b, m.a1, m.b1, m.a16, m.b16, m.out, p);
 }
 
 bool fits16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -529,10 +595,19 @@ extern "C" situ_status situ_moe_grouped_gemm(const situ_grouped_gemm_args* g, vo
     ok = make_map_nd(&m.a, dt, g->b, 3, dw, sw, boxw) && make_map_nd(&m.b, dt, g->a, 2, dx, sx, boxx);
   }
   if (!ok) return SITU_ERR_CUDA;
-  const long cap = items > 1e6 ? 1000000 : (long)items + 1;
+  // at most so many tiles have rows: a group of r rows has at most r, and at
+  // most (r - 1) / tn + 1
+  const double most = ((double)(g->S < g->E ? g->S : g->E) + (double)g->S / tn) * p.n_mt;
+  const long cap = most > 1e6 ? 1000000 : (long)most + 1;
+  const int steps = (p.L + kBK - 1) / kBK;
+  const int split = tn <= 64 ? split_of((double)cap, sm_count(), steps, kSplitLeast) : 1;
   cudaError_t e;
   if (mode == kWgrad) {
-    e = cg == 2 ? launch_t<2, kWgrad, 256>(m, p, cap, st) : launch_t<1, kWgrad, 256>(m, p, cap, st);
+    const long all = items > 1e6 ? 1000000 : (long)items;
+    e = cg == 2 ? launch_t<2, kWgrad, 256>(m, p, all, st) : launch_t<1, kWgrad, 256>(m, p, all, st);
+  } else if (split > 1) {
+    e = mode == kFwd ? (tn == 32 ? launch_t<1, kFwd, 32, true>(m, p, cap, st, split) : launch_t<1, kFwd, 64, true>(m, p, cap, st, split))
+                     : (tn == 32 ? launch_t<1, kDgrad, 32, true>(m, p, cap, st, split) : launch_t<1, kDgrad, 64, true>(m, p, cap, st, split));
   } else if (mode == kFwd) {
     e = tn == 32    ? launch_t<1, kFwd, 32>(m, p, cap, st)
         : tn == 64  ? launch_t<1, kFwd, 64>(m, p, cap, st)
