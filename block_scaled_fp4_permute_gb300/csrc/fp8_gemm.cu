@@ -136,7 +136,10 @@ f8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
   const uint32_t drain = bar0 + 8 * (2 * C::kStages + 2 * C::kBufs);
   uint32_t* tm_holder = reinterpret_cast<uint32_t*>(smem + C::kOffTm);
 
+  const int failed = *reinterpret_cast<volatile int*>(p.err);   // an earlier launch gave up a wait: no work then
   if (tid == 0) {
+    prefetch_map(&mapA);
+    prefetch_map(&mapB);
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(full(s), 1);
       mbar_init(empty(s), 1);
@@ -156,9 +159,8 @@ f8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = *tm_holder;
 
-  // an earlier launch that gave up a wait leaves its code in *err: no work then
   int total = tp[p.E] * p.n_mt;
-  if (*reinterpret_cast<volatile int*>(p.err) != 0) total = 0;
+  if (failed != 0) total = 0;
   const int first = blockIdx.x / (CG * parts), stride = gridDim.x / (CG * parts);
 
   if (warp < kEpiWarp) {
@@ -503,7 +505,10 @@ f8w_kernel(const __grid_constant__ CUtensorMap mapX, const __grid_constant__ CUt
   auto sc_empty = [&](int i) { return bar0 + 8 * (3 * C::kStages + 6 + C::kSlots + i); };
   uint32_t* tm_holder = reinterpret_cast<uint32_t*>(smem + C::kOffTm);
 
+  const int failed = *reinterpret_cast<volatile int*>(p.err);   // an earlier launch gave up a wait: no work then
   if (tid == 0) {
+    prefetch_map(&mapX);
+    prefetch_map(&mapW);
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(full(s), 1);
       mbar_init(done(0, s), 1);
@@ -530,7 +535,7 @@ f8w_kernel(const __grid_constant__ CUtensorMap mapX, const __grid_constant__ CUt
   const uint32_t tmem = *tm_holder;
 
   int total = tp[p.E] * p.n_mt;
-  if (*reinterpret_cast<volatile int*>(p.err) != 0) total = 0;
+  if (failed != 0) total = 0;
   const int first = blockIdx.x / CG, stride = gridDim.x / CG;
 
   const bool xvec = (p.nkb & 3) == 0 && ((reinterpret_cast<uintptr_t>(p.xs) | reinterpret_cast<uintptr_t>(p.ws)) & 15) == 0;
@@ -808,8 +813,16 @@ extern "C" situ_status situ_moe_fp8_gemm(const situ_fp8_gemm_args* g, void* stre
   p.zero_rest = !g->keep_rest;
   p.err = g->device_status;
 
+  // Tiles: up to about 20 rows per group (one group's rows are known) 32
+  // tokens on the MMA's N side, which stream the weights and little else (40
+  // experts of 4096 x 2048, 10 / 25 / 45 rows each: 62 / 65 / 101 us, wide
+  // tiles 63 / 63 / 65); above, wide tiles, on CTA pairs from 200 rows on
+  // (112 experts, 73 rows: one CTA 0.39 ms, pairs 0.54; 64 experts, 256 rows:
+  // 187, 171 us); but 64 tokens on the N side while such tiles fit the SMs
+  // once (256 rows, 4096 x 4096: 16 us, wide 19), with the contraction split.
   const double per = (double)g->S / g->E;
-  const int tn = per <= 20 ? 32 : per <= 64 ? 64 : 256;
+  const double groups = g->S < g->E ? g->S : g->E, rows = g->S;
+  const int tn = per <= (g->E == 1 ? 32. : 20.) ? 32 : (groups + rows / 64) * ((p.N + 127) / 128) <= sm_count() ? 64 : 256;
   const int cg = tn < 256 || per < 200 ? 1 : 2;
   const int tm = tn < 256 ? tn : 128 * cg;        // tokens per tile
   p.n_mt = tn < 256 ? (p.N + 127) / 128 : (p.N + kWideN - 1) / kWideN;
@@ -825,7 +838,7 @@ extern "C" situ_status situ_moe_fp8_gemm(const situ_fp8_gemm_args* g, void* stre
   cudaStream_t st = (cudaStream_t)stream;
   // at most so many tiles have rows: a group of r rows has at most r, and at
   // most (r - 1) / tm + 1
-  const double most = ((double)(g->S < g->E ? g->S : g->E) + (double)g->S / tm) * p.n_mt;
+  const double most = (groups + rows / tm) * p.n_mt;
   const long cap = most > 1e6 ? 1000000 : (long)most + 1;
   const int split = tn < 256 ? split_of((double)cap, sm_count(), p.nkb, kSplitLeast) : 1;
   cudaError_t e;

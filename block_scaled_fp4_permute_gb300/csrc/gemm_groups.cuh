@@ -109,6 +109,10 @@ __device__ __forceinline__ void mbar_arrive_at_if(uint32_t a, uint32_t rank, boo
       : "memory");
 }
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
 template <int CG>
 __device__ __forceinline__ void tmem_alloc(uint32_t dst, uint32_t cols) {
   if (CG == 1) {

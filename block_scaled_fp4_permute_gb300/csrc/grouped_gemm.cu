@@ -149,7 +149,10 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
   const uint32_t drain = bar0 + 8 * (2 * C::kStages + 4);
   uint32_t* tm_holder = reinterpret_cast<uint32_t*>(smem + C::kOffTm);
 
+  const int failed = *reinterpret_cast<volatile int*>(p.err);   // an earlier launch gave up a wait: no work then
   if (tid == 0) {
+    prefetch_map(&mapA);
+    prefetch_map(&mapB);
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(full(s), 1);
       mbar_init(empty(s), 1);
@@ -169,9 +172,8 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = *tm_holder;
 
-  // an earlier launch that gave up a wait leaves its code in *err: no work then
   int total = MODE == kWgrad ? p.E * p.n_mt * p.n_nt : tp[p.E] * p.n_mt;
-  if (*reinterpret_cast<volatile int*>(p.err) != 0) total = 0;
+  if (failed != 0) total = 0;
   const int first = blockIdx.x / (CG * parts), stride = gridDim.x / (CG * parts);
   // a split tile's CTAs take neighbouring ranges of its stages
   auto stage_from = [&](const Tile& t) { return SPLIT ? t.nk * part / parts : 0; };
@@ -564,10 +566,21 @@ extern "C" situ_status situ_moe_grouped_gemm(const situ_grouped_gemm_args* g, vo
   p.L = mode == kDgrad ? g->N : g->K;
   p.Ncol = g->K;
 
-  // tokens per tile by the average group: a group of few rows is bound by its
-  // weights' bytes, and a narrow tile leaves the ring more stages
+  // Tokens per tile: a group of few rows is bound by its weights' bytes, and a
+  // narrow tile leaves the ring more stages; the widths leave most groups room
+  // above the average (a second tile reads the weights again, from L2).  One
+  // group's rows are known.  112 experts of 6144 x 3584 with 75 rows each: 64
+  // tokens 0.91 ms, 128 0.77, 256 0.78; 32 of 4096 x 3584 with 128: 0.26, 0.18,
+  // 0.16.  256 tokens go to CTA pairs (32 experts, 1,024 rows: 0.56 ms, single
+  // CTAs 0.60), unless tiles of 128 fit the SMs once (512 rows, 4096 x 4096:
+  // 23 us, pairs 25).
   const double per = (double)g->S / g->E;
-  const int tn = mode == kWgrad ? 256 : per <= 20 ? 32 : per <= 44 ? 64 : per <= 98 ? 128 : 256;
+  const double groups = g->S < g->E ? g->S : g->E, rows = g->S;
+  const double room[3] = {g->E == 1 ? 32. : 20., g->E == 1 ? 64. : 44., g->E == 1 ? 128. : 98.};
+  const int tn = mode == kWgrad     ? 256
+                 : per <= room[0] ? 32
+                 : per <= room[1] ? 64
+                 : per <= room[2] || (groups + rows / 128) * ((p.M + 127) / 128) <= sm_count() ? 128 : 256;
   const int cg = tn == 256 && p.M > 128 ? 2 : 1;
   p.n_mt = (p.M + 128 * cg - 1) / (128 * cg);
   p.n_nt = (p.Ncol + tn - 1) / tn;
@@ -597,17 +610,21 @@ extern "C" situ_status situ_moe_grouped_gemm(const situ_grouped_gemm_args* g, vo
   if (!ok) return SITU_ERR_CUDA;
   // at most so many tiles have rows: a group of r rows has at most r, and at
   // most (r - 1) / tn + 1
-  const double most = ((double)(g->S < g->E ? g->S : g->E) + (double)g->S / tn) * p.n_mt;
+  const double most = (groups + rows / tn) * p.n_mt;
   const long cap = most > 1e6 ? 1000000 : (long)most + 1;
   const int steps = (p.L + kBK - 1) / kBK;
-  const int split = tn <= 64 ? split_of((double)cap, sm_count(), steps, kSplitLeast) : 1;
+  const int split = tn <= 128 ? split_of((double)cap, sm_count(), steps, kSplitLeast) : 1;
   cudaError_t e;
   if (mode == kWgrad) {
     const long all = items > 1e6 ? 1000000 : (long)items;
     e = cg == 2 ? launch_t<2, kWgrad, 256>(m, p, all, st) : launch_t<1, kWgrad, 256>(m, p, all, st);
   } else if (split > 1) {
-    e = mode == kFwd ? (tn == 32 ? launch_t<1, kFwd, 32, true>(m, p, cap, st, split) : launch_t<1, kFwd, 64, true>(m, p, cap, st, split))
-                     : (tn == 32 ? launch_t<1, kDgrad, 32, true>(m, p, cap, st, split) : launch_t<1, kDgrad, 64, true>(m, p, cap, st, split));
+    e = mode == kFwd ? (tn == 32   ? launch_t<1, kFwd, 32, true>(m, p, cap, st, split)
+                        : tn == 64 ? launch_t<1, kFwd, 64, true>(m, p, cap, st, split)
+                                   : launch_t<1, kFwd, 128, true>(m, p, cap, st, split))
+                     : (tn == 32   ? launch_t<1, kDgrad, 32, true>(m, p, cap, st, split)
+                        : tn == 64 ? launch_t<1, kDgrad, 64, true>(m, p, cap, st, split)
+                                   : launch_t<1, kDgrad, 128, true>(m, p, cap, st, split));
   } else if (mode == kFwd) {
     e = tn == 32    ? launch_t<1, kFwd, 32>(m, p, cap, st)
         : tn == 64  ? launch_t<1, kFwd, 64>(m, p, cap, st)
