@@ -354,6 +354,11 @@ def situ_moe_forward_profiled(args: SituMoeArgs, workspace: torch.Tensor, events
 
 # ---------------------------------------------------------------------------
 # expert products with 16-bit and with E4M3 weights
+#
+# Each call enqueues on ``stream`` (default: the current stream of the
+# operands' device); results and copies are allocated on that stream.  A
+# first call on a device waits for it once (its status word), so it does not
+# belong inside a graph capture.
 # ---------------------------------------------------------------------------
 
 _DTYPES = {torch.bfloat16: SITU_DT_BF16, torch.float16: SITU_DT_F16, torch.float32: SITU_DT_F32}
@@ -403,18 +408,26 @@ def _empty(shape, dtype, dev: torch.device) -> torch.Tensor:
     return torch.empty(shape, dtype=dtype, device=dev)
 
 
-def _enqueue(name: str, dev: torch.device, stream, *args) -> None:
-    """Calls the C entry point ``name`` on ``dev``, its stream last."""
+def _enqueue(name: str, dev: torch.device, *args) -> None:
+    """Calls the C entry point ``name`` on ``dev`` and its current stream."""
     index = dev.index
-    raw = _raw_stream(index) if stream is None else stream.cuda_stream
     fn = getattr(_lib or lib(), name)
     if _current_device() == index:
-        status = fn(*args, raw)
+        status = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
-            status = fn(*args, raw)
+            status = fn(*args, _raw_stream(index))
     if status:
         _check(name, status)
+
+
+def _on_stream(stream, dev: torch.device, f, *args, **kw):
+    """f(*args, **kw) with ``stream`` current: what it allocates and copies
+    belongs to that stream too."""
+    if stream.device != dev:
+        raise ValueError(f"a stream of {stream.device} for operands on {dev}")
+    with torch.cuda.stream(stream):
+        return f(*args, **kw)
 
 
 def _rows(t: torch.Tensor, unit: int):
@@ -464,6 +477,9 @@ def _groups(offsets: torch.Tensor, dev) -> torch.Tensor:
 
 def _grouped(direction, a, b, offsets, N, K, out, out_shape, out_dtype, accumulate, zero_rest, stream):
     dev, dtype = a.device, a.dtype
+    if stream is not None:
+        return _on_stream(stream, dev, _grouped, direction, a, b, offsets, N, K, out, out_shape, out_dtype, accumulate,
+                          zero_rest, None)
     if dev.type != "cuda" or b.device != dev:
         raise ValueError(f"the operands must be on one CUDA device, not on {dev} and {b.device}")
     if dtype is not torch.bfloat16 and dtype is not torch.float16 or b.dtype is not dtype:
@@ -483,7 +499,7 @@ def _grouped(direction, a, b, offsets, N, K, out, out_shape, out_dtype, accumula
     args = SituGroupedGemmArgs(direction, _DTYPES[dtype], _DTYPES[out_dtype], a.shape[0], N, K, offsets.shape[0] - 1,
                                1 if accumulate else 0, 0 if zero_rest else 1, pa, lda, pb, ldb, offsets.data_ptr(),
                                out.data_ptr(), ldo, _status_word(dev.index).data_ptr())
-    _enqueue("situ_moe_grouped_gemm", dev, stream, ctypes.byref(args))
+    _enqueue("situ_moe_grouped_gemm", dev, ctypes.byref(args))
     return out
 
 
@@ -558,6 +574,8 @@ def situ_moe_quant_fp8(x: torch.Tensor, block_rows: int = 1, *, out=None, stream
     scales per block of 128): block_rows 1, a scale per row and 128 columns
     (activations); 128, one per 128 x 128 block (weights)."""
     dev, dtype, dim = x.device, _DTYPES.get(x.dtype), x.dim()
+    if stream is not None:
+        return _on_stream(stream, dev, situ_moe_quant_fp8, x, block_rows, out=out)
     if dtype is None:
         raise TypeError("x must be bf16, f16 or fp32")
     if dev.type != "cuda":
@@ -582,12 +600,15 @@ def situ_moe_quant_fp8(x: torch.Tensor, block_rows: int = 1, *, out=None, stream
         for t, want, dts, what in ((q, shape, _E4M3, "q"), (scale, dims, (torch.float32,), "scale")):
             if tuple(t.shape) != want or t.dtype not in dts or t.device != dev or not t.is_contiguous():
                 raise ValueError(f"{what}: needs a contiguous {dts[0]} tensor {want} on {dev}")
-    _enqueue("situ_moe_quant_fp8", dev, stream, px, dtype, E, R, K, ldx, block_rows, q.data_ptr(), scale.data_ptr())
+    _enqueue("situ_moe_quant_fp8", dev, px, dtype, E, R, K, ldx, block_rows, q.data_ptr(), scale.data_ptr())
     return q, scale
 
 
 def _fp8_gemm(x_q, x_scale, w_q, w_scale, E, N, K, offsets, out, out_dtype, zero_rest, stream):
     dev = x_q.device
+    if stream is not None:
+        return _on_stream(stream, dev, _fp8_gemm, x_q, x_scale, w_q, w_scale, E, N, K, offsets, out, out_dtype,
+                          zero_rest, None)
     if dev.type != "cuda" or x_scale.device != dev or w_q.device != dev or w_scale.device != dev:
         raise ValueError("the operands must be on one CUDA device")
     if x_q.dtype not in _E4M3 or w_q.dtype not in _E4M3:
@@ -609,7 +630,7 @@ def _fp8_gemm(x_q, x_scale, w_q, w_scale, E, N, K, offsets, out, out_dtype, zero
     args = SituFp8GemmArgs(_DTYPES[out_dtype], S, N, K, E, 0 if zero_rest else 1, px, ldx, x_scale.data_ptr(),
                            w_q.data_ptr(), w_scale.data_ptr(), None if offsets is None else offsets.data_ptr(),
                            out.data_ptr(), ldo, _status_word(dev.index).data_ptr())
-    _enqueue("situ_moe_fp8_gemm", dev, stream, ctypes.byref(args))
+    _enqueue("situ_moe_fp8_gemm", dev, ctypes.byref(args))
     return out
 
 

@@ -144,6 +144,29 @@ def test_wide_persistent_walk(counts):
         assert_sum(got, ref, mag, L, torch.bfloat16)
 
 
+# one case per kernel form, by the rules on sizes (a GPU of 152 SMs): tiles of
+# 32, 64 and 128 tokens whose contraction is split over a cluster, with odd
+# shares of the stages; 128 and 256 tokens unsplit; a single CTA at 256 tokens
+# (M side of at most 128)
+FORMS = [([5], 136, 2056), ([5, 0, 20], 264, 2056), ([50], 200, 1032), ([90], 136, 1544), ([44, 40, 0, 30], 72, 1100 // 4 * 8),
+         ([90, 60, 0, 97, 80, 70, 88, 99], 1416, 200), ([150, 300, 0, 260, 129, 1, 90], 2056, 136),
+         ([700, 5, 900], 2312, 72), ([16000], 128, 128), ([9000, 0, 10000], 72, 120)]
+
+
+@pytest.mark.parametrize("form", range(len(FORMS)))
+@pytest.mark.parametrize("direction", ["forward", "dgrad"])
+def test_every_form_of_the_grouped_product(form, direction):
+    counts, M, L = FORMS[form]
+    N, K = (M, L) if direction == "forward" else (L, M)
+    S = 1 + sum(counts) + 2
+    dtype = (torch.bfloat16, torch.float16)[form % 2]
+    a, b, L = operands(direction, gen(form), S, len(counts), N, K, dtype)
+    for out_dtype in (dtype, torch.float32):
+        got = call(direction, a, b, offsets_of(counts, 1), out_dtype=out_dtype)
+        ref, mag = reference(direction, a, b, counts, 1, S, N, K)
+        assert_sum(got, ref, mag, L, out_dtype)
+
+
 @pytest.mark.parametrize("direction", ["forward", "dgrad", "wgrad"])
 @pytest.mark.parametrize("counts", [[5, 0, 18, 1, 40], [200, 0, 333, 70]])
 def test_infinities_and_nans_stay_in_their_group(direction, counts):
@@ -478,6 +501,68 @@ def test_fp8_dense_matches_64_bit_sums(S, N, K):
         got = B.situ_moe_fp8_gemm(xq, xs, wq[0], ws[0], out_dtype=out_dtype)
         ref, mag = fp8_reference(xq, xs, wq, ws, [S], 0)
         assert_sum(got, ref, mag, K, out_dtype)
+
+
+# wide tiles on one CTA and on pairs, with N's last tile in its first half, at
+# its end and in its second half, K's last block partial, and groups that end
+# in either CTA's rows; then the narrow forms split over clusters
+@pytest.mark.parametrize("counts,N,K", [
+    ([75, 0, 128, 129, 40, 90, 3, 200, 110], 2056, 208), ([60, 70, 80, 90, 100, 50, 40, 130], 2048, 1040),
+    ([257, 600, 0, 1, 511, 256], 2184, 144), ([640, 128, 700], 2056, 1168), ([900], 1928, 272),
+    ([17], 264, 4112), ([3, 0, 12, 9], 136, 2064), ([64], 264, 3088), ([100, 20], 136, 2192)])
+def test_every_form_of_the_fp8_product(counts, N, K):
+    S = 2 + sum(counts) + 3
+    ops = fp8_operands(gen(N + K), S, len(counts), N, K)
+    ref, mag = fp8_reference(*ops, counts, 2)
+    for out_dtype in (torch.bfloat16, torch.float32):
+        got = B.situ_moe_fp8_grouped_gemm(*ops, offsets_of(counts, 2), out_dtype=out_dtype)
+        assert_sum(got, ref, mag, K, out_dtype)
+
+
+def test_fp8_nan_and_infinite_scales_stay_in_their_rows():
+    # wide tiles: a NaN code in one row, an infinite scale in another, and rows
+    # of no group full of NaN, leave every other row alone
+    counts, N, K = [300, 0, 400, 350], 2056, 400
+    S = 4 + sum(counts) + 2
+    xq, xs, wq, ws = fp8_operands(gen(44), S, 4, N, K)
+    xq[:4] = 0x7F
+    xs[-2:] = float("nan")
+    xq[4 + 299, 7] = 0x7F
+    xs[4 + 300, 1] = float("inf")
+    y = B.situ_moe_fp8_grouped_gemm(xq, xs, wq, ws, offsets_of(counts, 4), out_dtype=torch.float32)
+    xq[4 + 299, 7], xs[4 + 300, 1] = 0, 1.0
+    ref, mag = fp8_reference(xq[4:-2], xs[4:-2], wq, ws, counts, 0)
+    assert (y[:4] == 0).all() and (y[-2:] == 0).all()
+    assert y[4 + 299].isnan().all() and not y[4 + 300].isfinite().any()
+    keep = torch.ones(sum(counts), dtype=torch.bool)
+    keep[299:301] = False
+    assert_sum(y[4:-2][keep.cuda()], ref[keep], mag[keep], K, torch.float32)
+
+
+def test_fp8_bad_offsets_stay_inside_the_operands():
+    for S, N, K in ((50, 64, 64), (900, 2056, 144)):
+        xq, xs, wq, ws = fp8_operands(gen(45), S, 4, N, K)
+        off = torch.tensor([0, 10, 5, 2000000000, 60], dtype=torch.int32, device="cuda")
+        y = B.situ_moe_fp8_grouped_gemm(xq, xs, wq, ws, off)
+        assert y.shape == (S, N) and B.situ_moe_gemm_status() == 0
+
+
+def test_fp8_split_repeats_bits_and_other_streams():
+    xq, xs, wq, ws = fp8_operands(gen(46), 9, 1, 264, 4112)
+    y1 = B.situ_moe_fp8_gemm(xq, xs, wq[0], ws[0], out_dtype=torch.float32)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    y2 = B.situ_moe_fp8_gemm(xq, xs, wq[0], ws[0], out_dtype=torch.float32, stream=s)
+    # a layout that is copied first: the copy belongs to that stream as well
+    wide = torch.zeros(9, 4112 + 48, dtype=torch.uint8, device="cuda")
+    wide[:, 5:5 + 4112] = xq
+    s.wait_stream(torch.cuda.current_stream())
+    y3 = B.situ_moe_fp8_gemm(wide[:, 5:5 + 4112], xs, wq[0], ws[0], out_dtype=torch.float32, stream=s)
+    q, sc = B.situ_moe_quant_fp8(y1, stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(y1, y2) and torch.equal(y1, y3)
+    q2, sc2 = B.situ_moe_quant_fp8(y1)
+    assert torch.equal(q, q2) and torch.equal(sc, sc2)
 
 
 def test_fp8_rows_of_no_expert_and_other_groups():
