@@ -44,6 +44,8 @@ constexpr int kThreads = 256;
 constexpr int kEpiWarp = 4;         // first epilogue warp
 constexpr int kSplitLeast = 8;      // stages that a CTA of a split tile takes at least
 constexpr int kOutPitch = 80;       // bytes of a staged token row: 32 elements and 16 bytes
+constexpr int kOutPitchF = 144;     // the same of 32 floats; 16 rows
+static_assert(16 * kOutPitchF <= 32 * kOutPitch, "staging");
 
 struct GgParams {
   const int32_t* offsets;
@@ -420,16 +422,29 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
 #pragma unroll
           for (int c = 0; c < 16; ++c) dst[(c0 + c) * 128] = v[c];
         }
-      } else if (p.out_f32) {   // column c is token c; a warp's lanes are 128 bytes of its row
+      } else if (p.out_f32) {
+        // through shared memory, 16 tokens x 32 elements at a time: 16-byte
+        // stores of 4 token rows each, where one column a store (128 bytes of
+        // a row) made the epilogue 2.5 times as long as a 16-bit one
+        const int chunk = lane & 7, n = m - lane + 4 * chunk;
+        uint8_t* box = smem + C::kOffOut + q * 32 * kOutPitch;
         for (int c0 = 0; c0 < t.cols; c0 += 16) {
           float v[16];
           __syncwarp();
           tmem_ld16(trow + c0, v);
-          if (!vm) continue;
-          float* dst = reinterpret_cast<float*>(p.out) + (size_t)(t.row0 + t.c0 + c0) * (size_t)p.ld_out + m;
 #pragma unroll
-          for (int c = 0; c < 16; ++c)
-            if (c0 + c < t.cols) dst[(size_t)c * p.ld_out] = v[c];
+          for (int c = 0; c < 16; ++c) *reinterpret_cast<float*>(box + c * kOutPitchF + 4 * lane) = v[c];
+          __syncwarp();
+          if (n < p.M) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int tok = (lane >> 3) + 4 * i;
+              if (c0 + tok < t.cols)
+                *reinterpret_cast<uint4*>(reinterpret_cast<float*>(p.out) +
+                                          (size_t)(t.row0 + t.c0 + c0 + tok) * (size_t)p.ld_out + n) =
+                    *reinterpret_cast<const uint4*>(box + tok * kOutPitchF + chunk * 16);
+            }
+          }
         }
       } else {
         // transposed through shared memory, 32 tokens at a time: a store
