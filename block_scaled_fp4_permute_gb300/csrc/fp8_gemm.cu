@@ -34,6 +34,8 @@ constexpr int kThreads = 384;
 constexpr int kEpiWarp = 4;
 constexpr int kEpiThreads = 256;
 constexpr int kSG = 4;   // blocks per group of staged factors
+constexpr int kOutPitch = 80, kOutPitchF = 144;   // bytes of a staged token row of 32 outputs, bf16 and fp32
+constexpr int kBoxBytes = 32 * kOutPitch;         // of a warp: 32 rows of bf16, 16 of fp32
 constexpr int kSplitLeast = 4;   // blocks that a CTA of a split tile takes at least
 
 struct F8Params {
@@ -57,11 +59,13 @@ struct Cfg {
   static constexpr int kBufs = TN >= 256 ? 2 : 4;              // TMEM accumulators
   static constexpr int kSPitch = TN + 8;                       // staged factors, conflict-free rows
   static constexpr int kSBytes = 2 * kSG * kSPitch * 4;
-  static constexpr int kMaxBytes = 232448 - 1024 - 4 * (kMaxGroups + 1) - 512 - kSBytes;
+  static constexpr int kOutBytes = 8 * kBoxBytes;              // output staging
+  static constexpr int kMaxBytes = 232448 - 1024 - 4 * (kMaxGroups + 1) - 512 - kSBytes - kOutBytes;
   static constexpr int kStages = kMaxBytes / kStageBytes;
   static constexpr int kOffB = kStages * kABytes;
   static constexpr int kOffS = kOffB + kStages * kBBytes;
-  static constexpr int kOffTp = kOffS + kSBytes;
+  static constexpr int kOffOut = kOffS + kSBytes;
+  static constexpr int kOffTp = kOffOut + kOutBytes;
   static constexpr int kOffBar = (kOffTp + 4 * (kMaxGroups + 1) + 15) / 16 * 16;
   static constexpr int kNumBars = 2 * kStages + 2 * kBufs + 1;
   static constexpr int kOffTm = kOffBar + 8 * kNumBars;
@@ -325,8 +329,7 @@ f8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
       }
       if (left) break;
       if (!ok) continue;
-      // column c is token row c; the warp's lanes are 32 neighbouring outputs of it
-      const int m = mtile * 128 + 32 * q + lane;
+      // column c is token c; a warp's lanes are 32 neighbouring outputs of it
       if (SPLIT) {   // this CTA's part, [token][128], over the ring: its copies and MMAs are done
         float* dst = reinterpret_cast<float*>(smem) + 32 * q + lane;
 #pragma unroll
@@ -338,22 +341,37 @@ f8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
             dst[((2 * i + h) * C::kCh + 2 * c) * 128] = v[0];
             dst[((2 * i + h) * C::kCh + 2 * c + 1) * 128] = v[1];
           }
-      } else if (m < p.N) {
+      } else {
+        // through shared memory, 16 tokens at a time: 16-byte stores
+        uint8_t* box = smem + C::kOffOut + (warp - kEpiWarp) * kBoxBytes;
+        const int el = p.out_f32 ? 4 : 2, pitch = p.out_f32 ? kOutPitchF : kOutPitch;
+        const int cpr = 2 * el, chunk = lane & (cpr - 1);   // 16-byte chunks of a row
+        const int nn = mtile * 128 + 32 * q + chunk * (16 / el);
 #pragma unroll
         for (int i = 0; i < C::kNch; ++i) {
-          const int c0 = (2 * i + h) * C::kCh;
-          const int el = p.out_f32 ? 4 : 2;
-          const size_t pitch = (size_t)p.ld_out * el;
-          uint8_t* dst = reinterpret_cast<uint8_t*>(p.out) + (size_t)(t.row0 + t.c0 + c0) * pitch + (size_t)m * el;
 #pragma unroll
-          for (int c = 0; c < C::kCh; ++c) {
-            if (c0 + c >= t.cols) break;
-            float v[2];
-            unpack2(acc[i][c >> 1], v[0], v[1]);
-            if (p.out_f32) *reinterpret_cast<float*>(dst) = v[c & 1];
-            else *reinterpret_cast<__nv_bfloat16*>(dst) = __float2bfloat16_rn(v[c & 1]);
-            dst += pitch;
-            asm volatile("" : "+l"(dst));   // one running pointer, not kCh addresses in registers
+          for (int c0 = 0; c0 < C::kCh; c0 += 16) {
+            const int col = (2 * i + h) * C::kCh + c0;
+            if (col >= t.cols) continue;
+            __syncwarp();
+#pragma unroll
+            for (int c = 0; c < 16; c += 2) {
+              float v[2];
+              unpack2(acc[i][(c0 + c) >> 1], v[0], v[1]);
+              if (p.out_f32) {
+                *reinterpret_cast<float*>(box + c * kOutPitchF + 4 * lane) = v[0];
+                *reinterpret_cast<float*>(box + (c + 1) * kOutPitchF + 4 * lane) = v[1];
+              } else {
+                *reinterpret_cast<__nv_bfloat16*>(box + c * kOutPitch + 2 * lane) = __float2bfloat16_rn(v[0]);
+                *reinterpret_cast<__nv_bfloat16*>(box + (c + 1) * kOutPitch + 2 * lane) = __float2bfloat16_rn(v[1]);
+              }
+            }
+            __syncwarp();
+            for (int tok = lane / cpr; tok < 16; tok += 32 / cpr)
+              if (nn < p.N && col + tok < t.cols)
+                *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) +
+                                          ((size_t)(t.row0 + t.c0 + col + tok) * (size_t)p.ld_out + nn) * el) =
+                    *reinterpret_cast<const uint4*>(box + tok * pitch + chunk * 16);
           }
         }
       }

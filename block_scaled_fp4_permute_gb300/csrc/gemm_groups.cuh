@@ -373,6 +373,14 @@ __device__ __forceinline__ void join_parts(uint32_t part, int cols, int t, int n
     emit(col, m, s);
   }
 }
+__device__ __forceinline__ float4 peer_f32x4(uint32_t addr, uint32_t rank) {
+  float4 v;
+  asm volatile(
+      "{\n .reg .b32 r;\n mapa.shared::cluster.u32 r, %4, %5;\n ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [r];\n}"
+      : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+      : "r"(addr), "r"(rank));
+  return v;
+}
 // CTAs per tile: as many as fit the GPU's SMs once for `tiles` tiles and leave
 // each at least `least` of the `steps` contraction steps
 inline int split_of(double tiles, int sms, int steps, int least) {

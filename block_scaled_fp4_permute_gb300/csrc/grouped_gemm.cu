@@ -43,6 +43,7 @@ constexpr int kBoxRows = 32;        // token rows per copy (forward, dgrad)
 constexpr int kThreads = 256;
 constexpr int kEpiWarp = 4;         // first epilogue warp
 constexpr int kSplitLeast = 8;      // stages that a CTA of a split tile takes at least
+constexpr int kPartPitch = 260;     // floats of a row of a split wgrad tile's part: 256 and 4
 constexpr int kOutPitch = 80;       // bytes of a staged token row: 32 elements and 16 bytes
 constexpr int kOutPitchF = 144;     // the same of 32 floats; 16 rows
 static_assert(16 * kOutPitchF <= 32 * kOutPitch, "staging");
@@ -128,6 +129,40 @@ __device__ __forceinline__ Tile tile_of(const GgParams& p, const int* tp, int id
   return t;
 }
 
+// Adds up the parts of a split wgrad tile: this CTA's share of its rows, four
+// k per thread, over the parts that had stages.
+__device__ __forceinline__ void join_dw(const GgParams& p, const Tile& t, uint32_t part_at, int part, int parts, int tid) {
+  const int quads = (t.cols + 3) / 4, rows = min(128, p.M - t.m0);   // columns come in eights
+  for (int i = part * kThreads + tid; i < rows * quads; i += parts * kThreads) {
+    const int n = i / quads, c = 4 * (i - n * quads);
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int r = 0; r < parts; ++r) {
+      if (t.nk * r / parts == t.nk * (r + 1) / parts) continue;
+      const float4 v = peer_f32x4(part_at + (uint32_t)(n * kPartPitch + c) * 4, (uint32_t)r);
+      s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
+    }
+    const size_t at = ((size_t)t.e * p.M + t.m0 + n) * (size_t)p.ld_out + t.c0 + c;
+    if (p.out_f32) {
+      float4* dst = reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + at);
+      if (p.accumulate) {
+        const float4 o = *dst;
+        s = make_float4(s.x + o.x, s.y + o.y, s.z + o.z, s.w + o.w);
+      }
+      *dst = s;
+    } else {
+      uint2* dst = reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.out) + at);
+      if (p.accumulate) {
+        const uint2 o = *dst;
+        s.x += from_16(o.x & 0xFFFFu, p.bf16);
+        s.y += from_16(o.x >> 16, p.bf16);
+        s.z += from_16(o.y & 0xFFFFu, p.bf16);
+        s.w += from_16(o.y >> 16, p.bf16);
+      }
+      *dst = make_uint2(to_16x2(s.x, s.y, p.bf16), to_16x2(s.z, s.w, p.bf16));
+    }
+  }
+}
+
 template <int CG, int MODE, int TN, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
 gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
@@ -139,7 +174,7 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = CG == 2 ? cluster_rank() : 0;
-  static_assert(!SPLIT || (CG == 1 && MODE != kWgrad), "split tiles");
+  static_assert(!SPLIT || CG == 1, "split tiles");
   const int part = SPLIT ? (int)cluster_rank() : 0, parts = SPLIT ? (int)cluster_size() : 1;
   const uint32_t sbase = saddr(smem);
   int* tp = reinterpret_cast<int*>(smem + C::kOffTp);
@@ -265,7 +300,7 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
                          (MODE == kWgrad ? 1u << 16 : 0u) | ((uint32_t)(128 * CG >> 4) << 24);
     for (int idx = first; idx < total && ok; idx += stride) {
       const Tile t = tile_of<CG, MODE, TN>(p, tp, idx);
-      if (t.nk == 0) continue;
+      if (stage_from(t) == stage_to(t)) continue;
       const int nact = (t.cols + 16 * CG - 1) / (16 * CG) * (16 * CG);
       const uint32_t idesc = id0 | ((uint32_t)(nact >> 3) << 17);
       const int buf = ab.s;
@@ -364,8 +399,8 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
       const Tile t = tile_of<CG, MODE, TN>(p, tp, idx);
       const int m = t.m0 + 128 * (int)rank + 32 * q + lane;
       const bool vm = m < p.M;
-      if (MODE == kWgrad && t.nk == 0) {   // an expert without rows
-        if (!p.accumulate) store_dw(t, m - lane, 0, false);
+      if (MODE == kWgrad && stage_from(t) == stage_to(t)) {   // an expert without rows; a part without stages
+        if (!SPLIT && !p.accumulate) store_dw(t, m - lane, 0, false);
         continue;
       }
       const int buf = ab.s;
@@ -373,12 +408,21 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
       ab.next();
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const uint32_t trow = tmem + buf * TN + ((uint32_t)(32 * q) << 16);
-      if (MODE == kWgrad && !p.accumulate) {
+      if (MODE == kWgrad && !SPLIT && !p.accumulate) {
         store_dw(t, m - lane, trow, true);
         release(buf);
         continue;
       }
-      if (MODE == kWgrad) {   // dw += sums
+      if (MODE == kWgrad && SPLIT) {   // this CTA's part, [n][k], over the ring: its copies and MMAs are done
+        float* dst = reinterpret_cast<float*>(smem) + (32 * q + lane) * kPartPitch;
+        for (int c0 = 0; c0 < t.cols; c0 += 16) {
+          float v[16];
+          __syncwarp();
+          tmem_ld16(trow + c0, v);
+#pragma unroll
+          for (int c = 0; c < 16; c += 4) *reinterpret_cast<float4*>(dst + c0 + c) = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
+        }
+      } else if (MODE == kWgrad) {   // dw += sums
         for (int c0 = 0; c0 < t.cols; c0 += 16) {
           float v[16];
           __syncwarp();
@@ -497,7 +541,8 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
     cluster_sync();              // every part is there
     if (first < total && *reinterpret_cast<volatile int*>(p.err) == 0) {
       const Tile t = tile_of<CG, MODE, TN>(p, tp, first);
-      join_parts(sbase, t.cols, tid, kThreads, [&](int col, int m, float2 v) {
+      if (MODE == kWgrad) join_dw(p, t, sbase, part, parts, tid);
+      else join_parts(sbase, t.cols, tid, kThreads, [&](int col, int m, float2 v) {
         if (t.m0 + m >= p.M) return;   // M is even
         const size_t at = (size_t)(t.row0 + t.c0 + col) * (size_t)p.ld_out + t.m0 + m;
         if (p.out_f32) *reinterpret_cast<float2*>(reinterpret_cast<float*>(p.out) + at) = v;
@@ -596,7 +641,12 @@ extern "C" situ_status situ_moe_grouped_gemm(const situ_grouped_gemm_args* g, vo
                  : per <= room[0] ? 32
                  : per <= room[1] ? 64
                  : per <= room[2] || (groups + rows / 128) * ((p.M + 127) / 128) <= sm_count() ? 128 : 256;
-  const int cg = tn == 256 && p.M > 128 ? 2 : 1;
+  // wgrad of few output tiles: the rows of a group split over clusters (a
+  // skewed group's rows are taken as up to twice the average)
+  const double wtiles = (double)p.E * ((p.M + 127) / 128) * ((p.Ncol + 255) / 256);
+  const int wsteps = (int)((g->E > 1 ? 2 * per : per) / kBK);
+  const int wsplit = mode == kWgrad ? split_of(wtiles, sm_count(), wsteps, kSplitLeast) : 1;
+  const int cg = tn == 256 && p.M > 128 && wsplit == 1 ? 2 : 1;
   p.n_mt = (p.M + 128 * cg - 1) / (128 * cg);
   p.n_nt = (p.Ncol + tn - 1) / tn;
   const double items = mode == kWgrad ? (double)p.E * p.n_mt * p.n_nt : ((double)g->S / tn + p.E) * p.n_mt;
@@ -630,7 +680,9 @@ extern "C" situ_status situ_moe_grouped_gemm(const situ_grouped_gemm_args* g, vo
   const int steps = (p.L + kBK - 1) / kBK;
   const int split = tn <= 128 ? split_of((double)cap, sm_count(), steps, kSplitLeast) : 1;
   cudaError_t e;
-  if (mode == kWgrad) {
+  if (mode == kWgrad && wsplit > 1) {
+    e = launch_t<1, kWgrad, 256, true>(m, p, (long)items, st, wsplit);
+  } else if (mode == kWgrad) {
     const long all = items > 1e6 ? 1000000 : (long)items;
     e = cg == 2 ? launch_t<2, kWgrad, 256>(m, p, all, st) : launch_t<1, kWgrad, 256>(m, p, all, st);
   } else if (split > 1) {

@@ -167,6 +167,29 @@ def test_every_form_of_the_grouped_product(form, direction):
         assert_sum(got, ref, mag, L, out_dtype)
 
 
+@pytest.mark.parametrize("counts,N,K", [([3000], 152, 264), ([1700, 0, 5, 900, 64, 63], 136, 72), ([5000, 1], 8, 8),
+                                        ([700, 1500], 264, 520), ([9999], 1000, 72)])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_weight_gradient_split_over_rows(counts, N, K, accumulate):
+    # few output tiles: a cluster takes one tile, each CTA some of the rows;
+    # groups with fewer stages than CTAs, and with none
+    S = 3 + sum(counts) + 1
+    dy, x, L = operands("wgrad", gen(N), S, len(counts), N, K, torch.bfloat16)
+    x[:3] = float("nan")
+    dy[-1:] = float("inf")
+    old = normal(gen(1), len(counts), N, K, dtype=torch.float32)
+    off = offsets_of(counts, 3)
+    ref, mag = reference("wgrad", dy, x, counts, 3, S, N, K)
+    for out_dtype in (torch.bfloat16, torch.float32):
+        out = old.to(out_dtype)
+        o = out.double().cpu() if accumulate else 0.0
+        got = B.situ_moe_grouped_gemm_wgrad(dy, x, off, out=out, accumulate=accumulate)
+        assert_sum(got, ref + o, mag + abs(o), L, out_dtype)
+        again = old.to(out_dtype)
+        B.situ_moe_grouped_gemm_wgrad(dy, x, off, out=again, accumulate=accumulate)
+        assert torch.equal(again, got)
+
+
 @pytest.mark.parametrize("direction", ["forward", "dgrad", "wgrad"])
 @pytest.mark.parametrize("counts", [[5, 0, 18, 1, 40], [200, 0, 333, 70]])
 def test_infinities_and_nans_stay_in_their_group(direction, counts):
