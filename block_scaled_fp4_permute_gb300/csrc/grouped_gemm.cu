@@ -13,22 +13,30 @@
 // dgrad; dy and x in wgrad), both as 128-byte-swizzled TMA tiles.
 //
 // Per CTA: warp 0 copies stages of 64 contraction elements into a ring,
-// warp 1 issues the MMAs into two TMEM accumulators in turn, warps 4..7 read
+// warp 1 issues the MMAs into two TMEM accumulators in turn, warps 4..11 read
 // the accumulator of the previous tile and store it meanwhile.  CTAs are
 // persistent and walk the tiles with a fixed stride.
 //
 // The contraction's end: k and n past the weight's extent read as zeros (the
 // maps end there; w is a 3D map, so that rows past n = N do not run into the
 // next expert).  In wgrad the contraction runs over a group's rows and ends
-// anywhere: a last stage of fewer than 64 rows is fetched row by row (gather
-// of four), with the rows past the group's end named out of bounds, so that
-// the MMA sees zeros in both operands there (a zero in one of them would not
-// do: the neighbour's rows may hold infinities).
+// anywhere: a last stage of fewer than 64 rows comes in whole sixteens and one
+// gather of the rest, with the rows past the group's end named out of bounds,
+// so that the MMA sees zeros in both operands there (a zero in one of them
+// would not do: the neighbour's rows may hold infinities).
+//
+// Large groups run on CTA pairs (cta_group::2, 256 x 256 per pair: each CTA
+// copies half of the N-side operand, so a stage is 32 KB per CTA and not 48).
+// Launches of few tiles split the contraction over a cluster.
+//
+// Measured (bf16, 4096 x 3584, 32 experts, 1,024 rows each): forward 0.53 to
+// 0.56 ms, dgrad 0.56, wgrad 0.59, that is 1.84 to 1.64 PFLOP/s, where cuBLAS
+// sustains 1.70 under the power limit: bound by the tensor cores.  With 128
+// rows each 0.16 / 0.15 / 0.18 ms: the weights' 0.94 GB at 5.9 to 6.3 TB/s;
+// wgrad's write of as much at 5.2 TB/s (a fill reaches 4.1).  One row per
+// expert (896 experts, 768 x 3584): 6.9 TB/s.
 #include "../../include/situ_moe.h"
 #include "gemm_groups.cuh"
-
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
 
 namespace situ {
 
@@ -40,8 +48,9 @@ constexpr int kFwd = SITU_GROUPED_FORWARD, kDgrad = SITU_GROUPED_DGRAD, kWgrad =
 constexpr int kBK = 64;             // contraction elements per stage
 constexpr int kABytes = 128 * 128;  // 128 weights (or n) x 64 elements
 constexpr int kBoxRows = 32;        // token rows per copy (forward, dgrad)
-constexpr int kThreads = 256;
-constexpr int kEpiWarp = 4;         // first epilogue warp
+constexpr int kThreads = 384;
+constexpr int kEpiWarp = 4;         // first of the eight epilogue warps: two per TMEM lane quarter
+constexpr int kEpiThreads = 256;
 constexpr int kSplitLeast = 8;      // stages that a CTA of a split tile takes at least
 constexpr int kPartPitch = 260;     // floats of a row of a split wgrad tile's part: 256 and 4
 constexpr int kOutPitch = 80;       // bytes of a staged token row: 32 elements and 16 bytes
@@ -64,9 +73,9 @@ struct Cfg {
   static constexpr int kTNB = TN / CG;                // N-side rows of one CTA
   static constexpr int kBBytes = kTNB * 128;
   static constexpr int kStageBytes = kABytes + kBBytes;
-  // output staging of the four epilogue warps: wgrad two 4 KB boxes each (and
-  // no tile prefix), else 32 tokens x 32 elements at a pitch without conflicts
-  static constexpr int kOutBytes = MODE == kWgrad ? 4 * 2 * 4096 : 4 * 32 * kOutPitch;
+  // output staging of the eight epilogue warps: wgrad two 4 KB boxes for four
+  // of them (and no tile prefix), else 32 tokens x 32 elements at a pitch without conflicts
+  static constexpr int kOutBytes = MODE == kWgrad ? 4 * 2 * 4096 : 8 * 32 * kOutPitch;
   static constexpr int kTpBytes = MODE == kWgrad ? 0 : 4 * (kMaxGroups + 1);
   static constexpr int kMaxBytes = 232448 - 1024 - kTpBytes - kOutBytes - 512;
   static constexpr int kStages = kMaxBytes / kStageBytes;
@@ -81,10 +90,6 @@ struct Cfg {
   static_assert(kSmem <= 232448 && kTmemCols <= 512 && kTmemCols >= 32, "shared memory and TMEM");
 };
 
-__device__ __forceinline__ uint16_t to_16(float v, int bf16) {
-  if (bf16) return __bfloat16_as_ushort(__float2bfloat16_rn(v));
-  return __half_as_ushort(__float2half_rn(v));
-}
 __device__ __forceinline__ uint32_t to_16x2(float a, float b, int bf16) {
   return bf16 ? f32x2_to_bf16x2(a, b) : pack_f16x2(a, b);
 }
@@ -196,7 +201,7 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(acc_full(b), 1);
-      mbar_init(acc_empty(b), 4 * CG);
+      mbar_init(acc_empty(b), 8 * CG);
     }
     mbar_init(drain, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -344,7 +349,7 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
     }
   } else if (warp >= kEpiWarp) {
     // ---------------- epilogue ----------------
-    const int q = warp - kEpiWarp;
+    const int q = warp & 3, h = (warp - kEpiWarp) >> 2, ew = warp - kEpiWarp;   // lane quarter; every other chunk of columns
     Ring<2> ab;
     auto release = [&](int buf) {   // the accumulator may be written again
       __syncwarp();
@@ -356,11 +361,13 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
       }
     };
     // 32 rows of dw from row n0: boxes of 128 bytes x 32 rows through shared
-    // memory (128-byte swizzle), two in flight; the map ends at N and K
+    // memory (128-byte swizzle), two in flight; the map ends at N and K.  By
+    // one warp per lane quarter: with all eight, the boxes cost the ring a
+    // stage (32 experts, 128 rows, 4096 x 3584: 183 us, 221)
     uint32_t obuf = 0;
     auto store_dw = [&](const Tile& t, int n0, uint32_t trow, bool sums) {
       const int per = p.out_f32 ? 32 : 64;
-      if (n0 >= p.M) return;
+      if (n0 >= p.M || h != 0) return;
       for (int c0 = 0; c0 < t.cols; c0 += per) {
         uint32_t v[64];
         if (sums) {
@@ -415,7 +422,7 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
       }
       if (MODE == kWgrad && SPLIT) {   // this CTA's part, [n][k], over the ring: its copies and MMAs are done
         float* dst = reinterpret_cast<float*>(smem) + (32 * q + lane) * kPartPitch;
-        for (int c0 = 0; c0 < t.cols; c0 += 16) {
+        for (int c0 = 16 * h; c0 < t.cols; c0 += 32) {
           float v[16];
           __syncwarp();
           tmem_ld16(trow + c0, v);
@@ -423,7 +430,7 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
           for (int c = 0; c < 16; c += 4) *reinterpret_cast<float4*>(dst + c0 + c) = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
         }
       } else if (MODE == kWgrad) {   // dw += sums
-        for (int c0 = 0; c0 < t.cols; c0 += 16) {
+        for (int c0 = 16 * h; c0 < t.cols; c0 += 32) {
           float v[16];
           __syncwarp();
           tmem_ld16(trow + c0, v);
@@ -459,7 +466,7 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
         }
       } else if (SPLIT) {   // this CTA's part, [token][128], over the ring: its copies and MMAs are done
         float* dst = reinterpret_cast<float*>(smem) + 32 * q + lane;
-        for (int c0 = 0; c0 < t.cols; c0 += 16) {
+        for (int c0 = 16 * h; c0 < t.cols; c0 += 32) {
           float v[16];
           __syncwarp();
           tmem_ld16(trow + c0, v);
@@ -471,8 +478,8 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
         // stores of 4 token rows each, where one column a store (128 bytes of
         // a row) made the epilogue 2.5 times as long as a 16-bit one
         const int chunk = lane & 7, n = m - lane + 4 * chunk;
-        uint8_t* box = smem + C::kOffOut + q * 32 * kOutPitch;
-        for (int c0 = 0; c0 < t.cols; c0 += 16) {
+        uint8_t* box = smem + C::kOffOut + ew * 32 * kOutPitch;
+        for (int c0 = 16 * h; c0 < t.cols; c0 += 32) {
           float v[16];
           __syncwarp();
           tmem_ld16(trow + c0, v);
@@ -494,9 +501,9 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
         // transposed through shared memory, 32 tokens at a time: a store
         // instruction is then 64 bytes of 8 token rows, where storing straight
         // from the accumulator's layout takes 2 bytes a lane
-        const uint32_t box = sbase + C::kOffOut + q * 32 * kOutPitch;
+        const uint32_t box = sbase + C::kOffOut + ew * 32 * kOutPitch;
         const int chunk = lane & 3, n = m - lane + 8 * chunk;
-        for (int c0 = 0; c0 < t.cols; c0 += 32) {
+        for (int c0 = 32 * h; c0 < t.cols; c0 += 64) {
           uint32_t v[32];
           __syncwarp();
           tmem_ld_frag_nowait(trow + c0, v);
@@ -516,7 +523,7 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
               if (c0 + tok < t.cols)
                 *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) +
                                           (size_t)(t.row0 + t.c0 + c0 + tok) * (size_t)p.ld_out + n) =
-                    *reinterpret_cast<const uint4*>(smem + C::kOffOut + q * 32 * kOutPitch + tok * kOutPitch + chunk * 16);
+                    *reinterpret_cast<const uint4*>(smem + C::kOffOut + ew * 32 * kOutPitch + tok * kOutPitch + chunk * 16);
             }
           }
         }
@@ -526,7 +533,7 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
     if (MODE == kWgrad && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     // rows of no group
     if (MODE != kWgrad && p.zero_rest && *reinterpret_cast<volatile int*>(p.err) == 0) {
-      const long t = (long)blockIdx.x * 128 + tid - 32 * kEpiWarp, n = (long)gridDim.x * 128;
+      const long t = (long)blockIdx.x * kEpiThreads + tid - 32 * kEpiWarp, n = (long)gridDim.x * kEpiThreads;
       const int el = p.out_f32 ? 4 : 2;
       uint8_t* out = reinterpret_cast<uint8_t*>(p.out);
       const int2 last = group_rows(p.offsets, p.E - 1, p.S);
