@@ -834,14 +834,20 @@ extern "C" situ_status situ_moe_fp8_gemm(const situ_fp8_gemm_args* g, void* stre
   // Tiles: up to about 20 rows per group (one group's rows are known) 32
   // tokens on the MMA's N side, which stream the weights and little else (40
   // experts of 4096 x 2048, 10 / 25 / 45 rows each: 62 / 65 / 101 us, wide
-  // tiles 63 / 63 / 65); above, wide tiles, on CTA pairs from 200 rows on
-  // (112 experts, 73 rows: one CTA 0.39 ms, pairs 0.54; 64 experts, 256 rows:
-  // 187, 171 us); but 64 tokens on the N side while such tiles fit the SMs
-  // once (256 rows, 4096 x 4096: 16 us, wide 19), with the contraction split.
+  // tiles 63 / 63 / 65); above, wide tiles; but 64 tokens on the N side while
+  // such tiles fit the SMs once (256 rows, 4096 x 4096: 16 us, wide 19), with
+  // the contraction split.
   const double per = (double)g->S / g->E;
   const double groups = g->S < g->E ? g->S : g->E, rows = g->S;
   const int tn = per <= (g->E == 1 ? 32. : 20.) ? 32 : (groups + rows / 64) * ((p.N + 127) / 128) <= sm_count() ? 64 : 256;
-  const int cg = tn < 256 || per < 200 ? 1 : 2;
+  // Wide tiles of one CTA (128 tokens) waste less of a group's last tile: 64
+  // experts of 3584 x 2048, 256 rows: 169 us, pairs 199; 512: 292, 315; 8,192
+  // rows of one: the same; 16,384: 228, 216.  Rows that do not start on
+  // 128-byte lines cost about twice the L2 requests, and a pair copies the
+  // weights half as often: 100 experts of 2048 x 2064, 164 rows: 134 us, pairs
+  // 117; one of 4096 x 2000, 16,384 rows: 162, 127.
+  const bool lines = g->K % 128 == 0 && g->ldx % 128 == 0;
+  const int cg = tn < 256 || per < (lines ? 4096. : 150.) ? 1 : 2;
   const int tm = tn < 256 ? tn : 128 * cg;        // tokens per tile
   p.n_mt = tn < 256 ? (p.N + 127) / 128 : (p.N + kWideN - 1) / kWideN;
   const double items = ((double)g->S / tm + p.E) * p.n_mt;

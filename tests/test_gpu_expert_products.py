@@ -532,6 +532,7 @@ def test_fp8_dense_matches_64_bit_sums(S, N, K):
 @pytest.mark.parametrize("counts,N,K", [
     ([75, 0, 128, 129, 40, 90, 3, 200, 110], 2056, 208), ([60, 70, 80, 90, 100, 50, 40, 130], 2048, 1040),
     ([257, 600, 0, 1, 511, 256], 2184, 144), ([640, 128, 700], 2056, 1168), ([900], 1928, 272),
+    ([4500, 4000], 264, 128), ([300, 700], 2056, 256),
     ([17], 264, 4112), ([3, 0, 12, 9], 136, 2064), ([64], 264, 3088), ([100, 20], 136, 2192)])
 def test_every_form_of_the_fp8_product(counts, N, K):
     S = 2 + sum(counts) + 3
