@@ -36,7 +36,7 @@ constexpr int kEpiThreads = 256;
 constexpr int kSG = 4;   // blocks per group of staged factors
 constexpr int kOutPitch = 80, kOutPitchF = 144;   // bytes of a staged token row of 32 outputs, bf16 and fp32
 constexpr int kBoxBytes = 32 * kOutPitch;         // of a warp: 32 rows of bf16, 16 of fp32
-constexpr int kSplitLeast = 4;   // blocks that a CTA of a split tile takes at least
+constexpr int kSplitLeast = 2;   // blocks that a CTA of a split tile takes at least
 
 struct F8Params {
   const int32_t* offsets;   // null: one dense group of S rows
@@ -838,8 +838,7 @@ extern "C" situ_status situ_moe_fp8_gemm(const situ_fp8_gemm_args* g, void* stre
   // such tiles fit the SMs once (256 rows, 4096 x 4096: 16 us, wide 19), with
   // the contraction split.
   const double per = (double)g->S / g->E;
-  const double groups = g->S < g->E ? g->S : g->E, rows = g->S;
-  const int tn = per <= (g->E == 1 ? 32. : 20.) ? 32 : (groups + rows / 64) * ((p.N + 127) / 128) <= sm_count() ? 64 : 256;
+  const int tn = per <= (g->E == 1 ? 32. : 20.) ? 32 : most_tiles(g->S, g->E, 64) * ((p.N + 127) / 128) <= sm_count() ? 64 : 256;
   // Wide tiles of one CTA (128 tokens) waste less of a group's last tile: 64
   // experts of 3584 x 2048, 256 rows: 169 us, pairs 199; 512: 292, 315; 8,192
   // rows of one: the same; 16,384: 228, 216.  Rows that do not start on
@@ -850,8 +849,7 @@ extern "C" situ_status situ_moe_fp8_gemm(const situ_fp8_gemm_args* g, void* stre
   const int cg = tn < 256 || per < (lines ? 4096. : 150.) ? 1 : 2;
   const int tm = tn < 256 ? tn : 128 * cg;        // tokens per tile
   p.n_mt = tn < 256 ? (p.N + 127) / 128 : (p.N + kWideN - 1) / kWideN;
-  const double items = ((double)g->S / tm + p.E) * p.n_mt;
-  if (items > 2.0e9) return SITU_ERR_BAD_SHAPE;
+  if (most_tiles(g->S, g->E, tm) * p.n_mt > 2.0e9) return SITU_ERR_BAD_SHAPE;
   CUtensorMap mw, mx;
   const uint64_t S = (uint64_t)g->S, N = (uint64_t)g->N, K = (uint64_t)g->K, E = (uint64_t)g->E;
   const uint64_t dw[3] = {K, N, E}, sw[2] = {K, N * K}, dx[2] = {K, S}, sx[1] = {(uint64_t)g->ldx};
@@ -860,11 +858,9 @@ extern "C" situ_status situ_moe_fp8_gemm(const situ_fp8_gemm_args* g, void* stre
       !make_map_nd(&mx, CU_TENSOR_MAP_DATA_TYPE_UINT8, g->x_q, 2, dx, sx, boxx))
     return SITU_ERR_CUDA;
   cudaStream_t st = (cudaStream_t)stream;
-  // at most so many tiles have rows: a group of r rows has at most r, and at
-  // most (r - 1) / tm + 1
-  const double most = (groups + rows / tm) * p.n_mt;
-  const long cap = most > 1e6 ? 1000000 : (long)most + 1;
-  const int split = tn < 256 ? split_of((double)cap, sm_count(), p.nkb, kSplitLeast) : 1;
+  const double most = most_tiles(g->S, g->E, tm) * p.n_mt;
+  const long cap = most > 1e6 ? 1000000 : (long)most;
+  const int split = tn < 256 ? split_of(f8_kernel<1, 32, true>, kThreads, Cfg<1, 32>::kSmem, most, p.nkb, kSplitLeast) : 1;
   cudaError_t e;
   if (split > 1)
     e = tn == 32 ? launch_t<1, 32, true>(mw, mx, p, cap, st, split) : launch_t<1, 64, true>(mw, mx, p, cap, st, split);

@@ -381,14 +381,13 @@ __device__ __forceinline__ float4 peer_f32x4(uint32_t addr, uint32_t rank) {
       : "r"(addr), "r"(rank));
   return v;
 }
-// CTAs per tile: as many as fit the GPU's SMs once for `tiles` tiles and leave
-// each at least `least` of the `steps` contraction steps
-inline int split_of(double tiles, int sms, int steps, int least) {
-  int c = tiles >= 1.0 ? (int)(sms / tiles) : 1;
-  if (c > steps / least) c = steps / least;
-  return c > 8 ? 8 : c < 1 ? 1 : c;
+// The most token tiles of `tile` rows that S rows in E groups can take: G
+// groups with rows, r each, take floor((r - 1) / tile) + 1, together at most
+// G + floor((S - G) / tile), which grows with G.
+inline double most_tiles(int S, int E, int tile) {
+  const int G = S < E ? S : E;
+  return (double)G + (S - G) / tile;
 }
-
 // zeros to rows [from, to) of a row-major output (width and pitch in bytes,
 // multiples of 16), spread over `n` threads of which this is number `t`
 __device__ __forceinline__ void zero_rows(uint8_t* out, long from, long to, size_t width, size_t pitch, long t, long n) {
@@ -470,6 +469,45 @@ cudaError_t launch_cluster(Kernel k, std::atomic<uint64_t>* raised, int cluster,
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, k, args...);
+}
+
+// How many clusters of c CTAs (one per SM) the current device holds at once
+// (152, 76, 46, 36, 28, 23, 15, 15 of 1 to 8 here: clusters do not span the
+// GPU's processing clusters).  Asked once per device; k is any of the kernels
+// that fill an SM.
+template <class Kernel>
+int clusters_at_once(Kernel k, int threads, size_t smem, int c) {
+  static std::atomic<int> known[64][9];
+  int dev = 0;
+  if (c < 1 || c > 8 || cudaGetDevice(&dev) != cudaSuccess) return 0;
+  int n = dev < 64 ? known[dev][c].load() : 0;
+  if (n != 0) return n;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)c;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)c);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  {
+    std::lock_guard<std::mutex> lock(attr_mutex());
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, k, &cfg) != cudaSuccess)
+      return 0;
+  }
+  if (dev < 64) known[dev][c].store(n);
+  return n;
+}
+// CTAs per tile: the largest cluster of which the device holds one per tile
+// at once and whose CTAs keep at least `least` of the `steps` contraction steps
+template <class Kernel>
+int split_of(Kernel k, int threads, size_t smem, double tiles, int steps, int least) {
+  for (int c = steps / least < 8 ? steps / least : 8; c > 1; --c)
+    if (tiles * c <= sm_count() && tiles <= clusters_at_once(k, threads, smem, c)) return c;
+  return 1;
 }
 
 }  // namespace gg

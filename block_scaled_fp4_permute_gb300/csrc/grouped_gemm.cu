@@ -642,17 +642,16 @@ extern "C" situ_status situ_moe_grouped_gemm(const situ_grouped_gemm_args* g, vo
   // CTAs 0.60), unless tiles of 128 fit the SMs once (512 rows, 4096 x 4096:
   // 23 us, pairs 25).
   const double per = (double)g->S / g->E;
-  const double groups = g->S < g->E ? g->S : g->E, rows = g->S;
   const double room[3] = {g->E == 1 ? 32. : 20., g->E == 1 ? 64. : 44., g->E == 1 ? 128. : 98.};
   const int tn = mode == kWgrad     ? 256
                  : per <= room[0] ? 32
                  : per <= room[1] ? 64
-                 : per <= room[2] || (groups + rows / 128) * ((p.M + 127) / 128) <= sm_count() ? 128 : 256;
+                 : per <= room[2] || most_tiles(g->S, g->E, 128) * ((p.M + 127) / 128) <= sm_count() ? 128 : 256;
   // wgrad of few output tiles: the rows of a group split over clusters (a
   // skewed group's rows are taken as up to twice the average)
   const double wtiles = (double)p.E * ((p.M + 127) / 128) * ((p.Ncol + 255) / 256);
   const int wsteps = (int)((g->E > 1 ? 2 * per : per) / kBK);
-  const int wsplit = mode == kWgrad ? split_of(wtiles, sm_count(), wsteps, kSplitLeast) : 1;
+  const int wsplit = mode == kWgrad ? split_of(gg_kernel<1, kWgrad, 256, true>, kThreads, Cfg<1, kWgrad, 256>::kSmem, wtiles, wsteps, kSplitLeast) : 1;
   const int cg = tn == 256 && p.M > 128 && wsplit == 1 ? 2 : 1;
   p.n_mt = (p.M + 128 * cg - 1) / (128 * cg);
   p.n_nt = (p.Ncol + tn - 1) / tn;
@@ -680,12 +679,10 @@ extern "C" situ_status situ_moe_grouped_gemm(const situ_grouped_gemm_args* g, vo
     ok = make_map_nd(&m.a, dt, g->b, 3, dw, sw, boxw) && make_map_nd(&m.b, dt, g->a, 2, dx, sx, boxx);
   }
   if (!ok) return SITU_ERR_CUDA;
-  // at most so many tiles have rows: a group of r rows has at most r, and at
-  // most (r - 1) / tn + 1
-  const double most = (groups + rows / tn) * p.n_mt;
-  const long cap = most > 1e6 ? 1000000 : (long)most + 1;
+  const double most = most_tiles(g->S, g->E, tn) * p.n_mt;
+  const long cap = most > 1e6 ? 1000000 : (long)most;
   const int steps = (p.L + kBK - 1) / kBK;
-  const int split = tn <= 128 ? split_of((double)cap, sm_count(), steps, kSplitLeast) : 1;
+  const int split = tn <= 128 ? split_of(gg_kernel<1, kFwd, 32, true>, kThreads, Cfg<1, kFwd, 32>::kSmem, most, steps, kSplitLeast) : 1;
   cudaError_t e;
   if (mode == kWgrad && wsplit > 1) {
     e = launch_t<1, kWgrad, 256, true>(m, p, (long)items, st, wsplit);
