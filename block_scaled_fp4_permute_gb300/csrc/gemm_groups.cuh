@@ -357,16 +357,16 @@ __device__ __forceinline__ float2 peer_f32x2(uint32_t addr, uint32_t rank) {
                : "r"(addr), "r"(rank));
   return v;
 }
-// The parts [cols][128] at `part` of every CTA, summed; emit(col, m, sums of m
-// and m + 1) for this CTA's share, over n threads of which this is number t.
+// The parts [cols][pitch] at `part` of every CTA (128 sums of a row in use),
+// added up; emit(col, m, sums of m and m + 1) for this CTA's share, over n threads of which this is number t.
 template <class Emit>
-__device__ __forceinline__ void join_parts(uint32_t part, int cols, int t, int n, Emit&& emit) {
+__device__ __forceinline__ void join_parts(uint32_t part, int pitch, int cols, int t, int n, Emit&& emit) {
   const uint32_t ranks = cluster_size();
   for (int i = (int)cluster_rank() * n + t; i < cols * 64; i += (int)ranks * n) {
     const int col = i >> 6, m = 2 * (i & 63);
     float2 s = make_float2(0.f, 0.f);
     for (uint32_t r = 0; r < ranks; ++r) {
-      const float2 v = peer_f32x2(part + (uint32_t)(col * 128 + m) * 4, r);
+      const float2 v = peer_f32x2(part + (uint32_t)(col * pitch + m) * 4, r);
       s.x += v.x;
       s.y += v.y;
     }

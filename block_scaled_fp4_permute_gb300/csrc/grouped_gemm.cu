@@ -52,7 +52,10 @@ constexpr int kThreads = 384;
 constexpr int kEpiWarp = 4;         // first of the eight epilogue warps: two per TMEM lane quarter
 constexpr int kEpiThreads = 256;
 constexpr int kSplitLeast = 8;      // stages that a CTA of a split tile takes at least
+constexpr int kSumStages = 8;       // stages summed in TMEM before the fp32 registers take them (fp32 results)
+constexpr int kLaunchRegs = 168;    // per thread of a launch, what kSplitRegs shares out
 constexpr int kPartPitch = 260;     // floats of a row of a split wgrad tile's part: 256 and 4
+constexpr int kJoinPitch = 132;     // floats of a token of a split forward or dgrad tile's part
 constexpr int kOutPitch = 80;       // bytes of a staged token row: 32 elements and 16 bytes
 constexpr int kOutPitchF = 144;     // the same of 32 floats; 16 rows
 static_assert(16 * kOutPitchF <= 32 * kOutPitch, "staging");
@@ -65,6 +68,7 @@ struct GgParams {
   void* out;
   long ld_out;      // elements
   int bf16, out_f32, accumulate, zero_rest;
+  int chunk;        // stages summed in TMEM
   int* err;
 };
 
@@ -73,9 +77,9 @@ struct Cfg {
   static constexpr int kTNB = TN / CG;                // N-side rows of one CTA
   static constexpr int kBBytes = kTNB * 128;
   static constexpr int kStageBytes = kABytes + kBBytes;
-  // output staging of the eight epilogue warps: wgrad two 4 KB boxes for four
-  // of them (and no tile prefix), else 32 tokens x 32 elements at a pitch without conflicts
-  static constexpr int kOutBytes = MODE == kWgrad ? 4 * 2 * 4096 : 8 * 32 * kOutPitch;
+  // output staging of the eight epilogue warps: wgrad 4 KB boxes (and no
+  // tile prefix), else 32 tokens x 32 elements at a pitch without conflicts
+  static constexpr int kOutBytes = MODE == kWgrad ? 8 * 4096 : 8 * 32 * kOutPitch;
   static constexpr int kTpBytes = MODE == kWgrad ? 0 : 4 * (kMaxGroups + 1);
   static constexpr int kMaxBytes = 232448 - 1024 - kTpBytes - kOutBytes - 512;
   static constexpr int kStages = kMaxBytes / kStageBytes;
@@ -87,6 +91,9 @@ struct Cfg {
   static constexpr int kOffTm = kOffBar + 8 * kNumBars;
   static constexpr int kSmem = kOffTm + 16 + 1024;
   static constexpr int kTmemCols = 2 * TN;
+  // 256 columns are 128 sums per epilogue thread: warps 0..3 hand registers
+  // over (56 * 128 + 224 * 256 = 168 * 384, the launch's total)
+  static constexpr bool kSplitRegs = TN >= 256;
   static_assert(kSmem <= 232448 && kTmemCols <= 512 && kTmemCols >= 32, "shared memory and TMEM");
 };
 
@@ -132,6 +139,32 @@ __device__ __forceinline__ Tile tile_of(const GgParams& p, const int* tp, int id
   }
   t.m0 = mt * 128 * CG;
   return t;
+}
+
+// Where element c of a thread's 32 of a 32-lane x 32-column load lies
+// (tmem_ld_frag_nowait of its two halves): lane and column.
+__device__ __forceinline__ int frag_row(int c, int lane) { return (lane >> 2) + 8 * ((c >> 1) & 1) + 16 * (c >> 4); }
+__device__ __forceinline__ int frag_col(int c, int lane) { return 8 * ((c >> 2) & 3) + 2 * (lane & 3) + (c & 1); }
+
+// dw[at..at + 7] += v
+__device__ __forceinline__ void add_dw(const GgParams& p, size_t at, const float* v) {
+  if (p.out_f32) {
+    float4* dst = reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + at);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float4 o = dst[h];
+      dst[h] = make_float4(v[4 * h] + o.x, v[4 * h + 1] + o.y, v[4 * h + 2] + o.z, v[4 * h + 3] + o.w);
+    }
+  } else {
+    uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + at);
+    const uint4 o = *dst;
+    const uint32_t w[4] = {o.x, o.y, o.z, o.w};
+    uint32_t r[4];
+#pragma unroll
+    for (int h = 0; h < 4; ++h)
+      r[h] = to_16x2(v[2 * h] + from_16(w[h] & 0xFFFFu, p.bf16), v[2 * h + 1] + from_16(w[h] >> 16, p.bf16), p.bf16);
+    *dst = make_uint4(r[0], r[1], r[2], r[3]);
+  }
 }
 
 // Adds up the parts of a split wgrad tile: this CTA's share of its rows, four
@@ -221,314 +254,340 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
   auto stage_from = [&](const Tile& t) { return SPLIT ? t.nk * part / parts : 0; };
   auto stage_to = [&](const Tile& t) { return SPLIT ? t.nk * (part + 1) / parts : t.nk; };
 
-  if (warp == 0) {
-    // ---------------- copies ----------------
-    const bool leader = elect_one();
-    Ring<C::kStages> r;
-    bool ok = true;
-    for (int idx = first; idx < total && ok; idx += stride) {
-      const Tile t = tile_of<CG, MODE, TN>(p, tp, idx);
-      const int nact = (t.cols + 16 * CG - 1) / (16 * CG) * (16 * CG);   // the MMA's N
-      const int half = nact / CG;                                       // this CTA's part of it
-      const int ma = t.m0 + 128 * (int)rank, cb = t.c0 + half * (int)rank;
-      const int nchunk = (half + 63) / 64;
-      for (int kk = stage_from(t), to = stage_to(t); kk < to; ++kk, r.next()) {
-        const int s = r.s;
-        if (r.used == C::kStages && !warp_wait(empty(s), r.ph ^ 1, p.err, 71)) {
-          ok = false;
-          break;
-        }
-        if (leader) {
-          const uint32_t a = sbase + s * kABytes, b = sbase + C::kOffB + s * C::kBBytes;
-          const int k0 = kk * kBK;
-          if (MODE != kWgrad) {
-            const int nbox = (half + kBoxRows - 1) / kBoxRows;   // token rows in boxes of 32: a short tile reads few
-            if (CG == 1 || rank == 0) mbar_expect_tx(full(s), CG * (kABytes + nbox * kBoxRows * 128));
-            if (MODE == kFwd) {
-              copy_3d<CG>(a, &mapA, k0, ma, t.e, full(s));
-            } else {   // w as [n, k], k contiguous: two chunks of 64 k
-              copy_3d<CG>(a, &mapA, ma, k0, t.e, full(s));
-              copy_3d<CG>(a + kABytes / 2, &mapA, ma + 64, k0, t.e, full(s));
-            }
-            for (int i = 0; i < nbox; ++i)
-              copy_2d<CG>(b + i * kBoxRows * 128, &mapB, k0, t.row0 + cb + i * kBoxRows, full(s));
-          } else {
-            const int rows = t.rows - k0;
-            if (rows >= kBK) {
-              if (CG == 1 || rank == 0) mbar_expect_tx(full(s), CG * (kABytes + nchunk * 8192));
-              for (int c = 0; c < 2; ++c) copy_2d<CG>(a + 8192 * c, &mapA, ma + 64 * c, t.row0 + k0, full(s));
-              for (int c = 0; c < nchunk; ++c) copy_2d<CG>(b + 8192 * c, &mapB, cb + 64 * c, t.row0 + k0, full(s));
+  if (warp < kEpiWarp) {
+    if (C::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == 0) {
+      // ---------------- copies ----------------
+      const bool leader = elect_one();
+      Ring<C::kStages> r;
+      bool ok = true;
+      for (int idx = first; idx < total && ok; idx += stride) {
+        const Tile t = tile_of<CG, MODE, TN>(p, tp, idx);
+        const int nact = (t.cols + 16 * CG - 1) / (16 * CG) * (16 * CG);   // the MMA's N
+        const int half = nact / CG;                                       // this CTA's part of it
+        const int ma = t.m0 + 128 * (int)rank, cb = t.c0 + half * (int)rank;
+        const int nchunk = (half + 63) / 64;
+        for (int kk = stage_from(t), to = stage_to(t); kk < to; ++kk, r.next()) {
+          const int s = r.s;
+          if (r.used == C::kStages && !warp_wait(empty(s), r.ph ^ 1, p.err, 71)) {
+            ok = false;
+            break;
+          }
+          if (leader) {
+            const uint32_t a = sbase + s * kABytes, b = sbase + C::kOffB + s * C::kBBytes;
+            const int k0 = kk * kBK;
+            if (MODE != kWgrad) {
+              const int nbox = (half + kBoxRows - 1) / kBoxRows;   // token rows in boxes of 32: a short tile reads few
+              if (CG == 1 || rank == 0) mbar_expect_tx(full(s), CG * (kABytes + nbox * kBoxRows * 128));
+              if (MODE == kFwd) {
+                copy_3d<CG>(a, &mapA, k0, ma, t.e, full(s));
+              } else {   // w as [n, k], k contiguous: two chunks of 64 k
+                copy_3d<CG>(a, &mapA, ma, k0, t.e, full(s));
+                copy_3d<CG>(a + kABytes / 2, &mapA, ma + 64, k0, t.e, full(s));
+              }
+              for (int i = 0; i < nbox; ++i)
+                copy_2d<CG>(b + i * kBoxRows * 128, &mapB, k0, t.row0 + cb + i * kBoxRows, full(s));
             } else {
-              // whole sixteens in boxes, the rest row by row below
-              const int whole = rows & ~15;
-              if (CG == 1 || rank == 0) mbar_expect_tx(full(s), CG * (2 + nchunk) * ((rows + 15) & ~15) * 128);
-              for (int i = 0; i < whole; i += 16) {
-                for (int c = 0; c < 2; ++c) copy_2d<CG>(a + 8192 * c + i * 128, &mapA16, ma + 64 * c, t.row0 + k0 + i, full(s));
-                for (int c = 0; c < nchunk; ++c)
-                  copy_2d<CG>(b + 8192 * c + i * 128, &mapB16, cb + 64 * c, t.row0 + k0 + i, full(s));
+              const int rows = t.rows - k0;
+              if (rows >= kBK) {
+                if (CG == 1 || rank == 0) mbar_expect_tx(full(s), CG * (kABytes + nchunk * 8192));
+                for (int c = 0; c < 2; ++c) copy_2d<CG>(a + 8192 * c, &mapA, ma + 64 * c, t.row0 + k0, full(s));
+                for (int c = 0; c < nchunk; ++c) copy_2d<CG>(b + 8192 * c, &mapB, cb + 64 * c, t.row0 + k0, full(s));
+              } else {
+                // whole sixteens in boxes, the rest row by row below
+                const int whole = rows & ~15;
+                if (CG == 1 || rank == 0) mbar_expect_tx(full(s), CG * (2 + nchunk) * ((rows + 15) & ~15) * 128);
+                for (int i = 0; i < whole; i += 16) {
+                  for (int c = 0; c < 2; ++c) copy_2d<CG>(a + 8192 * c + i * 128, &mapA16, ma + 64 * c, t.row0 + k0 + i, full(s));
+                  for (int c = 0; c < nchunk; ++c)
+                    copy_2d<CG>(b + 8192 * c + i * 128, &mapB16, cb + 64 * c, t.row0 + k0 + i, full(s));
+                }
               }
             }
           }
-        }
-        __syncwarp();
-        if (MODE == kWgrad && t.rows - kk * kBK < kBK && (t.rows & 15) != 0 && lane < 4 * (2 + nchunk)) {
-          // the last, partial sixteen: a lane per chunk and four rows; rows past
-          // the group's end are named S, out of bounds, and read as zeros
-          const int c = lane >> 2, i = (t.rows & ~15) - kk * kBK + 4 * (lane & 3), r0 = kk * kBK + i;
-          int row[4];
+          __syncwarp();
+          if (MODE == kWgrad && t.rows - kk * kBK < kBK && (t.rows & 15) != 0 && lane < 4 * (2 + nchunk)) {
+            // the last, partial sixteen: a lane per chunk and four rows; rows past
+            // the group's end are named S, out of bounds, and read as zeros
+            const int c = lane >> 2, i = (t.rows & ~15) - kk * kBK + 4 * (lane & 3), r0 = kk * kBK + i;
+            int row[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) row[j] = r0 + j < t.rows ? t.row0 + r0 + j : p.S;
-          const bool is_a = c < 2;
-          copy_rows4<CG>(sbase + (is_a ? s * kABytes + 8192 * c : C::kOffB + s * C::kBBytes + 8192 * (c - 2)) + i * 128,
-                         is_a ? &mapA1 : &mapB1, is_a ? ma + 64 * c : cb + 64 * (c - 2), row[0], row[1], row[2], row[3],
-                         full(s));
+            for (int j = 0; j < 4; ++j) row[j] = r0 + j < t.rows ? t.row0 + r0 + j : p.S;
+            const bool is_a = c < 2;
+            copy_rows4<CG>(sbase + (is_a ? s * kABytes + 8192 * c : C::kOffB + s * C::kBBytes + 8192 * (c - 2)) + i * 128,
+                           is_a ? &mapA1 : &mapB1, is_a ? ma + 64 * c : cb + 64 * (c - 2), row[0], row[1], row[2], row[3],
+                           full(s));
+          }
+          __syncwarp();
         }
-        __syncwarp();
       }
-    }
-    if (ok) {   // the last arrivals on this CTA's barriers, before it may leave
-      for (int j = 0; j < r.used; ++j) warp_wait(empty(j), j < r.s ? r.ph : r.ph ^ 1, p.err, 72);
-    } else if (rank == 0) {   // copies in flight
-      for (int j = 0; j < r.used; ++j) drain_wait(full(j), j < r.s ? r.ph : r.ph ^ 1);
-    } else {
-      const unsigned long long t0 = globaltimer();   // they complete on the other CTA's barriers
-      while (globaltimer() - t0 < 2000000ull) {
-      }
-    }
-  } else if (warp == 1 && rank == 0) {
-    // ---------------- MMAs ----------------
-    const bool leader = elect_one();
-    Ring<C::kStages> r;
-    Ring<2> ab;
-    bool ok = true;
-    const uint32_t id0 = (1u << 4) | (p.bf16 ? (1u << 7) | (1u << 10) : 0u) | (MODE != kFwd ? 1u << 15 : 0u) |
-                         (MODE == kWgrad ? 1u << 16 : 0u) | ((uint32_t)(128 * CG >> 4) << 24);
-    for (int idx = first; idx < total && ok; idx += stride) {
-      const Tile t = tile_of<CG, MODE, TN>(p, tp, idx);
-      if (stage_from(t) == stage_to(t)) continue;
-      const int nact = (t.cols + 16 * CG - 1) / (16 * CG) * (16 * CG);
-      const uint32_t idesc = id0 | ((uint32_t)(nact >> 3) << 17);
-      const int buf = ab.s;
-      if (ab.used == 2 && !warp_wait(acc_empty(buf), ab.ph ^ 1, p.err, 73)) {
-        ok = false;
-        break;
-      }
-      ab.next();
-      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      const int len = MODE == kWgrad ? t.rows : p.L;
-      const int from = stage_from(t);
-      for (int kk = from, to = stage_to(t); kk < to; ++kk, r.next()) {
-        const int s = r.s;
-        if (!warp_wait(full(s), r.ph, p.err, 74)) {
-          ok = false;
-          break;
+      if (ok) {   // the last arrivals on this CTA's barriers, before it may leave
+        for (int j = 0; j < r.used; ++j) warp_wait(empty(j), j < r.s ? r.ph : r.ph ^ 1, p.err, 72);
+      } else if (rank == 0) {   // copies in flight
+        for (int j = 0; j < r.used; ++j) drain_wait(full(j), j < r.s ? r.ph : r.ph ^ 1);
+      } else {
+        const unsigned long long t0 = globaltimer();   // they complete on the other CTA's barriers
+        while (globaltimer() - t0 < 2000000ull) {
         }
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        if (leader) {
-          const uint32_t a = sbase + s * kABytes, b = sbase + C::kOffB + s * C::kBBytes;
-          const uint64_t ad = MODE == kFwd ? sdesc(a) : sdesc_mn(a, 8192);
-          const uint64_t bd = MODE != kWgrad ? sdesc(b) : sdesc_mn(b, 8192);
-          const int steps = min(4, (len - kk * kBK + 15) >> 4);
-          // per 16 contraction elements: 32 bytes along a K-major row, 16 rows of 128 bytes else
-          for (int k = 0; k < steps; ++k)
-            mma_f16<CG>(tmem + buf * TN, ad + (MODE == kFwd ? 2 : 128) * k, bd + (MODE != kWgrad ? 2 : 128) * k, idesc,
-                        ((kk - from) | k) != 0);
-          commit<CG>(empty(s));
+      }
+    } else if (warp == 1 && rank == 0) {
+      // ---------------- MMAs ----------------
+      const bool leader = elect_one();
+      Ring<C::kStages> r;
+      Ring<2> ab;
+      bool ok = true;
+      const uint32_t id0 = (1u << 4) | (p.bf16 ? (1u << 7) | (1u << 10) : 0u) | (MODE != kFwd ? 1u << 15 : 0u) |
+                           (MODE == kWgrad ? 1u << 16 : 0u) | ((uint32_t)(128 * CG >> 4) << 24);
+      for (int idx = first; idx < total && ok; idx += stride) {
+        const Tile t = tile_of<CG, MODE, TN>(p, tp, idx);
+        if (stage_from(t) == stage_to(t)) continue;
+        const int nact = (t.cols + 16 * CG - 1) / (16 * CG) * (16 * CG);
+        const uint32_t idesc = id0 | ((uint32_t)(nact >> 3) << 17);
+        const int len = MODE == kWgrad ? t.rows : p.L;
+        const int from = stage_from(t), to = stage_to(t);
+        int buf = 0, in_chunk = 0;
+        for (int kk = from; kk < to; ++kk, r.next()) {
+          const bool begins = in_chunk == 0, ends = ++in_chunk == p.chunk || kk + 1 == to;
+          if (ends) in_chunk = 0;
+          if (begins) {   // a chunk's sums start from zero in the other accumulator
+            buf = ab.s;
+            if (!warp_wait(acc_empty(buf), ab.ph ^ 1, p.err, 73)) {
+              ok = false;
+              break;
+            }
+            ab.next();
+          }
+          const int s = r.s;
+          if (!warp_wait(full(s), r.ph, p.err, 74)) {
+            ok = false;
+            break;
+          }
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          if (leader) {
+            const uint32_t a = sbase + s * kABytes, b = sbase + C::kOffB + s * C::kBBytes;
+            const uint64_t ad = MODE == kFwd ? sdesc(a) : sdesc_mn(a, 8192);
+            const uint64_t bd = MODE != kWgrad ? sdesc(b) : sdesc_mn(b, 8192);
+            const int steps = min(4, (len - kk * kBK + 15) >> 4);
+            // per 16 contraction elements: 32 bytes along a K-major row, 16 rows of 128 bytes else
+            for (int k = 0; k < steps; ++k)
+              mma_f16<CG>(tmem + buf * TN, ad + (MODE == kFwd ? 2 : 128) * k, bd + (MODE != kWgrad ? 2 : 128) * k, idesc,
+                          !begins || k != 0);
+            commit<CG>(empty(s));
+            if (ends) commit<CG>(acc_full(buf));
+          }
+          __syncwarp();
         }
-        __syncwarp();
       }
-      if (ok) {
-        if (leader) commit<CG>(acc_full(buf));
+      if (!ok) {   // MMAs in flight
+        if (leader) commit<CG>(drain);
         __syncwarp();
+        drain_wait(drain, 0);
       }
     }
-    if (!ok) {   // MMAs in flight
-      if (leader) commit<CG>(drain);
-      __syncwarp();
-      drain_wait(drain, 0);
-    }
-  } else if (warp >= kEpiWarp) {
+  } else {
     // ---------------- epilogue ----------------
-    const int q = warp & 3, h = (warp - kEpiWarp) >> 2, ew = warp - kEpiWarp;   // lane quarter; every other chunk of columns
+    if (C::kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    const int q = warp & 3, h = (warp - kEpiWarp) >> 2, ew = warp - kEpiWarp;
     Ring<2> ab;
+    // this warp's 32 lanes and every other 32 columns (wgrad: 64)
+    constexpr int kOwn = TN >= 64 ? TN / 64 : 1;
+    auto own = [&](int i) { return MODE == kWgrad ? 128 * (i >> 1) + 64 * h + 32 * (i & 1) : 64 * i + 32 * h; };
     auto release = [&](int buf) {   // the accumulator may be written again
-      __syncwarp();
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+      if (CG == 1) mbar_arrive_if(acc_empty(buf), lane == 0);
+      else mbar_arrive_at_if(acc_empty(buf), 0, lane == 0);
+    };
+    // 32 tokens x 32 elements as 8 x 8 fragments to 16-bit token rows, transposed
+    // through shared memory: a store instruction is then 64 bytes of 8 rows (a
+    // column a store, 2 bytes a lane, made the epilogue 2.5 times as long)
+    auto store_16 = [&](const Tile& t, int m0, int c0, const uint32_t* v) {
+      uint8_t* box = smem + C::kOffOut + ew * 32 * kOutPitch;
+      const int chunk = lane & 3, n = m0 + 8 * chunk;
+      auto two = [&](int c) { return to_16x2(__uint_as_float(v[c]), __uint_as_float(v[c + 1]), p.bf16); };
+      __syncwarp();
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        store_transposed(saddr(box) + (8 * g + (lane & 7)) * kOutPitch + (lane >> 3) * 16, two(4 * g), two(4 * g + 2),
+                         two(16 + 4 * g), two(16 + 4 * g + 2));
+      __syncwarp();
+      if (n >= p.M) return;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int tok = (lane >> 2) + 8 * j;
+        if (c0 + tok < t.cols)
+          *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) +
+                                    (size_t)(t.row0 + t.c0 + c0 + tok) * (size_t)p.ld_out + n) =
+              *reinterpret_cast<const uint4*>(box + tok * kOutPitch + chunk * 16);
+      }
+    };
+    // 128 bytes x 32 rows of dw through shared memory (128-byte swizzle) and
+    // TMA; the map ends at N and K
+    auto store_box = [&](uint8_t* box, const Tile& t, int m0, int c0, const uint4* v) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) *reinterpret_cast<uint4*>(box + lane * 128 + ((j ^ (lane & 7)) << 4)) = v[j];
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) {
-        if (CG == 1) mbar_arrive(acc_empty(buf));
-        else mbar_arrive_at(acc_empty(buf), 0);
+        asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                         reinterpret_cast<uint64_t>(&mapO)),
+                     "r"(t.c0 + c0), "r"(m0), "r"(t.e), "r"(saddr(box))
+                     : "memory");
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
       }
     };
-    // 32 rows of dw from row n0: boxes of 128 bytes x 32 rows through shared
-    // memory (128-byte swizzle), two in flight; the map ends at N and K.  By
-    // one warp per lane quarter: with all eight, the boxes cost the ring a
-    // stage (32 experts, 128 rows, 4096 x 3584: 183 us, 221)
     uint32_t obuf = 0;
-    auto store_dw = [&](const Tile& t, int n0, uint32_t trow, bool sums) {
-      const int per = p.out_f32 ? 32 : 64;
-      if (n0 >= p.M || h != 0) return;
-      for (int c0 = 0; c0 < t.cols; c0 += per) {
-        uint32_t v[64];
-        if (sums) {
-          tmem_ld32_nowait(trow + c0, v);
-          if (!p.out_f32) tmem_ld32_nowait(trow + c0 + 32, v + 32);
-          tmem_ld_wait<64>(v);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 64; ++i) v[i] = 0u;
-        }
-        if (!p.out_f32) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = to_16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]), p.bf16);
-        }
-        // the box written two steps ago has been read
-        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-        __syncwarp();
-        uint8_t* box = smem + C::kOffOut + (2 * q + obuf) * 4096;
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          *reinterpret_cast<uint4*>(box + lane * 128 + ((j ^ (lane & 7)) << 4)) =
-              make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) {
-          asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
-                           reinterpret_cast<uint64_t>(&mapO)),
-                       "r"(t.c0 + c0), "r"(n0), "r"(t.e), "r"(saddr(box))
-                       : "memory");
-          asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-        }
-        obuf ^= 1;
-      }
-    };
-    for (int idx = first; idx < total; idx += stride) {
+    // 16-bit results go straight from TMEM to memory; fp32 ones, parts and
+    // additions to dw are summed up in registers first
+    const bool direct = !SPLIT && !p.out_f32 && !(MODE == kWgrad && p.accumulate);
+    for (int idx = first; idx < total && direct; idx += stride) {
       const Tile t = tile_of<CG, MODE, TN>(p, tp, idx);
-      const int m = t.m0 + 128 * (int)rank + 32 * q + lane;
-      const bool vm = m < p.M;
-      if (MODE == kWgrad && stage_from(t) == stage_to(t)) {   // an expert without rows; a part without stages
-        if (!SPLIT && !p.accumulate) store_dw(t, m - lane, 0, false);
-        continue;
+      const int m0 = t.m0 + 128 * (int)rank + 32 * q;
+      const bool sums = t.nk > 0;   // else an expert without rows: zeros
+      int buf = 0;
+      if (sums) {
+        buf = ab.s;
+        if (!warp_wait(acc_full(buf), ab.ph, p.err, 75)) break;
+        ab.next();
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       }
-      const int buf = ab.s;
-      if (!warp_wait(acc_full(buf), ab.ph, p.err, 75)) break;
-      ab.next();
-      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const uint32_t trow = tmem + buf * TN + ((uint32_t)(32 * q) << 16);
-      if (MODE == kWgrad && !SPLIT && !p.accumulate) {
-        store_dw(t, m - lane, trow, true);
-        release(buf);
-        continue;
-      }
-      if (MODE == kWgrad && SPLIT) {   // this CTA's part, [n][k], over the ring: its copies and MMAs are done
-        float* dst = reinterpret_cast<float*>(smem) + (32 * q + lane) * kPartPitch;
-        for (int c0 = 16 * h; c0 < t.cols; c0 += 32) {
-          float v[16];
+      if (MODE != kWgrad) {
+#pragma unroll 1
+        for (int c0 = 32 * h; c0 < t.cols; c0 += 64) {
+          uint32_t d[32];
           __syncwarp();
-          tmem_ld16(trow + c0, v);
-#pragma unroll
-          for (int c = 0; c < 16; c += 4) *reinterpret_cast<float4*>(dst + c0 + c) = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
+          tmem_ld_frag_nowait(trow + c0, d);
+          tmem_ld_frag_nowait(trow + (16u << 16) + c0, d + 16);
+          tmem_ld_wait<32>(d);
+          store_16(t, m0, c0, d);
         }
-      } else if (MODE == kWgrad) {   // dw += sums
-        for (int c0 = 16 * h; c0 < t.cols; c0 += 32) {
-          float v[16];
+      } else if (h == 0 && m0 < p.M) {
+        // by one warp per lane quarter, two boxes each: with all eight the
+        // stores came out slower (32 experts, 128 rows, 4096 x 3584: 221 us, 183)
+#pragma unroll 1
+        for (int c0 = 0; c0 < t.cols; c0 += 64) {
+          uint32_t d[64];
+          if (sums) {
+            tmem_ld32_nowait(trow + c0, d);
+            tmem_ld32_nowait(trow + c0 + 32, d + 32);
+            tmem_ld_wait<64>(d);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 64; ++i) d[i] = 0u;
+          }
+          uint4 v[8];
+          auto two = [&](int c) { return to_16x2(__uint_as_float(d[c]), __uint_as_float(d[c + 1]), p.bf16); };
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] = make_uint4(two(8 * j), two(8 * j + 2), two(8 * j + 4), two(8 * j + 6));
+          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");   // the box two steps ago has been read
           __syncwarp();
-          tmem_ld16(trow + c0, v);
-          if (!vm) continue;
-          const size_t at = ((size_t)t.e * p.M + m) * (size_t)p.ld_out + t.c0 + c0;
+          store_box(smem + C::kOffOut + (2 * q + obuf) * 4096, t, m0, c0, v);
+          obuf ^= 1;
+        }
+      }
+      __syncwarp();
+      if (sums) release(buf);
+    }
+    for (int idx = first; idx < total && !direct; idx += stride) {
+      const Tile t = tile_of<CG, MODE, TN>(p, tp, idx);
+      float acc[kOwn][32];
 #pragma unroll
-          for (int g = 0; g < 2; ++g) {   // columns come in eights
-            if (c0 + 8 * g >= t.cols) continue;
-            float* w = v + 8 * g;
-            if (p.out_f32) {
-              float4* dst = reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + at + 8 * g);
+      for (int i = 0; i < kOwn; ++i)
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                float4 f = make_float4(w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3]);
-                if (p.accumulate) {
-                  const float4 o = dst[h];
-                  f = make_float4(f.x + o.x, f.y + o.y, f.z + o.z, f.w + o.w);
-                }
-                dst[h] = f;
-              }
-            } else {
-              uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + at + 8 * g);
-              if (p.accumulate) {
-                const uint4 o = *dst;
-                const uint32_t ow[4] = {o.x, o.y, o.z, o.w};
+        for (int c = 0; c < 32; ++c) acc[i][c] = 0.f;
+      bool ok = true;
+      for (int kk = stage_from(t), to = stage_to(t); kk < to; kk += p.chunk) {
+        const int buf = ab.s;
+        if (!warp_wait(acc_full(buf), ab.ph, p.err, 75)) {
+          ok = false;
+          break;
+        }
+        ab.next();
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const uint32_t trow = tmem + buf * TN + ((uint32_t)(32 * q) << 16);
 #pragma unroll
-                for (int h = 0; h < 8; ++h) w[h] += from_16((ow[h >> 1] >> (16 * (h & 1))) & 0xFFFFu, p.bf16);
-              }
-              *dst = make_uint4(to_16x2(w[0], w[1], p.bf16), to_16x2(w[2], w[3], p.bf16), to_16x2(w[4], w[5], p.bf16),
-                                to_16x2(w[6], w[7], p.bf16));
-            }
+        for (int i = 0; i < kOwn; ++i) {
+          if (own(i) >= t.cols) continue;
+          uint32_t d[32];
+          if (MODE == kWgrad) {   // a lane is a row of dw
+            tmem_ld32_nowait(trow + own(i), d);
+          } else {                // 8 x 8 fragments, to be stored transposed
+            tmem_ld_frag_nowait(trow + own(i), d);
+            tmem_ld_frag_nowait(trow + (16u << 16) + own(i), d + 16);
+          }
+          tmem_ld_wait<32>(d);
+#pragma unroll
+          for (int c = 0; c < 32; ++c) acc[i][c] += __uint_as_float(d[c]);
+        }
+        release(buf);
+      }
+      if (!ok) break;
+      const int m0 = t.m0 + 128 * (int)rank + 32 * q;
+      if (SPLIT) {   // this CTA's part, over the ring: its copies and MMAs are done
+        float* part_at = reinterpret_cast<float*>(smem);
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) {
+          if (own(i) >= t.cols) continue;
+          if (MODE == kWgrad) {
+#pragma unroll
+            for (int c = 0; c < 32; c += 4)
+              *reinterpret_cast<float4*>(part_at + (32 * q + lane) * kPartPitch + own(i) + c) =
+                  make_float4(acc[i][c], acc[i][c + 1], acc[i][c + 2], acc[i][c + 3]);
+          } else {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) part_at[(own(i) + frag_col(c, lane)) * kJoinPitch + 32 * q + frag_row(c, lane)] = acc[i][c];
           }
         }
-      } else if (SPLIT) {   // this CTA's part, [token][128], over the ring: its copies and MMAs are done
-        float* dst = reinterpret_cast<float*>(smem) + 32 * q + lane;
-        for (int c0 = 16 * h; c0 < t.cols; c0 += 32) {
-          float v[16];
-          __syncwarp();
-          tmem_ld16(trow + c0, v);
+      } else if (MODE == kWgrad && p.accumulate) {
+        if (m0 + lane < p.M && t.nk > 0) {
 #pragma unroll
-          for (int c = 0; c < 16; ++c) dst[(c0 + c) * 128] = v[c];
+          for (int i = 0; i < kOwn; ++i)
+#pragma unroll
+            for (int c = 0; c < 32; c += 8)   // columns come in eights
+              if (own(i) + c < t.cols)
+                add_dw(p, ((size_t)t.e * p.M + m0 + lane) * (size_t)p.ld_out + t.c0 + own(i) + c, acc[i] + c);
         }
-      } else if (p.out_f32) {
-        // through shared memory, 16 tokens x 32 elements at a time: 16-byte
-        // stores of 4 token rows each, where one column a store (128 bytes of
-        // a row) made the epilogue 2.5 times as long as a 16-bit one
-        const int chunk = lane & 7, n = m - lane + 4 * chunk;
+      } else if (MODE == kWgrad) {   // fp32
+        uint8_t* box = smem + C::kOffOut + ew * 4096;
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) {
+          if (own(i) >= t.cols || m0 >= p.M) continue;
+          uint4 v[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            v[j] = make_uint4(__float_as_uint(acc[i][4 * j]), __float_as_uint(acc[i][4 * j + 1]),
+                              __float_as_uint(acc[i][4 * j + 2]), __float_as_uint(acc[i][4 * j + 3]));
+          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");   // the box before has been read
+          __syncwarp();
+          store_box(box, t, m0, own(i), v);
+        }
+      } else {   // fp32: 16 tokens x 32 elements at a time, 128 bytes of 4 token rows a store
         uint8_t* box = smem + C::kOffOut + ew * 32 * kOutPitch;
-        for (int c0 = 16 * h; c0 < t.cols; c0 += 32) {
-          float v[16];
-          __syncwarp();
-          tmem_ld16(trow + c0, v);
+        const int chunk = lane & 7, n = m0 + 4 * chunk;
 #pragma unroll
-          for (int c = 0; c < 16; ++c) *reinterpret_cast<float*>(box + c * kOutPitchF + 4 * lane) = v[c];
-          __syncwarp();
-          if (n < p.M) {
+        for (int i = 0; i < kOwn; ++i) {
+          const int c0 = own(i);
+          if (c0 >= t.cols) continue;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int tok = (lane >> 3) + 4 * i;
-              if (c0 + tok < t.cols)
+          for (int s = 0; s < 2; ++s) {
+            __syncwarp();
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (((c >> 3) & 1) == s)
+                *reinterpret_cast<float*>(box + (frag_col(c, lane) - 16 * s) * kOutPitchF + 4 * frag_row(c, lane)) = acc[i][c];
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int tok = (lane >> 3) + 4 * j;
+              if (n < p.M && c0 + 16 * s + tok < t.cols)
                 *reinterpret_cast<uint4*>(reinterpret_cast<float*>(p.out) +
-                                          (size_t)(t.row0 + t.c0 + c0 + tok) * (size_t)p.ld_out + n) =
+                                          (size_t)(t.row0 + t.c0 + c0 + 16 * s + tok) * (size_t)p.ld_out + n) =
                     *reinterpret_cast<const uint4*>(box + tok * kOutPitchF + chunk * 16);
             }
           }
         }
-      } else {
-        // transposed through shared memory, 32 tokens at a time: a store
-        // instruction is then 64 bytes of 8 token rows, where storing straight
-        // from the accumulator's layout takes 2 bytes a lane
-        const uint32_t box = sbase + C::kOffOut + ew * 32 * kOutPitch;
-        const int chunk = lane & 3, n = m - lane + 8 * chunk;
-        for (int c0 = 32 * h; c0 < t.cols; c0 += 64) {
-          uint32_t v[32];
-          __syncwarp();
-          tmem_ld_frag_nowait(trow + c0, v);
-          tmem_ld_frag_nowait(trow + (16u << 16) + c0, v + 16);
-          tmem_ld_wait<32>(v);
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            auto two = [&](int i) { return to_16x2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]), p.bf16); };
-            store_transposed(box + (8 * g + (lane & 7)) * kOutPitch + (lane >> 3) * 16, two(4 * g), two(4 * g + 2),
-                             two(16 + 4 * g), two(16 + 4 * g + 2));
-          }
-          __syncwarp();
-          if (n < p.M) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int tok = (lane >> 2) + 8 * i;
-              if (c0 + tok < t.cols)
-                *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) +
-                                          (size_t)(t.row0 + t.c0 + c0 + tok) * (size_t)p.ld_out + n) =
-                    *reinterpret_cast<const uint4*>(smem + C::kOffOut + ew * 32 * kOutPitch + tok * kOutPitch + chunk * 16);
-            }
-          }
-        }
       }
-      release(buf);
+      __syncwarp();
     }
     if (MODE == kWgrad && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     // rows of no group
@@ -549,7 +608,7 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
     if (first < total && *reinterpret_cast<volatile int*>(p.err) == 0) {
       const Tile t = tile_of<CG, MODE, TN>(p, tp, first);
       if (MODE == kWgrad) join_dw(p, t, sbase, part, parts, tid);
-      else join_parts(sbase, t.cols, tid, kThreads, [&](int col, int m, float2 v) {
+      else join_parts(sbase, kJoinPitch, t.cols, tid, kThreads, [&](int col, int m, float2 v) {
         if (t.m0 + m >= p.M) return;   // M is even
         const size_t at = (size_t)(t.row0 + t.c0 + col) * (size_t)p.ld_out + t.m0 + m;
         if (p.out_f32) *reinterpret_cast<float2*>(reinterpret_cast<float*>(p.out) + at) = v;
@@ -576,6 +635,13 @@ cudaError_t launch_t(const Maps& m, const GgParams& p, long max_items, cudaStrea
   static std::atomic<uint64_t> raised{0};
   const long sms = sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
+  if (Cfg<CG, MODE, TN>::kSplitRegs) {   // the shares need the launch to hold their sum
+    static const int regs = [] {
+      cudaFuncAttributes fa;
+      return cudaFuncGetAttributes(&fa, gg_kernel<CG, MODE, TN, SPLIT>) == cudaSuccess ? fa.numRegs : 0;
+    }();
+    if (regs < kLaunchRegs) return cudaErrorInvalidConfiguration;
+  }
   const int cluster = SPLIT ? split : CG;
   const long tiles = SPLIT || max_items < sms / CG ? max_items : sms / CG;
   return launch_cluster(gg_kernel<CG, MODE, TN, SPLIT>, &raised, cluster, (int)(tiles < 1 ? 1 : tiles) * cluster, kThreads,
@@ -628,6 +694,7 @@ extern "C" situ_status situ_moe_grouped_gemm(const situ_grouped_gemm_args* g, vo
   p.out_f32 = g->out_dtype == SITU_DT_F32;
   p.accumulate = g->accumulate;
   p.zero_rest = !g->keep_rest;
+  p.chunk = p.out_f32 ? kSumStages : 1 << 30;
   p.err = g->device_status;
   p.M = mode == kDgrad ? g->K : g->N;
   p.L = mode == kDgrad ? g->N : g->K;
