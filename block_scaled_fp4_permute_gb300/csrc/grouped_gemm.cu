@@ -68,7 +68,6 @@ struct GgParams {
   void* out;
   long ld_out;      // elements
   int bf16, out_f32, accumulate, zero_rest;
-  int chunk;        // stages summed in TMEM
   int* err;
 };
 
@@ -201,7 +200,10 @@ __device__ __forceinline__ void join_dw(const GgParams& p, const Tile& t, uint32
   }
 }
 
-template <int CG, int MODE, int TN, bool SPLIT>
+// SUMS: the sums of a chunk of stages are added up in registers (fp32 results,
+// additions to dw); else 16-bit results go straight from TMEM to memory.  A
+// build of each, because carrying both cost the 16-bit form 2 to 4 %.
+template <int CG, int MODE, int TN, bool SUMS, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
 gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
           const __grid_constant__ CUtensorMap mapA1, const __grid_constant__ CUtensorMap mapB1,
@@ -212,7 +214,7 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = CG == 2 ? cluster_rank() : 0;
-  static_assert(!SPLIT || CG == 1, "split tiles");
+  static_assert(!SPLIT || (CG == 1 && SUMS), "split tiles");
   const int part = SPLIT ? (int)cluster_rank() : 0, parts = SPLIT ? (int)cluster_size() : 1;
   const uint32_t sbase = saddr(smem);
   int* tp = reinterpret_cast<int*>(smem + C::kOffTp);
@@ -255,7 +257,7 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
   auto stage_to = [&](const Tile& t) { return SPLIT ? t.nk * (part + 1) / parts : t.nk; };
 
   if (warp < kEpiWarp) {
-    if (C::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (C::kSplitRegs && SUMS) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 0) {
       // ---------------- copies ----------------
       const bool leader = elect_one();
@@ -345,37 +347,39 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
         const uint32_t idesc = id0 | ((uint32_t)(nact >> 3) << 17);
         const int len = MODE == kWgrad ? t.rows : p.L;
         const int from = stage_from(t), to = stage_to(t);
-        int buf = 0, in_chunk = 0;
-        for (int kk = from; kk < to; ++kk, r.next()) {
-          const bool begins = in_chunk == 0, ends = ++in_chunk == p.chunk || kk + 1 == to;
-          if (ends) in_chunk = 0;
-          if (begins) {   // a chunk's sums start from zero in the other accumulator
-            buf = ab.s;
-            if (!warp_wait(acc_empty(buf), ab.ph ^ 1, p.err, 73)) {
-              ok = false;
-              break;
-            }
-            ab.next();
-          }
-          const int s = r.s;
-          if (!warp_wait(full(s), r.ph, p.err, 74)) {
+        for (int k0 = from; k0 < to && ok;) {   // a chunk's sums start from zero in the other accumulator
+          const int k1 = SUMS ? min(k0 + kSumStages, to) : to, buf = ab.s;
+          if (ab.used == 2 && !warp_wait(acc_empty(buf), ab.ph ^ 1, p.err, 73)) {
             ok = false;
             break;
           }
+          ab.next();
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          if (leader) {
-            const uint32_t a = sbase + s * kABytes, b = sbase + C::kOffB + s * C::kBBytes;
-            const uint64_t ad = MODE == kFwd ? sdesc(a) : sdesc_mn(a, 8192);
-            const uint64_t bd = MODE != kWgrad ? sdesc(b) : sdesc_mn(b, 8192);
-            const int steps = min(4, (len - kk * kBK + 15) >> 4);
-            // per 16 contraction elements: 32 bytes along a K-major row, 16 rows of 128 bytes else
-            for (int k = 0; k < steps; ++k)
-              mma_f16<CG>(tmem + buf * TN, ad + (MODE == kFwd ? 2 : 128) * k, bd + (MODE != kWgrad ? 2 : 128) * k, idesc,
-                          !begins || k != 0);
-            commit<CG>(empty(s));
-            if (ends) commit<CG>(acc_full(buf));
+          for (int kk = k0; kk < k1; ++kk, r.next()) {
+            const int s = r.s;
+            if (!warp_wait(full(s), r.ph, p.err, 74)) {
+              ok = false;
+              break;
+            }
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            if (leader) {
+              const uint32_t a = sbase + s * kABytes, b = sbase + C::kOffB + s * C::kBBytes;
+              const uint64_t ad = MODE == kFwd ? sdesc(a) : sdesc_mn(a, 8192);
+              const uint64_t bd = MODE != kWgrad ? sdesc(b) : sdesc_mn(b, 8192);
+              const int steps = min(4, (len - kk * kBK + 15) >> 4);
+              // per 16 contraction elements: 32 bytes along a K-major row, 16 rows of 128 bytes else
+              for (int k = 0; k < steps; ++k)
+                mma_f16<CG>(tmem + buf * TN, ad + (MODE == kFwd ? 2 : 128) * k, bd + (MODE != kWgrad ? 2 : 128) * k, idesc,
+                            ((kk - k0) | k) != 0);
+              commit<CG>(empty(s));
+            }
+            __syncwarp();
           }
-          __syncwarp();
+          if (ok) {
+            if (leader) commit<CG>(acc_full(buf));
+            __syncwarp();
+          }
+          k0 = k1;
         }
       }
       if (!ok) {   // MMAs in flight
@@ -386,7 +390,7 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
     }
   } else {
     // ---------------- epilogue ----------------
-    if (C::kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    if (C::kSplitRegs && SUMS) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
     const int q = warp & 3, h = (warp - kEpiWarp) >> 2, ew = warp - kEpiWarp;
     Ring<2> ab;
     // this warp's 32 lanes and every other 32 columns (wgrad: 64)
@@ -436,10 +440,7 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
       }
     };
     uint32_t obuf = 0;
-    // 16-bit results go straight from TMEM to memory; fp32 ones, parts and
-    // additions to dw are summed up in registers first
-    const bool direct = !SPLIT && !p.out_f32 && !(MODE == kWgrad && p.accumulate);
-    for (int idx = first; idx < total && direct; idx += stride) {
+    for (int idx = first; idx < total && !SUMS; idx += stride) {
       const Tile t = tile_of<CG, MODE, TN>(p, tp, idx);
       const int m0 = t.m0 + 128 * (int)rank + 32 * q;
       const bool sums = t.nk > 0;   // else an expert without rows: zeros
@@ -488,7 +489,7 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
       __syncwarp();
       if (sums) release(buf);
     }
-    for (int idx = first; idx < total && !direct; idx += stride) {
+    for (int idx = first; idx < total && SUMS; idx += stride) {
       const Tile t = tile_of<CG, MODE, TN>(p, tp, idx);
       float acc[kOwn][32];
 #pragma unroll
@@ -496,7 +497,7 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
 #pragma unroll
         for (int c = 0; c < 32; ++c) acc[i][c] = 0.f;
       bool ok = true;
-      for (int kk = stage_from(t), to = stage_to(t); kk < to; kk += p.chunk) {
+      for (int kk = stage_from(t), to = stage_to(t); kk < to; kk += kSumStages) {
         const int buf = ab.s;
         if (!warp_wait(acc_full(buf), ab.ph, p.err, 75)) {
           ok = false;
@@ -630,22 +631,38 @@ struct Maps {
 };
 
 // split: CTAs per tile (SPLIT), with one tile per cluster
-template <int CG, int MODE, int TN, bool SPLIT = false>
+template <int CG, int MODE, int TN, bool SUMS, bool SPLIT = false>
 cudaError_t launch_t(const Maps& m, const GgParams& p, long max_items, cudaStream_t st, int split = 1) {
   static std::atomic<uint64_t> raised{0};
   const long sms = sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
-  if (Cfg<CG, MODE, TN>::kSplitRegs) {   // the shares need the launch to hold their sum
+  if (Cfg<CG, MODE, TN>::kSplitRegs && SUMS) {   // the shares need the launch to hold their sum
     static const int regs = [] {
       cudaFuncAttributes fa;
-      return cudaFuncGetAttributes(&fa, gg_kernel<CG, MODE, TN, SPLIT>) == cudaSuccess ? fa.numRegs : 0;
+      return cudaFuncGetAttributes(&fa, gg_kernel<CG, MODE, TN, SUMS, SPLIT>) == cudaSuccess ? fa.numRegs : 0;
     }();
     if (regs < kLaunchRegs) return cudaErrorInvalidConfiguration;
   }
   const int cluster = SPLIT ? split : CG;
   const long tiles = SPLIT || max_items < sms / CG ? max_items : sms / CG;
-  return launch_cluster(gg_kernel<CG, MODE, TN, SPLIT>, &raised, cluster, (int)(tiles < 1 ? 1 : tiles) * cluster, kThreads,
+  return launch_cluster(gg_kernel<CG, MODE, TN, SUMS, SPLIT>, &raised, cluster, (int)(tiles < 1 ? 1 : tiles) * cluster, kThreads,
                         Cfg<CG, MODE, TN>::kSmem, st, m.a, m.b, m.a1, m.b1, m.a16, m.b16, m.out, p);
+}
+
+// forward and dgrad by their tiles
+template <int MODE, bool SUMS>
+cudaError_t launch_rows(int tn, int cg, const Maps& m, const GgParams& p, long cap, cudaStream_t st) {
+  return tn == 32    ? launch_t<1, MODE, 32, SUMS>(m, p, cap, st)
+         : tn == 64  ? launch_t<1, MODE, 64, SUMS>(m, p, cap, st)
+         : tn == 128 ? launch_t<1, MODE, 128, SUMS>(m, p, cap, st)
+         : cg == 2   ? launch_t<2, MODE, 256, SUMS>(m, p, cap, st)
+                     : launch_t<1, MODE, 256, SUMS>(m, p, cap, st);
+}
+template <int MODE>
+cudaError_t launch_split(int tn, const Maps& m, const GgParams& p, long cap, cudaStream_t st, int split) {
+  return tn == 32   ? launch_t<1, MODE, 32, true, true>(m, p, cap, st, split)
+         : tn == 64 ? launch_t<1, MODE, 64, true, true>(m, p, cap, st, split)
+                    : launch_t<1, MODE, 128, true, true>(m, p, cap, st, split);
 }
 
 bool fits16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -694,7 +711,6 @@ extern "C" situ_status situ_moe_grouped_gemm(const situ_grouped_gemm_args* g, vo
   p.out_f32 = g->out_dtype == SITU_DT_F32;
   p.accumulate = g->accumulate;
   p.zero_rest = !g->keep_rest;
-  p.chunk = p.out_f32 ? kSumStages : 1 << 30;
   p.err = g->device_status;
   p.M = mode == kDgrad ? g->K : g->N;
   p.L = mode == kDgrad ? g->N : g->K;
@@ -718,7 +734,7 @@ extern "C" situ_status situ_moe_grouped_gemm(const situ_grouped_gemm_args* g, vo
   // skewed group's rows are taken as up to twice the average)
   const double wtiles = (double)p.E * ((p.M + 127) / 128) * ((p.Ncol + 255) / 256);
   const int wsteps = (int)((g->E > 1 ? 2 * per : per) / kBK);
-  const int wsplit = mode == kWgrad ? split_of(gg_kernel<1, kWgrad, 256, true>, kThreads, Cfg<1, kWgrad, 256>::kSmem, wtiles, wsteps, kSplitLeast) : 1;
+  const int wsplit = mode == kWgrad ? split_of(gg_kernel<1, kWgrad, 256, true, true>, kThreads, Cfg<1, kWgrad, 256>::kSmem, wtiles, wsteps, kSplitLeast) : 1;
   const int cg = tn == 256 && p.M > 128 && wsplit == 1 ? 2 : 1;
   p.n_mt = (p.M + 128 * cg - 1) / (128 * cg);
   p.n_nt = (p.Ncol + tn - 1) / tn;
@@ -749,32 +765,21 @@ extern "C" situ_status situ_moe_grouped_gemm(const situ_grouped_gemm_args* g, vo
   const double most = most_tiles(g->S, g->E, tn) * p.n_mt;
   const long cap = most > 1e6 ? 1000000 : (long)most;
   const int steps = (p.L + kBK - 1) / kBK;
-  const int split = tn <= 128 ? split_of(gg_kernel<1, kFwd, 32, true>, kThreads, Cfg<1, kFwd, 32>::kSmem, most, steps, kSplitLeast) : 1;
+  const int split = tn <= 128 ? split_of(gg_kernel<1, kFwd, 32, true, true>, kThreads, Cfg<1, kFwd, 32>::kSmem, most, steps, kSplitLeast) : 1;
+  const bool sums = p.out_f32 || p.accumulate;
   cudaError_t e;
   if (mode == kWgrad && wsplit > 1) {
-    e = launch_t<1, kWgrad, 256, true>(m, p, (long)items, st, wsplit);
+    e = launch_t<1, kWgrad, 256, true, true>(m, p, (long)items, st, wsplit);
   } else if (mode == kWgrad) {
     const long all = items > 1e6 ? 1000000 : (long)items;
-    e = cg == 2 ? launch_t<2, kWgrad, 256>(m, p, all, st) : launch_t<1, kWgrad, 256>(m, p, all, st);
+    e = cg == 2 ? (sums ? launch_t<2, kWgrad, 256, true>(m, p, all, st) : launch_t<2, kWgrad, 256, false>(m, p, all, st))
+                : (sums ? launch_t<1, kWgrad, 256, true>(m, p, all, st) : launch_t<1, kWgrad, 256, false>(m, p, all, st));
   } else if (split > 1) {
-    e = mode == kFwd ? (tn == 32   ? launch_t<1, kFwd, 32, true>(m, p, cap, st, split)
-                        : tn == 64 ? launch_t<1, kFwd, 64, true>(m, p, cap, st, split)
-                                   : launch_t<1, kFwd, 128, true>(m, p, cap, st, split))
-                     : (tn == 32   ? launch_t<1, kDgrad, 32, true>(m, p, cap, st, split)
-                        : tn == 64 ? launch_t<1, kDgrad, 64, true>(m, p, cap, st, split)
-                                   : launch_t<1, kDgrad, 128, true>(m, p, cap, st, split));
+    e = mode == kFwd ? launch_split<kFwd>(tn, m, p, cap, st, split) : launch_split<kDgrad>(tn, m, p, cap, st, split);
   } else if (mode == kFwd) {
-    e = tn == 32    ? launch_t<1, kFwd, 32>(m, p, cap, st)
-        : tn == 64  ? launch_t<1, kFwd, 64>(m, p, cap, st)
-        : tn == 128 ? launch_t<1, kFwd, 128>(m, p, cap, st)
-        : cg == 2   ? launch_t<2, kFwd, 256>(m, p, cap, st)
-                    : launch_t<1, kFwd, 256>(m, p, cap, st);
+    e = sums ? launch_rows<kFwd, true>(tn, cg, m, p, cap, st) : launch_rows<kFwd, false>(tn, cg, m, p, cap, st);
   } else {
-    e = tn == 32    ? launch_t<1, kDgrad, 32>(m, p, cap, st)
-        : tn == 64  ? launch_t<1, kDgrad, 64>(m, p, cap, st)
-        : tn == 128 ? launch_t<1, kDgrad, 128>(m, p, cap, st)
-        : cg == 2   ? launch_t<2, kDgrad, 256>(m, p, cap, st)
-                    : launch_t<1, kDgrad, 256>(m, p, cap, st);
+    e = sums ? launch_rows<kDgrad, true>(tn, cg, m, p, cap, st) : launch_rows<kDgrad, false>(tn, cg, m, p, cap, st);
   }
   return e == cudaSuccess ? SITU_OK : SITU_ERR_CUDA;
 }
