@@ -38,6 +38,8 @@
 #include "../../include/situ_moe.h"
 #include "gemm_groups.cuh"
 
+#include <type_traits>
+
 namespace situ {
 
 using namespace gg;
@@ -68,6 +70,7 @@ struct GgParams {
   void* out;
   long ld_out;      // elements
   int bf16, out_f32, accumulate, zero_rest;
+  int store8;       // 16-bit dw stored by all eight epilogue warps
   int* err;
 };
 
@@ -462,29 +465,36 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
           tmem_ld_wait<32>(d);
           store_16(t, m0, c0, d);
         }
-      } else if (h == 0 && m0 < p.M) {
-        // by one warp per lane quarter, two boxes each: with all eight the
-        // stores came out slower (32 experts, 128 rows, 4096 x 3584: 221 us, 183)
+      } else if (m0 < p.M) {
+        // by one warp per lane quarter with two boxes, or by two with one each
+        auto store_dw = [&](auto eight) {
+          constexpr bool kEight = decltype(eight)::value;
 #pragma unroll 1
-        for (int c0 = 0; c0 < t.cols; c0 += 64) {
-          uint32_t d[64];
-          if (sums) {
-            tmem_ld32_nowait(trow + c0, d);
-            tmem_ld32_nowait(trow + c0 + 32, d + 32);
-            tmem_ld_wait<64>(d);
-          } else {
+          for (int c0 = kEight ? 64 * h : 0; c0 < t.cols; c0 += kEight ? 128 : 64) {
+            uint32_t d[64];
+            if (sums) {
+              tmem_ld32_nowait(trow + c0, d);
+              tmem_ld32_nowait(trow + c0 + 32, d + 32);
+              tmem_ld_wait<64>(d);
+            } else {
 #pragma unroll
-            for (int i = 0; i < 64; ++i) d[i] = 0u;
+              for (int i = 0; i < 64; ++i) d[i] = 0u;
+            }
+            uint4 v[8];
+            auto two = [&](int c) { return to_16x2(__uint_as_float(d[c]), __uint_as_float(d[c + 1]), p.bf16); };
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = make_uint4(two(8 * j), two(8 * j + 2), two(8 * j + 4), two(8 * j + 6));
+            if (lane == 0) {   // the box's last store has read it
+              if (kEight) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+              else asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+            }
+            __syncwarp();
+            store_box(smem + C::kOffOut + (kEight ? ew : 2 * q + obuf) * 4096, t, m0, c0, v);
+            obuf ^= 1;
           }
-          uint4 v[8];
-          auto two = [&](int c) { return to_16x2(__uint_as_float(d[c]), __uint_as_float(d[c + 1]), p.bf16); };
-#pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] = make_uint4(two(8 * j), two(8 * j + 2), two(8 * j + 4), two(8 * j + 6));
-          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");   // the box two steps ago has been read
-          __syncwarp();
-          store_box(smem + C::kOffOut + (2 * q + obuf) * 4096, t, m0, c0, v);
-          obuf ^= 1;
-        }
+        };
+        if (p.store8) store_dw(std::true_type{});
+        else if (h == 0) store_dw(std::false_type{});
       }
       __syncwarp();
       if (sums) release(buf);
@@ -732,9 +742,15 @@ extern "C" situ_status situ_moe_grouped_gemm(const situ_grouped_gemm_args* g, vo
                  : per <= room[2] || most_tiles(g->S, g->E, 128) * ((p.M + 127) / 128) <= sm_count() ? 128 : 256;
   // wgrad of few output tiles: the rows of a group split over clusters (a
   // skewed group's rows are taken as up to twice the average)
+  // Short contractions are bound by the stores, which eight warps issue faster
+  // (896 experts, one row each, 768 x 3584: 0.79 ms, four warps 0.89; 112 of
+  // 6144 x 3584, 75 rows: 0.93, 0.94; 32 of 4096 x 3584, 128 rows: 0.21, 0.18).
+  p.store8 = per <= 75;
   const double wtiles = (double)p.E * ((p.M + 127) / 128) * ((p.Ncol + 255) / 256);
   const int wsteps = (int)((g->E > 1 ? 2 * per : per) / kBK);
-  const int wsplit = mode == kWgrad ? split_of(gg_kernel<1, kWgrad, 256, true, true>, kThreads, Cfg<1, kWgrad, 256>::kSmem, wtiles, wsteps, kSplitLeast) : 1;
+  const int wsplit = mode == kWgrad ? split_of(gg_kernel<1, kWgrad, 256, true, true>, kThreads,
+                                               Cfg<1, kWgrad, 256>::kSmem, wtiles, wsteps, kSplitLeast)
+                                    : 1;
   const int cg = tn == 256 && p.M > 128 && wsplit == 1 ? 2 : 1;
   p.n_mt = (p.M + 128 * cg - 1) / (128 * cg);
   p.n_nt = (p.Ncol + tn - 1) / tn;
