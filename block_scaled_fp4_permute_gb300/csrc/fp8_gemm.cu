@@ -7,17 +7,15 @@
 // goes to its own TMEM accumulator, and the epilogue warps add it, times its
 // scales, to fp32 sums that they keep in registers over the whole of K.
 //
-// 256 tokens per tile are 128 sums per promoting thread, more than an even
-// split of the registers over twelve warps leaves room for: warps 0..3 hand
-// back to 56 each and the promoting warps take 224 (56 * 128 + 224 * 256 =
-// 168 * 384, the launch's own total).
-//
-// Weights on the MMA's M side (128 rows per CTA: one weight scale per block
-// and CTA), tokens on its N side: a token's scale is a column's factor.  Per
-// CTA: warp 0 copies stages of one block (128 elements = one 128-byte
-// swizzled row), warp 1 issues the four MMAs of a block, warps 4..11 promote:
-// each owns 32 lanes and half of the columns.  The factors sx * sw of four
-// blocks at a time are staged in shared memory, one group ahead.
+// Two kernels.  f8_kernel, for groups of few rows and launches of few tiles:
+// weights on the MMA's M side (128 rows per CTA, one weight scale per block),
+// 32 or 64 tokens on its N side, a token's scale being a column's factor.  It
+// streams the weights (112 experts of 6144 x 3584, 128 rows: 0.25 to 0.26 ms,
+// 6.4 TB/s).  Per CTA: warp 0 copies stages of one block (128 elements = one
+// 128-byte swizzled row), warp 1 issues the four MMAs of a block, warps 4..11
+// promote: each owns 32 lanes and half of the columns.  The factors sx * sw of
+// four blocks at a time are staged in shared memory, one group ahead.
+// f8w_kernel, for the rest, is described below.
 #include "../../include/situ_moe.h"
 #include "gemm_groups.cuh"
 
@@ -51,12 +49,11 @@ struct F8Params {
   int* err;
 };
 
-template <int CG, int TN>
+template <int TN>
 struct Cfg {
-  static constexpr int kTNB = TN / CG;
-  static constexpr int kBBytes = kTNB * 128;
+  static constexpr int kBBytes = TN * 128;
   static constexpr int kStageBytes = kABytes + kBBytes;
-  static constexpr int kBufs = TN >= 256 ? 2 : 4;              // TMEM accumulators
+  static constexpr int kBufs = 4;                              // TMEM accumulators
   static constexpr int kSPitch = TN + 8;                       // staged factors, conflict-free rows
   static constexpr int kSBytes = 2 * kSG * kSPitch * 4;
   static constexpr int kOutBytes = 8 * kBoxBytes;              // output staging
@@ -79,7 +76,7 @@ struct Cfg {
 struct Tile {
   int e, row0, mt, c0, cols;
 };
-template <int CG, int TN>
+template <int TN>
 __device__ __forceinline__ Tile tile_of(const F8Params& p, const int* tp, int idx) {
   Tile t;
   t.e = find_group(tp, p.E, idx / p.n_mt);
@@ -119,14 +116,13 @@ __device__ __forceinline__ void zero_rest(const F8Params& p, int et, int per_cta
   zero_rows(out, last.x + last.y, p.S, (size_t)p.N * el, (size_t)p.ld_out * el, t, n);
 }
 
-template <int CG, int TN, bool SPLIT>
+template <int TN, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
 f8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB, const F8Params p) {
-  using C = Cfg<CG, TN>;
+  using C = Cfg<TN>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t rank = CG == 2 ? cluster_rank() : 0;
   const int part = SPLIT ? (int)cluster_rank() : 0, parts = SPLIT ? (int)cluster_size() : 1;
   // a split tile's CTAs take neighbouring ranges of its blocks
   const int kb0 = p.nkb * part / parts, kb1 = p.nkb * (part + 1) / parts;
@@ -150,22 +146,21 @@ f8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
     }
     for (int b = 0; b < C::kBufs; ++b) {
       mbar_init(acc_full(b), 1);
-      mbar_init(acc_empty(b), 8 * CG);
+      mbar_init(acc_empty(b), 8);
     }
     mbar_init(drain, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 1) tmem_alloc<CG>(saddr(tm_holder), C::kTmemCols);
+  if (warp == 1) tmem_alloc<1>(saddr(tm_holder), C::kTmemCols);
   scan_tiles(p.offsets, p.E, p.S, TN, tp, kThreads);
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
-  if (CG == 2) cluster_sync();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = *tm_holder;
 
   int total = tp[p.E] * p.n_mt;
   if (failed != 0) total = 0;
-  const int first = blockIdx.x / (CG * parts), stride = gridDim.x / (CG * parts);
+  const int first = blockIdx.x / parts, stride = gridDim.x / parts;
 
   if (warp < kEpiWarp) {
       if (warp == 0) {
@@ -174,9 +169,8 @@ f8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
       Ring<C::kStages> r;
       bool ok = true;
       for (int idx = first; idx < total && ok; idx += stride) {
-        const Tile t = tile_of<CG, TN>(p, tp, idx);
-        const int half = (t.cols + 16 * CG - 1) / (16 * CG) * 16;
-        const int m0 = (t.mt * CG + (int)rank) * 128, row = t.row0 + t.c0 + half * (int)rank;
+        const Tile t = tile_of<TN>(p, tp, idx);
+        const int m0 = t.mt * 128, row = t.row0 + t.c0;
         for (int kb = kb0; kb < kb1; ++kb, r.next()) {
           const int s = r.s;
           if (r.used == C::kStages && !warp_wait(empty(s), r.ph ^ 1, p.err, 81)) {
@@ -184,32 +178,28 @@ f8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
             break;
           }
           if (leader) {
-            if (CG == 1 || rank == 0) mbar_expect_tx(full(s), CG * C::kStageBytes);
-            copy_3d<CG>(sbase + s * kABytes, &mapA, kb * 128, m0, t.e, full(s));
-            copy_2d<CG>(sbase + C::kOffB + s * C::kBBytes, &mapB, kb * 128, row, full(s));
+            mbar_expect_tx(full(s), C::kStageBytes);
+            copy_3d<1>(sbase + s * kABytes, &mapA, kb * 128, m0, t.e, full(s));
+            copy_2d<1>(sbase + C::kOffB + s * C::kBBytes, &mapB, kb * 128, row, full(s));
           }
           __syncwarp();
         }
       }
       if (ok) {   // the last arrivals on this CTA's barriers, before it may leave
         for (int j = 0; j < r.used; ++j) warp_wait(empty(j), j < r.s ? r.ph : r.ph ^ 1, p.err, 82);
-      } else if (rank == 0) {   // copies in flight
+      } else {   // copies in flight
         for (int j = 0; j < r.used; ++j) drain_wait(full(j), j < r.s ? r.ph : r.ph ^ 1);
-      } else {
-        const unsigned long long t0 = globaltimer();   // they complete on the other CTA's barriers
-        while (globaltimer() - t0 < 2000000ull) {
-        }
       }
-    } else if (warp == 1 && rank == 0) {
+    } else if (warp == 1) {
       // ---------------- MMAs ----------------
       const bool leader = elect_one();
       Ring<C::kStages> r;
       Ring<C::kBufs> ab;
       bool ok = true;
-      const uint32_t id0 = (1u << 4) | ((uint32_t)(128 * CG >> 4) << 24);   // E4M3 x E4M3 -> fp32, K-major
+      const uint32_t id0 = (1u << 4) | ((uint32_t)(128 >> 4) << 24);   // E4M3 x E4M3 -> fp32, K-major
       for (int idx = first; idx < total && ok; idx += stride) {
-        const Tile t = tile_of<CG, TN>(p, tp, idx);
-        const int nact = (t.cols + 16 * CG - 1) / (16 * CG) * (16 * CG);
+        const Tile t = tile_of<TN>(p, tp, idx);
+        const int nact = (t.cols + 15) / 16 * 16;
         const uint32_t idesc = id0 | ((uint32_t)(nact >> 3) << 17);
         for (int kb = kb0; kb < kb1; ++kb, r.next(), ab.next()) {
           const int s = r.s, buf = ab.s;
@@ -223,15 +213,15 @@ f8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
             const uint64_t ad = sdesc(sbase + s * kABytes), bd = sdesc(sbase + C::kOffB + s * C::kBBytes);
             // 32 bytes along the rows each; past K the stage holds zeros
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mma_f8<CG>(tmem + buf * TN, ad + 2 * k, bd + 2 * k, idesc, k != 0);
-            commit<CG>(empty(s));
-            commit<CG>(acc_full(buf));
+            for (int k = 0; k < 4; ++k) mma_f8<1>(tmem + buf * TN, ad + 2 * k, bd + 2 * k, idesc, k != 0);
+            commit<1>(empty(s));
+            commit<1>(acc_full(buf));
           }
           __syncwarp();
         }
       }
       if (!ok) {   // MMAs in flight
-        if (leader) commit<CG>(drain);
+        if (leader) commit<1>(drain);
         __syncwarp();
         drain_wait(drain, 0);
       }
@@ -245,10 +235,9 @@ f8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
     Ring<C::kBufs> ab;
     bool ok = true, left = false;
     for (int idx = first; idx < total; idx += stride) {
-      const Tile t = tile_of<CG, TN>(p, tp, idx);
-      const int mtile = t.mt * CG + (int)rank;   // past N's last block in a pair's second CTA: no factors, no rows
+      const Tile t = tile_of<TN>(p, tp, idx);
       const float* xs = p.xs + (size_t)(t.row0 + t.c0) * p.nkb;
-      const float* ws = p.ws + ((size_t)t.e * p.nrb + min(mtile, p.nrb - 1)) * p.nkb;
+      const float* ws = p.ws + ((size_t)t.e * p.nrb + t.mt) * p.nkb;
       float f[kPer], fw;
       auto fetch = [&](int g) {   // the factors of blocks [kSG * g, ...)
         const int kb = kb0 + kSG * g + j;
@@ -306,10 +295,7 @@ f8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
             ld(i + 1);
           } else {   // read: the accumulator may be written again
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-            if (lane == 0) {
-              if (CG == 1) mbar_arrive(acc_empty(buf));
-              else mbar_arrive_at(acc_empty(buf), 0);
-            }
+            mbar_arrive_if(acc_empty(buf), lane == 0);
           }
 #pragma unroll
           for (int c = 0; c < C::kCh / 4; ++c) {
@@ -346,7 +332,7 @@ f8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
         uint8_t* box = smem + C::kOffOut + (warp - kEpiWarp) * kBoxBytes;
         const int el = p.out_f32 ? 4 : 2, pitch = p.out_f32 ? kOutPitchF : kOutPitch;
         const int cpr = 2 * el, chunk = lane & (cpr - 1);   // 16-byte chunks of a row
-        const int nn = mtile * 128 + 32 * q + chunk * (16 / el);
+        const int nn = t.mt * 128 + 32 * q + chunk * (16 / el);
 #pragma unroll
         for (int i = 0; i < C::kNch; ++i) {
 #pragma unroll
@@ -381,11 +367,10 @@ f8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
-  if (CG == 2) cluster_sync();   // no CTA leaves while the other may still signal it
   if (SPLIT) {
     cluster_sync();              // every part is there
     if (first < total && *reinterpret_cast<volatile int*>(p.err) == 0) {
-      const Tile t = tile_of<CG, TN>(p, tp, first);
+      const Tile t = tile_of<TN>(p, tp, first);
       join_parts(sbase, 128, t.cols, tid, kThreads, [&](int col, int m, float2 v) {
         if (t.mt * 128 + m >= p.N) return;   // N is even
         const size_t at = (size_t)(t.row0 + t.c0 + col) * (size_t)p.ld_out + t.mt * 128 + m;
@@ -398,12 +383,28 @@ f8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
   if (warp == 1) {
     __syncwarp();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-    tmem_free<CG>(tmem, C::kTmemCols);
+    tmem_free<1>(tmem, C::kTmemCols);
   }
 }
 
 // ---------------------------------------------------------------------------
-// Wide tiles: tokens on the MMA's M side
+// Wide tiles: tokens on the MMA's M side (128 per CTA), 256 weight rows on its
+// N side.  A lane is a token, so a block's factor is one register and the
+// additions need nothing from shared memory (with tokens along the columns the
+// factors were a broadcast load per column, more shared-memory wavefronts than
+// the MMA and the copies together: 8,192 x 6144 x 3584 0.33 ms, now 0.148).
+//
+// A tile is two halves of 128 weight rows, that is of one weight block each,
+// with an MMA issuer and a promoting warpgroup per half and two accumulators
+// each in TMEM: warp 0 copies, warps 1 and 2 issue, warp 3 copies scales ahead,
+// warps 4..11 promote (32 lanes x 128 columns, 128 sums a thread).  That is
+// more registers than an even split leaves: warps 0..3 hand back to 40 each,
+// the promoting warps take 232 (40 * 128 + 232 * 256 = 168 * 384, the
+// launch's own total).  No spills: a spilled value in these loops comes back
+// through an L1 that the scales and results thrash, and cost 40 %.
+//
+// Bound by the promotion: 102 us of that case without its additions and
+// stores, 28 more for the additions, 16 for the stores.
 // ---------------------------------------------------------------------------
 
 constexpr int kWideN = 256;
@@ -770,16 +771,15 @@ f8w_kernel(const __grid_constant__ CUtensorMap mapX, const __grid_constant__ CUt
 }
 
 // split: CTAs per tile (SPLIT), with one tile per cluster
-template <int CG, int TN, bool SPLIT>
+template <int TN, bool SPLIT>
 cudaError_t launch_t(const CUtensorMap& a, const CUtensorMap& b, const F8Params& p, long max_items, cudaStream_t st,
                      int split = 1) {
   static std::atomic<uint64_t> raised{0};
   const long sms = sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
-  const int cluster = SPLIT ? split : CG;
-  const long tiles = SPLIT || max_items < sms / CG ? max_items : sms / CG;
-  return launch_cluster(f8_kernel<CG, TN, SPLIT>, &raised, cluster, (int)(tiles < 1 ? 1 : tiles) * cluster, kThreads,
-                        Cfg<CG, TN>::kSmem, st, a, b, p);
+  const long tiles = SPLIT || max_items < sms ? max_items : sms;
+  return launch_cluster(f8_kernel<TN, SPLIT>, &raised, split, (int)(tiles < 1 ? 1 : tiles) * split, kThreads,
+                        Cfg<TN>::kSmem, st, a, b, p);
 }
 
 template <int CG>
@@ -860,13 +860,13 @@ extern "C" situ_status situ_moe_fp8_gemm(const situ_fp8_gemm_args* g, void* stre
   cudaStream_t st = (cudaStream_t)stream;
   const double most = most_tiles(g->S, g->E, tm) * p.n_mt;
   const long cap = most > 1e6 ? 1000000 : (long)most;
-  const int split = tn < 256 ? split_of(f8_kernel<1, 32, true>, kThreads, Cfg<1, 32>::kSmem, most, p.nkb, kSplitLeast) : 1;
+  const int split = tn < 256 ? split_of(f8_kernel<32, true>, kThreads, Cfg<32>::kSmem, most, p.nkb, kSplitLeast) : 1;
   cudaError_t e;
   if (split > 1)
-    e = tn == 32 ? launch_t<1, 32, true>(mw, mx, p, cap, st, split) : launch_t<1, 64, true>(mw, mx, p, cap, st, split);
+    e = tn == 32 ? launch_t<32, true>(mw, mx, p, cap, st, split) : launch_t<64, true>(mw, mx, p, cap, st, split);
   else
-    e = tn == 32   ? launch_t<1, 32, false>(mw, mx, p, cap, st)
-        : tn == 64 ? launch_t<1, 64, false>(mw, mx, p, cap, st)
+    e = tn == 32   ? launch_t<32, false>(mw, mx, p, cap, st)
+        : tn == 64 ? launch_t<64, false>(mw, mx, p, cap, st)
         : cg == 1  ? launch_wide<1>(mx, mw, p, cap, st)
                    : launch_wide<2>(mx, mw, p, cap, st);
   return e == cudaSuccess ? SITU_OK : SITU_ERR_CUDA;

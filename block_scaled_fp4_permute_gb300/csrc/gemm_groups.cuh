@@ -83,19 +83,11 @@ __device__ __forceinline__ void cluster_sync() {
 }
 // the shared::cluster address of `a` in the pair's even CTA
 __device__ __forceinline__ uint32_t leader_addr(uint32_t a) { return a & 0xFEFFFFFFu; }
-// One arrival on a barrier of CTA `rank` of the cluster.  It orders tensor
-// memory reads (with the tcgen05 fences around it) and nothing in global
-// memory: with release at cluster scope it would wait for the thread's
+// One arrival where p holds, as a predicated instruction without a branch: on
+// a barrier of this CTA, or of CTA `rank` of the cluster.  The latter orders
+// tensor memory reads (with the tcgen05 fences around it) and nothing in
+// global memory: with release at cluster scope it would wait for the thread's
 // output stores, about 1 us each time.
-__device__ __forceinline__ void mbar_arrive_at(uint32_t a, uint32_t rank) {
-  asm volatile(
-      "{\n .reg .b32 r;\n mapa.shared::cluster.u32 r, %0, %1;\n"
-      " mbarrier.arrive.shared::cluster.b64 _, [r];\n}" ::"r"(a),
-      "r"(rank)
-      : "memory");
-}
-
-// the same as predicated instructions, without a branch
 __device__ __forceinline__ void mbar_arrive_if(uint32_t a, bool p) {
   asm volatile("{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n @q mbarrier.arrive.shared::cta.b64 _, [%0];\n}" ::"r"(a),
                "r"((uint32_t)p)
