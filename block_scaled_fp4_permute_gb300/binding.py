@@ -517,7 +517,9 @@ def situ_moe_grouped_gemm(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tenso
     """y[r] = x[r] @ w[e].T for the rows r of each expert e: x [S, K] sorted by
     expert, w [E, N, K] of the same 16-bit type, offsets int32 [E + 1] (as
     situ_moe_permute returns them).  Rows of no expert give zeros, or are left
-    unwritten with ``zero_rest=False``."""
+    unwritten with ``zero_rest=False``.  Rows may be strided; a layout that the
+    kernels cannot read in place (weights that are not contiguous, columns
+    apart, rows off 16 bytes) is copied first, in each of these calls."""
     w = _experts(w, offsets)
     _, N, K = w.shape
     if x.dim() != 2 or x.shape[1] != K:
@@ -554,6 +556,7 @@ class _GroupedLinear(torch.autograd.Function):
         return situ_moe_grouped_gemm(x, w, offsets)
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
         x, w, offsets = ctx.saved_tensors
         dx = situ_moe_grouped_gemm_dgrad(dy, w, offsets) if ctx.needs_input_grad[0] else None

@@ -369,9 +369,9 @@ f8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
   __syncthreads();
   if (SPLIT) {
     cluster_sync();              // every part is there
-    if (first < total && *reinterpret_cast<volatile int*>(p.err) == 0) {
+    if (warp >= kEpiWarp && first < total && *reinterpret_cast<volatile int*>(p.err) == 0) {
       const Tile t = tile_of<TN>(p, tp, first);
-      join_parts(sbase, 128, t.cols, tid, kThreads, [&](int col, int m, float2 v) {
+      join_parts(sbase, 128, t.cols, tid - 32 * kEpiWarp, kEpiThreads, [&](int col, int m, float2 v) {
         if (t.mt * 128 + m >= p.N) return;   // N is even
         const size_t at = (size_t)(t.row0 + t.c0 + col) * (size_t)p.ld_out + t.mt * 128 + m;
         if (p.out_f32) *reinterpret_cast<float2*>(reinterpret_cast<float*>(p.out) + at) = v;

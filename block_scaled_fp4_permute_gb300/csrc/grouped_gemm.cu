@@ -173,7 +173,7 @@ __device__ __forceinline__ void add_dw(const GgParams& p, size_t at, const float
 // k per thread, over the parts that had stages.
 __device__ __forceinline__ void join_dw(const GgParams& p, const Tile& t, uint32_t part_at, int part, int parts, int tid) {
   const int quads = (t.cols + 3) / 4, rows = min(128, p.M - t.m0);   // columns come in eights
-  for (int i = part * kThreads + tid; i < rows * quads; i += parts * kThreads) {
+  for (int i = part * kEpiThreads + tid; i < rows * quads; i += parts * kEpiThreads) {
     const int n = i / quads, c = 4 * (i - n * quads);
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int r = 0; r < parts; ++r) {
@@ -616,10 +616,11 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
   if (CG == 2) cluster_sync();   // no CTA leaves while the other may still signal it
   if (SPLIT) {
     cluster_sync();              // every part is there
-    if (first < total && *reinterpret_cast<volatile int*>(p.err) == 0) {
+    // by the epilogue warps: the others may have handed registers back
+    if (warp >= kEpiWarp && first < total && *reinterpret_cast<volatile int*>(p.err) == 0) {
       const Tile t = tile_of<CG, MODE, TN>(p, tp, first);
-      if (MODE == kWgrad) join_dw(p, t, sbase, part, parts, tid);
-      else join_parts(sbase, kJoinPitch, t.cols, tid, kThreads, [&](int col, int m, float2 v) {
+      if (MODE == kWgrad) join_dw(p, t, sbase, part, parts, tid - 32 * kEpiWarp);
+      else join_parts(sbase, kJoinPitch, t.cols, tid - 32 * kEpiWarp, kEpiThreads, [&](int col, int m, float2 v) {
         if (t.m0 + m >= p.M) return;   // M is even
         const size_t at = (size_t)(t.row0 + t.c0 + col) * (size_t)p.ld_out + t.m0 + m;
         if (p.out_f32) *reinterpret_cast<float2*>(reinterpret_cast<float*>(p.out) + at) = v;

@@ -357,6 +357,21 @@ def test_grouped_linear_gradients():
     assert (x.grad[-6:] == 0).all() and (w.grad[1] == 0).all()
 
 
+def test_grouped_linear_takes_expanded_gradients_and_frozen_operands():
+    counts, N, K = [10, 0, 22], 24, 32
+    g = gen(23)
+    off = offsets_of(counts)
+    x, w = normal(g, 32, K), normal(g, 3, N, K, std=0.1).requires_grad_()
+    B.grouped_linear(x, w, off).float().sum().backward()          # a broadcast gradient, x frozen
+    ones = torch.ones(32, N, dtype=torch.bfloat16, device="cuda")
+    assert_sum(w.grad, *reference("wgrad", ones, x, counts, 0, 32, N, K), 32, torch.bfloat16)
+    assert x.grad is None
+    x.requires_grad_()
+    y = B.grouped_linear(x, w.detach(), off)
+    y.backward(ones[:1].expand(32, N))
+    assert_sum(x.grad, *reference("dgrad", ones, w.detach(), counts, 0, 32, N, K), N, torch.bfloat16)
+
+
 def test_gradients_against_differences():
     # the product is linear in x and in w, so a central difference is exact up
     # to the sums' own error: with h = 1/4 and values on a grid of 1/8, x +- h d
