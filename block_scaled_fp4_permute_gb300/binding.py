@@ -393,24 +393,24 @@ def situ_moe_gemm_status(device=None, reset: bool = False) -> int:
 
 
 # The short calls (a decode step's) take the GPU less time than their
-# marshalling takes the host, so the two helpers below use the direct forms of
-# torch.cuda.current_stream (0.1 for 2.9 us here) and, where this torch has
-# it, of torch.empty (0.9 for 2.3 us).
+# marshalling takes the host, so what every call passes through is kept short:
+# the direct forms of torch.cuda.current_stream (0.1 for 2.9 us here) and,
+# where this torch has it, of torch.empty (0.9 for 2.3 us), and no helper calls
+# for operands that need none.
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
 _empty_cuda = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None)
 
 
-def _empty(shape, dtype, dev: torch.device) -> torch.Tensor:
-    if _empty_cuda is not None and _current_device() == dev.index:
-        n = len(shape)
-        return _empty_cuda(shape, (shape[1], 1) if n == 2 else (shape[1] * shape[2], shape[2], 1), dtype)
-    return torch.empty(shape, dtype=dtype, device=dev)
+def _empty(shape, strides, dtype, index: int) -> torch.Tensor:
+    """An uninitialised packed tensor on GPU ``index``."""
+    if _empty_cuda is not None and _current_device() == index:
+        return _empty_cuda(shape, strides, dtype)
+    return torch.empty(shape, dtype=dtype, device=f"cuda:{index}")
 
 
-def _enqueue(name: str, dev: torch.device, *args) -> None:
-    """Calls the C entry point ``name`` on ``dev`` and its current stream."""
-    index = dev.index
+def _enqueue(name: str, index: int, *args) -> None:
+    """Calls the C entry point ``name`` on GPU ``index`` and its current stream."""
     fn = getattr(_lib or lib(), name)
     if _current_device() == index:
         status = fn(*args, _raw_stream(index))
@@ -421,13 +421,13 @@ def _enqueue(name: str, dev: torch.device, *args) -> None:
         _check(name, status)
 
 
-def _on_stream(stream, dev: torch.device, f, *args, **kw):
-    """f(*args, **kw) with ``stream`` current: what it allocates and copies
+def _on_stream(stream, f, x: torch.Tensor, *args, **kw):
+    """f(x, *args, **kw) with ``stream`` current: what it allocates and copies
     belongs to that stream too."""
-    if stream.device != dev:
-        raise ValueError(f"a stream of {stream.device} for operands on {dev}")
+    if stream.device != x.device:
+        raise ValueError(f"a stream of {stream.device} for operands on {x.device}")
     with torch.cuda.stream(stream):
-        return f(*args, **kw)
+        return f(x, *args, **kw)
 
 
 def _rows(t: torch.Tensor, unit: int):
@@ -435,118 +435,124 @@ def _rows(t: torch.Tensor, unit: int):
     the kernels can read it in place (columns packed, rows a multiple of
     ``unit`` elements apart, 16-byte aligned), else a copy."""
     R, C = t.shape
-    s0, s1 = t.stride()
     p = t.data_ptr()
-    if s1 == 1 and p & 15 == 0:
-        if R <= 1:
+    if not p & 15:
+        if t.is_contiguous():
             return t, p, C
-        if s0 >= C and s0 % unit == 0:
+        s0, s1 = t.stride()
+        if s1 == 1 and s0 >= C and s0 % unit == 0:
             return t, p, s0
     t = t.clone(memory_format=torch.contiguous_format)
     return t, t.data_ptr(), C
 
 
-def _packed(t: torch.Tensor) -> torch.Tensor:
-    """``t`` contiguous and 16-byte aligned."""
-    t = t.contiguous()
-    return t.clone() if t.data_ptr() & 15 else t
+def _packed(t: torch.Tensor):
+    """(tensor, pointer) of ``t`` contiguous and 16-byte aligned: itself or a copy."""
+    p = t.data_ptr()
+    if not t.is_contiguous() or p & 15:
+        t = t.clone(memory_format=torch.contiguous_format)
+        p = t.data_ptr()
+    return t, p
 
 
-def _result(out, shape, dtype, dev, unit: int):
-    """(tensor to write, elements between rows): a new one, or ``out`` after
-    its checks."""
-    if out is None:
-        return _empty(shape, dtype, dev), shape[-1]
-    if tuple(out.shape) != shape or out.dtype != dtype or out.device != dev:
-        raise ValueError(f"out: needs {dtype} {shape} on {dev}")
-    if out.data_ptr() & 15 == 0:
+def _given(out: torch.Tensor, shape, dtype, index: int, unit: int) -> int:
+    """The elements between the rows of a caller's ``out``, after its checks."""
+    if tuple(out.shape) != shape or out.dtype is not dtype or out.get_device() != index:
+        raise ValueError(f"out: needs {dtype} {shape} on cuda:{index}")
+    if not out.data_ptr() & 15:
         if out.is_contiguous():
-            return out, shape[-1]
+            return shape[-1]
         if len(shape) == 2 and out.stride(1) == 1 and out.stride(0) >= shape[1] and out.stride(0) % unit == 0:
-            return out, out.stride(0)
+            return out.stride(0)
     raise ValueError("out: needs 16-byte aligned rows, packed along the last dimension")
 
 
-def _groups(offsets: torch.Tensor, dev) -> torch.Tensor:
-    if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.shape[0] < 2:
+def _groups(offsets: torch.Tensor, index: int) -> int:
+    """The number of groups that ``offsets`` bounds."""
+    if offsets.dtype is not torch.int32 or offsets.dim() != 1 or offsets.shape[0] < 2:
         raise TypeError("offsets must be int32 [E + 1]")
-    if offsets.device != dev:
-        raise ValueError(f"operands on {offsets.device} and {dev}")
-    return offsets.contiguous()
+    if offsets.get_device() != index:
+        raise ValueError(f"offsets on {offsets.device}, the operands on cuda:{index}")
+    return offsets.shape[0] - 1
 
 
-def _grouped(direction, a, b, offsets, N, K, out, out_shape, out_dtype, accumulate, zero_rest, stream):
-    dev, dtype = a.device, a.dtype
-    if stream is not None:
-        return _on_stream(stream, dev, _grouped, direction, a, b, offsets, N, K, out, out_shape, out_dtype, accumulate,
-                          zero_rest, None)
-    if dev.type != "cuda" or b.device != dev:
-        raise ValueError(f"the operands must be on one CUDA device, not on {dev} and {b.device}")
+def _grouped(a, direction, b, offsets, S, E, N, K, out, shape, strides, out_dtype, accumulate, zero_rest):
+    index, dtype = a.get_device(), a.dtype
+    if index < 0 or b.get_device() != index:
+        raise ValueError(f"the operands must be on one CUDA device, not on {a.device} and {b.device}")
     if dtype is not torch.bfloat16 and dtype is not torch.float16 or b.dtype is not dtype:
         raise TypeError("the operands must be both bf16 or both f16")
     if out_dtype is None:
         out_dtype = out.dtype if out is not None else dtype
     if out_dtype is not dtype and out_dtype is not torch.float32:
         raise TypeError("the output must be of the operands' type or fp32")
-    offsets = _groups(offsets, dev)
-    out, ldo = _result(out, out_shape, out_dtype, dev, 8)
+    if _groups(offsets, index) != E:
+        raise ValueError("weights must be [E, N, K] with offsets [E + 1]")
+    if out is None:
+        out, ldo = _empty(shape, strides, out_dtype, index), shape[-1]
+    else:
+        ldo = _given(out, shape, out_dtype, index, 8)
+    if not offsets.is_contiguous():
+        offsets = offsets.contiguous()
     a, pa, lda = _rows(a, 8)
     if direction == SITU_GROUPED_WGRAD:
         b, pb, ldb = _rows(b, 8)
     else:
-        b = _packed(b)
-        pb, ldb = b.data_ptr(), 0
-    args = SituGroupedGemmArgs(direction, _DTYPES[dtype], _DTYPES[out_dtype], a.shape[0], N, K, offsets.shape[0] - 1,
-                               1 if accumulate else 0, 0 if zero_rest else 1, pa, lda, pb, ldb, offsets.data_ptr(),
-                               out.data_ptr(), ldo, _status_word(dev.index).data_ptr())
-    _enqueue("situ_moe_grouped_gemm", dev, ctypes.byref(args))
+        b, pb = _packed(b)
+        ldb = 0
+    args = SituGroupedGemmArgs(direction, _DTYPES[dtype], _DTYPES[out_dtype], S, N, K, E, accumulate, not zero_rest,
+                               pa, lda, pb, ldb, offsets.data_ptr(), out.data_ptr(), ldo, _status_word(index).data_ptr())
+    _enqueue("situ_moe_grouped_gemm", index, ctypes.byref(args))
     return out
-
-
-def _experts(w: torch.Tensor, offsets: torch.Tensor):
-    """w [E, N, K] (or one expert's [N, K]) against its offsets."""
-    if w.dim() == 2:
-        w = w.unsqueeze(0)
-    if w.dim() != 3 or w.shape[0] != offsets.shape[0] - 1:
-        raise ValueError("weights must be [E, N, K] with offsets [E + 1]")
-    return w
 
 
 def situ_moe_grouped_gemm(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, *, out=None, out_dtype=None,
                           zero_rest: bool = True, stream=None) -> torch.Tensor:
     """y[r] = x[r] @ w[e].T for the rows r of each expert e: x [S, K] sorted by
-    expert, w [E, N, K] of the same 16-bit type, offsets int32 [E + 1] (as
-    situ_moe_permute returns them).  Rows of no expert give zeros, or are left
-    unwritten with ``zero_rest=False``.  Rows may be strided; a layout that the
-    kernels cannot read in place (weights that are not contiguous, columns
-    apart, rows off 16 bytes) is copied first, in each of these calls."""
-    w = _experts(w, offsets)
-    _, N, K = w.shape
-    if x.dim() != 2 or x.shape[1] != K:
+    expert, w [E, N, K] of the same 16-bit type (or one expert's [N, K]),
+    offsets int32 [E + 1] (as situ_moe_permute returns them).  Rows of no expert
+    give zeros, or are left unwritten with ``zero_rest=False``.  Rows may be
+    strided; a layout that the kernels cannot read in place (weights that are
+    not contiguous, columns apart, rows off 16 bytes) is copied first, in each
+    of these calls."""
+    if stream is not None:
+        return _on_stream(stream, situ_moe_grouped_gemm, x, w, offsets, out=out, out_dtype=out_dtype, zero_rest=zero_rest)
+    E, N, K = w.shape if w.dim() == 3 else (1, *w.shape)
+    S, Kx = x.shape
+    if Kx != K:
         raise ValueError("x must be [S, K]")
-    return _grouped(SITU_GROUPED_FORWARD, x, w, offsets, N, K, out, (x.shape[0], N), out_dtype, False, zero_rest, stream)
+    return _grouped(x, SITU_GROUPED_FORWARD, w, offsets, S, E, N, K, out, (S, N), (N, 1), out_dtype, False, zero_rest)
 
 
 def situ_moe_grouped_gemm_dgrad(dy: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, *, out=None,
                                 out_dtype=None, zero_rest: bool = True, stream=None) -> torch.Tensor:
     """The gradient of situ_moe_grouped_gemm's x: dx[r] = dy[r] @ w[e], [S, K]."""
-    w = _experts(w, offsets)
-    _, N, K = w.shape
-    if dy.dim() != 2 or dy.shape[1] != N:
+    if stream is not None:
+        return _on_stream(stream, situ_moe_grouped_gemm_dgrad, dy, w, offsets, out=out, out_dtype=out_dtype,
+                          zero_rest=zero_rest)
+    E, N, K = w.shape if w.dim() == 3 else (1, *w.shape)
+    S, Ny = dy.shape
+    if Ny != N:
         raise ValueError("dy must be [S, N]")
-    return _grouped(SITU_GROUPED_DGRAD, dy, w, offsets, N, K, out, (dy.shape[0], K), out_dtype, False, zero_rest, stream)
+    return _grouped(dy, SITU_GROUPED_DGRAD, w, offsets, S, E, N, K, out, (S, K), (K, 1), out_dtype, False, zero_rest)
 
 
 def situ_moe_grouped_gemm_wgrad(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor, *, out=None,
                                 out_dtype=None, accumulate: bool = False, stream=None) -> torch.Tensor:
     """The gradient of its w: dw[e] = dy[rows of e].T @ x[rows of e], [E, N, K];
     zeros for an expert without rows.  ``accumulate`` adds to ``out``."""
-    if dy.dim() != 2 or x.dim() != 2 or dy.shape[0] != x.shape[0]:
+    if stream is not None:
+        return _on_stream(stream, situ_moe_grouped_gemm_wgrad, dy, x, offsets, out=out, out_dtype=out_dtype,
+                          accumulate=accumulate)
+    S, N = dy.shape
+    Sx, K = x.shape
+    if S != Sx:
         raise ValueError("dy must be [S, N] and x [S, K]")
     if accumulate and out is None:
         raise ValueError("accumulate adds to out: none given")
-    return _grouped(SITU_GROUPED_WGRAD, dy, x, offsets, dy.shape[1], x.shape[1], out,
-                    (offsets.shape[0] - 1, dy.shape[1], x.shape[1]), out_dtype, accumulate, True, stream)
+    E = offsets.shape[0] - 1
+    return _grouped(dy, SITU_GROUPED_WGRAD, x, offsets, S, E, N, K, out, (E, N, K), (N * K, K, 1), out_dtype, accumulate,
+                    True)
 
 
 class _GroupedLinear(torch.autograd.Function):
@@ -576,43 +582,42 @@ def situ_moe_quant_fp8(x: torch.Tensor, block_rows: int = 1, *, out=None, stream
     """bf16, f16 or fp32 [R, K] or [E, R, K] -> (E4M3 uint8 of x's shape, fp32
     scales per block of 128): block_rows 1, a scale per row and 128 columns
     (activations); 128, one per 128 x 128 block (weights)."""
-    dev, dtype, dim = x.device, _DTYPES.get(x.dtype), x.dim()
     if stream is not None:
-        return _on_stream(stream, dev, situ_moe_quant_fp8, x, block_rows, out=out)
+        return _on_stream(stream, situ_moe_quant_fp8, x, block_rows, out=out)
+    index, dtype, dim = x.get_device(), _DTYPES.get(x.dtype), x.dim()
     if dtype is None:
         raise TypeError("x must be bf16, f16 or fp32")
-    if dev.type != "cuda":
+    if index < 0:
         raise ValueError("x must be a CUDA tensor")
     if block_rows != 1 and block_rows != 128:
         raise ValueError("block_rows must be 1 or 128")
     if dim == 2:
         E, (R, K) = 1, x.shape
+        nr, nk = -(-R // block_rows), -(-K // 128)
         x, px, ldx = _rows(x, 4 if dtype == SITU_DT_F32 else 8)
-        shape, dims = (R, K), (-(-R // block_rows), -(-K // 128))
+        shape, strides, dims, dstrides = (R, K), (K, 1), (nr, nk), (nk, 1)
     elif dim == 3:
         E, R, K = x.shape
-        x = _packed(x)
-        px, ldx = x.data_ptr(), K
-        shape, dims = (E, R, K), (E, -(-R // block_rows), -(-K // 128))
+        nr, nk = -(-R // block_rows), -(-K // 128)
+        x, px = _packed(x)
+        ldx = K
+        shape, strides, dims, dstrides = (E, R, K), (R * K, K, 1), (E, nr, nk), (nr * nk, nk, 1)
     else:
         raise ValueError("x must be [R, K] or [E, R, K]")
     if out is None:
-        q, scale = _empty(shape, torch.uint8, dev), _empty(dims, torch.float32, dev)
+        q, scale = _empty(shape, strides, torch.uint8, index), _empty(dims, dstrides, torch.float32, index)
     else:
         q, scale = out
         for t, want, dts, what in ((q, shape, _E4M3, "q"), (scale, dims, (torch.float32,), "scale")):
-            if tuple(t.shape) != want or t.dtype not in dts or t.device != dev or not t.is_contiguous():
-                raise ValueError(f"{what}: needs a contiguous {dts[0]} tensor {want} on {dev}")
-    _enqueue("situ_moe_quant_fp8", dev, px, dtype, E, R, K, ldx, block_rows, q.data_ptr(), scale.data_ptr())
+            if tuple(t.shape) != want or t.dtype not in dts or t.get_device() != index or not t.is_contiguous():
+                raise ValueError(f"{what}: needs a contiguous {dts[0]} tensor {want} on cuda:{index}")
+    _enqueue("situ_moe_quant_fp8", index, px, dtype, E, R, K, ldx, block_rows, q.data_ptr(), scale.data_ptr())
     return q, scale
 
 
-def _fp8_gemm(x_q, x_scale, w_q, w_scale, E, N, K, offsets, out, out_dtype, zero_rest, stream):
-    dev = x_q.device
-    if stream is not None:
-        return _on_stream(stream, dev, _fp8_gemm, x_q, x_scale, w_q, w_scale, E, N, K, offsets, out, out_dtype,
-                          zero_rest, None)
-    if dev.type != "cuda" or x_scale.device != dev or w_q.device != dev or w_scale.device != dev:
+def _fp8_gemm(x_q, x_scale, w_q, w_scale, E, N, K, offsets, out, out_dtype, zero_rest):
+    index = x_q.get_device()
+    if index < 0 or x_scale.get_device() != index or w_q.get_device() != index or w_scale.get_device() != index:
         raise ValueError("the operands must be on one CUDA device")
     if x_q.dtype not in _E4M3 or w_q.dtype not in _E4M3:
         raise TypeError("x_q and w_q must hold E4M3 codes (uint8 or float8_e4m3fn)")
@@ -622,18 +627,33 @@ def _fp8_gemm(x_q, x_scale, w_q, w_scale, E, N, K, offsets, out, out_dtype, zero
         out_dtype = out.dtype if out is not None else torch.bfloat16
     if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
         raise TypeError("the output must be bf16 or fp32")
-    if x_q.dim() != 2 or x_q.shape[1] != K:
-        raise ValueError("x_q must be [S, K]")
-    S, nkb, nrb = x_q.shape[0], -(-K // 128), -(-N // 128)
-    if x_scale.shape != (S, nkb) or w_scale.shape != ((nrb, nkb) if w_scale.dim() == 2 and E == 1 else (E, nrb, nkb)):
-        raise ValueError(f"needs x_scale {(S, nkb)} and w_scale {(E, nrb, nkb)}")
-    out, ldo = _result(out, (S, N), out_dtype, dev, 8)
+    S, Kx = x_q.shape
+    nkb, nrb = -(-K // 128), -(-N // 128)
+    if Kx != K or x_scale.shape != (S, nkb):
+        raise ValueError(f"needs x_q [S, {K}] and x_scale [S, {nkb}]")
+    if w_scale.shape != (E, nrb, nkb) and (E != 1 or w_scale.shape != (nrb, nkb)):
+        raise ValueError(f"needs w_scale {(E, nrb, nkb)}")
+    if offsets is None:
+        poff = None
+    else:
+        if _groups(offsets, index) != E:
+            raise ValueError("weights must be [E, N, K] with offsets [E + 1]")
+        if not offsets.is_contiguous():
+            offsets = offsets.contiguous()
+        poff = offsets.data_ptr()
+    if out is None:
+        out, ldo = _empty((S, N), (N, 1), out_dtype, index), N
+    else:
+        ldo = _given(out, (S, N), out_dtype, index, 8)
     x_q, px, ldx = _rows(x_q, 16)
-    w_q, x_scale, w_scale = _packed(w_q), x_scale.contiguous(), w_scale.contiguous()
-    args = SituFp8GemmArgs(_DTYPES[out_dtype], S, N, K, E, 0 if zero_rest else 1, px, ldx, x_scale.data_ptr(),
-                           w_q.data_ptr(), w_scale.data_ptr(), None if offsets is None else offsets.data_ptr(),
-                           out.data_ptr(), ldo, _status_word(dev.index).data_ptr())
-    _enqueue("situ_moe_fp8_gemm", dev, ctypes.byref(args))
+    w_q, pw = _packed(w_q)
+    if not x_scale.is_contiguous():
+        x_scale = x_scale.contiguous()
+    if not w_scale.is_contiguous():
+        w_scale = w_scale.contiguous()
+    args = SituFp8GemmArgs(_DTYPES[out_dtype], S, N, K, E, not zero_rest, px, ldx, x_scale.data_ptr(), pw,
+                           w_scale.data_ptr(), poff, out.data_ptr(), ldo, _status_word(index).data_ptr())
+    _enqueue("situ_moe_fp8_gemm", index, ctypes.byref(args))
     return out
 
 
@@ -642,21 +662,25 @@ def situ_moe_fp8_gemm(x_q: torch.Tensor, x_scale: torch.Tensor, w_q: torch.Tenso
     """x @ w.T of operands quantised by situ_moe_quant_fp8: x_q [S, K] with a
     scale per row and 128 columns, w_q [N, K] with one per 128 x 128 block;
     bf16 (default) or fp32 [S, N]."""
-    if w_q.dim() != 2 or w_scale.dim() != 2:
+    if stream is not None:
+        return _on_stream(stream, situ_moe_fp8_gemm, x_q, x_scale, w_q, w_scale, out=out, out_dtype=out_dtype)
+    if w_scale.dim() != 2:
         raise ValueError("w_q must be [N, K] and w_scale [ceil(N/128), ceil(K/128)]")
     N, K = w_q.shape
-    return _fp8_gemm(x_q, x_scale, w_q, w_scale, 1, N, K, None, out, out_dtype, True, stream)
+    return _fp8_gemm(x_q, x_scale, w_q, w_scale, 1, N, K, None, out, out_dtype, True)
 
 
 def situ_moe_fp8_grouped_gemm(x_q: torch.Tensor, x_scale: torch.Tensor, w_q: torch.Tensor, w_scale: torch.Tensor,
                               offsets: torch.Tensor, *, out=None, out_dtype=None, zero_rest: bool = True,
                               stream=None) -> torch.Tensor:
-    """The same per expert: rows of x_q sorted by expert, w_q [E, N, K],
-    offsets int32 [E + 1].  Rows of no expert give zeros, or are left
-    unwritten with ``zero_rest=False``."""
-    offsets = _groups(offsets, x_q.device)
-    w_q = _experts(w_q, offsets)
-    return _fp8_gemm(x_q, x_scale, w_q, w_scale, *w_q.shape, offsets, out, out_dtype, zero_rest, stream)
+    """The same per expert: rows of x_q sorted by expert, w_q [E, N, K] (or one
+    expert's [N, K]), offsets int32 [E + 1].  Rows of no expert give zeros, or
+    are left unwritten with ``zero_rest=False``."""
+    if stream is not None:
+        return _on_stream(stream, situ_moe_fp8_grouped_gemm, x_q, x_scale, w_q, w_scale, offsets, out=out,
+                          out_dtype=out_dtype, zero_rest=zero_rest)
+    E, N, K = w_q.shape if w_q.dim() == 3 else (1, *w_q.shape)
+    return _fp8_gemm(x_q, x_scale, w_q, w_scale, E, N, K, offsets, out, out_dtype, zero_rest)
 
 
 class Layer:
