@@ -10,11 +10,11 @@
 // Two kernels.  f8_kernel, for groups of few rows and launches of few tiles:
 // weights on the MMA's M side (128 rows per CTA, one weight scale per block),
 // 32 or 64 tokens on its N side, a token's scale being a column's factor.  It
-// streams the weights (112 experts of 6144 x 3584, 128 rows: 0.25 to 0.26 ms,
-// 6.4 TB/s).  Per CTA: warp 0 copies stages of one block (128 elements = one
+// streams the weights (112 experts of 6144 x 3584, 128 rows: 0.255 ms,
+// 6.6 TB/s).  Per CTA: warp 0 copies stages of one block (128 elements = one
 // 128-byte swizzled row), warp 1 issues the four MMAs of a block, warps 4..11
-// promote: each owns 32 lanes and half of the columns.  The factors sx * sw of
-// four blocks at a time are staged in shared memory, one group ahead.
+// promote: each owns 32 lanes and half of the columns.  Warps 2 and 3 copy
+// the scales, up to 16 blocks and the tile's end ahead.
 // f8w_kernel, for the rest, is described below.
 #include "../../include/situ_moe.h"
 #include "gemm_groups.cuh"
@@ -31,9 +31,9 @@ constexpr int kABytes = 128 * 128;
 constexpr int kThreads = 384;
 constexpr int kEpiWarp = 4;
 constexpr int kEpiThreads = 256;
-constexpr int kSG = 4;   // blocks per group of staged factors
+constexpr int kSG = 4;   // blocks per slot of scales
 constexpr int kOutPitch = 80, kOutPitchF = 144;   // bytes of a staged token row of 32 outputs, bf16 and fp32
-constexpr int kBoxBytes = 32 * kOutPitch;         // of a warp: 32 rows of bf16, 16 of fp32
+constexpr int kBoxBytes = 16 * kOutPitchF;        // of a warp: 16 rows
 constexpr int kSplitLeast = 2;   // blocks that a CTA of a split tile takes at least
 
 struct F8Params {
@@ -54,22 +54,26 @@ struct Cfg {
   static constexpr int kBBytes = TN * 128;
   static constexpr int kStageBytes = kABytes + kBBytes;
   static constexpr int kBufs = 4;                              // TMEM accumulators
-  static constexpr int kSPitch = TN + 8;                       // staged factors, conflict-free rows
-  static constexpr int kSBytes = 2 * kSG * kSPitch * 4;
+  static constexpr int kSlots = 4;                             // of scales: [block][token], then the weights'
+  static constexpr int kSPitch = TN + 8;                       // conflict-free rows
+  static constexpr int kSlotBytes = 4 * kSG * (kSPitch + 1);
   static constexpr int kOutBytes = 8 * kBoxBytes;              // output staging
-  static constexpr int kMaxBytes = 232448 - 1024 - 4 * (kMaxGroups + 1) - 512 - kSBytes - kOutBytes;
-  static constexpr int kStages = kMaxBytes / kStageBytes;
+  static constexpr int kMaxBytes = 232448 - 1024 - 4 * (kMaxGroups + 1) - 512 - kSlots * kSlotBytes - kOutBytes;
+  // 8 stages, 160 or 192 KB: all that fit at 32 tokens (10) made the HBM
+  // slower (112 experts of 6144 x 3584: 0.267 ms, 8: 0.255, 6: 0.257)
+  static constexpr int kStages = 8;
+  static_assert(kStages * kStageBytes <= kMaxBytes, "shared memory");
   static constexpr int kOffB = kStages * kABytes;
   static constexpr int kOffS = kOffB + kStages * kBBytes;
-  static constexpr int kOffOut = kOffS + kSBytes;
+  static constexpr int kOffOut = kOffS + kSlots * kSlotBytes;
   static constexpr int kOffTp = kOffOut + kOutBytes;
   static constexpr int kOffBar = (kOffTp + 4 * (kMaxGroups + 1) + 15) / 16 * 16;
-  static constexpr int kNumBars = 2 * kStages + 2 * kBufs + 1;
+  static constexpr int kNumBars = 2 * kStages + kBufs + 1 + 2 * kSlots;
   static constexpr int kOffTm = kOffBar + 8 * kNumBars;
   static constexpr int kSmem = kOffTm + 16 + 1024;
   static constexpr int kTmemCols = kBufs * TN;
-  static constexpr int kCh = TN >= 64 ? 32 : 16;               // columns per TMEM load
-  static constexpr int kNch = TN / (2 * kCh);                  // loads per promoting warp and block
+  static constexpr int kCh = TN / 2;                           // columns of a promoting warp: one TMEM load
+  static_assert(kCh == 16 || kCh == 32, "TMEM loads");
   static_assert(kSmem <= 232448 && kTmemCols <= 512, "shared memory and TMEM");
 };
 
@@ -91,6 +95,14 @@ __device__ __forceinline__ Tile tile_of(const F8Params& p, const int* tp, int id
 
 __device__ __forceinline__ void fma2(uint64_t& acc, uint64_t a, uint64_t b) {
   asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(a), "l"(b));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ void copy_f32(uint32_t dst, const float* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
   uint64_t d;
@@ -130,10 +142,11 @@ f8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
   int* tp = reinterpret_cast<int*>(smem + C::kOffTp);
   const uint32_t bar0 = sbase + C::kOffBar;
   auto full = [&](int s) { return bar0 + 8 * s; };
-  auto empty = [&](int s) { return bar0 + 8 * (C::kStages + s); };
-  auto acc_full = [&](int b) { return bar0 + 8 * (2 * C::kStages + b); };
-  auto acc_empty = [&](int b) { return bar0 + 8 * (2 * C::kStages + C::kBufs + b); };
-  const uint32_t drain = bar0 + 8 * (2 * C::kStages + 2 * C::kBufs);
+  auto done = [&](int s) { return bar0 + 8 * (C::kStages + s); };
+  auto acc_empty = [&](int b) { return bar0 + 8 * (2 * C::kStages + b); };
+  auto sc_full = [&](int i) { return bar0 + 8 * (2 * C::kStages + C::kBufs + i); };
+  auto sc_empty = [&](int i) { return bar0 + 8 * (2 * C::kStages + C::kBufs + C::kSlots + i); };
+  const uint32_t drain = bar0 + 8 * (2 * C::kStages + C::kBufs + 2 * C::kSlots);
   uint32_t* tm_holder = reinterpret_cast<uint32_t*>(smem + C::kOffTm);
 
   const int failed = *reinterpret_cast<volatile int*>(p.err);   // an earlier launch gave up a wait: no work then
@@ -142,11 +155,12 @@ f8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
     prefetch_map(&mapB);
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(full(s), 1);
-      mbar_init(empty(s), 1);
+      mbar_init(done(s), 1);
     }
-    for (int b = 0; b < C::kBufs; ++b) {
-      mbar_init(acc_full(b), 1);
-      mbar_init(acc_empty(b), 8);
+    for (int b = 0; b < C::kBufs; ++b) mbar_init(acc_empty(b), 8);
+    for (int i = 0; i < C::kSlots; ++i) {
+      mbar_init(sc_full(i), 64);
+      mbar_init(sc_empty(i), 8);
     }
     mbar_init(drain, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -163,7 +177,7 @@ f8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
   const int first = blockIdx.x / parts, stride = gridDim.x / parts;
 
   if (warp < kEpiWarp) {
-      if (warp == 0) {
+    if (warp == 0) {
       // ---------------- copies ----------------
       const bool leader = elect_one();
       Ring<C::kStages> r;
@@ -173,7 +187,7 @@ f8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
         const int m0 = t.mt * 128, row = t.row0 + t.c0;
         for (int kb = kb0; kb < kb1; ++kb, r.next()) {
           const int s = r.s;
-          if (r.used == C::kStages && !warp_wait(empty(s), r.ph ^ 1, p.err, 81)) {
+          if (r.used == C::kStages && !warp_wait(done(s), r.ph ^ 1, p.err, 81)) {
             ok = false;
             break;
           }
@@ -186,7 +200,7 @@ f8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
         }
       }
       if (ok) {   // the last arrivals on this CTA's barriers, before it may leave
-        for (int j = 0; j < r.used; ++j) warp_wait(empty(j), j < r.s ? r.ph : r.ph ^ 1, p.err, 82);
+        for (int j = 0; j < r.used; ++j) warp_wait(done(j), j < r.s ? r.ph : r.ph ^ 1, p.err, 82);
       } else {   // copies in flight
         for (int j = 0; j < r.used; ++j) drain_wait(full(j), j < r.s ? r.ph : r.ph ^ 1);
       }
@@ -203,8 +217,8 @@ f8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
         const uint32_t idesc = id0 | ((uint32_t)(nact >> 3) << 17);
         for (int kb = kb0; kb < kb1; ++kb, r.next(), ab.next()) {
           const int s = r.s, buf = ab.s;
-          if ((ab.used == C::kBufs && !warp_wait(acc_empty(buf), ab.ph ^ 1, p.err, 83)) ||
-              !warp_wait(full(s), r.ph, p.err, 84)) {
+          // the first blocks find their accumulators empty: any completed phase will do
+          if (!warp_wait2(acc_empty(buf), ab.ph ^ 1, full(s), r.ph, p.err, 83)) {
             ok = false;
             break;
           }
@@ -214,8 +228,7 @@ f8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
             // 32 bytes along the rows each; past K the stage holds zeros
 #pragma unroll
             for (int k = 0; k < 4; ++k) mma_f8<1>(tmem + buf * TN, ad + 2 * k, bd + 2 * k, idesc, k != 0);
-            commit<1>(empty(s));
-            commit<1>(acc_full(buf));
+            commit<1>(done(s));   // the stage is free, its product there
           }
           __syncwarp();
         }
@@ -225,108 +238,97 @@ f8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
         __syncwarp();
         drain_wait(drain, 0);
       }
+    } else {
+      // ---------------- scales ----------------
+      Ring<C::kSlots> sr;
+      bool ok = true;
+      const int st = tid - 64, j = st & (kSG - 1);   // this thread's block of a slot
+      for (int idx = first; idx < total && ok; idx += stride) {
+        const Tile t = tile_of<TN>(p, tp, idx);
+        const float* xs = p.xs + (size_t)(t.row0 + t.c0) * p.nkb;
+        const float* ws = p.ws + ((size_t)t.e * p.nrb + t.mt) * p.nkb;
+        for (int kb = kb0; kb < kb1; kb += kSG, sr.next()) {
+          if (sr.used == C::kSlots && !warp_wait(sc_empty(sr.s), sr.ph ^ 1, p.err, 87)) {
+            ok = false;
+            break;
+          }
+          const uint32_t slot = sbase + C::kOffS + sr.s * C::kSlotBytes;
+          const int b = min(kb + j, kb1 - 1);
+#pragma unroll
+          for (int i = 0; i < TN; i += 64 / kSG) {
+            const int r = i + st / kSG;
+            if (r < t.cols) copy_f32(slot + 4 * (j * C::kSPitch + r), xs + (size_t)r * p.nkb + b);
+          }
+          if (st < kSG) copy_f32(slot + 4 * (kSG * C::kSPitch + st), ws + b);
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(sc_full(sr.s)) : "memory");
+        }
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
     }
   } else {
     // ---------------- promotion and store ----------------
     const int q = warp & 3, h = (warp - kEpiWarp) >> 2, et = tid - 32 * kEpiWarp;
-    float* stage = reinterpret_cast<float*>(smem + C::kOffS);
-    constexpr int kPer = kSG * TN / kEpiThreads > 0 ? kSG * TN / kEpiThreads : 1;   // factors per thread and group
-    const int j = et & (kSG - 1);   // this thread's block within a group
+    Ring<C::kStages> r;
     Ring<C::kBufs> ab;
-    bool ok = true, left = false;
-    for (int idx = first; idx < total; idx += stride) {
+    Ring<C::kSlots> sr;
+    bool ok = true;
+    for (int idx = first; idx < total && ok; idx += stride) {
       const Tile t = tile_of<TN>(p, tp, idx);
-      const float* xs = p.xs + (size_t)(t.row0 + t.c0) * p.nkb;
-      const float* ws = p.ws + ((size_t)t.e * p.nrb + t.mt) * p.nkb;
-      float f[kPer], fw;
-      auto fetch = [&](int g) {   // the factors of blocks [kSG * g, ...)
-        const int kb = kb0 + kSG * g + j;
-        fw = kb < kb1 ? __ldg(ws + kb) : 0.f;
+      uint64_t acc[C::kCh / 2];
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          const int r = (et >> 2) + i * (kEpiThreads / kSG);
-          f[i] = (kb < kb1 && r < t.cols) ? __ldg(xs + (size_t)r * p.nkb + kb) : 0.f;
+      for (int c = 0; c < C::kCh / 2; ++c) acc[c] = 0ull;
+      for (int k0 = kb0; k0 < kb1 && ok; k0 += kSG, sr.next()) {
+        if (!warp_wait(sc_full(sr.s), sr.ph, p.err, 86)) {
+          ok = false;
+          break;
         }
-      };
-      auto put = [&](int g) {
+        const float* slot = reinterpret_cast<const float*>(smem + C::kOffS + sr.s * C::kSlotBytes);
+        const float4 fw = *reinterpret_cast<const float4*>(slot + kSG * C::kSPitch);
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          const int r = (et >> 2) + i * (kEpiThreads / kSG);
-          if (r < TN) stage[((g & 1) * kSG + j) * C::kSPitch + r] = f[i] * fw;
-        }
-      };
-      uint64_t acc[C::kNch][C::kCh / 2];
-#pragma unroll
-      for (int i = 0; i < C::kNch; ++i)
-#pragma unroll
-        for (int c = 0; c < C::kCh / 2; ++c) acc[i][c] = 0ull;
-      fetch(0);
-      // every warp is done with the last tile's factors; a warp whose wait ran
-      // out still takes part in the barriers, and all of them leave at one
-      if (!bar_and(1, kEpiThreads, ok)) break;
-      put(0);
-      bar_and(1, kEpiThreads, true);
-      for (int kb = 0, n = kb1 - kb0; kb < n; ++kb, ab.next()) {
-        const int g = kb / kSG;
-        if (kb % kSG == 0 && kb + kSG < n) fetch(g + 1);
-        const int buf = ab.s;
-        ok = ok && warp_wait(acc_full(buf), ab.ph, p.err, 85);
-        if (!ok) {
-          if (kb % kSG == kSG - 1 && kb + 1 < n) {
-            bar_and(1, kEpiThreads, false);
-            left = true;
+        for (int j = 0; j < kSG; ++j) {
+          if (k0 + j >= kb1) break;
+          const float w = j == 0 ? fw.x : j == 1 ? fw.y : j == 2 ? fw.z : fw.w;
+          const uint64_t w2 = pack2(__float_as_uint(w), __float_as_uint(w));
+          const float* fac = slot + j * C::kSPitch + h * C::kCh;
+          if (!warp_wait(done(r.s), r.ph, p.err, 85)) {
+            ok = false;
             break;
           }
-          continue;
-        }
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const uint32_t trow = tmem + buf * TN + ((uint32_t)(32 * q) << 16) + h * C::kCh;
-        const float* fac = stage + ((g & 1) * kSG + kb % kSG) * C::kSPitch + h * C::kCh;
-        uint32_t d[2][C::kCh];
-        auto ld = [&](int i) {
-          if (C::kCh == 32) tmem_ld32_nowait(trow + 2 * C::kCh * i, d[i & 1]);
-          else tmem_ld16_nowait(trow + 2 * C::kCh * i, d[i & 1]);
-        };
-        ld(0);
-#pragma unroll
-        for (int i = 0; i < C::kNch; ++i) {
-          tmem_ld_wait<C::kCh>(d[i & 1]);
-          if (i + 1 < C::kNch) {
-            ld(i + 1);
-          } else {   // read: the accumulator may be written again
-            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-            mbar_arrive_if(acc_empty(buf), lane == 0);
-          }
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          const uint32_t trow = tmem + ab.s * TN + ((uint32_t)(32 * q) << 16) + h * C::kCh;
+          uint32_t d[C::kCh];
+          if (C::kCh == 32) tmem_ld32_nowait(trow, d);
+          else tmem_ld16_nowait(trow, d);
+          uint64_t f[C::kCh / 2];
 #pragma unroll
           for (int c = 0; c < C::kCh / 4; ++c) {
-            const ulonglong2 s = *reinterpret_cast<const ulonglong2*>(fac + 2 * C::kCh * i + 4 * c);
-            fma2(acc[i][2 * c], pack2(d[i & 1][4 * c], d[i & 1][4 * c + 1]), s.x);
-            fma2(acc[i][2 * c + 1], pack2(d[i & 1][4 * c + 2], d[i & 1][4 * c + 3]), s.y);
+            const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(fac + 4 * c);
+            f[2 * c] = mul2(x.x, w2);
+            f[2 * c + 1] = mul2(x.y, w2);
           }
+          tmem_ld_wait<C::kCh>(d);
+          // read: the accumulator may be written again
+          asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+          mbar_arrive_if(acc_empty(ab.s), lane == 0);
+#pragma unroll
+          for (int c = 0; c < C::kCh / 2; ++c) fma2(acc[c], pack2(d[2 * c], d[2 * c + 1]), f[c]);
+          ab.next();
+          r.next();
         }
-        if (kb % kSG == kSG - 1 && kb + 1 < n) {
-          put(g + 1);   // the buffer of group g - 1, which every warp left before the last barrier
-          if (!bar_and(1, kEpiThreads, true)) {
-            ok = false;
-            left = true;
-            break;
-          }
-        }
+        __syncwarp();
+        mbar_arrive_if(sc_empty(sr.s), lane == 0);
       }
-      if (left) break;
-      if (!ok) continue;
+      if (!ok) break;
       // column c is token c; a warp's lanes are 32 neighbouring outputs of it
       if (SPLIT) {   // this CTA's part, [token][128], over the ring: its copies and MMAs are done
         float* dst = reinterpret_cast<float*>(smem) + 32 * q + lane;
 #pragma unroll
-        for (int i = 0; i < C::kNch; ++i)
-#pragma unroll
-          for (int c = 0; c < C::kCh / 2; ++c) {
-            float v[2];
-            unpack2(acc[i][c], v[0], v[1]);
-            dst[((2 * i + h) * C::kCh + 2 * c) * 128] = v[0];
-            dst[((2 * i + h) * C::kCh + 2 * c + 1) * 128] = v[1];
-          }
+        for (int c = 0; c < C::kCh / 2; ++c) {
+          float v[2];
+          unpack2(acc[c], v[0], v[1]);
+          dst[(h * C::kCh + 2 * c) * 128] = v[0];
+          dst[(h * C::kCh + 2 * c + 1) * 128] = v[1];
+        }
       } else {
         // through shared memory, 16 tokens at a time: 16-byte stores
         uint8_t* box = smem + C::kOffOut + (warp - kEpiWarp) * kBoxBytes;
@@ -334,31 +336,28 @@ f8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
         const int cpr = 2 * el, chunk = lane & (cpr - 1);   // 16-byte chunks of a row
         const int nn = t.mt * 128 + 32 * q + chunk * (16 / el);
 #pragma unroll
-        for (int i = 0; i < C::kNch; ++i) {
+        for (int c0 = 0; c0 < C::kCh; c0 += 16) {
+          const int col = h * C::kCh + c0;
+          if (col >= t.cols) continue;
+          __syncwarp();
 #pragma unroll
-          for (int c0 = 0; c0 < C::kCh; c0 += 16) {
-            const int col = (2 * i + h) * C::kCh + c0;
-            if (col >= t.cols) continue;
-            __syncwarp();
-#pragma unroll
-            for (int c = 0; c < 16; c += 2) {
-              float v[2];
-              unpack2(acc[i][(c0 + c) >> 1], v[0], v[1]);
-              if (p.out_f32) {
-                *reinterpret_cast<float*>(box + c * kOutPitchF + 4 * lane) = v[0];
-                *reinterpret_cast<float*>(box + (c + 1) * kOutPitchF + 4 * lane) = v[1];
-              } else {
-                *reinterpret_cast<__nv_bfloat16*>(box + c * kOutPitch + 2 * lane) = __float2bfloat16_rn(v[0]);
-                *reinterpret_cast<__nv_bfloat16*>(box + (c + 1) * kOutPitch + 2 * lane) = __float2bfloat16_rn(v[1]);
-              }
+          for (int c = 0; c < 16; c += 2) {
+            float v[2];
+            unpack2(acc[(c0 + c) >> 1], v[0], v[1]);
+            if (p.out_f32) {
+              *reinterpret_cast<float*>(box + c * kOutPitchF + 4 * lane) = v[0];
+              *reinterpret_cast<float*>(box + (c + 1) * kOutPitchF + 4 * lane) = v[1];
+            } else {
+              *reinterpret_cast<__nv_bfloat16*>(box + c * kOutPitch + 2 * lane) = __float2bfloat16_rn(v[0]);
+              *reinterpret_cast<__nv_bfloat16*>(box + (c + 1) * kOutPitch + 2 * lane) = __float2bfloat16_rn(v[1]);
             }
-            __syncwarp();
-            for (int tok = lane / cpr; tok < 16; tok += 32 / cpr)
-              if (nn < p.N && col + tok < t.cols)
-                *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) +
-                                          ((size_t)(t.row0 + t.c0 + col + tok) * (size_t)p.ld_out + nn) * el) =
-                    *reinterpret_cast<const uint4*>(box + tok * pitch + chunk * 16);
           }
+          __syncwarp();
+          for (int tok = lane / cpr; tok < 16; tok += 32 / cpr)
+            if (nn < p.N && col + tok < t.cols)
+              *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) +
+                                        ((size_t)(t.row0 + t.c0 + col + tok) * (size_t)p.ld_out + nn) * el) =
+                  *reinterpret_cast<const uint4*>(box + tok * pitch + chunk * 16);
         }
       }
       __syncwarp();

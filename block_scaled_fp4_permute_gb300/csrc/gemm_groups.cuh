@@ -275,17 +275,6 @@ __device__ __forceinline__ void drain_wait(uint32_t a, uint32_t parity) {
     if (globaltimer() - t0 > kWaitNs) return;
 }
 
-// barrier `id` over `threads` threads; the AND of every thread's v
-__device__ __forceinline__ bool bar_and(int id, int threads, bool v) {
-  uint32_t r;
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.b32 p, %3, 0;\n barrier.cta.red.and.pred q, %1, %2, p;\n selp.u32 %0, 1, 0, q;\n}"
-      : "=r"(r)
-      : "r"(id), "r"(threads), "r"((uint32_t)v)
-      : "memory");
-  return r != 0;
-}
-
 // tcgen05.ld of 32 columns, without the wait
 __device__ __forceinline__ void tmem_ld32_nowait(uint32_t taddr, uint32_t* r) {
   asm volatile(
