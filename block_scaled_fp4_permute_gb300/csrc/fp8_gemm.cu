@@ -831,13 +831,18 @@ extern "C" situ_status situ_moe_fp8_gemm(const situ_fp8_gemm_args* g, void* stre
   p.err = g->device_status;
 
   // Tiles: up to about 20 rows per group (one group's rows are known) 32
-  // tokens on the MMA's N side, which stream the weights and little else (40
-  // experts of 4096 x 2048, 10 / 25 / 45 rows each: 62 / 65 / 101 us, wide
-  // tiles 63 / 63 / 65); above, wide tiles; but 64 tokens on the N side while
-  // such tiles fit the SMs once (256 rows, 4096 x 4096: 16 us, wide 19), with
-  // the contraction split.
+  // tokens on the MMA's N side, up to about 50 of them 64, which stream the
+  // weights and little else; above, wide tiles (40 experts of 4096 x 2048 with
+  // 10 / 25 / 45 / 64 / 80 rows each: 32 tokens 57 / 59 / 80 / 98 / 116 us, 64
+  // tokens 57 / 58 / 60 / 72 / 92, wide 62 / 66 / 65 / 65 / 67; one of 24,576 x
+  // 4096, 64 and 100 rows: 64 tokens 27, 32 us, wide 31, 27).  But 64 tokens
+  // while such tiles fit the SMs once (256 rows, 4096 x 4096: 13.5 us, wide
+  // 19), with the contraction split.
   const double per = (double)g->S / g->E;
-  const int tn = per <= (g->E == 1 ? 32. : 20.) ? 32 : most_tiles(g->S, g->E, 64) * ((p.N + 127) / 128) <= sm_count() ? 64 : 256;
+  const bool one = g->E == 1;
+  const int tn = per <= (one ? 32. : 20.) ? 32
+                 : per <= (one ? 64. : 50.) || most_tiles(g->S, g->E, 64) * ((p.N + 127) / 128) <= sm_count() ? 64
+                                                                                                             : 256;
   // Wide tiles of one CTA (128 tokens) waste less of a group's last tile: 64
   // experts of 3584 x 2048, 256 rows: 169 us, pairs 199; 512: 292, 315; 8,192
   // rows of one: the same; 16,384: 228, 216.  Rows that do not start on

@@ -558,6 +558,20 @@ def test_every_form_of_the_fp8_product(counts, N, K):
         assert_sum(got, ref, mag, K, out_dtype)
 
 
+@pytest.mark.parametrize("counts,N,K", [
+    ([(7 * i) % 90 for i in range(40)], 520, 1040),      # 64-token tiles, several a CTA, some groups of two tiles
+    ([33] * 45, 640, 128),                               # one block of scales
+    ([(5 * i) % 38 for i in range(170)], 136, 1680),     # 32-token tiles, a partial block of rows and of columns
+])
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+def test_fp8_several_narrow_tiles_per_cta(counts, N, K, out_dtype):
+    S = sum(counts) + 6
+    ops = fp8_operands(gen(N + K), S, len(counts), N, K)
+    ref, mag = fp8_reference(*ops, counts, 3)
+    got = B.situ_moe_fp8_grouped_gemm(*ops, offsets_of(counts, 3), out_dtype=out_dtype)
+    assert_sum(got, ref, mag, K, out_dtype)
+
+
 def test_fp8_nan_and_infinite_scales_stay_in_their_rows():
     # wide tiles: a NaN code in one row, an infinite scale in another, and rows
     # of no group full of NaN, leave every other row alone
