@@ -550,7 +550,7 @@ def situ_moe_grouped_gemm_wgrad(dy: torch.Tensor, x: torch.Tensor, offsets: torc
         raise ValueError("dy must be [S, N] and x [S, K]")
     if accumulate and out is None:
         raise ValueError("accumulate adds to out: none given")
-    E = offsets.shape[0] - 1
+    E = offsets.numel() - 1
     return _grouped(dy, SITU_GROUPED_WGRAD, x, offsets, S, E, N, K, out, (E, N, K), (N * K, K, 1), out_dtype, accumulate,
                     True)
 

@@ -741,12 +741,13 @@ extern "C" situ_status situ_moe_grouped_gemm(const situ_grouped_gemm_args* g, vo
                  : per <= room[0] ? 32
                  : per <= room[1] ? 64
                  : per <= room[2] || most_tiles(g->S, g->E, 128) * ((p.M + 127) / 128) <= sm_count() ? 128 : 256;
+  // wgrad's short contractions are bound by the stores, which eight warps issue
+  // faster (896 experts, one row each, 768 x 3584: 0.79 ms, four warps 0.89;
+  // 112 of 6144 x 3584, 75 rows: 0.93, 0.94; 32 of 4096 x 3584, 128 rows: 0.21,
+  // 0.18).
+  p.store8 = per <= 75;
   // wgrad of few output tiles: the rows of a group split over clusters (a
   // skewed group's rows are taken as up to twice the average)
-  // Short contractions are bound by the stores, which eight warps issue faster
-  // (896 experts, one row each, 768 x 3584: 0.79 ms, four warps 0.89; 112 of
-  // 6144 x 3584, 75 rows: 0.93, 0.94; 32 of 4096 x 3584, 128 rows: 0.21, 0.18).
-  p.store8 = per <= 75;
   const double wtiles = (double)p.E * ((p.M + 127) / 128) * ((p.Ncol + 255) / 256);
   const int wsteps = (int)((g->E > 1 ? 2 * per : per) / kBK);
   const int wsplit = mode == kWgrad ? split_of(gg_kernel<1, kWgrad, 256, true, true>, kThreads,
