@@ -53,7 +53,7 @@ class SituGroupedGemmArgs(ctypes.Structure):
                                               "keep_rest")] + [
         ("a", ctypes.c_void_p), ("lda", ctypes.c_int64), ("b", ctypes.c_void_p), ("ldb", ctypes.c_int64),
         ("offsets", ctypes.c_void_p), ("out", ctypes.c_void_p), ("ldo", ctypes.c_int64),
-        ("device_status", ctypes.c_void_p)]
+        ("device_status", ctypes.c_void_p), ("ldw", ctypes.c_int64), ("stride_w", ctypes.c_int64)]
 
 
 class SituFp8GemmArgs(ctypes.Structure):
@@ -61,7 +61,8 @@ class SituFp8GemmArgs(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("out_dtype", "S", "N", "K", "E", "keep_rest")] + [
         ("x_q", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("x_scale", ctypes.c_void_p), ("w_q", ctypes.c_void_p),
         ("w_scale", ctypes.c_void_p), ("offsets", ctypes.c_void_p), ("out", ctypes.c_void_p),
-        ("ldo", ctypes.c_int64), ("device_status", ctypes.c_void_p)]
+        ("ldo", ctypes.c_int64), ("device_status", ctypes.c_void_p), ("ldw", ctypes.c_int64),
+        ("stride_w", ctypes.c_int64)]
 
 
 def library_path() -> str:
@@ -455,6 +456,25 @@ def _packed(t: torch.Tensor):
     return t, p
 
 
+def _weights(t: torch.Tensor, unit: int):
+    """(tensor, pointer, elements between rows, between experts; 0 and 0:
+    contiguous) of weights [E, N, K] or [N, K]: itself where the kernels can
+    read it in place (a part of a larger array, as one half of gate and up
+    weights held together), else a copy."""
+    p = t.data_ptr()
+    if not p & 15:
+        if t.is_contiguous():
+            return t, p, 0, 0
+        N, K = t.shape[-2:]
+        ld = t.stride(-2)
+        if t.stride(-1) == 1 and ld >= K and ld % unit == 0:
+            se = N * ld if t.dim() == 2 or t.shape[0] == 1 else t.stride(0)
+            if se >= N * ld and se % ld == 0:
+                return t, p, ld, se
+    t = t.clone(memory_format=torch.contiguous_format)
+    return t, t.data_ptr(), 0, 0
+
+
 def _given(out: torch.Tensor, shape, dtype, index: int, unit: int) -> int:
     """The elements between the rows of a caller's ``out``, after its checks."""
     if tuple(out.shape) != shape or out.dtype is not dtype or out.get_device() != index:
@@ -495,13 +515,14 @@ def _grouped(a, direction, b, offsets, S, E, N, K, out, shape, strides, out_dtyp
     if not offsets.is_contiguous():
         offsets = offsets.contiguous()
     a, pa, lda = _rows(a, 8)
+    ldb = ldw = stride_w = 0
     if direction == SITU_GROUPED_WGRAD:
         b, pb, ldb = _rows(b, 8)
     else:
-        b, pb = _packed(b)
-        ldb = 0
+        b, pb, ldw, stride_w = _weights(b, 8)
     args = SituGroupedGemmArgs(direction, _DTYPES[dtype], _DTYPES[out_dtype], S, N, K, E, accumulate, not zero_rest,
-                               pa, lda, pb, ldb, offsets.data_ptr(), out.data_ptr(), ldo, _status_word(index).data_ptr())
+                               pa, lda, pb, ldb, offsets.data_ptr(), out.data_ptr(), ldo, _status_word(index).data_ptr(),
+                               ldw, stride_w)
     _enqueue("situ_moe_grouped_gemm", index, ctypes.byref(args))
     return out
 
@@ -511,10 +532,10 @@ def situ_moe_grouped_gemm(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tenso
     """y[r] = x[r] @ w[e].T for the rows r of each expert e: x [S, K] sorted by
     expert, w [E, N, K] of the same 16-bit type (or one expert's [N, K]),
     offsets int32 [E + 1] (as situ_moe_permute returns them).  Rows of no expert
-    give zeros, or are left unwritten with ``zero_rest=False``.  Rows may be
-    strided; a layout that the kernels cannot read in place (weights that are
-    not contiguous, columns apart, rows off 16 bytes) is copied first, in each
-    of these calls."""
+    give zeros, or are left unwritten with ``zero_rest=False``.  Rows, of
+    weights too, may be strided; a layout that the kernels cannot read in place
+    (columns apart, rows off 16 bytes, experts broadcast) is copied first, in
+    each of these calls."""
     if stream is not None:
         return _on_stream(stream, situ_moe_grouped_gemm, x, w, offsets, out=out, out_dtype=out_dtype, zero_rest=zero_rest)
     E, N, K = w.shape if w.dim() == 3 else (1, *w.shape)
@@ -646,13 +667,13 @@ def _fp8_gemm(x_q, x_scale, w_q, w_scale, E, N, K, offsets, out, out_dtype, zero
     else:
         ldo = _given(out, (S, N), out_dtype, index, 8)
     x_q, px, ldx = _rows(x_q, 16)
-    w_q, pw = _packed(w_q)
+    w_q, pw, ldw, stride_w = _weights(w_q, 16)
     if not x_scale.is_contiguous():
         x_scale = x_scale.contiguous()
     if not w_scale.is_contiguous():
         w_scale = w_scale.contiguous()
     args = SituFp8GemmArgs(_DTYPES[out_dtype], S, N, K, E, not zero_rest, px, ldx, x_scale.data_ptr(), pw,
-                           w_scale.data_ptr(), poff, out.data_ptr(), ldo, _status_word(index).data_ptr())
+                           w_scale.data_ptr(), poff, out.data_ptr(), ldo, _status_word(index).data_ptr(), ldw, stride_w)
     _enqueue("situ_moe_fp8_gemm", index, ctypes.byref(args))
     return out
 

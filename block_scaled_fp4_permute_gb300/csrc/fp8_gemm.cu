@@ -807,6 +807,10 @@ extern "C" situ_status situ_moe_fp8_gemm(const situ_fp8_gemm_args* g, void* stre
       g->N > SITU_GEMM_MAX_DIM || g->K > SITU_GEMM_MAX_DIM || g->S > SITU_GEMM_MAX_ROWS || (!g->offsets && g->E != 1) ||
       g->ldx < g->K || g->ldx % 16 != 0 || g->ldo < g->N || g->ldo % 8 != 0)
     return SITU_ERR_BAD_SHAPE;
+  const int64_t ldw = g->ldw ? g->ldw : g->K;
+  if (ldw > kMaxStride) return SITU_ERR_BAD_SHAPE;
+  const int64_t stride_w = g->stride_w ? g->stride_w : g->N * ldw;
+  if (ldw < g->K || ldw % 16 != 0 || stride_w < g->N * ldw || stride_w % ldw != 0) return SITU_ERR_BAD_SHAPE;
   if (g->S == 0) return SITU_OK;
   if (!g->x_q || !g->x_scale || !g->w_q || !g->w_scale || !g->out || !g->device_status) return SITU_ERR_NULL_ARG;
   for (const void* q : {(const void*)g->x_q, (const void*)g->w_q, (const void*)g->out})
@@ -849,14 +853,14 @@ extern "C" situ_status situ_moe_fp8_gemm(const situ_fp8_gemm_args* g, void* stre
   // 128-byte lines cost about twice the L2 requests, and a pair copies the
   // weights half as often: 100 experts of 2048 x 2064, 164 rows: 134 us, pairs
   // 117; one of 4096 x 2000, 16,384 rows: 162, 127.
-  const bool lines = g->K % 128 == 0 && g->ldx % 128 == 0;
+  const bool lines = ldw % 128 == 0 && g->ldx % 128 == 0;
   const int cg = tn < 256 || per < (lines ? 4096. : 150.) ? 1 : 2;
   const int tm = tn < 256 ? tn : 128 * cg;        // tokens per tile
   p.n_mt = tn < 256 ? (p.N + 127) / 128 : (p.N + kWideN - 1) / kWideN;
   if (most_tiles(g->S, g->E, tm) * p.n_mt > 2.0e9) return SITU_ERR_BAD_SHAPE;
   CUtensorMap mw, mx;
   const uint64_t S = (uint64_t)g->S, N = (uint64_t)g->N, K = (uint64_t)g->K, E = (uint64_t)g->E;
-  const uint64_t dw[3] = {K, N, E}, sw[2] = {K, N * K}, dx[2] = {K, S}, sx[1] = {(uint64_t)g->ldx};
+  const uint64_t dw[3] = {K, N, E}, sw[2] = {(uint64_t)ldw, (uint64_t)stride_w}, dx[2] = {K, S}, sx[1] = {(uint64_t)g->ldx};
   const uint32_t boxw[3] = {128, tn < 256 ? 128u : (uint32_t)(kWideN / 2 / cg), 1}, boxx[2] = {128, tn < 256 ? (uint32_t)tn : 128u};
   if (!make_map_nd(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, g->w_q, 3, dw, sw, boxw) ||
       !make_map_nd(&mx, CU_TENSOR_MAP_DATA_TYPE_UINT8, g->x_q, 2, dx, sx, boxx))

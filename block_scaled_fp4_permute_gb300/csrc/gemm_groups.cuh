@@ -18,6 +18,7 @@ namespace gg {
 using namespace tc;
 
 constexpr int kMaxGroups = 1024;   // tile prefix in shared memory, 4 KB
+constexpr int64_t kMaxStride = int64_t(1) << 39;   // elements; the tensor maps' own limit is 2^40 bytes
 
 __device__ __forceinline__ int2 group_rows(const int32_t* off, int e, int S) {
   if (off == nullptr) return make_int2(0, S);   // one dense group

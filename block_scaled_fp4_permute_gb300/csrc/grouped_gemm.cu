@@ -699,6 +699,12 @@ extern "C" situ_status situ_moe_grouped_gemm(const situ_grouped_gemm_args* g, vo
   if (g->lda < ca || g->lda % 8 != 0 || (mode == kWgrad && (g->ldb < cb || g->ldb % 8 != 0)) ||
       (mode != kWgrad && (g->ldo < co || g->ldo % 8 != 0)))
     return SITU_ERR_BAD_SHAPE;
+  const int64_t ldw = g->ldw ? g->ldw : g->K;
+  if (ldw > kMaxStride) return SITU_ERR_BAD_SHAPE;
+  const int64_t stride_w = g->stride_w ? g->stride_w : g->N * ldw;
+  if (mode == kWgrad ? g->ldw != 0 || g->stride_w != 0
+                     : ldw < g->K || ldw % 8 != 0 || stride_w < g->N * ldw || stride_w % ldw != 0)
+    return SITU_ERR_BAD_SHAPE;
   if (g->S == 0 && mode != kWgrad) return SITU_OK;
   if (!g->out || !g->offsets || !g->device_status || (g->S > 0 && (!g->a || !g->b)) || (mode != kWgrad && !g->b))
     return SITU_ERR_NULL_ARG;
@@ -773,7 +779,7 @@ extern "C" situ_status situ_moe_grouped_gemm(const situ_grouped_gemm_args* g, vo
          make_map_nd(&m.a16, dt, g->a, 2, da, sa, box16) && make_map_nd(&m.b16, dt, g->b, 2, db, sb, box16) &&
          make_map_nd(&m.out, p.out_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : dt, g->out, 3, dout, sout, boxo);
   } else {
-    const uint64_t dw[3] = {K, N, E}, sw[2] = {K * 2, N * K * 2};
+    const uint64_t dw[3] = {K, N, E}, sw[2] = {(uint64_t)ldw * 2, (uint64_t)stride_w * 2};
     const uint32_t boxw[3] = {64, mode == kFwd ? 128u : 64u, 1};
     const uint64_t dx[2] = {(uint64_t)p.L, S}, sx[1] = {(uint64_t)g->lda * 2};
     const uint32_t boxx[2] = {64, (uint32_t)kBoxRows};

@@ -534,8 +534,11 @@ typedef enum situ_grouped_direction {
  * a and b are of one 16-bit type; sums are fp32, rounded once to out_dtype
  * (the operands' type or fp32; an accumulating bf16 / f16 dw is rounded once
  * per call).  N and K are multiples of 8, rows may be strided (lda, ldb, ldo
- * in elements, multiples of 8; ldb is wgrad's x, ldo y or dx; weights and dw
- * are contiguous).  a, b, out are 16-byte aligned.  S == 0 launches nothing,
+ * in elements, multiples of 8; ldb is wgrad's x, ldo y or dx; dw is
+ * contiguous).  Weights may be a part of a larger array: ldw elements between
+ * rows (a multiple of 8), stride_w between experts (a multiple of ldw, at
+ * least N * ldw); 0 and 0, and for WGRAD always: contiguous.  a, b, out are
+ * 16-byte aligned.  S == 0 launches nothing,
  * or sets dw to zeros.  Results do not depend on the order of execution.
  * Errors: NULL_ARG, BAD_SHAPE, UNSUPPORTED, MISALIGNED, CUDA. */
 typedef struct situ_grouped_gemm_args {
@@ -552,6 +555,7 @@ typedef struct situ_grouped_gemm_args {
   void* out;
   int64_t ldo;
   int32_t* device_status;
+  int64_t ldw, stride_w;          /* FORWARD, DGRAD: of w; 0: K and N * ldw */
 } situ_grouped_gemm_args;
 situ_status situ_moe_grouped_gemm(const situ_grouped_gemm_args* args, void* stream);
 
@@ -576,7 +580,8 @@ situ_status situ_moe_quant_fp8(const void* x, int32_t dtype, int32_t E, int32_t 
  * [E, ceil(N/128), ceil(K/128)] (contiguous); out bf16 or fp32 [S, N].  A
  * block's products are summed in the tensor cores, the scaled blocks in
  * fp32.  K is a multiple of 16, N of 8; x_q rows may be ldx bytes apart (a
- * multiple of 16), out rows ldo elements (a multiple of 8).
+ * multiple of 16), out rows ldo elements (a multiple of 8), w_q rows and
+ * experts ldw and stride_w bytes (as above, ldw a multiple of 16).
  * Errors: NULL_ARG, BAD_SHAPE, UNSUPPORTED, MISALIGNED, CUDA. */
 typedef struct situ_fp8_gemm_args {
   int32_t out_dtype;              /* SITU_DT_BF16 or SITU_DT_F32 */
@@ -591,6 +596,7 @@ typedef struct situ_fp8_gemm_args {
   void* out;
   int64_t ldo;
   int32_t* device_status;
+  int64_t ldw, stride_w;          /* of w_q; 0: K and N * ldw */
 } situ_fp8_gemm_args;
 situ_status situ_moe_fp8_gemm(const situ_fp8_gemm_args* args, void* stream);
 

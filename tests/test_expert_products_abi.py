@@ -73,6 +73,24 @@ def test_quant_refusals(lib, args, status):
     assert lib.situ_moe_quant_fp8(*args, None) == status
 
 
+@pytest.mark.parametrize("over,status", [
+    (dict(ldw=120), 2), (dict(ldw=132), 2), (dict(ldw=-128), 2), (dict(ldw=1 << 62), 2),
+    (dict(stride_w=63 * 128), 2), (dict(stride_w=64 * 128 + 8), 2), (dict(ldw=256, stride_w=64 * 128), 2),
+    (dict(stride_w=-64 * 128), 2), (dict(direction=2, lda=64, ldw=128), 2), (dict(direction=2, lda=64, stride_w=64 * 128), 2),
+    (dict(S=0, ldw=256), 0), (dict(S=0, ldw=256, stride_w=128 * 256), 0),
+])
+def test_grouped_refuses_weight_strides(lib, over, status):
+    assert grouped(lib, **over) == status
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(ldw=112), 2), (dict(ldw=136), 2), (dict(ldw=1 << 62), 2), (dict(stride_w=64 * 112), 2),
+    (dict(ldw=256, stride_w=64 * 256 + 128), 2), (dict(S=0, ldw=144, stride_w=65 * 144), 0),
+])
+def test_fp8_refuses_weight_strides(lib, over, status):
+    assert fp8(lib, **over) == status
+
+
 def test_null_args(lib):
     assert lib.situ_moe_grouped_gemm(None, None) == 1
     assert lib.situ_moe_fp8_gemm(None, None) == 1

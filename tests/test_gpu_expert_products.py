@@ -558,6 +558,44 @@ def test_every_form_of_the_fp8_product(counts, N, K):
         assert_sum(got, ref, mag, K, out_dtype)
 
 
+# Weights that are a part of a larger array are read where they lie: the same
+# bits as from a copy, and no copy made; what surrounds them is NaN.
+@pytest.mark.parametrize("counts,N,K", [([5, 0, 20], 264, 2064), ([90, 60, 0, 97], 1416, 208),
+                                        ([300, 700], 2056, 256), ([9000, 0, 10000], 72, 128)])
+@pytest.mark.parametrize("part", ["rows", "columns", "both"])
+def test_products_read_parts_of_weights_in_place(counts, N, K, part):
+    E, S, off = len(counts), sum(counts) + 2, offsets_of(counts, 1)
+    r0, c0 = (N if part != "columns" else 0), (16 if part != "rows" else 0)
+    shape = (E, r0 + N + (8 if r0 else 0), c0 + K + (32 if c0 else 0))
+    g = gen(N + K)
+    x = torch.randn(S, K, device="cuda", generator=g).bfloat16()
+    dy = torch.randn(S, N, device="cuda", generator=g).bfloat16()
+    w = torch.full(shape, float("nan"), device="cuda", dtype=torch.bfloat16)[:, r0:r0 + N, c0:c0 + K]
+    wc = torch.randn(E, N, K, device="cuda", generator=g).bfloat16()
+    w.copy_(wc)
+    xq, xs, wq, ws = fp8_operands(g, S, E, N, K)
+    wv = torch.full(shape, 127, device="cuda", dtype=torch.uint8)[:, r0:r0 + N, c0:c0 + K]   # E4M3 NaN
+    wv.copy_(wq)
+    assert not w.is_contiguous() and not wv.is_contiguous()
+    for make, small in ((lambda v: B.situ_moe_grouped_gemm(x, v, off), (w, wc)),
+                        (lambda v: B.situ_moe_grouped_gemm_dgrad(dy, v, off, out_dtype=torch.float32), (w, wc)),
+                        (lambda v: B.situ_moe_fp8_grouped_gemm(xq, xs, v, ws, off), (wv, wq))):
+        ref = make(small[1])
+        torch.cuda.synchronize()
+        torch.cuda.reset_peak_memory_stats()
+        before = torch.cuda.memory_stats()["requested_bytes.all.current"]
+        got = make(small[0])
+        torch.cuda.synchronize()
+        grown = torch.cuda.memory_stats()["requested_bytes.all.peak"] - before
+        assert grown <= got.numel() * got.element_size()
+        assert torch.isfinite(got).all() and torch.equal(got, ref)
+    # one expert's part, and one expert's weights for all (copied)
+    y = B.situ_moe_fp8_gemm(xq, xs, wv[0], ws[0])
+    assert torch.equal(y, B.situ_moe_fp8_gemm(xq, xs, wq[0], ws[0]))
+    one = w[:1].expand(E, N, K)
+    assert torch.equal(B.situ_moe_grouped_gemm(x, one, off), B.situ_moe_grouped_gemm(x, one.contiguous(), off))
+
+
 @pytest.mark.parametrize("counts,N,K", [
     ([(7 * i) % 90 for i in range(40)], 520, 1040),      # 64-token tiles, several a CTA, some groups of two tiles
     ([33] * 45, 640, 128),                               # one block of scales
