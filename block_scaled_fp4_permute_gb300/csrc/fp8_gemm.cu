@@ -391,7 +391,7 @@ f8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
 // N side.  A lane is a token, so a block's factor is one register and the
 // additions need nothing from shared memory (with tokens along the columns the
 // factors were a broadcast load per column, more shared-memory wavefronts than
-// the MMA and the copies together: 8,192 x 6144 x 3584 0.33 ms, now 0.148).
+// the MMA and the copies together: 8,192 x 6144 x 3584 0.33 ms, now 0.139).
 //
 // A tile is two halves of 128 weight rows, that is of one weight block each,
 // with an MMA issuer and a promoting warpgroup per half and two accumulators
@@ -403,14 +403,16 @@ f8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
 // through an L1 that the scales and results thrash, and cost 40 %.
 //
 // Bound by the promotion: 102 us of that case without its additions and
-// stores, 28 more for the additions, 16 for the stores.
+// stores, 28 more for the additions; stores by the promoting warps took 16,
+// boxes that TMA takes away while the next tile is promoted take 7 (fp32
+// results: 172 to 153 us).
 // ---------------------------------------------------------------------------
 
 constexpr int kWideN = 256;
 constexpr int kWideParts = 2;                          // halves of a tile: an MMA and a promoting warpgroup each
 constexpr int kWideThreads = 128 + 128 * kWideParts;
 
-template <int CG>
+template <int CG, int BOXES>
 struct WCfg {
   static constexpr int kTM = 128 * CG;                 // tokens per tile
   static constexpr int kTN = kWideN;                     // weight rows per tile
@@ -420,13 +422,19 @@ struct WCfg {
   // scales: slots of four blocks, 128 tokens' and two weight blocks' factors
   static constexpr int kSlots = 4;
   static constexpr int kSlotBytes = (128 + 2) * 16;
-  static constexpr int kOutBytes = 2048;               // output staging of a promoting warp
+  // output boxes of a promoting warp, 32 rows: a CTA of its own has no room
+  // for more than one of 64 bytes beside four stages (three: 16,384 rows of 64
+  // experts, 3584 x 2048: 152 us, four 145); a pair has five stages and a box
+  // of 128 bytes, or four and two
+  static constexpr int kRow = CG == 2 ? 128 : 64;
+  static constexpr int kBoxBytes = 32 * kRow;
+  static constexpr int kOutBytes = BOXES * kBoxBytes;
   static constexpr int kMaxBytes = 232448 - 1024 - 4 * (kMaxGroups + 1) - 512 - kSlots * kSlotBytes - 4 * kWideParts * kOutBytes;
   static constexpr int kStages = kMaxBytes / kStageBytes;
   static constexpr int kOffB = kStages * kABytes;
-  static constexpr int kOffS = kOffB + kStages * kBBytes;
-  static constexpr int kOffOut = kOffS + kSlots * kSlotBytes;
-  static constexpr int kOffTp = kOffOut + 4 * kWideParts * kOutBytes;
+  static constexpr int kOffOut = kOffB + kStages * kBBytes;
+  static constexpr int kOffS = kOffOut + 4 * kWideParts * kOutBytes;
+  static constexpr int kOffTp = kOffS + kSlots * kSlotBytes;
   static constexpr int kOffBar = (kOffTp + 4 * (kMaxGroups + 1) + 15) / 16 * 16;
   // full, done[2] per stage; acc_empty[2][2]; drain[2]; scale slots full, empty
   static constexpr int kNumBars = 3 * kStages + 6 + 2 * kSlots;
@@ -442,7 +450,7 @@ struct WTile {
 };
 template <int CG>
 __device__ __forceinline__ WTile wide_tile_of(const F8Params& p, const int* tp, int idx) {
-  using C = WCfg<CG>;
+  using C = WCfg<CG, 1>;
   WTile t;
   t.e = find_group(tp, p.E, idx / p.n_mt);
   const int r = idx - tp[t.e] * p.n_mt, tt = tp[t.e + 1] - tp[t.e], nt = r / tt;
@@ -474,23 +482,11 @@ __device__ __forceinline__ float4 lds_f32x4(uint32_t a) {
   asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
   return v;
 }
-// A box of 32 rows x 64 bytes, 16-byte chunks exchanged within row pairs so
-// that neither a column of chunks nor whole rows conflict.
-__device__ __forceinline__ void stage16(uint8_t* box, int row, int chunk, uint4 v) {
-  *reinterpret_cast<uint4*>(box + row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4)) = v;
-}
-// the box to rows [row, row + min(rows, 32)) of the output from column n on
-// (el bytes per element), as far as N goes
-__device__ __forceinline__ void store_box(const F8Params& p, const uint8_t* box, int lane, int row, int rows, int n, int el) {
-  const int chunk = lane & 3, col = n + chunk * (16 / el);
-  if (col >= p.N) return;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = (lane >> 2) + 8 * i;
-    if (r < rows)
-      *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + ((size_t)(row + r) * (size_t)p.ld_out + col) * el) =
-          *reinterpret_cast<const uint4*>(box + r * 64 + ((chunk ^ ((r >> 1) & 3)) << 4));
-  }
+// Where a box of 32 rows x ROW bytes in the ROW-byte swizzle holds the 16-byte
+// chunk c of row r: neither a column of chunks nor whole rows conflict.
+template <int ROW>
+__device__ __forceinline__ int box_at(int r, int c) {
+  return r * ROW + ((c ^ (ROW == 128 ? r & 7 : (r >> 1) & 3)) << 4);
 }
 // acc += d * f, kept in its place between the TMEM loads and the arrivals
 __device__ __forceinline__ void fma_in_order(float& acc, uint32_t d, float f) {
@@ -504,10 +500,11 @@ __device__ __forceinline__ int half_cols(const WTile& t, int h) {
   return (c + 16 * CG - 1) / (16 * CG) * (16 * CG);
 }
 
-template <int CG>
+template <int CG, int BOXES>
 __global__ void __launch_bounds__(kWideThreads, 1)
-f8w_kernel(const __grid_constant__ CUtensorMap mapX, const __grid_constant__ CUtensorMap mapW, const F8Params p) {
-  using C = WCfg<CG>;
+f8w_kernel(const __grid_constant__ CUtensorMap mapX, const __grid_constant__ CUtensorMap mapW,
+           const __grid_constant__ CUtensorMap mapO, const F8Params p) {
+  using C = WCfg<CG, BOXES>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -527,6 +524,7 @@ f8w_kernel(const __grid_constant__ CUtensorMap mapX, const __grid_constant__ CUt
   if (tid == 0) {
     prefetch_map(&mapX);
     prefetch_map(&mapW);
+    prefetch_map(&mapO);
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(full(s), 1);
       mbar_init(done(0, s), 1);
@@ -728,35 +726,64 @@ f8w_kernel(const __grid_constant__ CUtensorMap mapX, const __grid_constant__ CUt
       }
       if (!ok) break;
       const WTile t = wide_tile_of<CG>(p, tp, idx);
-      // through shared memory, 64 bytes of each of the warp's 32 rows at a time:
-      // a warp's store then covers 8 rows' whole sectors, not 32 rows' halves
+      // through shared memory, kRow bytes of the warp's 32 rows at a time: whole
+      // boxes by TMA, which takes them away while the next tile is promoted,
+      // and a group's last rows, next to another group's, by plain stores
       const int row0 = t.t0 + 128 * (int)rank + 32 * q, n0 = t.n0 + C::kCols * h;
-      uint8_t* box = smem + C::kOffOut + (warp - kEpiWarp) * C::kOutBytes;
+      uint8_t* boxes = smem + C::kOffOut + (warp - kEpiWarp) * C::kOutBytes;
+      auto store = [&](int i, int el, auto value) {
+        uint8_t* box = boxes + C::kBoxBytes * (i % BOXES);
+        const int n = n0 + i * (C::kRow / el);
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(BOXES - 1) : "memory");   // the box is free
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < C::kRow / 16; ++c) *reinterpret_cast<uint4*>(box + box_at<C::kRow>(lane, c)) = value(c);
+        if (row0 + 32 <= t.rows) {
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) {
+            if (n < p.N)
+              asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                               reinterpret_cast<uint64_t>(&mapO)),
+                           "r"(n), "r"(t.row0 + row0), "r"(saddr(box))
+                           : "memory");
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          }
+        } else {
+          constexpr int kCpr = C::kRow / 16;
+          const int c = lane % kCpr, col = n + c * (16 / el);
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < kCpr; ++k) {
+            const int r = lane / kCpr + 32 / kCpr * k;
+            if (row0 + r < t.rows && col < p.N)
+              *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) +
+                                        ((size_t)(t.row0 + row0 + r) * (size_t)p.ld_out + col) * el) =
+                  *reinterpret_cast<const uint4*>(box + box_at<C::kRow>(r, c));
+          }
+        }
+      };
       if (p.out_f32) {
 #pragma unroll
-        for (int i = 0; i < C::kCols / 16; ++i) {
-          const float* v = acc + 16 * i;
-          __syncwarp();
-#pragma unroll
-          for (int c = 0; c < 4; ++c) stage16(box, lane, c, make_uint4(__float_as_uint(v[4 * c]), __float_as_uint(v[4 * c + 1]),
-                                                                       __float_as_uint(v[4 * c + 2]), __float_as_uint(v[4 * c + 3])));
-          __syncwarp();
-          store_box(p, box, lane, t.row0 + row0, t.rows - row0, n0 + 16 * i, 4);
+        for (int i = 0; i < C::kCols * 4 / C::kRow; ++i) {
+          const float* v = acc + C::kRow / 4 * i;
+          store(i, 4, [&](int c) {
+            return make_uint4(__float_as_uint(v[4 * c]), __float_as_uint(v[4 * c + 1]), __float_as_uint(v[4 * c + 2]),
+                              __float_as_uint(v[4 * c + 3]));
+          });
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < C::kCols / 32; ++i) {
-          const float* v = acc + 32 * i;
-          __syncwarp();
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            stage16(box, lane, c, make_uint4(f32x2_to_bf16x2(v[8 * c], v[8 * c + 1]), f32x2_to_bf16x2(v[8 * c + 2], v[8 * c + 3]),
-                                             f32x2_to_bf16x2(v[8 * c + 4], v[8 * c + 5]), f32x2_to_bf16x2(v[8 * c + 6], v[8 * c + 7])));
-          __syncwarp();
-          store_box(p, box, lane, t.row0 + row0, t.rows - row0, n0 + 32 * i, 2);
+        for (int i = 0; i < C::kCols * 2 / C::kRow; ++i) {
+          const float* v = acc + C::kRow / 2 * i;
+          store(i, 2, [&](int c) {
+            return make_uint4(f32x2_to_bf16x2(v[8 * c], v[8 * c + 1]), f32x2_to_bf16x2(v[8 * c + 2], v[8 * c + 3]),
+                              f32x2_to_bf16x2(v[8 * c + 4], v[8 * c + 5]), f32x2_to_bf16x2(v[8 * c + 6], v[8 * c + 7]));
+          });
         }
       }
     }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     zero_rest(p, et, 128 * kWideParts);
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -781,18 +808,20 @@ cudaError_t launch_t(const CUtensorMap& a, const CUtensorMap& b, const F8Params&
                         Cfg<TN>::kSmem, st, a, b, p);
 }
 
-template <int CG>
-cudaError_t launch_wide(const CUtensorMap& x, const CUtensorMap& w, const F8Params& p, long max_items, cudaStream_t st) {
+template <int CG, int BOXES>
+cudaError_t launch_wide(const CUtensorMap& x, const CUtensorMap& w, const CUtensorMap& o, const F8Params& p, long max_items,
+                        cudaStream_t st) {
   static std::atomic<uint64_t> raised{0};
   // the register shares need the launch to hold their sum
   static const int regs = [] {
     cudaFuncAttributes fa;
-    return cudaFuncGetAttributes(&fa, f8w_kernel<CG>) == cudaSuccess ? fa.numRegs : 0;
+    return cudaFuncGetAttributes(&fa, f8w_kernel<CG, BOXES>) == cudaSuccess ? fa.numRegs : 0;
   }();
   const long sms = sm_count();
   if (sms <= 0 || regs < kLaunchRegs) return cudaErrorInvalidConfiguration;
   const long ctas = max_items < sms / CG ? max_items * CG : sms / CG * CG;
-  return launch_cluster(f8w_kernel<CG>, &raised, CG, (int)(ctas < CG ? CG : ctas), kWideThreads, WCfg<CG>::kSmem, st, x, w, p);
+  return launch_cluster(f8w_kernel<CG, BOXES>, &raised, CG, (int)(ctas < CG ? CG : ctas), kWideThreads,
+                        WCfg<CG, BOXES>::kSmem, st, x, w, o, p);
 }
 
 }  // namespace
@@ -847,24 +876,36 @@ extern "C" situ_status situ_moe_fp8_gemm(const situ_fp8_gemm_args* g, void* stre
   const int tn = per <= (one ? 32. : 20.) ? 32
                  : per <= (one ? 64. : 50.) || most_tiles(g->S, g->E, 64) * ((p.N + 127) / 128) <= sm_count() ? 64
                                                                                                              : 256;
-  // Wide tiles of one CTA (128 tokens) waste less of a group's last tile: 64
-  // experts of 3584 x 2048, 256 rows: 169 us, pairs 199; 512: 292, 315; 8,192
-  // rows of one: the same; 16,384: 228, 216.  Rows that do not start on
-  // 128-byte lines cost about twice the L2 requests, and a pair copies the
-  // weights half as often: 100 experts of 2048 x 2064, 164 rows: 134 us, pairs
-  // 117; one of 4096 x 2000, 16,384 rows: 162, 127.
+  // Wide tiles of one CTA (128 tokens) waste less of a group's last tile, a
+  // pair copies the weights half as often: 64 experts of 3584 x 2048, 256 rows:
+  // 143 us, pairs 159; 32, 512 rows: 128, 130; 16, 1,024: 119, 119; 8, 2,048:
+  // 117, 109.  Rows that do not start on 128-byte lines cost about twice the L2
+  // requests: 64 experts of 3584 x 2000, 100 / 128 rows: 93 / 121 us, pairs 118 /
+  // 119; 100 of 2048 x 2064, 164 rows: 135, 117.
   const bool lines = ldw % 128 == 0 && g->ldx % 128 == 0;
-  const int cg = tn < 256 || per < (lines ? 4096. : 150.) ? 1 : 2;
+  const int cg = tn < 256 || per < (lines ? 1024. : 150.) ? 1 : 2;
+  // A pair's second output box costs it its fifth stage: 8,192 rows, 6144 x
+  // 3584: 146 us, two boxes 143; rows off the lines need the stage (16,384 rows,
+  // 4096 x 2000, fp32: 148 us, two boxes 163).
+  const bool two = lines;
   const int tm = tn < 256 ? tn : 128 * cg;        // tokens per tile
   p.n_mt = tn < 256 ? (p.N + 127) / 128 : (p.N + kWideN - 1) / kWideN;
   if (most_tiles(g->S, g->E, tm) * p.n_mt > 2.0e9) return SITU_ERR_BAD_SHAPE;
-  CUtensorMap mw, mx;
+  CUtensorMap mw, mx, mo = {};
   const uint64_t S = (uint64_t)g->S, N = (uint64_t)g->N, K = (uint64_t)g->K, E = (uint64_t)g->E;
   const uint64_t dw[3] = {K, N, E}, sw[2] = {(uint64_t)ldw, (uint64_t)stride_w}, dx[2] = {K, S}, sx[1] = {(uint64_t)g->ldx};
   const uint32_t boxw[3] = {128, tn < 256 ? 128u : (uint32_t)(kWideN / 2 / cg), 1}, boxx[2] = {128, tn < 256 ? (uint32_t)tn : 128u};
   if (!make_map_nd(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, g->w_q, 3, dw, sw, boxw) ||
       !make_map_nd(&mx, CU_TENSOR_MAP_DATA_TYPE_UINT8, g->x_q, 2, dx, sx, boxx))
     return SITU_ERR_CUDA;
+  if (tn == 256) {
+    const uint64_t el = p.out_f32 ? 4 : 2, dout[2] = {N, S}, so[1] = {(uint64_t)g->ldo * el};
+    const int row = cg == 1 ? WCfg<1, 1>::kRow : WCfg<2, 1>::kRow;
+    const uint32_t boxo[2] = {(uint32_t)(row / el), 32};
+    if (!make_map_nd(&mo, p.out_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, g->out, 2, dout, so,
+                     boxo, row == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B))
+      return SITU_ERR_CUDA;
+  }
   cudaStream_t st = (cudaStream_t)stream;
   const double most = most_tiles(g->S, g->E, tm) * p.n_mt;
   const long cap = most > 1e6 ? 1000000 : (long)most;
@@ -875,7 +916,8 @@ extern "C" situ_status situ_moe_fp8_gemm(const situ_fp8_gemm_args* g, void* stre
   else
     e = tn == 32   ? launch_t<32, false>(mw, mx, p, cap, st)
         : tn == 64 ? launch_t<64, false>(mw, mx, p, cap, st)
-        : cg == 1  ? launch_wide<1>(mx, mw, p, cap, st)
-                   : launch_wide<2>(mx, mw, p, cap, st);
+        : cg == 1  ? launch_wide<1, 1>(mx, mw, mo, p, cap, st)
+        : two      ? launch_wide<2, 2>(mx, mw, mo, p, cap, st)
+                   : launch_wide<2, 1>(mx, mw, mo, p, cap, st);
   return e == cudaSuccess ? SITU_OK : SITU_ERR_CUDA;
 }

@@ -396,7 +396,8 @@ inline bool bind_thread() {
 
 // dims[i] elements, stride[i - 1] bytes between elements of dims[i] (i >= 1)
 inline bool make_map_nd(CUtensorMap* m, CUtensorMapDataType dt, const void* base, int nd, const uint64_t* dims,
-                        const uint64_t* strides, const uint32_t* box) {
+                        const uint64_t* strides, const uint32_t* box,
+                        CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
   if (!fn || !bind_thread()) return false;
   const cuuint32_t estr[3] = {1, 1, 1};
@@ -408,7 +409,7 @@ inline bool make_map_nd(CUtensorMap* m, CUtensorMapDataType dt, const void* base
     if (i > 0) st[i - 1] = strides[i - 1];
   }
   return fn(m, dt, (cuuint32_t)nd, const_cast<void*>(base), d, st, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+            swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // SMs of the current device (looked up once per device)

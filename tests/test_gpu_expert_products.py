@@ -558,6 +558,31 @@ def test_every_form_of_the_fp8_product(counts, N, K):
         assert_sum(got, ref, mag, K, out_dtype)
 
 
+# Wide tiles write whole boxes of 32 rows and, at a group's end, single rows:
+# into a part of a larger array, what lies beside it and the rows of no expert
+# stay as they were.
+@pytest.mark.parametrize("counts,N,K", [
+    ([1100, 0, 2501, 33, 1600], 264, 256), ([1025, 31, 4000], 2184, 128),       # pairs, rows on lines
+    ([170, 0, 333, 32, 500], 1928, 144), ([900], 72, 1040),                    # pairs, rows off the lines
+    ([75, 0, 128, 129, 40, 190, 31], 2056, 256), ([1000, 20, 3, 0, 960], 136, 384)])   # one CTA
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+def test_fp8_wide_tiles_write_their_rows_only(counts, N, K, out_dtype):
+    S, start = sum(counts) + 9, 4
+    ops = fp8_operands(gen(N + K), S, len(counts), N, K)
+    ref, mag = fp8_reference(*ops, counts, start)
+    big = torch.full((S + 2, N + 24), 77.0, device="cuda", dtype=out_dtype)
+    out = big[1:1 + S, 8:8 + N]
+    got = B.situ_moe_fp8_grouped_gemm(*ops, offsets_of(counts, start), out=out, zero_rest=False)
+    assert got is out
+    end = start + sum(counts)
+    assert_sum(out[start:end], ref[start:end], mag[start:end], K, out_dtype)
+    assert (out[:start] == 77).all() and (out[end:] == 77).all()
+    assert (big[0] == 77).all() and (big[-1] == 77).all() and (big[:, :8] == 77).all() and (big[:, 8 + N:] == 77).all()
+    twice = B.situ_moe_fp8_grouped_gemm(*ops, offsets_of(counts, start))
+    again = B.situ_moe_fp8_grouped_gemm(*ops, offsets_of(counts, start))
+    assert torch.equal(twice, again)
+
+
 # Weights that are a part of a larger array are read where they lie: the same
 # bits as from a copy, and no copy made; what surrounds them is NaN.
 @pytest.mark.parametrize("counts,N,K", [([5, 0, 20], 264, 2064), ([90, 60, 0, 97], 1416, 208),
