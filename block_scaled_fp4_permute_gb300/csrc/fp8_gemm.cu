@@ -728,8 +728,13 @@ f8w_kernel(const __grid_constant__ CUtensorMap mapX, const __grid_constant__ CUt
       const WTile t = wide_tile_of<CG>(p, tp, idx);
       // through shared memory, kRow bytes of the warp's 32 rows at a time: whole
       // boxes by TMA, which takes them away while the next tile is promoted,
-      // and a group's last rows, next to another group's, by plain stores
+      // and a group's last rows, next to another group's, by plain stores.
+      // Boxes are used in turn and a tile takes a multiple of them; every use
+      // commits one group, empty where TMA reads nothing, so that all but the
+      // newest BOXES - 1 groups read means that the next box is free.
+      static_assert(C::kCols * 2 / C::kRow % BOXES == 0, "a tile's boxes");
       const int row0 = t.t0 + 128 * (int)rank + 32 * q, n0 = t.n0 + C::kCols * h;
+      if (row0 >= t.rows) continue;   // past the group's end: no rows, no boxes
       uint8_t* boxes = smem + C::kOffOut + (warp - kEpiWarp) * C::kOutBytes;
       auto store = [&](int i, int el, auto value) {
         uint8_t* box = boxes + C::kBoxBytes * (i % BOXES);
@@ -747,7 +752,6 @@ f8w_kernel(const __grid_constant__ CUtensorMap mapX, const __grid_constant__ CUt
                                reinterpret_cast<uint64_t>(&mapO)),
                            "r"(n), "r"(t.row0 + row0), "r"(saddr(box))
                            : "memory");
-            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
           }
         } else {
           constexpr int kCpr = C::kRow / 16;
@@ -762,6 +766,7 @@ f8w_kernel(const __grid_constant__ CUtensorMap mapX, const __grid_constant__ CUt
                   *reinterpret_cast<const uint4*>(box + box_at<C::kRow>(r, c));
           }
         }
+        if (lane == 0) asm volatile("cp.async.bulk.commit_group;" ::: "memory");
       };
       if (p.out_f32) {
 #pragma unroll
