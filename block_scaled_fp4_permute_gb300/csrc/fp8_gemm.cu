@@ -58,7 +58,7 @@ struct Cfg {
   static constexpr int kSPitch = TN + 8;                       // conflict-free rows
   static constexpr int kSlotBytes = 4 * kSG * (kSPitch + 1);
   static constexpr int kOutBytes = 8 * kBoxBytes;              // output staging
-  static constexpr int kMaxBytes = 232448 - 1024 - 4 * (kMaxGroups + 1) - 512 - kSlots * kSlotBytes - kOutBytes;
+  static constexpr int kMaxBytes = 232448 - 1024 - 4 * kScanInts - 512 - kSlots * kSlotBytes - kOutBytes;
   // 8 stages, 160 or 192 KB: all that fit at 32 tokens (10) made the HBM
   // slower (112 experts of 6144 x 3584: 0.267 ms, 8: 0.255, 6: 0.257)
   static constexpr int kStages = 8;
@@ -67,7 +67,7 @@ struct Cfg {
   static constexpr int kOffS = kOffB + kStages * kBBytes;
   static constexpr int kOffOut = kOffS + kSlots * kSlotBytes;
   static constexpr int kOffTp = kOffOut + kOutBytes;
-  static constexpr int kOffBar = (kOffTp + 4 * (kMaxGroups + 1) + 15) / 16 * 16;
+  static constexpr int kOffBar = (kOffTp + 4 * kScanInts + 15) / 16 * 16;
   static constexpr int kNumBars = 2 * kStages + kBufs + 1 + 2 * kSlots;
   static constexpr int kOffTm = kOffBar + 8 * kNumBars;
   static constexpr int kSmem = kOffTm + 16 + 1024;
@@ -87,9 +87,9 @@ __device__ __forceinline__ Tile tile_of(const F8Params& p, const int* tp, int id
   const int r = idx - tp[t.e] * p.n_mt, tt = tp[t.e + 1] - tp[t.e];
   t.mt = r / tt;
   t.c0 = (r - t.mt * tt) * TN;
-  const int2 g = group_rows(p.offsets, t.e, p.S);
-  t.row0 = g.x;
-  t.cols = min(TN, g.y - t.c0);
+  const int* row = tp + kMaxGroups + 1;
+  t.row0 = row[t.e];
+  t.cols = min(TN, row[t.e + 1] - t.row0 - t.c0);
   return t;
 }
 
@@ -116,16 +116,15 @@ __device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
   hi = __uint_as_float(b);
 }
 
-// zeros to the rows of no group; et: this thread's number among the CTA's
-// per_cta promoting threads
-__device__ __forceinline__ void zero_rest(const F8Params& p, int et, int per_cta) {
+// zeros to the rows of no group (row: scan_tiles'); et: this thread's number
+// among the CTA's per_cta promoting threads
+__device__ __forceinline__ void zero_rest(const F8Params& p, const int* row, int et, int per_cta) {
   if (!p.offsets || !p.zero_rest || *reinterpret_cast<volatile int*>(p.err) != 0) return;
   const long t = (long)blockIdx.x * per_cta + et, n = (long)gridDim.x * per_cta;
   const int el = p.out_f32 ? 4 : 2;
   uint8_t* out = reinterpret_cast<uint8_t*>(p.out);
-  const int2 last = group_rows(p.offsets, p.E - 1, p.S);
-  zero_rows(out, 0, group_rows(p.offsets, 0, p.S).x, (size_t)p.N * el, (size_t)p.ld_out * el, t, n);
-  zero_rows(out, last.x + last.y, p.S, (size_t)p.N * el, (size_t)p.ld_out * el, t, n);
+  zero_rows(out, 0, row[0], (size_t)p.N * el, (size_t)p.ld_out * el, t, n);
+  zero_rows(out, row[p.E], p.S, (size_t)p.N * el, (size_t)p.ld_out * el, t, n);
 }
 
 template <int TN, bool SPLIT>
@@ -166,7 +165,7 @@ f8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) tmem_alloc<1>(saddr(tm_holder), C::kTmemCols);
-  scan_tiles(p.offsets, p.E, p.S, TN, tp, kThreads);
+  scan_tiles(p.offsets, p.E, p.S, TN, tp, tp + kMaxGroups + 1, kThreads);
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -362,7 +361,7 @@ f8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
       }
       __syncwarp();
     }
-    zero_rest(p, et, kEpiThreads);
+    zero_rest(p, tp + kMaxGroups + 1, et, kEpiThreads);
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
@@ -429,13 +428,13 @@ struct WCfg {
   static constexpr int kRow = CG == 2 ? 128 : 64;
   static constexpr int kBoxBytes = 32 * kRow;
   static constexpr int kOutBytes = BOXES * kBoxBytes;
-  static constexpr int kMaxBytes = 232448 - 1024 - 4 * (kMaxGroups + 1) - 512 - kSlots * kSlotBytes - 4 * kWideParts * kOutBytes;
+  static constexpr int kMaxBytes = 232448 - 1024 - 4 * kScanInts - 512 - kSlots * kSlotBytes - 4 * kWideParts * kOutBytes;
   static constexpr int kStages = kMaxBytes / kStageBytes;
   static constexpr int kOffB = kStages * kABytes;
   static constexpr int kOffOut = kOffB + kStages * kBBytes;
   static constexpr int kOffS = kOffOut + 4 * kWideParts * kOutBytes;
   static constexpr int kOffTp = kOffS + kSlots * kSlotBytes;
-  static constexpr int kOffBar = (kOffTp + 4 * (kMaxGroups + 1) + 15) / 16 * 16;
+  static constexpr int kOffBar = (kOffTp + 4 * kScanInts + 15) / 16 * 16;
   // full, done[2] per stage; acc_empty[2][2]; drain[2]; scale slots full, empty
   static constexpr int kNumBars = 3 * kStages + 6 + 2 * kSlots;
   static constexpr int kOffTm = kOffBar + 8 * kNumBars;
@@ -456,9 +455,9 @@ __device__ __forceinline__ WTile wide_tile_of(const F8Params& p, const int* tp, 
   const int r = idx - tp[t.e] * p.n_mt, tt = tp[t.e + 1] - tp[t.e], nt = r / tt;
   t.t0 = (r - nt * tt) * C::kTM;   // a group's token tiles run side by side: they read the same weights
   t.n0 = nt * C::kTN;
-  const int2 g = group_rows(p.offsets, t.e, p.S);
-  t.row0 = g.x;
-  t.rows = g.y;
+  const int* row = tp + kMaxGroups + 1;
+  t.row0 = row[t.e];
+  t.rows = row[t.e + 1] - t.row0;
   t.cols = min(C::kTN, p.N - t.n0);
   return t;
 }
@@ -543,7 +542,7 @@ f8w_kernel(const __grid_constant__ CUtensorMap mapX, const __grid_constant__ CUt
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) tmem_alloc<CG>(saddr(tm_holder), 512);
-  scan_tiles(p.offsets, p.E, p.S, C::kTM, tp, kWideThreads);
+  scan_tiles(p.offsets, p.E, p.S, C::kTM, tp, tp + kMaxGroups + 1, kWideThreads);
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   if (CG == 2) cluster_sync();
@@ -789,7 +788,7 @@ f8w_kernel(const __grid_constant__ CUtensorMap mapX, const __grid_constant__ CUt
       }
     }
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-    zero_rest(p, et, 128 * kWideParts);
+    zero_rest(p, tp + kMaxGroups + 1, et, 128 * kWideParts);
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();

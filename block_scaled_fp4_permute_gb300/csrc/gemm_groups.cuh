@@ -5,9 +5,13 @@
 // Rows are sorted by expert: group e holds rows [offsets[e], offsets[e + 1]).
 // The offsets live on the device (the permute writes them), so the host never
 // sees them: grids are sized for the GPU, and every CTA scans the groups'
-// tile counts into shared memory once and walks its share of the tiles.
-// Offsets are clamped to [0, S] and to ascending order before use, so that no
-// content of the array can address outside the operands.
+// bounds and tile counts into shared memory once and walks its share of the
+// tiles (the weight gradient, whose tiles do not depend on the rows and whose
+// shared memory is full, reads the bounds of each tile).
+// Offsets are clamped to [0, S] and to ascending order before use: group e
+// starts at the largest of offsets[0..e] and ends at the largest of
+// offsets[0..e + 1].  So whatever the array holds, the groups are disjoint,
+// lie inside the operands and have S rows together at most.
 #pragma once
 #include "situ_internal.h"
 #include "tc_common.cuh"
@@ -17,26 +21,68 @@ namespace gg {
 
 using namespace tc;
 
-constexpr int kMaxGroups = 1024;   // tile prefix in shared memory, 4 KB
+constexpr int kMaxGroups = 1024;
+constexpr int kScanInts = 2 * (kMaxGroups + 1);   // of a scan in shared memory
 constexpr int64_t kMaxStride = int64_t(1) << 39;   // elements; the tensor maps' own limit is 2^40 bytes
 
-__device__ __forceinline__ int2 group_rows(const int32_t* off, int e, int S) {
-  if (off == nullptr) return make_int2(0, S);   // one dense group
-  const int b = min(max(__ldg(off + e), 0), S);
-  return make_int2(b, min(max(__ldg(off + e + 1), b), S) - b);   // (first row, rows)
+__host__ __device__ __forceinline__ int offset_at(const int32_t* off, int i, int S) {
+#ifdef __CUDA_ARCH__
+  const int v = __ldg(off + i);
+#else
+  const int v = off[i];
+#endif
+  return v < 0 ? 0 : v < S ? v : S;
+}
+// (first row, rows) of group e; ascending offsets, the usual case, need no
+// look at the groups before
+__host__ __device__ __forceinline__ int2 group_rows(const int32_t* off, int e, int S, bool ascending) {
+  int b = offset_at(off, e, S);
+  const int end = offset_at(off, e + 1, S);
+  if (!ascending) {
+#pragma unroll 1
+    for (int i = 0; i < e; ++i) {
+      const int o = offset_at(off, i, S);
+      b = o > b ? o : b;
+    }
+  }
+  return make_int2(b, end > b ? end - b : 0);
+}
+// Whether the offsets that this one of the block's `threads` threads looks at ascend.
+__device__ __forceinline__ bool offsets_ascend(const int32_t* off, int E, int S, int threads) {
+  bool ok = true;
+  for (int e = threadIdx.x; e < E; e += threads) ok = ok && offset_at(off, e, S) <= offset_at(off, e + 1, S);
+  return ok;
 }
 
-// tp[e] = token tiles of the groups before e, tp[E] = all of them (E <=
-// kMaxGroups).  Called by all `threads` threads of the block; ends synced.
-__device__ __forceinline__ void scan_tiles(const int32_t* off, int E, int S, int tile, int* tp, int threads) {
+// tp[e] = token tiles of the groups before e, tp[E] = all of them; row[e] =
+// the first row of e, row[E] = the end of the last (E <= kMaxGroups).  Called
+// by all `threads` threads of the block; ends synced.
+__device__ __forceinline__ void scan_tiles(const int32_t* off, int E, int S, int tile, int* tp, int* row, int threads) {
   __shared__ int warp_sum[32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (off == nullptr) {   // one dense group
+    if (tid == 0) {
+      tp[0] = row[0] = 0;
+      tp[1] = (S + tile - 1) / tile;
+      row[1] = S;
+    }
+    __syncthreads();
+    return;
+  }
   const int per = (E + threads - 1) / threads;
   int cnt[(kMaxGroups + 255) / 256], sum = 0;   // blocks here have at least 256 threads
+  bool ok = true;
 #pragma unroll
   for (int j = 0; j < (kMaxGroups + 255) / 256; ++j) {
     const int e = tid * per + j;
-    cnt[j] = (j < per && e < E) ? (group_rows(off, e, S).y + tile - 1) / tile : 0;
+    cnt[j] = 0;
+    if (j < per && e < E) {
+      const int from = offset_at(off, e, S), to = offset_at(off, e + 1, S);
+      row[e] = from;
+      if (e == E - 1) row[E] = to;
+      ok = ok && from <= to;
+      cnt[j] = (to - from + tile - 1) / tile;
+    }
     sum += cnt[j];
   }
   int inc = sum;
@@ -46,7 +92,7 @@ __device__ __forceinline__ void scan_tiles(const int32_t* off, int E, int S, int
     if (lane >= d) inc += o;
   }
   if (lane == 31) warp_sum[warp] = inc;
-  __syncthreads();
+  const bool ascending = __syncthreads_and(ok);
   int base = 0;
   for (int w = 0; w < warp; ++w) base += warp_sum[w];
   int run = base + inc - sum;
@@ -58,6 +104,17 @@ __device__ __forceinline__ void scan_tiles(const int32_t* off, int E, int S, int
   }
   if (tid == threads - 1) tp[E] = base + inc;
   __syncthreads();
+  if (!ascending) {   // counted anew from the clamped order, by one thread
+    if (tid == 0) {
+      tp[0] = 0;
+#pragma unroll 1
+      for (int e = 0; e < E; ++e) {
+        row[e + 1] = max(row[e + 1], row[e]);
+        tp[e + 1] = tp[e] + (row[e + 1] - row[e] + tile - 1) / tile;
+      }
+    }
+    __syncthreads();
+  }
 }
 
 // the group of token tile v: the largest e with tp[e] <= v (v < tp[E])

@@ -80,9 +80,10 @@ struct Cfg {
   static constexpr int kBBytes = kTNB * 128;
   static constexpr int kStageBytes = kABytes + kBBytes;
   // output staging of the eight epilogue warps: wgrad 4 KB boxes (and no
-  // tile prefix), else 32 tokens x 32 elements at a pitch without conflicts
-  static constexpr int kOutBytes = MODE == kWgrad ? 8 * 4096 : 8 * 32 * kOutPitch;
-  static constexpr int kTpBytes = MODE == kWgrad ? 0 : 4 * (kMaxGroups + 1);
+  // scan), else 32 tokens x 32 elements at a pitch without conflicts (tiles of
+  // 32 tokens: four of the warps)
+  static constexpr int kOutBytes = MODE == kWgrad ? 8 * 4096 : (TN > 32 ? 8 : 4) * 32 * kOutPitch;
+  static constexpr int kTpBytes = MODE == kWgrad ? 0 : 4 * kScanInts;
   static constexpr int kMaxBytes = 232448 - 1024 - kTpBytes - kOutBytes - 512;
   static constexpr int kStages = kMaxBytes / kStageBytes;
   static constexpr int kOffB = kStages * kABytes;
@@ -113,6 +114,7 @@ struct Tile {
   int nk;              // stages
 };
 
+// tp: what scan_tiles wrote, first tiles and then rows; wgrad: whether the offsets ascend
 template <int CG, int MODE, int TN>
 __device__ __forceinline__ Tile tile_of(const GgParams& p, const int* tp, int idx) {
   Tile t;
@@ -123,7 +125,7 @@ __device__ __forceinline__ Tile tile_of(const GgParams& p, const int* tp, int id
     const int r = idx - t.e * per;
     mt = r / p.n_nt;
     t.c0 = (r - mt * p.n_nt) * TN;
-    const int2 g = group_rows(p.offsets, t.e, p.S);
+    const int2 g = group_rows(p.offsets, t.e, p.S, tp[0] != 0);
     t.row0 = g.x;
     t.rows = g.y;
     t.cols = min(TN, p.Ncol - t.c0);
@@ -133,9 +135,9 @@ __device__ __forceinline__ Tile tile_of(const GgParams& p, const int* tp, int id
     const int r = idx - tp[t.e] * p.n_mt, tt = tp[t.e + 1] - tp[t.e];
     mt = r / tt;   // a group's token tiles run side by side: they read the same weights
     t.c0 = (r - mt * tt) * TN;
-    const int2 g = group_rows(p.offsets, t.e, p.S);
-    t.row0 = g.x;
-    t.rows = g.y;
+    const int* row = tp + kMaxGroups + 1;
+    t.row0 = row[t.e];
+    t.rows = row[t.e + 1] - t.row0;
     t.cols = min(TN, t.rows - t.c0);
     t.nk = (p.L + kBK - 1) / kBK;
   }
@@ -220,7 +222,7 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
   static_assert(!SPLIT || (CG == 1 && SUMS), "split tiles");
   const int part = SPLIT ? (int)cluster_rank() : 0, parts = SPLIT ? (int)cluster_size() : 1;
   const uint32_t sbase = saddr(smem);
-  int* tp = reinterpret_cast<int*>(smem + C::kOffTp);
+  int* tp = reinterpret_cast<int*>(smem + (MODE == kWgrad ? C::kOffTm + 4 : C::kOffTp));
   const uint32_t bar0 = sbase + C::kOffBar;
   auto full = [&](int s) { return bar0 + 8 * s; };
   auto empty = [&](int s) { return bar0 + 8 * (C::kStages + s); };
@@ -245,9 +247,12 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) tmem_alloc<CG>(saddr(tm_holder), C::kTmemCols);
-  if (MODE != kWgrad) scan_tiles(p.offsets, p.E, p.S, TN, tp, kThreads);
+  bool ascend = true;
+  if (MODE == kWgrad) ascend = offsets_ascend(p.offsets, p.E, p.S, kThreads);
+  else scan_tiles(p.offsets, p.E, p.S, TN, tp, tp + kMaxGroups + 1, kThreads);
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-  __syncthreads();
+  if (MODE == kWgrad) tp[0] = __syncthreads_and(ascend);   // each thread writes it, the same: a register would be spilled
+  else __syncthreads();
   if (CG == 2) cluster_sync();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = *tm_holder;
@@ -606,9 +611,9 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
       const long t = (long)blockIdx.x * kEpiThreads + tid - 32 * kEpiWarp, n = (long)gridDim.x * kEpiThreads;
       const int el = p.out_f32 ? 4 : 2;
       uint8_t* out = reinterpret_cast<uint8_t*>(p.out);
-      const int2 last = group_rows(p.offsets, p.E - 1, p.S);
-      zero_rows(out, 0, group_rows(p.offsets, 0, p.S).x, (size_t)p.M * el, (size_t)p.ld_out * el, t, n);
-      zero_rows(out, last.x + last.y, p.S, (size_t)p.M * el, (size_t)p.ld_out * el, t, n);
+      const int* row = tp + kMaxGroups + 1;
+      zero_rows(out, 0, row[0], (size_t)p.M * el, (size_t)p.ld_out * el, t, n);
+      zero_rows(out, row[p.E], p.S, (size_t)p.M * el, (size_t)p.ld_out * el, t, n);
     }
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");

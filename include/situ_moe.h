@@ -506,9 +506,10 @@ situ_status situ_moe_pack_scales(const situ_moe_args* args, void* packed, size_t
  * or whose checkpoint holds E4M3 weights with one fp32 scale per block of
  * 128.  Rows of local expert e are [offsets[e], offsets[e + 1]), offsets an
  * int32 [E + 1] device array in ascending order (situ_moe_permute's
- * expert_offsets); entries are clamped to [0, S] on the device.  Rows before
- * offsets[0] and from offsets[E] on belong to no expert: their output rows
- * are set to zero, unless keep_rest = 1 leaves them as they are.
+ * expert_offsets); on the device entries are clamped to [0, S] and to
+ * ascending order (each to the largest up to it).  Rows before offsets[0] and
+ * from offsets[E] on belong to no expert: their output rows are set to zero,
+ * unless keep_rest = 1 leaves them as they are.
  *
  * Each of these kernels bounds its waits as the layer's do; one that gives
  * up records a nonzero code in *device_status (one int32 in device memory,

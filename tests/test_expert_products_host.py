@@ -1,0 +1,54 @@
+"""What the expert products' kernels decide in plain arithmetic, compiled for
+the host and run on the CPU."""
+import os
+import random
+import subprocess
+
+
+from block_scaled_fp4_permute_gb300 import build
+
+ROWS = r"""
+#include <cstdio>
+#include <vector>
+#include "gemm_groups.cuh"
+int main() {
+  int S, E;
+  while (scanf("%d %d", &S, &E) == 2) {
+    std::vector<int32_t> off(E + 1);
+    for (auto& o : off) scanf("%d", &o);
+    bool asc = true;
+    for (int e = 0; e < E; ++e) asc = asc && situ::gg::offset_at(off.data(), e, S) <= situ::gg::offset_at(off.data(), e + 1, S);
+    for (int e = 0; e < E; ++e) {
+      const int2 g = situ::gg::group_rows(off.data(), e, S, asc);
+      printf("%d %d ", g.x, g.y);
+    }
+    printf("\n");
+  }
+}
+"""
+
+
+def run(tmp_path, source, text):
+    src, exe = tmp_path / "host.cu", tmp_path / "host"
+    src.write_text(source)
+    subprocess.run([build._nvcc(), *build.ARCH, "-std=c++17", "--expt-relaxed-constexpr", "-I", build.CSRC, "-I",
+                    os.path.join(build.ROOT, "include"), "-o", str(exe), str(src)], check=True, capture_output=True)
+    return subprocess.run([str(exe)], input=text, check=True, capture_output=True, text=True).stdout
+
+
+def test_groups_are_disjoint_whatever_the_offsets_hold(tmp_path):
+    rng = random.Random(1)
+    cases = [(50, [0, 10, 5, 2000000000, 60]), (50, [50, 0, 50, 0, 50, 0]), (7, [-3, -2147483648, 2147483647]), (0, [0, 5, 0]),
+             (100, [0, 30, 30, 31, 100]), (1 << 30, [0, 1 << 30, 0, 1 << 30, 0, 2147483647])]
+    for _ in range(300):
+        S, E = rng.randrange(0, 60), rng.randrange(1, 9)
+        off = [rng.randrange(-10, 70) for _ in range(E + 1)]
+        cases.append((S, sorted(off) if rng.random() < 0.3 else off))
+    text = "".join(f"{S} {len(off) - 1} {' '.join(map(str, off))}\n" for S, off in cases)
+    lines = run(tmp_path, ROWS, text).splitlines()
+    assert len(lines) == len(cases)
+    for (S, off), line in zip(cases, lines):
+        v = list(map(int, line.split()))
+        at = [min(max(o, 0), S) for o in off]
+        bound = [max(at[:i + 1]) for i in range(len(at))]
+        assert v == [x for e in range(len(off) - 1) for x in (bound[e], bound[e + 1] - bound[e])]

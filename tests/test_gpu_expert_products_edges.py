@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from block_scaled_fp4_permute_gb300 import binding as B, build
-from test_gpu_expert_products import fp8_operands, gen, offsets_of
+from test_gpu_expert_products import fp8_operands, gen, normal, offsets_of
 
 pytestmark = pytest.mark.gpu
 
@@ -37,3 +37,33 @@ def test_fp8_output_boxes_in_turn(counts, N, K, out_dtype):
     assert torch.isfinite(want).all()
     for _ in range(8):
         assert torch.equal(B.situ_moe_fp8_grouped_gemm(xq, xs, wq, ws, off, out_dtype=out_dtype), want)
+
+
+# Offsets that descend or leave [0, S] are clamped to ascending order: the
+# results are those of the clamped array, and the same on every call.  Groups
+# taken pair by pair would overlap here, with more tiles than a split launch
+# (few tiles) has clusters.
+BAD_OFFSETS = [[0, 10, 5, 2000000000, 60], [50, 0, 50, 0, 50, 0, 50], [-7, -2147483648, 3, 2, 9], [40, 30, 20, 10],
+               [0, 1 << 30, 0, 2147483647, -1]]
+
+
+@pytest.mark.parametrize("bad", BAD_OFFSETS + [[(37 * i) % 1200 - 100 for i in range(1025)]])
+@pytest.mark.parametrize("S,N,K", [(50, 264, 2064), (900, 136, 144), (1500, 2056, 128)])
+def test_offsets_are_clamped_to_ascending_order(bad, S, N, K):
+    E = len(bad) - 1
+    if E > 100:
+        N = 136
+    off = torch.tensor(bad, dtype=torch.int32, device="cuda")
+    ok = torch.cummax(off.clamp(0, S), 0).values.int()
+    g = gen(S + E)
+    x, dy, w = normal(g, S, K), normal(g, S, N), normal(g, E, N, K, std=0.1)
+    fp8 = fp8_operands(g, S, E, N, K)
+    for out_dtype in (torch.bfloat16, torch.float32):
+        for f in (lambda o: B.situ_moe_grouped_gemm(x, w, o, out_dtype=out_dtype),
+                  lambda o: B.situ_moe_grouped_gemm_dgrad(dy, w, o, out_dtype=out_dtype),
+                  lambda o: B.situ_moe_grouped_gemm_wgrad(dy, x, o, out_dtype=out_dtype),
+                  lambda o: B.situ_moe_fp8_grouped_gemm(*fp8, o, out_dtype=out_dtype)):
+            want = f(ok)
+            assert torch.isfinite(want).all()
+            for _ in range(3):
+                assert torch.equal(f(off), want)
