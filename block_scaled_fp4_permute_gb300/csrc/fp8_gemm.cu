@@ -148,8 +148,9 @@ f8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
   const uint32_t drain = bar0 + 8 * (2 * C::kStages + C::kBufs + 2 * C::kSlots);
   uint32_t* tm_holder = reinterpret_cast<uint32_t*>(smem + C::kOffTm);
 
-  const int failed = *reinterpret_cast<volatile int*>(p.err);   // an earlier launch gave up a wait: no work then
+  int status = 0;   // an earlier launch gave up a wait: no work then; read once, so that all warps do the same
   if (tid == 0) {
+    status = *reinterpret_cast<volatile int*>(p.err);
     prefetch_map(&mapA);
     prefetch_map(&mapB);
     for (int s = 0; s < C::kStages; ++s) {
@@ -166,13 +167,14 @@ f8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
   }
   if (warp == 1) tmem_alloc<1>(saddr(tm_holder), C::kTmemCols);
   scan_tiles(p.offsets, p.E, p.S, TN, tp, tp + kMaxGroups + 1, kThreads);
+  if (tid == 0) tm_holder[2] = (uint32_t)status;
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = *tm_holder;
 
   int total = tp[p.E] * p.n_mt;
-  if (failed != 0) total = 0;
+  if (tm_holder[2] != 0) total = 0;
   const int first = blockIdx.x / parts, stride = gridDim.x / parts;
 
   if (warp < kEpiWarp) {
@@ -198,11 +200,9 @@ f8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
           __syncwarp();
         }
       }
-      if (ok) {   // the last arrivals on this CTA's barriers, before it may leave
-        for (int j = 0; j < r.used; ++j) warp_wait(done(j), j < r.s ? r.ph : r.ph ^ 1, p.err, 82);
-      } else {   // copies in flight
-        for (int j = 0; j < r.used; ++j) drain_wait(full(j), j < r.s ? r.ph : r.ph ^ 1);
-      }
+      leave(
+          ok, [&] { return last_uses(r, [&](int j, uint32_t ph) { return warp_wait(done(j), ph, p.err, 82); }); },
+          [&] { last_uses(r, [&](int j, uint32_t ph) { return drain_wait(full(j), ph); }); });
     } else if (warp == 1) {
       // ---------------- MMAs ----------------
       const bool leader = elect_one();
@@ -232,11 +232,13 @@ f8_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
           __syncwarp();
         }
       }
-      if (!ok) {   // MMAs in flight
-        if (leader) commit<1>(drain);
-        __syncwarp();
-        drain_wait(drain, 0);
-      }
+      leave(
+          ok, [&] { return last_use(r, [&](int j, uint32_t ph) { return warp_wait(done(j), ph, p.err, 88); }); },
+          [&] {
+            if (leader) commit<1>(drain);
+            __syncwarp();
+            drain_wait(drain, 0);
+          });
     } else {
       // ---------------- scales ----------------
       Ring<C::kSlots> sr;
@@ -519,8 +521,9 @@ f8w_kernel(const __grid_constant__ CUtensorMap mapX, const __grid_constant__ CUt
   auto sc_empty = [&](int i) { return bar0 + 8 * (3 * C::kStages + 6 + C::kSlots + i); };
   uint32_t* tm_holder = reinterpret_cast<uint32_t*>(smem + C::kOffTm);
 
-  const int failed = *reinterpret_cast<volatile int*>(p.err);   // an earlier launch gave up a wait: no work then
+  int status = 0;   // an earlier launch gave up a wait: no work then; read once, so that all warps do the same
   if (tid == 0) {
+    status = *reinterpret_cast<volatile int*>(p.err);
     prefetch_map(&mapX);
     prefetch_map(&mapW);
     prefetch_map(&mapO);
@@ -543,6 +546,7 @@ f8w_kernel(const __grid_constant__ CUtensorMap mapX, const __grid_constant__ CUt
   }
   if (warp == 1) tmem_alloc<CG>(saddr(tm_holder), 512);
   scan_tiles(p.offsets, p.E, p.S, C::kTM, tp, tp + kMaxGroups + 1, kWideThreads);
+  if (tid == 0) tm_holder[2] = (uint32_t)status;
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   if (CG == 2) cluster_sync();
@@ -550,7 +554,7 @@ f8w_kernel(const __grid_constant__ CUtensorMap mapX, const __grid_constant__ CUt
   const uint32_t tmem = *tm_holder;
 
   int total = tp[p.E] * p.n_mt;
-  if (failed != 0) total = 0;
+  if (tm_holder[2] != 0) total = 0;
   const int first = blockIdx.x / CG, stride = gridDim.x / CG;
 
   const bool xvec = (p.nkb & 3) == 0 && ((reinterpret_cast<uintptr_t>(p.xs) | reinterpret_cast<uintptr_t>(p.ws)) & 15) == 0;
@@ -583,18 +587,18 @@ f8w_kernel(const __grid_constant__ CUtensorMap mapX, const __grid_constant__ CUt
           __syncwarp();
         }
       }
-      if (ok) {   // the last arrivals on this CTA's barriers, before it may leave
-        for (int j = 0; j < r.used; ++j) {
-          warp_wait(done(0, j), j < r.s ? r.ph : r.ph ^ 1, p.err, 92);
-          warp_wait(done(1, j), j < r.s ? r.ph : r.ph ^ 1, p.err, 92);
-        }
-      } else if (rank == 0) {   // copies in flight
-        for (int j = 0; j < r.used; ++j) drain_wait(full(j), j < r.s ? r.ph : r.ph ^ 1);
-      } else {
-        const unsigned long long t0 = globaltimer();   // they complete on the other CTA's barriers
-        while (globaltimer() - t0 < 2000000ull) {
-        }
-      }
+      leave(
+          ok,
+          [&] {
+            return last_uses(r, [&](int j, uint32_t ph) {
+              const bool first_half = warp_wait(done(0, j), ph, p.err, 92);
+              return warp_wait(done(1, j), ph, p.err, 92) && first_half;
+            });
+          },
+          [&] {
+            if (rank == 0) last_uses(r, [&](int j, uint32_t ph) { return drain_wait(full(j), ph); });
+            else pause_2ms();
+          });
     } else if (warp <= 2) {
       // ---------------- MMAs ----------------
       // A warp per half: the waits and the commit of a product take an issuer
@@ -631,11 +635,13 @@ f8w_kernel(const __grid_constant__ CUtensorMap mapX, const __grid_constant__ CUt
             __syncwarp();
           }
         }
-        if (!ok) {   // MMAs in flight
-          if (leader) commit<CG>(drain(h));
-          __syncwarp();
-          drain_wait(drain(h), 0);
-        }
+        leave(
+            ok, [&] { return last_use(r, [&](int j, uint32_t ph) { return warp_wait(done(h, j), ph, p.err, 98); }); },
+            [&] {
+              if (leader) commit<CG>(drain(h));
+              __syncwarp();
+              drain_wait(drain(h), 0);
+            });
       }
     } else {
       // ---------------- scales ----------------

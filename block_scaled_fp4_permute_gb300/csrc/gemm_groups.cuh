@@ -315,7 +315,7 @@ struct Ring {
   int s = 0;
   uint32_t ph = 0;
   int used = 0;   // steps taken, up to N
-  __device__ __forceinline__ void next() {
+  __host__ __device__ __forceinline__ void next() {
     if (used < N) ++used;
     if (++s == N) {
       s = 0;
@@ -327,10 +327,41 @@ struct Ring {
 // Bounded wait (kWaitNs) for what this CTA itself put in flight, on the way
 // out after a failure; unlike mbar_wait it does not give up on another CTA's
 // error.
-__device__ __forceinline__ void drain_wait(uint32_t a, uint32_t parity) {
+__device__ __forceinline__ bool drain_wait(uint32_t a, uint32_t parity) {
   const unsigned long long t0 = globaltimer();
   while (!mbar_try(a, parity))
-    if (globaltimer() - t0 > kWaitNs) return;
+    if (globaltimer() - t0 > kWaitNs) return false;
+  return true;
+}
+
+// wait(stage, parity) for the last use of each stage of a ring; whether all came
+template <int N, class Wait>
+__host__ __device__ __forceinline__ bool last_uses(const Ring<N>& r, Wait&& wait) {
+  bool ok = true;
+  for (int j = 0; j < r.used; ++j) ok = wait(j, j < r.s ? r.ph : r.ph ^ 1) && ok;
+  return ok;
+}
+// the same for the ring's last stage alone: it stands for all where each use
+// ends after those before it, as MMAs committed by one thread do
+template <int N, class Wait>
+__host__ __device__ __forceinline__ bool last_use(const Ring<N>& r, Wait&& wait) {
+  return r.used == 0 || (r.s > 0 ? wait(r.s - 1, r.ph) : wait(N - 1, r.ph ^ 1));
+}
+// How a warp that puts copies or MMAs in flight leaves: ok, it has been through
+// all of its stages, and then arrived() tells whether their last uses are over.
+// If a wait was given up, here or before (an error of any CTA ends them all),
+// that is not known, and drain() waits for what this warp has in flight, so that
+// none of it reaches into shared memory or TMEM that is no longer the CTA's.
+template <class Arrived, class Drain>
+__host__ __device__ __forceinline__ void leave(bool ok, Arrived&& arrived, Drain&& drain) {
+  if (ok) ok = arrived();
+  if (!ok) drain();
+}
+// drain() of copies that complete on the other CTA's barriers
+__device__ __forceinline__ void pause_2ms() {
+  const unsigned long long t0 = globaltimer();
+  while (globaltimer() - t0 < 2000000ull) {
+  }
 }
 
 // tcgen05.ld of 32 columns, without the wait

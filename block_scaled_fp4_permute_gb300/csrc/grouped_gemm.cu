@@ -231,8 +231,9 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
   const uint32_t drain = bar0 + 8 * (2 * C::kStages + 4);
   uint32_t* tm_holder = reinterpret_cast<uint32_t*>(smem + C::kOffTm);
 
-  const int failed = *reinterpret_cast<volatile int*>(p.err);   // an earlier launch gave up a wait: no work then
+  int status = 0;   // an earlier launch gave up a wait: no work then; read once, so that all warps do the same
   if (tid == 0) {
+    status = *reinterpret_cast<volatile int*>(p.err);
     prefetch_map(&mapA);
     prefetch_map(&mapB);
     for (int s = 0; s < C::kStages; ++s) {
@@ -250,6 +251,7 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
   bool ascend = true;
   if (MODE == kWgrad) ascend = offsets_ascend(p.offsets, p.E, p.S, kThreads);
   else scan_tiles(p.offsets, p.E, p.S, TN, tp, tp + kMaxGroups + 1, kThreads);
+  if (tid == 0) tm_holder[2] = (uint32_t)status;
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   if (MODE == kWgrad) tp[0] = __syncthreads_and(ascend);   // each thread writes it, the same: a register would be spilled
   else __syncthreads();
@@ -258,7 +260,7 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
   const uint32_t tmem = *tm_holder;
 
   int total = MODE == kWgrad ? p.E * p.n_mt * p.n_nt : tp[p.E] * p.n_mt;
-  if (failed != 0) total = 0;
+  if (tm_holder[2] != 0) total = 0;
   const int first = blockIdx.x / (CG * parts), stride = gridDim.x / (CG * parts);
   // a split tile's CTAs take neighbouring ranges of its stages
   auto stage_from = [&](const Tile& t) { return SPLIT ? t.nk * part / parts : 0; };
@@ -331,15 +333,12 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
           __syncwarp();
         }
       }
-      if (ok) {   // the last arrivals on this CTA's barriers, before it may leave
-        for (int j = 0; j < r.used; ++j) warp_wait(empty(j), j < r.s ? r.ph : r.ph ^ 1, p.err, 72);
-      } else if (rank == 0) {   // copies in flight
-        for (int j = 0; j < r.used; ++j) drain_wait(full(j), j < r.s ? r.ph : r.ph ^ 1);
-      } else {
-        const unsigned long long t0 = globaltimer();   // they complete on the other CTA's barriers
-        while (globaltimer() - t0 < 2000000ull) {
-        }
-      }
+      leave(
+          ok, [&] { return last_uses(r, [&](int j, uint32_t ph) { return warp_wait(empty(j), ph, p.err, 72); }); },
+          [&] {
+            if (rank == 0) last_uses(r, [&](int j, uint32_t ph) { return drain_wait(full(j), ph); });
+            else pause_2ms();
+          });
     } else if (warp == 1 && rank == 0) {
       // ---------------- MMAs ----------------
       const bool leader = elect_one();
@@ -390,11 +389,13 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
           k0 = k1;
         }
       }
-      if (!ok) {   // MMAs in flight
-        if (leader) commit<CG>(drain);
-        __syncwarp();
-        drain_wait(drain, 0);
-      }
+      leave(
+          ok, [&] { return last_use(r, [&](int j, uint32_t ph) { return warp_wait(empty(j), ph, p.err, 76); }); },
+          [&] {
+            if (leader) commit<CG>(drain);
+            __syncwarp();
+            drain_wait(drain, 0);
+          });
     }
   } else {
     // ---------------- epilogue ----------------

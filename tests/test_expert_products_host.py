@@ -52,3 +52,43 @@ def test_groups_are_disjoint_whatever_the_offsets_hold(tmp_path):
         at = [min(max(o, 0), S) for o in off]
         bound = [max(at[:i + 1]) for i in range(len(at))]
         assert v == [x for e in range(len(off) - 1) for x in (bound[e], bound[e + 1] - bound[e])]
+
+LEAVE = r"""
+#include <cstdio>
+#include "gemm_groups.cuh"
+int main() {
+  // steps through a ring of three, whether the warp got through, the stage whose last arrival fails (-1: none)
+  int steps, ok, fails;
+  while (scanf("%d %d %d", &steps, &ok, &fails) == 3) {
+    situ::gg::Ring<3> r;
+    for (int i = 0; i < steps; ++i) r.next();
+    auto arrived = [&](int j, uint32_t ph) {
+      printf("a%d%u ", j, ph);
+      return j != fails;
+    };
+    auto drain = [&] {
+      situ::gg::last_uses(r, [&](int j, uint32_t ph) {
+        printf("d%d%u ", j, ph);
+        return false;
+      });
+    };
+    situ::gg::leave(ok != 0, [&] { return situ::gg::last_uses(r, arrived); }, drain);
+    printf("\n");
+    situ::gg::leave(ok != 0, [&] { return situ::gg::last_use(r, arrived); }, drain);
+    printf("\n");
+  }
+}
+"""
+
+
+def test_a_warp_drains_what_it_has_in_flight_unless_all_of_it_arrived(tmp_path):
+    cases = [(steps, ok, fails) for steps in range(9) for ok in (0, 1) for fails in range(-1, 3)]
+    lines = run(tmp_path, LEAVE, "".join("%d %d %d\n" % c for c in cases)).split("\n")
+    for (steps, ok, fails), every, newest in zip(cases, lines[0::2], lines[1::2]):
+        last = {i % 3: i // 3 % 2 for i in range(steps)}       # stage: parity of its last use
+        drained = [f"d{j}{last[j]}" for j in sorted(last)]
+        arrived = [f"a{j}{last[j]}" for j in sorted(last)] if ok else []
+        assert every.split() == arrived + (drained if not ok or fails in last else []), (steps, ok, fails)
+        j = (steps - 1) % 3
+        arrived = [f"a{j}{last[j]}"] if ok and steps else []
+        assert newest.split() == arrived + (drained if not ok or (steps and fails == j) else []), (steps, ok, fails)
