@@ -34,6 +34,14 @@ struct In {
 #pragma unroll
     for (int i = 0; i < kVec; ++i) v[i] = __ldg(q + i);
   }
+  // the signs of elements 4h to 4h + 3 at the tops of four bytes
+  __device__ __forceinline__ uint32_t signs(int h) const {
+    const uint4& u = v[DT == SITU_DT_F32 ? h : 0];
+    uint32_t w;
+    if (DT == SITU_DT_F32) w = __byte_perm(__byte_perm(u.x, u.y, 0x0073), __byte_perm(u.z, u.w, 0x0073), 0x5410);
+    else w = h == 0 ? __byte_perm(u.x, u.y, 0x7531) : __byte_perm(u.z, u.w, 0x7531);
+    return w & 0x80808080u;
+  }
   // elements 2j and 2j + 1
   __device__ __forceinline__ void pair(int j, float& a, float& b) const {
     const uint4& u = v[DT == SITU_DT_F32 ? j >> 1 : 0];
@@ -73,7 +81,8 @@ __device__ __forceinline__ float amax_value(uint32_t m) {
 // (Markstein, "Computation of elementary functions on the IBM RISC
 // System/6000 processor", 1990).  Needs s in [2^-80, inf): the residuals of
 // any quotient of at least 2^-20 are then exact, and a smaller one becomes
-// the code 0 all the same.  As packed pairs that is 2.5 instructions an
+// the code 0 all the same.  A zero loses its sign in the residual (-0 gives
+// +0 - 0): the codes take x's.  As packed pairs that is 2.5 instructions an
 // element; with divisions the kernels were bound by issue slots.
 __device__ __forceinline__ float quotient(float x, float s, float r) {
   float q = x * r;
@@ -129,6 +138,7 @@ __device__ __forceinline__ uint2 codes(const In<DT>& in, const Scale& sc) {
       asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(q));
       c[i] = f32x2_to_e4m3x2(a, b);
     }
+    return make_uint2(c[0] | (c[1] << 16) | in.signs(0), c[2] | (c[3] << 16) | in.signs(1));
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {

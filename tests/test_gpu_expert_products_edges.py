@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from block_scaled_fp4_permute_gb300 import binding as B, build
-from test_gpu_expert_products import fp8_operands, gen, normal, offsets_of
+from test_gpu_expert_products import fp8_operands, gen, normal, offsets_of, plain_quant
 
 pytestmark = pytest.mark.gpu
 
@@ -67,3 +67,23 @@ def test_offsets_are_clamped_to_ascending_order(bad, S, N, K):
             assert torch.isfinite(want).all()
             for _ in range(3):
                 assert torch.equal(f(off), want)
+
+
+# The codes are compared as bytes: zeros, and values that round to zero, keep
+# their sign, in blocks whose scale the fast quotient takes and in others.
+@pytest.mark.parametrize("rows", [1, 128])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("amax", [0.0, 1e-7, 1.0, 3000.0, 1e-37, 1e30])
+def test_quant_keeps_the_sign_of_zero(rows, dtype, amax):
+    g = gen(int(rows + amax % 97))
+    x = torch.randint(-4, 5, (2 * rows + 3, 264), generator=g, device="cuda").float() * (amax / 4)
+    x[:, 1::3] = -0.0
+    x[:, 2::9] *= 1e-5                  # rounds to a zero of either sign
+    x = x.to(dtype)
+    if dtype == torch.float16 and not torch.isfinite(x).all():
+        pytest.skip("beyond f16")
+    q, s = B.situ_moe_quant_fp8(x, rows)
+    rq, rs = plain_quant(x, rows)
+    assert torch.equal(s.cpu(), rs)
+    assert (rq.view(torch.uint8) == 0x80).any()
+    assert torch.equal(q.cpu(), rq.view(torch.uint8))
