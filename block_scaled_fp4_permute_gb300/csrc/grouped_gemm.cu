@@ -54,7 +54,8 @@ constexpr int kThreads = 384;
 constexpr int kEpiWarp = 4;         // first of the eight epilogue warps: two per TMEM lane quarter
 constexpr int kEpiThreads = 256;
 constexpr int kSplitLeast = 8;      // stages that a CTA of a split tile takes at least
-constexpr int kSumStages = 8;       // stages summed in TMEM before the fp32 registers take them (fp32 results)
+constexpr int kSumStages = 8;       // stages summed in TMEM before the fp32 registers take them
+constexpr int kOneSum = 0, kSums = 1, kLongSums = 2;   // how a tile is summed, see gg_kernel
 constexpr int kLaunchRegs = 168;    // per thread of a launch, what kSplitRegs shares out
 constexpr int kPartPitch = 260;     // floats of a row of a split wgrad tile's part: 256 and 4
 constexpr int kJoinPitch = 132;     // floats of a token of a split forward or dgrad tile's part
@@ -71,6 +72,7 @@ struct GgParams {
   long ld_out;      // elements
   int bf16, out_f32, accumulate, zero_rest;
   int store8;       // 16-bit dw stored by all eight epilogue warps
+  int one_sum;      // stages that 16-bit results take in one TMEM sum at most
   int* err;
 };
 
@@ -205,10 +207,12 @@ __device__ __forceinline__ void join_dw(const GgParams& p, const Tile& t, uint32
   }
 }
 
-// SUMS: the sums of a chunk of stages are added up in registers (fp32 results,
-// additions to dw); else 16-bit results go straight from TMEM to memory.  A
-// build of each, because carrying both cost the 16-bit form 2 to 4 %.
-template <int CG, int MODE, int TN, bool SUMS, bool SPLIT>
+// SUMS: kOneSum, 16-bit results go straight from TMEM to memory; kSums, the
+// sums of a chunk of stages are added up in registers (fp32 results, additions
+// to dw, split tiles); kLongSums, so are those of 16-bit results whose
+// contraction takes more than one_sum stages.  A build of each: carrying two
+// cost the first 2 to 4 %, additions to dw 3 to 4.
+template <int CG, int MODE, int TN, int SUMS, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
 gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
           const __grid_constant__ CUtensorMap mapA1, const __grid_constant__ CUtensorMap mapB1,
@@ -219,7 +223,7 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = CG == 2 ? cluster_rank() : 0;
-  static_assert(!SPLIT || (CG == 1 && SUMS), "split tiles");
+  static_assert(!SPLIT || (CG == 1 && SUMS == kSums), "split tiles");
   const int part = SPLIT ? (int)cluster_rank() : 0, parts = SPLIT ? (int)cluster_size() : 1;
   const uint32_t sbase = saddr(smem);
   int* tp = reinterpret_cast<int*>(smem + (MODE == kWgrad ? C::kOffTm + 4 : C::kOffTp));
@@ -265,9 +269,12 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
   // a split tile's CTAs take neighbouring ranges of its stages
   auto stage_from = [&](const Tile& t) { return SPLIT ? t.nk * part / parts : 0; };
   auto stage_to = [&](const Tile& t) { return SPLIT ? t.nk * (part + 1) / parts : t.nk; };
+  auto chunk = [&](const Tile& t) {   // stages of one sum in TMEM
+    return SUMS == kOneSum || (SUMS == kLongSums && t.nk <= p.one_sum) ? t.nk : kSumStages;
+  };
 
   if (warp < kEpiWarp) {
-    if (C::kSplitRegs && SUMS) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (C::kSplitRegs && SUMS != kOneSum) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 0) {
       // ---------------- copies ----------------
       const bool leader = elect_one();
@@ -355,7 +362,7 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
         const int len = MODE == kWgrad ? t.rows : p.L;
         const int from = stage_from(t), to = stage_to(t);
         for (int k0 = from; k0 < to && ok;) {   // a chunk's sums start from zero in the other accumulator
-          const int k1 = SUMS ? min(k0 + kSumStages, to) : to, buf = ab.s;
+          const int k1 = SUMS == kOneSum ? to : min(k0 + chunk(t), to), buf = ab.s;
           if (ab.used == 2 && !warp_wait(acc_empty(buf), ab.ph ^ 1, p.err, 73)) {
             ok = false;
             break;
@@ -399,7 +406,7 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
     }
   } else {
     // ---------------- epilogue ----------------
-    if (C::kSplitRegs && SUMS) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    if (C::kSplitRegs && SUMS != kOneSum) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
     const int q = warp & 3, h = (warp - kEpiWarp) >> 2, ew = warp - kEpiWarp;
     Ring<2> ab;
     // this warp's 32 lanes and every other 32 columns (wgrad: 64)
@@ -449,7 +456,7 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
       }
     };
     uint32_t obuf = 0;
-    for (int idx = first; idx < total && !SUMS; idx += stride) {
+    for (int idx = first; idx < total && SUMS == kOneSum; idx += stride) {
       const Tile t = tile_of<CG, MODE, TN>(p, tp, idx);
       const int m0 = t.m0 + 128 * (int)rank + 32 * q;
       const bool sums = t.nk > 0;   // else an expert without rows: zeros
@@ -505,7 +512,7 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
       __syncwarp();
       if (sums) release(buf);
     }
-    for (int idx = first; idx < total && SUMS; idx += stride) {
+    for (int idx = first; idx < total && SUMS != kOneSum; idx += stride) {
       const Tile t = tile_of<CG, MODE, TN>(p, tp, idx);
       float acc[kOwn][32];
 #pragma unroll
@@ -513,7 +520,7 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
 #pragma unroll
         for (int c = 0; c < 32; ++c) acc[i][c] = 0.f;
       bool ok = true;
-      for (int kk = stage_from(t), to = stage_to(t); kk < to; kk += kSumStages) {
+      for (int kk = stage_from(t), to = stage_to(t); kk < to; kk += chunk(t)) {
         const int buf = ab.s;
         if (!warp_wait(acc_full(buf), ab.ph, p.err, 75)) {
           ok = false;
@@ -555,7 +562,7 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
             for (int c = 0; c < 32; ++c) part_at[(own(i) + frag_col(c, lane)) * kJoinPitch + 32 * q + frag_row(c, lane)] = acc[i][c];
           }
         }
-      } else if (MODE == kWgrad && p.accumulate) {
+      } else if (MODE == kWgrad && SUMS == kSums && p.accumulate) {
         if (m0 + lane < p.M && t.nk > 0) {
 #pragma unroll
           for (int i = 0; i < kOwn; ++i)
@@ -564,20 +571,38 @@ gg_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUte
               if (own(i) + c < t.cols)
                 add_dw(p, ((size_t)t.e * p.M + m0 + lane) * (size_t)p.ld_out + t.c0 + own(i) + c, acc[i] + c);
         }
-      } else if (MODE == kWgrad) {   // fp32
+      } else if (MODE == kWgrad) {
         uint8_t* box = smem + C::kOffOut + ew * 4096;
+        auto box_free = [&] {   // the store before has read it
+          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+          __syncwarp();
+        };
+        auto two = [&](int i, int c) { return to_16x2(acc[i][c], acc[i][c + 1], p.bf16); };
 #pragma unroll
         for (int i = 0; i < kOwn; ++i) {
           if (own(i) >= t.cols || m0 >= p.M) continue;
           uint4 v[8];
+          if (SUMS == kSums) {   // fp32
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            v[j] = make_uint4(__float_as_uint(acc[i][4 * j]), __float_as_uint(acc[i][4 * j + 1]),
-                              __float_as_uint(acc[i][4 * j + 2]), __float_as_uint(acc[i][4 * j + 3]));
-          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");   // the box before has been read
-          __syncwarp();
+            for (int j = 0; j < 8; ++j)
+              v[j] = make_uint4(__float_as_uint(acc[i][4 * j]), __float_as_uint(acc[i][4 * j + 1]),
+                                __float_as_uint(acc[i][4 * j + 2]), __float_as_uint(acc[i][4 * j + 3]));
+          } else if (i % 2 == 0) {   // 64 columns a box: this one's 32 and the next's
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const int k = i + j / 4, c = 8 * (j % 4);
+              v[j] = make_uint4(two(k, c), two(k, c + 2), two(k, c + 4), two(k, c + 6));
+            }
+          } else {
+            continue;
+          }
+          box_free();
           store_box(box, t, m0, own(i), v);
         }
+      } else if (SUMS == kLongSums) {
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i)
+          if (own(i) < t.cols) store_16(t, m0, own(i), reinterpret_cast<const uint32_t*>(acc[i]));
       } else {   // fp32: 16 tokens x 32 elements at a time, 128 bytes of 4 token rows a store
         uint8_t* box = smem + C::kOffOut + ew * 32 * kOutPitch;
         const int chunk = lane & 7, n = m0 + 4 * chunk;
@@ -648,12 +673,12 @@ struct Maps {
 };
 
 // split: CTAs per tile (SPLIT), with one tile per cluster
-template <int CG, int MODE, int TN, bool SUMS, bool SPLIT = false>
+template <int CG, int MODE, int TN, int SUMS, bool SPLIT = false>
 cudaError_t launch_t(const Maps& m, const GgParams& p, long max_items, cudaStream_t st, int split = 1) {
   static std::atomic<uint64_t> raised{0};
   const long sms = sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
-  if (Cfg<CG, MODE, TN>::kSplitRegs && SUMS) {   // the shares need the launch to hold their sum
+  if (Cfg<CG, MODE, TN>::kSplitRegs && SUMS != kOneSum) {   // the shares need the launch to hold their sum
     static const int regs = [] {
       cudaFuncAttributes fa;
       return cudaFuncGetAttributes(&fa, gg_kernel<CG, MODE, TN, SUMS, SPLIT>) == cudaSuccess ? fa.numRegs : 0;
@@ -667,7 +692,7 @@ cudaError_t launch_t(const Maps& m, const GgParams& p, long max_items, cudaStrea
 }
 
 // forward and dgrad by their tiles
-template <int MODE, bool SUMS>
+template <int MODE, int SUMS>
 cudaError_t launch_rows(int tn, int cg, const Maps& m, const GgParams& p, long cap, cudaStream_t st) {
   return tn == 32    ? launch_t<1, MODE, 32, SUMS>(m, p, cap, st)
          : tn == 64  ? launch_t<1, MODE, 64, SUMS>(m, p, cap, st)
@@ -677,9 +702,9 @@ cudaError_t launch_rows(int tn, int cg, const Maps& m, const GgParams& p, long c
 }
 template <int MODE>
 cudaError_t launch_split(int tn, const Maps& m, const GgParams& p, long cap, cudaStream_t st, int split) {
-  return tn == 32   ? launch_t<1, MODE, 32, true, true>(m, p, cap, st, split)
-         : tn == 64 ? launch_t<1, MODE, 64, true, true>(m, p, cap, st, split)
-                    : launch_t<1, MODE, 128, true, true>(m, p, cap, st, split);
+  return tn == 32   ? launch_t<1, MODE, 32, kSums, true>(m, p, cap, st, split)
+         : tn == 64 ? launch_t<1, MODE, 64, kSums, true>(m, p, cap, st, split)
+                    : launch_t<1, MODE, 128, kSums, true>(m, p, cap, st, split);
 }
 
 bool fits16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -762,7 +787,7 @@ extern "C" situ_status situ_moe_grouped_gemm(const situ_grouped_gemm_args* g, vo
   // skewed group's rows are taken as up to twice the average)
   const double wtiles = (double)p.E * ((p.M + 127) / 128) * ((p.Ncol + 255) / 256);
   const int wsteps = (int)((g->E > 1 ? 2 * per : per) / kBK);
-  const int wsplit = mode == kWgrad ? split_of(gg_kernel<1, kWgrad, 256, true, true>, kThreads,
+  const int wsplit = mode == kWgrad ? split_of(gg_kernel<1, kWgrad, 256, kSums, true>, kThreads,
                                                Cfg<1, kWgrad, 256>::kSmem, wtiles, wsteps, kSplitLeast)
                                     : 1;
   const int cg = tn == 256 && p.M > 128 && wsplit == 1 ? 2 : 1;
@@ -795,21 +820,33 @@ extern "C" situ_status situ_moe_grouped_gemm(const situ_grouped_gemm_args* g, vo
   const double most = most_tiles(g->S, g->E, tn) * p.n_mt;
   const long cap = most > 1e6 ? 1000000 : (long)most;
   const int steps = (p.L + kBK - 1) / kBK;
-  const int split = tn <= 128 ? split_of(gg_kernel<1, kFwd, 32, true, true>, kThreads, Cfg<1, kFwd, 32>::kSmem, most, steps, kSplitLeast) : 1;
-  const bool sums = p.out_f32 || p.accumulate;
+  const int split = tn <= 128 ? split_of(gg_kernel<1, kFwd, 32, kSums, true>, kThreads, Cfg<1, kFwd, 32>::kSmem, most, steps, kSplitLeast) : 1;
+  // The tensor cores truncate when they add: sums of one sign come out smaller
+  // by 6e-9 of themselves per contraction element.  16-bit results take that
+  // in one TMEM sum while it stays below a tenth of their last unit (largest
+  // error 0.6 units where rounding alone is 0.5: f16 at 8,192, bf16 at 65,536
+  // elements; f16 at 262,144: 3.7 units in one sum, 0.5 in chunks).  A group's
+  // rows are not known here, but are S at most; its own tiles then count.
+  p.one_sum = (p.bf16 ? 65536 : 8192) / kBK;
+  const bool longer = ((mode == kWgrad ? p.S : p.L) + kBK - 1) / kBK > p.one_sum;
+  const int sums = p.out_f32 || p.accumulate ? kSums : longer ? kLongSums : kOneSum;
   cudaError_t e;
   if (mode == kWgrad && wsplit > 1) {
-    e = launch_t<1, kWgrad, 256, true, true>(m, p, (long)items, st, wsplit);
-  } else if (mode == kWgrad) {
-    const long all = items > 1e6 ? 1000000 : (long)items;
-    e = cg == 2 ? (sums ? launch_t<2, kWgrad, 256, true>(m, p, all, st) : launch_t<2, kWgrad, 256, false>(m, p, all, st))
-                : (sums ? launch_t<1, kWgrad, 256, true>(m, p, all, st) : launch_t<1, kWgrad, 256, false>(m, p, all, st));
+    e = launch_t<1, kWgrad, 256, kSums, true>(m, p, (long)items, st, wsplit);
   } else if (split > 1) {
     e = mode == kFwd ? launch_split<kFwd>(tn, m, p, cap, st, split) : launch_split<kDgrad>(tn, m, p, cap, st, split);
-  } else if (mode == kFwd) {
-    e = sums ? launch_rows<kFwd, true>(tn, cg, m, p, cap, st) : launch_rows<kFwd, false>(tn, cg, m, p, cap, st);
   } else {
-    e = sums ? launch_rows<kDgrad, true>(tn, cg, m, p, cap, st) : launch_rows<kDgrad, false>(tn, cg, m, p, cap, st);
+    const long all = items > 1e6 ? 1000000 : (long)items;
+    auto launch = [&](auto form) {
+      constexpr int F = decltype(form)::value;
+      return mode == kFwd      ? launch_rows<kFwd, F>(tn, cg, m, p, cap, st)
+             : mode == kDgrad  ? launch_rows<kDgrad, F>(tn, cg, m, p, cap, st)
+             : cg == 2         ? launch_t<2, kWgrad, 256, F>(m, p, all, st)
+                               : launch_t<1, kWgrad, 256, F>(m, p, all, st);
+    };
+    e = sums == kOneSum ? launch(std::integral_constant<int, kOneSum>{})
+        : sums == kSums ? launch(std::integral_constant<int, kSums>{})
+                        : launch(std::integral_constant<int, kLongSums>{});
   }
   return e == cudaSuccess ? SITU_OK : SITU_ERR_CUDA;
 }

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from block_scaled_fp4_permute_gb300 import binding as B, build
-from test_gpu_expert_products import fp8_operands, gen, normal, offsets_of, plain_quant
+from test_gpu_expert_products import HALF_ULP, call, fp8_operands, gen, normal, offsets_of, operands, plain_quant
 
 pytestmark = pytest.mark.gpu
 
@@ -87,3 +87,60 @@ def test_quant_keeps_the_sign_of_zero(rows, dtype, amax):
     assert torch.equal(s.cpu(), rs)
     assert (rq.view(torch.uint8) == 0x80).any()
     assert torch.equal(q.cpu(), rq.view(torch.uint8))
+
+
+# Long contractions with terms of one sign, where truncated additions would
+# pile up.  The bar: the rounding to 16 bits, 2^-23 per element of a chunk of
+# 512 that the tensor cores add, and 2^-24 per rounded addition of a chunk.
+def long_bar(ref, L, dtype):
+    return ref * ((512 * 2.0 ** -23 + -(-L // 512) * 2.0 ** -24) * (1 + HALF_ULP[dtype]) + HALF_ULP[dtype])
+
+
+@pytest.mark.parametrize("dtype,log2", [(torch.float16, 14), (torch.float16, 18), (torch.bfloat16, 17), (torch.bfloat16, 19)])
+def test_long_weight_gradients_of_one_sign(dtype, log2):
+    N, K, S = 1024, 2560, 1 << log2
+    g = gen(log2)
+    dy = (torch.rand(S, N, generator=g, device="cuda") * 2.0 ** (12 - log2)).to(dtype)
+    x = torch.rand(S, K, generator=g, device="cuda").to(dtype)
+    got = B.situ_moe_grouped_gemm_wgrad(dy, x, offsets_of([S]))[0, :48].double()
+    ref = sum(dy[i:i + 65536, :48].double().T @ x[i:i + 65536].double() for i in range(0, S, 65536))
+    assert ((got - ref).abs() <= long_bar(ref, S, dtype)).all()
+
+
+@pytest.mark.parametrize("direction", ["forward", "dgrad"])
+@pytest.mark.parametrize("dtype,log2", [(torch.float16, 17), (torch.bfloat16, 18)])
+def test_long_products_of_one_sign(direction, dtype, log2):
+    M, L, S = 4096, 1 << log2, 300
+    g = gen(log2)
+    a = (torch.rand(S, L, generator=g, device="cuda") * 2.0 ** (12 - log2)).to(dtype)
+    w = torch.rand(1, *((M, L) if direction == "forward" else (L, M)), generator=g, device="cuda", dtype=torch.float16).to(dtype)
+    got = call(direction, a, w, offsets_of([S]))[:, :48].double()
+    part = w[0, :48].T if direction == "forward" else w[0][:, :48]
+    ref = a.double() @ part.double()
+    assert ((got - ref).abs() <= long_bar(ref, L, dtype)).all()
+
+
+# the 16-bit results of long contractions in every form of tile: groups short,
+# empty and uneven, sizes off the tiles
+@pytest.mark.parametrize("counts,M", [([(7 * i) % 24 for i in range(160)], 136), ([(11 * i) % 60 for i in range(60)], 264),
+                                      ([70, 90, 0, 97, 5] * 8, 520), ([20000], 120), ([300, 0, 700, 129, 1], 2312)])
+@pytest.mark.parametrize("direction", ["forward", "dgrad"])
+def test_long_products_in_every_form(counts, M, direction):
+    L, S, E = 8200, sum(counts) + 5, len(counts)
+    N, K = (M, L) if direction == "forward" else (L, M)
+    a, b, _ = operands(direction, gen(M), S, E, N, K, torch.float16)
+    off = offsets_of(counts, 2)
+    got = call(direction, a, b, off)
+    want = call(direction, a, b, off, out_dtype=torch.float32)     # the same sums, rounded once
+    assert torch.isfinite(want).all() and (want != 0).any()
+    assert torch.equal(got, want.half())
+
+
+@pytest.mark.parametrize("counts,N,K", [([9000, 0, 37, 5], 1000, 2056), ([8200], 120, 20488), ([16, 8300, 33, 64, 65], 264, 5000)])
+def test_long_weight_gradients_in_every_form(counts, N, K):
+    S = sum(counts) + 5
+    dy, x, _ = operands("wgrad", gen(N), S, len(counts), N, K, torch.float16)
+    off = offsets_of(counts, 2)
+    got = B.situ_moe_grouped_gemm_wgrad(dy, x, off)
+    want = B.situ_moe_grouped_gemm_wgrad(dy, x, off, out_dtype=torch.float32)
+    assert torch.isfinite(want).all() and torch.equal(got, want.half())
