@@ -496,8 +496,14 @@ def _groups(offsets: torch.Tensor, index: int) -> int:
     return offsets.shape[0] - 1
 
 
+def _too_large(*sizes):
+    return ValueError(f"sizes {sizes} must be below 2^31")
+
+
 def _grouped(a, direction, b, offsets, S, E, N, K, out, shape, strides, out_dtype, accumulate, zero_rest):
     index, dtype = a.get_device(), a.dtype
+    if (S | E | N | K) >> 31:   # ctypes would cut them to 32 bits
+        raise _too_large(S, E, N, K)
     if index < 0 or b.get_device() != index:
         raise ValueError(f"the operands must be on one CUDA device, not on {a.device} and {b.device}")
     if dtype is not torch.bfloat16 and dtype is not torch.float16 or b.dtype is not dtype:
@@ -608,6 +614,8 @@ def situ_moe_quant_fp8(x: torch.Tensor, block_rows: int = 1, *, out=None, stream
     index, dtype, dim = x.get_device(), _DTYPES.get(x.dtype), x.dim()
     if dtype is None:
         raise TypeError("x must be bf16, f16 or fp32")
+    if max(x.shape) >> 31:
+        raise _too_large(*x.shape)
     if index < 0:
         raise ValueError("x must be a CUDA tensor")
     if block_rows != 1 and block_rows != 128:
@@ -638,6 +646,9 @@ def situ_moe_quant_fp8(x: torch.Tensor, block_rows: int = 1, *, out=None, stream
 
 def _fp8_gemm(x_q, x_scale, w_q, w_scale, E, N, K, offsets, out, out_dtype, zero_rest):
     index = x_q.get_device()
+    S, Kx = x_q.shape
+    if (S | E | N | K) >> 31:
+        raise _too_large(S, E, N, K)
     if index < 0 or x_scale.get_device() != index or w_q.get_device() != index or w_scale.get_device() != index:
         raise ValueError("the operands must be on one CUDA device")
     if x_q.dtype not in _E4M3 or w_q.dtype not in _E4M3:
@@ -648,7 +659,6 @@ def _fp8_gemm(x_q, x_scale, w_q, w_scale, E, N, K, offsets, out, out_dtype, zero
         out_dtype = out.dtype if out is not None else torch.bfloat16
     if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
         raise TypeError("the output must be bf16 or fp32")
-    S, Kx = x_q.shape
     nkb, nrb = -(-K // 128), -(-N // 128)
     if Kx != K or x_scale.shape != (S, nkb):
         raise ValueError(f"needs x_q [S, {K}] and x_scale [S, {nkb}]")

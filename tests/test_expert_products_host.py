@@ -4,8 +4,10 @@ import os
 import random
 import subprocess
 
+import pytest
+import torch
 
-from block_scaled_fp4_permute_gb300 import build
+from block_scaled_fp4_permute_gb300 import binding as B, build
 
 ROWS = r"""
 #include <cstdio>
@@ -92,3 +94,24 @@ def test_a_warp_drains_what_it_has_in_flight_unless_all_of_it_arrived(tmp_path):
         j = (steps - 1) % 3
         arrived = [f"a{j}{last[j]}"] if ok and steps else []
         assert newest.split() == arrived + (drained if not ok or (steps and fails == j) else []), (steps, ok, fails)
+
+
+def test_sizes_past_31_bits_are_refused_not_cut():
+    # expanded tensors: one row of memory
+    S = 2 ** 32 + 8
+    off = torch.tensor([0, 4], dtype=torch.int32)
+
+    def rows(n, dtype=torch.bfloat16):
+        return torch.zeros(1, n, dtype=dtype).expand(S, n)
+
+    w, wq = torch.zeros(1, 64, 64, dtype=torch.bfloat16), torch.zeros(64, 64, dtype=torch.uint8)
+    calls = [lambda: B.situ_moe_grouped_gemm(rows(64), w, off), lambda: B.situ_moe_grouped_gemm_dgrad(rows(64), w, off),
+             lambda: B.situ_moe_grouped_gemm_wgrad(rows(64), rows(64), off),
+             lambda: B.situ_moe_grouped_gemm_wgrad(rows(8)[:8], rows(8)[:8], off[:1].expand(S)),
+             lambda: B.situ_moe_grouped_gemm(rows(64)[:4], rows(64)[None], off),
+             lambda: B.situ_moe_quant_fp8(rows(64)), lambda: B.situ_moe_quant_fp8(rows(64)[None], 128),
+             lambda: B.situ_moe_fp8_gemm(rows(64, torch.uint8), rows(1, torch.float32), wq, torch.zeros(1, 1)),
+             lambda: B.situ_moe_fp8_gemm(wq, torch.zeros(64, 1), rows(64, torch.uint8), rows(1, torch.float32))]
+    for call in calls:
+        with pytest.raises(ValueError, match=r"below 2\^31"):
+            call()
