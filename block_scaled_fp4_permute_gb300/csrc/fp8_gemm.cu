@@ -847,7 +847,7 @@ extern "C" situ_status situ_moe_fp8_gemm(const situ_fp8_gemm_args* g, void* stre
       g->ldx < g->K || g->ldx % 16 != 0 || g->ldo < g->N || g->ldo % 8 != 0)
     return SITU_ERR_BAD_SHAPE;
   const int64_t ldw = g->ldw ? g->ldw : g->K;
-  if (ldw > kMaxStride) return SITU_ERR_BAD_SHAPE;
+  if (g->ldx > kMaxStride || g->ldo > kMaxStride || ldw > kMaxStride) return SITU_ERR_BAD_SHAPE;
   const int64_t stride_w = g->stride_w ? g->stride_w : g->N * ldw;
   if (ldw < g->K || ldw % 16 != 0 || stride_w < g->N * ldw || stride_w % ldw != 0) return SITU_ERR_BAD_SHAPE;
   if (g->S == 0) return SITU_OK;

@@ -731,7 +731,7 @@ extern "C" situ_status situ_moe_grouped_gemm(const situ_grouped_gemm_args* g, vo
       (mode != kWgrad && (g->ldo < co || g->ldo % 8 != 0)))
     return SITU_ERR_BAD_SHAPE;
   const int64_t ldw = g->ldw ? g->ldw : g->K;
-  if (ldw > kMaxStride) return SITU_ERR_BAD_SHAPE;
+  if (g->lda > kMaxStride || (mode == kWgrad ? g->ldb : g->ldo) > kMaxStride || ldw > kMaxStride) return SITU_ERR_BAD_SHAPE;
   const int64_t stride_w = g->stride_w ? g->stride_w : g->N * ldw;
   if (mode == kWgrad ? g->ldw != 0 || g->stride_w != 0
                      : ldw < g->K || ldw % 8 != 0 || stride_w < g->N * ldw || stride_w % ldw != 0)

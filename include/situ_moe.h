@@ -526,6 +526,7 @@ typedef enum situ_grouped_direction {
 #define SITU_GEMM_MAX_GROUPS 1024
 #define SITU_GEMM_MAX_DIM (1 << 20)    /* N, K */
 #define SITU_GEMM_MAX_ROWS (1 << 30)   /* S */
+/* and strides of 2^39 elements */
 
 /* situ_moe_grouped_gemm -- y = x w_e^T and its gradients, per expert:
  *   FORWARD  y[r, n]     = sum_k x[r, k] w[e, n, k]      (r a row of e)

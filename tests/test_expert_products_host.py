@@ -1,5 +1,6 @@
 """What the expert products' kernels decide in plain arithmetic, compiled for
 the host and run on the CPU."""
+import ctypes
 import os
 import random
 import subprocess
@@ -115,3 +116,21 @@ def test_sizes_past_31_bits_are_refused_not_cut():
     for call in calls:
         with pytest.raises(ValueError, match=r"below 2\^31"):
             call()
+
+
+@pytest.mark.parametrize("over", [dict(lda=1 << 62), dict(ldo=1 << 62), dict(ldw=1 << 40), dict(direction=2, lda=64, ldb=1 << 62)])
+def test_strides_beyond_the_tensor_maps_are_refused_by_their_size(over):
+    build.build()
+    a = dict(direction=0, dtype=0, out_dtype=0, S=16, N=64, K=128, E=4, accumulate=0, keep_rest=0, a=0x1000, lda=128,
+             b=0x2000, ldb=128, offsets=0x3000, out=0x4000, ldo=64, device_status=0x5000)
+    a.update(over)
+    assert B.lib().situ_moe_grouped_gemm(ctypes.byref(B.SituGroupedGemmArgs(**a)), None) == 2
+
+
+@pytest.mark.parametrize("over", [dict(ldx=1 << 62), dict(ldo=1 << 62), dict(ldw=1 << 40)])
+def test_fp8_strides_beyond_the_tensor_maps_are_refused_by_their_size(over):
+    build.build()
+    a = dict(out_dtype=0, S=16, N=64, K=128, E=1, keep_rest=0, x_q=0x1000, ldx=128, x_scale=0x2000, w_q=0x3000,
+             w_scale=0x4000, offsets=None, out=0x5000, ldo=64, device_status=0x6000)
+    a.update(over)
+    assert B.lib().situ_moe_fp8_gemm(ctypes.byref(B.SituFp8GemmArgs(**a)), None) == 2
