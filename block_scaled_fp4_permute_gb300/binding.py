@@ -357,7 +357,9 @@ def situ_moe_forward_profiled(args: SituMoeArgs, workspace: torch.Tensor, events
 # expert products with 16-bit and with E4M3 weights
 #
 # Each call enqueues on ``stream`` (default: the current stream of the
-# operands' device); results and copies are allocated on that stream.  A
+# operands' device); results and copies are allocated on that stream.  The
+# caller orders it after the work that makes the operands, and before the work
+# that reads the results; the operands may be dropped at once.  A
 # first call on a device waits for it once (its status word), so it does not
 # belong inside a graph capture.
 # ---------------------------------------------------------------------------
@@ -424,11 +426,17 @@ def _enqueue(name: str, index: int, *args) -> None:
 
 def _on_stream(stream, f, x: torch.Tensor, *args, **kw):
     """f(x, *args, **kw) with ``stream`` current: what it allocates and copies
-    belongs to that stream too."""
+    belongs to that stream too, and the memory of operands that belong to
+    another is not given to anyone else before this work is done."""
     if stream.device != x.device:
         raise ValueError(f"a stream of {stream.device} for operands on {x.device}")
     with torch.cuda.stream(stream):
-        return f(x, *args, **kw)
+        result = f(x, *args, **kw)
+    for t in (x, *args, *kw.values()):
+        for u in t if isinstance(t, (tuple, list)) else (t,):
+            if isinstance(u, torch.Tensor) and u.is_cuda:
+                u.record_stream(stream)
+    return result
 
 
 def _rows(t: torch.Tensor, unit: int):

@@ -144,3 +144,55 @@ def test_long_weight_gradients_in_every_form(counts, N, K):
     got = B.situ_moe_grouped_gemm_wgrad(dy, x, off)
     want = B.situ_moe_grouped_gemm_wgrad(dy, x, off, out_dtype=torch.float32)
     assert torch.isfinite(want).all() and torch.equal(got, want.half())
+
+
+def test_operands_of_another_stream_outlive_their_last_reference():
+    # the side stream is held up while the operands are dropped: their memory
+    # must not come back for anyone else until its work is done
+    counts, N, K = [40, 0, 25], 136, 272
+    S = sum(counts)
+    g = gen(71)
+    off = offsets_of(counts)
+    big = normal(g, S, 1 << 16)                      # a block of its own size
+    x, w, dy = normal(g, S, K), normal(g, 3, N, K, std=0.1), normal(g, S, N)
+    fp8 = fp8_operands(g, S, 3, N, K)
+    calls = {
+        "forward": (B.situ_moe_grouped_gemm, (x, w, off)), "dgrad": (B.situ_moe_grouped_gemm_dgrad, (dy, w, off)),
+        "wgrad": (B.situ_moe_grouped_gemm_wgrad, (dy, x, off)), "quant": (B.situ_moe_quant_fp8, (big,)),
+        "fp8": (B.situ_moe_fp8_grouped_gemm, (*fp8, off)),
+        "dense": (B.situ_moe_fp8_gemm, (fp8[0], fp8[1], fp8[2][0].clone(), fp8[3][0].clone())),
+    }
+    side = torch.cuda.Stream()
+    for name, (f, operands_) in calls.items():
+        want = f(*operands_)
+        mine = [t.clone() for t in operands_]
+        at = {t.data_ptr() for t in mine}
+        shapes = [(t.shape, t.dtype) for t in mine]
+        torch.cuda.synchronize()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(100_000_000)           # about 50 ms
+        got = f(*mine, stream=side)
+        del mine
+        others = [torch.empty(shape, dtype=dtype, device="cuda") for shape, dtype in shapes for _ in range(4)]
+        assert not at & {t.data_ptr() for t in others}, name
+        torch.cuda.synchronize()
+        got, want = (got, want) if isinstance(got, tuple) else ((got,), (want,))
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), name
+
+
+def test_a_given_result_of_another_stream_outlives_its_last_reference():
+    x, w, off = torch.ones(40, 64, device="cuda").bfloat16(), torch.ones(1, 64, 64, device="cuda").bfloat16(), offsets_of([40])
+    side = torch.cuda.Stream()
+    out, q, s = torch.empty(40, 64, device="cuda"), torch.empty(40, 64, dtype=torch.uint8, device="cuda"), torch.empty(40, 1, device="cuda")
+    at = {t.data_ptr() for t in (out, q, s)}
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)
+    B.situ_moe_grouped_gemm(x, w, off, out=out, stream=side)
+    B.situ_moe_quant_fp8(x, out=(q, s), stream=side)
+    del out, q, s
+    others = [torch.empty_like(t) for t in (torch.empty(40, 64, device="cuda"), torch.empty(40, 64, dtype=torch.uint8, device="cuda"),
+                                            torch.empty(40, 1, device="cuda")) for _ in range(4)]
+    assert not at & {t.data_ptr() for t in others}
+    torch.cuda.synchronize()
