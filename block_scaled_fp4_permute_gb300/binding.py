@@ -397,11 +397,12 @@ def situ_moe_gemm_status(device=None, reset: bool = False) -> int:
 
 # The short calls (a decode step's) take the GPU less time than their
 # marshalling takes the host, so what every call passes through is kept short:
-# the direct forms of torch.cuda.current_stream (0.1 for 2.9 us here) and,
-# where this torch has it, of torch.empty (0.9 for 2.3 us), and no helper calls
-# for operands that need none.
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+# where this torch has them, the direct forms of torch.cuda.current_stream (0.1
+# for 2.9 us here) and of torch.empty (0.9 for 2.3 us), and no helper calls for
+# operands that need none.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _empty_cuda = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None)
 
 

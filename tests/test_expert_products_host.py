@@ -4,6 +4,7 @@ import ctypes
 import os
 import random
 import subprocess
+import sys
 
 import pytest
 import torch
@@ -134,3 +135,16 @@ def test_fp8_strides_beyond_the_tensor_maps_are_refused_by_their_size(over):
              w_scale=0x4000, offsets=None, out=0x5000, ldo=64, device_status=0x6000)
     a.update(over)
     assert B.lib().situ_moe_fp8_gemm(ctypes.byref(B.SituFp8GemmArgs(**a)), None) == 2
+
+
+def test_a_torch_without_the_direct_calls_takes_the_public_ones():
+    # such as one built without CUDA
+    code = ("import torch\n"
+            "for name in ('_cuda_getCurrentRawStream', '_cuda_getDevice'):\n"
+            "    if hasattr(torch._C, name):\n"
+            "        delattr(torch._C, name)\n"
+            "from block_scaled_fp4_permute_gb300 import binding as B\n"
+            "assert B._current_device is torch.cuda.current_device\n"
+            "torch.cuda.current_stream = lambda index: type('S', (), {'cuda_stream': 7 + index})\n"
+            "assert B._raw_stream(1) == 8\n")
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=build.ROOT)
