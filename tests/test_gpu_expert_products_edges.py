@@ -186,13 +186,13 @@ def test_a_given_result_of_another_stream_outlives_its_last_reference():
     side = torch.cuda.Stream()
     out, q, s = torch.empty(40, 64, device="cuda"), torch.empty(40, 64, dtype=torch.uint8, device="cuda"), torch.empty(40, 1, device="cuda")
     at = {t.data_ptr() for t in (out, q, s)}
+    shapes = [(t.shape, t.dtype) for t in (out, q, s)]
     torch.cuda.synchronize()
     with torch.cuda.stream(side):
         torch.cuda._sleep(100_000_000)
     B.situ_moe_grouped_gemm(x, w, off, out=out, stream=side)
     B.situ_moe_quant_fp8(x, out=(q, s), stream=side)
     del out, q, s
-    others = [torch.empty_like(t) for t in (torch.empty(40, 64, device="cuda"), torch.empty(40, 64, dtype=torch.uint8, device="cuda"),
-                                            torch.empty(40, 1, device="cuda")) for _ in range(4)]
+    others = [torch.empty(shape, dtype=dtype, device="cuda") for shape, dtype in shapes for _ in range(4)]
     assert not at & {t.data_ptr() for t in others}
     torch.cuda.synchronize()
