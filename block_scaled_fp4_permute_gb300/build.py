@@ -10,9 +10,11 @@ from __future__ import annotations
 import concurrent.futures as cf
 import glob
 import os
+import re
 import shutil
 import subprocess
 import sys
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -20,7 +22,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libsitu_moe.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
-NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
+# -v: the registers of each kernel, for short_of_registers()
+NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xptxas", "-v", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
               "-I", os.path.join(ROOT, "include")]
 
 
@@ -47,16 +50,36 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
+# Kernels whose warps share out the launch's registers (setmaxnreg) and so
+# refuse to launch with fewer than this per thread: the wide tiles of the expert
+# products (gg_kernel: 256 tokens with sums in registers).
+SHARED_REGISTERS = 168
+_SHARING = re.compile(r"f8w_kernelI|gg_kernelILi\dELi\dELi256ELi[12]E")
+
+
+def short_of_registers(log: str):
+    """The kernels in ptxas's -v output that share registers out and were given
+    too few: [(name, registers)]."""
+    short, name = [], None
+    for line in log.splitlines():
+        m = re.search(r"Compiling entry function '(\S+)'", line)
+        if m:
+            name = m.group(1)
+        m = re.search(r"Used (\d+) registers", line)
+        if m and name and _SHARING.search(name) and int(m.group(1)) < SHARED_REGISTERS:
+            short.append((name, int(m.group(1))))
+    return short
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
     if not force and up_to_date():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
-    extra = ["-Xptxas", "-v"] if ptxas_verbose else []
 
     def compile_one(src):
         obj = os.path.join(BUILD, os.path.basename(src) + ".o")
-        cmd = [nvcc, *ARCH, *NVCC_FLAGS, *extra, "-c", src, "-o", obj]
+        cmd = [nvcc, *ARCH, *NVCC_FLAGS, "-c", src, "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
@@ -64,8 +87,15 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
 
     with cf.ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
         results = list(ex.map(compile_one, _sources()))
-    if verbose or ptxas_verbose:
-        for obj, log in results:
+    for obj, log in results:
+        with open(obj[:-2] + ".ptxas", "w") as f:
+            f.write(log)
+        for name, regs in short_of_registers(log):
+            warnings.warn(f"{name} was compiled to {regs} registers a thread and will refuse to launch "
+                          f"(it needs {SHARED_REGISTERS})")
+        if verbose and not ptxas_verbose:
+            log = "\n".join(x for x in log.splitlines() if "ptxas info" not in x and "bytes stack frame" not in x)
+        if verbose or ptxas_verbose:
             if log.strip():
                 print(f"== {os.path.basename(obj)}\n{log}", file=sys.stderr)
     tmp = LIB + f".{os.getpid()}.tmp"

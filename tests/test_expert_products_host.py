@@ -3,6 +3,7 @@ the host and run on the CPU."""
 import ctypes
 import os
 import random
+import re
 import subprocess
 import sys
 
@@ -148,3 +149,18 @@ def test_a_torch_without_the_direct_calls_takes_the_public_ones():
             "torch.cuda.current_stream = lambda index: type('S', (), {'cuda_stream': 7 + index})\n"
             "assert B._raw_stream(1) == 8\n")
     subprocess.run([sys.executable, "-c", code], check=True, cwd=build.ROOT)
+
+
+def test_kernels_that_share_registers_out_have_enough():
+    build.build()
+    for name, kernels in (("fp8_gemm", 3), ("grouped_gemm", 13)):
+        with open(os.path.join(build.BUILD, name + ".cu.ptxas")) as f:
+            log = f.read()
+        names = re.findall(r"Compiling entry function '(\S+)'", log)
+        assert sum(build._SHARING.search(n) is not None for n in names) == kernels
+        assert build.short_of_registers(log) == []
+    entry = "ptxas info    : Compiling entry function '_ZN4situ{}' for 'sm_103a'\n    0 bytes stack frame\nptxas info    : Used {} registers\n"
+    log = entry.format("10f8w_kernelILi2ELi2EEEv", 160) + entry.format("9f8_kernelILi32ELb0EEEv", 40) + \
+        entry.format("9gg_kernelILi2ELi0ELi256ELi1ELb0EEEv", 168) + entry.format("9gg_kernelILi2ELi0ELi256ELi2ELb0EEEv", 167) + \
+        entry.format("9gg_kernelILi2ELi0ELi256ELi0ELb0EEEv", 72)
+    assert [regs for _, regs in build.short_of_registers(log)] == [160, 167]
