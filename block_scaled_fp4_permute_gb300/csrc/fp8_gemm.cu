@@ -5,13 +5,14 @@
 // The scales are arbitrary fp32 numbers, so they cannot ride along in the
 // MMA (its block scales are powers of two): each block's 128-element product
 // goes to its own TMEM accumulator, and the epilogue warps add it, times its
-// scales, to fp32 sums that they keep in registers over the whole of K.
+// scales, to fp32 sums that they keep in registers over the whole of K.  The
+// two scales are multiplied first, in fp32, one factor for the block.
 //
 // Two kernels.  f8_kernel, for groups of few rows and launches of few tiles:
 // weights on the MMA's M side (128 rows per CTA, one weight scale per block),
 // 32 or 64 tokens on its N side, a token's scale being a column's factor.  It
-// streams the weights (112 experts of 6144 x 3584, 128 rows: 0.255 ms,
-// 6.6 TB/s).  Per CTA: warp 0 copies stages of one block (128 elements = one
+// streams the weights (112 experts of 6144 x 3584, 128 rows: 0.26 ms,
+// 6.5 TB/s).  Per CTA: warp 0 copies stages of one block (128 elements = one
 // 128-byte swizzled row), warp 1 issues the four MMAs of a block, warps 4..11
 // promote: each owns 32 lanes and half of the columns.  Warps 2 and 3 copy
 // the scales, up to 16 blocks and the tile's end ahead.

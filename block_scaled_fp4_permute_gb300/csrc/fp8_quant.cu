@@ -4,9 +4,9 @@
 //   scale = max(amax / 448, 2^-126),  q = E4M3(x / scale), nearest even
 // in IEEE fp32 (both divisions correctly rounded), so the codes are a
 // function of the inputs alone.  The floor keeps the scale of a zero or
-// vanishing block a normal number.  A block with an infinity or a NaN gets a
-// non-finite scale and NaN codes where x / scale is a NaN: the damage stays
-// visible in what is computed from it.
+// vanishing block a normal number.  Zeros keep their sign.  A block with an
+// infinity or a NaN gets a non-finite scale and NaN codes where x / scale is a
+// NaN: the damage stays visible in what is computed from it.
 //
 // Bound by memory: one read of x, one byte written per element.  Each lane
 // takes eight neighbouring elements (16 bytes of a 16-bit type), sixteen

@@ -25,16 +25,21 @@
 // so that the MMA sees zeros in both operands there (a zero in one of them
 // would not do: the neighbour's rows may hold infinities).
 //
+// 16-bit results keep one TMEM sum, up to a length; fp32 results and longer
+// contractions take it out every 512 elements and add in registers, because the
+// tensor cores' additions truncate (the entry point has the figures).
+//
 // Large groups run on CTA pairs (cta_group::2, 256 x 256 per pair: each CTA
 // copies half of the N-side operand, so a stage is 32 KB per CTA and not 48).
 // Launches of few tiles split the contraction over a cluster.
 //
-// Measured (bf16, 4096 x 3584, 32 experts, 1,024 rows each): forward 0.53 to
-// 0.56 ms, dgrad 0.56, wgrad 0.59, that is 1.84 to 1.64 PFLOP/s, where cuBLAS
-// sustains 1.70 under the power limit: bound by the tensor cores.  With 128
-// rows each 0.16 / 0.15 / 0.18 ms: the weights' 0.94 GB at 5.9 to 6.3 TB/s;
-// wgrad's write of as much at 5.2 TB/s (a fill reaches 4.1).  One row per
-// expert (896 experts, 768 x 3584): 6.9 TB/s.
+// Measured (bf16, 4096 x 3584, 32 experts, 1,024 rows each): forward 0.51 to
+// 0.56 ms, dgrad 0.54 to 0.59, wgrad 0.53 to 0.61, that is 1.9 to 1.6 PFLOP/s,
+// where cuBLAS sustains 1.70 under the power limit: bound by the tensor cores.
+// With 128 rows each 0.16 / 0.15 / 0.18 ms, 1.0 GB at 6.4, 6.8 and 5.5 TB/s:
+// forward and dgrad are bound by the weights' bytes, wgrad by its stores (a
+// fill of dw reaches 7.7).  One row per expert (896 experts, 768 x 3584): 7.3
+// TB/s.
 #include "../../include/situ_moe.h"
 #include "gemm_groups.cuh"
 

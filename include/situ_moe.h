@@ -535,13 +535,16 @@ typedef enum situ_grouped_direction {
  *            expert without rows, or added to dw with accumulate = 1
  * a and b are of one 16-bit type; sums are fp32, rounded once to out_dtype
  * (the operands' type or fp32; an accumulating bf16 / f16 dw is rounded once
- * per call).  N and K are multiples of 8, rows may be strided (lda, ldb, ldo
- * in elements, multiples of 8; ldb is wgrad's x, ldo y or dx; dw is
- * contiguous).  Weights may be a part of a larger array: ldw elements between
- * rows (a multiple of 8), stride_w between experts (a multiple of ldw, at
- * least N * ldw); 0 and 0, and for WGRAD always: contiguous.  a, b, out are
- * 16-byte aligned.  S == 0 launches nothing,
- * or sets dw to zeros.  Results do not depend on the order of execution.
+ * per call).  The tensor cores truncate when they add: 16-bit results are off
+ * by 0.1 of their last unit more than their rounding at most, fp32 ones by up
+ * to 3e-6 of a sum of terms of one sign (about 5e-7 on random terms).
+ * N and K are multiples of 8, rows may be strided (lda, ldb, ldo in elements,
+ * multiples of 8; ldb is wgrad's x, ldo y or dx; dw is contiguous).  Weights
+ * may be a part of a larger array: ldw elements between rows (a multiple of
+ * 8), stride_w between experts (a multiple of ldw, at least N * ldw); 0 and 0,
+ * and for WGRAD always: contiguous.  a, b, out are 16-byte aligned.  S == 0
+ * launches nothing, or sets dw to zeros.  Results do not depend on the order
+ * of execution.
  * Errors: NULL_ARG, BAD_SHAPE, UNSUPPORTED, MISALIGNED, CUDA. */
 typedef struct situ_grouped_gemm_args {
   int32_t direction;              /* situ_grouped_direction */
@@ -581,9 +584,12 @@ situ_status situ_moe_quant_fp8(const void* x, int32_t dtype, int32_t E, int32_t 
  * x_q [S, K] with x_scale [S, ceil(K/128)], w_q [E, N, K] with w_scale
  * [E, ceil(N/128), ceil(K/128)] (contiguous); out bf16 or fp32 [S, N].  A
  * block's products are summed in the tensor cores, the scaled blocks in
- * fp32.  K is a multiple of 16, N of 8; x_q rows may be ldx bytes apart (a
- * multiple of 16), out rows ldo elements (a multiple of 8), w_q rows and
- * experts ldw and stride_w bytes (as above, ldw a multiple of 16).
+ * fp32.  A block's two scales are multiplied first, in fp32: a product below
+ * 2^-126 loses bits (blocks of zeros are none the worse), and one of 2^128 or
+ * more is an infinity.
+ * K is a multiple of 16, N of 8; x_q rows may be ldx bytes apart (a multiple
+ * of 16), out rows ldo elements (a multiple of 8), w_q rows and experts ldw
+ * and stride_w bytes (as above, ldw a multiple of 16).
  * Errors: NULL_ARG, BAD_SHAPE, UNSUPPORTED, MISALIGNED, CUDA. */
 typedef struct situ_fp8_gemm_args {
   int32_t out_dtype;              /* SITU_DT_BF16 or SITU_DT_F32 */
