@@ -65,6 +65,49 @@ class SituFp8GemmArgs(ctypes.Structure):
         ("stride_w", ctypes.c_int64)]
 
 
+class SituBalanceArgs(ctypes.Structure):
+    """Mirror of ``situ_balance_args``."""
+    _fields_ = [("router_logits", ctypes.c_void_p), ("ld", ctypes.c_int64), ("topk_ids", ctypes.c_void_p),
+                ("mask", ctypes.c_void_p), ("T", ctypes.c_int32), ("num_experts_total", ctypes.c_int32),
+                ("top_k", ctypes.c_int32), ("coef", ctypes.c_float), ("loss", ctypes.c_void_p),
+                ("counts", ctypes.c_void_p), ("tokens", ctypes.c_void_p), ("row_stats", ctypes.c_void_p)]
+
+
+class SituRouterBackwardArgs(ctypes.Structure):
+    """Mirror of ``situ_router_backward_args``."""
+    _fields_ = [("router_logits", ctypes.c_void_p), ("ld", ctypes.c_int64), ("topk_ids", ctypes.c_void_p),
+                ("mask", ctypes.c_void_p)] + [(n, ctypes.c_int32) for n in (
+                    "T", "num_experts_total", "top_k", "renormalize")] + [("coef", ctypes.c_float)] + [
+        (n, ctypes.c_void_p) for n in ("counts", "tokens", "row_stats", "dloss", "topk_weights", "dweights", "dlogits")] + [
+        ("ldo", ctypes.c_int64)]
+
+
+class SituGatedArgs(ctypes.Structure):
+    """Mirror of ``situ_gated_args``."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("dtype", "activation", "S", "I", "E")] + [
+        ("gate_up", ctypes.c_void_p), ("ld_gate_up", ctypes.c_int64), ("p0", ctypes.c_void_p), ("p1", ctypes.c_void_p),
+        ("offsets", ctypes.c_void_p), ("h", ctypes.c_void_p), ("ldh", ctypes.c_int64), ("q", ctypes.c_void_p),
+        ("scale", ctypes.c_void_p), ("dh", ctypes.c_void_p), ("ld_dh", ctypes.c_int64), ("dgate_up", ctypes.c_void_p),
+        ("ld_dgate_up", ctypes.c_int64)]
+
+
+class SituLoraArgs(ctypes.Structure):
+    """Mirror of ``situ_lora_args``."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("dtype", "out_dtype", "S", "K", "N", "r", "n")] + [
+        ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("a", ctypes.c_void_p), ("b", ctypes.c_void_p),
+        ("ids", ctypes.c_void_p), ("offsets", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("base", ctypes.c_void_p),
+        ("ld_base", ctypes.c_int64), ("out", ctypes.c_void_p), ("ldo", ctypes.c_int64), ("u", ctypes.c_void_p)]
+
+
+class SituLoraBackwardArgs(ctypes.Structure):
+    """Mirror of ``situ_lora_backward_args``."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("dtype", "dx_dtype", "S", "K", "N", "r", "n")] + [
+        ("dy", ctypes.c_void_p), ("ld_dy", ctypes.c_int64), ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64),
+        ("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("offsets", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+        ("u", ctypes.c_void_p), ("dx0", ctypes.c_void_p), ("ld_dx0", ctypes.c_int64), ("dx", ctypes.c_void_p),
+        ("ld_dx", ctypes.c_int64), ("da", ctypes.c_void_p), ("db", ctypes.c_void_p), ("device_status", ctypes.c_void_p)]
+
+
 def library_path() -> str:
     return _build.LIB
 
@@ -123,6 +166,27 @@ def lib() -> ctypes.CDLL:
             l.situ_moe_quant_fp8.argtypes = [vp, i32, i32, i32, i32, ctypes.c_int64, i32, vp, vp, vp]
             l.situ_moe_fp8_gemm.restype = ctypes.c_int
             l.situ_moe_fp8_gemm.argtypes = [ctypes.POINTER(SituFp8GemmArgs), vp]
+            i64 = ctypes.c_int64
+            l.situ_moe_balance_loss_workspace_size.restype = sz
+            l.situ_moe_balance_loss_workspace_size.argtypes = [i32, i32]
+            l.situ_moe_balance_loss.restype = ctypes.c_int
+            l.situ_moe_balance_loss.argtypes = [ctypes.POINTER(SituBalanceArgs), vp, sz, vp]
+            l.situ_moe_router_backward.restype = ctypes.c_int
+            l.situ_moe_router_backward.argtypes = [ctypes.POINTER(SituRouterBackwardArgs), vp]
+            l.situ_moe_save_mxfp8.restype = ctypes.c_int
+            l.situ_moe_save_mxfp8.argtypes = [vp, i32, i32, i32, i64, vp, vp, vp]
+            l.situ_moe_restore_mxfp8.restype = ctypes.c_int
+            l.situ_moe_restore_mxfp8.argtypes = [vp, vp, i32, i32, i32, vp, i64, vp]
+            for fn in (l.situ_moe_gated, l.situ_moe_gated_backward):
+                fn.restype = ctypes.c_int
+                fn.argtypes = [ctypes.POINTER(SituGatedArgs), vp]
+            for fn in (l.situ_moe_lora_workspace_size, l.situ_moe_lora_backward_workspace_size):
+                fn.restype = sz
+                fn.argtypes = [i32, i32, i32, i32]
+            l.situ_moe_lora.restype = ctypes.c_int
+            l.situ_moe_lora.argtypes = [ctypes.POINTER(SituLoraArgs), vp, sz, vp]
+            l.situ_moe_lora_backward.restype = ctypes.c_int
+            l.situ_moe_lora_backward.argtypes = [ctypes.POINTER(SituLoraBackwardArgs), vp, sz, vp]
             _lib = l
     return _lib
 
@@ -721,6 +785,467 @@ def situ_moe_fp8_grouped_gemm(x_q: torch.Tensor, x_scale: torch.Tensor, w_q: tor
                           out_dtype=out_dtype, zero_rest=zero_rest)
     E, N, K = w_q.shape if w_q.dim() == 3 else (1, *w_q.shape)
     return _fp8_gemm(x_q, x_scale, w_q, w_scale, E, N, K, offsets, out, out_dtype, zero_rest)
+
+
+# ---------------------------------------------------------------------------
+# fine-tuning: the router's balance loss, the gated activation with its input
+# kept in 8 bits, low-rank adapters
+#
+# Streams, devices and copies are as for the expert products above.  None of
+# these calls waits for the host, except a first situ_moe_lora_backward on a
+# device (the products' status word).
+# ---------------------------------------------------------------------------
+
+def _on_device(index: int, **tensors) -> None:
+    for name, t in tensors.items():
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"{name} on {t.device}, the operands on cuda:{index}")
+
+
+def _vector(t: torch.Tensor, dtype, n: int, name: str, index: int) -> torch.Tensor:
+    """``t`` as a contiguous [n] of ``dtype``, checked."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if t.shape != (n,):
+        raise ValueError(f"{name} must be [{n}], not {tuple(t.shape)}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} on {t.device}, the operands on cuda:{index}")
+    return t if t.is_contiguous() else t.contiguous()
+
+
+def _logits(t: torch.Tensor):
+    """(tensor, elements between rows) of router logits: itself or a copy."""
+    if t.is_contiguous():
+        return t, t.shape[1]
+    if t.stride(1) == 1 and t.stride(0) >= t.shape[1]:
+        return t, t.stride(0)
+    return t.contiguous(), t.shape[1]
+
+
+def _router(router_logits, topk_ids, mask):
+    """Checks what both router calls take: (logits, ld, ids, mask, index, T, E, k)."""
+    index = router_logits.get_device()
+    if router_logits.dtype is not torch.float32:
+        raise TypeError("router_logits must be fp32")
+    if topk_ids.dtype is not torch.int32:
+        raise TypeError("topk_ids must be int32")
+    if router_logits.dim() != 2 or topk_ids.dim() != 2 or topk_ids.shape[0] != router_logits.shape[0]:
+        raise ValueError("needs router_logits [T, E] and topk_ids [T, k]")
+    if index < 0 or topk_ids.get_device() != index:
+        raise ValueError(f"the operands must be on one CUDA device, not on {router_logits.device} and {topk_ids.device}")
+    T, E = router_logits.shape
+    k = topk_ids.shape[1]
+    if (T | E | k) >> 31:
+        raise _too_large(T, E, k)
+    if mask is not None:
+        if mask.dtype is torch.bool:
+            mask = mask.view(torch.uint8)
+        mask = _vector(mask, torch.uint8, T, "mask", index)
+    logits, ld = _logits(router_logits)
+    return logits, ld, topk_ids if topk_ids.is_contiguous() else topk_ids.contiguous(), mask, index, T, E, k
+
+
+def situ_moe_balance_loss(router_logits: torch.Tensor, topk_ids: torch.Tensor, *, mask=None, coef: float = 1.0,
+                          stream=None):
+    """The router's balance loss over the tokens that ``mask`` (bool or uint8
+    [T]; None: all) leaves: coef * E * sum_e f_e P_e, f_e the share of the
+    chosen slots that name expert e, P_e its mean softmax probability.  Returns
+    (loss fp32 [], counts int32 [E] of the slots per expert, tokens int32 [1],
+    row_stats fp32 [T, 2]), the last two for situ_moe_router_backward."""
+    if stream is not None:
+        return _on_stream(stream, situ_moe_balance_loss, router_logits, topk_ids, mask=mask, coef=coef)
+    logits, ld, ids, mask, index, T, E, k = _router(router_logits, topk_ids, mask)
+    loss, counts = _empty((), (), torch.float32, index), _empty((E,), (1,), torch.int32, index)
+    tokens, stats = _empty((1,), (1,), torch.int32, index), _empty((T, 2), (2, 1), torch.float32, index)
+    n = max(16, (_lib or lib()).situ_moe_balance_loss_workspace_size(T, E))
+    ws = _empty((n,), (1,), torch.uint8, index)
+    args = SituBalanceArgs(logits.data_ptr(), ld, ids.data_ptr(), None if mask is None else mask.data_ptr(), T, E, k, coef,
+                           loss.data_ptr(), counts.data_ptr(), tokens.data_ptr(), stats.data_ptr())
+    _enqueue("situ_moe_balance_loss", index, ctypes.byref(args), ws.data_ptr(), n)
+    return loss, counts, tokens, stats
+
+
+def situ_moe_router_backward(router_logits: torch.Tensor, topk_ids: torch.Tensor, counts, tokens, row_stats, *,
+                             dloss=None, coef: float = 1.0, mask=None, topk_weights=None, dweights=None,
+                             renormalize: bool = True, out=None, stream=None) -> torch.Tensor:
+    """The gradient fp32 [T, E] of the router's logits, from that of the balance
+    loss (``dloss``, one fp32 on the device) with the forward's coef and mask,
+    and those of situ_moe_route_topk's weights (``dweights`` [T, k] beside
+    ``topk_weights``, with its ``renormalize``); either may be None."""
+    if stream is not None:
+        return _on_stream(stream, situ_moe_router_backward, router_logits, topk_ids, counts, tokens, row_stats,
+                          dloss=dloss, coef=coef, mask=mask, topk_weights=topk_weights, dweights=dweights,
+                          renormalize=renormalize, out=out)
+    logits, ld, ids, mask, index, T, E, k = _router(router_logits, topk_ids, mask)
+    if row_stats.shape != (T, 2) or row_stats.dtype is not torch.float32 or not row_stats.is_contiguous():
+        raise ValueError(f"row_stats must be contiguous fp32 [{T}, 2]")
+    _on_device(index, row_stats=row_stats)
+    pl = pc = pt = pw = pd = None
+    if dloss is not None:
+        counts, tokens = _vector(counts, torch.int32, E, "counts", index), _vector(tokens, torch.int32, 1, "tokens", index)
+        dloss = _vector(dloss.reshape(1), torch.float32, 1, "dloss", index)
+        pl, pc, pt = dloss.data_ptr(), counts.data_ptr(), tokens.data_ptr()
+    if dweights is not None:
+        if topk_weights is None:
+            raise ValueError("dweights needs the topk_weights")
+        for name, t in (("topk_weights", topk_weights), ("dweights", dweights)):
+            if t.dtype is not torch.float32 or t.shape != (T, k):
+                raise ValueError(f"{name} must be fp32 [{T}, {k}]")
+        _on_device(index, topk_weights=topk_weights, dweights=dweights)
+        topk_weights, dweights = topk_weights.contiguous(), dweights.contiguous()
+        pw, pd = topk_weights.data_ptr(), dweights.data_ptr()
+    if out is None:
+        out, ldo = _empty((T, E), (E, 1), torch.float32, index), E
+    else:
+        ldo = _given(out, (T, E), torch.float32, index, 1)
+    args = SituRouterBackwardArgs(logits.data_ptr(), ld, ids.data_ptr(), None if mask is None else mask.data_ptr(), T, E, k,
+                                  1 if renormalize else 0, coef, pc, pt, row_stats.data_ptr(), pl, pw, pd, out.data_ptr(),
+                                  ldo)
+    _enqueue("situ_moe_router_backward", index, ctypes.byref(args))
+    return out
+
+
+class _BalancedRoute(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, router_logits, top_k, renormalize, mask, coef):
+        with torch.cuda.device(router_logits.device):
+            ids, weights = situ_moe_route_topk(router_logits, top_k, renormalize)
+            loss, counts, tokens, stats = situ_moe_balance_loss(router_logits, ids, mask=mask, coef=coef)
+        ctx.save_for_backward(router_logits, ids, weights, counts, tokens, stats, mask)
+        ctx.renormalize, ctx.coef = renormalize, coef
+        ctx.mark_non_differentiable(ids, counts)
+        ctx.set_materialize_grads(False)
+        return ids, weights, counts, loss
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, _ids, dweights, _counts, dloss):
+        logits, ids, weights, counts, tokens, stats, mask = ctx.saved_tensors
+        if dweights is None and dloss is None:
+            return None, None, None, None, None
+        d = situ_moe_router_backward(logits, ids, counts, tokens, stats, dloss=dloss, coef=ctx.coef, mask=mask,
+                                     topk_weights=weights, dweights=dweights, renormalize=ctx.renormalize)
+        return d, None, None, None, None
+
+
+def balanced_route(router_logits: torch.Tensor, top_k: int, *, renormalize: bool = True, mask=None, coef: float = 0.01):
+    """situ_moe_route_topk for training: (topk_ids, topk_weights, counts, loss),
+    the weights and the balance loss differentiable in the logits."""
+    return _BalancedRoute.apply(router_logits, top_k, renormalize, mask, coef)
+
+
+def situ_moe_save_mxfp8(x: torch.Tensor, *, out=None, stream=None):
+    """16-bit activations [S, K] kept in 8 bits: (E4M3 uint8 [S, K], UE8M0 uint8
+    [S, ceil(K/32)])."""
+    if stream is not None:
+        return _on_stream(stream, situ_moe_save_mxfp8, x, out=out)
+    index = x.get_device()
+    if x.dtype is not torch.bfloat16 and x.dtype is not torch.float16:
+        raise TypeError("x must be bf16 or f16")
+    if x.dim() != 2 or index < 0:
+        raise ValueError("x must be [S, K] on a CUDA device")
+    S, K = x.shape
+    if (S | K) >> 31:
+        raise _too_large(S, K)
+    nk = -(-K // 32)
+    x, px, ldx = _rows(x, 8)
+    if out is None:
+        q, scale = _empty((S, K), (K, 1), torch.uint8, index), _empty((S, nk), (nk, 1), torch.uint8, index)
+    else:
+        q, scale = out
+        for t, want, what in ((q, (S, K), "q"), (scale, (S, nk), "scale")):
+            if tuple(t.shape) != want or t.dtype is not torch.uint8 or t.get_device() != index or not t.is_contiguous():
+                raise ValueError(f"{what}: needs a contiguous uint8 tensor {want} on cuda:{index}")
+    _enqueue("situ_moe_save_mxfp8", index, px, _DTYPES[x.dtype], S, K, ldx, q.data_ptr(), scale.data_ptr())
+    return q, scale
+
+
+def _kept(q, scale, S, K, blocks, index):
+    """(q, scale) of a kept form, checked and contiguous."""
+    if q.dtype not in _E4M3 or scale.dtype is not torch.uint8:
+        raise TypeError("q must hold E4M3 codes (uint8 or float8_e4m3fn) and scale bytes")
+    if q.shape != (S, K) or scale.shape != (S, blocks):
+        raise ValueError(f"needs q [{S}, {K}] and scale [{S}, {blocks}]")
+    _on_device(index, q=q, scale=scale)
+    if not q.is_contiguous() or q.data_ptr() & 7:
+        q = q.clone(memory_format=torch.contiguous_format)
+    return q, scale if scale.is_contiguous() else scale.contiguous()
+
+
+def situ_moe_restore_mxfp8(q: torch.Tensor, scale: torch.Tensor, dtype=torch.bfloat16, *, out=None,
+                           stream=None) -> torch.Tensor:
+    """What situ_moe_save_mxfp8 kept, as bf16, f16 or fp32 [S, K]."""
+    if stream is not None:
+        return _on_stream(stream, situ_moe_restore_mxfp8, q, scale, dtype, out=out)
+    if dtype not in _DTYPES:
+        raise TypeError("dtype must be bf16, f16 or fp32")
+    index = q.get_device()
+    if q.dim() != 2 or index < 0:
+        raise ValueError("q must be [S, K] on a CUDA device")
+    S, K = q.shape
+    if (S | K) >> 31:
+        raise _too_large(S, K)
+    q, scale = _kept(q, scale, S, K, -(-K // 32), index)
+    if out is None:
+        out, ldx = _empty((S, K), (K, 1), dtype, index), K
+    else:
+        ldx = _given(out, (S, K), dtype, index, 4 if dtype is torch.float32 else 8)
+    _enqueue("situ_moe_restore_mxfp8", index, q.data_ptr(), scale.data_ptr(), _DTYPES[dtype], S, K, out.data_ptr(), ldx)
+    return out
+
+
+def _caps(p0, p1, offsets, index):
+    """(p0, p1, offsets, their pointer, E) of the gated activation, checked."""
+    E = 1 if offsets is None else _groups(offsets, index)
+    p0, p1 = _vector(p0, torch.float32, E, "p0", index), _vector(p1, torch.float32, E, "p1", index)
+    if offsets is not None and not offsets.is_contiguous():
+        offsets = offsets.contiguous()
+    return p0, p1, offsets, None if offsets is None else offsets.data_ptr(), E
+
+
+def situ_moe_gated(gate_up: torch.Tensor, p0: torch.Tensor, p1: torch.Tensor, offsets=None, *,
+                   activation: int = SITU_ACT_FN_SITU, save: bool = False, out=None, stream=None):
+    """The layer's gated activation h [S, I] of 16-bit gate_up [S, 2I] (gate
+    first): SITU with the caps p0 and p1, or SWIGLU_BIAS with alpha p0 and beta
+    p1, fp32 [E] per expert of the rows that ``offsets`` [E + 1] bounds (None:
+    [1], one for all).  Rows of no expert give zeros.  With ``save``: (h, q,
+    scale), gate_up kept in 8 bits for situ_moe_gated_backward."""
+    if stream is not None:
+        return _on_stream(stream, situ_moe_gated, gate_up, p0, p1, offsets, activation=activation, save=save, out=out)
+    index, dtype = gate_up.get_device(), gate_up.dtype
+    if dtype is not torch.bfloat16 and dtype is not torch.float16:
+        raise TypeError("gate_up must be bf16 or f16")
+    if gate_up.dim() != 2 or gate_up.shape[1] % 2 or index < 0:
+        raise ValueError("gate_up must be [S, 2I] on a CUDA device")
+    S, I = gate_up.shape[0], gate_up.shape[1] // 2
+    if (S | 2 * I) >> 31:
+        raise _too_large(S, 2 * I)
+    p0, p1, offsets, poff, E = _caps(p0, p1, offsets, index)
+    x, px, ldx = _rows(gate_up, 8)
+    if out is None:
+        h, ldh = _empty((S, I), (I, 1), dtype, index), I
+    else:
+        h, ldh = out, _given(out, (S, I), dtype, index, 8)
+    q = scale = pq = ps = None
+    if save:
+        nb = 2 * -(-I // 32)
+        q, scale = _empty((S, 2 * I), (2 * I, 1), torch.uint8, index), _empty((S, nb), (nb, 1), torch.uint8, index)
+        pq, ps = q.data_ptr(), scale.data_ptr()
+    args = SituGatedArgs(_DTYPES[dtype], activation, S, I, E, px, ldx, p0.data_ptr(), p1.data_ptr(), poff, h.data_ptr(),
+                         ldh, pq, ps, None, 0, None, 0)
+    _enqueue("situ_moe_gated", index, ctypes.byref(args))
+    return (h, q, scale) if save else h
+
+
+def situ_moe_gated_backward(dh: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, p0: torch.Tensor, p1: torch.Tensor,
+                            offsets=None, *, activation: int = SITU_ACT_FN_SITU, want_h: bool = False, out=None,
+                            stream=None):
+    """From dh [S, I] and what situ_moe_gated kept: (dgate_up [S, 2I], h [S, I]
+    once more, or None without ``want_h``), both at the restored gate and up."""
+    if stream is not None:
+        return _on_stream(stream, situ_moe_gated_backward, dh, q, scale, p0, p1, offsets, activation=activation,
+                          want_h=want_h, out=out)
+    index, dtype = dh.get_device(), dh.dtype
+    if dtype is not torch.bfloat16 and dtype is not torch.float16:
+        raise TypeError("dh must be bf16 or f16")
+    if dh.dim() != 2 or index < 0:
+        raise ValueError("dh must be [S, I] on a CUDA device")
+    S, I = dh.shape
+    if (S | 2 * I) >> 31:
+        raise _too_large(S, 2 * I)
+    q, scale = _kept(q, scale, S, 2 * I, 2 * -(-I // 32), index)
+    p0, p1, offsets, poff, E = _caps(p0, p1, offsets, index)
+    dh, pdh, ldh = _rows(dh, 8)
+    if out is None:
+        out, ldo = _empty((S, 2 * I), (2 * I, 1), dtype, index), 2 * I
+    else:
+        ldo = _given(out, (S, 2 * I), dtype, index, 8)
+    h = _empty((S, I), (I, 1), dtype, index) if want_h else None
+    args = SituGatedArgs(_DTYPES[dtype], activation, S, I, E, None, 0, p0.data_ptr(), p1.data_ptr(), poff,
+                         None if h is None else h.data_ptr(), I, q.data_ptr(), scale.data_ptr(), pdh, ldh, out.data_ptr(),
+                         ldo)
+    _enqueue("situ_moe_gated_backward", index, ctypes.byref(args))
+    return out, h
+
+
+class _ExpertFfn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w1, w2, offsets, p0, p1, activation, keep):
+        gate_up = situ_moe_grouped_gemm(x, w1, offsets)
+        h, q, scale = situ_moe_gated(gate_up, p0, p1, offsets, activation=activation, save=True)
+        kept = situ_moe_save_mxfp8(x) if keep == "mxfp8" and ctx.needs_input_grad[1] else (x, None)
+        ctx.save_for_backward(*kept, q, scale, w1, w2, offsets, p0, p1)
+        ctx.activation, ctx.dtype = activation, x.dtype
+        return situ_moe_grouped_gemm(h, w2, offsets)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        x, x_scale, q, scale, w1, w2, offsets, p0, p1 = ctx.saved_tensors
+        need_x, need_w1, need_w2 = ctx.needs_input_grad[:3]
+        dx = dw1 = dw2 = None
+        dh = situ_moe_grouped_gemm_dgrad(dy, w2, offsets)
+        d, h = situ_moe_gated_backward(dh, q, scale, p0, p1, offsets, activation=ctx.activation, want_h=need_w2)
+        if need_w2:
+            dw2 = situ_moe_grouped_gemm_wgrad(dy, h, offsets)
+        del dh, h
+        if need_x:
+            dx = situ_moe_grouped_gemm_dgrad(d, w1, offsets)
+        if need_w1:
+            dw1 = situ_moe_grouped_gemm_wgrad(d, x if x_scale is None else situ_moe_restore_mxfp8(x, x_scale, ctx.dtype),
+                                              offsets)
+        return dx, dw1, dw2, None, None, None, None, None
+
+
+def expert_ffn(x: torch.Tensor, w1: torch.Tensor, w2: torch.Tensor, offsets: torch.Tensor, p0: torch.Tensor,
+               p1: torch.Tensor, *, activation: int = SITU_ACT_FN_SITU, keep: str = "mxfp8") -> torch.Tensor:
+    """The routed experts for training: y = w2_e gated(w1_e x) over rows sorted by
+    expert, differentiable in x [S, H], w1 [E, 2I, H] and w2 [E, H, I].  For the
+    backward pass it keeps the gate/up columns in 8 bits, x in 8 bits
+    (``keep`` "mxfp8") or as it is ("16bit"), and no h: 2 I + H bytes a row and
+    a 32nd, where 16 bits take 6 I + 2 H."""
+    if keep not in ("mxfp8", "16bit"):
+        raise ValueError('keep must be "mxfp8" or "16bit"')
+    if w1.dim() != 3 or w2.dim() != 3:
+        raise ValueError("w1 must be [E, 2I, H] and w2 [E, H, I]")
+    return _ExpertFfn.apply(x, w1, w2, offsets, p0, p1, activation, keep)
+
+
+def _adapters(x, a, b, scale, index):
+    """Checks an adapter set beside x [S, K]: (a, b, scale, S, K, N, r, n)."""
+    dtype = x.dtype
+    if dtype is not torch.bfloat16 and dtype is not torch.float16 or a.dtype is not dtype or b.dtype is not dtype:
+        raise TypeError("x, a and b must be all bf16 or all f16")
+    if x.dim() != 2 or a.dim() != 3 or b.dim() != 3:
+        raise ValueError("needs x [S, K], a [n, r, K] and b [n, N, r]")
+    S, K = x.shape
+    n, r, Ka = a.shape
+    N = b.shape[1]
+    if Ka != K or b.shape != (n, N, r):
+        raise ValueError(f"needs a [n, r, {K}] and b [n, N, r], not {tuple(a.shape)} and {tuple(b.shape)}")
+    if (S | K | N | n) >> 31:
+        raise _too_large(S, K, N, n)
+    if index < 0 or a.get_device() != index or b.get_device() != index:
+        raise ValueError(f"the operands must be on one CUDA device, not on {x.device}, {a.device} and {b.device}")
+    if scale is not None:
+        scale = _vector(scale, torch.float32, n, "scale", index)
+    return _packed(a)[0], _packed(b)[0], scale, S, K, N, r, n
+
+
+def _beside(t, shape, dtypes, name, index):
+    """(tensor, pointer, elements between rows) of base or dx0."""
+    if tuple(t.shape) != shape or t.dtype not in dtypes:
+        raise ValueError(f"{name} must be {shape} of the operands' type or fp32, not {tuple(t.shape)} of {t.dtype}")
+    _on_device(index, **{name: t})
+    return _rows(t, 4 if t.dtype is torch.float32 else 8)
+
+
+def situ_moe_lora(base, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, *, ids=None, offsets=None, scale=None, out=None,
+                  keep: bool = False, stream=None):
+    """base + scale[e] (x a[e].T) b[e].T row by row: base [S, N] the shared
+    projection of x [S, K] (None: zeros, of x's type), a [n, r, K] and b
+    [n, N, r], e = ids[i] (int32 [S]; outside [0, n): no adapter) or the one
+    whose rows ``offsets`` [n + 1] bounds.  ``out`` may be base.  ``keep``
+    returns (out, u [S, r]) for situ_moe_lora_backward."""
+    if stream is not None:
+        return _on_stream(stream, lambda x, a, b, base, **kw: situ_moe_lora(base, x, a, b, **kw), x, a, b, base, ids=ids,
+                          offsets=offsets, scale=scale, out=out, keep=keep)
+    index = x.get_device()
+    a, b, scale, S, K, N, r, n = _adapters(x, a, b, scale, index)
+    if (ids is None) == (offsets is None):
+        raise ValueError("needs one of ids and offsets")
+    dtype, pids, poff = x.dtype, None, None
+    if ids is not None:
+        ids = _vector(ids, torch.int32, S, "ids", index)
+        pids = ids.data_ptr()
+    else:
+        if _groups(offsets, index) != n:
+            raise ValueError(f"offsets must be [{n + 1}]")
+        if not offsets.is_contiguous():
+            offsets = offsets.contiguous()
+        poff = offsets.data_ptr()
+    x, px, ldx = _rows(x, 8)
+    pbase, ld_base, out_dtype = None, 0, dtype if out is None else out.dtype
+    if base is not None:
+        base, pbase, ld_base = _beside(base, (S, N), (dtype, torch.float32), "base", index)
+        out_dtype = base.dtype
+    if out is None:
+        out, ldo = _empty((S, N), (N, 1), out_dtype, index), N
+    else:
+        ldo = _given(out, (S, N), out_dtype, index, 4 if out_dtype is torch.float32 else 8)
+    u = _empty((S, r), (r, 1), dtype, index) if keep else None
+    size = (_lib or lib()).situ_moe_lora_workspace_size(S, K, N, r)
+    ws = _empty((max(16, size),), (1,), torch.uint8, index)
+    args = SituLoraArgs(_DTYPES[dtype], _DTYPES.get(out_dtype, -1), S, K, N, r, n, px, ldx, a.data_ptr(), b.data_ptr(), pids,
+                        poff, None if scale is None else scale.data_ptr(), pbase, ld_base, out.data_ptr(), ldo,
+                        None if u is None else u.data_ptr())
+    _enqueue("situ_moe_lora", index, ctypes.byref(args), ws.data_ptr(), max(16, size))
+    return (out, u) if keep else out
+
+
+def situ_moe_lora_backward(dy: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, offsets: torch.Tensor,
+                           u: torch.Tensor, *, scale=None, dx=None, out=None, stream=None):
+    """The gradients of situ_moe_lora with rows sorted by adapter, from dy [S, N]
+    and its u: (dx [S, K], da, db).  ``dx`` is what x's gradient is added to
+    (that of the shared projection; None: zeros, of x's type), and ``out``,
+    which may be it, receives the sum."""
+    if stream is not None:
+        return _on_stream(stream, situ_moe_lora_backward, dy, x, a, b, offsets, u, scale=scale, dx=dx, out=out)
+    index = x.get_device()
+    a, b, scale, S, K, N, r, n = _adapters(x, a, b, scale, index)
+    dtype = x.dtype
+    if dy.dtype is not dtype or u.dtype is not dtype:
+        raise TypeError(f"dy and u must be {dtype}, as x")
+    if dy.shape != (S, N) or u.shape != (S, r):
+        raise ValueError(f"needs dy {(S, N)} and u {(S, r)}")
+    _on_device(index, dy=dy, u=u)
+    if _groups(offsets, index) != n:
+        raise ValueError(f"offsets must be [{n + 1}]")
+    if not offsets.is_contiguous():
+        offsets = offsets.contiguous()
+    x, px, ldx = _rows(x, 8)
+    dy, pdy, ld_dy = _rows(dy, 8)
+    u, pu = _packed(u)
+    pdx0, ld_dx0, dx_dtype = None, 0, dtype if out is None else out.dtype
+    if dx is not None:
+        dx, pdx0, ld_dx0 = _beside(dx, (S, K), (dtype, torch.float32), "dx", index)
+        dx_dtype = dx.dtype
+    if out is None:
+        out, ldo = _empty((S, K), (K, 1), dx_dtype, index), K
+    else:
+        ldo = _given(out, (S, K), dx_dtype, index, 4 if dx_dtype is torch.float32 else 8)
+    da, db = _empty((n, r, K), (r * K, K, 1), dtype, index), _empty((n, N, r), (N * r, r, 1), dtype, index)
+    size = (_lib or lib()).situ_moe_lora_backward_workspace_size(S, K, N, r)
+    ws = _empty((max(16, size),), (1,), torch.uint8, index)
+    args = SituLoraBackwardArgs(_DTYPES[dtype], _DTYPES.get(dx_dtype, -1), S, K, N, r, n, pdy, ld_dy, px, ldx, a.data_ptr(),
+                                b.data_ptr(), offsets.data_ptr(), None if scale is None else scale.data_ptr(), pu, pdx0,
+                                ld_dx0, out.data_ptr(), ldo, da.data_ptr(), db.data_ptr(), _status_word(index).data_ptr())
+    _enqueue("situ_moe_lora_backward", index, ctypes.byref(args), ws.data_ptr(), max(16, size))
+    return out, da, db
+
+
+class _LoraLinear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, base, x, a, b, offsets, scale):
+        y, u = situ_moe_lora(base, x, a, b, offsets=offsets, scale=scale, keep=True)
+        ctx.save_for_backward(x, a, b, offsets, u, scale)
+        return y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        x, a, b, offsets, u, scale = ctx.saved_tensors
+        dx = da = db = None
+        if any(ctx.needs_input_grad[1:4]):
+            dx, da, db = situ_moe_lora_backward(dy.to(x.dtype), x, a, b, offsets, u, scale=scale)
+        return dy, dx, da, db, None, None
+
+
+def lora_linear(base: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, offsets: torch.Tensor,
+                scale=None) -> torch.Tensor:
+    """situ_moe_lora for training, rows sorted by adapter: differentiable in
+    base, x, a and b."""
+    return _LoraLinear.apply(base, x, a, b, offsets, scale)
 
 
 class Layer:

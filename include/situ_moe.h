@@ -608,6 +608,200 @@ typedef struct situ_fp8_gemm_args {
 } situ_fp8_gemm_args;
 situ_status situ_moe_fp8_gemm(const situ_fp8_gemm_args* args, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Fine-tuning the expert layer: the router's balance loss and gradient, the
+ * gated activation with its input kept in 8 bits, and low-rank adapters.
+ * These operators have no counterpart in the pages; adapters beside this layer
+ * are what the FlashInfer 0.6.18 MoE-LoRA notes are about, without a
+ * definition.  No kernel of theirs waits on another, so none has a status.
+ * --------------------------------------------------------------------- */
+
+/* situ_moe_balance_loss -- over the n tokens whose mask byte is not 0 (all with
+ * mask NULL), with p = softmax(logits) over all E = num_experts_total experts
+ * and c_e the slots of these tokens that name expert e (IDs outside [0, E)
+ * name none):
+ *   loss = coef E sum_e f_e P_e,  f_e = c_e / (n top_k),  P_e = mean_t p[t, e]
+ * and 0 where n = 0.  A perfectly even routing gives coef.  Also written:
+ * counts[e] = c_e, tokens = n, and per row (masked ones too) its largest logit
+ * and 1 / sum exp(l - largest), which the gradient takes.  A row of -inf has
+ * p = 0; a NaN or +inf makes its row's p NaN.  What a masked row holds reaches
+ * neither loss nor counts.  Sums are fp32 over a few hundred rows and fp64
+ * beyond, in a fixed order.  T == 0 gives zeros.  E up to
+ * SITU_MAX_LOCAL_EXPERTS; rows ld elements apart.
+ * Errors: NULL_ARG, BAD_SHAPE, MISALIGNED (row_stats 8 bytes, workspace 16),
+ * WORKSPACE_TOO_SMALL, CUDA. */
+typedef struct situ_balance_args {
+  const float* router_logits;     /* fp32 [T, E] */
+  int64_t ld;
+  const int32_t* topk_ids;        /* int32 [T, top_k], as situ_moe_route_topk gives them */
+  const uint8_t* mask;            /* [T] or NULL */
+  int32_t T, num_experts_total, top_k;
+  float coef;
+  float* loss;                    /* [1] */
+  int32_t* counts;                /* [E] */
+  int32_t* tokens;                /* [1] */
+  float* row_stats;               /* [T, 2] */
+} situ_balance_args;
+size_t situ_moe_balance_loss_workspace_size(int32_t T, int32_t num_experts_total);
+situ_status situ_moe_balance_loss(const situ_balance_args* args, void* workspace, size_t workspace_bytes,
+                                  void* stream);
+
+/* situ_moe_router_backward -- the gradient of the router's logits, from that
+ * of the balance loss (dloss, or NULL: none) and those of the routing weights
+ * (dweights [T, top_k], or NULL: none):
+ *   dlogits[t, e] = dloss coef E / n p (f_e - sum_j f_j p[t, j])     where the mask is not 0
+ *     + w_j (dw_j - sum_i w_i dw_i)                at e = topk_ids[t, j] (renormalize = 1)
+ *     or + w_j dw_j at those, - p sum_i w_i dw_i   at every e            (renormalize = 0)
+ * for the routing weights w that situ_moe_route_topk gave with that
+ * `renormalize`.  counts and tokens are the forward's, or their sums over
+ * several ranks' tokens (f_e is a constant here; the gradient is then that of
+ * this rank's tokens in the joint loss).  Terms of an ID that a row names
+ * twice are added; IDs outside [0, E) take none.  A masked row without weight
+ * gradients gives zeros, whatever its logits hold.  Results do not depend on
+ * the order of execution.  Errors: as above, UNSUPPORTED (renormalize). */
+typedef struct situ_router_backward_args {
+  const float* router_logits;
+  int64_t ld;
+  const int32_t* topk_ids;
+  const uint8_t* mask;
+  int32_t T, num_experts_total, top_k, renormalize;
+  float coef;
+  const int32_t* counts;
+  const int32_t* tokens;
+  const float* row_stats;
+  const float* dloss;             /* [1] on the device, or NULL */
+  const float* topk_weights;
+  const float* dweights;          /* [T, top_k], or NULL */
+  float* dlogits;                 /* fp32 [T, E], rows ldo apart */
+  int64_t ldo;
+} situ_router_backward_args;
+situ_status situ_moe_router_backward(const situ_router_backward_args* args, void* stream);
+
+/* situ_moe_save_mxfp8, situ_moe_restore_mxfp8 -- 16-bit activations kept in 8
+ * bits for a backward pass: x [S, K] (rows ldx apart) as E4M3 codes q [S, K]
+ * and one UE8M0 byte per 32 columns, scale [S, ceil(K/32)], by the rule of
+ * situ_moe_quant_mxfp8 (the same bytes for bf16 and K a multiple of 32); the
+ * last block may be partial.  A block with an infinity or a NaN gets scale
+ * byte 255 and NaN codes: all of it is restored as NaN.  Restoring gives q 2^(b
+ * - 127) in bf16, f16 or fp32, exact but for values beyond a 16-bit type's
+ * range, which become its largest (a block's largest element may have been
+ * rounded up past it).  K a multiple of 8, ldx too; x 16-byte aligned, q 8.
+ * Errors: NULL_ARG, BAD_SHAPE, UNSUPPORTED (dtype), MISALIGNED, CUDA. */
+situ_status situ_moe_save_mxfp8(const void* x, int32_t dtype, int32_t S, int32_t K, int64_t ldx, uint8_t* q,
+                                uint8_t* scale, void* stream);
+situ_status situ_moe_restore_mxfp8(const uint8_t* q, const uint8_t* scale, int32_t dtype, int32_t S, int32_t K, void* x,
+                                   int64_t ldx, void* stream);
+
+/* situ_moe_gated -- the layer's gated activation on the 16-bit products' gate
+ * and up columns (gate_up [S, 2I], gate first):
+ *   SITU          h = [b tanh(g/b) sigmoid(g)] [bl tanh(u/bl)],  b = p0[e], bl = p1[e]
+ *   SWIGLU_BIAS   h = g sigmoid(p0[e] g) (u + p1[e])
+ * in fp32, rounded once to the operands' type; e is the expert whose rows
+ * [offsets[e], offsets[e + 1]) hold the row (offsets ascending, as
+ * situ_moe_permute's expert_offsets), or 0 for every row with offsets NULL.  A
+ * cap <= 0 switches its factor to its limit, as in situ_moe_forward.  With q
+ * and scale not NULL, gate_up is kept as situ_moe_save_mxfp8 of the rows of
+ * both halves: q [S, 2I], scale [S, 2 ceil(I/32)] (gate's blocks first).  Rows
+ * of no expert give h = 0 and are kept as zeros.
+ *
+ * situ_moe_gated_backward -- from the kept form and dh [S, I]: dgate_up
+ * [S, 2I] = dh dh/d(g, u) at the restored g and u, and with h not NULL the
+ * activation of these once more (what the down weights' gradient needs, so
+ * that h need not be kept).  Rows of no expert give zeros.
+ * I a multiple of 8, rows strided by multiples of 8 elements; pointers 16-byte
+ * aligned, q 8, p0, p1 and offsets 4.  E up to SITU_MAX_LOCAL_EXPERTS.
+ * Errors: NULL_ARG, BAD_SHAPE, UNSUPPORTED (dtype, activation), MISALIGNED,
+ * CUDA. */
+typedef struct situ_gated_args {
+  int32_t dtype;                  /* SITU_DT_BF16 or SITU_DT_F16 */
+  int32_t activation;             /* situ_act_fn */
+  int32_t S, I, E;
+  const void* gate_up;            /* forward: [S, 2I], rows ld_gate_up apart */
+  int64_t ld_gate_up;
+  const float *p0, *p1;           /* fp32 [E] */
+  const int32_t* offsets;         /* int32 [E + 1], or NULL (E = 1) */
+  void* h;                        /* [S, I], rows ldh apart (backward: or NULL) */
+  int64_t ldh;
+  uint8_t* q;                     /* forward: or NULL; backward: read */
+  uint8_t* scale;
+  const void* dh;                 /* backward: [S, I], rows ld_dh apart */
+  int64_t ld_dh;
+  void* dgate_up;                 /* backward: [S, 2I], rows ld_dgate_up apart */
+  int64_t ld_dgate_up;
+} situ_gated_args;
+situ_status situ_moe_gated(const situ_gated_args* args, void* stream);
+situ_status situ_moe_gated_backward(const situ_gated_args* args, void* stream);
+
+/* situ_moe_lora -- low-rank adapters of many requests beside a projection
+ * that they share: row i of x [S, K] takes adapter e = ids[i] (none where that
+ * is outside [0, n)), or with offsets the adapter whose rows [offsets[e],
+ * offsets[e + 1]) hold i (ascending, as situ_moe_permute's expert_offsets):
+ *   u[i] = scale[e] x[i] a[e]^T,   out[i] = base[i] + u[i] b[e]^T
+ * a [n, r, K], b [n, N, r] (contiguous), r a multiple of 8 up to 128.  Rows
+ * without an adapter give base; base NULL: zeros; it may be out itself, or not
+ * overlap it.  base and out are of one type, that of the operands or fp32.
+ * Sums are fp32, out is rounded once; on more than a few rows u enters the
+ * second product rounded to 16 bits for 16-bit results, with 22 bits or more
+ * for fp32 ones.  u (or NULL) receives u [S, r] in the operands' type (zeros
+ * without an adapter), which the gradients take.  For experts, an adapter per
+ * (request's adapter, expert) pair is one of n, its rows in any order.
+ * Results do not depend on the order of execution, nor on what other rows'
+ * adapters hold.  K, N multiples of 8, rows strided by multiples of 8 elements
+ * (fp32: 4), pointers 16-byte aligned, ids, offsets, scale 4.
+ * Errors: NULL_ARG (one of ids and offsets is given), BAD_SHAPE, UNSUPPORTED,
+ * MISALIGNED, WORKSPACE_TOO_SMALL, CUDA. */
+#define SITU_LORA_MAX_ADAPTERS (1 << 20)
+typedef struct situ_lora_args {
+  int32_t dtype, out_dtype;       /* situ_dtype */
+  int32_t S, K, N, r, n;
+  const void* x;
+  int64_t ldx;
+  const void* a;
+  const void* b;
+  const int32_t* ids;             /* int32 [S], or NULL */
+  const int32_t* offsets;         /* int32 [n + 1], or NULL */
+  const float* scale;             /* fp32 [n], or NULL: 1 */
+  const void* base;               /* [S, N], rows ld_base apart, or NULL */
+  int64_t ld_base;
+  void* out;                      /* [S, N], rows ldo apart */
+  int64_t ldo;
+  void* u;                        /* [S, r], or NULL */
+} situ_lora_args;
+size_t situ_moe_lora_workspace_size(int32_t S, int32_t K, int32_t N, int32_t r);
+situ_status situ_moe_lora(const situ_lora_args* args, void* workspace, size_t workspace_bytes, void* stream);
+
+/* situ_moe_lora_backward -- from dy [S, N] and the forward's u, rows sorted by
+ * adapter (offsets; n up to SITU_GEMM_MAX_GROUPS):
+ *   v = scale dy b,  dx = dx0 + v a,  da[e] = v^T x,  db[e] = dy^T u   over e's rows
+ * dx0 (or NULL: zeros) is the shared projection's gradient, dx may be it, both
+ * of the operands' type or fp32; da [n, r, K] and db [n, N, r] are of the
+ * operands' type, zeros for an adapter without rows, products of v and u
+ * rounded to it.  The last two are situ_moe_grouped_gemm's, with its
+ * device_status.  S == 0 sets da and db to zeros. */
+typedef struct situ_lora_backward_args {
+  int32_t dtype, dx_dtype;
+  int32_t S, K, N, r, n;
+  const void* dy;
+  int64_t ld_dy;
+  const void* x;
+  int64_t ldx;
+  const void* a;
+  const void* b;
+  const int32_t* offsets;
+  const float* scale;
+  const void* u;                  /* [S, r] */
+  const void* dx0;
+  int64_t ld_dx0;
+  void* dx;
+  int64_t ld_dx;
+  void* da;
+  void* db;
+  int32_t* device_status;
+} situ_lora_backward_args;
+size_t situ_moe_lora_backward_workspace_size(int32_t S, int32_t K, int32_t N, int32_t r);
+situ_status situ_moe_lora_backward(const situ_lora_backward_args* args, void* workspace, size_t workspace_bytes,
+                                   void* stream);
+
 #ifdef __cplusplus
 }
 #endif
