@@ -96,7 +96,8 @@ class SituLoraArgs(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("dtype", "out_dtype", "S", "K", "N", "r", "n")] + [
         ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("a", ctypes.c_void_p), ("b", ctypes.c_void_p),
         ("ids", ctypes.c_void_p), ("offsets", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("base", ctypes.c_void_p),
-        ("ld_base", ctypes.c_int64), ("out", ctypes.c_void_p), ("ldo", ctypes.c_int64), ("u", ctypes.c_void_p)]
+        ("ld_base", ctypes.c_int64), ("out", ctypes.c_void_p), ("ldo", ctypes.c_int64), ("u", ctypes.c_void_p),
+        ("device_status", ctypes.c_void_p)]
 
 
 class SituLoraBackwardArgs(ctypes.Structure):
@@ -1178,7 +1179,7 @@ def situ_moe_lora(base, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, *, id
     ws = _empty((max(16, size),), (1,), torch.uint8, index)
     args = SituLoraArgs(_DTYPES[dtype], _DTYPES.get(out_dtype, -1), S, K, N, r, n, px, ldx, a.data_ptr(), b.data_ptr(), pids,
                         poff, None if scale is None else scale.data_ptr(), pbase, ld_base, out.data_ptr(), ldo,
-                        None if u is None else u.data_ptr())
+                        None if u is None else u.data_ptr(), _status_word(index).data_ptr())
     _enqueue("situ_moe_lora", index, ctypes.byref(args), ws.data_ptr(), max(16, size))
     return (out, u) if keep else out
 

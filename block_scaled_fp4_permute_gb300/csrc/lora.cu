@@ -32,29 +32,29 @@
 // f16 rows are brought to [2^14, 2^15) by a power of two first, taken out of the
 // sums again, so that a u beyond f16 neither overflows nor vanishes.
 #include "../../include/situ_moe.h"
-#include "situ_internal.h"
+#include "gemm_groups.cuh"
 
 #include <cooperative_groups.h>
 
 namespace situ {
 
+using namespace gg;
+
 namespace {
 
-constexpr int kTile = 64;          // rows of a tile, 16 per warp
-constexpr int kTileThreads = 128;
+constexpr int kTile = 128;         // rows of a tile
 constexpr int kChunk = 64;         // contraction elements of a stage (shrink)
-constexpr int kStages = 4;
+constexpr int kStages = 4;         // of shrink
+constexpr int kMaxStages = 3;      // of expand
 constexpr int kCols = 128;         // columns of a step (expand)
 constexpr int kMaxRank = 128;
 constexpr int kCluster = 8;        // CTAs of a row
 constexpr int kRowThreads = 256;
 
 struct LoraParams {
-  const void* x;                   // shrink's rows
-  long ldx;
-  const void* w;                   // this kernel's adapter factor
   const int32_t *ids, *offsets;
   int S, C, r, n;                  // C: the other extent (contraction or columns)
+  int r16;                         // r rounded up to 16
   int splits, chunks;              // shrink: parts of the contraction, stages in all
   float* part;                     // [splits][S][r]
   const float* scale;              // [n] or null
@@ -64,7 +64,12 @@ struct LoraParams {
   long ldo;
   void* u16;                       // [S, r] scaled, of the operands' type, or null
   int groups;                      // expand: column groups of a tile
+  int stages, w_stage, u_bytes;    // shared memory: stages of w (expand), bytes of one, of u
+  int* err;
 };
+
+// 16-bit terms that u is taken in
+__host__ __device__ constexpr int terms_of(int dt, bool f32) { return !f32 ? 1 : dt == SITU_DT_BF16 ? 3 : 2; }
 
 struct RowParams {
   const void *x, *a, *b, *base;
@@ -213,543 +218,637 @@ lora_row_kernel(RowParams p) {
 }
 
 // --------------------------------------------------------------------------
-// tiles of 64 rows
+// tiles of 128 rows
 // --------------------------------------------------------------------------
-
-__device__ __forceinline__ uint32_t smem_at(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-// 16 bytes to shared memory, zeros where `have` is false
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool have) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(have ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool have) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(have ? 4 : 0) : "memory");
-}
-__device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void wait_copies() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-template <bool TRANS>
-__device__ __forceinline__ void ldmatrix4(uint32_t (&d)[4], uint32_t at) {
-  if (TRANS)
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3]) : "r"(at) : "memory");
-  else
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3]) : "r"(at) : "memory");
-}
-template <int DT>
-__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  if (DT == SITU_DT_BF16)
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  else
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
 
 // A tile's adapters: each row's (kNone: none, kNoRow: past the end), and the
 // distinct ones in the order of their first rows.
 constexpr int kNone = -1, kNoRow = -2;
 struct Adapters {
-  int of[kTile];       // row -> adapter
+  alignas(16) int of[kTile];   // row -> adapter
   int at[kTile];       // row -> its place in `list`, or kNone / kNoRow
   int list[kTile];
+  uint32_t lead[kTile / 32];
   int count;
 };
+// by all threads of the block, kTile or more
 __device__ __forceinline__ void find_adapters(Adapters& t, const LoraParams& p, int row0) {
   const int i = threadIdx.x;
-  if (i < kTile) t.of[i] = row0 + i < p.S ? adapter_of(p.ids, p.offsets, p.n, row0 + i) : kNoRow;
+  const bool mine = i < kTile;
+  int e = kNoRow;
+  if (mine) {
+    e = row0 + i < p.S ? adapter_of(p.ids, p.offsets, p.n, row0 + i) : kNoRow;
+    t.of[i] = e;
+  }
   __syncthreads();
-  const bool same = __syncthreads_and(i >= kTile || t.of[i] == t.of[0] || t.of[i] == kNoRow);
-  if (same) {
-    if (i < kTile) t.at[i] = t.of[i] >= 0 ? 0 : t.of[i];
+  const int e0 = t.of[0];
+  if (__syncthreads_and(!mine || e == e0 || e == kNoRow)) {
+    if (mine) t.at[i] = e >= 0 ? 0 : e;
     if (i == 0) {
-      t.list[0] = t.of[0];
-      t.count = t.of[0] >= 0 ? 1 : 0;
+      t.list[0] = e0;
+      t.count = e0 >= 0 ? 1 : 0;
     }
-  } else if (i < 32) {
-    // the first row of each adapter, by the first warp: rows i and i + 32
-    int first[2];
-    unsigned lead[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int e = t.of[i + 32 * h];
-      first[h] = i + 32 * h;
-      for (int j = 0; j < i + 32 * h; ++j)
-        if (t.of[j] == e) {
-          first[h] = j;
-          break;
-        }
-      lead[h] = __ballot_sync(0xffffffffu, e >= 0 && first[h] == i + 32 * h);
+    __syncthreads();
+    return;
+  }
+  int first = i;       // the first row of this one's adapter
+  if (mine && e >= 0) {
+    const int4* of = reinterpret_cast<const int4*>(t.of);
+    for (int j = 0; 4 * j < i; ++j) {
+      const int4 v = of[j];
+      const int f = v.x == e ? 0 : v.y == e ? 1 : v.z == e ? 2 : v.w == e ? 3 : 4;
+      if (f < 4) {
+        first = min(i, 4 * j + f);
+        break;
+      }
     }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int e = t.of[i + 32 * h], f = first[h];
-      const int place = f < 32 ? __popc(lead[0] & ((1u << f) - 1u))
-                               : __popc(lead[0]) + __popc(lead[1] & ((1u << (f - 32)) - 1u));
-      t.at[i + 32 * h] = e >= 0 ? place : e;
-      if (e >= 0 && f == i + 32 * h) t.list[place] = e;
-    }
-    if (i == 0) t.count = __popc(lead[0]) + __popc(lead[1]);
+  }
+  if (mine) {
+    __syncwarp();
+    const uint32_t lead = __ballot_sync(0xffffffffu, e >= 0 && first == i);
+    if ((i & 31) == 0) t.lead[i >> 5] = lead;
+  }
+  __syncthreads();
+  if (mine) {
+    int place = __popc(t.lead[first >> 5] & ((1u << (first & 31)) - 1u));
+    for (int w = 0; w < first >> 5; ++w) place += __popc(t.lead[w]);
+    t.at[i] = e >= 0 ? place : e;
+    if (e >= 0 && first == i) t.list[place] = e;
+    if (i == 0) t.count = __popc(t.lead[0]) + __popc(t.lead[1]) + __popc(t.lead[2]) + __popc(t.lead[3]);
   }
   __syncthreads();
 }
-// Which of a tile's adapters the warp's 16 rows take (bit d: list[d]).
-__device__ __forceinline__ uint64_t adapters_of_warp(const Adapters& t) {
-  const int lane = threadIdx.x & 31, a = t.at[(threadIdx.x >> 5) * 16 + (lane & 15)];
-  const uint32_t lo = __reduce_or_sync(0xffffffffu, a >= 0 && a < 32 ? 1u << a : 0u);
-  const uint32_t hi = __reduce_or_sync(0xffffffffu, a >= 32 ? 1u << (a - 32) : 0u);
-  return (uint64_t)hi << 32 | lo;
-}
 
-constexpr int kXPitch = kChunk + 8;   // elements: 144 bytes, ldmatrix without conflicts
-
-template <int RP, bool TRANS>
-struct ShrinkCfg {
-  static constexpr int kWPitch = TRANS ? RP + 8 : kXPitch;
-  static constexpr int kWRows = TRANS ? kChunk : RP;
-  static constexpr int kXBytes = kTile * kXPitch * 2, kWBytes = kWRows * kWPitch * 2;
-  static constexpr int kSmem = kStages * (kXBytes + kWBytes);
+// A ring whose length the launch chooses.
+struct Turns {
+  int n, s = 0, used = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ explicit Turns(int stages) : n(stages) {}
+  __device__ __forceinline__ bool again() const { return used == n; }   // the stage has been used before
+  __device__ __forceinline__ void next() {
+    if (used < n) ++used;
+    if (++s == n) {
+      s = 0;
+      ph ^= 1;
+    }
+  }
+  // wait(stage, parity) for the last use of each stage
+  template <class Wait>
+  __device__ __forceinline__ bool last(Wait&& wait) const {
+    bool ok = true;
+    for (int j = 0; j < used; ++j) ok = wait(j, j < s ? ph : ph ^ 1) && ok;
+    return ok;
+  }
 };
 
-// part[split][i][j] = sum over the split's k of x[i, k] W[e(i)][j][k] (TRANS: W[e][k][j]).
-template <int DT, int RP, bool TRANS>
-__global__ void __launch_bounds__(kTileThreads)
-shrink_kernel(LoraParams p) {
-  using Cfg = ShrinkCfg<RP, TRANS>;
-  extern __shared__ __align__(16) uint8_t smem[];
+constexpr int kXBytes = kTile * 128;          // 64 elements of 128 rows
+constexpr int kTmemCols = 256;                // of a CTA: two CTAs per SM
+constexpr int kShrinkThreads = 192;           // copies, MMAs, four epilogue warps
+constexpr int kExpandThreads = 320;           // copies, MMAs, eight epilogue warps
+constexpr int kEpiThreads = 256;
+constexpr int kStagePitch = 36;               // floats of a row of a warp's 32 x 32 sums in shared memory
+
+// D[128, N] of 16-bit operands in fp32; trans_b: B's N elements contiguous
+__device__ __forceinline__ uint32_t idesc_of(bool bf16, bool trans_b, int N) {
+  return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (trans_b ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) |
+         ((uint32_t)(128 >> 4) << 24);
+}
+
+// part[split][i][j] = sum over the split's k of x[i, k] W[e(i)][j][k] (TRANS:
+// W[e][k][j]): the tile's rows on the MMA's M side, an adapter's r on its N
+// side, in TMEM columns of its own.  As many adapters as the columns hold share
+// a pass over x.
+template <int DT, bool TRANS>
+__global__ void __launch_bounds__(kShrinkThreads)
+shrink_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w, const LoraParams p) {
+  extern __shared__ uint8_t smem_raw[];
   __shared__ Adapters ad;
+  __shared__ uint64_t bars[4 * kStages + 3];
+  __shared__ uint32_t holder[2];
+  const uint32_t sbase = (saddr(smem_raw) + 1023) & ~1023u;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int row0 = blockIdx.x * kTile, split = blockIdx.y;
+  const uint32_t bar0 = saddr(bars);
+  auto xfull = [&](int s) { return bar0 + 8 * s; };
+  auto xempty = [&](int s) { return bar0 + 8 * (kStages + s); };
+  auto wfull = [&](int s) { return bar0 + 8 * (2 * kStages + s); };
+  auto wempty = [&](int s) { return bar0 + 8 * (3 * kStages + s); };
+  const uint32_t acc_full = bar0 + 8 * 4 * kStages, acc_empty = acc_full + 8, drain = acc_full + 16;
+  if (tid == 0) {
+    holder[1] = (uint32_t)*reinterpret_cast<volatile int*>(p.err);   // an earlier launch gave up a wait: no work then
+    prefetch_map(&map_x);
+    prefetch_map(&map_w);
+    for (int s = 0; s < 4 * kStages; ++s) mbar_init(bar0 + 8 * s, 1);
+    mbar_init(acc_full, 1);
+    mbar_init(acc_empty, 4);
+    mbar_init(drain, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) tmem_alloc<1>(saddr(holder), kTmemCols);
   find_adapters(ad, p, row0);
-  const int nd = ad.count;
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const uint32_t tmem = holder[0];
+  const int nd = holder[1] != 0 ? 0 : ad.count, per = kTmemCols / p.r16;
   const int k0 = (int)((long)p.chunks * split / p.splits), k1 = (int)((long)p.chunks * (split + 1) / p.splits);
-  const int total = nd * (k1 - k0), pairs = (p.r + 15) / 16;
-  const uint32_t xs = smem_at(smem), ws = xs + kStages * Cfg::kXBytes;
-  const uint16_t* x = static_cast<const uint16_t*>(p.x);
-  const uint16_t* w = static_cast<const uint16_t*>(p.w);
-  // the step that is copied next: chunk and place in the list
-  int lk = k0, ld = 0;
-  auto load = [&](int stage) {
-    const int c0 = lk * kChunk;
-    if (ld == 0) {                   // a chunk of x serves all the adapters
-      const uint32_t at = xs + (lk - k0) % kStages * Cfg::kXBytes;
-#pragma unroll
-      for (int i = 0; i < kTile * kChunk / 8 / kTileThreads; ++i) {
-        const int piece = tid + i * kTileThreads, r = piece / (kChunk / 8), c = piece % (kChunk / 8) * 8;
-        const bool have = row0 + r < p.S && c0 + c < p.C;
-        copy16(at + (r * kXPitch + c) * 2, have ? x + (size_t)(row0 + r) * p.ldx + c0 + c : x, have);
+  const uint32_t wbase = sbase + kStages * kXBytes;
+  const int wboxes = (p.r + 63) / 64;
+
+  if (warp == 0) {
+    // ---------------- copies ----------------
+    const bool leader = elect_one();
+    Turns x(kStages), w(kStages);
+    bool ok = true;
+    for (int d0 = 0; d0 < nd && ok; d0 += per) {
+      const int d1 = min(nd, d0 + per);
+      for (int k = k0; k < k1 && ok; ++k) {
+        if (x.again() && !warp_wait(xempty(x.s), x.ph ^ 1, p.err, 81)) {
+          ok = false;
+          break;
+        }
+        if (leader) {
+          mbar_expect_tx(xfull(x.s), kXBytes);
+          copy_2d<1>(sbase + x.s * kXBytes, &map_x, k * kChunk, row0, xfull(x.s));
+        }
+        __syncwarp();
+        x.next();
+        for (int d = d0; d < d1; ++d, w.next()) {
+          if (w.again() && !warp_wait(wempty(w.s), w.ph ^ 1, p.err, 82)) {
+            ok = false;
+            break;
+          }
+          if (leader) {
+            const uint32_t to = wbase + w.s * p.w_stage;
+            mbar_expect_tx(wfull(w.s), TRANS ? wboxes * 8192 : p.r16 * 128);
+            if (!TRANS) copy_3d<1>(to, &map_w, k * kChunk, 0, ad.list[d], wfull(w.s));
+            else
+              for (int c = 0; c < wboxes; ++c) copy_3d<1>(to + 8192 * c, &map_w, 64 * c, k * kChunk, ad.list[d], wfull(w.s));
+          }
+          __syncwarp();
+        }
       }
     }
-    const uint16_t* we = w + (size_t)ad.list[ld] * p.r * p.C;
-    const uint32_t at = ws + stage * Cfg::kWBytes;
-    if (!TRANS) {
-      for (int piece = tid; piece < pairs * 16 * (kChunk / 8); piece += kTileThreads) {
-        const int r = piece / (kChunk / 8), c = piece % (kChunk / 8) * 8;
-        const bool have = r < p.r && c0 + c < p.C;
-        copy16(at + (r * Cfg::kWPitch + c) * 2, have ? we + (size_t)r * p.C + c0 + c : we, have);
+    leave(
+        ok,
+        [&] {
+          const bool a = x.last([&](int j, uint32_t ph) { return warp_wait(xempty(j), ph, p.err, 83); });
+          return w.last([&](int j, uint32_t ph) { return warp_wait(wempty(j), ph, p.err, 84); }) && a;
+        },
+        [&] {
+          x.last([&](int j, uint32_t ph) { return drain_wait(xfull(j), ph); });
+          w.last([&](int j, uint32_t ph) { return drain_wait(wfull(j), ph); });
+        });
+  } else if (warp == 1) {
+    // ---------------- MMAs ----------------
+    const bool leader = elect_one();
+    const uint32_t idesc = idesc_of(DT == SITU_DT_BF16, TRANS, p.r16);
+    Turns x(kStages), w(kStages);
+    bool ok = true;
+    int pass = 0;
+    for (int d0 = 0; d0 < nd && ok; d0 += per, ++pass) {
+      const int d1 = min(nd, d0 + per);
+      if (pass > 0 && !warp_wait(acc_empty, (pass - 1) & 1, p.err, 85)) {
+        ok = false;
+        break;
       }
-    } else {
-      const int per = pairs * 2;
-      for (int piece = tid; piece < kChunk * per; piece += kTileThreads) {
-        const int c = piece / per, r = piece % per * 8;
-        const bool have = r < p.r && c0 + c < p.C;
-        copy16(at + (c * Cfg::kWPitch + r) * 2, have ? we + (size_t)(c0 + c) * p.r + r : we, have);
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      for (int k = k0; k < k1 && ok; ++k, x.next()) {
+        if (!warp_wait(xfull(x.s), x.ph, p.err, 86)) {
+          ok = false;
+          break;
+        }
+        const int steps = min(kChunk / 16, (p.C - k * kChunk + 15) >> 4);
+        for (int d = d0; d < d1; ++d, w.next()) {
+          if (!warp_wait(wfull(w.s), w.ph, p.err, 87)) {
+            ok = false;
+            break;
+          }
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          if (leader) {
+            const uint32_t wa = wbase + w.s * p.w_stage;
+            const uint64_t xd = sdesc(sbase + x.s * kXBytes), wd = TRANS ? sdesc_mn(wa, 8192) : sdesc(wa);
+            for (int i = 0; i < steps; ++i)
+              mma_f16<1>(tmem + (d - d0) * p.r16, xd + 2 * i, wd + (TRANS ? 128 : 2) * i, idesc, ((k - k0) | i) != 0);
+            mma_commit(wempty(w.s));
+            if (d + 1 == d1) mma_commit(xempty(x.s));
+          }
+          __syncwarp();
+        }
+      }
+      if (ok) {
+        if (leader) mma_commit(acc_full);
+        __syncwarp();
       }
     }
-    if (++ld == nd) {
-      ld = 0;
-      ++lk;
+    leave(
+        ok, [&] { return w.last([&](int j, uint32_t ph) { return warp_wait(wempty(j), ph, p.err, 88); }); },
+        [&] {
+          if (leader) mma_commit(drain);
+          __syncwarp();
+          drain_wait(drain, 0);
+        });
+  } else {
+    // ---------------- sums to memory, a row per lane ----------------
+    const int q = warp & 3, at = ad.at[32 * q + lane], row = row0 + 32 * q + lane;
+    float* out = p.part + ((size_t)split * p.S + row) * p.r;
+    bool ok = true;
+    int pass = 0;
+    for (int d0 = 0; d0 < nd && ok; d0 += per, ++pass) {
+      const int d1 = min(nd, d0 + per);
+      ok = warp_wait(acc_full, pass & 1, p.err, 89);
+      if (!ok) break;
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      for (int d = d0; d < d1; ++d) {
+        if (!__any_sync(0xffffffffu, at == d)) continue;
+        for (int j = 0; j < p.r16; j += 16) {
+          uint32_t v[16];
+          tmem_ld16_nowait(tmem + ((uint32_t)(32 * q) << 16) + (d - d0) * p.r16 + j, v);
+          tmem_ld_wait<16>(v);
+          if (at == d) {
+#pragma unroll
+            for (int i = 0; i < 16; i += 4)
+              if (j + i < p.r)
+                *reinterpret_cast<uint4*>(out + j + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+          }
+        }
+      }
+      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+      mbar_arrive_if(acc_empty, lane == 0);
     }
-  };
-  float acc[RP / 8][4];
-#pragma unroll
-  for (int t = 0; t < RP / 8; ++t)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) acc[t][i] = 0.f;
-  const uint64_t mine = adapters_of_warp(ad);
-  const int at0 = ad.at[warp * 16 + (lane >> 2)], at1 = ad.at[warp * 16 + (lane >> 2) + 8];
-  const bool one = (mine & (mine - 1)) == 0;
-#pragma unroll
-  for (int s = 0; s < kStages - 1; ++s) {
-    if (s < total) load(s);
-    commit();
   }
-  int k = k0, d = 0;
-  for (int i = 0; i < total; ++i) {
-    wait_copies<kStages - 2>();
-    __syncthreads();
-    if (i + kStages - 1 < total) load((i + kStages - 1) % kStages);
-    commit();
-    if (mine >> d & 1) {
-      const uint32_t xa = xs + (k - k0) % kStages * Cfg::kXBytes +
-                          ((warp * 16 + (lane & 15)) * kXPitch + (lane >> 4) * 8) * 2;
-      const uint32_t wa = ws + i % kStages * Cfg::kWBytes;
-      float t[RP / 8][4];
-#pragma unroll
-      for (int j = 0; j < RP / 8; ++j)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) t[j][q] = acc[j][q];
-#pragma unroll
-      for (int ks = 0; ks < kChunk / 16; ++ks) {
-        uint32_t a[4];
-        ldmatrix4<false>(a, xa + ks * 32);
-#pragma unroll
-        for (int j = 0; j < RP / 16; ++j) {
-          if (j >= pairs) break;
-          uint32_t b[4];
-          if (!TRANS)
-            ldmatrix4<false>(b, wa + ((j * 16 + (lane >> 4) * 8 + (lane & 7)) * Cfg::kWPitch + ks * 16 + ((lane >> 3) & 1) * 8) * 2);
-          else
-            ldmatrix4<true>(b, wa + ((ks * 16 + ((lane >> 3) & 1) * 8 + (lane & 7)) * Cfg::kWPitch + j * 16 + (lane >> 4) * 8) * 2);
-          mma<DT>(t[2 * j], a, b[0], b[1]);
-          mma<DT>(t[2 * j + 1], a, b[2], b[3]);
-        }
-      }
-      // of several adapters' sums each row keeps its own
-#pragma unroll
-      for (int j = 0; j < RP / 8; ++j) {
-        if (one || at0 == d) {
-          acc[j][0] = t[j][0];
-          acc[j][1] = t[j][1];
-        }
-        if (one || at1 == d) {
-          acc[j][2] = t[j][2];
-          acc[j][3] = t[j][3];
-        }
-      }
-    }
-    if (++d == nd) {
-      d = 0;
-      ++k;
-    }
-  }
-  wait_copies<0>();
   griddep_launch_dependents();
-  // rows of no adapter give zeros
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int at = h ? at1 : at0, row = row0 + warp * 16 + (lane >> 2) + 8 * h;
-    if (at == kNoRow) continue;
-    float* o = p.part + ((size_t)split * p.S + row) * p.r + (lane & 3) * 2;
-#pragma unroll
-    for (int j = 0; j < RP / 8; ++j)
-      if (8 * j < p.r)
-        *reinterpret_cast<float2*>(o + 8 * j) =
-            at >= 0 ? make_float2(acc[j][2 * h], acc[j][2 * h + 1]) : make_float2(0.f, 0.f);
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    tmem_free<1>(tmem, kTmemCols);
   }
 }
 
-template <int DT, int RP, bool TRANS, bool F32>
-struct ExpandCfg {
-  static constexpr int kTerms = !F32 ? 1 : DT == SITU_DT_BF16 ? 3 : 2;
-  static constexpr int kUPitch = RP + 8;
-  static constexpr int kUBytes = kTile * kUPitch * 2;                // of a term
-  static constexpr int kWPitch = TRANS ? kCols + 8 : RP + 8;
-  static constexpr int kWBytes = (TRANS ? RP : kCols) * kWPitch * 2;
-  static constexpr int kSmem = kTerms * kUBytes + 2 * kWBytes;
-};
-
-// Where a column goes in shared memory: 8q + 2t + i of each 32 to 8t + 2q + i.
-__device__ __forceinline__ int dealt(int c) { return (c & ~30) + (c & 6) * 4 + (c & 24) / 4; }
-
 // out[i][c] = base[i][c] + s[e] sum_j u[i][j] W[e][c][j] (TRANS: W[e][j][c]),
-// u the sum of its parts.
-//
-// The MMA's columns are dealt out so that a thread's sums of four of its
-// 8-column tiles are eight neighbours of a row: 16-byte loads of base and
-// stores of out straight from registers.
-template <int DT, int RP, bool TRANS, bool F32>
-__global__ void __launch_bounds__(kTileThreads)
-expand_kernel(LoraParams p) {
-  using Cfg = ExpandCfg<DT, RP, TRANS, F32>;
-  constexpr int kTerms = Cfg::kTerms;
-  extern __shared__ __align__(16) uint8_t smem[];
+// u the sum of its parts: the tile's rows on the MMA's M side, 128 columns on
+// its N side, u in shared memory for all the CTA's columns (its 16-bit terms
+// one after the other along the contraction).  The sums go through shared memory
+// into the order in which 16 bytes a lane of base and out are coalesced.
+template <int DT, bool TRANS, bool F32>
+__global__ void __launch_bounds__(kExpandThreads)
+expand_kernel(const __grid_constant__ CUtensorMap map_w, const LoraParams p) {
+  constexpr int kTerms = terms_of(DT, F32);
+  extern __shared__ uint8_t smem_raw[];
   __shared__ Adapters ad;
   __shared__ float back[kTile];      // f16: the power of two that a row's u was divided by
+  __shared__ uint64_t bars[2 * kMaxStages + 6];
+  __shared__ uint32_t holder[2];
+  uint8_t* smem = smem_raw + (((saddr(smem_raw) + 1023) & ~1023u) - saddr(smem_raw));
+  const uint32_t sbase = saddr(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int row0 = blockIdx.x * kTile;
+  const uint32_t bar0 = saddr(bars);
+  auto full = [&](int s) { return bar0 + 8 * s; };
+  auto empty = [&](int s) { return bar0 + 8 * (kMaxStages + s); };
+  auto acc_full = [&](int b) { return bar0 + 8 * (2 * kMaxStages + b); };
+  auto acc_empty = [&](int b) { return bar0 + 8 * (2 * kMaxStages + 2 + b); };
+  const uint32_t u_full = bar0 + 8 * (2 * kMaxStages + 4), drain = u_full + 8;
+  if (tid == 0) {
+    prefetch_map(&map_w);
+    for (int s = 0; s < 2 * kMaxStages; ++s) mbar_init(bar0 + 8 * s, 1);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(acc_full(b), 1);
+      mbar_init(acc_empty(b), kEpiThreads / 32);
+    }
+    mbar_init(u_full, kEpiThreads / 32);
+    mbar_init(drain, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) tmem_alloc<1>(saddr(holder), kTmemCols);
   find_adapters(ad, p, row0);
-  const int nd = ad.count, pairs = (p.r + 15) / 16;
+  griddep_wait();                    // the parts, and the status, are the predecessor's
+  if (tid == 0) holder[1] = (uint32_t)*reinterpret_cast<volatile int*>(p.err);
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const uint32_t tmem = holder[0];
+  const bool dead = holder[1] != 0;
+  const int nd = dead ? 0 : ad.count;
   const int blocks = (p.C + kCols - 1) / kCols;
   const int b0 = (int)((long)blocks * blockIdx.y / p.groups), b1 = (int)((long)blocks * (blockIdx.y + 1) / p.groups);
-  const int total = nd * (b1 - b0);
-  const uint32_t us = smem_at(smem), ws = us + kTerms * Cfg::kUBytes;
-  const uint16_t* w = static_cast<const uint16_t*>(p.w);
-  int lb = b0, ld = 0;
-  auto load = [&](int stage) {
-    const uint16_t* we = w + (size_t)ad.list[ld] * p.r * p.C;
-    const int c0 = lb * kCols;
-    const uint32_t at = ws + stage * Cfg::kWBytes;
-    if (!TRANS) {
-      const int per = pairs * 2;
-      for (int piece = tid; piece < kCols * per; piece += kTileThreads) {
-        const int c = piece / per, r = piece % per * 8;
-        const bool have = r < p.r && c0 + c < p.C;
-        copy16(at + (dealt(c) * Cfg::kWPitch + r) * 2, have ? we + (size_t)(c0 + c) * p.r + r : we, have);
-      }
-    } else {
-      for (int piece = tid; piece < pairs * 16 * (kCols / 2); piece += kTileThreads) {
-        const int r = piece / (kCols / 2), c = piece % (kCols / 2) * 2;
-        const bool have = r < p.r && c0 + c < p.C;
-        copy4(at + (r * Cfg::kWPitch + dealt(c)) * 2, have ? we + (size_t)r * p.C + c0 + c : we, have);
-      }
-    }
-    if (++ld == nd) {
-      ld = 0;
-      ++lb;
-    }
-  };
-  if (total > 0) load(0);
-  commit();
-  griddep_wait();                    // the parts are the predecessor's output
-  {
-    // two threads to a row, half of its u each
-    const int i = tid >> 1, half = RP / 2, j0 = (tid & 1) * half, row = row0 + i;
-    const int e = ad.of[i];
-    float u[RP / 2];
-#pragma unroll
-    for (int j = 0; j < half; ++j) u[j] = 0.f;
-    if (e >= 0) {
-      for (int s = 0; s < p.splits; ++s) {
-        const float* src = p.part + ((size_t)s * p.S + row) * p.r + j0;
-#pragma unroll
-        for (int j = 0; j < half; j += 4) {
-          if (j0 + j >= p.r) break;
-          const float4 v = __ldcg(reinterpret_cast<const float4*>(src + j));
-          u[j] += v.x;
-          u[j + 1] += v.y;
-          u[j + 2] += v.z;
-          u[j + 3] += v.w;
+  const uint32_t ubase = sbase, wbase = sbase + p.u_bytes;
+  const int rboxes = (p.r + 63) / 64, steps = p.r16 / 16;
+
+  if (warp == 0) {
+    // ---------------- copies ----------------
+    const bool leader = elect_one();
+    Turns w(p.stages);
+    bool ok = true;
+    const int rrows = min(64, p.r16);                   // TRANS: contraction rows of a box
+    for (int b = b0; b < b1 && ok; ++b)
+      for (int d = 0; d < nd; ++d, w.next()) {
+        if (w.again() && !warp_wait(empty(w.s), w.ph ^ 1, p.err, 91)) {
+          ok = false;
+          break;
         }
-      }
-      const float f = p.scale ? __ldg(p.scale + e) : 1.f;
-#pragma unroll
-      for (int j = 0; j < half; ++j) u[j] *= f;
-    }
-    if (p.u16 && blockIdx.y == 0 && e != kNoRow) {
-      uint32_t* o = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.u16) + (size_t)row * p.r + j0);
-#pragma unroll
-      for (int j = 0; j < half; j += 2)
-        if (j0 + j < p.r) o[j / 2] = pack16<DT>(u[j], u[j + 1]);
-    }
-    if (DT == SITU_DT_F16) {
-      float m = 0.f;
-#pragma unroll
-      for (int j = 0; j < half; ++j) m = fmaxf(m, fabsf(u[j]));
-      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-      const int k = (int)(__float_as_uint(m) >> 23) - 127;            // m in [2^k, 2^(k + 1))
-      const int ex = m > 0.f && m < INFINITY ? max(-100, min(120, k - 14)) : 0;
-      const float to = exp2i(-ex);
-#pragma unroll
-      for (int j = 0; j < half; ++j) u[j] *= to;
-      if ((tid & 1) == 0) back[i] = exp2i(ex);
-    }
-#pragma unroll
-    for (int t = 0; t < kTerms; ++t) {
-#pragma unroll
-      for (int j = 0; j < half; j += 2) {
-        const uint32_t v = pack16<DT>(u[j], u[j + 1]);
-        *reinterpret_cast<uint32_t*>(smem + t * Cfg::kUBytes + (i * Cfg::kUPitch + j0 + j) * 2) = v;
-        if (t + 1 < kTerms) {        // what the term leaves; an infinity leaves nothing
-          u[j] = fabsf(u[j]) < INFINITY ? u[j] - lo16<DT>(v) : 0.f;
-          u[j + 1] = fabsf(u[j + 1]) < INFINITY ? u[j + 1] - hi16<DT>(v) : 0.f;
-        }
-      }
-    }
-  }
-  const uint64_t mine = adapters_of_warp(ad);
-  const int g = lane >> 2, q = lane & 3;
-  int at[2];
-  size_t from[2], to[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int i = warp * 16 + g + 8 * h;
-    at[h] = ad.at[i];
-    from[h] = (size_t)(row0 + i) * p.ld_base;
-    to[h] = (size_t)(row0 + i) * p.ldo;
-  }
-  __syncthreads();
-  const float f0 = DT == SITU_DT_F16 ? back[warp * 16 + g] : 1.f, f1 = DT == SITU_DT_F16 ? back[warp * 16 + g + 8] : 1.f;
-  constexpr int kEl = F32 ? 4 : 2, kVec = F32 ? 2 : 1;   // bytes of an element; 16-byte pieces of eight
-  const uint8_t* base = static_cast<const uint8_t*>(p.base);
-  uint8_t* out = static_cast<uint8_t*>(p.out);
-  // rows without an adapter take base as it is
-  if (p.base != p.out && (at[0] == kNone || at[1] == kNone)) {
-    for (int b = b0; b < b1; ++b)
-#pragma unroll
-      for (int s = 0; s < kCols / 32; ++s) {
-        const int c = b * kCols + 32 * s + 8 * q;
-        if (c >= p.C) break;
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          if (at[h] == kNone)
-#pragma unroll
-            for (int v = 0; v < kVec; ++v)
-              *reinterpret_cast<uint4*>(out + (to[h] + c) * kEl + 16 * v) =
-                  base ? *reinterpret_cast<const uint4*>(base + (from[h] + c) * kEl + 16 * v) : make_uint4(0, 0, 0, 0);
-      }
-  }
-  int b = b0, d = 0;
-  for (int i = 0; i < total; ++i) {
-    const bool work = mine >> d & 1;
-    // base on its way while the weights arrive
-    uint4 y[kCols / 32][2][kVec];
-    if (work && base) {
-#pragma unroll
-      for (int s = 0; s < kCols / 32; ++s) {
-        const int c = b * kCols + 32 * s + 8 * q;
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int v = 0; v < kVec; ++v)
-            y[s][h][v] = at[h] == d && c < p.C ? *reinterpret_cast<const uint4*>(base + (from[h] + c) * kEl + 16 * v)
-                                               : make_uint4(0, 0, 0, 0);
-      }
-    } else {
-#pragma unroll
-      for (int s = 0; s < kCols / 32; ++s)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int v = 0; v < kVec; ++v) y[s][h][v] = make_uint4(0, 0, 0, 0);
-    }
-    wait_copies<0>();
-    __syncthreads();
-    if (i + 1 < total) load((i + 1) & 1);
-    commit();
-    if (work) {
-      const uint32_t wa = ws + (i & 1) * Cfg::kWBytes;
-      float acc[kCols / 8][4];
-#pragma unroll
-      for (int t = 0; t < kCols / 8; ++t)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) acc[t][v] = 0.f;
-#pragma unroll 1
-      for (int ks = 0; ks < pairs; ++ks) {
-        uint32_t a[kTerms][4];
-#pragma unroll
-        for (int t = 0; t < kTerms; ++t)
-          ldmatrix4<false>(a[t], us + t * Cfg::kUBytes + ((warp * 16 + (lane & 15)) * Cfg::kUPitch + ks * 16 + (lane >> 4) * 8) * 2);
-#pragma unroll
-        for (int j = 0; j < kCols / 16; ++j) {      // tiles 2j and 2j + 1
-          uint32_t f[4];
+        if (leader) {
+          const uint32_t to = wbase + w.s * p.w_stage;
+          const int c0 = b * kCols, e = ad.list[d];
           if (!TRANS) {
-            ldmatrix4<false>(f, wa + ((j * 16 + (lane >> 4) * 8 + (lane & 7)) * Cfg::kWPitch + ks * 16 + ((lane >> 3) & 1) * 8) * 2);
+            mbar_expect_tx(full(w.s), rboxes * kXBytes);
+            for (int i = 0; i < rboxes; ++i) copy_3d<1>(to + i * kXBytes, &map_w, 64 * i, c0, e, full(w.s));
           } else {
-            ldmatrix4<true>(f, wa + ((ks * 16 + ((lane >> 3) & 1) * 8 + (lane & 7)) * Cfg::kWPitch + j * 16 + (lane >> 4) * 8) * 2);
-          }
-#pragma unroll
-          for (int t = kTerms - 1; t >= 0; --t) {   // the smallest first
-            mma<DT>(acc[2 * j], a[t], f[0], f[1]);
-            mma<DT>(acc[2 * j + 1], a[t], f[2], f[3]);
+            mbar_expect_tx(full(w.s), rboxes * 2 * rrows * 128);
+            for (int i = 0; i < rboxes; ++i)
+              for (int h = 0; h < 2; ++h)
+                copy_3d<1>(to + (2 * i + h) * rrows * 128, &map_w, c0 + 64 * h, 64 * i, e, full(w.s));
           }
         }
+        __syncwarp();
       }
+    leave(
+        ok, [&] { return w.last([&](int j, uint32_t ph) { return warp_wait(empty(j), ph, p.err, 92); }); },
+        [&] { w.last([&](int j, uint32_t ph) { return drain_wait(full(j), ph); }); });
+  } else if (warp == 1) {
+    // ---------------- MMAs ----------------
+    const bool leader = elect_one();
+    const uint32_t idesc = idesc_of(DT == SITU_DT_BF16, TRANS, kCols);
+    const uint32_t rrows = (uint32_t)min(64, p.r16);
+    Turns w(p.stages), acc(2);
+    bool ok = nd == 0 || b0 == b1 || warp_wait(u_full, 0, p.err, 93);
+    for (int b = b0; b < b1 && ok; ++b)
+      for (int d = 0; d < nd; ++d, w.next(), acc.next()) {
+        if ((acc.again() && !warp_wait(acc_empty(acc.s), acc.ph ^ 1, p.err, 94)) || !warp_wait(full(w.s), w.ph, p.err, 95)) {
+          ok = false;
+          break;
+        }
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        if (leader) {
+          const uint32_t wa = wbase + w.s * p.w_stage;
+          for (int t = kTerms - 1; t >= 0; --t)         // the smallest term first
+            for (int i = 0; i < steps; ++i) {
+              const int k = t * steps + i;              // sixteens along u's terms
+              const uint64_t ud = sdesc(ubase + (k >> 2) * kXBytes) + 2 * (k & 3);
+              const uint64_t wd = TRANS ? sdesc_mn(wa + (i >> 2) * 2 * rrows * 128, rrows * 128) + 128 * (i & 3)
+                                        : sdesc(wa + (i >> 2) * kXBytes) + 2 * (i & 3);
+              mma_f16<1>(tmem + acc.s * kCols, ud, wd, idesc, t != kTerms - 1 || i != 0);
+            }
+          mma_commit(empty(w.s));
+          mma_commit(acc_full(acc.s));
+        }
+        __syncwarp();
+      }
+    leave(
+        ok, [&] { return w.last([&](int j, uint32_t ph) { return warp_wait(empty(j), ph, p.err, 96); }); },
+        [&] {
+          if (leader) mma_commit(drain);
+          __syncwarp();
+          drain_wait(drain, 0);
+        });
+  } else if (!dead) {
+    const int et = tid - 64;
+    {
+      // u of the tile: two threads to a row, eight elements of each sixteen each
+      const int i = et >> 1, row = row0 + i, e = ad.of[i];
+      const float f = e >= 0 && p.scale ? __ldg(p.scale + e) : 1.f;
+      const bool write = p.u16 && blockIdx.y == 0 && e != kNoRow;
+      auto sum8 = [&](int j, float (&u)[8]) {
 #pragma unroll
-      for (int s = 0; s < kCols / 32; ++s) {
-        const int c = b * kCols + 32 * s + 8 * q;
-        if (c >= p.C) break;
+        for (int k = 0; k < 8; ++k) u[k] = 0.f;
+        if (e < 0 || j >= p.r) return;
+        for (int s = 0; s < p.splits; ++s) {
+          const float4* src = reinterpret_cast<const float4*>(p.part + ((size_t)s * p.S + row) * p.r + j);
+          const float4 v = __ldcg(src), w = __ldcg(src + 1);
+          u[0] += v.x;
+          u[1] += v.y;
+          u[2] += v.z;
+          u[3] += v.w;
+          u[4] += w.x;
+          u[5] += w.y;
+          u[6] += w.z;
+          u[7] += w.w;
+        }
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (at[h] != d) continue;
-          const float f = h ? f1 : f0;
-          uint4 o[kVec];
-          uint32_t* ow = reinterpret_cast<uint32_t*>(o);
-          const uint32_t* yw = reinterpret_cast<const uint32_t*>(y[s][h]);
+        for (int k = 0; k < 8; ++k) u[k] *= f;
+      };
+      float to = 1.f;
+      if (DT == SITU_DT_F16) {
+        float m = 0.f;
+        for (int j = 8 * (et & 1); j < p.r16; j += 16) {
+          float u[8];
+          sum8(j, u);
 #pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            const float e0 = acc[4 * s + t][2 * h] * f, e1 = acc[4 * s + t][2 * h + 1] * f;
-            if (F32) {
-              ow[2 * t] = __float_as_uint(__uint_as_float(yw[2 * t]) + e0);
-              ow[2 * t + 1] = __float_as_uint(__uint_as_float(yw[2 * t + 1]) + e1);
-            } else {
-              ow[t] = pack16<DT>(lo16<DT>(yw[t]) + e0, hi16<DT>(yw[t]) + e1);
+          for (int k = 0; k < 8; ++k) m = fmaxf(m, fabsf(u[k]));
+        }
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        const int k = (int)(__float_as_uint(m) >> 23) - 127;          // m in [2^k, 2^(k + 1))
+        const int ex = m > 0.f && m < INFINITY ? max(-100, min(120, k - 14)) : 0;
+        to = exp2i(-ex);
+        if ((et & 1) == 0) back[i] = exp2i(ex);
+      }
+      for (int j = 8 * (et & 1); j < p.r16; j += 16) {
+        float u[8];
+        sum8(j, u);
+        if (write && j < p.r)
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.u16) + (size_t)row * p.r + j) =
+              make_uint4(pack16<DT>(u[0], u[1]), pack16<DT>(u[2], u[3]), pack16<DT>(u[4], u[5]), pack16<DT>(u[6], u[7]));
+#pragma unroll
+        for (int t = 0; t < kTerms; ++t) {
+          uint32_t v[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float a = u[2 * k] * (t == 0 ? to : 1.f), b = u[2 * k + 1] * (t == 0 ? to : 1.f);
+            v[k] = pack16<DT>(a, b);
+            // what the term leaves; an infinity leaves nothing
+            u[2 * k] = fabsf(a) < INFINITY ? a - lo16<DT>(v[k]) : 0.f;
+            u[2 * k + 1] = fabsf(b) < INFINITY ? b - hi16<DT>(v[k]) : 0.f;
+          }
+          const int k = t * p.r16 + j;                  // along u's terms: 128-byte swizzled rows of 64
+          *reinterpret_cast<uint4*>(smem + (k >> 6) * kXBytes + i * 128 + ((((k & 63) >> 3) ^ (i & 7)) << 4)) =
+              make_uint4(v[0], v[1], v[2], v[3]);
+        }
+      }
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    asm volatile("bar.sync 1, 256;" ::: "memory");      // back[] and, before the barrier below, every lane's u
+    mbar_arrive_if(u_full, lane == 0);
+
+    // ---------------- sums to memory ----------------
+    const int q = warp & 3, h = (warp - 2) >> 2;        // this warp's 32 rows, and 64 of the 128 columns
+    constexpr int kEl = F32 ? 4 : 2, kLanes = F32 ? 8 : 4, kRows = 32 / kLanes, kIts = kLanes;   // lanes per row of 32 columns
+    const uint8_t* base = static_cast<const uint8_t*>(p.base);
+    uint8_t* out = static_cast<uint8_t*>(p.out);
+    float* stage = reinterpret_cast<float*>(smem + p.u_bytes + p.stages * p.w_stage) + (warp - 2) * 32 * kStagePitch;
+    const int my_at = ad.at[32 * q + lane];
+    const float my_back = DT == SITU_DT_F16 ? back[32 * q + lane] : 1.f;
+    const int r_in = lane / kLanes, c_in = lane % kLanes * (16 / kEl);
+    auto place = [&](int it, int col, long ld) {        // of 16 bytes: bytes from the array's start
+      return ((size_t)(row0 + 32 * q + it * kRows + r_in) * (size_t)ld + col + c_in) * kEl;
+    };
+    // rows without an adapter take base as it is
+    if (p.base != p.out && __any_sync(0xffffffffu, my_at == kNone)) {
+      for (int b = b0; b < b1; ++b)
+        for (int c = 0; c < 64; c += 32) {
+          const int col = b * kCols + 64 * h + c;
+#pragma unroll
+          for (int it = 0; it < kIts; ++it)
+            if (ad.at[32 * q + it * kRows + r_in] == kNone && col + c_in < p.C)
+              *reinterpret_cast<uint4*>(out + place(it, col, p.ldo)) =
+                  base ? *reinterpret_cast<const uint4*>(base + place(it, col, p.ld_base)) : make_uint4(0, 0, 0, 0);
+        }
+    }
+    Turns acc(2);
+    bool ok = true;
+    for (int b = b0; b < b1 && ok; ++b)
+      for (int d = 0; d < nd; ++d, acc.next()) {
+        const bool work = __any_sync(0xffffffffu, my_at == d);
+        uint4 y[2][kIts];
+        if (work) {
+          // base on its way while the sums are made
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int it = 0; it < kIts; ++it) {
+              const int col = b * kCols + 64 * h + 32 * c;
+              y[c][it] = base && ad.at[32 * q + it * kRows + r_in] == d && col + c_in < p.C
+                             ? *reinterpret_cast<const uint4*>(base + place(it, col, p.ld_base))
+                             : make_uint4(0, 0, 0, 0);
+            }
+        }
+        if (!warp_wait(acc_full(acc.s), acc.ph, p.err, 97)) {
+          ok = false;
+          break;
+        }
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        if (work) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int col = b * kCols + 64 * h + 32 * c;
+            uint32_t v[32];
+            tmem_ld32_nowait(tmem + ((uint32_t)(32 * q) << 16) + acc.s * kCols + 64 * h + 32 * c, v);
+            tmem_ld_wait<32>(v);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+              *reinterpret_cast<float4*>(stage + lane * kStagePitch + i) =
+                  make_float4(__uint_as_float(v[i]) * my_back, __uint_as_float(v[i + 1]) * my_back,
+                              __uint_as_float(v[i + 2]) * my_back, __uint_as_float(v[i + 3]) * my_back);
+            __syncwarp();
+#pragma unroll
+            for (int it = 0; it < kIts; ++it) {
+              const int r = it * kRows + r_in;
+              if (ad.at[32 * q + r] != d || col + c_in >= p.C) continue;
+              const float* src = stage + r * kStagePitch + c_in;
+              const float4 a = *reinterpret_cast<const float4*>(src);
+              uint4 o = y[c][it];
+              if (F32) {
+                o.x = __float_as_uint(__uint_as_float(o.x) + a.x);
+                o.y = __float_as_uint(__uint_as_float(o.y) + a.y);
+                o.z = __float_as_uint(__uint_as_float(o.z) + a.z);
+                o.w = __float_as_uint(__uint_as_float(o.w) + a.w);
+              } else {
+                const float4 e = *reinterpret_cast<const float4*>(src + 4);
+                o.x = pack16<DT>(lo16<DT>(o.x) + a.x, hi16<DT>(o.x) + a.y);
+                o.y = pack16<DT>(lo16<DT>(o.y) + a.z, hi16<DT>(o.y) + a.w);
+                o.z = pack16<DT>(lo16<DT>(o.z) + e.x, hi16<DT>(o.z) + e.y);
+                o.w = pack16<DT>(lo16<DT>(o.w) + e.z, hi16<DT>(o.w) + e.w);
+              }
+              *reinterpret_cast<uint4*>(out + place(it, col, p.ldo)) = o;
             }
           }
-#pragma unroll
-          for (int v = 0; v < kVec; ++v) *reinterpret_cast<uint4*>(out + (to[h] + c) * kEl + 16 * v) = o[v];
         }
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+        mbar_arrive_if(acc_empty(acc.s), lane == 0);
       }
-    }
-    if (++d == nd) {
-      d = 0;
-      ++b;
-    }
   }
-  wait_copies<0>();
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    tmem_free<1>(tmem, kTmemCols);
+  }
 }
 
 // --------------------------------------------------------------------------
 // launches
 // --------------------------------------------------------------------------
 
-// Tiles of rows times parts of the contraction: about three CTAs per SM, parts
-// of at least two stages, and partial sums (4 r splits bytes a row) of an
-// eighth of the row's bytes at most.
-int splits_of(int S, int C, int r) {
+// Parts of the contraction: two CTAs per SM, parts of at least two stages.  For
+// fp32 results a part is 1,024 elements at most: the tensor cores truncate when
+// they add (6e-9 of a sum of one sign per element), the parts meet in fp32.
+int splits_of(int S, int C, bool f32) {
   const int tiles = (S + kTile - 1) / kTile, chunks = (C + kChunk - 1) / kChunk;
-  int s = (3 * 152 + tiles - 1) / tiles;
-  const int most = S > 2 * kTile ? C / (16 * r) : 32;
-  s = s < most ? s : most;
-  s = s < chunks / 2 ? s : chunks / 2;
+  int s = 2 * 152 / tiles;
+  if (s > chunks / 2) s = chunks / 2;
+  if (f32 && s < (chunks + 15) / 16) s = (chunks + 15) / 16;
   return s < 1 ? 1 : s;
 }
 
-// Raises a kernel's shared memory limit: in every call, so that a context
-// created anew has it too.
-template <class K>
-cudaError_t allow_smem(K* kernel, int bytes) {
-  if (bytes <= 44 * 1024) return cudaSuccess;   // 48 KB with the static part
-  return cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+template <int DT, bool TRANS, bool F32>
+cudaError_t launch_pair(const CUtensorMap& mx, const CUtensorMap& mw, const LoraParams& s, const CUtensorMap& mo, LoraParams x,
+                        cudaStream_t st) {
+  auto* shrink = shrink_kernel<DT, TRANS>;
+  auto* expand = expand_kernel<DT, TRANS, F32>;
+  const unsigned tiles = (unsigned)((s.S + kTile - 1) / kTile);
+  const int shrink_smem = 1024 + kStages * (kXBytes + s.w_stage);
+  x.u_bytes = (terms_of(DT, F32) * x.r16 + 63) / 64 * kXBytes;
+  const int rest = 1024 + x.u_bytes + kEpiThreads / 32 * 32 * kStagePitch * 4;
+  x.stages = rest + 3 * x.w_stage <= 108 * 1024 || rest + 2 * x.w_stage > 108 * 1024 ? 3 : 2;   // two CTAs per SM where that does it
+  if (rest + x.stages * x.w_stage > 224 * 1024) x.stages = 2;
+  const int expand_smem = rest + x.stages * x.w_stage;
+  // in every call, so that a context created anew has them too
+  cudaError_t e = cudaFuncSetAttribute(shrink, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(expand, cudaFuncAttributeMaxDynamicSharedMemorySize, 224 * 1024);
+  if (e != cudaSuccess) return e;
+  shrink<<<dim3(tiles, (unsigned)s.splits), kShrinkThreads, shrink_smem, st>>>(mx, mw, s);
+  e = cudaGetLastError();
+  return e != cudaSuccess ? e : launch_pdl(expand, dim3(tiles, (unsigned)x.groups), dim3(kExpandThreads), expand_smem, st, mo, x);
 }
 
-template <int DT, int RP, bool TRANS>
-cudaError_t launch_shrink(const LoraParams& p, cudaStream_t st) {
-  auto* k = shrink_kernel<DT, RP, TRANS>;
-  constexpr int smem = ShrinkCfg<RP, TRANS>::kSmem;
-  const cudaError_t e = allow_smem(k, smem);
-  if (e != cudaSuccess) return e;
-  k<<<dim3((unsigned)((p.S + kTile - 1) / kTile), (unsigned)p.splits), kTileThreads, smem, st>>>(p);
-  return cudaGetLastError();
-}
-template <int DT, int RP, bool TRANS, bool F32>
-cudaError_t launch_expand(const LoraParams& p, cudaStream_t st) {
-  auto* k = expand_kernel<DT, RP, TRANS, F32>;
-  constexpr int smem = ExpandCfg<DT, RP, TRANS, F32>::kSmem;
-  const cudaError_t e = allow_smem(k, smem);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(k, dim3((unsigned)((p.S + kTile - 1) / kTile), (unsigned)p.groups), dim3(kTileThreads), smem, st, p);
-}
-
-template <int RP, bool TRANS>
-cudaError_t launch_pair(int dtype, int out_f32, const LoraParams& s, const LoraParams& x, cudaStream_t st) {
-  constexpr int kB = SITU_DT_BF16, kF = SITU_DT_F16;
-  cudaError_t e = dtype == kB ? launch_shrink<kB, RP, TRANS>(s, st) : launch_shrink<kF, RP, TRANS>(s, st);
-  if (e != cudaSuccess) return e;
-  if (out_f32) return dtype == kB ? launch_expand<kB, RP, TRANS, true>(x, st) : launch_expand<kF, RP, TRANS, true>(x, st);
-  return dtype == kB ? launch_expand<kB, RP, TRANS, false>(x, st) : launch_expand<kF, RP, TRANS, false>(x, st);
-}
+// x [S, C] times the adapters' w [n, r, C] (TRANS: [n, C, r]), and that times
+// the other factor [n, C', r] (TRANS: [n, r, C']), onto out.
 template <bool TRANS>
-cudaError_t launch_tiles(int dtype, int out_f32, LoraParams s, LoraParams x, cudaStream_t st) {
+situ_status launch_tiles(int dtype, bool f32, const void* rows, int64_t ld_rows, const void* w, const void* other, LoraParams s,
+                         LoraParams x, cudaStream_t st) {
+  const uint64_t S = (uint64_t)s.S, C = (uint64_t)s.C, O = (uint64_t)x.C, r = (uint64_t)s.r, n = (uint64_t)s.n;
+  s.r16 = x.r16 = (s.r + 15) / 16 * 16;
   s.chunks = (s.C + kChunk - 1) / kChunk;
-  s.splits = x.splits = splits_of(s.S, s.C, s.r);
+  s.splits = x.splits = splits_of(s.S, s.C, f32);
+  const int boxes = (s.r + 63) / 64;
+  s.w_stage = boxes * 8192;
+  const int rrows = s.r16 < 64 ? s.r16 : 64;
+  x.w_stage = TRANS ? boxes * 2 * rrows * 128 : boxes * kXBytes;
   const int tiles = (s.S + kTile - 1) / kTile, blocks = (x.C + kCols - 1) / kCols;
-  const int groups = (8 * 152 + tiles - 1) / tiles;        // about eight CTAs per SM
-  x.groups = groups < blocks ? groups : blocks;
-  if (s.r <= 16) return launch_pair<16, TRANS>(dtype, out_f32, s, x, st);
-  if (s.r <= 32) return launch_pair<32, TRANS>(dtype, out_f32, s, x, st);
-  if (s.r <= 64) return launch_pair<64, TRANS>(dtype, out_f32, s, x, st);
-  return launch_pair<128, TRANS>(dtype, out_f32, s, x, st);
+  // column groups: about four CTAs per SM, of two blocks or more (u is read and laid out by each)
+  const int groups = (4 * 152 + tiles - 1) / tiles, most = blocks > 2 ? blocks / 2 : 1;
+  x.groups = groups < most ? groups : most;
+  const CUtensorMapDataType dt = dtype == SITU_DT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  CUtensorMap mx, mw, mo;
+  const uint64_t dx[2] = {C, S}, sx[1] = {(uint64_t)ld_rows * 2};
+  const uint32_t bx[2] = {64, kTile};
+  bool ok = make_map_nd(&mx, dt, rows, 2, dx, sx, bx);
+  if (TRANS) {
+    const uint64_t dw[3] = {r, C, n}, sw[2] = {r * 2, r * C * 2}, dof[3] = {O, r, n}, so[2] = {O * 2, r * O * 2};
+    const uint32_t bw[3] = {64, kChunk, 1}, bo[3] = {64, (uint32_t)rrows, 1};
+    ok = ok && make_map_nd(&mw, dt, w, 3, dw, sw, bw) && make_map_nd(&mo, dt, other, 3, dof, so, bo);
+  } else {
+    const uint64_t dw[3] = {C, r, n}, sw[2] = {C * 2, r * C * 2}, dof[3] = {r, O, n}, so[2] = {r * 2, r * O * 2};
+    const uint32_t bw[3] = {64, (uint32_t)s.r16, 1}, bo[3] = {64, kCols, 1};
+    ok = ok && make_map_nd(&mw, dt, w, 3, dw, sw, bw) && make_map_nd(&mo, dt, other, 3, dof, so, bo);
+  }
+  if (!ok) return SITU_ERR_CUDA;
+  constexpr int kB = SITU_DT_BF16, kF = SITU_DT_F16;
+  const cudaError_t e = dtype == kB ? (f32 ? launch_pair<kB, TRANS, true>(mx, mw, s, mo, x, st)
+                                           : launch_pair<kB, TRANS, false>(mx, mw, s, mo, x, st))
+                                    : (f32 ? launch_pair<kF, TRANS, true>(mx, mw, s, mo, x, st)
+                                           : launch_pair<kF, TRANS, false>(mx, mw, s, mo, x, st));
+  return e == cudaSuccess ? SITU_OK : SITU_ERR_CUDA;
 }
 
 // A cluster per row, or tiles.
 bool by_rows(int S) { return S <= 64; }
 
-size_t part_bytes(int S, int C, int r) { return ((size_t)splits_of(S, C, r) * S * r * 4 + 15) / 16 * 16; }
+// for either type of result
+size_t part_bytes(int S, int C, int r) { return S == 0 ? 0 : (size_t)splits_of(S, C, true) * S * r * 4; }
 
 bool bad(const void* q, uintptr_t mask) { return (reinterpret_cast<uintptr_t>(q) & mask) != 0; }
 bool bad_ld(int64_t ld, int64_t cols, int64_t unit) { return ld < cols || ld % unit != 0 || ld > (int64_t)1 << 39; }
@@ -809,8 +908,8 @@ extern "C" situ_status situ_moe_lora(const situ_lora_args* a, void* workspace, s
       f32 ? launch(lora_row_kernel<SITU_DT_F16, true>) : launch(lora_row_kernel<SITU_DT_F16, false>);
     return cudaGetLastError() == cudaSuccess ? SITU_OK : SITU_ERR_CUDA;
   }
-  if (!workspace) return SITU_ERR_NULL_ARG;
-  if (bad(workspace, 15)) return SITU_ERR_MISALIGNED;
+  if (!workspace || !a->device_status) return SITU_ERR_NULL_ARG;
+  if (bad(workspace, 15) || bad(a->device_status, 3)) return SITU_ERR_MISALIGNED;
   if (workspace_bytes < part_bytes(a->S, a->K, a->r)) return SITU_ERR_WORKSPACE_TOO_SMALL;
   LoraParams s = {};
   s.ids = a->ids;
@@ -820,19 +919,16 @@ extern "C" situ_status situ_moe_lora(const situ_lora_args* a, void* workspace, s
   s.n = a->n;
   s.part = static_cast<float*>(workspace);
   s.scale = a->scale;
+  s.err = a->device_status;
   LoraParams x = s;
-  s.x = a->x;
-  s.ldx = (long)a->ldx;
-  s.w = a->a;
   s.C = a->K;
-  x.w = a->b;
   x.C = a->N;
   x.base = a->base;
   x.ld_base = (long)a->ld_base;
   x.out = a->out;
   x.ldo = (long)a->ldo;
   x.u16 = a->u;
-  return launch_tiles<false>(a->dtype, f32, s, x, st) == cudaSuccess ? SITU_OK : SITU_ERR_CUDA;
+  return launch_tiles<false>(a->dtype, f32 != 0, a->x, a->ldx, a->a, a->b, s, x, st);
 }
 
 extern "C" size_t situ_moe_lora_backward_workspace_size(int32_t S, int32_t K, int32_t N, int32_t r) {
@@ -867,19 +963,18 @@ extern "C" situ_status situ_moe_lora_backward(const situ_lora_backward_args* a, 
     s.n = a->n;
     s.part = static_cast<float*>(workspace);
     s.scale = a->scale;
+    s.err = a->device_status;
     LoraParams x = s;
-    s.x = a->dy;
-    s.ldx = (long)a->ld_dy;
-    s.w = a->b;
     s.C = a->N;
-    x.w = a->a;
     x.C = a->K;
     x.base = a->dx0;
     x.ld_base = (long)a->ld_dx0;
     x.out = a->dx;
     x.ldo = (long)a->ld_dx;
     x.u16 = v;
-    if (launch_tiles<true>(a->dtype, f32, s, x, (cudaStream_t)stream) != cudaSuccess) return SITU_ERR_CUDA;
+    const situ_status t =
+        launch_tiles<true>(a->dtype, f32 != 0, a->dy, a->ld_dy, a->b, a->a, s, x, (cudaStream_t)stream);
+    if (t != SITU_OK) return t;
   }
   // over an adapter's rows: dA = v^T x, dB = dy^T u
   situ_grouped_gemm_args g = {};

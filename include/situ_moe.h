@@ -766,6 +766,7 @@ typedef struct situ_lora_args {
   void* out;                      /* [S, N], rows ldo apart */
   int64_t ldo;
   void* u;                        /* [S, r], or NULL */
+  int32_t* device_status;         /* as for the expert products */
 } situ_lora_args;
 size_t situ_moe_lora_workspace_size(int32_t S, int32_t K, int32_t N, int32_t r);
 situ_status situ_moe_lora(const situ_lora_args* args, void* workspace, size_t workspace_bytes, void* stream);

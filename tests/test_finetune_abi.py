@@ -120,7 +120,7 @@ def test_restore_refusals(lib, args, status):
 
 def lora(lib, ws=0xf000, nbytes=1 << 30, **over):
     a = dict(dtype=0, out_dtype=0, S=100, K=64, N=128, r=16, n=4, x=0x1000, ldx=64, a=0x2000, b=0x3000, ids=0x4000,
-             offsets=None, scale=None, base=0x5000, ld_base=128, out=0x6000, ldo=128, u=None)
+             offsets=None, scale=None, base=0x5000, ld_base=128, out=0x6000, ldo=128, u=None, device_status=0xd000)
     a.update(over)
     return lib.situ_moe_lora(ctypes.byref(B.SituLoraArgs(**a)), ws, nbytes, None)
 
@@ -130,7 +130,8 @@ def lora(lib, ws=0xf000, nbytes=1 << 30, **over):
     (dict(K=0), 2), (dict(N=4), 2), (dict(r=0), 2), (dict(r=12), 2), (dict(r=136), 2), (dict(n=0), 2),
     (dict(n=(1 << 20) + 1), 2), (dict(ldx=56), 2), (dict(ldx=68), 2), (dict(ldo=120), 2), (dict(ld_base=64), 2),
     (dict(ld_base=132), 2), (dict(x=None), 1), (dict(a=None), 1), (dict(b=None), 1), (dict(out=None), 1),
-    (dict(ids=None), 1), (dict(offsets=0x7000), 1), (dict(ws=None), 1), (dict(x=0x1008), 6), (dict(a=0x2008), 6),
+    (dict(ids=None), 1), (dict(offsets=0x7000), 1), (dict(ws=None), 1), (dict(device_status=None), 1),
+    (dict(device_status=0xd001), 6), (dict(x=0x1008), 6), (dict(a=0x2008), 6),
     (dict(b=0x3002), 6), (dict(base=0x5008), 6), (dict(out=0x6004), 6), (dict(u=0x8008), 6), (dict(ids=0x4001), 6),
     (dict(scale=0x9002), 6), (dict(ws=0xf008), 6), (dict(nbytes=16), 4), (dict(S=0, x=None), 0),
 ])
