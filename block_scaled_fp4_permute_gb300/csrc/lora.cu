@@ -44,9 +44,9 @@ namespace {
 
 constexpr int kTile = 128;         // rows of a tile
 constexpr int kChunk = 64;         // contraction elements of a stage (shrink)
-constexpr int kStages = 4;         // of shrink
-constexpr int kMaxStages = 3;      // of expand
-constexpr int kCols = 128;         // columns of a step (expand)
+constexpr int kXBytes = kTile * 128;   // a box: 128 bytes of 128 rows
+constexpr int kMaxStages = 8;      // of a ring
+constexpr int kSmemMost = 222 * 1024;
 constexpr int kMaxRank = 128;
 constexpr int kCluster = 8;        // CTAs of a row
 constexpr int kRowThreads = 256;
@@ -55,21 +55,26 @@ struct LoraParams {
   const int32_t *ids, *offsets;
   int S, C, r, n;                  // C: the other extent (contraction or columns)
   int r16;                         // r rounded up to 16
-  int splits, chunks;              // shrink: parts of the contraction, stages in all
-  float* part;                     // [splits][S][r]
+  int tiles, chunks;               // of rows; of the contraction
+  long shrink_ctas;
+  float* part;                     // [parts of a tile][S][r]
   const float* scale;              // [n] or null
   const void* base;
   long ld_base;
   void* out;
   long ldo;
   void* u16;                       // [S, r] scaled, of the operands' type, or null
-  int groups;                      // expand: column groups of a tile
-  int stages, w_stage, u_bytes;    // shared memory: stages of w (expand), bytes of one, of u
+  int stages, w_stage;             // shared memory: stages of w (shrink: and of x), bytes of one
+  int tmem_cols;                   // shrink: of a CTA
+  int y_stages, u_bytes;           // expand: items of base in shared memory, bytes of u
   int* err;
 };
 
 // 16-bit terms that u is taken in
 __host__ __device__ constexpr int terms_of(int dt, bool f32) { return !f32 ? 1 : dt == SITU_DT_BF16 ? 3 : 2; }
+
+// columns of an item of expand
+__host__ __device__ constexpr int cols_of(bool f32) { return f32 ? 64 : 128; }
 
 struct RowParams {
   const void *x, *a, *b, *base;
@@ -221,34 +226,36 @@ lora_row_kernel(RowParams p) {
 // tiles of 128 rows
 // --------------------------------------------------------------------------
 
-// A tile's adapters: each row's (kNone: none, kNoRow: past the end), and the
-// distinct ones in the order of their first rows.
-constexpr int kNone = -1, kNoRow = -2;
+// A tile's adapters: each row's (-1: none), and the distinct ones in the order
+// of their first rows.
 struct Adapters {
   alignas(16) int of[kTile];   // row -> adapter
-  int at[kTile];       // row -> its place in `list`, or kNone / kNoRow
+  int at[kTile];               // row -> its place in `list`, or -1
   int list[kTile];
-  uint32_t lead[kTile / 32];
+  uint32_t lead[kTile / 32], same[kTile / 32];
   int count;
 };
-// by all threads of the block, kTile or more
-__device__ __forceinline__ void find_adapters(Adapters& t, const LoraParams& p, int row0) {
-  const int i = threadIdx.x;
+__device__ __forceinline__ void epi_sync(int threads) { asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory"); }
+// by the `threads` (kTile or more) epilogue threads, of which this is number i
+__device__ __forceinline__ void find_adapters(Adapters& t, const LoraParams& p, int row0, int i, int threads) {
   const bool mine = i < kTile;
-  int e = kNoRow;
+  int e = -1;
   if (mine) {
-    e = row0 + i < p.S ? adapter_of(p.ids, p.offsets, p.n, row0 + i) : kNoRow;
+    if (row0 + i < p.S) e = adapter_of(p.ids, p.offsets, p.n, row0 + i);
     t.of[i] = e;
   }
-  __syncthreads();
+  epi_sync(threads);
   const int e0 = t.of[0];
-  if (__syncthreads_and(!mine || e == e0 || e == kNoRow)) {
-    if (mine) t.at[i] = e >= 0 ? 0 : e;
+  const bool same = __all_sync(0xffffffffu, !mine || e == e0 || row0 + i >= p.S);
+  if (mine && (i & 31) == 0) t.same[i >> 5] = same;
+  epi_sync(threads);
+  if (t.same[0] & t.same[1] & t.same[2] & t.same[3]) {
+    if (mine) t.at[i] = e >= 0 ? 0 : -1;
     if (i == 0) {
       t.list[0] = e0;
       t.count = e0 >= 0 ? 1 : 0;
     }
-    __syncthreads();
+    epi_sync(threads);
     return;
   }
   int first = i;       // the first row of this one's adapter
@@ -263,20 +270,18 @@ __device__ __forceinline__ void find_adapters(Adapters& t, const LoraParams& p, 
       }
     }
   }
-  if (mine) {
-    __syncwarp();
-    const uint32_t lead = __ballot_sync(0xffffffffu, e >= 0 && first == i);
-    if ((i & 31) == 0) t.lead[i >> 5] = lead;
-  }
-  __syncthreads();
+  __syncwarp();
+  const uint32_t lead = __ballot_sync(0xffffffffu, mine && e >= 0 && first == i);
+  if (mine && (i & 31) == 0) t.lead[i >> 5] = lead;
+  epi_sync(threads);
   if (mine) {
     int place = __popc(t.lead[first >> 5] & ((1u << (first & 31)) - 1u));
     for (int w = 0; w < first >> 5; ++w) place += __popc(t.lead[w]);
-    t.at[i] = e >= 0 ? place : e;
+    t.at[i] = e >= 0 ? place : -1;
     if (e >= 0 && first == i) t.list[place] = e;
     if (i == 0) t.count = __popc(t.lead[0]) + __popc(t.lead[1]) + __popc(t.lead[2]) + __popc(t.lead[3]);
   }
-  __syncthreads();
+  epi_sync(threads);
 }
 
 // A ring whose length the launch chooses.
@@ -301,12 +306,11 @@ struct Turns {
   }
 };
 
-constexpr int kXBytes = kTile * 128;          // 64 elements of 128 rows
-constexpr int kTmemCols = 256;                // of a CTA: two CTAs per SM
-constexpr int kShrinkThreads = 192;           // copies, MMAs, four epilogue warps
-constexpr int kExpandThreads = 320;           // copies, MMAs, eight epilogue warps
-constexpr int kEpiThreads = 256;
-constexpr int kStagePitch = 36;               // floats of a row of a warp's 32 x 32 sums in shared memory
+constexpr int kTmemCols = 512;                // of an SM
+constexpr int kShrinkThreads = 192;           // copies, MMAs; four epilogue warps
+constexpr int kShrinkEpi = 128;
+constexpr int kExpandThreads = 384;           // copies of base and out, MMAs, copies of weights; eight epilogue warps
+constexpr int kExpandEpi = 256;
 
 // D[128, N] of 16-bit operands in fp32; trans_b: B's N elements contiguous
 __device__ __forceinline__ uint32_t idesc_of(bool bf16, bool trans_b, int N) {
@@ -314,167 +318,258 @@ __device__ __forceinline__ uint32_t idesc_of(bool bf16, bool trans_b, int N) {
          ((uint32_t)(128 >> 4) << 24);
 }
 
-// part[split][i][j] = sum over the split's k of x[i, k] W[e(i)][j][k] (TRANS:
+// Items dealt out evenly: CTA c of G takes [c T / G, (c + 1) T / G) of T, and
+// item i is CTA ((i + 1) G - 1) / T's.
+__host__ __device__ __forceinline__ long first_item(long c, long T, long G) { return c * T / G; }
+__host__ __device__ __forceinline__ long cta_of(long i, long T, long G) { return ((i + 1) * G - 1) / T; }
+// A CTA's items of one tile, `per` items to a tile, and the next tile's.
+struct Segment {
+  long i, end;
+  int per, tile, from, to;
+  __device__ __forceinline__ Segment(long i0, long i1, int per_tile) : i(i0), end(i1), per(per_tile) { set(); }
+  __device__ __forceinline__ bool more() const { return i < end; }
+  __device__ __forceinline__ void next() {
+    i += to - from;
+    set();
+  }
+  __device__ __forceinline__ void set() {
+    tile = (int)(i / per);
+    from = (int)(i - (long)tile * per);
+    to = (int)min((long)per, from + (end - i));
+  }
+};
+
+__device__ __forceinline__ void prefetch_2d(const CUtensorMap* map, int x, int y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(map)), "r"(x),
+               "r"(y)
+               : "memory");
+}
+__device__ __forceinline__ void store_2d(const CUtensorMap* map, uint32_t src, int x, int y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y), "r"(src)
+               : "memory");
+}
+__device__ __forceinline__ void store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void store_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+
+// part[.][i][j] = sum over a range of k of x[i, k] W[e(i)][j][k] (TRANS:
 // W[e][k][j]): the tile's rows on the MMA's M side, an adapter's r on its N
-// side, in TMEM columns of its own.  As many adapters as the columns hold share
-// a pass over x.
+// side, in TMEM columns of its own.  As many adapters as half of the columns
+// hold share a pass over x; the other half takes the next pass meanwhile.  The
+// chunks of all tiles are dealt out evenly over the CTAs; what a CTA
+// has of a tile is that tile's next part.
 template <int DT, bool TRANS>
-__global__ void __launch_bounds__(kShrinkThreads)
+__global__ void __launch_bounds__(kShrinkThreads, 2)
 shrink_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w, const LoraParams p) {
   extern __shared__ uint8_t smem_raw[];
-  __shared__ Adapters ad;
-  __shared__ uint64_t bars[4 * kStages + 3];
+  __shared__ Adapters lists[2];
+  __shared__ uint64_t bars[4 * kMaxStages + 9];
   __shared__ uint32_t holder[2];
   const uint32_t sbase = (saddr(smem_raw) + 1023) & ~1023u;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int row0 = blockIdx.x * kTile, split = blockIdx.y;
   const uint32_t bar0 = saddr(bars);
   auto xfull = [&](int s) { return bar0 + 8 * s; };
-  auto xempty = [&](int s) { return bar0 + 8 * (kStages + s); };
-  auto wfull = [&](int s) { return bar0 + 8 * (2 * kStages + s); };
-  auto wempty = [&](int s) { return bar0 + 8 * (3 * kStages + s); };
-  const uint32_t acc_full = bar0 + 8 * 4 * kStages, acc_empty = acc_full + 8, drain = acc_full + 16;
+  auto xempty = [&](int s) { return bar0 + 8 * (kMaxStages + s); };
+  auto wfull = [&](int s) { return bar0 + 8 * (2 * kMaxStages + s); };
+  auto wempty = [&](int s) { return bar0 + 8 * (3 * kMaxStages + s); };
+  const uint32_t tail = bar0 + 8 * 4 * kMaxStages;
+  auto acc_full = [&](int b) { return tail + 8 * b; };
+  auto acc_empty = [&](int b) { return tail + 16 + 8 * b; };
+  auto list_full = [&](int b) { return tail + 32 + 8 * b; };
+  auto list_empty = [&](int b) { return tail + 48 + 8 * b; };
+  const uint32_t drain = tail + 64;
+  const long total = (long)p.tiles * p.chunks, G = gridDim.x;
+  const long i0 = first_item(blockIdx.x, total, G), i1 = first_item(blockIdx.x + 1, total, G);
   if (tid == 0) {
+    for (long i = i0; i < i1 && i < i0 + p.stages; ++i)   // x does not wait for the adapters' list
+      prefetch_2d(&map_x, (int)(i % p.chunks) * kChunk, (int)(i / p.chunks) * kTile);
     holder[1] = (uint32_t)*reinterpret_cast<volatile int*>(p.err);   // an earlier launch gave up a wait: no work then
-    prefetch_map(&map_x);
     prefetch_map(&map_w);
-    for (int s = 0; s < 4 * kStages; ++s) mbar_init(bar0 + 8 * s, 1);
-    mbar_init(acc_full, 1);
-    mbar_init(acc_empty, 4);
+    for (int s = 0; s < 4 * kMaxStages; ++s) mbar_init(bar0 + 8 * s, 1);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(acc_full(b), 1);
+      mbar_init(acc_empty(b), 4);
+      mbar_init(list_full(b), 1);
+      mbar_init(list_empty(b), 2);
+    }
     mbar_init(drain, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 1) tmem_alloc<1>(saddr(holder), kTmemCols);
-  find_adapters(ad, p, row0);
+  if (warp == 1) tmem_alloc<1>(saddr(holder), (uint32_t)p.tmem_cols);
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = holder[0];
-  const int nd = holder[1] != 0 ? 0 : ad.count, per = kTmemCols / p.r16;
-  const int k0 = (int)((long)p.chunks * split / p.splits), k1 = (int)((long)p.chunks * (split + 1) / p.splits);
-  const uint32_t wbase = sbase + kStages * kXBytes;
-  const int wboxes = (p.r + 63) / 64;
+  const bool dead = holder[1] != 0;
+  const int half = p.tmem_cols / 2, per = half / p.r16;                // adapters of a pass
+  const uint32_t wbase = sbase + p.stages * kXBytes;
 
-  if (warp == 0) {
+  if (warp == 0 && !dead) {
     // ---------------- copies ----------------
     const bool leader = elect_one();
-    Turns x(kStages), w(kStages);
+    const int wboxes = (p.r + 63) / 64;
+    Turns x(p.stages), w(p.stages), l(2);
     bool ok = true;
-    for (int d0 = 0; d0 < nd && ok; d0 += per) {
-      const int d1 = min(nd, d0 + per);
-      for (int k = k0; k < k1 && ok; ++k) {
-        if (x.again() && !warp_wait(xempty(x.s), x.ph ^ 1, p.err, 81)) {
-          ok = false;
-          break;
-        }
-        if (leader) {
-          mbar_expect_tx(xfull(x.s), kXBytes);
-          copy_2d<1>(sbase + x.s * kXBytes, &map_x, k * kChunk, row0, xfull(x.s));
-        }
-        __syncwarp();
-        x.next();
-        for (int d = d0; d < d1; ++d, w.next()) {
-          if (w.again() && !warp_wait(wempty(w.s), w.ph ^ 1, p.err, 82)) {
+    for (Segment g(i0, i1, p.chunks); g.more() && ok; g.next()) {
+      if (!warp_wait(list_full(l.s), l.ph, p.err, 81)) {
+        ok = false;
+        break;
+      }
+      const Adapters& ad = lists[l.s];
+      const int nd = ad.count, row0 = g.tile * kTile;
+      for (int d0 = 0; d0 < nd && ok; d0 += per) {
+        const int d1 = min(nd, d0 + per);
+        for (int k = g.from; k < g.to && ok; ++k) {
+          if (x.again() && !warp_wait(xempty(x.s), x.ph ^ 1, p.err, 82)) {
             ok = false;
             break;
           }
           if (leader) {
-            const uint32_t to = wbase + w.s * p.w_stage;
-            mbar_expect_tx(wfull(w.s), TRANS ? wboxes * 8192 : p.r16 * 128);
-            if (!TRANS) copy_3d<1>(to, &map_w, k * kChunk, 0, ad.list[d], wfull(w.s));
-            else
-              for (int c = 0; c < wboxes; ++c) copy_3d<1>(to + 8192 * c, &map_w, 64 * c, k * kChunk, ad.list[d], wfull(w.s));
+            mbar_expect_tx(xfull(x.s), kXBytes);
+            copy_2d<1>(sbase + x.s * kXBytes, &map_x, k * kChunk, row0, xfull(x.s));
           }
           __syncwarp();
+          x.next();
+          for (int d = d0; d < d1; ++d, w.next()) {
+            if (w.again() && !warp_wait(wempty(w.s), w.ph ^ 1, p.err, 83)) {
+              ok = false;
+              break;
+            }
+            if (leader) {
+              const uint32_t to = wbase + w.s * p.w_stage;
+              mbar_expect_tx(wfull(w.s), TRANS ? wboxes * 8192 : p.r16 * 128);
+              if (!TRANS) copy_3d<1>(to, &map_w, k * kChunk, 0, ad.list[d], wfull(w.s));
+              else
+                for (int c = 0; c < wboxes; ++c) copy_3d<1>(to + 8192 * c, &map_w, 64 * c, k * kChunk, ad.list[d], wfull(w.s));
+            }
+            __syncwarp();
+          }
         }
       }
+      __syncwarp();
+      mbar_arrive_if(list_empty(l.s), lane == 0);
+      l.next();
     }
     leave(
         ok,
         [&] {
-          const bool a = x.last([&](int j, uint32_t ph) { return warp_wait(xempty(j), ph, p.err, 83); });
-          return w.last([&](int j, uint32_t ph) { return warp_wait(wempty(j), ph, p.err, 84); }) && a;
+          const bool a = x.last([&](int j, uint32_t ph) { return warp_wait(xempty(j), ph, p.err, 84); });
+          return w.last([&](int j, uint32_t ph) { return warp_wait(wempty(j), ph, p.err, 85); }) && a;
         },
         [&] {
           x.last([&](int j, uint32_t ph) { return drain_wait(xfull(j), ph); });
           w.last([&](int j, uint32_t ph) { return drain_wait(wfull(j), ph); });
         });
-  } else if (warp == 1) {
+  } else if (warp == 1 && !dead) {
     // ---------------- MMAs ----------------
     const bool leader = elect_one();
     const uint32_t idesc = idesc_of(DT == SITU_DT_BF16, TRANS, p.r16);
-    Turns x(kStages), w(kStages);
+    Turns x(p.stages), w(p.stages), l(2), acc(2);
     bool ok = true;
-    int pass = 0;
-    for (int d0 = 0; d0 < nd && ok; d0 += per, ++pass) {
-      const int d1 = min(nd, d0 + per);
-      if (pass > 0 && !warp_wait(acc_empty, (pass - 1) & 1, p.err, 85)) {
+    for (Segment g(i0, i1, p.chunks); g.more() && ok; g.next()) {
+      if (!warp_wait(list_full(l.s), l.ph, p.err, 86)) {
         ok = false;
         break;
       }
-      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      for (int k = k0; k < k1 && ok; ++k, x.next()) {
-        if (!warp_wait(xfull(x.s), x.ph, p.err, 86)) {
+      const int nd = lists[l.s].count;
+      __syncwarp();
+      mbar_arrive_if(list_empty(l.s), lane == 0);
+      l.next();
+      for (int d0 = 0; d0 < nd && ok; d0 += per) {
+        const int d1 = min(nd, d0 + per);
+        if (acc.again() && !warp_wait(acc_empty(acc.s), acc.ph ^ 1, p.err, 87)) {
           ok = false;
           break;
         }
-        const int steps = min(kChunk / 16, (p.C - k * kChunk + 15) >> 4);
-        for (int d = d0; d < d1; ++d, w.next()) {
-          if (!warp_wait(wfull(w.s), w.ph, p.err, 87)) {
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        for (int k = g.from; k < g.to && ok; ++k, x.next()) {
+          if (!warp_wait(xfull(x.s), x.ph, p.err, 88)) {
             ok = false;
             break;
           }
-          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          if (leader) {
-            const uint32_t wa = wbase + w.s * p.w_stage;
-            const uint64_t xd = sdesc(sbase + x.s * kXBytes), wd = TRANS ? sdesc_mn(wa, 8192) : sdesc(wa);
-            for (int i = 0; i < steps; ++i)
-              mma_f16<1>(tmem + (d - d0) * p.r16, xd + 2 * i, wd + (TRANS ? 128 : 2) * i, idesc, ((k - k0) | i) != 0);
-            mma_commit(wempty(w.s));
-            if (d + 1 == d1) mma_commit(xempty(x.s));
+          const int steps = min(kChunk / 16, (p.C - k * kChunk + 15) >> 4);
+          for (int d = d0; d < d1; ++d, w.next()) {
+            if (!warp_wait(wfull(w.s), w.ph, p.err, 89)) {
+              ok = false;
+              break;
+            }
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            if (leader) {
+              const uint32_t wa = wbase + w.s * p.w_stage;
+              const uint64_t xd = sdesc(sbase + x.s * kXBytes), wd = TRANS ? sdesc_mn(wa, 8192) : sdesc(wa);
+              for (int j = 0; j < steps; ++j)
+                mma_f16<1>(tmem + acc.s * half + (d - d0) * p.r16, xd + 2 * j, wd + (TRANS ? 128 : 2) * j, idesc,
+                           ((k - g.from) | j) != 0);
+              mma_commit(wempty(w.s));
+              if (d + 1 == d1) mma_commit(xempty(x.s));
+            }
+            __syncwarp();
           }
-          __syncwarp();
         }
-      }
-      if (ok) {
-        if (leader) mma_commit(acc_full);
-        __syncwarp();
+        if (ok) {
+          if (leader) mma_commit(acc_full(acc.s));
+          __syncwarp();
+          acc.next();
+        }
       }
     }
     leave(
-        ok, [&] { return w.last([&](int j, uint32_t ph) { return warp_wait(wempty(j), ph, p.err, 88); }); },
+        ok, [&] { return w.last([&](int j, uint32_t ph) { return warp_wait(wempty(j), ph, p.err, 90); }); },
         [&] {
           if (leader) mma_commit(drain);
           __syncwarp();
           drain_wait(drain, 0);
         });
-  } else {
-    // ---------------- sums to memory, a row per lane ----------------
-    const int q = warp & 3, at = ad.at[32 * q + lane], row = row0 + 32 * q + lane;
-    float* out = p.part + ((size_t)split * p.S + row) * p.r;
+  } else if (warp >= 2 && !dead) {
+    // ---------------- lists, and sums to memory, a row per lane ----------------
+    const int et = tid - 64, q = warp & 3;
+    Turns l(2), acc(2);
     bool ok = true;
-    int pass = 0;
-    for (int d0 = 0; d0 < nd && ok; d0 += per, ++pass) {
-      const int d1 = min(nd, d0 + per);
-      ok = warp_wait(acc_full, pass & 1, p.err, 89);
-      if (!ok) break;
-      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      for (int d = d0; d < d1; ++d) {
-        if (!__any_sync(0xffffffffu, at == d)) continue;
-        for (int j = 0; j < p.r16; j += 16) {
-          uint32_t v[16];
-          tmem_ld16_nowait(tmem + ((uint32_t)(32 * q) << 16) + (d - d0) * p.r16 + j, v);
-          tmem_ld_wait<16>(v);
-          if (at == d) {
+    auto list = [&](const Segment& g) {                 // of a tile, while the one before is worked on
+      if (l.again() && !warp_wait(list_empty(l.s), l.ph ^ 1, p.err, 91)) ok = false;
+      find_adapters(lists[l.s], p, g.tile * kTile, et, kShrinkEpi);
+      mbar_arrive_if(list_full(l.s), et == 0);
+      l.next();
+    };
+    Segment g(i0, i1, p.chunks);
+    if (g.more()) list(g);
+    for (int b = 0; g.more(); b ^= 1) {
+      Segment n = g;
+      n.next();
+      if (n.more()) list(n);
+      const Adapters& ad = lists[b];
+      const int nd = ad.count, at = ad.at[32 * q + lane], row = g.tile * kTile + 32 * q + lane;
+      const int part = (int)((long)blockIdx.x - cta_of((long)g.tile * p.chunks, total, G));
+      float* out = p.part + ((size_t)part * p.S + row) * p.r;
+      for (int d0 = 0; d0 < nd && ok; d0 += per, acc.next()) {
+        const int d1 = min(nd, d0 + per);
+        if (!warp_wait(acc_full(acc.s), acc.ph, p.err, 92)) {
+          ok = false;
+          break;
+        }
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        for (int d = d0; d < d1; ++d) {
+          if (!__any_sync(0xffffffffu, at == d)) continue;
+          for (int j = 0; j < p.r16; j += 16) {
+            uint32_t v[16];
+            tmem_ld16_nowait(tmem + ((uint32_t)(32 * q) << 16) + acc.s * half + (d - d0) * p.r16 + j, v);
+            tmem_ld_wait<16>(v);
+            if (at == d) {
 #pragma unroll
-            for (int i = 0; i < 16; i += 4)
-              if (j + i < p.r)
-                *reinterpret_cast<uint4*>(out + j + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+              for (int t = 0; t < 16; t += 4)
+                if (j + t < p.r)
+                  *reinterpret_cast<uint4*>(out + j + t) = make_uint4(v[t], v[t + 1], v[t + 2], v[t + 3]);
+            }
           }
         }
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+        mbar_arrive_if(acc_empty(acc.s), lane == 0);
       }
-      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-      mbar_arrive_if(acc_empty, lane == 0);
+      g = n;
     }
   }
   griddep_launch_dependents();
@@ -483,148 +578,239 @@ shrink_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
   if (warp == 1) {
     __syncwarp();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-    tmem_free<1>(tmem, kTmemCols);
+    tmem_free<1>(tmem, (uint32_t)p.tmem_cols);
   }
 }
 
 // out[i][c] = base[i][c] + s[e] sum_j u[i][j] W[e][c][j] (TRANS: W[e][j][c]),
-// u the sum of its parts: the tile's rows on the MMA's M side, 128 columns on
-// its N side, u in shared memory for all the CTA's columns (its 16-bit terms
-// one after the other along the contraction).  The sums go through shared memory
-// into the order in which 16 bytes a lane of base and out are coalesced.
+// u the sum of its parts: the tile's rows on the MMA's M side, 128 columns
+// (fp32: 64) on its N side.  Base comes into shared memory by TMA, two boxes of
+// 128 rows by 128 bytes an item, several items ahead; the epilogue adds each
+// adapter's sums to its rows there, and TMA takes the boxes to out.  So
+// rows without an adapter pass through, and no thread waits for memory: with
+// base loaded and out stored by the epilogue's own instructions, the loads', the
+// sums' and the stores' times added up (403 MB in 116 us).  u stays in shared
+// memory for all the CTA's items of a tile, its 16-bit terms one after the
+// other along the contraction.  The items are dealt out evenly over the CTAs,
+// one per SM.
 template <int DT, bool TRANS, bool F32>
-__global__ void __launch_bounds__(kExpandThreads)
-expand_kernel(const __grid_constant__ CUtensorMap map_w, const LoraParams p) {
-  constexpr int kTerms = terms_of(DT, F32);
+__global__ void __launch_bounds__(kExpandThreads, 1)
+expand_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_base,
+              const __grid_constant__ CUtensorMap map_out, const LoraParams p) {
+  constexpr int kTerms = terms_of(DT, F32), kCols = cols_of(F32), kBoxCols = kCols / 2;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ Adapters ad;
+  __shared__ Adapters lists[2];
   __shared__ float back[kTile];      // f16: the power of two that a row's u was divided by
-  __shared__ uint64_t bars[2 * kMaxStages + 6];
+  __shared__ uint64_t bars[4 * kMaxStages + 10];
   __shared__ uint32_t holder[2];
   uint8_t* smem = smem_raw + (((saddr(smem_raw) + 1023) & ~1023u) - saddr(smem_raw));
   const uint32_t sbase = saddr(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int row0 = blockIdx.x * kTile;
   const uint32_t bar0 = saddr(bars);
-  auto full = [&](int s) { return bar0 + 8 * s; };
-  auto empty = [&](int s) { return bar0 + 8 * (kMaxStages + s); };
-  auto acc_full = [&](int b) { return bar0 + 8 * (2 * kMaxStages + b); };
-  auto acc_empty = [&](int b) { return bar0 + 8 * (2 * kMaxStages + 2 + b); };
-  const uint32_t u_full = bar0 + 8 * (2 * kMaxStages + 4), drain = u_full + 8;
+  auto wfull = [&](int s) { return bar0 + 8 * s; };
+  auto wempty = [&](int s) { return bar0 + 8 * (kMaxStages + s); };
+  auto yfull = [&](int s) { return bar0 + 8 * (2 * kMaxStages + s); };
+  auto ydone = [&](int s) { return bar0 + 8 * (3 * kMaxStages + s); };
+  const uint32_t tail = bar0 + 8 * 4 * kMaxStages;
+  auto acc_full = [&](int b) { return tail + 8 * b; };
+  auto acc_empty = [&](int b) { return tail + 16 + 8 * b; };
+  auto list_full = [&](int b) { return tail + 32 + 8 * b; };
+  auto list_empty = [&](int b) { return tail + 48 + 8 * b; };
+  const uint32_t u_full = tail + 64, drain = tail + 72;
   if (tid == 0) {
     prefetch_map(&map_w);
-    for (int s = 0; s < 2 * kMaxStages; ++s) mbar_init(bar0 + 8 * s, 1);
+    if (p.base) prefetch_map(&map_base);
+    prefetch_map(&map_out);
+    for (int s = 0; s < kMaxStages; ++s) {
+      mbar_init(wfull(s), 1);
+      mbar_init(wempty(s), 1);
+      mbar_init(yfull(s), 1);
+      mbar_init(ydone(s), kExpandEpi / 32);
+    }
     for (int b = 0; b < 2; ++b) {
       mbar_init(acc_full(b), 1);
-      mbar_init(acc_empty(b), kEpiThreads / 32);
+      mbar_init(acc_empty(b), kExpandEpi / 32);
+      mbar_init(list_full(b), 1);
+      mbar_init(list_empty(b), 2);
     }
-    mbar_init(u_full, kEpiThreads / 32);
+    mbar_init(u_full, kExpandEpi / 32);
     mbar_init(drain, 1);
+    holder[1] = (uint32_t)*reinterpret_cast<volatile int*>(p.err);   // an earlier call gave up a wait: no work then
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 1) tmem_alloc<1>(saddr(holder), kTmemCols);
-  find_adapters(ad, p, row0);
-  griddep_wait();                    // the parts, and the status, are the predecessor's
-  if (tid == 0) holder[1] = (uint32_t)*reinterpret_cast<volatile int*>(p.err);
+  if (warp == 1) tmem_alloc<1>(saddr(holder), 256);
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = holder[0];
   const bool dead = holder[1] != 0;
-  const int nd = dead ? 0 : ad.count;
   const int blocks = (p.C + kCols - 1) / kCols;
-  const int b0 = (int)((long)blocks * blockIdx.y / p.groups), b1 = (int)((long)blocks * (blockIdx.y + 1) / p.groups);
-  const uint32_t ubase = sbase, wbase = sbase + p.u_bytes;
+  const long total = (long)p.tiles * blocks, G = gridDim.x;
+  const long i0 = first_item(blockIdx.x, total, G), i1 = first_item(blockIdx.x + 1, total, G);
+  const uint32_t ubase = sbase, wbase = sbase + p.u_bytes, ybase = wbase + p.stages * p.w_stage;
   const int rboxes = (p.r + 63) / 64, steps = p.r16 / 16;
+  const int rrows = min(64, p.r16);                     // TRANS: contraction rows of a box
 
-  if (warp == 0) {
-    // ---------------- copies ----------------
+  if (warp == 0 && !dead) {
+    // ---------------- base in, out ----------------
     const bool leader = elect_one();
-    Turns w(p.stages);
+    Turns in(p.y_stages), out(p.y_stages);
     bool ok = true;
-    const int rrows = min(64, p.r16);                   // TRANS: contraction rows of a box
-    for (int b = b0; b < b1 && ok; ++b)
-      for (int d = 0; d < nd; ++d, w.next()) {
-        if (w.again() && !warp_wait(empty(w.s), w.ph ^ 1, p.err, 91)) {
-          ok = false;
-          break;
-        }
-        if (leader) {
-          const uint32_t to = wbase + w.s * p.w_stage;
-          const int c0 = b * kCols, e = ad.list[d];
-          if (!TRANS) {
-            mbar_expect_tx(full(w.s), rboxes * kXBytes);
-            for (int i = 0; i < rboxes; ++i) copy_3d<1>(to + i * kXBytes, &map_w, 64 * i, c0, e, full(w.s));
-          } else {
-            mbar_expect_tx(full(w.s), rboxes * 2 * rrows * 128);
-            for (int i = 0; i < rboxes; ++i)
-              for (int h = 0; h < 2; ++h)
-                copy_3d<1>(to + (2 * i + h) * rrows * 128, &map_w, c0 + 64 * h, 64 * i, e, full(w.s));
-          }
-        }
-        __syncwarp();
+    long next = i0;
+    auto load = [&] {
+      if (leader) {
+        const int tile = (int)(next / blocks), c0 = (int)(next - (long)tile * blocks) * kCols;
+        const int boxes = c0 + kBoxCols < p.C ? 2 : 1;
+        mbar_expect_tx(yfull(in.s), p.base ? boxes * kXBytes : 0);
+        if (p.base)
+          for (int h = 0; h < boxes; ++h)
+            copy_2d<1>(ybase + in.s * 2 * kXBytes + h * kXBytes, &map_base, c0 + h * kBoxCols, tile * kTile, yfull(in.s));
       }
-    leave(
-        ok, [&] { return w.last([&](int j, uint32_t ph) { return warp_wait(empty(j), ph, p.err, 92); }); },
-        [&] { w.last([&](int j, uint32_t ph) { return drain_wait(full(j), ph); }); });
-  } else if (warp == 1) {
+      __syncwarp();
+      in.next();
+      ++next;
+    };
+    for (int j = 0; j < p.y_stages - 1 && next < i1; ++j) load();
+    for (long i = i0; i < i1; ++i, out.next()) {
+      if (!warp_wait(ydone(out.s), out.ph, p.err, 101)) {
+        ok = false;
+        break;
+      }
+      if (leader) {
+        const int tile = (int)(i / blocks), c0 = (int)(i - (long)tile * blocks) * kCols;
+        for (int h = 0; h < 2 && c0 + h * kBoxCols < p.C; ++h)
+          store_2d(&map_out, ybase + out.s * 2 * kXBytes + h * kXBytes, c0 + h * kBoxCols, tile * kTile);
+        store_commit();
+        store_wait_read<1>();                           // the item before: its place takes the next load
+      }
+      __syncwarp();
+      if (next < i1) load();
+    }
+    if (leader) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    __syncwarp();
+    if (!ok) in.last([&](int j, uint32_t ph) { return drain_wait(yfull(j), ph); });
+  } else if (warp == 1 && !dead) {
     // ---------------- MMAs ----------------
     const bool leader = elect_one();
     const uint32_t idesc = idesc_of(DT == SITU_DT_BF16, TRANS, kCols);
-    const uint32_t rrows = (uint32_t)min(64, p.r16);
-    Turns w(p.stages), acc(2);
-    bool ok = nd == 0 || b0 == b1 || warp_wait(u_full, 0, p.err, 93);
-    for (int b = b0; b < b1 && ok; ++b)
-      for (int d = 0; d < nd; ++d, w.next(), acc.next()) {
-        if ((acc.again() && !warp_wait(acc_empty(acc.s), acc.ph ^ 1, p.err, 94)) || !warp_wait(full(w.s), w.ph, p.err, 95)) {
-          ok = false;
-          break;
-        }
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        if (leader) {
-          const uint32_t wa = wbase + w.s * p.w_stage;
-          for (int t = kTerms - 1; t >= 0; --t)         // the smallest term first
-            for (int i = 0; i < steps; ++i) {
-              const int k = t * steps + i;              // sixteens along u's terms
-              const uint64_t ud = sdesc(ubase + (k >> 2) * kXBytes) + 2 * (k & 3);
-              const uint64_t wd = TRANS ? sdesc_mn(wa + (i >> 2) * 2 * rrows * 128, rrows * 128) + 128 * (i & 3)
-                                        : sdesc(wa + (i >> 2) * kXBytes) + 2 * (i & 3);
-              mma_f16<1>(tmem + acc.s * kCols, ud, wd, idesc, t != kTerms - 1 || i != 0);
-            }
-          mma_commit(empty(w.s));
-          mma_commit(acc_full(acc.s));
-        }
-        __syncwarp();
+    Turns w(p.stages), acc(2), l(2);
+    uint32_t seg = 0;
+    bool ok = true;
+    for (Segment g(i0, i1, blocks); g.more() && ok; g.next(), seg ^= 1) {
+      if (!warp_wait(list_full(l.s), l.ph, p.err, 102)) {
+        ok = false;
+        break;
       }
+      const int nd = lists[l.s].count;
+      __syncwarp();
+      mbar_arrive_if(list_empty(l.s), lane == 0);
+      l.next();
+      ok = warp_wait(u_full, seg, p.err, 103);
+      for (int b = g.from; b < g.to && ok; ++b)
+        for (int d = 0; d < nd; ++d, w.next(), acc.next()) {
+          if ((acc.again() && !warp_wait(acc_empty(acc.s), acc.ph ^ 1, p.err, 104)) || !warp_wait(wfull(w.s), w.ph, p.err, 105)) {
+            ok = false;
+            break;
+          }
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          if (leader) {
+            const uint32_t wa = wbase + w.s * p.w_stage;
+            for (int t = kTerms - 1; t >= 0; --t)         // the smallest term first
+              for (int j = 0; j < steps; ++j) {
+                const int k = t * steps + j;              // sixteens along u's terms
+                const uint64_t ud = sdesc(ubase + (k >> 2) * kXBytes) + 2 * (k & 3);
+                const uint64_t wd = TRANS ? sdesc_mn(wa + (j >> 2) * (kCols / 64) * rrows * 128, rrows * 128) + 128 * (j & 3)
+                                          : sdesc(wa + (j >> 2) * kCols * 128) + 2 * (j & 3);
+                mma_f16<1>(tmem + acc.s * kCols, ud, wd, idesc, t != kTerms - 1 || j != 0);
+              }
+            mma_commit(wempty(w.s));
+            mma_commit(acc_full(acc.s));
+          }
+          __syncwarp();
+        }
+    }
     leave(
-        ok, [&] { return w.last([&](int j, uint32_t ph) { return warp_wait(empty(j), ph, p.err, 96); }); },
+        ok, [&] { return w.last([&](int j, uint32_t ph) { return warp_wait(wempty(j), ph, p.err, 106); }); },
         [&] {
           if (leader) mma_commit(drain);
           __syncwarp();
           drain_wait(drain, 0);
         });
-  } else if (!dead) {
-    const int et = tid - 64;
-    {
-      // u of the tile: two threads to a row, eight elements of each sixteen each
-      const int i = et >> 1, row = row0 + i, e = ad.of[i];
+  } else if (warp == 2 && !dead) {
+    // ---------------- weights ----------------
+    const bool leader = elect_one();
+    Turns w(p.stages), l(2);
+    bool ok = true;
+    for (Segment g(i0, i1, blocks); g.more() && ok; g.next()) {
+      if (!warp_wait(list_full(l.s), l.ph, p.err, 107)) {
+        ok = false;
+        break;
+      }
+      const Adapters& ad = lists[l.s];
+      const int nd = ad.count;
+      for (int b = g.from; b < g.to && ok; ++b)
+        for (int d = 0; d < nd; ++d, w.next()) {
+          if (w.again() && !warp_wait(wempty(w.s), w.ph ^ 1, p.err, 108)) {
+            ok = false;
+            break;
+          }
+          if (leader) {
+            const uint32_t to = wbase + w.s * p.w_stage;
+            const int c0 = b * kCols, e = ad.list[d];
+            if (!TRANS) {
+              mbar_expect_tx(wfull(w.s), rboxes * kCols * 128);
+              for (int j = 0; j < rboxes; ++j) copy_3d<1>(to + j * kCols * 128, &map_w, 64 * j, c0, e, wfull(w.s));
+            } else {
+              constexpr int kHalves = kCols / 64;
+              mbar_expect_tx(wfull(w.s), rboxes * kHalves * rrows * 128);
+              for (int j = 0; j < rboxes; ++j)
+                for (int h = 0; h < kHalves; ++h)
+                  copy_3d<1>(to + (kHalves * j + h) * rrows * 128, &map_w, c0 + 64 * h, 64 * j, e, wfull(w.s));
+            }
+          }
+          __syncwarp();
+        }
+      __syncwarp();
+      mbar_arrive_if(list_empty(l.s), lane == 0);
+      l.next();
+    }
+    leave(
+        ok, [&] { return w.last([&](int j, uint32_t ph) { return warp_wait(wempty(j), ph, p.err, 109); }); },
+        [&] { w.last([&](int j, uint32_t ph) { return drain_wait(wfull(j), ph); }); });
+  } else if (warp >= 4 && !dead) {
+    // ---------------- lists, u, and sums onto base ----------------
+    const int et = tid - 128, q = warp & 3, h = (warp - 4) >> 2;   // this warp's 32 rows, and box of an item
+    Turns l(2), acc(2), y(p.y_stages);
+    bool ok = true;
+    auto list = [&](const Segment& g) {                 // of a tile, while the one before is worked on
+      if (l.again() && !warp_wait(list_empty(l.s), l.ph ^ 1, p.err, 110)) ok = false;
+      find_adapters(lists[l.s], p, g.tile * kTile, et, kExpandEpi);
+      mbar_arrive_if(list_full(l.s), et == 0);
+      l.next();
+    };
+    // u of a tile: two threads to a row, eight elements of each sixteen each
+    auto stage_u = [&](const Segment& g, const Adapters& ad) {
+      const int r = et >> 1, row = g.tile * kTile + r, e = ad.of[r];
       const float f = e >= 0 && p.scale ? __ldg(p.scale + e) : 1.f;
-      const bool write = p.u16 && blockIdx.y == 0 && e != kNoRow;
+      const bool write = p.u16 && g.from == 0 && row < p.S;
+      const long t0 = (long)g.tile * p.chunks, all = (long)p.tiles * p.chunks;
+      const int parts = (int)(cta_of(t0 + p.chunks - 1, all, p.shrink_ctas) - cta_of(t0, all, p.shrink_ctas)) + 1;
       auto sum8 = [&](int j, float (&u)[8]) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) u[k] = 0.f;
         if (e < 0 || j >= p.r) return;
-        for (int s = 0; s < p.splits; ++s) {
+#pragma unroll 4
+        for (int s = 0; s < parts; ++s) {
           const float4* src = reinterpret_cast<const float4*>(p.part + ((size_t)s * p.S + row) * p.r + j);
-          const float4 v = __ldcg(src), w = __ldcg(src + 1);
+          const float4 v = __ldcg(src), z = __ldcg(src + 1);
           u[0] += v.x;
           u[1] += v.y;
           u[2] += v.z;
           u[3] += v.w;
-          u[4] += w.x;
-          u[5] += w.y;
-          u[6] += w.z;
-          u[7] += w.w;
+          u[4] += z.x;
+          u[5] += z.y;
+          u[6] += z.z;
+          u[7] += z.w;
         }
 #pragma unroll
         for (int k = 0; k < 8; ++k) u[k] *= f;
@@ -642,8 +828,9 @@ expand_kernel(const __grid_constant__ CUtensorMap map_w, const LoraParams p) {
         const int k = (int)(__float_as_uint(m) >> 23) - 127;          // m in [2^k, 2^(k + 1))
         const int ex = m > 0.f && m < INFINITY ? max(-100, min(120, k - 14)) : 0;
         to = exp2i(-ex);
-        if ((et & 1) == 0) back[i] = exp2i(ex);
+        if ((et & 1) == 0) back[r] = exp2i(ex);
       }
+#pragma unroll 2
       for (int j = 8 * (et & 1); j < p.r16; j += 16) {
         float u[8];
         sum8(j, u);
@@ -662,109 +849,102 @@ expand_kernel(const __grid_constant__ CUtensorMap map_w, const LoraParams p) {
             u[2 * k + 1] = fabsf(b) < INFINITY ? b - hi16<DT>(v[k]) : 0.f;
           }
           const int k = t * p.r16 + j;                  // along u's terms: 128-byte swizzled rows of 64
-          *reinterpret_cast<uint4*>(smem + (k >> 6) * kXBytes + i * 128 + ((((k & 63) >> 3) ^ (i & 7)) << 4)) =
+          *reinterpret_cast<uint4*>(smem + (k >> 6) * kXBytes + r * 128 + ((((k & 63) >> 3) ^ (r & 7)) << 4)) =
               make_uint4(v[0], v[1], v[2], v[3]);
         }
       }
-    }
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    asm volatile("bar.sync 1, 256;" ::: "memory");      // back[] and, before the barrier below, every lane's u
-    mbar_arrive_if(u_full, lane == 0);
-
-    // ---------------- sums to memory ----------------
-    const int q = warp & 3, h = (warp - 2) >> 2;        // this warp's 32 rows, and 64 of the 128 columns
-    constexpr int kEl = F32 ? 4 : 2, kLanes = F32 ? 8 : 4, kRows = 32 / kLanes, kIts = kLanes;   // lanes per row of 32 columns
-    const uint8_t* base = static_cast<const uint8_t*>(p.base);
-    uint8_t* out = static_cast<uint8_t*>(p.out);
-    float* stage = reinterpret_cast<float*>(smem + p.u_bytes + p.stages * p.w_stage) + (warp - 2) * 32 * kStagePitch;
-    const int my_at = ad.at[32 * q + lane];
-    const float my_back = DT == SITU_DT_F16 ? back[32 * q + lane] : 1.f;
-    const int r_in = lane / kLanes, c_in = lane % kLanes * (16 / kEl);
-    auto place = [&](int it, int col, long ld) {        // of 16 bytes: bytes from the array's start
-      return ((size_t)(row0 + 32 * q + it * kRows + r_in) * (size_t)ld + col + c_in) * kEl;
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      epi_sync(kExpandEpi);                             // back[] and, before the arrivals, every lane's u
+      mbar_arrive_if(u_full, lane == 0);
     };
-    // rows without an adapter take base as it is
-    if (p.base != p.out && __any_sync(0xffffffffu, my_at == kNone)) {
-      for (int b = b0; b < b1; ++b)
-        for (int c = 0; c < 64; c += 32) {
-          const int col = b * kCols + 64 * h + c;
-#pragma unroll
-          for (int it = 0; it < kIts; ++it)
-            if (ad.at[32 * q + it * kRows + r_in] == kNone && col + c_in < p.C)
-              *reinterpret_cast<uint4*>(out + place(it, col, p.ldo)) =
-                  base ? *reinterpret_cast<const uint4*>(base + place(it, col, p.ld_base)) : make_uint4(0, 0, 0, 0);
-        }
+    Segment g(i0, i1, blocks);
+    if (g.more()) {
+      list(g);
+      griddep_wait();                                   // the parts are the predecessor's: base and weights come meanwhile
+      stage_u(g, lists[0]);
     }
-    Turns acc(2);
-    bool ok = true;
-    for (int b = b0; b < b1 && ok; ++b)
-      for (int d = 0; d < nd; ++d, acc.next()) {
-        const bool work = __any_sync(0xffffffffu, my_at == d);
-        uint4 y[2][kIts];
-        if (work) {
-          // base on its way while the sums are made
-#pragma unroll
-          for (int c = 0; c < 2; ++c)
-#pragma unroll
-            for (int it = 0; it < kIts; ++it) {
-              const int col = b * kCols + 64 * h + 32 * c;
-              y[c][it] = base && ad.at[32 * q + it * kRows + r_in] == d && col + c_in < p.C
-                             ? *reinterpret_cast<const uint4*>(base + place(it, col, p.ld_base))
-                             : make_uint4(0, 0, 0, 0);
-            }
-        }
-        if (!warp_wait(acc_full(acc.s), acc.ph, p.err, 97)) {
+    for (int lb = 0; g.more(); lb ^= 1) {
+      Segment n = g;
+      n.next();
+      if (n.more()) list(n);
+      const Adapters& ad = lists[lb];
+      const int nd = ad.count, at = ad.at[32 * q + lane];
+      const float my_back = DT == SITU_DT_F16 ? back[32 * q + lane] : 1.f;
+      for (int b = g.from; b < g.to && ok; ++b, y.next()) {
+        uint8_t* mine = smem + (ybase - sbase) + y.s * 2 * kXBytes + h * kXBytes + (32 * q + lane) * 128;
+        auto piece = [&](int j) { return reinterpret_cast<uint4*>(mine + ((j ^ (lane & 7)) << 4)); };
+        if (!warp_wait(yfull(y.s), y.ph, p.err, 111)) {
           ok = false;
           break;
         }
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        if (work) {
+        if (!p.base) {
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int col = b * kCols + 64 * h + 32 * c;
-            uint32_t v[32];
-            tmem_ld32_nowait(tmem + ((uint32_t)(32 * q) << 16) + acc.s * kCols + 64 * h + 32 * c, v);
-            tmem_ld_wait<32>(v);
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 32; i += 4)
-              *reinterpret_cast<float4*>(stage + lane * kStagePitch + i) =
-                  make_float4(__uint_as_float(v[i]) * my_back, __uint_as_float(v[i + 1]) * my_back,
-                              __uint_as_float(v[i + 2]) * my_back, __uint_as_float(v[i + 3]) * my_back);
-            __syncwarp();
-#pragma unroll
-            for (int it = 0; it < kIts; ++it) {
-              const int r = it * kRows + r_in;
-              if (ad.at[32 * q + r] != d || col + c_in >= p.C) continue;
-              const float* src = stage + r * kStagePitch + c_in;
-              const float4 a = *reinterpret_cast<const float4*>(src);
-              uint4 o = y[c][it];
-              if (F32) {
-                o.x = __float_as_uint(__uint_as_float(o.x) + a.x);
-                o.y = __float_as_uint(__uint_as_float(o.y) + a.y);
-                o.z = __float_as_uint(__uint_as_float(o.z) + a.z);
-                o.w = __float_as_uint(__uint_as_float(o.w) + a.w);
-              } else {
-                const float4 e = *reinterpret_cast<const float4*>(src + 4);
-                o.x = pack16<DT>(lo16<DT>(o.x) + a.x, hi16<DT>(o.x) + a.y);
-                o.y = pack16<DT>(lo16<DT>(o.y) + a.z, hi16<DT>(o.y) + a.w);
-                o.z = pack16<DT>(lo16<DT>(o.z) + e.x, hi16<DT>(o.z) + e.y);
-                o.w = pack16<DT>(lo16<DT>(o.w) + e.z, hi16<DT>(o.w) + e.w);
-              }
-              *reinterpret_cast<uint4*>(out + place(it, col, p.ldo)) = o;
-            }
-          }
+          for (int j = 0; j < 8; ++j) *piece(j) = make_uint4(0, 0, 0, 0);
         }
-        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-        mbar_arrive_if(acc_empty(acc.s), lane == 0);
+        for (int d = 0; d < nd; ++d, acc.next()) {
+          if (!warp_wait(acc_full(acc.s), acc.ph, p.err, 112)) {
+            ok = false;
+            break;
+          }
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          if (__any_sync(0xffffffffu, at == d)) {
+            const uint32_t from = tmem + ((uint32_t)(32 * q) << 16) + acc.s * kCols + kBoxCols * h;
+#pragma unroll
+            for (int c = 0; c < kBoxCols / 32; ++c) {
+              uint32_t v[32];
+              __syncwarp();
+              tmem_ld32_nowait(from + 32 * c, v);
+              tmem_ld_wait<32>(v);
+              if (DT == SITU_DT_F16) {
+#pragma unroll
+                for (int t = 0; t < 32; ++t) v[t] = __float_as_uint(__uint_as_float(v[t]) * my_back);
+              }
+              if (at == d && F32) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                  uint4 o = *piece(j);
+                  o.x = __float_as_uint(__uint_as_float(o.x) + __uint_as_float(v[4 * j]));
+                  o.y = __float_as_uint(__uint_as_float(o.y) + __uint_as_float(v[4 * j + 1]));
+                  o.z = __float_as_uint(__uint_as_float(o.z) + __uint_as_float(v[4 * j + 2]));
+                  o.w = __float_as_uint(__uint_as_float(o.w) + __uint_as_float(v[4 * j + 3]));
+                  *piece(j) = o;
+                }
+              } else if (at == d) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  uint4 o = *piece(4 * c + j);
+                  uint32_t* ow = reinterpret_cast<uint32_t*>(&o);
+#pragma unroll
+                  for (int t = 0; t < 4; ++t)
+                    ow[t] = pack16<DT>(lo16<DT>(ow[t]) + __uint_as_float(v[8 * j + 2 * t]),
+                                       hi16<DT>(ow[t]) + __uint_as_float(v[8 * j + 2 * t + 1]));
+                  *piece(4 * c + j) = o;
+                }
+              }
+            }
+            __syncwarp();
+          }
+          asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+          mbar_arrive_if(acc_empty(acc.s), lane == 0);
+        }
+        if (!ok) break;
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        mbar_arrive_if(ydone(y.s), lane == 0);
       }
+      g = n;
+      if (g.more()) {
+        epi_sync(kExpandEpi);                           // every warp is done with back[], and the MMAs with u
+        stage_u(g, lists[lb ^ 1]);
+      }
+    }
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   if (warp == 1) {
     __syncwarp();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-    tmem_free<1>(tmem, kTmemCols);
+    tmem_free<1>(tmem, 256);
   }
 }
 
@@ -772,36 +952,65 @@ expand_kernel(const __grid_constant__ CUtensorMap map_w, const LoraParams p) {
 // launches
 // --------------------------------------------------------------------------
 
-// Parts of the contraction: two CTAs per SM, parts of at least two stages.  For
-// fp32 results a part is 1,024 elements at most: the tensor cores truncate when
-// they add (6e-9 of a sum of one sign per element), the parts meet in fp32.
-int splits_of(int S, int C, bool f32) {
-  const int tiles = (S + kTile - 1) / kTile, chunks = (C + kChunk - 1) / kChunk;
-  int s = 2 * 152 / tiles;
-  if (s > chunks / 2) s = chunks / 2;
-  if (f32 && s < (chunks + 15) / 16) s = (chunks + 15) / 16;
-  return s < 1 ? 1 : s;
+// CTAs of the shrink: one per SM, of at least two chunks.  For fp32 results a
+// CTA takes 1,024 elements at most: the tensor cores truncate when they add (6e-9
+// of a sum of one sign per element), a tile's parts meet in fp32.  Then they come
+// in whole rounds of two per SM.
+long shrink_ctas(int S, int C, bool f32) {
+  const long tiles = (S + kTile - 1) / kTile, chunks = (C + kChunk - 1) / kChunk, total = tiles * chunks;
+  const long sms = sm_count(), most = total / 2, least = f32 ? (total + 15) / 16 : 1;
+  long g = least <= sms ? sms : (least + 2 * sms - 1) / (2 * sms) * 2 * sms;
+  if (g > most) g = most > least ? most : least;
+  return g < 1 ? 1 : g;
+}
+// the most parts that a tile's chunks can come in
+long most_parts(int S, int C, bool f32) {
+  const long tiles = (S + kTile - 1) / kTile, chunks = (C + kChunk - 1) / kChunk, G = shrink_ctas(S, C, f32);
+  const long least = tiles * chunks / G, most = (chunks + least - 2) / least + 1;
+  return most < chunks ? most : chunks;
 }
 
+struct Maps {
+  CUtensorMap x, w, other, base, out;
+};
+
 template <int DT, bool TRANS, bool F32>
-cudaError_t launch_pair(const CUtensorMap& mx, const CUtensorMap& mw, const LoraParams& s, const CUtensorMap& mo, LoraParams x,
-                        cudaStream_t st) {
+cudaError_t launch_pair(const Maps& m, LoraParams s, LoraParams x, cudaStream_t st) {
   auto* shrink = shrink_kernel<DT, TRANS>;
   auto* expand = expand_kernel<DT, TRANS, F32>;
-  const unsigned tiles = (unsigned)((s.S + kTile - 1) / kTile);
-  const int shrink_smem = 1024 + kStages * (kXBytes + s.w_stage);
-  x.u_bytes = (terms_of(DT, F32) * x.r16 + 63) / 64 * kXBytes;
-  const int rest = 1024 + x.u_bytes + kEpiThreads / 32 * 32 * kStagePitch * 4;
-  x.stages = rest + 3 * x.w_stage <= 108 * 1024 || rest + 2 * x.w_stage > 108 * 1024 ? 3 : 2;   // two CTAs per SM where that does it
-  if (rest + x.stages * x.w_stage > 224 * 1024) x.stages = 2;
-  const int expand_smem = rest + x.stages * x.w_stage;
-  // in every call, so that a context created anew has them too
-  cudaError_t e = cudaFuncSetAttribute(shrink, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(expand, cudaFuncAttributeMaxDynamicSharedMemorySize, 224 * 1024);
+  static std::atomic<uint64_t> raised{0};   // the shared memory limits, once per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  shrink<<<dim3(tiles, (unsigned)s.splits), kShrinkThreads, shrink_smem, st>>>(mx, mw, s);
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (bit == 0 || !(raised.load() & bit)) {
+    std::lock_guard<std::mutex> lock(attr_mutex());
+    e = cudaFuncSetAttribute(shrink, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(expand, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost);
+    if (e != cudaSuccess) return e;
+    raised.fetch_or(bit);
+  }
+  const long sms = sm_count();
+  const int at_once = s.shrink_ctas > sms ? 2 : 1;      // shrink CTAs per SM
+  s.tmem_cols = kTmemCols / at_once;
+  s.stages = (kSmemMost / at_once - 1024 - 4096 * (at_once - 1)) / (kXBytes + s.w_stage);
+  if (s.stages > kMaxStages) s.stages = kMaxStages;
+  shrink<<<(unsigned)s.shrink_ctas, kShrinkThreads, 1024 + s.stages * (kXBytes + s.w_stage), st>>>(m.x, m.w, s);
   e = cudaGetLastError();
-  return e != cudaSuccess ? e : launch_pdl(expand, dim3(tiles, (unsigned)x.groups), dim3(kExpandThreads), expand_smem, st, mo, x);
+  if (e != cudaSuccess) return e;
+  x.u_bytes = (terms_of(DT, F32) * x.r16 + 63) / 64 * kXBytes;
+  // four items of base and four of weights where they fit (16,384 x 6144 bf16 at
+  // rank 64: 69 us; five and two: 75, three and two: 79), else base first
+  int rest;
+  for (x.stages = 4;; --x.stages) {
+    rest = 1024 + x.u_bytes + x.stages * x.w_stage;
+    x.y_stages = (kSmemMost - rest) / (2 * kXBytes);
+    if (x.y_stages > 4) x.y_stages = 4;
+    if (x.y_stages >= 3 || x.stages == 2) break;
+  }
+  const long items = (long)x.tiles * ((x.C + cols_of(F32) - 1) / cols_of(F32));
+  return launch_pdl(expand, dim3((unsigned)(items < sms ? items : sms)), dim3(kExpandThreads), rest + x.y_stages * 2 * kXBytes,
+                    st, m.other, m.base, m.out, x);
 }
 
 // x [S, C] times the adapters' w [n, r, C] (TRANS: [n, C, r]), and that times
@@ -812,35 +1021,41 @@ situ_status launch_tiles(int dtype, bool f32, const void* rows, int64_t ld_rows,
   const uint64_t S = (uint64_t)s.S, C = (uint64_t)s.C, O = (uint64_t)x.C, r = (uint64_t)s.r, n = (uint64_t)s.n;
   s.r16 = x.r16 = (s.r + 15) / 16 * 16;
   s.chunks = (s.C + kChunk - 1) / kChunk;
-  s.splits = x.splits = splits_of(s.S, s.C, f32);
+  s.tiles = x.tiles = (s.S + kTile - 1) / kTile;
+  s.shrink_ctas = x.shrink_ctas = shrink_ctas(s.S, s.C, f32);
+  x.chunks = s.chunks;
   const int boxes = (s.r + 63) / 64;
   s.w_stage = boxes * 8192;
   const int rrows = s.r16 < 64 ? s.r16 : 64;
-  x.w_stage = TRANS ? boxes * 2 * rrows * 128 : boxes * kXBytes;
-  const int tiles = (s.S + kTile - 1) / kTile, blocks = (x.C + kCols - 1) / kCols;
-  // column groups: about four CTAs per SM, of two blocks or more (u is read and laid out by each)
-  const int groups = (4 * 152 + tiles - 1) / tiles, most = blocks > 2 ? blocks / 2 : 1;
-  x.groups = groups < most ? groups : most;
+  const int cols = cols_of(f32);
+  x.w_stage = TRANS ? boxes * (cols / 64) * rrows * 128 : boxes * cols * 128;
   const CUtensorMapDataType dt = dtype == SITU_DT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  CUtensorMap mx, mw, mo;
+  Maps m;
   const uint64_t dx[2] = {C, S}, sx[1] = {(uint64_t)ld_rows * 2};
   const uint32_t bx[2] = {64, kTile};
-  bool ok = make_map_nd(&mx, dt, rows, 2, dx, sx, bx);
+  bool ok = make_map_nd(&m.x, dt, rows, 2, dx, sx, bx);
   if (TRANS) {
     const uint64_t dw[3] = {r, C, n}, sw[2] = {r * 2, r * C * 2}, dof[3] = {O, r, n}, so[2] = {O * 2, r * O * 2};
     const uint32_t bw[3] = {64, kChunk, 1}, bo[3] = {64, (uint32_t)rrows, 1};
-    ok = ok && make_map_nd(&mw, dt, w, 3, dw, sw, bw) && make_map_nd(&mo, dt, other, 3, dof, so, bo);
+    ok = ok && make_map_nd(&m.w, dt, w, 3, dw, sw, bw) && make_map_nd(&m.other, dt, other, 3, dof, so, bo);
   } else {
     const uint64_t dw[3] = {C, r, n}, sw[2] = {C * 2, r * C * 2}, dof[3] = {r, O, n}, so[2] = {r * 2, r * O * 2};
-    const uint32_t bw[3] = {64, (uint32_t)s.r16, 1}, bo[3] = {64, kCols, 1};
-    ok = ok && make_map_nd(&mw, dt, w, 3, dw, sw, bw) && make_map_nd(&mo, dt, other, 3, dof, so, bo);
+    const uint32_t bw[3] = {64, (uint32_t)s.r16, 1}, bo[3] = {64, (uint32_t)cols, 1};
+    ok = ok && make_map_nd(&m.w, dt, w, 3, dw, sw, bw) && make_map_nd(&m.other, dt, other, 3, dof, so, bo);
+  }
+  const uint64_t dy[2] = {O, S}, el = f32 ? 4 : 2, syo[1] = {(uint64_t)x.ldo * el};
+  const uint32_t by[2] = {(uint32_t)cols / 2, kTile};
+  const CUtensorMapDataType ot = f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : dt;
+  ok = ok && make_map_nd(&m.out, ot, x.out, 2, dy, syo, by);
+  m.base = m.out;
+  if (x.base) {
+    const uint64_t syb[1] = {(uint64_t)x.ld_base * el};
+    ok = ok && make_map_nd(&m.base, ot, x.base, 2, dy, syb, by);
   }
   if (!ok) return SITU_ERR_CUDA;
   constexpr int kB = SITU_DT_BF16, kF = SITU_DT_F16;
-  const cudaError_t e = dtype == kB ? (f32 ? launch_pair<kB, TRANS, true>(mx, mw, s, mo, x, st)
-                                           : launch_pair<kB, TRANS, false>(mx, mw, s, mo, x, st))
-                                    : (f32 ? launch_pair<kF, TRANS, true>(mx, mw, s, mo, x, st)
-                                           : launch_pair<kF, TRANS, false>(mx, mw, s, mo, x, st));
+  const cudaError_t e = dtype == kB ? (f32 ? launch_pair<kB, TRANS, true>(m, s, x, st) : launch_pair<kB, TRANS, false>(m, s, x, st))
+                                    : (f32 ? launch_pair<kF, TRANS, true>(m, s, x, st) : launch_pair<kF, TRANS, false>(m, s, x, st));
   return e == cudaSuccess ? SITU_OK : SITU_ERR_CUDA;
 }
 
@@ -848,10 +1063,15 @@ situ_status launch_tiles(int dtype, bool f32, const void* rows, int64_t ld_rows,
 bool by_rows(int S) { return S <= 64; }
 
 // for either type of result
-size_t part_bytes(int S, int C, int r) { return S == 0 ? 0 : (size_t)splits_of(S, C, true) * S * r * 4; }
+size_t part_bytes(int S, int C, int r) {
+  if (S == 0) return 0;
+  const long a = most_parts(S, C, false), b = most_parts(S, C, true);
+  return (size_t)(a > b ? a : b) * S * r * 4;
+}
 
 bool bad(const void* q, uintptr_t mask) { return (reinterpret_cast<uintptr_t>(q) & mask) != 0; }
-bool bad_ld(int64_t ld, int64_t cols, int64_t unit) { return ld < cols || ld % unit != 0 || ld > (int64_t)1 << 39; }
+// the tensor maps take strides below 2^40 bytes
+bool bad_ld(int64_t ld, int64_t cols, int64_t unit) { return ld < cols || ld % unit != 0 || ld >= (int64_t)1 << 38; }
 bool bad_extent(int C) { return C < 8 || C % 8 != 0 || C > SITU_GEMM_MAX_DIM; }
 bool bad_sizes(int S, int K, int N, int r, int n) {
   return S < 0 || S > SITU_GEMM_MAX_ROWS || bad_extent(K) || bad_extent(N) || r < 8 || r % 8 != 0 || r > kMaxRank || n < 1 ||
