@@ -12,11 +12,15 @@
 // Bound by memory: the forward reads the logits once, the gradient reads them
 // again (keeping p would take a write and a read more) and writes as much.
 // A group of L lanes holds a row in registers, 4 NV columns a lane, so that
-// maximum, sum and the weighted sum take no second read; the same lanes see
-// the same columns in every row, so column sums and the f_e stay in registers
-// too.  The next row's loads are issued before the present row is worked on.
-// Column sums are fp32 within a CTA (a few hundred rows), fp64 across CTAs, in
-// a fixed order: results do not depend on the order of execution.
+// maximum, sum and the weighted sum take no second read.  The same lanes see the
+// same columns in every row, so the forward's column sums stay in registers too;
+// it issues the next row's loads before it works on the present one.  The
+// gradient's f_e are in shared memory, which leaves room for half as many rows
+// again.  Column sums are fp32 within a CTA (a few hundred rows) and two-sums of
+// fp32 across CTAs, in a fixed order: results do not depend on the order of
+// execution.
+// Measured (65,536 x 896, top-16): forward 43 us (5.5 TB/s) and 7 for the join,
+// gradient 76 to 81 (6 TB/s).
 #include "../../include/situ_moe.h"
 #include "situ_internal.h"
 
@@ -28,11 +32,12 @@ namespace situ {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kFwdThreads = 512;     // one CTA per SM, so that there are few partial sums
+constexpr int kBackThreads = 256;    // three CTAs per SM
 constexpr int kMaxExperts = SITU_MAX_LOCAL_EXPERTS;
 constexpr int kFinalCtas = 8;        // of the joining kernel's one cluster
 constexpr int kFinalThreads = 512;
-constexpr int kMaxGrid = 2 * 152;    // two CTAs per SM: also the number of partial sums
+constexpr int kSms = 152;
 
 struct BalanceParams {
   const float* logits;
@@ -44,7 +49,8 @@ struct BalanceParams {
   float* loss;
   int32_t *counts, *tokens;
   float2* stats;
-  // partial sums: [grid][E] each, then a token count per CTA
+  // partial sums: [grid][pitch] each, pitch = E rounded up to 4, then a token count per CTA
+  int pitch;
   float* part_p;
   int32_t *part_c, *part_n;
 };
@@ -112,16 +118,16 @@ __device__ __forceinline__ float fmax_op(float a, float b) { return fmaxf(a, b);
 __device__ __forceinline__ float add_op(float a, float b) { return a + b; }
 
 template <int L, int NV, bool VEC>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kFwdThreads, 1)
 balance_kernel(BalanceParams p) {
-  constexpr int kGroups = kThreads / L, V = 4 * NV;
+  constexpr int kGroups = kFwdThreads / L, V = 4 * NV;
   extern __shared__ float smem[];              // column sums [E], counts [E]
   __shared__ float red[kGroups][8];
   __shared__ int tokens_s;
-  __shared__ double loss_s[kThreads / kWarp];
+  __shared__ double loss_s[kFwdThreads / kWarp];
   float* sum_p = smem;
   int* hist = reinterpret_cast<int*>(smem + p.E);
-  for (int e = threadIdx.x; e < p.E; e += kThreads) {
+  for (int e = threadIdx.x; e < p.E; e += kFwdThreads) {
     sum_p[e] = 0.f;
     hist[e] = 0;
   }
@@ -167,13 +173,14 @@ balance_kernel(BalanceParams p) {
     }
     if (id >= 0 && id < p.E) atomicAdd(hist + id, 1);
   }
+  griddep_launch_dependents();
   if (mine) atomicAdd(&tokens_s, mine);
   // the groups' column sums, in the groups' order
   if (L < kWarp) {
 #pragma unroll
     for (int c = 0; c < V; ++c) acc[c] += __shfl_xor_sync(0xffffffffu, acc[c], 16);
   }
-  constexpr int kTurns = L < kWarp ? kThreads / kWarp : kGroups;
+  constexpr int kTurns = L < kWarp ? kFwdThreads / kWarp : kGroups;
   for (int w = 0; w < kTurns; ++w) {
     if (L < kWarp ? (int)threadIdx.x / kWarp == w && (threadIdx.x & 31) < L : g.id == w) {
 #pragma unroll
@@ -187,17 +194,17 @@ balance_kernel(BalanceParams p) {
     __syncthreads();
   }
   if (gridDim.x > 1) {
-    const size_t at = (size_t)blockIdx.x * p.E;
-    for (int e = threadIdx.x; e < p.E; e += kThreads) {
-      p.part_p[at + e] = sum_p[e];
-      p.part_c[at + e] = hist[e];
+    const size_t at = (size_t)blockIdx.x * p.pitch;
+    for (int e = threadIdx.x; e < p.pitch; e += kFwdThreads) {
+      p.part_p[at + e] = e < p.E ? sum_p[e] : 0.f;
+      p.part_c[at + e] = e < p.E ? hist[e] : 0;
     }
     if (threadIdx.x == 0) p.part_n[blockIdx.x] = tokens_s;
     return;
   }
   // the only CTA: the whole result
   double l = 0.0;
-  for (int e = threadIdx.x; e < p.E; e += kThreads) {
+  for (int e = threadIdx.x; e < p.E; e += kFwdThreads) {
     p.counts[e] = hist[e];
     l += (double)hist[e] * (double)sum_p[e];
   }
@@ -207,104 +214,137 @@ balance_kernel(BalanceParams p) {
   __syncthreads();
   if (threadIdx.x == 0) {
     double a = 0.0;
-    for (int w = 0; w < kThreads / kWarp; ++w) a += loss_s[w];
+    for (int w = 0; w < kFwdThreads / kWarp; ++w) a += loss_s[w];
     const double n = tokens_s;
     *p.tokens = tokens_s;
     *p.loss = n > 0 ? (float)((double)p.coef * p.E * a / (n * n * p.k)) : 0.f;
   }
 }
 
-// Joins `parts` CTAs' sums: one cluster, a share of the columns per CTA, each
-// column's parts in slices; the loss's terms meet in CTA 0.
-__global__ void __cluster_dims__(kFinalCtas, 1, 1) __launch_bounds__(kFinalThreads)
+// An fp32 sum and what its additions lost (Knuth's two-sum): 48 bits at the
+// price of six fp32 additions, of which this GPU does 64 times as many as fp64
+// ones (with these the join of 304 parts of 896 took 25 us).
+struct Sum {
+  float s = 0.f, lost = 0.f;
+  __device__ __forceinline__ void add(float a) {
+    const float t = __fadd_rn(s, a), z = __fadd_rn(t, -s);
+    lost = __fadd_rn(lost, __fadd_rn(__fadd_rn(s, -__fadd_rn(t, -z)), __fadd_rn(a, -z)));
+    s = t;
+  }
+};
+
+// Joins `parts` CTAs' sums: one cluster of CTAS, a share of the columns per CTA,
+// four columns a thread, their parts in up to 32 slices; the loss's terms meet in
+// CTA 0.  One CTA where that is no more than 256 KB to read.
+template <int CTAS>
+__global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kFinalThreads)
 balance_join_kernel(BalanceParams p, int parts) {
   namespace cg = cooperative_groups;
-  __shared__ double slice_p[kFinalThreads];
-  __shared__ int slice_c[kFinalThreads];
+  __shared__ float2 slice_p[4][kFinalThreads];
+  __shared__ int slice_c[4][kFinalThreads];
   __shared__ double warp_l[kFinalThreads / kWarp];
-  __shared__ double cta_l[kFinalCtas];
+  __shared__ double cta_l[CTAS];
   __shared__ int tokens_s;
+  if (CTAS > 1) cluster_arrive();                      // CTA 0 has begun before its shared memory is written
+  if (threadIdx.x == 0) tokens_s = 0;
   griddep_wait();
   cg::cluster_group cluster = cg::this_cluster();
-  const int rank = (int)cluster.block_rank();
-  const int cols = (p.E + kFinalCtas - 1) / kFinalCtas, c0 = rank * cols, width = max(0, min(cols, p.E - c0));
-  const int slices = max(1, kFinalThreads / cols);      // cols <= 512
+  const int rank = CTAS > 1 ? (int)cluster.block_rank() : 0;
+  const int quads = p.pitch / 4, cols = (quads + CTAS - 1) / CTAS, c0 = rank * cols, width = max(0, min(cols, quads - c0));
+  const int slices = min(32, kFinalThreads / cols);      // cols <= 128
   const int c = threadIdx.x % cols, s = threadIdx.x / cols;
-  double a = 0.0;
-  int n = 0;
+  Sum a[4];
+  int n[4] = {0, 0, 0, 0};
   if (c < width && s < slices) {
-#pragma unroll 4
+    const float4* pp = reinterpret_cast<const float4*>(p.part_p) + c0 + c;
+    const int4* pc = reinterpret_cast<const int4*>(p.part_c) + c0 + c;
+#pragma unroll 8
     for (int i = s; i < parts; i += slices) {
-      a += (double)__ldcg(p.part_p + (size_t)i * p.E + c0 + c);
-      n += __ldcg(p.part_c + (size_t)i * p.E + c0 + c);
+      const float4 v = __ldcg(pp + (size_t)i * quads);
+      const int4 k = __ldcg(pc + (size_t)i * quads);
+      a[0].add(v.x);
+      a[1].add(v.y);
+      a[2].add(v.z);
+      a[3].add(v.w);
+      n[0] += k.x;
+      n[1] += k.y;
+      n[2] += k.z;
+      n[3] += k.w;
     }
   }
-  slice_p[threadIdx.x] = a;
-  slice_c[threadIdx.x] = n;
-  if (threadIdx.x == 0) tokens_s = 0;
-  cluster_arrive();                      // CTA 0 has begun before its shared memory is written
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    slice_p[j][threadIdx.x] = make_float2(a[j].s, a[j].lost);
+    slice_c[j][threadIdx.x] = n[j];
+  }
   __syncthreads();
   double l = 0.0;
-  if (s == 0 && c < width) {
-    for (int i = 1; i < slices; ++i) {
-      a += slice_p[i * cols + c];
-      n += slice_c[i * cols + c];
+  for (int o = threadIdx.x; o < 4 * width; o += kFinalThreads) {   // a column a thread
+    const int q = o >> 2, j = o & 3, e = 4 * (c0 + q) + j;
+    Sum t;
+    float lost = 0.f;
+    int k = 0;
+    for (int i = 0; i < slices; ++i) {
+      const float2 v = slice_p[j][i * cols + q];
+      t.add(v.x);
+      lost += v.y;
+      k += slice_c[j][i * cols + q];
     }
-    p.counts[c0 + c] = n;
-    l = (double)n * a;
+    if (e < p.E) {
+      p.counts[e] = k;
+      l += (double)k * ((double)t.s + (double)(t.lost + lost));
+    }
   }
   if (rank == 0 && (int)threadIdx.x < parts) atomicAdd(&tokens_s, __ldcg(p.part_n + threadIdx.x));
 #pragma unroll
   for (int d = 16; d >= 1; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
   if ((threadIdx.x & 31) == 0) warp_l[threadIdx.x >> 5] = l;
   __syncthreads();
-  cluster_wait();
+  if (CTAS > 1) cluster_wait();
   if (threadIdx.x == 0) {
     double t = 0.0;
     for (int w = 0; w < kFinalThreads / kWarp; ++w) t += warp_l[w];
-    *cluster.map_shared_rank(&cta_l[rank], 0) = t;
+    *(CTAS > 1 ? cluster.map_shared_rank(&cta_l[rank], 0) : &cta_l[0]) = t;
   }
-  cluster.sync();
+  if (CTAS > 1) cluster.sync();
   if (rank == 0 && threadIdx.x == 0) {
     double t = 0.0;
-    for (int i = 0; i < kFinalCtas; ++i) t += cta_l[i];
+    for (int i = 0; i < CTAS; ++i) t += cta_l[i];
     const double tok = tokens_s;
     *p.tokens = tokens_s;
     *p.loss = tok > 0 ? (float)((double)p.coef * p.E * t / (tok * tok * p.k)) : 0.f;
   }
 }
-static_assert(kMaxExperts / kFinalCtas <= kFinalThreads && kMaxGrid <= kFinalThreads, "a thread per column, per part");
+static_assert(kMaxExperts / 4 / kFinalCtas <= kFinalThreads && kSms <= kFinalThreads, "a thread per four columns, per part");
 
 template <int L, int NV, bool VEC>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kBackThreads, 3)
 router_back_kernel(RouterBackParams p) {
-  constexpr int kGroups = kThreads / L, V = 4 * NV, kPitch = 4 * L * NV;
+  constexpr int kGroups = kBackThreads / L, V = 4 * NV, kPitch = 4 * L * NV;
   extern __shared__ float4 smem4[];            // a row of the chosen slots' terms per group, zeros between rows
   __shared__ float red[kGroups][8];
   const Group<L> g;
   float* mine = reinterpret_cast<float*>(smem4) + g.id * kPitch;
   for (int c = g.lane; c < kPitch; c += L) mine[c] = 0.f;
   g.sync();
-  // F_e = dloss coef E / n f_e in this lane's columns
-  float F[V], cur[V];
+  // F_e = dloss coef E / n f_e of every column: in shared memory, the lanes' own in
+  // registers would leave room for half the rows
+  float* F_s = reinterpret_cast<float*>(smem4) + kGroups * kPitch;
   {
     const int n = p.tokens ? *p.tokens : 0;
     const float gl = p.dloss && n > 0 ? (float)((double)*p.dloss * p.coef * p.E / ((double)n * n * p.k)) : 0.f;
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int c = 4 * (g.lane + L * j) + i;
-        F[4 * j + i] = p.dloss && c < p.E ? (float)p.counts[c] * gl : 0.f;
-      }
+    for (int c = threadIdx.x; c < kPitch; c += kBackThreads) F_s[c] = p.dloss && c < p.E ? (float)p.counts[c] * gl : 0.f;
   }
+  __syncthreads();
+  auto F4 = [&](int j) { return *reinterpret_cast<const float4*>(F_s + 4 * (g.lane + L * j)); };
   int turn = 0;
   const long step = (long)gridDim.x * kGroups;
   const long first = (long)blockIdx.x * kGroups + g.id;
   const long rounds = (p.T - (long)blockIdx.x * kGroups + step - 1) / step;
-  load_row<L, NV, VEC>(cur, p.logits + (size_t)min(first, (long)p.T - 1) * p.ld, g.lane, p.E, -INFINITY);
   for (long i = 0; i < rounds; ++i) {
     const long t = first + i * step;
+    float v[V];
+    load_row<L, NV, VEC>(v, p.logits + (size_t)min(t, (long)p.T - 1) * p.ld, g.lane, p.E, -INFINITY);
     const bool have = t < p.T;
     const bool slot = have && p.dw && g.lane < p.k;
     const float2 st = have ? __ldg(p.stats + t) : make_float2(0.f, 0.f);
@@ -320,14 +360,14 @@ router_back_kernel(RouterBackParams p) {
       }
     }
     const bool keep = have && (!p.mask || p.mask[t] != 0);
-    float v[V];
     float dot = 0.f;
 #pragma unroll
-    for (int c = 0; c < V; ++c) {
-      v[c] = exp2_approx((cur[c] - st.x) * kLog2e) * st.y;
-      dot = fmaf(F[c], v[c], dot);
+    for (int j = 0; j < NV; ++j) {
+      const float4 F = F4(j);
+#pragma unroll
+      for (int c = 4 * j; c < 4 * j + 4; ++c) v[c] = exp2_approx((v[c] - st.x) * kLog2e) * st.y;
+      dot = fmaf(F.x, v[4 * j], fmaf(F.y, v[4 * j + 1], fmaf(F.z, v[4 * j + 2], fmaf(F.w, v[4 * j + 3], dot))));
     }
-    load_row<L, NV, VEC>(cur, p.logits + (size_t)min(t + step, (long)p.T - 1) * p.ld, g.lane, p.E, -INFINITY);
     dot = g.reduce(dot, red[g.id], turn, add_op);
     float wd = 0.f;
     if (p.dw) {
@@ -361,10 +401,11 @@ router_back_kernel(RouterBackParams p) {
     for (int j = 0; j < NV; ++j) {
       const int c = 4 * (g.lane + L * j);
       float4 x = p.dw ? *reinterpret_cast<const float4*>(mine + c) : make_float4(0.f, 0.f, 0.f, 0.f);
-      x.x = fmaf(v[4 * j], (keep ? F[4 * j] : 0.f) - sub, x.x);
-      x.y = fmaf(v[4 * j + 1], (keep ? F[4 * j + 1] : 0.f) - sub, x.y);
-      x.z = fmaf(v[4 * j + 2], (keep ? F[4 * j + 2] : 0.f) - sub, x.z);
-      x.w = fmaf(v[4 * j + 3], (keep ? F[4 * j + 3] : 0.f) - sub, x.w);
+      const float4 F = keep ? F4(j) : make_float4(0.f, 0.f, 0.f, 0.f);
+      x.x = fmaf(v[4 * j], F.x - sub, x.x);
+      x.y = fmaf(v[4 * j + 1], F.y - sub, x.y);
+      x.z = fmaf(v[4 * j + 2], F.z - sub, x.z);
+      x.w = fmaf(v[4 * j + 3], F.w - sub, x.w);
       if (!have) continue;
       float* o = p.out + (size_t)t * p.ldo + c;
       if (VEC) {
@@ -407,15 +448,15 @@ cudaError_t with_shape(int E, bool vec, F&& f) {
 #undef SITU_SHAPE
 }
 
-int grid_of(int T, int E) {
-  const int groups = kThreads / (E <= 128 ? 16 : E <= 1024 ? 32 : 128);
+int grid_of(int T, int E, int threads, int most) {
+  const int groups = threads / (E <= 128 ? 16 : E <= 1024 ? 32 : 128);
   const long rows = (T + groups - 1) / groups;
-  return (int)(rows < 1 ? 1 : rows > kMaxGrid ? kMaxGrid : rows);
+  return (int)(rows < 1 ? 1 : rows > most ? most : rows);
 }
 // One CTA does the whole forward up to this many rows per group: a second
 // launch costs about 3 us, as do four rows in turn.
 int forward_grid(int T, int E) {
-  const int g = grid_of(T, E);
+  const int g = grid_of(T, E, kFwdThreads, kSms);
   return g <= 4 ? 1 : g;
 }
 
@@ -427,8 +468,8 @@ bool bad(const void* q, uintptr_t mask) { return (reinterpret_cast<uintptr_t>(q)
 extern "C" size_t situ_moe_balance_loss_workspace_size(int32_t T, int32_t num_experts_total) {
   using namespace situ;
   if (T < 0 || num_experts_total < 1 || num_experts_total > kMaxExperts) return 0;
-  const size_t grid = (size_t)forward_grid(T, num_experts_total);
-  return (grid * (2 * (size_t)num_experts_total + 1) * 4 + 15) / 16 * 16;
+  const size_t grid = (size_t)forward_grid(T, num_experts_total), pitch = (size_t)(num_experts_total + 3) / 4 * 4;
+  return (grid * (2 * pitch + 1) * 4 + 15) / 16 * 16;
 }
 
 extern "C" situ_status situ_moe_balance_loss(const situ_balance_args* a, void* workspace, size_t workspace_bytes,
@@ -461,18 +502,22 @@ extern "C" situ_status situ_moe_balance_loss(const situ_balance_args* a, void* w
   p.tokens = a->tokens;
   p.stats = reinterpret_cast<float2*>(a->row_stats);
   p.part_p = static_cast<float*>(workspace);
-  p.part_c = reinterpret_cast<int32_t*>(p.part_p + (size_t)grid * E);
-  p.part_n = p.part_c + (size_t)grid * E;
-  if (a->T == 0) return launch_pdl(balance_join_kernel, dim3(kFinalCtas), dim3(kFinalThreads), 0, st, p, 0) == cudaSuccess
-                            ? SITU_OK
-                            : SITU_ERR_CUDA;
+  p.pitch = (E + 3) / 4 * 4;
+  p.part_c = reinterpret_cast<int32_t*>(p.part_p + (size_t)grid * p.pitch);
+  p.part_n = p.part_c + (size_t)grid * p.pitch;
+  auto join = [&](int parts) {
+    return (size_t)parts * p.pitch * 8 <= 256 * 1024 && p.pitch <= 4 * kFinalThreads
+               ? launch_pdl(balance_join_kernel<1>, dim3(1), dim3(kFinalThreads), 0, st, p, parts)
+               : launch_pdl(balance_join_kernel<kFinalCtas>, dim3(kFinalCtas), dim3(kFinalThreads), 0, st, p, parts);
+  };
+  if (a->T == 0) return join(0) == cudaSuccess ? SITU_OK : SITU_ERR_CUDA;
   const bool vec = E % 4 == 0 && a->ld % 4 == 0 && !bad(a->router_logits, 15);
   cudaError_t e = with_shape(E, vec, [&](auto l, auto nv, auto v) {
-    balance_kernel<l.value, nv.value, v.value><<<grid, kThreads, (size_t)E * 8, st>>>(p);
+    balance_kernel<l.value, nv.value, v.value><<<grid, kFwdThreads, (size_t)E * 8, st>>>(p);
     return cudaGetLastError();
   });
   if (e == cudaSuccess && grid > 1)
-    e = launch_pdl(balance_join_kernel, dim3(kFinalCtas), dim3(kFinalThreads), 0, st, p, grid);
+    e = join(grid);
   return e == cudaSuccess ? SITU_OK : SITU_ERR_CUDA;
 }
 
@@ -511,9 +556,13 @@ extern "C" situ_status situ_moe_router_backward(const situ_router_backward_args*
   p.ldo = (long)a->ldo;
   const bool vec = E % 4 == 0 && a->ld % 4 == 0 && a->ldo % 4 == 0 && !bad(a->router_logits, 15) && !bad(a->dlogits, 15);
   const cudaError_t e = with_shape(E, vec, [&](auto l, auto nv, auto v) {
-    constexpr int kSmem = kThreads / l.value * 4 * l.value * nv.value * 4;   // 4 KB per piece of a lane
-    static_assert(kSmem <= 48 * 1024, "no opt-in needed");
-    router_back_kernel<l.value, nv.value, v.value><<<grid_of(p.T, E), kThreads, kSmem, (cudaStream_t)stream>>>(p);
+    constexpr int kSmem = (kBackThreads / l.value + 1) * 4 * l.value * nv.value * 4;   // a row of each group, and F
+    auto* k = router_back_kernel<l.value, nv.value, v.value>;
+    if (kSmem > 44 * 1024) {   // 48 KB with the static part
+      const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+      if (e != cudaSuccess) return e;
+    }
+    k<<<grid_of(p.T, E, kBackThreads, 3 * kSms), kBackThreads, kSmem, (cudaStream_t)stream>>>(p);
     return cudaGetLastError();
   });
   return e == cudaSuccess ? SITU_OK : SITU_ERR_CUDA;
