@@ -46,7 +46,7 @@ constexpr int kTile = 128;         // rows of a tile
 constexpr int kChunk = 64;         // contraction elements of a stage (shrink)
 constexpr int kXBytes = kTile * 128;   // a box: 128 bytes of 128 rows
 constexpr int kMaxStages = 8;      // of a ring
-constexpr int kSmemMost = 222 * 1024;
+constexpr int kShrinkSmem = 218 * 1024, kExpandSmem = 222 * 1024;   // 227 KB with the static parts
 constexpr int kMaxRank = 128;
 constexpr int kCluster = 8;        // CTAs of a row
 constexpr int kRowThreads = 256;
@@ -55,7 +55,8 @@ struct LoraParams {
   const int32_t *ids, *offsets;
   int S, C, r, n;                  // C: the other extent (contraction or columns)
   int r16;                         // r rounded up to 16
-  int tiles, chunks;               // of rows; of the contraction
+  int tiles, shrink_tiles, chunks; // of rows, expand's and shrink's; of the contraction
+  int run;                         // shrink: chunks of a sum in tensor memory
   long shrink_ctas;
   float* part;                     // [parts of a tile][S][r]
   const float* scale;              // [n] or null
@@ -64,9 +65,9 @@ struct LoraParams {
   void* out;
   long ldo;
   void* u16;                       // [S, r] scaled, of the operands' type, or null
-  int stages, w_stage;             // shared memory: stages of w (shrink: and of x), bytes of one
-  int tmem_cols;                   // shrink: of a CTA
-  int y_stages, u_bytes;           // expand: items of base in shared memory, bytes of u
+  int stages, w_stage;             // shared memory: stages of w, bytes of one
+  int x_stages;                    // shrink: of x
+  int y_stages, u_bytes;           // expand: items of base, bytes of u
   int* err;
 };
 
@@ -226,36 +227,46 @@ lora_row_kernel(RowParams p) {
 // tiles of 128 rows
 // --------------------------------------------------------------------------
 
-// A tile's adapters: each row's (-1: none), and the distinct ones in the order
-// of their first rows.
+// The adapters of a tile of R rows: each row's (-1: none), and the distinct ones
+// in the order of their first rows.
+template <int R>
 struct Adapters {
-  alignas(16) int of[kTile];   // row -> adapter
-  int at[kTile];               // row -> its place in `list`, or -1
-  int list[kTile];
-  uint32_t lead[kTile / 32], same[kTile / 32];
+  alignas(16) int of[R];   // row -> adapter
+  int at[R];               // row -> its place in `list`, or -1
+  int list[R];
+  int halves[R];           // of each in `list`: whether rows of the first 128 take it (1), and of the others (2)
+  uint32_t lead[R / 32], same[R / 32];
   int count;
 };
-__device__ __forceinline__ void epi_sync(int threads) { asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory"); }
-// by the `threads` (kTile or more) epilogue threads, of which this is number i
-__device__ __forceinline__ void find_adapters(Adapters& t, const LoraParams& p, int row0, int i, int threads) {
-  const bool mine = i < kTile;
+constexpr int kEpi = 256;   // epilogue threads of either kernel
+__device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+// by the epilogue threads, of which this is number i
+template <int R>
+__device__ __forceinline__ void find_adapters(Adapters<R>& t, const LoraParams& p, int row0, int i) {
+  static_assert(R <= kEpi, "a thread per row");
+  const bool mine = i < R;
   int e = -1;
   if (mine) {
     if (row0 + i < p.S) e = adapter_of(p.ids, p.offsets, p.n, row0 + i);
     t.of[i] = e;
+    t.halves[i] = 0;
   }
-  epi_sync(threads);
+  epi_sync();
   const int e0 = t.of[0];
   const bool same = __all_sync(0xffffffffu, !mine || e == e0 || row0 + i >= p.S);
   if (mine && (i & 31) == 0) t.same[i >> 5] = same;
-  epi_sync(threads);
-  if (t.same[0] & t.same[1] & t.same[2] & t.same[3]) {
+  epi_sync();
+  uint32_t all = 1;
+#pragma unroll
+  for (int w = 0; w < R / 32; ++w) all &= t.same[w];
+  if (all) {
     if (mine) t.at[i] = e >= 0 ? 0 : -1;
     if (i == 0) {
       t.list[0] = e0;
+      t.halves[0] = p.S - row0 > 128 ? 3 : 1;
       t.count = e0 >= 0 ? 1 : 0;
     }
-    epi_sync(threads);
+    epi_sync();
     return;
   }
   int first = i;       // the first row of this one's adapter
@@ -273,15 +284,21 @@ __device__ __forceinline__ void find_adapters(Adapters& t, const LoraParams& p, 
   __syncwarp();
   const uint32_t lead = __ballot_sync(0xffffffffu, mine && e >= 0 && first == i);
   if (mine && (i & 31) == 0) t.lead[i >> 5] = lead;
-  epi_sync(threads);
+  epi_sync();
   if (mine) {
     int place = __popc(t.lead[first >> 5] & ((1u << (first & 31)) - 1u));
     for (int w = 0; w < first >> 5; ++w) place += __popc(t.lead[w]);
     t.at[i] = e >= 0 ? place : -1;
     if (e >= 0 && first == i) t.list[place] = e;
-    if (i == 0) t.count = __popc(t.lead[0]) + __popc(t.lead[1]) + __popc(t.lead[2]) + __popc(t.lead[3]);
+    if (e >= 0) atomicOr(&t.halves[place], 1 << (i >> 7));
+    if (i == 0) {
+      int n = 0;
+#pragma unroll
+      for (int w = 0; w < R / 32; ++w) n += __popc(t.lead[w]);
+      t.count = n;
+    }
   }
-  epi_sync(threads);
+  epi_sync();
 }
 
 // A ring whose length the launch chooses.
@@ -307,10 +324,9 @@ struct Turns {
 };
 
 constexpr int kTmemCols = 512;                // of an SM
-constexpr int kShrinkThreads = 192;           // copies, MMAs; four epilogue warps
-constexpr int kShrinkEpi = 128;
-constexpr int kExpandThreads = 384;           // copies of base and out, MMAs, copies of weights; eight epilogue warps
-constexpr int kExpandEpi = 256;
+constexpr int kShrinkRows = 256;              // of a tile of the shrink: two MMAs share an adapter's weights
+constexpr int kShrinkThreads = 64 + kEpi;     // copies, MMAs; eight epilogue warps
+constexpr int kExpandThreads = 128 + kEpi;    // copies of base and out, MMAs, copies of weights; eight epilogue warps
 
 // D[128, N] of 16-bit operands in fp32; trans_b: B's N elements contiguous
 __device__ __forceinline__ uint32_t idesc_of(bool bf16, bool trans_b, int N) {
@@ -356,17 +372,41 @@ __device__ __forceinline__ void store_wait_read() {
   asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
 
+// eight sums to memory, a whole sector a lane; add: to what is there
+__device__ __forceinline__ void put8(float* o, const uint32_t* v, bool add) {
+  float f[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[i]);
+  if (add) {
+    const float4 a = *reinterpret_cast<const float4*>(o), b = *reinterpret_cast<const float4*>(o + 4);
+    f[0] += a.x;
+    f[1] += a.y;
+    f[2] += a.z;
+    f[3] += a.w;
+    f[4] += b.x;
+    f[5] += b.y;
+    f[6] += b.z;
+    f[7] += b.w;
+  }
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(o), "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]),
+               "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7])
+               : "memory");
+}
+
 // part[.][i][j] = sum over a range of k of x[i, k] W[e(i)][j][k] (TRANS:
-// W[e][k][j]): the tile's rows on the MMA's M side, an adapter's r on its N
-// side, in TMEM columns of its own.  As many adapters as half of the columns
-// hold share a pass over x; the other half takes the next pass meanwhile.  The
-// chunks of all tiles are dealt out evenly over the CTAs; what a CTA
-// has of a tile is that tile's next part.
+// W[e][k][j]): the tile's rows on the MMA's M side (two MMAs of 128: with one the
+// weights were a third of what the SMs take in, 16,384 rows at rank 64 W128 us,
+// W256 so), an adapter's r on its N side, in TMEM columns of its own.  As many
+// adapters as half of the columns hold share a pass over x; the other half takes
+// the next sums meanwhile.  The chunks of all tiles are dealt out evenly over the
+// CTAs, one per SM; what a CTA has of a tile is that tile's next part.  For fp32
+// results p.run chunks (1,024 elements) make a sum: the tensor cores truncate when
+// they add, 6e-9 of a sum of one sign per element; the sums meet in fp32.
 template <int DT, bool TRANS>
-__global__ void __launch_bounds__(kShrinkThreads, 2)
+__global__ void __launch_bounds__(kShrinkThreads, 1)
 shrink_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w, const LoraParams p) {
   extern __shared__ uint8_t smem_raw[];
-  __shared__ Adapters lists[2];
+  __shared__ Adapters<kShrinkRows> lists[2];
   __shared__ uint64_t bars[4 * kMaxStages + 9];
   __shared__ uint32_t holder[2];
   const uint32_t sbase = (saddr(smem_raw) + 1023) & ~1023u;
@@ -382,45 +422,48 @@ shrink_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
   auto list_full = [&](int b) { return tail + 32 + 8 * b; };
   auto list_empty = [&](int b) { return tail + 48 + 8 * b; };
   const uint32_t drain = tail + 64;
-  const long total = (long)p.tiles * p.chunks, G = gridDim.x;
+  const long total = (long)p.shrink_tiles * p.chunks, G = gridDim.x;
   const long i0 = first_item(blockIdx.x, total, G), i1 = first_item(blockIdx.x + 1, total, G);
   if (tid == 0) {
-    for (long i = i0; i < i1 && i < i0 + p.stages; ++i)   // x does not wait for the adapters' list
-      prefetch_2d(&map_x, (int)(i % p.chunks) * kChunk, (int)(i / p.chunks) * kTile);
+    for (long i = i0; i < i1 && i < i0 + p.x_stages; ++i)   // x does not wait for the adapters' list
+      for (int h = 0; h < kShrinkRows; h += kTile)
+        if ((i / p.chunks) * kShrinkRows + h < p.S)
+          prefetch_2d(&map_x, (int)(i % p.chunks) * kChunk, (int)(i / p.chunks) * kShrinkRows + h);
     holder[1] = (uint32_t)*reinterpret_cast<volatile int*>(p.err);   // an earlier launch gave up a wait: no work then
     prefetch_map(&map_w);
     for (int s = 0; s < 4 * kMaxStages; ++s) mbar_init(bar0 + 8 * s, 1);
     for (int b = 0; b < 2; ++b) {
       mbar_init(acc_full(b), 1);
-      mbar_init(acc_empty(b), 4);
+      mbar_init(acc_empty(b), kEpi / 32);
       mbar_init(list_full(b), 1);
       mbar_init(list_empty(b), 2);
     }
     mbar_init(drain, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 1) tmem_alloc<1>(saddr(holder), (uint32_t)p.tmem_cols);
+  if (warp == 1) tmem_alloc<1>(saddr(holder), kTmemCols);
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = holder[0];
   const bool dead = holder[1] != 0;
-  const int half = p.tmem_cols / 2, per = half / p.r16;                // adapters of a pass
-  const uint32_t wbase = sbase + p.stages * kXBytes;
+  constexpr int kSumCols = kTmemCols / 2, kHalfCols = kSumCols / 2;   // of a sum's columns, those of 128 rows
+  const int per = kHalfCols / p.r16;                    // adapters of a pass
+  const uint32_t wbase = sbase + p.x_stages * 2 * kXBytes;
 
   if (warp == 0 && !dead) {
     // ---------------- copies ----------------
     const bool leader = elect_one();
     const int wboxes = (p.r + 63) / 64;
-    Turns x(p.stages), w(p.stages), l(2);
+    Turns x(p.x_stages), w(p.stages), l(2);
     bool ok = true;
     for (Segment g(i0, i1, p.chunks); g.more() && ok; g.next()) {
       if (!warp_wait(list_full(l.s), l.ph, p.err, 81)) {
         ok = false;
         break;
       }
-      const Adapters& ad = lists[l.s];
-      const int nd = ad.count, row0 = g.tile * kTile;
+      const Adapters<kShrinkRows>& ad = lists[l.s];
+      const int nd = ad.count, row0 = g.tile * kShrinkRows, halves = p.S - row0 > kTile ? 2 : 1;
       for (int d0 = 0; d0 < nd && ok; d0 += per) {
         const int d1 = min(nd, d0 + per);
         for (int k = g.from; k < g.to && ok; ++k) {
@@ -429,8 +472,9 @@ shrink_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
             break;
           }
           if (leader) {
-            mbar_expect_tx(xfull(x.s), kXBytes);
-            copy_2d<1>(sbase + x.s * kXBytes, &map_x, k * kChunk, row0, xfull(x.s));
+            mbar_expect_tx(xfull(x.s), halves * kXBytes);
+            for (int h = 0; h < halves; ++h)
+              copy_2d<1>(sbase + (2 * x.s + h) * kXBytes, &map_x, k * kChunk, row0 + h * kTile, xfull(x.s));
           }
           __syncwarp();
           x.next();
@@ -468,54 +512,63 @@ shrink_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     // ---------------- MMAs ----------------
     const bool leader = elect_one();
     const uint32_t idesc = idesc_of(DT == SITU_DT_BF16, TRANS, p.r16);
-    Turns x(p.stages), w(p.stages), l(2), acc(2);
+    Turns x(p.x_stages), w(p.stages), l(2), acc(2);
     bool ok = true;
     for (Segment g(i0, i1, p.chunks); g.more() && ok; g.next()) {
       if (!warp_wait(list_full(l.s), l.ph, p.err, 86)) {
         ok = false;
         break;
       }
-      const int nd = lists[l.s].count;
-      __syncwarp();
-      mbar_arrive_if(list_empty(l.s), lane == 0);
-      l.next();
+      const Adapters<kShrinkRows>& ad = lists[l.s];
+      const int nd = ad.count;
       for (int d0 = 0; d0 < nd && ok; d0 += per) {
         const int d1 = min(nd, d0 + per);
-        if (acc.again() && !warp_wait(acc_empty(acc.s), acc.ph ^ 1, p.err, 87)) {
-          ok = false;
-          break;
-        }
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        for (int k = g.from; k < g.to && ok; ++k, x.next()) {
-          if (!warp_wait(xfull(x.s), x.ph, p.err, 88)) {
+        for (int from = g.from; from < g.to && ok; from += p.run) {
+          const int to = min(g.to, from + p.run);
+          if (acc.again() && !warp_wait(acc_empty(acc.s), acc.ph ^ 1, p.err, 87)) {
             ok = false;
             break;
           }
-          const int steps = min(kChunk / 16, (p.C - k * kChunk + 15) >> 4);
-          for (int d = d0; d < d1; ++d, w.next()) {
-            if (!warp_wait(wfull(w.s), w.ph, p.err, 89)) {
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          for (int k = from; k < to && ok; ++k, x.next()) {
+            if (!warp_wait(xfull(x.s), x.ph, p.err, 88)) {
               ok = false;
               break;
             }
-            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            if (leader) {
-              const uint32_t wa = wbase + w.s * p.w_stage;
-              const uint64_t xd = sdesc(sbase + x.s * kXBytes), wd = TRANS ? sdesc_mn(wa, 8192) : sdesc(wa);
-              for (int j = 0; j < steps; ++j)
-                mma_f16<1>(tmem + acc.s * half + (d - d0) * p.r16, xd + 2 * j, wd + (TRANS ? 128 : 2) * j, idesc,
-                           ((k - g.from) | j) != 0);
-              mma_commit(wempty(w.s));
-              if (d + 1 == d1) mma_commit(xempty(x.s));
+            const int steps = min(kChunk / 16, (p.C - k * kChunk + 15) >> 4);
+            for (int d = d0; d < d1; ++d, w.next()) {
+              if (!warp_wait(wfull(w.s), w.ph, p.err, 89)) {
+                ok = false;
+                break;
+              }
+              asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+              if (leader) {
+                const uint32_t wa = wbase + w.s * p.w_stage;
+                const uint64_t wd = TRANS ? sdesc_mn(wa, 8192) : sdesc(wa);
+                const int halves = ad.halves[d];       // the other rows' sums are not read
+                for (int h = 0; h < 2; ++h) {
+                  if (!(halves >> h & 1)) continue;
+                  const uint64_t xd = sdesc(sbase + (2 * x.s + h) * kXBytes);
+                  for (int j = 0; j < steps; ++j)
+                    mma_f16<1>(tmem + acc.s * kSumCols + h * kHalfCols + (d - d0) * p.r16, xd + 2 * j, wd + (TRANS ? 128 : 2) * j,
+                               idesc, ((k - from) | j) != 0);
+                }
+                mma_commit(wempty(w.s));
+                if (d + 1 == d1) mma_commit(xempty(x.s));
+              }
+              __syncwarp();
             }
+          }
+          if (ok) {
+            if (leader) mma_commit(acc_full(acc.s));
             __syncwarp();
+            acc.next();
           }
         }
-        if (ok) {
-          if (leader) mma_commit(acc_full(acc.s));
-          __syncwarp();
-          acc.next();
-        }
       }
+      __syncwarp();
+      mbar_arrive_if(list_empty(l.s), lane == 0);
+      l.next();
     }
     leave(
         ok, [&] { return w.last([&](int j, uint32_t ph) { return warp_wait(wempty(j), ph, p.err, 90); }); },
@@ -526,12 +579,12 @@ shrink_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
         });
   } else if (warp >= 2 && !dead) {
     // ---------------- lists, and sums to memory, a row per lane ----------------
-    const int et = tid - 64, q = warp & 3;
+    const int et = tid - 64, q = warp & 3, h = (warp - 2) >> 2, mine = h * kTile + 32 * q + lane;
     Turns l(2), acc(2);
     bool ok = true;
     auto list = [&](const Segment& g) {                 // of a tile, while the one before is worked on
       if (l.again() && !warp_wait(list_empty(l.s), l.ph ^ 1, p.err, 91)) ok = false;
-      find_adapters(lists[l.s], p, g.tile * kTile, et, kShrinkEpi);
+      find_adapters(lists[l.s], p, g.tile * kShrinkRows, et);
       mbar_arrive_if(list_full(l.s), et == 0);
       l.next();
     };
@@ -541,33 +594,36 @@ shrink_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
       Segment n = g;
       n.next();
       if (n.more()) list(n);
-      const Adapters& ad = lists[b];
-      const int nd = ad.count, at = ad.at[32 * q + lane], row = g.tile * kTile + 32 * q + lane;
+      const Adapters<kShrinkRows>& ad = lists[b];
+      const int nd = ad.count, at = ad.at[mine], row = g.tile * kShrinkRows + mine;
       const int part = (int)((long)blockIdx.x - cta_of((long)g.tile * p.chunks, total, G));
       float* out = p.part + ((size_t)part * p.S + row) * p.r;
-      for (int d0 = 0; d0 < nd && ok; d0 += per, acc.next()) {
+      for (int d0 = 0; d0 < nd && ok; d0 += per) {
         const int d1 = min(nd, d0 + per);
-        if (!warp_wait(acc_full(acc.s), acc.ph, p.err, 92)) {
-          ok = false;
-          break;
-        }
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        for (int d = d0; d < d1; ++d) {
-          if (!__any_sync(0xffffffffu, at == d)) continue;
-          for (int j = 0; j < p.r16; j += 16) {
-            uint32_t v[16];
-            tmem_ld16_nowait(tmem + ((uint32_t)(32 * q) << 16) + acc.s * half + (d - d0) * p.r16 + j, v);
-            tmem_ld_wait<16>(v);
-            if (at == d) {
+        for (int from = g.from; from < g.to && ok; from += p.run, acc.next()) {
+          if (!warp_wait(acc_full(acc.s), acc.ph, p.err, 92)) {
+            ok = false;
+            break;
+          }
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          for (int d = d0; d < d1; ++d) {
+            if (!__any_sync(0xffffffffu, at == d)) continue;
+            for (int j = 0; j < p.r16; j += 16) {
+              uint32_t v[16];
+              __syncwarp();
+              tmem_ld16_nowait(tmem + ((uint32_t)(32 * q) << 16) + acc.s * kSumCols + h * kHalfCols + (d - d0) * p.r16 + j, v);
+              tmem_ld_wait<16>(v);
+              if (at == d) {
 #pragma unroll
-              for (int t = 0; t < 16; t += 4)
-                if (j + t < p.r)
-                  *reinterpret_cast<uint4*>(out + j + t) = make_uint4(v[t], v[t + 1], v[t + 2], v[t + 3]);
+                for (int t = 0; t < 16; t += 8)
+                  if (j + t < p.r) put8(out + j + t, v + t, from > g.from);
+              }
+              __syncwarp();
             }
           }
+          asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+          mbar_arrive_if(acc_empty(acc.s), lane == 0);
         }
-        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-        mbar_arrive_if(acc_empty(acc.s), lane == 0);
       }
       g = n;
     }
@@ -578,7 +634,7 @@ shrink_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
   if (warp == 1) {
     __syncwarp();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-    tmem_free<1>(tmem, (uint32_t)p.tmem_cols);
+    tmem_free<1>(tmem, kTmemCols);
   }
 }
 
@@ -599,7 +655,7 @@ expand_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
               const __grid_constant__ CUtensorMap map_out, const LoraParams p) {
   constexpr int kTerms = terms_of(DT, F32), kCols = cols_of(F32), kBoxCols = kCols / 2;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ Adapters lists[2];
+  __shared__ Adapters<kTile> lists[2];
   __shared__ float back[kTile];      // f16: the power of two that a row's u was divided by
   __shared__ uint64_t bars[4 * kMaxStages + 10];
   __shared__ uint32_t holder[2];
@@ -625,15 +681,15 @@ expand_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
       mbar_init(wfull(s), 1);
       mbar_init(wempty(s), 1);
       mbar_init(yfull(s), 1);
-      mbar_init(ydone(s), kExpandEpi / 32);
+      mbar_init(ydone(s), kEpi / 32);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(acc_full(b), 1);
-      mbar_init(acc_empty(b), kExpandEpi / 32);
+      mbar_init(acc_empty(b), kEpi / 32);
       mbar_init(list_full(b), 1);
       mbar_init(list_empty(b), 2);
     }
-    mbar_init(u_full, kExpandEpi / 32);
+    mbar_init(u_full, kEpi / 32);
     mbar_init(drain, 1);
     holder[1] = (uint32_t)*reinterpret_cast<volatile int*>(p.err);   // an earlier call gave up a wait: no work then
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -746,7 +802,7 @@ expand_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
         ok = false;
         break;
       }
-      const Adapters& ad = lists[l.s];
+      const Adapters<kTile>& ad = lists[l.s];
       const int nd = ad.count;
       for (int b = g.from; b < g.to && ok; ++b)
         for (int d = 0; d < nd; ++d, w.next()) {
@@ -784,16 +840,16 @@ expand_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
     bool ok = true;
     auto list = [&](const Segment& g) {                 // of a tile, while the one before is worked on
       if (l.again() && !warp_wait(list_empty(l.s), l.ph ^ 1, p.err, 110)) ok = false;
-      find_adapters(lists[l.s], p, g.tile * kTile, et, kExpandEpi);
+      find_adapters(lists[l.s], p, g.tile * kTile, et);
       mbar_arrive_if(list_full(l.s), et == 0);
       l.next();
     };
     // u of a tile: two threads to a row, eight elements of each sixteen each
-    auto stage_u = [&](const Segment& g, const Adapters& ad) {
+    auto stage_u = [&](const Segment& g, const Adapters<kTile>& ad) {
       const int r = et >> 1, row = g.tile * kTile + r, e = ad.of[r];
       const float f = e >= 0 && p.scale ? __ldg(p.scale + e) : 1.f;
       const bool write = p.u16 && g.from == 0 && row < p.S;
-      const long t0 = (long)g.tile * p.chunks, all = (long)p.tiles * p.chunks;
+      const long t0 = (long)(g.tile / (kShrinkRows / kTile)) * p.chunks, all = (long)p.shrink_tiles * p.chunks;
       const int parts = (int)(cta_of(t0 + p.chunks - 1, all, p.shrink_ctas) - cta_of(t0, all, p.shrink_ctas)) + 1;
       auto sum8 = [&](int j, float (&u)[8]) {
 #pragma unroll
@@ -854,7 +910,7 @@ expand_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
         }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      epi_sync(kExpandEpi);                             // back[] and, before the arrivals, every lane's u
+      epi_sync();                             // back[] and, before the arrivals, every lane's u
       mbar_arrive_if(u_full, lane == 0);
     };
     Segment g(i0, i1, blocks);
@@ -867,7 +923,7 @@ expand_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
       Segment n = g;
       n.next();
       if (n.more()) list(n);
-      const Adapters& ad = lists[lb];
+      const Adapters<kTile>& ad = lists[lb];
       const int nd = ad.count, at = ad.at[32 * q + lane];
       const float my_back = DT == SITU_DT_F16 ? back[32 * q + lane] : 1.f;
       for (int b = g.from; b < g.to && ok; ++b, y.next()) {
@@ -934,7 +990,7 @@ expand_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
       }
       g = n;
       if (g.more()) {
-        epi_sync(kExpandEpi);                           // every warp is done with back[], and the MMAs with u
+        epi_sync();                           // every warp is done with back[], and the MMAs with u
         stage_u(g, lists[lb ^ 1]);
       }
     }
@@ -952,21 +1008,16 @@ expand_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
 // launches
 // --------------------------------------------------------------------------
 
-// CTAs of the shrink: one per SM, of at least two chunks.  For fp32 results a
-// CTA takes 1,024 elements at most: the tensor cores truncate when they add (6e-9
-// of a sum of one sign per element), a tile's parts meet in fp32.  Then they come
-// in whole rounds of two per SM.
-long shrink_ctas(int S, int C, bool f32) {
-  const long tiles = (S + kTile - 1) / kTile, chunks = (C + kChunk - 1) / kChunk, total = tiles * chunks;
-  const long sms = sm_count(), most = total / 2, least = f32 ? (total + 15) / 16 : 1;
-  long g = least <= sms ? sms : (least + 2 * sms - 1) / (2 * sms) * 2 * sms;
-  if (g > most) g = most > least ? most : least;
+// CTAs of the shrink: one per SM, of at least two chunks.
+long shrink_ctas(int S, int C) {
+  const long tiles = (S + kShrinkRows - 1) / kShrinkRows, total = tiles * ((C + kChunk - 1) / kChunk), sms = sm_count();
+  const long g = total / 2 < sms ? total / 2 : sms;
   return g < 1 ? 1 : g;
 }
 // the most parts that a tile's chunks can come in
-long most_parts(int S, int C, bool f32) {
-  const long tiles = (S + kTile - 1) / kTile, chunks = (C + kChunk - 1) / kChunk, G = shrink_ctas(S, C, f32);
-  const long least = tiles * chunks / G, most = (chunks + least - 2) / least + 1;
+long most_parts(int S, int C) {
+  const long tiles = (S + kShrinkRows - 1) / kShrinkRows, chunks = (C + kChunk - 1) / kChunk;
+  const long least = tiles * chunks / shrink_ctas(S, C), most = (chunks + least - 2) / least + 1;
   return most < chunks ? most : chunks;
 }
 
@@ -985,17 +1036,18 @@ cudaError_t launch_pair(const Maps& m, LoraParams s, LoraParams x, cudaStream_t 
   const uint64_t bit = dev < 64 ? 1ull << dev : 0;
   if (bit == 0 || !(raised.load() & bit)) {
     std::lock_guard<std::mutex> lock(attr_mutex());
-    e = cudaFuncSetAttribute(shrink, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(expand, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost);
+    e = cudaFuncSetAttribute(shrink, cudaFuncAttributeMaxDynamicSharedMemorySize, kShrinkSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(expand, cudaFuncAttributeMaxDynamicSharedMemorySize, kExpandSmem);
     if (e != cudaSuccess) return e;
     raised.fetch_or(bit);
   }
-  const long sms = sm_count();
-  const int at_once = s.shrink_ctas > sms ? 2 : 1;      // shrink CTAs per SM
-  s.tmem_cols = kTmemCols / at_once;
-  s.stages = (kSmemMost / at_once - 1024 - 4096 * (at_once - 1)) / (kXBytes + s.w_stage);
+  // five stages of x and seven of weights at ranks up to 64, else four and five:
+  // a tile of several adapters takes more of the latter
+  s.x_stages = s.w_stage <= 8192 ? 5 : 4;
+  s.stages = (kShrinkSmem - 1024 - s.x_stages * 2 * kXBytes) / s.w_stage;
   if (s.stages > kMaxStages) s.stages = kMaxStages;
-  shrink<<<(unsigned)s.shrink_ctas, kShrinkThreads, 1024 + s.stages * (kXBytes + s.w_stage), st>>>(m.x, m.w, s);
+  const long sms = sm_count();
+  shrink<<<(unsigned)s.shrink_ctas, kShrinkThreads, 1024 + s.x_stages * 2 * kXBytes + s.stages * s.w_stage, st>>>(m.x, m.w, s);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   x.u_bytes = (terms_of(DT, F32) * x.r16 + 63) / 64 * kXBytes;
@@ -1004,7 +1056,7 @@ cudaError_t launch_pair(const Maps& m, LoraParams s, LoraParams x, cudaStream_t 
   int rest;
   for (x.stages = 4;; --x.stages) {
     rest = 1024 + x.u_bytes + x.stages * x.w_stage;
-    x.y_stages = (kSmemMost - rest) / (2 * kXBytes);
+    x.y_stages = (kExpandSmem - rest) / (2 * kXBytes);
     if (x.y_stages > 4) x.y_stages = 4;
     if (x.y_stages >= 3 || x.stages == 2) break;
   }
@@ -1022,7 +1074,9 @@ situ_status launch_tiles(int dtype, bool f32, const void* rows, int64_t ld_rows,
   s.r16 = x.r16 = (s.r + 15) / 16 * 16;
   s.chunks = (s.C + kChunk - 1) / kChunk;
   s.tiles = x.tiles = (s.S + kTile - 1) / kTile;
-  s.shrink_ctas = x.shrink_ctas = shrink_ctas(s.S, s.C, f32);
+  s.shrink_tiles = x.shrink_tiles = (s.S + kShrinkRows - 1) / kShrinkRows;
+  s.shrink_ctas = x.shrink_ctas = shrink_ctas(s.S, s.C);
+  s.run = f32 ? 1024 / kChunk : s.chunks;
   x.chunks = s.chunks;
   const int boxes = (s.r + 63) / 64;
   s.w_stage = boxes * 8192;
@@ -1062,12 +1116,7 @@ situ_status launch_tiles(int dtype, bool f32, const void* rows, int64_t ld_rows,
 // A cluster per row, or tiles.
 bool by_rows(int S) { return S <= 64; }
 
-// for either type of result
-size_t part_bytes(int S, int C, int r) {
-  if (S == 0) return 0;
-  const long a = most_parts(S, C, false), b = most_parts(S, C, true);
-  return (size_t)(a > b ? a : b) * S * r * 4;
-}
+size_t part_bytes(int S, int C, int r) { return S == 0 ? 0 : (size_t)most_parts(S, C) * S * r * 4; }
 
 bool bad(const void* q, uintptr_t mask) { return (reinterpret_cast<uintptr_t>(q) & mask) != 0; }
 // the tensor maps take strides below 2^40 bytes
@@ -1129,7 +1178,7 @@ extern "C" situ_status situ_moe_lora(const situ_lora_args* a, void* workspace, s
     return cudaGetLastError() == cudaSuccess ? SITU_OK : SITU_ERR_CUDA;
   }
   if (!workspace || !a->device_status) return SITU_ERR_NULL_ARG;
-  if (bad(workspace, 15) || bad(a->device_status, 3)) return SITU_ERR_MISALIGNED;
+  if (bad(workspace, 31) || bad(a->device_status, 3)) return SITU_ERR_MISALIGNED;
   if (workspace_bytes < part_bytes(a->S, a->K, a->r)) return SITU_ERR_WORKSPACE_TOO_SMALL;
   LoraParams s = {};
   s.ids = a->ids;
@@ -1169,9 +1218,10 @@ extern "C" situ_status situ_moe_lora_backward(const situ_lora_backward_args* a, 
     return SITU_ERR_BAD_SHAPE;
   if (!a->da || !a->db || !a->offsets || !a->device_status || !workspace) return SITU_ERR_NULL_ARG;
   if (a->S > 0 && (!a->dy || !a->x || !a->a || !a->b || !a->u || !a->dx)) return SITU_ERR_NULL_ARG;
-  const void* ptrs[] = {a->dy, a->x, a->a, a->b, a->u, a->dx0, a->dx, a->da, a->db, workspace};
+  const void* ptrs[] = {a->dy, a->x, a->a, a->b, a->u, a->dx0, a->dx, a->da, a->db};
   for (const void* q : ptrs)
     if (bad(q, 15)) return SITU_ERR_MISALIGNED;
+  if (bad(workspace, 31)) return SITU_ERR_MISALIGNED;
   if (bad(a->offsets, 3) || bad(a->scale, 3) || bad(a->device_status, 3)) return SITU_ERR_MISALIGNED;
   if (workspace_bytes < situ_moe_lora_backward_workspace_size(a->S, a->K, a->N, a->r)) return SITU_ERR_WORKSPACE_TOO_SMALL;
   uint8_t* v = static_cast<uint8_t*>(workspace) + part_bytes(a->S, a->N, a->r);
