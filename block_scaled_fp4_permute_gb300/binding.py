@@ -8,6 +8,7 @@ the call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 from typing import Optional
@@ -797,6 +798,35 @@ def situ_moe_fp8_grouped_gemm(x_q: torch.Tensor, x_scale: torch.Tensor, w_q: tor
 # device (the products' status word).
 # ---------------------------------------------------------------------------
 
+# workspace sizes of shapes already seen: a call into the library less
+@functools.lru_cache(maxsize=4096)
+def _balance_bytes(T, E, index):
+    return _size("situ_moe_balance_loss_workspace_size", index, T, E)
+
+
+@functools.lru_cache(maxsize=4096)
+def _lora_bytes(S, K, N, r, index):
+    return _size("situ_moe_lora_workspace_size", index, S, K, N, r)
+
+
+@functools.lru_cache(maxsize=4096)
+def _lora_backward_bytes(S, K, N, r, index):
+    return _size("situ_moe_lora_backward_workspace_size", index, S, K, N, r)
+
+
+def _size(name, index, *args) -> int:
+    with torch.cuda.device(index):
+        return getattr(_lib or lib(), name)(*args)
+
+
+def _scratch(n: int, index: int):
+    """(tensor or None, pointer or None) of n bytes; the caller keeps the tensor until the call is enqueued."""
+    if n == 0:
+        return None, None
+    t = _empty((n,), (1,), torch.uint8, index)
+    return t, t.data_ptr()
+
+
 def _on_device(index: int, **tensors) -> None:
     for name, t in tensors.items():
         if t is not None and t.get_device() != index:
@@ -839,9 +869,7 @@ def _router(router_logits, topk_ids, mask):
     if (T | E | k) >> 31:
         raise _too_large(T, E, k)
     if mask is not None:
-        if mask.dtype is torch.bool:
-            mask = mask.view(torch.uint8)
-        mask = _vector(mask, torch.uint8, T, "mask", index)
+        mask = _vector(mask, torch.uint8 if mask.dtype is torch.uint8 else torch.bool, T, "mask", index)
     logits, ld = _logits(router_logits)
     return logits, ld, topk_ids if topk_ids.is_contiguous() else topk_ids.contiguous(), mask, index, T, E, k
 
@@ -858,11 +886,11 @@ def situ_moe_balance_loss(router_logits: torch.Tensor, topk_ids: torch.Tensor, *
     logits, ld, ids, mask, index, T, E, k = _router(router_logits, topk_ids, mask)
     loss, counts = _empty((), (), torch.float32, index), _empty((E,), (1,), torch.int32, index)
     tokens, stats = _empty((1,), (1,), torch.int32, index), _empty((T, 2), (2, 1), torch.float32, index)
-    n = max(16, (_lib or lib()).situ_moe_balance_loss_workspace_size(T, E))
-    ws = _empty((n,), (1,), torch.uint8, index)
+    n = _balance_bytes(T, E, index)
+    ws, pws = _scratch(n, index)
     args = SituBalanceArgs(logits.data_ptr(), ld, ids.data_ptr(), None if mask is None else mask.data_ptr(), T, E, k, coef,
                            loss.data_ptr(), counts.data_ptr(), tokens.data_ptr(), stats.data_ptr())
-    _enqueue("situ_moe_balance_loss", index, ctypes.byref(args), ws.data_ptr(), n)
+    _enqueue("situ_moe_balance_loss", index, ctypes.byref(args), pws, n)
     return loss, counts, tokens, stats
 
 
@@ -878,22 +906,25 @@ def situ_moe_router_backward(router_logits: torch.Tensor, topk_ids: torch.Tensor
                           dloss=dloss, coef=coef, mask=mask, topk_weights=topk_weights, dweights=dweights,
                           renormalize=renormalize, out=out)
     logits, ld, ids, mask, index, T, E, k = _router(router_logits, topk_ids, mask)
-    if row_stats.shape != (T, 2) or row_stats.dtype is not torch.float32 or not row_stats.is_contiguous():
-        raise ValueError(f"row_stats must be contiguous fp32 [{T}, 2]")
-    _on_device(index, row_stats=row_stats)
+    if (row_stats.shape != (T, 2) or row_stats.dtype is not torch.float32 or not row_stats.is_contiguous()
+            or row_stats.get_device() != index):
+        raise ValueError(f"row_stats must be contiguous fp32 [{T}, 2] on cuda:{index}")
     pl = pc = pt = pw = pd = None
     if dloss is not None:
         counts, tokens = _vector(counts, torch.int32, E, "counts", index), _vector(tokens, torch.int32, 1, "tokens", index)
-        dloss = _vector(dloss.reshape(1), torch.float32, 1, "dloss", index)
+        if dloss.dtype is not torch.float32 or dloss.numel() != 1 or dloss.get_device() != index:
+            raise ValueError(f"dloss must be one fp32 on cuda:{index}")
         pl, pc, pt = dloss.data_ptr(), counts.data_ptr(), tokens.data_ptr()
     if dweights is not None:
         if topk_weights is None:
             raise ValueError("dweights needs the topk_weights")
         for name, t in (("topk_weights", topk_weights), ("dweights", dweights)):
-            if t.dtype is not torch.float32 or t.shape != (T, k):
-                raise ValueError(f"{name} must be fp32 [{T}, {k}]")
-        _on_device(index, topk_weights=topk_weights, dweights=dweights)
-        topk_weights, dweights = topk_weights.contiguous(), dweights.contiguous()
+            if t.dtype is not torch.float32 or t.shape != (T, k) or t.get_device() != index:
+                raise ValueError(f"{name} must be fp32 [{T}, {k}] on cuda:{index}")
+        if not topk_weights.is_contiguous():
+            topk_weights = topk_weights.contiguous()
+        if not dweights.is_contiguous():
+            dweights = dweights.contiguous()
         pw, pd = topk_weights.data_ptr(), dweights.data_ptr()
     if out is None:
         out, ldo = _empty((T, E), (E, 1), torch.float32, index), E
@@ -967,7 +998,8 @@ def _kept(q, scale, S, K, blocks, index):
         raise TypeError("q must hold E4M3 codes (uint8 or float8_e4m3fn) and scale bytes")
     if q.shape != (S, K) or scale.shape != (S, blocks):
         raise ValueError(f"needs q [{S}, {K}] and scale [{S}, {blocks}]")
-    _on_device(index, q=q, scale=scale)
+    if q.get_device() != index or scale.get_device() != index:
+        raise ValueError(f"q on {q.device} and scale on {scale.device}, the operands on cuda:{index}")
     if not q.is_contiguous() or q.data_ptr() & 7:
         q = q.clone(memory_format=torch.contiguous_format)
     return q, scale if scale.is_contiguous() else scale.contiguous()
@@ -1135,9 +1167,10 @@ def _adapters(x, a, b, scale, index):
 
 def _beside(t, shape, dtypes, name, index):
     """(tensor, pointer, elements between rows) of base or dx0."""
-    if tuple(t.shape) != shape or t.dtype not in dtypes:
+    if t.shape != shape or t.dtype not in dtypes:
         raise ValueError(f"{name} must be {shape} of the operands' type or fp32, not {tuple(t.shape)} of {t.dtype}")
-    _on_device(index, **{name: t})
+    if t.get_device() != index:
+        raise ValueError(f"{name} on {t.device}, the operands on cuda:{index}")
     return _rows(t, 4 if t.dtype is torch.float32 else 8)
 
 
@@ -1175,12 +1208,12 @@ def situ_moe_lora(base, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, *, id
     else:
         ldo = _given(out, (S, N), out_dtype, index, 4 if out_dtype is torch.float32 else 8)
     u = _empty((S, r), (r, 1), dtype, index) if keep else None
-    size = (_lib or lib()).situ_moe_lora_workspace_size(S, K, N, r)
-    ws = _empty((max(16, size),), (1,), torch.uint8, index)
+    size = _lora_bytes(S, K, N, r, index)
+    ws, pws = _scratch(size, index)
     args = SituLoraArgs(_DTYPES[dtype], _DTYPES.get(out_dtype, -1), S, K, N, r, n, px, ldx, a.data_ptr(), b.data_ptr(), pids,
                         poff, None if scale is None else scale.data_ptr(), pbase, ld_base, out.data_ptr(), ldo,
                         None if u is None else u.data_ptr(), _status_word(index).data_ptr())
-    _enqueue("situ_moe_lora", index, ctypes.byref(args), ws.data_ptr(), max(16, size))
+    _enqueue("situ_moe_lora", index, ctypes.byref(args), pws, size)
     return (out, u) if keep else out
 
 
@@ -1216,12 +1249,12 @@ def situ_moe_lora_backward(dy: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b
     else:
         ldo = _given(out, (S, K), dx_dtype, index, 4 if dx_dtype is torch.float32 else 8)
     da, db = _empty((n, r, K), (r * K, K, 1), dtype, index), _empty((n, N, r), (N * r, r, 1), dtype, index)
-    size = (_lib or lib()).situ_moe_lora_backward_workspace_size(S, K, N, r)
-    ws = _empty((max(16, size),), (1,), torch.uint8, index)
+    size = _lora_backward_bytes(S, K, N, r, index)
+    ws, pws = _scratch(size, index)
     args = SituLoraBackwardArgs(_DTYPES[dtype], _DTYPES.get(dx_dtype, -1), S, K, N, r, n, pdy, ld_dy, px, ldx, a.data_ptr(),
                                 b.data_ptr(), offsets.data_ptr(), None if scale is None else scale.data_ptr(), pu, pdx0,
                                 ld_dx0, out.data_ptr(), ldo, da.data_ptr(), db.data_ptr(), _status_word(index).data_ptr())
-    _enqueue("situ_moe_lora_backward", index, ctypes.byref(args), ws.data_ptr(), max(16, size))
+    _enqueue("situ_moe_lora_backward", index, ctypes.byref(args), pws, size)
     return out, da, db
 
 

@@ -468,6 +468,7 @@ bool bad(const void* q, uintptr_t mask) { return (reinterpret_cast<uintptr_t>(q)
 extern "C" size_t situ_moe_balance_loss_workspace_size(int32_t T, int32_t num_experts_total) {
   using namespace situ;
   if (T < 0 || num_experts_total < 1 || num_experts_total > kMaxExperts) return 0;
+  if (forward_grid(T, num_experts_total) == 1) return 0;   // one CTA writes the result itself
   const size_t grid = (size_t)forward_grid(T, num_experts_total), pitch = (size_t)(num_experts_total + 3) / 4 * 4;
   return (grid * (2 * pitch + 1) * 4 + 15) / 16 * 16;
 }
@@ -480,12 +481,13 @@ extern "C" situ_status situ_moe_balance_loss(const situ_balance_args* a, void* w
   if (a->T < 0 || E < 1 || E > kMaxExperts || a->top_k < 1 || a->top_k > SITU_MAX_TOP_K || a->top_k > E || a->ld < E ||
       a->ld > (int64_t)1 << 39)
     return SITU_ERR_BAD_SHAPE;
-  if (!a->loss || !a->counts || !a->tokens || !workspace) return SITU_ERR_NULL_ARG;
+  const size_t need = situ_moe_balance_loss_workspace_size(a->T, E);
+  if (!a->loss || !a->counts || !a->tokens || (need > 0 && !workspace)) return SITU_ERR_NULL_ARG;
   if (a->T > 0 && (!a->router_logits || !a->topk_ids || !a->row_stats)) return SITU_ERR_NULL_ARG;
   if (bad(a->router_logits, 3) || bad(a->topk_ids, 3) || bad(a->loss, 3) || bad(a->counts, 3) || bad(a->tokens, 3) ||
       bad(a->row_stats, 7) || bad(workspace, 15))
     return SITU_ERR_MISALIGNED;
-  if (workspace_bytes < situ_moe_balance_loss_workspace_size(a->T, E)) return SITU_ERR_WORKSPACE_TOO_SMALL;
+  if (workspace_bytes < need) return SITU_ERR_WORKSPACE_TOO_SMALL;
   cudaStream_t st = (cudaStream_t)stream;
   const int grid = forward_grid(a->T, E);
   BalanceParams p;

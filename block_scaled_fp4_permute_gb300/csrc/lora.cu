@@ -31,14 +31,13 @@
 // 16-bit terms, three in bf16 and two in f16, which hold 24 and 22 of its bits.
 // f16 rows are brought to [2^14, 2^15) by a power of two first, taken out of the
 // sums again, so that a u beyond f16 neither overflows nor vanishes.
-#include "../../include/situ_moe.h"
-#include "gemm_groups.cuh"
+#include "lora_common.cuh"
 
 #include <cooperative_groups.h>
 
 namespace situ {
 
-using namespace gg;
+using namespace lora;
 
 namespace {
 
@@ -46,8 +45,7 @@ constexpr int kTile = 128;         // rows of a tile
 constexpr int kChunk = 64;         // contraction elements of a stage (shrink)
 constexpr int kXBytes = kTile * 128;   // a box: 128 bytes of 128 rows
 constexpr int kMaxStages = 8;      // of a ring
-constexpr int kShrinkSmem = 218 * 1024, kExpandSmem = 222 * 1024;   // 227 KB with the static parts
-constexpr int kMaxRank = 128;
+constexpr int kShrinkSmem = 218 * 1024, kExpandSmem = 221 * 1024;   // 227 KB with the static parts
 constexpr int kCluster = 8;        // CTAs of a row
 constexpr int kRowThreads = 256;
 
@@ -100,18 +98,6 @@ __device__ __forceinline__ int adapter_of(const int32_t* ids, const int32_t* off
   return lo <= n ? lo - 1 : -1;
 }
 
-template <int DT>
-__device__ __forceinline__ uint32_t pack16(float a, float b) {
-  return DT == SITU_DT_BF16 ? f32x2_to_bf16x2(a, b) : pack_f16x2(a, b);
-}
-template <int DT>
-__device__ __forceinline__ float lo16(uint32_t w) {
-  return DT == SITU_DT_BF16 ? bf16_lo(w) : f16_to_f32(w & 0xFFFFu);
-}
-template <int DT>
-__device__ __forceinline__ float hi16(uint32_t w) {
-  return DT == SITU_DT_BF16 ? bf16_hi(w) : f16_to_f32(w >> 16);
-}
 template <int DT>
 __device__ __forceinline__ float dot8(const uint4& a, const uint4& b, float acc) {
   const uint32_t u[4] = {a.x, a.y, a.z, a.w}, v[4] = {b.x, b.y, b.z, b.w};
@@ -301,43 +287,11 @@ __device__ __forceinline__ void find_adapters(Adapters<R>& t, const LoraParams& 
   epi_sync();
 }
 
-// A ring whose length the launch chooses.
-struct Turns {
-  int n, s = 0, used = 0;
-  uint32_t ph = 0;
-  __device__ __forceinline__ explicit Turns(int stages) : n(stages) {}
-  __device__ __forceinline__ bool again() const { return used == n; }   // the stage has been used before
-  __device__ __forceinline__ void next() {
-    if (used < n) ++used;
-    if (++s == n) {
-      s = 0;
-      ph ^= 1;
-    }
-  }
-  // wait(stage, parity) for the last use of each stage
-  template <class Wait>
-  __device__ __forceinline__ bool last(Wait&& wait) const {
-    bool ok = true;
-    for (int j = 0; j < used; ++j) ok = wait(j, j < s ? ph : ph ^ 1) && ok;
-    return ok;
-  }
-};
-
 constexpr int kTmemCols = 512;                // of an SM
 constexpr int kShrinkRows = 256;              // of a tile of the shrink: two MMAs share an adapter's weights
 constexpr int kShrinkThreads = 64 + kEpi;     // copies, MMAs; eight epilogue warps
 constexpr int kExpandThreads = 128 + kEpi;    // copies of base and out, MMAs, copies of weights; eight epilogue warps
 
-// D[128, N] of 16-bit operands in fp32; trans_b: B's N elements contiguous
-__device__ __forceinline__ uint32_t idesc_of(bool bf16, bool trans_b, int N) {
-  return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (trans_b ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) |
-         ((uint32_t)(128 >> 4) << 24);
-}
-
-// Items dealt out evenly: CTA c of G takes [c T / G, (c + 1) T / G) of T, and
-// item i is CTA ((i + 1) G - 1) / T's.
-__host__ __device__ __forceinline__ long first_item(long c, long T, long G) { return c * T / G; }
-__host__ __device__ __forceinline__ long cta_of(long i, long T, long G) { return ((i + 1) * G - 1) / T; }
 // A CTA's items of one tile, `per` items to a tile, and the next tile's.
 struct Segment {
   long i, end;
@@ -370,27 +324,6 @@ __device__ __forceinline__ void store_commit() { asm volatile("cp.async.bulk.com
 template <int N>
 __device__ __forceinline__ void store_wait_read() {
   asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
-}
-
-// eight sums to memory, a whole sector a lane; add: to what is there
-__device__ __forceinline__ void put8(float* o, const uint32_t* v, bool add) {
-  float f[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[i]);
-  if (add) {
-    const float4 a = *reinterpret_cast<const float4*>(o), b = *reinterpret_cast<const float4*>(o + 4);
-    f[0] += a.x;
-    f[1] += a.y;
-    f[2] += a.z;
-    f[3] += a.w;
-    f[4] += b.x;
-    f[5] += b.y;
-    f[6] += b.z;
-    f[7] += b.w;
-  }
-  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(o), "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]),
-               "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7])
-               : "memory");
 }
 
 // part[.][i][j] = sum over a range of k of x[i, k] W[e(i)][j][k] (TRANS:
@@ -511,7 +444,7 @@ shrink_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
   } else if (warp == 1 && !dead) {
     // ---------------- MMAs ----------------
     const bool leader = elect_one();
-    const uint32_t idesc = idesc_of(DT == SITU_DT_BF16, TRANS, p.r16);
+    const uint32_t idesc = idesc_of(DT == SITU_DT_BF16, false, TRANS, p.r16);
     Turns x(p.x_stages), w(p.stages), l(2), acc(2);
     bool ok = true;
     for (Segment g(i0, i1, p.chunks); g.more() && ok; g.next()) {
@@ -748,7 +681,7 @@ expand_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
   } else if (warp == 1 && !dead) {
     // ---------------- MMAs ----------------
     const bool leader = elect_one();
-    const uint32_t idesc = idesc_of(DT == SITU_DT_BF16, TRANS, kCols);
+    const uint32_t idesc = idesc_of(DT == SITU_DT_BF16, false, TRANS, kCols);
     Turns w(p.stages), acc(2), l(2);
     uint32_t seg = 0;
     bool ok = true;
@@ -995,6 +928,7 @@ expand_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
       }
     }
   }
+  if (dead) griddep_wait();          // the others have, or wait for a warp that has
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   if (warp == 1) {
@@ -1118,9 +1052,12 @@ bool by_rows(int S) { return S <= 64; }
 
 size_t part_bytes(int S, int C, int r) { return S == 0 ? 0 : (size_t)most_parts(S, C) * S * r * 4; }
 
-bool bad(const void* q, uintptr_t mask) { return (reinterpret_cast<uintptr_t>(q) & mask) != 0; }
-// the tensor maps take strides below 2^40 bytes
-bool bad_ld(int64_t ld, int64_t cols, int64_t unit) { return ld < cols || ld % unit != 0 || ld >= (int64_t)1 << 38; }
+// of the backward pass: first the parts of v, then those of the gradients
+size_t shared_bytes(int S, int N, int r) {
+  const size_t a = part_bytes(S, N, r), b = outer_bytes(r);
+  return a > b ? a : b;
+}
+
 bool bad_extent(int C) { return C < 8 || C % 8 != 0 || C > SITU_GEMM_MAX_DIM; }
 bool bad_sizes(int S, int K, int N, int r, int n) {
   return S < 0 || S > SITU_GEMM_MAX_ROWS || bad_extent(K) || bad_extent(N) || r < 8 || r % 8 != 0 || r > kMaxRank || n < 1 ||
@@ -1133,7 +1070,7 @@ bool bad_sizes(int S, int K, int N, int r, int n) {
 extern "C" size_t situ_moe_lora_workspace_size(int32_t S, int32_t K, int32_t N, int32_t r) {
   using namespace situ;
   if (bad_sizes(S, K, N, r, 1)) return 0;
-  return S == 0 || by_rows(S) ? 16 : part_bytes(S, K, r);
+  return S == 0 || by_rows(S) ? 0 : part_bytes(S, K, r);
 }
 
 extern "C" situ_status situ_moe_lora(const situ_lora_args* a, void* workspace, size_t workspace_bytes, void* stream) {
@@ -1203,7 +1140,7 @@ extern "C" situ_status situ_moe_lora(const situ_lora_args* a, void* workspace, s
 extern "C" size_t situ_moe_lora_backward_workspace_size(int32_t S, int32_t K, int32_t N, int32_t r) {
   using namespace situ;
   if (bad_sizes(S, K, N, r, 1)) return 0;
-  return part_bytes(S, N, r) + ((size_t)S * r * 2 + 15) / 16 * 16 + 16;
+  return shared_bytes(S, N, r) + ((size_t)S * r * 2 + 15) / 16 * 16 + 16;
 }
 
 extern "C" situ_status situ_moe_lora_backward(const situ_lora_backward_args* a, void* workspace, size_t workspace_bytes,
@@ -1224,7 +1161,7 @@ extern "C" situ_status situ_moe_lora_backward(const situ_lora_backward_args* a, 
   if (bad(workspace, 31)) return SITU_ERR_MISALIGNED;
   if (bad(a->offsets, 3) || bad(a->scale, 3) || bad(a->device_status, 3)) return SITU_ERR_MISALIGNED;
   if (workspace_bytes < situ_moe_lora_backward_workspace_size(a->S, a->K, a->N, a->r)) return SITU_ERR_WORKSPACE_TOO_SMALL;
-  uint8_t* v = static_cast<uint8_t*>(workspace) + part_bytes(a->S, a->N, a->r);
+  uint8_t* v = static_cast<uint8_t*>(workspace) + shared_bytes(a->S, a->N, a->r);
   if (a->S > 0) {
     LoraParams s = {};
     s.offsets = a->offsets;
@@ -1246,6 +1183,25 @@ extern "C" situ_status situ_moe_lora_backward(const situ_lora_backward_args* a, 
         launch_tiles<true>(a->dtype, f32 != 0, a->dy, a->ld_dy, a->b, a->a, s, x, (cudaStream_t)stream);
     if (t != SITU_OK) return t;
   }
+  OuterArgs o;
+  o.dtype = a->dtype;
+  o.S = a->S;
+  o.K = a->K;
+  o.N = a->N;
+  o.r = a->r;
+  o.n = a->n;
+  o.x = a->x;
+  o.dy = a->dy;
+  o.v = v;
+  o.u = a->u;
+  o.ldx = a->ldx;
+  o.ld_dy = a->ld_dy;
+  o.offsets = a->offsets;
+  o.da = a->da;
+  o.db = a->db;
+  o.parts = static_cast<float*>(workspace);             // u's parts have been read
+  o.err = a->device_status;
+  if (a->S > 0 && outer_takes(a->dtype, a->S, a->K, a->N)) return launch_outer(o, (cudaStream_t)stream);
   // over an adapter's rows: dA = v^T x, dB = dy^T u
   situ_grouped_gemm_args g = {};
   g.direction = SITU_GROUPED_WGRAD;

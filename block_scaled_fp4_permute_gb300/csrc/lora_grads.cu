@@ -1,0 +1,360 @@
+// lora_grads.cu -- the gradients of low-rank adapters: sums over the rows of each.
+//
+//   dA[e][j][k] = sum_{rows i of e} v[i, j] x[i, k],   dB[e][n][j] = sum dy[i, n] u[i, j]
+//
+// Both are one form: 128 columns of a wide operand (x or dy) on the MMA's M side,
+// the r columns of a narrow one on its N side, rows along the contraction (both
+// operands MN-major).  Bound by the bytes of x and dy: r operations a byte.  The
+// general products over groups (situ_moe_grouped_gemm) give whole tiles to CTAs, and
+// four adapters of 3584 x 6144 make 56 and 96 tiles for 152 SMs.  Here the
+// chunks of 64 rows of all tiles of both gradients are dealt out evenly over one CTA
+// per SM; tiles that part between CTAs leave fp32 sums, which a second kernel
+// adds in order (16,384 rows, rank 64: 93 us as two general products, 61 so).
+//
+// A tile's last chunk has fewer than 64 rows: it comes row by row (four an
+// instruction), rows past the adapter's end named out of bounds, so that the MMA
+// sees zeros in both operands there: the neighbour's rows may hold infinities.
+#include "lora_common.cuh"
+
+namespace situ {
+namespace lora {
+
+namespace {
+
+constexpr int kThreads = 256;            // copies, MMAs, two idle; four epilogue warps
+constexpr int kRows = 64;                // of a stage
+constexpr int kWide = 2 * kRows * 128;   // bytes of 128 columns of them
+constexpr int kMaxStages = 8;
+constexpr int kSmem = 212 * 1024;        // 227 KB with the scan and the static part
+
+struct OuterParams {
+  const int32_t* offsets;
+  int S, n, r, r16;
+  int C[2], blocks[2];                   // of x and dy: columns, tiles of 128
+  void* out[2];                          // da, db
+  float* parts;                          // [CTA][2][128][r]
+  int stages;
+  int* err;
+};
+// wide and narrow operand of each gradient, by 64 rows and by single ones
+struct OuterMaps {
+  CUtensorMap wide[2], narrow[2], wide1[2], narrow1[2];
+};
+
+// What a CTA has of one tile.
+struct Piece {
+  int which, e, block, from, to, chunks, row0, rows;   // chunks of the tile, the adapter's rows
+  __device__ __forceinline__ bool whole() const { return from == 0 && to == chunks; }
+};
+struct Deal {
+  const int *tp, *row;
+  int n, blocks_a, blocks_b;
+  long total;
+  __device__ __forceinline__ Deal(const OuterParams& p, const int* tp_, const int* row_)
+      : tp(tp_), row(row_), n(p.n), blocks_a(p.blocks[0]), blocks_b(p.blocks[1]), total((long)tp_[p.n] * (blocks_a + blocks_b)) {}
+  // of items [i, end) the part in i's tile: first dA's tiles, by adapter, then dB's
+  __device__ __forceinline__ Piece at(long i, long end) const {
+    Piece t;
+    const long a = (long)tp[n] * blocks_a;
+    t.which = i >= a;
+    const long j = t.which ? i - a : i;
+    const int blocks = t.which ? blocks_b : blocks_a;
+    t.e = find_group(tp, n, (int)(j / blocks));
+    t.chunks = tp[t.e + 1] - tp[t.e];
+    const long rem = j - (long)tp[t.e] * blocks;
+    t.block = (int)(rem / t.chunks);
+    t.from = (int)(rem - (long)t.block * t.chunks);
+    t.to = (int)min((long)t.chunks, t.from + (end - i));
+    t.row0 = row[t.e];
+    t.rows = row[t.e + 1] - row[t.e];
+    return t;
+  }
+};
+
+// Sums of column c of a tile to the gradient, rounded: da is [j][c], db [c][j].
+template <int DT>
+__device__ __forceinline__ void store16(const OuterParams& p, const Piece& t, int c, int j, const float* v) {
+  uint16_t* out = static_cast<uint16_t*>(p.out[t.which]);
+  if (t.which == 0) {
+    out += ((size_t)t.e * p.r + j) * p.C[0] + c;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) out[(size_t)i * p.C[0]] = (uint16_t)pack16<DT>(v[i], 0.f);
+  } else {
+    *reinterpret_cast<uint4*>(out + ((size_t)t.e * p.C[1] + c) * p.r + j) =
+        make_uint4(pack16<DT>(v[0], v[1]), pack16<DT>(v[2], v[3]), pack16<DT>(v[4], v[5]), pack16<DT>(v[6], v[7]));
+  }
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kThreads, 1)
+outer_kernel(const __grid_constant__ OuterMaps m, const OuterParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ int scan[kScanInts];
+  __shared__ uint64_t bars[2 * kMaxStages + 5];
+  __shared__ uint32_t holder[2];
+  const uint32_t sbase = (saddr(smem_raw) + 1023) & ~1023u;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t bar0 = saddr(bars);
+  auto full = [&](int s) { return bar0 + 8 * s; };
+  auto empty = [&](int s) { return bar0 + 8 * (kMaxStages + s); };
+  auto acc_full = [&](int b) { return bar0 + 8 * (2 * kMaxStages + b); };
+  auto acc_empty = [&](int b) { return bar0 + 8 * (2 * kMaxStages + 2 + b); };
+  const uint32_t drain = bar0 + 8 * (2 * kMaxStages + 4);
+  if (tid == 0) {
+    holder[1] = (uint32_t)*reinterpret_cast<volatile int*>(p.err);   // an earlier launch gave up a wait: no work then
+    for (int s = 0; s < 2 * kMaxStages; ++s) mbar_init(bar0 + 8 * s, 1);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(acc_full(b), 1);
+      mbar_init(acc_empty(b), 4);
+    }
+    mbar_init(drain, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) tmem_alloc<1>(saddr(holder), 256);
+  scan_tiles(p.offsets, p.n, p.S, kRows, scan, scan + kMaxGroups + 1, kThreads);
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const uint32_t tmem = holder[0];
+  const bool dead = holder[1] != 0;
+  const Deal deal(p, scan, scan + kMaxGroups + 1);
+  const long i0 = first_item(blockIdx.x, deal.total, gridDim.x), i1 = first_item(blockIdx.x + 1, deal.total, gridDim.x);
+  const int nboxes = (p.r + 63) / 64, stage = kWide + nboxes * kRows * 128;
+
+  if (warp == 0 && !dead) {
+    // ---------------- copies ----------------
+    const bool leader = elect_one();
+    Turns r(p.stages);
+    bool ok = true;
+    for (long i = i0; i < i1 && ok;) {
+      const Piece t = deal.at(i, i1);
+      i += t.to - t.from;
+      const int c0 = t.block * 128, wboxes = c0 + 64 < p.C[t.which] ? 2 : 1;
+      for (int k = t.from; k < t.to; ++k, r.next()) {
+        if (r.again() && !warp_wait(empty(r.s), r.ph ^ 1, p.err, 121)) {
+          ok = false;
+          break;
+        }
+        const uint32_t to = sbase + r.s * stage;
+        const int left = t.rows - k * kRows, row = t.row0 + k * kRows;
+        if (left >= kRows) {
+          if (leader) {
+            mbar_expect_tx(full(r.s), (wboxes + nboxes) * kRows * 128);
+            for (int h = 0; h < wboxes; ++h) copy_2d<1>(to + h * kRows * 128, &m.wide[t.which], c0 + 64 * h, row, full(r.s));
+            for (int h = 0; h < nboxes; ++h) copy_2d<1>(to + kWide + h * kRows * 128, &m.narrow[t.which], 64 * h, row, full(r.s));
+          }
+        } else {
+          const int fours = (left + 15) / 16 * 4, boxes = wboxes + nboxes;
+          if (leader) mbar_expect_tx(full(r.s), boxes * fours * 512);
+          __syncwarp();
+          for (int g = lane; g < boxes * fours; g += 32) {
+            const int box = g / fours, f = 4 * (g - box * fours);
+            int at[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) at[j] = f + j < left ? row + f + j : p.S;
+            const bool wide = box < wboxes;
+            copy_rows4<1>(to + (wide ? box : 2 + box - wboxes) * kRows * 128 + f * 128,
+                          wide ? &m.wide1[t.which] : &m.narrow1[t.which], wide ? c0 + 64 * box : 64 * (box - wboxes), at[0], at[1],
+                          at[2], at[3], full(r.s));
+          }
+        }
+        __syncwarp();
+      }
+    }
+    leave(
+        ok, [&] { return r.last([&](int j, uint32_t ph) { return warp_wait(empty(j), ph, p.err, 122); }); },
+        [&] { r.last([&](int j, uint32_t ph) { return drain_wait(full(j), ph); }); });
+  } else if (warp == 1 && !dead) {
+    // ---------------- MMAs ----------------
+    const bool leader = elect_one();
+    const uint32_t idesc = idesc_of(DT == SITU_DT_BF16, true, true, p.r16);
+    Turns r(p.stages), acc(2);
+    bool ok = true;
+    for (long i = i0; i < i1 && ok;) {
+      const Piece t = deal.at(i, i1);
+      i += t.to - t.from;
+      if (acc.again() && !warp_wait(acc_empty(acc.s), acc.ph ^ 1, p.err, 123)) {
+        ok = false;
+        break;
+      }
+      for (int k = t.from; k < t.to; ++k, r.next()) {
+        if (!warp_wait(full(r.s), r.ph, p.err, 124)) {
+          ok = false;
+          break;
+        }
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        if (leader) {
+          const uint32_t a = sbase + r.s * stage;
+          const int steps = min(kRows / 16, (t.rows - k * kRows + 15) / 16);
+          for (int j = 0; j < steps; ++j)
+            mma_f16<1>(tmem + acc.s * 128, sdesc_mn(a, kRows * 128) + 128 * j, sdesc_mn(a + kWide, kRows * 128) + 128 * j, idesc,
+                       ((k - t.from) | j) != 0);
+          mma_commit(empty(r.s));
+        }
+        __syncwarp();
+      }
+      if (ok) {
+        if (leader) mma_commit(acc_full(acc.s));
+        __syncwarp();
+        acc.next();
+      }
+    }
+    leave(
+        ok, [&] { return r.last([&](int j, uint32_t ph) { return warp_wait(empty(j), ph, p.err, 125); }); },
+        [&] {
+          if (leader) mma_commit(drain);
+          __syncwarp();
+          drain_wait(drain, 0);
+        });
+  } else if (warp >= 4 && !dead) {
+    // ---------------- sums to memory, a column per lane ----------------
+    const int q = warp & 3;
+    // adapters without rows
+    for (int e = 0; e < p.n; ++e) {
+      if (scan[e] != scan[e + 1]) continue;
+      for (int w = 0; w < 2; ++w) {
+        uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out[w]) + (size_t)e * p.r * p.C[w]);
+        const long pieces = (long)p.r * p.C[w] / 8;
+        for (long i = (long)blockIdx.x * 128 + tid - 128; i < pieces; i += (long)gridDim.x * 128) out[i] = make_uint4(0, 0, 0, 0);
+      }
+    }
+    Turns acc(2);
+    for (long i = i0; i < i1; acc.next()) {
+      const Piece t = deal.at(i, i1);
+      i += t.to - t.from;
+      if (!warp_wait(acc_full(acc.s), acc.ph, p.err, 126)) break;
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      const int c = t.block * 128 + 32 * q + lane;
+      float* part = p.parts + (((size_t)blockIdx.x * 2 + (t.from == 0)) * 128 + 32 * q + lane) * p.r;
+      for (int j = 0; j < p.r16; j += 16) {
+        uint32_t v[16];
+        __syncwarp();
+        tmem_ld16_nowait(tmem + ((uint32_t)(32 * q) << 16) + acc.s * 128 + j, v);
+        tmem_ld_wait<16>(v);
+#pragma unroll
+        for (int k = 0; k < 16; k += 8) {
+          if (c >= p.C[t.which] || j + k >= p.r) continue;
+          if (t.whole()) store16<DT>(p, t, c, j + k, reinterpret_cast<const float*>(v + k));
+          else put8(part + j + k, v + k, false);
+        }
+      }
+      __syncwarp();
+      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+      mbar_arrive_if(acc_empty(acc.s), lane == 0);
+    }
+  }
+  griddep_launch_dependents();
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    tmem_free<1>(tmem, 256);
+  }
+}
+
+// The tile that begins in CTA blockIdx.x and goes on in later ones: its sums
+// added up in their order.
+template <int DT>
+__global__ void __launch_bounds__(kThreads)
+outer_join_kernel(const OuterParams p) {
+  __shared__ int scan[kScanInts];
+  scan_tiles(p.offsets, p.n, p.S, kRows, scan, scan + kMaxGroups + 1, kThreads);
+  const Deal deal(p, scan, scan + kMaxGroups + 1);
+  const long G = gridDim.x, i0 = first_item(blockIdx.x, deal.total, G), i1 = first_item(blockIdx.x + 1, deal.total, G);
+  griddep_wait();
+  if (i0 == i1) return;
+  // the piece that holds the CTA's last item
+  Piece t = deal.at(i1 - 1, deal.total);
+  if (t.from + 1 == t.chunks || t.from >= i1 - i0) return;   // it ends here, or began before
+  const int last = (int)cta_of(i1 - 1 + (t.chunks - t.from - 1), deal.total, G);
+  for (int i = threadIdx.x; i < 128 * p.r / 8; i += kThreads) {
+    const int c = i * 8 / p.r, j = i * 8 - c * p.r;
+    if (t.block * 128 + c >= p.C[t.which]) continue;
+    float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int k = blockIdx.x; k <= last; ++k) {
+      if (first_item(k, deal.total, G) == first_item(k + 1, deal.total, G)) continue;   // more CTAs than items
+      const float4* v =
+          reinterpret_cast<const float4*>(p.parts + (((size_t)k * 2 + (k == (int)blockIdx.x)) * 128 + c) * p.r + j);
+      const float4 a = __ldcg(v), b = __ldcg(v + 1);
+      s[0] += a.x;
+      s[1] += a.y;
+      s[2] += a.z;
+      s[3] += a.w;
+      s[4] += b.x;
+      s[5] += b.y;
+      s[6] += b.z;
+      s[7] += b.w;
+    }
+    store16<DT>(p, t, t.block * 128 + c, j, s);
+  }
+}
+
+template <int DT>
+cudaError_t launch_dt(const OuterMaps& m, const OuterParams& p, int smem, cudaStream_t st) {
+  static std::atomic<uint64_t> raised{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (bit == 0 || !(raised.load() & bit)) {
+    std::lock_guard<std::mutex> lock(attr_mutex());
+    e = cudaFuncSetAttribute(outer_kernel<DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    raised.fetch_or(bit);
+  }
+  const unsigned grid = (unsigned)sm_count();
+  outer_kernel<DT><<<grid, kThreads, smem, st>>>(m, p);
+  e = cudaGetLastError();
+  return e != cudaSuccess ? e : launch_pdl(outer_join_kernel<DT>, dim3(grid), dim3(kThreads), 0, st, p);
+}
+
+}  // namespace
+
+size_t outer_bytes(int r) { return (size_t)sm_count() * 2 * 128 * r * 4; }
+
+// The tensor cores truncate when they add, 6e-9 of a sum of one sign per element:
+// a tenth of a 16-bit result's last unit after 65,536 (bf16) and 8,192 (f16).
+bool outer_takes(int dtype, int S, int K, int N) {
+  const double rows = (double)S * ((K + 127) / 128 + (N + 127) / 128) / sm_count() + kRows;   // of a CTA
+  return (rows < S ? rows : S) <= (dtype == SITU_DT_BF16 ? 65536 : 8192);
+}
+
+situ_status launch_outer(const OuterArgs& a, cudaStream_t st) {
+  OuterParams p = {};
+  p.offsets = a.offsets;
+  p.S = a.S;
+  p.n = a.n;
+  p.r = a.r;
+  p.r16 = (a.r + 15) / 16 * 16;
+  p.C[0] = a.K;
+  p.C[1] = a.N;
+  p.blocks[0] = (a.K + 127) / 128;
+  p.blocks[1] = (a.N + 127) / 128;
+  p.out[0] = a.da;
+  p.out[1] = a.db;
+  p.parts = a.parts;
+  p.err = a.err;
+  const int stage = kWide + (a.r + 63) / 64 * kRows * 128;
+  p.stages = (kSmem - 1024) / stage;
+  if (p.stages > kMaxStages) p.stages = kMaxStages;
+  const CUtensorMapDataType dt = a.dtype == SITU_DT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  OuterMaps m;
+  const void *wide[2] = {a.x, a.dy}, *narrow[2] = {a.v, a.u};
+  const int64_t ld[2] = {a.ldx, a.ld_dy};
+  const uint32_t box[2] = {64, kRows}, one[2] = {64, 1};
+  bool ok = true;
+  for (int i = 0; i < 2 && ok; ++i) {
+    const uint64_t dw[2] = {(uint64_t)p.C[i], (uint64_t)a.S}, sw[1] = {(uint64_t)ld[i] * 2};
+    const uint64_t dn[2] = {(uint64_t)a.r, (uint64_t)a.S}, sn[1] = {(uint64_t)a.r * 2};
+    ok = make_map_nd(&m.wide[i], dt, wide[i], 2, dw, sw, box) && make_map_nd(&m.wide1[i], dt, wide[i], 2, dw, sw, one) &&
+         make_map_nd(&m.narrow[i], dt, narrow[i], 2, dn, sn, box) && make_map_nd(&m.narrow1[i], dt, narrow[i], 2, dn, sn, one);
+  }
+  if (!ok) return SITU_ERR_CUDA;
+  const int smem = 1024 + p.stages * stage;
+  const cudaError_t e = a.dtype == SITU_DT_BF16 ? launch_dt<SITU_DT_BF16>(m, p, smem, st) : launch_dt<SITU_DT_F16>(m, p, smem, st);
+  return e == cudaSuccess ? SITU_OK : SITU_ERR_CUDA;
+}
+
+}  // namespace lora
+}  // namespace situ

@@ -642,6 +642,7 @@ typedef struct situ_balance_args {
   int32_t* tokens;                /* [1] */
   float* row_stats;               /* [T, 2] */
 } situ_balance_args;
+/* 0 for few tokens, which take none (and for bad arguments) */
 size_t situ_moe_balance_loss_workspace_size(int32_t T, int32_t num_experts_total);
 situ_status situ_moe_balance_loss(const situ_balance_args* args, void* workspace, size_t workspace_bytes,
                                   void* stream);
@@ -768,6 +769,7 @@ typedef struct situ_lora_args {
   void* u;                        /* [S, r], or NULL */
   int32_t* device_status;         /* as for the expert products */
 } situ_lora_args;
+/* of the current device; 0 for few rows, which take none (and for bad arguments) */
 size_t situ_moe_lora_workspace_size(int32_t S, int32_t K, int32_t N, int32_t r);
 situ_status situ_moe_lora(const situ_lora_args* args, void* workspace, size_t workspace_bytes, void* stream);
 

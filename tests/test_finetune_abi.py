@@ -48,9 +48,9 @@ def balance(lib, ws=0x9000, nbytes=1 << 30, **over):
     (dict(T=-1), 2), (dict(num_experts_total=0), 2), (dict(num_experts_total=4097, ld=4097), 2), (dict(top_k=0), 2),
     (dict(top_k=9), 2), (dict(top_k=17, num_experts_total=64, ld=64), 2), (dict(ld=7), 2), (dict(ld=1 << 40), 2),
     (dict(router_logits=None), 1), (dict(topk_ids=None), 1), (dict(loss=None), 1), (dict(counts=None), 1),
-    (dict(tokens=None), 1), (dict(row_stats=None), 1), (dict(ws=None), 1), (dict(T=0, loss=None), 1),
+    (dict(tokens=None), 1), (dict(row_stats=None), 1), (dict(T=4000, ws=None), 1), (dict(T=0, loss=None), 1),
     (dict(router_logits=0x1002), 6), (dict(row_stats=0x6004), 6), (dict(ws=0x9008), 6), (dict(counts=0x4001), 6),
-    (dict(nbytes=0), 4),
+    (dict(T=4000, nbytes=16), 4),
 ])
 def test_balance_refusals(lib, over, status):
     assert balance(lib, **over) == status
@@ -164,7 +164,9 @@ def test_null_args_and_sizes(lib):
         assert f(None, None) == 1
     assert lib.situ_moe_balance_loss_workspace_size(-1, 8) == 0 and lib.situ_moe_balance_loss_workspace_size(8, 5000) == 0
     assert lib.situ_moe_lora_workspace_size(8, 64, 64, 12) == 0 and lib.situ_moe_lora_backward_workspace_size(8, 60, 64, 8) == 0
-    assert lib.situ_moe_balance_loss_workspace_size(0, 8) > 0 and lib.situ_moe_lora_workspace_size(0, 64, 64, 8) > 0
+    assert lib.situ_moe_balance_loss_workspace_size(4000, 8) > 0 and lib.situ_moe_lora_workspace_size(100, 64, 64, 8) > 0
+    # few tokens or rows take none
+    assert lib.situ_moe_balance_loss_workspace_size(10, 8) == 0 and lib.situ_moe_lora_workspace_size(8, 64, 64, 8) == 0
 
 
 def test_binding_refuses_host_tensors_and_wrong_types():

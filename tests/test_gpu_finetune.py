@@ -680,6 +680,50 @@ def test_lora_gradients(counts, spare, K, N, r, dtype, dx_dtype):
     assert bare.dtype is dtype and (bare[sum(counts):] == 0).all()
 
 
+@pytest.mark.parametrize("counts,K,N,r", [([1] * 40 + [0] * 20 + [3] * 30, 64, 72, 8), ([63, 64, 65, 0, 127, 128, 129], 136, 64, 40),
+                                          ([2000, 0, 3, 700], 1160, 2056, 16), ([5], 8, 4104, 128)])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_lora_gradients_of_many_and_ragged_adapters(counts, K, N, r, dtype):
+    # rows before the first and after the last adapter's hold NaN
+    g = gen(sum(counts) + K)
+    S, n = sum(counts) + 9, len(counts)
+    off = offsets_of(counts) + 4
+    x, dy = normal(g, S, K, dtype=dtype), normal(g, S, N, std=0.1, dtype=dtype)
+    a, b = normal(g, n, r, K, std=K ** -0.5, dtype=dtype), normal(g, n, N, r, std=r ** -0.5, dtype=dtype)
+    x[:4], x[-5:], dy[:4], dy[-5:] = float("nan"), float("inf"), float("inf"), float("nan")
+    _, u = B.situ_moe_lora(None, x, a, b, offsets=off, keep=True)
+    dx, da, db = B.situ_moe_lora_backward(dy, x, a, b, off, u)
+    v = B.situ_moe_lora(None, dy, b.transpose(1, 2).contiguous(), a.transpose(1, 2).contiguous(), offsets=off, keep=True)[1]
+    assert (dx[:4] == 0).all() and (dx[-5:] == 0).all() and torch.isfinite(dx).all()
+    # v as the backward pass rounds it: the same sums by another kernel, so off by a rounding at most
+    for e in range(n):
+        rows = slice(int(off[e]), int(off[e + 1]))
+        L = counts[e]
+        for got, p, t, one in ((da[e], v[rows].double(), x[rows].double(), 2 * H[dtype]),
+                               (db[e].T, u[rows].double(), dy[rows].double(), 0.0)):
+            want, terms = p.T @ t, p.abs().T @ t.abs()
+            within(got, want, 1.2 * H[dtype] * want.abs() + (one + 2 * L * U + 2 * max(K, N) * U) * terms
+                   + TINY[dtype] * (1 + (t.abs().sum(0)[None] if L else 0)))
+            if L == 0:
+                assert (got == 0).all()
+    again = B.situ_moe_lora_backward(dy, x, a, b, off, u)
+    assert torch.equal(again[0], dx) and torch.equal(again[1], da) and torch.equal(again[2], db)
+
+
+def test_lora_gradients_of_long_f16_sums():
+    # more rows than one sum of f16 results takes, and terms of one sign
+    S, C, r = 9000, 10240, 8
+    g = gen(77)
+    x, dy = torch.rand(S, C, generator=g, device="cuda").half(), (torch.rand(S, C, generator=g, device="cuda") * 0.01).half()
+    a, b = torch.full((1, r, C), 1e-3, device="cuda").half(), torch.full((1, C, r), 1e-2, device="cuda").half()
+    off = torch.tensor([0, S], dtype=torch.int32, device="cuda")
+    _, u = B.situ_moe_lora(None, x, a, b, offsets=off, keep=True)
+    _, da, db = B.situ_moe_lora_backward(dy, x, a, b, off, u)
+    want = dy.double().T[:512] @ u.double()
+    # the rounding, a tenth of it more, and 2 U a term of the sums of a chunk of 512
+    within(db[0, :512], want, (1.1 * H[F16] + 512 * 2 * U + 20 * U) * want)
+
+
 def test_lora_linear_by_autograd():
     g = gen(8)
     counts, K, N, r = [60, 0, 41], 64, 128, 8
