@@ -182,9 +182,10 @@ def lib() -> ctypes.CDLL:
             for fn in (l.situ_moe_gated, l.situ_moe_gated_backward):
                 fn.restype = ctypes.c_int
                 fn.argtypes = [ctypes.POINTER(SituGatedArgs), vp]
-            for fn in (l.situ_moe_lora_workspace_size, l.situ_moe_lora_backward_workspace_size):
-                fn.restype = sz
-                fn.argtypes = [i32, i32, i32, i32]
+            l.situ_moe_lora_workspace_size.restype = sz
+            l.situ_moe_lora_workspace_size.argtypes = [i32, i32, i32, i32, i32]
+            l.situ_moe_lora_backward_workspace_size.restype = sz
+            l.situ_moe_lora_backward_workspace_size.argtypes = [i32, i32, i32, i32]
             l.situ_moe_lora.restype = ctypes.c_int
             l.situ_moe_lora.argtypes = [ctypes.POINTER(SituLoraArgs), vp, sz, vp]
             l.situ_moe_lora_backward.restype = ctypes.c_int
@@ -805,8 +806,8 @@ def _balance_bytes(T, E, index):
 
 
 @functools.lru_cache(maxsize=4096)
-def _lora_bytes(S, K, N, r, index):
-    return _size("situ_moe_lora_workspace_size", index, S, K, N, r)
+def _lora_bytes(S, K, N, r, n, index):
+    return _size("situ_moe_lora_workspace_size", index, S, K, N, r, n)
 
 
 @functools.lru_cache(maxsize=4096)
@@ -1208,7 +1209,7 @@ def situ_moe_lora(base, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, *, id
     else:
         ldo = _given(out, (S, N), out_dtype, index, 4 if out_dtype is torch.float32 else 8)
     u = _empty((S, r), (r, 1), dtype, index) if keep else None
-    size = _lora_bytes(S, K, N, r, index)
+    size = _lora_bytes(S, K, N, r, n, index)
     ws, pws = _scratch(size, index)
     args = SituLoraArgs(_DTYPES[dtype], _DTYPES.get(out_dtype, -1), S, K, N, r, n, px, ldx, a.data_ptr(), b.data_ptr(), pids,
                         poff, None if scale is None else scale.data_ptr(), pbase, ld_base, out.data_ptr(), ldo,

@@ -1,30 +1,31 @@
-// lora.cu -- low-rank adapters of many requests beside a shared projection,
-// and their gradients.
+// lora.cu -- low-rank adapters of many requests beside a shared projection, and
+// the gradient of their input.
 //
 // Row i of x [S, K] takes adapter e = ids[i] (or the one whose rows
 // [offsets[e], offsets[e + 1]) hold i), or none:
-//   u[i] = x[i] A[e]^T            A [n, r, K]
-//   y[i] = base[i] + s[e] u[i] B[e]^T     B [n, N, r]
-// and from dy: v = s dy B, dx = dx0 + v A, dA[e] = v^T x, dB[e] = dy^T (s u)
-// over e's rows.  r is small (8 to 128), so all of it is bound by the bytes of
-// x, base and y and of the adapters in use: 2 r (K + N) operations a row
-// against 2 K + 4 N bytes, 16 to 100 a byte.
+//   u[i] = s[e] x[i] A[e]^T          A [n, r, K]
+//   y[i] = base[i] + u[i] B[e]^T     B [n, N, r]
+// and from dy: v = s dy B, dx = dx0 + v A (lora_grads.cu has dA and dB).  r is
+// small (8 to 128), so all of it is bound by the bytes of x, base and y and of the
+// adapters in use: 2 r (K + N) operations a row against 2 K + 4 N bytes.
 //
 // Few rows (a decode step): lora_row_kernel, a cluster of eight CTAs per row.
 // Each CTA takes an eighth of u's sums and, after they have met in shared
 // memory, an eighth of y's columns; its part of B is on its way into the L2
-// meanwhile.  One launch, fp32 multiply-adds.
+// meanwhile.  One launch, fp32 multiply-adds: 64 rows at rank 16 beside 3584 x 6144
+// in 6.4 us.
 //
-// More rows: two kernels on tiles of 64 rows.  shrink_kernel streams x and
-// the adapter once into partial sums of u (split over K where there are few
-// tiles); expand_kernel joins them and adds s u B^T to base.  Neighbouring rows
-// of one request share an adapter, so a tile has one or a few: it goes through
-// its distinct adapters and keeps, of each one's sums, its own rows.  Any order
-// of rows works without sorting or copying them, and a row's result holds
-// nothing of another adapter's weights, infinities or NaN among them.  At 16
-// rows per warp's MMA, with the weights in shared memory by cp.async, mma.sync
-// keeps up with the bytes: tcgen05 would need 128 rows of one adapter to a tile
-// and operands copied to where it reads them.
+// More rows: two kernels on tcgen05.  shrink_kernel streams x and the adapter once
+// into partial sums of u; expand_kernel joins them and adds u B^T to base.
+// Neighbouring rows of one request share an adapter, so a tile has one or a few:
+// it goes through its distinct adapters and keeps, of each one's sums, its own
+// rows.  A row's result then holds nothing of another adapter's weights, infinities
+// and NaN among them, and rows need no order.  Where they have none and the
+// adapters are many, they are sorted first and copied row by row.
+// (mma.sync gave 266 multiply-adds a clock and SM, a thirtieth of tcgen05's: it held
+// a shrink at rank 32 at 28 us where the bytes take 9.)
+// Measured (bf16, 16,384 rows, 3584 -> 6144, rank 64, four adapters): shrink 36 us
+// (117 MB of x), expand 77 (403 MB; a plain copy 62); backwards 58 and 51.
 //
 // u enters the second product in 16 bits.  For 16-bit results it is rounded
 // once (half an ulp of u, as y itself is); for fp32 results it goes as a sum of
@@ -53,9 +54,9 @@ struct LoraParams {
   const int32_t *ids, *offsets;
   int S, C, r, n;                  // C: the other extent (contraction or columns)
   int r16;                         // r rounded up to 16
-  int tiles, shrink_tiles, chunks; // of rows, expand's and shrink's; of the contraction
+  int chunks;                      // of the contraction
   int run;                         // shrink: chunks of a sum in tensor memory
-  long shrink_ctas;
+  long shrink_ctas, least;         // CTAs that the shrink's chunks are dealt out over, chunks of each at least
   float* part;                     // [parts of a tile][S][r]
   const float* scale;              // [n] or null
   const void* base;
@@ -66,6 +67,9 @@ struct LoraParams {
   int stages, w_stage;             // shared memory: stages of w, bytes of one
   int x_stages;                    // shrink: of x
   int y_stages, u_bytes;           // expand: items of base, bytes of u
+  // Rows sorted by adapter, where *mixed (null: never): their numbers, how many
+  // have an adapter, and of each row its place among them (-1: none).
+  const int32_t *mixed, *perm, *kept, *place;
   int* err;
 };
 
@@ -86,13 +90,13 @@ struct RowParams {
 
 __device__ __forceinline__ int adapter_of(const int32_t* ids, const int32_t* offsets, int n, int row) {
   if (ids) {
-    const int e = __ldg(ids + row);
+    const int e = __ldcg(ids + row);
     return e >= 0 && e < n ? e : -1;
   }
   int lo = 0, hi = n + 1;          // the first entry beyond row lies in [lo, hi]
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
-    if (__ldg(offsets + mid) > row) hi = mid;
+    if (__ldcg(offsets + mid) > row) hi = mid;
     else lo = mid + 1;
   }
   return lo <= n ? lo - 1 : -1;
@@ -210,7 +214,7 @@ lora_row_kernel(RowParams p) {
 }
 
 // --------------------------------------------------------------------------
-// tiles of 128 rows
+// tiles
 // --------------------------------------------------------------------------
 
 // The adapters of a tile of R rows: each row's (-1: none), and the distinct ones
@@ -226,20 +230,35 @@ struct Adapters {
 };
 constexpr int kEpi = 256;   // epilogue threads of either kernel
 __device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+// The rows to go through: `count` of them, the i-th is number row(i), S where there
+// is none.
+struct Rows {
+  const int32_t* perm;   // null: as they are
+  int S, count;
+  __device__ __forceinline__ explicit Rows(const LoraParams& p)
+      : perm(p.mixed && __ldcg(p.mixed) ? p.perm : nullptr), S(p.S), count(perm ? __ldcg(p.kept) : p.S) {}
+  __device__ __forceinline__ int row(int i) const { return i >= count ? S : perm ? __ldcg(perm + i) : i; }
+};
+// CTAs that have a share of the shrink's `total` chunks: fewer where sorting has
+// left rows out, so that a tile still comes in no more parts than there is room for.
+__device__ __forceinline__ long sharers(const LoraParams& p, long total) {
+  const long g = total / p.least;
+  return g < 1 ? 1 : g < p.shrink_ctas ? g : p.shrink_ctas;
+}
 // by the epilogue threads, of which this is number i
 template <int R>
-__device__ __forceinline__ void find_adapters(Adapters<R>& t, const LoraParams& p, int row0, int i) {
+__device__ __forceinline__ void find_adapters(Adapters<R>& t, const LoraParams& p, const Rows& rows, int row0, int i) {
   static_assert(R <= kEpi, "a thread per row");
   const bool mine = i < R;
   int e = -1;
   if (mine) {
-    if (row0 + i < p.S) e = adapter_of(p.ids, p.offsets, p.n, row0 + i);
+    if (row0 + i < rows.count) e = adapter_of(p.ids, p.offsets, p.n, rows.row(row0 + i));
     t.of[i] = e;
     t.halves[i] = 0;
   }
   epi_sync();
   const int e0 = t.of[0];
-  const bool same = __all_sync(0xffffffffu, !mine || e == e0 || row0 + i >= p.S);
+  const bool same = __all_sync(0xffffffffu, !mine || e == e0 || row0 + i >= rows.count);
   if (mine && (i & 31) == 0) t.same[i >> 5] = same;
   epi_sync();
   uint32_t all = 1;
@@ -249,7 +268,7 @@ __device__ __forceinline__ void find_adapters(Adapters<R>& t, const LoraParams& 
     if (mine) t.at[i] = e >= 0 ? 0 : -1;
     if (i == 0) {
       t.list[0] = e0;
-      t.halves[0] = p.S - row0 > 128 ? 3 : 1;
+      t.halves[0] = rows.count - row0 > 128 ? 3 : 1;
       t.count = e0 >= 0 ? 1 : 0;
     }
     epi_sync();
@@ -328,8 +347,7 @@ __device__ __forceinline__ void store_wait_read() {
 
 // part[.][i][j] = sum over a range of k of x[i, k] W[e(i)][j][k] (TRANS:
 // W[e][k][j]): the tile's rows on the MMA's M side (two MMAs of 128: with one the
-// weights were a third of what the SMs take in, 16,384 rows at rank 64 W128 us,
-// W256 so), an adapter's r on its N side, in TMEM columns of its own.  As many
+// weights were a third of what the SMs take in), an adapter's r on its N side, in TMEM columns of its own.  As many
 // adapters as half of the columns hold share a pass over x; the other half takes
 // the next sums meanwhile.  The chunks of all tiles are dealt out evenly over the
 // CTAs, one per SM; what a CTA has of a tile is that tile's next part.  For fp32
@@ -337,7 +355,8 @@ __device__ __forceinline__ void store_wait_read() {
 // they add, 6e-9 of a sum of one sign per element; the sums meet in fp32.
 template <int DT, bool TRANS>
 __global__ void __launch_bounds__(kShrinkThreads, 1)
-shrink_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w, const LoraParams p) {
+shrink_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_x1,
+              const __grid_constant__ CUtensorMap map_w, const LoraParams p) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ Adapters<kShrinkRows> lists[2];
   __shared__ uint64_t bars[4 * kMaxStages + 9];
@@ -355,10 +374,12 @@ shrink_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
   auto list_full = [&](int b) { return tail + 32 + 8 * b; };
   auto list_empty = [&](int b) { return tail + 48 + 8 * b; };
   const uint32_t drain = tail + 64;
-  const long total = (long)p.shrink_tiles * p.chunks, G = gridDim.x;
-  const long i0 = first_item(blockIdx.x, total, G), i1 = first_item(blockIdx.x + 1, total, G);
+  const Rows rows(p);
+  const long total = (long)((rows.count + kShrinkRows - 1) / kShrinkRows) * p.chunks, G = sharers(p, total);
+  const bool shares = blockIdx.x < G;
+  const long i0 = shares ? first_item(blockIdx.x, total, G) : 0, i1 = shares ? first_item(blockIdx.x + 1, total, G) : 0;
   if (tid == 0) {
-    for (long i = i0; i < i1 && i < i0 + p.x_stages; ++i)   // x does not wait for the adapters' list
+    for (long i = i0; !rows.perm && i < i1 && i < i0 + p.x_stages; ++i)   // x does not wait for the adapters' list
       for (int h = 0; h < kShrinkRows; h += kTile)
         if ((i / p.chunks) * kShrinkRows + h < p.S)
           prefetch_2d(&map_x, (int)(i % p.chunks) * kChunk, (int)(i / p.chunks) * kShrinkRows + h);
@@ -396,7 +417,11 @@ shrink_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
         break;
       }
       const Adapters<kShrinkRows>& ad = lists[l.s];
-      const int nd = ad.count, row0 = g.tile * kShrinkRows, halves = p.S - row0 > kTile ? 2 : 1;
+      const int nd = ad.count, row0 = g.tile * kShrinkRows, halves = rows.count - row0 > kTile ? 2 : 1;
+      int at[2][4];                                     // sorted rows: this lane's four of each 128
+      if (rows.perm)
+        for (int h = 0; h < 2; ++h)
+          for (int j = 0; j < 4; ++j) at[h][j] = rows.row(row0 + h * kTile + 4 * lane + j);
       for (int d0 = 0; d0 < nd && ok; d0 += per) {
         const int d1 = min(nd, d0 + per);
         for (int k = g.from; k < g.to && ok; ++k) {
@@ -406,9 +431,14 @@ shrink_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
           }
           if (leader) {
             mbar_expect_tx(xfull(x.s), halves * kXBytes);
-            for (int h = 0; h < halves; ++h)
+            for (int h = 0; h < halves && !rows.perm; ++h)
               copy_2d<1>(sbase + (2 * x.s + h) * kXBytes, &map_x, k * kChunk, row0 + h * kTile, xfull(x.s));
           }
+          __syncwarp();
+          if (rows.perm)
+            for (int h = 0; h < halves; ++h)
+              copy_rows4<1>(sbase + (2 * x.s + h) * kXBytes + lane * 512, &map_x1, k * kChunk, at[h][0], at[h][1], at[h][2],
+                            at[h][3], xfull(x.s));
           __syncwarp();
           x.next();
           for (int d = d0; d < d1; ++d, w.next()) {
@@ -517,7 +547,7 @@ shrink_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     bool ok = true;
     auto list = [&](const Segment& g) {                 // of a tile, while the one before is worked on
       if (l.again() && !warp_wait(list_empty(l.s), l.ph ^ 1, p.err, 91)) ok = false;
-      find_adapters(lists[l.s], p, g.tile * kShrinkRows, et);
+      find_adapters(lists[l.s], p, rows, g.tile * kShrinkRows, et);
       mbar_arrive_if(list_full(l.s), et == 0);
       l.next();
     };
@@ -585,7 +615,7 @@ shrink_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
 template <int DT, bool TRANS, bool F32>
 __global__ void __launch_bounds__(kExpandThreads, 1)
 expand_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_base,
-              const __grid_constant__ CUtensorMap map_out, const LoraParams p) {
+              const __grid_constant__ CUtensorMap map_base1, const __grid_constant__ CUtensorMap map_out, const LoraParams p) {
   constexpr int kTerms = terms_of(DT, F32), kCols = cols_of(F32), kBoxCols = kCols / 2;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Adapters<kTile> lists[2];
@@ -634,7 +664,8 @@ expand_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
   const uint32_t tmem = holder[0];
   const bool dead = holder[1] != 0;
   const int blocks = (p.C + kCols - 1) / kCols;
-  const long total = (long)p.tiles * blocks, G = gridDim.x;
+  const Rows rows(p);
+  const long total = (long)((rows.count + kTile - 1) / kTile) * blocks, G = gridDim.x;
   const long i0 = first_item(blockIdx.x, total, G), i1 = first_item(blockIdx.x + 1, total, G);
   const uint32_t ubase = sbase, wbase = sbase + p.u_bytes, ybase = wbase + p.stages * p.w_stage;
   const int rboxes = (p.r + 63) / 64, steps = p.r16 / 16;
@@ -646,14 +677,23 @@ expand_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
     Turns in(p.y_stages), out(p.y_stages);
     bool ok = true;
     long next = i0;
+    int of_tile = -1, at[4];                            // sorted rows: this lane's four of a tile
     auto load = [&] {
+      const int tile = (int)(next / blocks), c0 = (int)(next - (long)tile * blocks) * kCols;
+      const int boxes = c0 + kBoxCols < p.C ? 2 : 1;
+      const uint32_t to = ybase + in.s * 2 * kXBytes;
       if (leader) {
-        const int tile = (int)(next / blocks), c0 = (int)(next - (long)tile * blocks) * kCols;
-        const int boxes = c0 + kBoxCols < p.C ? 2 : 1;
         mbar_expect_tx(yfull(in.s), p.base ? boxes * kXBytes : 0);
-        if (p.base)
-          for (int h = 0; h < boxes; ++h)
-            copy_2d<1>(ybase + in.s * 2 * kXBytes + h * kXBytes, &map_base, c0 + h * kBoxCols, tile * kTile, yfull(in.s));
+        if (p.base && !rows.perm)
+          for (int h = 0; h < boxes; ++h) copy_2d<1>(to + h * kXBytes, &map_base, c0 + h * kBoxCols, tile * kTile, yfull(in.s));
+      }
+      __syncwarp();
+      if (p.base && rows.perm) {
+        if (tile != of_tile)
+          for (int j = 0; j < 4; ++j) at[j] = rows.row(tile * kTile + 4 * lane + j);
+        of_tile = tile;
+        for (int h = 0; h < boxes; ++h)
+          copy_rows4<1>(to + h * kXBytes + lane * 512, &map_base1, c0 + h * kBoxCols, at[0], at[1], at[2], at[3], yfull(in.s));
       }
       __syncwarp();
       in.next();
@@ -665,7 +705,7 @@ expand_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
         ok = false;
         break;
       }
-      if (leader) {
+      if (leader && !rows.perm) {                          // sorted rows: the epilogue has stored them
         const int tile = (int)(i / blocks), c0 = (int)(i - (long)tile * blocks) * kCols;
         for (int h = 0; h < 2 && c0 + h * kBoxCols < p.C; ++h)
           store_2d(&map_out, ybase + out.s * 2 * kXBytes + h * kXBytes, c0 + h * kBoxCols, tile * kTile);
@@ -766,6 +806,22 @@ expand_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
     leave(
         ok, [&] { return w.last([&](int j, uint32_t ph) { return warp_wait(wempty(j), ph, p.err, 109); }); },
         [&] { w.last([&](int j, uint32_t ph) { return drain_wait(wfull(j), ph); }); });
+  } else if (warp == 3 && !dead && rows.perm) {
+    // ---------------- rows without an adapter, where they are not in a tile ----------------
+    constexpr int kEl = F32 ? 4 : 2;
+    for (long r0 = (long)blockIdx.x * 32; r0 < p.S; r0 += G * 32) {
+      uint32_t none = __ballot_sync(0xffffffffu, r0 + lane < p.S && __ldcg(p.place + r0 + lane) < 0);
+      for (; none; none &= none - 1) {
+        const long row = r0 + __ffs(none) - 1;
+        uint4* out = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + (size_t)row * p.ldo * kEl);
+        const uint4* base = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.base) + (size_t)row * p.ld_base * kEl);
+        if (p.out != p.base)
+          for (int i = lane; i < p.C / (16 / kEl); i += 32) out[i] = p.base ? base[i] : make_uint4(0, 0, 0, 0);
+        if (p.u16)
+          for (int i = lane; i < p.r / 8; i += 32)
+            reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.u16) + (size_t)row * p.r)[i] = make_uint4(0, 0, 0, 0);
+      }
+    }
   } else if (warp >= 4 && !dead) {
     // ---------------- lists, u, and sums onto base ----------------
     const int et = tid - 128, q = warp & 3, h = (warp - 4) >> 2;   // this warp's 32 rows, and box of an item
@@ -773,24 +829,26 @@ expand_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
     bool ok = true;
     auto list = [&](const Segment& g) {                 // of a tile, while the one before is worked on
       if (l.again() && !warp_wait(list_empty(l.s), l.ph ^ 1, p.err, 110)) ok = false;
-      find_adapters(lists[l.s], p, g.tile * kTile, et);
+      find_adapters(lists[l.s], p, rows, g.tile * kTile, et);
       mbar_arrive_if(list_full(l.s), et == 0);
       l.next();
     };
     // u of a tile: two threads to a row, eight elements of each sixteen each
     auto stage_u = [&](const Segment& g, const Adapters<kTile>& ad) {
-      const int r = et >> 1, row = g.tile * kTile + r, e = ad.of[r];
+      const int r = et >> 1, place = g.tile * kTile + r, row = rows.row(place), e = ad.of[r];
       const float f = e >= 0 && p.scale ? __ldg(p.scale + e) : 1.f;
       const bool write = p.u16 && g.from == 0 && row < p.S;
-      const long t0 = (long)(g.tile / (kShrinkRows / kTile)) * p.chunks, all = (long)p.shrink_tiles * p.chunks;
-      const int parts = (int)(cta_of(t0 + p.chunks - 1, all, p.shrink_ctas) - cta_of(t0, all, p.shrink_ctas)) + 1;
+      const long t0 = (long)(g.tile / (kShrinkRows / kTile)) * p.chunks;
+      const long all = (long)((rows.count + kShrinkRows - 1) / kShrinkRows) * p.chunks;
+      const long sharing = sharers(p, all);
+      const int parts = (int)(cta_of(t0 + p.chunks - 1, all, sharing) - cta_of(t0, all, sharing)) + 1;
       auto sum8 = [&](int j, float (&u)[8]) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) u[k] = 0.f;
         if (e < 0 || j >= p.r) return;
 #pragma unroll 4
         for (int s = 0; s < parts; ++s) {
-          const float4* src = reinterpret_cast<const float4*>(p.part + ((size_t)s * p.S + row) * p.r + j);
+          const float4* src = reinterpret_cast<const float4*>(p.part + ((size_t)s * p.S + place) * p.r + j);
           const float4 v = __ldcg(src), z = __ldcg(src + 1);
           u[0] += v.x;
           u[1] += v.y;
@@ -859,6 +917,7 @@ expand_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
       const Adapters<kTile>& ad = lists[lb];
       const int nd = ad.count, at = ad.at[32 * q + lane];
       const float my_back = DT == SITU_DT_F16 ? back[32 * q + lane] : 1.f;
+      const int my_row = rows.perm ? rows.row(g.tile * kTile + 32 * q + lane) : 0;
       for (int b = g.from; b < g.to && ok; ++b, y.next()) {
         uint8_t* mine = smem + (ybase - sbase) + y.s * 2 * kXBytes + h * kXBytes + (32 * q + lane) * 128;
         auto piece = [&](int j) { return reinterpret_cast<uint4*>(mine + ((j ^ (lane & 7)) << 4)); };
@@ -917,6 +976,18 @@ expand_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
           mbar_arrive_if(acc_empty(acc.s), lane == 0);
         }
         if (!ok) break;
+        if (rows.perm) {                                   // 32 rows of 128 bytes, four a time
+          __syncwarp();
+          const uint8_t* box = smem + (ybase - sbase) + y.s * 2 * kXBytes + h * kXBytes + 32 * q * 128;
+          const int col = b * kCols + kBoxCols * h + (lane & 7) * (kBoxCols / 8);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int r = 4 * j + (lane >> 3), row = __shfl_sync(0xffffffffu, my_row, r);
+            const uint4 o = *reinterpret_cast<const uint4*>(box + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+            if (row < p.S && col < p.C)
+              *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + ((size_t)row * p.ldo + col) * (F32 ? 4 : 2)) = o;
+          }
+        }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         mbar_arrive_if(ydone(y.s), lane == 0);
@@ -928,7 +999,7 @@ expand_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
       }
     }
   }
-  if (dead) griddep_wait();          // the others have, or wait for a warp that has
+  if (dead || i0 == i1) griddep_wait();   // the others have, or wait for a warp that has
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   if (warp == 1) {
@@ -942,22 +1013,57 @@ expand_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
 // launches
 // --------------------------------------------------------------------------
 
-// CTAs of the shrink: one per SM, of at least two chunks.
-long shrink_ctas(int S, int C) {
-  const long tiles = (S + kShrinkRows - 1) / kShrinkRows, total = tiles * ((C + kChunk - 1) / kChunk), sms = sm_count();
-  const long g = total / 2 < sms ? total / 2 : sms;
-  return g < 1 ? 1 : g;
-}
-// the most parts that a tile's chunks can come in
-long most_parts(int S, int C) {
-  const long tiles = (S + kShrinkRows - 1) / kShrinkRows, chunks = (C + kChunk - 1) / kChunk;
-  const long least = tiles * chunks / shrink_ctas(S, C), most = (chunks + least - 2) / least + 1;
-  return most < chunks ? most : chunks;
-}
+// How the shrink's chunks are dealt out: one CTA per SM, of at least two chunks;
+// `most`: parts that a tile's chunks can come in.
+struct Shares {
+  long ctas, least, most;
+  Shares(int S, int C) {
+    const long tiles = (S + kShrinkRows - 1) / kShrinkRows, chunks = (C + kChunk - 1) / kChunk, total = tiles * chunks;
+    const long sms = sm_count();
+    ctas = total / 2 < sms ? total / 2 : sms;
+    if (ctas < 1) ctas = 1;
+    least = total / ctas;
+    if (least < 1) least = 1;
+    most = (chunks + least - 2) / least + 1;
+    if (most > chunks) most = chunks;
+  }
+};
 
 struct Maps {
-  CUtensorMap x, w, other, base, out;
+  CUtensorMap x, x1, w, other, base, base1, out;   // x1, base1: row by row, for sorted rows
 };
+
+// *mixed: whether going through the rows as they are takes the tiles through many
+// more adapters than sorted.  Counted over up to kLooked tiles: neighbours that
+// differ, and one, but no more than there are adapters; sorted, a tile takes one
+// and each adapter one more.  Five per tile are as many as the sorted rows' way of
+// copying costs (16,384 rows in any order of 4 adapters 159 us as they are and 207
+// sorted, of 9 309 and 209, of 256 3406 and 246; in runs of 256 150).
+constexpr int kLooked = 1024;
+__global__ void __launch_bounds__(1024)
+mixed_kernel(const int32_t* ids, int S, int n, int32_t* mixed) {
+  __shared__ int found[32];
+  const int tiles = (S + kTile - 1) / kTile, step = (tiles + kLooked - 1) / kLooked, looked = (tiles + step - 1) / step;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int sum = 0;
+  for (int t = warp; t < looked; t += 32) {
+    const long r0 = (long)t * step * kTile;
+    int changes = 0;
+#pragma unroll
+    for (int j = 0; j < kTile / 32; ++j) {
+      const long r = r0 + 32 * j + lane;
+      changes += r > r0 && r < S && __ldg(ids + r) != __ldg(ids + r - 1);
+    }
+    sum += min(__reduce_add_sync(0xffffffffu, changes) + 1, n);
+  }
+  if (lane == 0) found[warp] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    long total = 0;
+    for (int w = 0; w < 32; ++w) total += found[w];
+    *mixed = total * tiles / looked > 5l * tiles + n;
+  }
+}
 
 template <int DT, bool TRANS, bool F32>
 cudaError_t launch_pair(const Maps& m, LoraParams s, LoraParams x, cudaStream_t st) {
@@ -981,7 +1087,8 @@ cudaError_t launch_pair(const Maps& m, LoraParams s, LoraParams x, cudaStream_t 
   s.stages = (kShrinkSmem - 1024 - s.x_stages * 2 * kXBytes) / s.w_stage;
   if (s.stages > kMaxStages) s.stages = kMaxStages;
   const long sms = sm_count();
-  shrink<<<(unsigned)s.shrink_ctas, kShrinkThreads, 1024 + s.x_stages * 2 * kXBytes + s.stages * s.w_stage, st>>>(m.x, m.w, s);
+  shrink<<<(unsigned)s.shrink_ctas, kShrinkThreads, 1024 + s.x_stages * 2 * kXBytes + s.stages * s.w_stage, st>>>(m.x, m.x1, m.w,
+                                                                                                               s);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   x.u_bytes = (terms_of(DT, F32) * x.r16 + 63) / 64 * kXBytes;
@@ -994,9 +1101,9 @@ cudaError_t launch_pair(const Maps& m, LoraParams s, LoraParams x, cudaStream_t 
     if (x.y_stages > 4) x.y_stages = 4;
     if (x.y_stages >= 3 || x.stages == 2) break;
   }
-  const long items = (long)x.tiles * ((x.C + cols_of(F32) - 1) / cols_of(F32));
+  const long items = (long)((x.S + kTile - 1) / kTile) * ((x.C + cols_of(F32) - 1) / cols_of(F32));
   return launch_pdl(expand, dim3((unsigned)(items < sms ? items : sms)), dim3(kExpandThreads), rest + x.y_stages * 2 * kXBytes,
-                    st, m.other, m.base, m.out, x);
+                    st, m.other, m.base, m.base1, m.out, x);
 }
 
 // x [S, C] times the adapters' w [n, r, C] (TRANS: [n, C, r]), and that times
@@ -1007,9 +1114,9 @@ situ_status launch_tiles(int dtype, bool f32, const void* rows, int64_t ld_rows,
   const uint64_t S = (uint64_t)s.S, C = (uint64_t)s.C, O = (uint64_t)x.C, r = (uint64_t)s.r, n = (uint64_t)s.n;
   s.r16 = x.r16 = (s.r + 15) / 16 * 16;
   s.chunks = (s.C + kChunk - 1) / kChunk;
-  s.tiles = x.tiles = (s.S + kTile - 1) / kTile;
-  s.shrink_tiles = x.shrink_tiles = (s.S + kShrinkRows - 1) / kShrinkRows;
-  s.shrink_ctas = x.shrink_ctas = shrink_ctas(s.S, s.C);
+  const Shares shares(s.S, s.C);
+  s.shrink_ctas = x.shrink_ctas = shares.ctas;
+  s.least = x.least = shares.least;
   s.run = f32 ? 1024 / kChunk : s.chunks;
   x.chunks = s.chunks;
   const int boxes = (s.r + 63) / 64;
@@ -1020,8 +1127,10 @@ situ_status launch_tiles(int dtype, bool f32, const void* rows, int64_t ld_rows,
   const CUtensorMapDataType dt = dtype == SITU_DT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   Maps m;
   const uint64_t dx[2] = {C, S}, sx[1] = {(uint64_t)ld_rows * 2};
-  const uint32_t bx[2] = {64, kTile};
+  const uint32_t bx[2] = {64, kTile}, bx1[2] = {64, 1};
   bool ok = make_map_nd(&m.x, dt, rows, 2, dx, sx, bx);
+  m.x1 = m.x;
+  if (s.mixed) ok = ok && make_map_nd(&m.x1, dt, rows, 2, dx, sx, bx1);
   if (TRANS) {
     const uint64_t dw[3] = {r, C, n}, sw[2] = {r * 2, r * C * 2}, dof[3] = {O, r, n}, so[2] = {O * 2, r * O * 2};
     const uint32_t bw[3] = {64, kChunk, 1}, bo[3] = {64, (uint32_t)rrows, 1};
@@ -1035,10 +1144,12 @@ situ_status launch_tiles(int dtype, bool f32, const void* rows, int64_t ld_rows,
   const uint32_t by[2] = {(uint32_t)cols / 2, kTile};
   const CUtensorMapDataType ot = f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : dt;
   ok = ok && make_map_nd(&m.out, ot, x.out, 2, dy, syo, by);
-  m.base = m.out;
+  m.base = m.base1 = m.out;
   if (x.base) {
     const uint64_t syb[1] = {(uint64_t)x.ld_base * el};
+    const uint32_t by1[2] = {(uint32_t)cols / 2, 1};
     ok = ok && make_map_nd(&m.base, ot, x.base, 2, dy, syb, by);
+    if (s.mixed) ok = ok && make_map_nd(&m.base1, ot, x.base, 2, dy, syb, by1);
   }
   if (!ok) return SITU_ERR_CUDA;
   constexpr int kB = SITU_DT_BF16, kF = SITU_DT_F16;
@@ -1047,10 +1158,19 @@ situ_status launch_tiles(int dtype, bool f32, const void* rows, int64_t ld_rows,
   return e == cudaSuccess ? SITU_OK : SITU_ERR_CUDA;
 }
 
-// A cluster per row, or tiles.
-bool by_rows(int S) { return S <= 64; }
+// A cluster per row, or tiles.  A row's cluster reads its adapter, about 0.07 us a
+// row at rank 16 (3584 x 6144, four times that at rank 64), whatever the others
+// take; tiles take 15 us or more, and share one adapter's weights but go through
+// each of several: 512 rows at rank 16 of one adapter 37 us by rows and 19 in tiles,
+// of 16 in any order 37 and 48, 128 rows of 16 at rank 64 48 and 57.
+bool by_rows(int S, int r, int n) { return S <= 64 || (long)S * r <= 512l * (n < 16 ? n : 16); }
+// Whether rows named by ids may be sorted by adapter first: the look at them and
+// the sorting cost 8 to 17 us, which few adapters in any order hardly do.
+bool sortable(const int32_t* ids, int n) { return ids && n > 16 && n <= SITU_MAX_LOCAL_EXPERTS; }
+// its scratch: *mixed; numbers, places; counts, offsets, the permute's own
+size_t sort_ints(int S, int n) { return 1 + 2 * (size_t)S + 2 * (size_t)n + 1 + permute_scratch_bytes(S, 1, n) / 4; }
 
-size_t part_bytes(int S, int C, int r) { return S == 0 ? 0 : (size_t)most_parts(S, C) * S * r * 4; }
+size_t part_bytes(int S, int C, int r) { return S == 0 ? 0 : (size_t)Shares(S, C).most * S * r * 4; }
 
 // of the backward pass: first the parts of v, then those of the gradients
 size_t shared_bytes(int S, int N, int r) {
@@ -1067,10 +1187,10 @@ bool bad_sizes(int S, int K, int N, int r, int n) {
 }  // namespace
 }  // namespace situ
 
-extern "C" size_t situ_moe_lora_workspace_size(int32_t S, int32_t K, int32_t N, int32_t r) {
+extern "C" size_t situ_moe_lora_workspace_size(int32_t S, int32_t K, int32_t N, int32_t r, int32_t n) {
   using namespace situ;
-  if (bad_sizes(S, K, N, r, 1)) return 0;
-  return S == 0 || by_rows(S) ? 0 : part_bytes(S, K, r);
+  if (bad_sizes(S, K, N, r, n) || S == 0 || by_rows(S, r, n)) return 0;
+  return part_bytes(S, K, r) + (n > 16 && n <= SITU_MAX_LOCAL_EXPERTS ? (sort_ints(S, n) * 4 + 31) / 32 * 32 : 0);
 }
 
 extern "C" situ_status situ_moe_lora(const situ_lora_args* a, void* workspace, size_t workspace_bytes, void* stream) {
@@ -1088,7 +1208,7 @@ extern "C" situ_status situ_moe_lora(const situ_lora_args* a, void* workspace, s
       bad(a->ids, 3) || bad(a->offsets, 3) || bad(a->scale, 3))
     return SITU_ERR_MISALIGNED;
   cudaStream_t st = (cudaStream_t)stream;
-  if (by_rows(a->S)) {
+  if (by_rows(a->S, a->r, a->n)) {
     RowParams p;
     p.x = a->x;
     p.a = a->a;
@@ -1116,7 +1236,7 @@ extern "C" situ_status situ_moe_lora(const situ_lora_args* a, void* workspace, s
   }
   if (!workspace || !a->device_status) return SITU_ERR_NULL_ARG;
   if (bad(workspace, 31) || bad(a->device_status, 3)) return SITU_ERR_MISALIGNED;
-  if (workspace_bytes < part_bytes(a->S, a->K, a->r)) return SITU_ERR_WORKSPACE_TOO_SMALL;
+  if (workspace_bytes < situ_moe_lora_workspace_size(a->S, a->K, a->N, a->r, a->n)) return SITU_ERR_WORKSPACE_TOO_SMALL;
   LoraParams s = {};
   s.ids = a->ids;
   s.offsets = a->offsets;
@@ -1126,6 +1246,20 @@ extern "C" situ_status situ_moe_lora(const situ_lora_args* a, void* workspace, s
   s.part = static_cast<float*>(workspace);
   s.scale = a->scale;
   s.err = a->device_status;
+  if (sortable(a->ids, a->n)) {
+    int32_t* mixed = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + part_bytes(a->S, a->K, a->r));
+    int32_t *perm = mixed + 1, *place = perm + a->S, *counts = place + a->S, *offsets = counts + a->n,
+            *scratch = offsets + a->n + 1;
+    mixed_kernel<<<1, 1024, 0, st>>>(a->ids, a->S, a->n, mixed);
+    if (cudaGetLastError() != cudaSuccess ||
+        launch_permute(a->ids, a->S, 1, a->n, 0, 1, counts, offsets, nullptr, nullptr, perm, place, nullptr, scratch, st) !=
+            cudaSuccess)
+      return SITU_ERR_CUDA;
+    s.mixed = mixed;
+    s.perm = perm;
+    s.place = place;
+    s.kept = offsets + a->n;
+  }
   LoraParams x = s;
   s.C = a->K;
   x.C = a->N;

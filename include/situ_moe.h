@@ -770,7 +770,7 @@ typedef struct situ_lora_args {
   int32_t* device_status;         /* as for the expert products */
 } situ_lora_args;
 /* of the current device; 0 for few rows, which take none (and for bad arguments) */
-size_t situ_moe_lora_workspace_size(int32_t S, int32_t K, int32_t N, int32_t r);
+size_t situ_moe_lora_workspace_size(int32_t S, int32_t K, int32_t N, int32_t r, int32_t n);
 situ_status situ_moe_lora(const situ_lora_args* args, void* workspace, size_t workspace_bytes, void* stream);
 
 /* situ_moe_lora_backward -- from dy [S, N] and the forward's u, rows sorted by

@@ -119,7 +119,7 @@ def test_restore_refusals(lib, args, status):
 
 
 def lora(lib, ws=0xf000, nbytes=1 << 30, **over):
-    a = dict(dtype=0, out_dtype=0, S=100, K=64, N=128, r=16, n=4, x=0x1000, ldx=64, a=0x2000, b=0x3000, ids=0x4000,
+    a = dict(dtype=0, out_dtype=0, S=200, K=64, N=128, r=16, n=4, x=0x1000, ldx=64, a=0x2000, b=0x3000, ids=0x4000,
              offsets=None, scale=None, base=0x5000, ld_base=128, out=0x6000, ldo=128, u=None, device_status=0xd000)
     a.update(over)
     return lib.situ_moe_lora(ctypes.byref(B.SituLoraArgs(**a)), ws, nbytes, None)
@@ -163,10 +163,10 @@ def test_null_args_and_sizes(lib):
     for f in (lib.situ_moe_router_backward, lib.situ_moe_gated, lib.situ_moe_gated_backward):
         assert f(None, None) == 1
     assert lib.situ_moe_balance_loss_workspace_size(-1, 8) == 0 and lib.situ_moe_balance_loss_workspace_size(8, 5000) == 0
-    assert lib.situ_moe_lora_workspace_size(8, 64, 64, 12) == 0 and lib.situ_moe_lora_backward_workspace_size(8, 60, 64, 8) == 0
-    assert lib.situ_moe_balance_loss_workspace_size(4000, 8) > 0 and lib.situ_moe_lora_workspace_size(100, 64, 64, 8) > 0
+    assert lib.situ_moe_lora_workspace_size(8, 64, 64, 12, 1) == 0 and lib.situ_moe_lora_backward_workspace_size(8, 60, 64, 8) == 0
+    assert lib.situ_moe_balance_loss_workspace_size(4000, 8) > 0 and lib.situ_moe_lora_workspace_size(100, 64, 64, 8, 1) > 0
     # few tokens or rows take none
-    assert lib.situ_moe_balance_loss_workspace_size(10, 8) == 0 and lib.situ_moe_lora_workspace_size(8, 64, 64, 8) == 0
+    assert lib.situ_moe_balance_loss_workspace_size(10, 8) == 0 and lib.situ_moe_lora_workspace_size(8, 64, 64, 8, 1) == 0
 
 
 def test_binding_refuses_host_tensors_and_wrong_types():

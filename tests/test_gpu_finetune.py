@@ -531,7 +531,7 @@ def lora_bar(y, both, second, K, r, dtype, out_dtype, rows):
 @pytest.mark.parametrize("S,K,N,r,n", [(1, 8, 8, 8, 1), (1, 3584, 768, 16, 3), (5, 264, 1000, 24, 2), (33, 72, 136, 128, 40),
                                        (64, 128, 64, 40, 7), (65, 64, 128, 8, 2), (130, 200, 264, 16, 3), (300, 1032, 72, 32, 300),
                                        (700, 136, 1160, 48, 4), (1000, 520, 520, 64, 11), (257, 2048, 392, 128, 5),
-                                       (2100, 64, 64, 104, 1)])
+                                       (2100, 64, 64, 104, 1), (3000, 136, 200, 24, 40), (2049, 520, 1032, 16, 700)])
 @pytest.mark.parametrize("dtype,out_dtype", [(BF16, BF16), (F16, F16), (BF16, F32), (F16, F32)])
 @pytest.mark.parametrize("order", ["mixed", "runs"])
 def test_lora(S, K, N, r, n, dtype, out_dtype, order):
@@ -577,11 +577,11 @@ def test_lora_rows_by_offsets(S, dtype):
     assert torch.equal(B.situ_moe_lora(c["base"], c["x"], c["a"], c["b"], offsets=off, scale=c["scale"]), want)
 
 
-@pytest.mark.parametrize("S", [50, 400])
-def test_lora_rows_do_not_touch_each_other(S):
+@pytest.mark.parametrize("S,n", [(50, 5), (400, 5), (1500, 20)])
+def test_lora_rows_do_not_touch_each_other(S, n):
     # an adapter of NaN and infinities, and rows of them, in the same tiles as others
     g = gen(S)
-    n, K, N, r = 5, 136, 264, 24
+    K, N, r = 136, 264, 24
     c = lora_case(g, S, K, N, r, n, BF16, BF16)
     ids = torch.randint(0, n, (S,), generator=g, device="cuda").int()
     want = B.situ_moe_lora(c["base"], c["x"], c["a"], c["b"], ids=ids)
