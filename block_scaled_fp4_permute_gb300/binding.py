@@ -1181,7 +1181,8 @@ def situ_moe_lora(base, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, *, id
     projection of x [S, K] (None: zeros, of x's type), a [n, r, K] and b
     [n, N, r], e = ids[i] (int32 [S]; outside [0, n): no adapter) or the one
     whose rows ``offsets`` [n + 1] bounds.  ``out`` may be base.  ``keep``
-    returns (out, u [S, r]) for situ_moe_lora_backward."""
+    returns (out, u [S, 2, r], rounded and what that leaves) for
+    situ_moe_lora_backward."""
     if stream is not None:
         return _on_stream(stream, lambda x, a, b, base, **kw: situ_moe_lora(base, x, a, b, **kw), x, a, b, base, ids=ids,
                           offsets=offsets, scale=scale, out=out, keep=keep)
@@ -1208,7 +1209,7 @@ def situ_moe_lora(base, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, *, id
         out, ldo = _empty((S, N), (N, 1), out_dtype, index), N
     else:
         ldo = _given(out, (S, N), out_dtype, index, 4 if out_dtype is torch.float32 else 8)
-    u = _empty((S, r), (r, 1), dtype, index) if keep else None
+    u = _empty((S, 2, r), (2 * r, r, 1), dtype, index) if keep else None
     size = _lora_bytes(S, K, N, r, n, index)
     ws, pws = _scratch(size, index)
     args = SituLoraArgs(_DTYPES[dtype], _DTYPES.get(out_dtype, -1), S, K, N, r, n, px, ldx, a.data_ptr(), b.data_ptr(), pids,
@@ -1231,8 +1232,8 @@ def situ_moe_lora_backward(dy: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b
     dtype = x.dtype
     if dy.dtype is not dtype or u.dtype is not dtype:
         raise TypeError(f"dy and u must be {dtype}, as x")
-    if dy.shape != (S, N) or u.shape != (S, r):
-        raise ValueError(f"needs dy {(S, N)} and u {(S, r)}")
+    if dy.shape != (S, N) or u.shape != (S, 2, r):
+        raise ValueError(f"needs dy {(S, N)} and u {(S, 2, r)}")
     _on_device(index, dy=dy, u=u)
     if _groups(offsets, index) != n:
         raise ValueError(f"offsets must be [{n + 1}]")

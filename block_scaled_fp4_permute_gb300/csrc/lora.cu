@@ -63,7 +63,7 @@ struct LoraParams {
   long ld_base;
   void* out;
   long ldo;
-  void* u16;                       // [S, r] scaled, of the operands' type, or null
+  void* u16;                       // [S, 2, r] scaled, in two terms of the operands' type, or null
   int stages, w_stage;             // shared memory: stages of w, bytes of one
   int x_stages;                    // shrink: of x
   int y_stages, u_bytes;           // expand: items of base, bytes of u
@@ -179,9 +179,13 @@ lora_row_kernel(RowParams p) {
     }
   }
   cluster.sync();
-  if (p.u16 && rank == 0 && (int)threadIdx.x < p.r)
-    static_cast<uint16_t*>(p.u16)[(size_t)row * p.r + threadIdx.x] =
-        e >= 0 ? (uint16_t)pack16<DT>(u_s[threadIdx.x], 0.f) : (uint16_t)0;
+  if (p.u16 && rank == 0 && (int)threadIdx.x < p.r) {
+    uint32_t hi = 0, lo = 0;
+    if (e >= 0) two_terms<DT>(u_s[threadIdx.x], 0.f, hi, lo);
+    uint16_t* o = static_cast<uint16_t*>(p.u16) + (size_t)row * 2 * p.r + threadIdx.x;
+    o[0] = (uint16_t)hi;
+    o[p.r] = (uint16_t)lo;
+  }
   const float* base32 = static_cast<const float*>(p.base);
   const uint16_t* base16 = static_cast<const uint16_t*>(p.base);
   for (int c = threadIdx.x; c < c1 - c0; c += kRowThreads) {
@@ -239,12 +243,6 @@ struct Rows {
       : perm(p.mixed && __ldcg(p.mixed) ? p.perm : nullptr), S(p.S), count(perm ? __ldcg(p.kept) : p.S) {}
   __device__ __forceinline__ int row(int i) const { return i >= count ? S : perm ? __ldcg(perm + i) : i; }
 };
-// CTAs that have a share of the shrink's `total` chunks: fewer where sorting has
-// left rows out, so that a tile still comes in no more parts than there is room for.
-__device__ __forceinline__ long sharers(const LoraParams& p, long total) {
-  const long g = total / p.least;
-  return g < 1 ? 1 : g < p.shrink_ctas ? g : p.shrink_ctas;
-}
 // by the epilogue threads, of which this is number i
 template <int R>
 __device__ __forceinline__ void find_adapters(Adapters<R>& t, const LoraParams& p, const Rows& rows, int row0, int i) {
@@ -375,7 +373,7 @@ shrink_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
   auto list_empty = [&](int b) { return tail + 48 + 8 * b; };
   const uint32_t drain = tail + 64;
   const Rows rows(p);
-  const long total = (long)((rows.count + kShrinkRows - 1) / kShrinkRows) * p.chunks, G = sharers(p, total);
+  const long total = (long)((rows.count + kShrinkRows - 1) / kShrinkRows) * p.chunks, G = sharers(total, p.shrink_ctas, p.least);
   const bool shares = blockIdx.x < G;
   const long i0 = shares ? first_item(blockIdx.x, total, G) : 0, i1 = shares ? first_item(blockIdx.x + 1, total, G) : 0;
   if (tid == 0) {
@@ -578,8 +576,14 @@ shrink_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
               tmem_ld_wait<16>(v);
               if (at == d) {
 #pragma unroll
-                for (int t = 0; t < 16; t += 8)
-                  if (j + t < p.r) put8(out + j + t, v + t, from > g.from);
+                for (int t = 0; t < 16; t += 8) {
+                  if (j + t >= p.r) break;
+                  float f[8];
+#pragma unroll
+                  for (int i = 0; i < 8; ++i)
+                    f[i] = __uint_as_float(v[t + i]) + (from > g.from ? out[j + t + i] : 0.f);   // onto the run before
+                  put8(out + j + t, f);
+                }
               }
               __syncwarp();
             }
@@ -818,8 +822,8 @@ expand_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
         if (p.out != p.base)
           for (int i = lane; i < p.C / (16 / kEl); i += 32) out[i] = p.base ? base[i] : make_uint4(0, 0, 0, 0);
         if (p.u16)
-          for (int i = lane; i < p.r / 8; i += 32)
-            reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.u16) + (size_t)row * p.r)[i] = make_uint4(0, 0, 0, 0);
+          for (int i = lane; i < p.r / 4; i += 32)
+            reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.u16) + (size_t)row * 2 * p.r)[i] = make_uint4(0, 0, 0, 0);
       }
     }
   } else if (warp >= 4 && !dead) {
@@ -840,7 +844,7 @@ expand_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
       const bool write = p.u16 && g.from == 0 && row < p.S;
       const long t0 = (long)(g.tile / (kShrinkRows / kTile)) * p.chunks;
       const long all = (long)((rows.count + kShrinkRows - 1) / kShrinkRows) * p.chunks;
-      const long sharing = sharers(p, all);
+      const long sharing = sharers(all, p.shrink_ctas, p.least);
       const int parts = (int)(cta_of(t0 + p.chunks - 1, all, sharing) - cta_of(t0, all, sharing)) + 1;
       auto sum8 = [&](int j, float (&u)[8]) {
 #pragma unroll
@@ -881,9 +885,15 @@ expand_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
       for (int j = 8 * (et & 1); j < p.r16; j += 16) {
         float u[8];
         sum8(j, u);
-        if (write && j < p.r)
-          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.u16) + (size_t)row * p.r + j) =
-              make_uint4(pack16<DT>(u[0], u[1]), pack16<DT>(u[2], u[3]), pack16<DT>(u[4], u[5]), pack16<DT>(u[6], u[7]));
+        if (write && j < p.r) {
+          uint4 *o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.u16) + (size_t)row * 2 * p.r + j), hi, lo;
+          two_terms<DT>(u[0], u[1], hi.x, lo.x);
+          two_terms<DT>(u[2], u[3], hi.y, lo.y);
+          two_terms<DT>(u[4], u[5], hi.z, lo.z);
+          two_terms<DT>(u[6], u[7], hi.w, lo.w);
+          o[0] = hi;
+          o[p.r / 8] = lo;
+        }
 #pragma unroll
         for (int t = 0; t < kTerms; ++t) {
           uint32_t v[4];
@@ -1013,21 +1023,9 @@ expand_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
 // launches
 // --------------------------------------------------------------------------
 
-// How the shrink's chunks are dealt out: one CTA per SM, of at least two chunks;
-// `most`: parts that a tile's chunks can come in.
-struct Shares {
-  long ctas, least, most;
-  Shares(int S, int C) {
-    const long tiles = (S + kShrinkRows - 1) / kShrinkRows, chunks = (C + kChunk - 1) / kChunk, total = tiles * chunks;
-    const long sms = sm_count();
-    ctas = total / 2 < sms ? total / 2 : sms;
-    if (ctas < 1) ctas = 1;
-    least = total / ctas;
-    if (least < 1) least = 1;
-    most = (chunks + least - 2) / least + 1;
-    if (most > chunks) most = chunks;
-  }
-};
+Shares shares_of(int S, int C) {
+  return Shares((S + kShrinkRows - 1) / kShrinkRows, (C + kChunk - 1) / kChunk, sm_count());
+}
 
 struct Maps {
   CUtensorMap x, x1, w, other, base, base1, out;   // x1, base1: row by row, for sorted rows
@@ -1114,7 +1112,7 @@ situ_status launch_tiles(int dtype, bool f32, const void* rows, int64_t ld_rows,
   const uint64_t S = (uint64_t)s.S, C = (uint64_t)s.C, O = (uint64_t)x.C, r = (uint64_t)s.r, n = (uint64_t)s.n;
   s.r16 = x.r16 = (s.r + 15) / 16 * 16;
   s.chunks = (s.C + kChunk - 1) / kChunk;
-  const Shares shares(s.S, s.C);
+  const Shares shares = shares_of(s.S, s.C);
   s.shrink_ctas = x.shrink_ctas = shares.ctas;
   s.least = x.least = shares.least;
   s.run = f32 ? 1024 / kChunk : s.chunks;
@@ -1170,7 +1168,7 @@ bool sortable(const int32_t* ids, int n) { return ids && n > 16 && n <= SITU_MAX
 // its scratch: *mixed; numbers, places; counts, offsets, the permute's own
 size_t sort_ints(int S, int n) { return 1 + 2 * (size_t)S + 2 * (size_t)n + 1 + permute_scratch_bytes(S, 1, n) / 4; }
 
-size_t part_bytes(int S, int C, int r) { return S == 0 ? 0 : (size_t)Shares(S, C).most * S * r * 4; }
+size_t part_bytes(int S, int C, int r) { return S == 0 ? 0 : (size_t)shares_of(S, C).most * S * r * 4; }
 
 // of the backward pass: first the parts of v, then those of the gradients
 size_t shared_bytes(int S, int N, int r) {
@@ -1274,7 +1272,7 @@ extern "C" situ_status situ_moe_lora(const situ_lora_args* a, void* workspace, s
 extern "C" size_t situ_moe_lora_backward_workspace_size(int32_t S, int32_t K, int32_t N, int32_t r) {
   using namespace situ;
   if (bad_sizes(S, K, N, r, 1)) return 0;
-  return shared_bytes(S, N, r) + ((size_t)S * r * 2 + 15) / 16 * 16 + 16;
+  return shared_bytes(S, N, r) + (size_t)S * r * 4 + 16;
 }
 
 extern "C" situ_status situ_moe_lora_backward(const situ_lora_backward_args* a, void* workspace, size_t workspace_bytes,
@@ -1335,30 +1333,8 @@ extern "C" situ_status situ_moe_lora_backward(const situ_lora_backward_args* a, 
   o.db = a->db;
   o.parts = static_cast<float*>(workspace);             // u's parts have been read
   o.err = a->device_status;
-  if (a->S > 0 && outer_takes(a->dtype, a->S, a->K, a->N)) return launch_outer(o, (cudaStream_t)stream);
-  // over an adapter's rows: dA = v^T x, dB = dy^T u
-  situ_grouped_gemm_args g = {};
-  g.direction = SITU_GROUPED_WGRAD;
-  g.dtype = g.out_dtype = a->dtype;
-  g.S = a->S;
-  g.E = a->n;
-  g.offsets = a->offsets;
-  g.device_status = a->device_status;
-  g.a = v;
-  g.lda = g.N = a->r;
-  g.b = a->x;
-  g.ldb = a->ldx;
-  g.K = a->K;
-  g.out = a->da;
-  g.ldo = a->K;
-  const situ_status st = situ_moe_grouped_gemm(&g, stream);
-  if (st != SITU_OK) return st;
-  g.a = a->dy;
-  g.lda = a->ld_dy;
-  g.N = a->N;
-  g.b = a->u;
-  g.ldb = g.K = a->r;
-  g.out = a->db;
-  g.ldo = a->r;
-  return situ_moe_grouped_gemm(&g, stream);
+  if (a->S > 0) return launch_outer(o, (cudaStream_t)stream);
+  const bool zero = cudaMemsetAsync(a->da, 0, (size_t)a->n * a->r * a->K * 2, (cudaStream_t)stream) == cudaSuccess &&
+                    cudaMemsetAsync(a->db, 0, (size_t)a->n * a->N * a->r * 2, (cudaStream_t)stream) == cudaSuccess;
+  return zero ? SITU_OK : SITU_ERR_CUDA;
 }

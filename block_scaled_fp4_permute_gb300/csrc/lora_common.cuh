@@ -54,22 +54,29 @@ __device__ __forceinline__ uint32_t idesc_of(bool bf16, bool trans_a, bool trans
 // item i is CTA ((i + 1) G - 1) / T's.
 __host__ __device__ __forceinline__ long first_item(long c, long T, long G) { return c * T / G; }
 __host__ __device__ __forceinline__ long cta_of(long i, long T, long G) { return ((i + 1) * G - 1) / T; }
-// eight sums to memory, a whole sector a lane; add: to what is there
-__device__ __forceinline__ void put8(float* o, const uint32_t* v, bool add) {
-  float f[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[i]);
-  if (add) {
-    const float4 a = *reinterpret_cast<const float4*>(o), b = *reinterpret_cast<const float4*>(o + 4);
-    f[0] += a.x;
-    f[1] += a.y;
-    f[2] += a.z;
-    f[3] += a.w;
-    f[4] += b.x;
-    f[5] += b.y;
-    f[6] += b.z;
-    f[7] += b.w;
+// How a product's chunks (`chunks` to each of `tiles`) are dealt out: one CTA per
+// SM, of at least two chunks; `most`: the parts that a tile can come in.
+struct Shares {
+  long ctas, least, most;
+  Shares(long tiles, long chunks, long sms) {
+    const long total = tiles * chunks;
+    ctas = total / 2 < sms ? total / 2 : sms;
+    if (ctas < 1) ctas = 1;
+    least = total / ctas;
+    if (least < 1) least = 1;
+    most = (chunks + least - 2) / least + 1;
+    if (most > chunks) most = chunks;
   }
+};
+// The CTAs that have a share where only `total` chunks are left (rows without an
+// adapter sorted out): fewer, so that a tile still comes in no more parts.
+__host__ __device__ __forceinline__ long sharers(long total, long ctas, long least) {
+  const long g = total / least;
+  return g < 1 ? 1 : g < ctas ? g : ctas;
+}
+
+// eight sums to memory, a whole sector a lane
+__device__ __forceinline__ void put8(float* o, const float* f) {
   asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(o), "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]),
                "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7])
                : "memory");
@@ -79,8 +86,18 @@ inline bool bad(const void* q, uintptr_t mask) { return (reinterpret_cast<uintpt
 // the tensor maps take strides below 2^40 bytes
 inline bool bad_ld(int64_t ld, int64_t cols, int64_t unit) { return ld < cols || ld % unit != 0 || ld >= (int64_t)1 << 38; }
 
+// u or v of a row is kept in two terms of the operands' type, [2][r]: rounded, and
+// what that leaves (an infinity leaves nothing), together 16 bits of it in bf16 and
+// 22 in f16.
+template <int DT>
+__device__ __forceinline__ void two_terms(float a, float b, uint32_t& hi, uint32_t& lo) {
+  hi = pack16<DT>(a, b);
+  const float x = lo16<DT>(hi), y = hi16<DT>(hi);
+  lo = pack16<DT>(fabsf(x) < INFINITY ? a - x : 0.f, fabsf(y) < INFINITY ? b - y : 0.f);
+}
+
 // da [n, r, K] = v^T x and db [n, N, r] = dy^T u over each adapter's rows, v and
-// u [S, r] of the operands' type.  parts: outer_bytes(r) of scratch.
+// u [S, 2, r] in two terms.  parts: outer_bytes(r) of scratch.
 struct OuterArgs {
   int dtype, S, K, N, r, n;
   const void *x, *dy, *v, *u;
@@ -91,7 +108,6 @@ struct OuterArgs {
   int32_t* err;
 };
 size_t outer_bytes(int r);
-bool outer_takes(int dtype, int S, int K, int N);   // else the sums are too long for one in tensor memory
 situ_status launch_outer(const OuterArgs& a, cudaStream_t st);
 
 }  // namespace lora

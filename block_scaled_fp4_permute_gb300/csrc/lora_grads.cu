@@ -3,13 +3,16 @@
 //   dA[e][j][k] = sum_{rows i of e} v[i, j] x[i, k],   dB[e][n][j] = sum dy[i, n] u[i, j]
 //
 // Both are one form: 128 columns of a wide operand (x or dy) on the MMA's M side,
-// the r columns of a narrow one on its N side, rows along the contraction (both
-// operands MN-major).  Bound by the bytes of x and dy: r operations a byte.  The
+// the columns of a narrow one on its N side, rows along the contraction (both
+// operands MN-major).  u and v come in two 16-bit terms, side by side on the N side:
+// rounded to one, the gradients would be off by as much again as their own
+// rounding.  Bound by the bytes of x and dy: r operations a byte.  The
 // general products over groups (situ_moe_grouped_gemm) give whole tiles to CTAs, and
 // four adapters of 3584 x 6144 make 56 and 96 tiles for 152 SMs.  Here the
 // chunks of 64 rows of all tiles of both gradients are dealt out evenly over one CTA
 // per SM; tiles that part between CTAs leave fp32 sums, which a second kernel
-// adds in order (16,384 rows, rank 64: 93 us as two general products, 61 so).
+// adds in order (16,384 rows, rank 64: 93 us as two general products of single
+// terms, 72 so, at 4.4 TB/s).
 //
 // A tile's last chunk has fewer than 64 rows: it comes row by row (four an
 // instruction), rows past the adapter's end named out of bounds, so that the MMA
@@ -29,11 +32,11 @@ constexpr int kSmem = 212 * 1024;        // 227 KB with the scan and the static 
 
 struct OuterParams {
   const int32_t* offsets;
-  int S, n, r, r16;
+  int S, n, r;
   int C[2], blocks[2];                   // of x and dy: columns, tiles of 128
   void* out[2];                          // da, db
   float* parts;                          // [CTA][2][128][r]
-  int stages;
+  int stages, run;                       // run: chunks of a sum in tensor memory
   int* err;
 };
 // wide and narrow operand of each gradient, by 64 rows and by single ones
@@ -110,7 +113,7 @@ outer_kernel(const __grid_constant__ OuterMaps m, const OuterParams p) {
     mbar_init(drain, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 1) tmem_alloc<1>(saddr(holder), 256);
+  if (warp == 1) tmem_alloc<1>(saddr(holder), 512);
   scan_tiles(p.offsets, p.n, p.S, kRows, scan, scan + kMaxGroups + 1, kThreads);
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
@@ -119,7 +122,7 @@ outer_kernel(const __grid_constant__ OuterMaps m, const OuterParams p) {
   const bool dead = holder[1] != 0;
   const Deal deal(p, scan, scan + kMaxGroups + 1);
   const long i0 = first_item(blockIdx.x, deal.total, gridDim.x), i1 = first_item(blockIdx.x + 1, deal.total, gridDim.x);
-  const int nboxes = (p.r + 63) / 64, stage = kWide + nboxes * kRows * 128;
+  const int nboxes = (2 * p.r + 63) / 64, stage = kWide + nboxes * kRows * 128;
 
   if (warp == 0 && !dead) {
     // ---------------- copies ----------------
@@ -167,36 +170,40 @@ outer_kernel(const __grid_constant__ OuterMaps m, const OuterParams p) {
   } else if (warp == 1 && !dead) {
     // ---------------- MMAs ----------------
     const bool leader = elect_one();
-    const uint32_t idesc = idesc_of(DT == SITU_DT_BF16, true, true, p.r16);
+    const uint32_t idesc = idesc_of(DT == SITU_DT_BF16, true, true, 2 * p.r);
     Turns r(p.stages), acc(2);
     bool ok = true;
     for (long i = i0; i < i1 && ok;) {
       const Piece t = deal.at(i, i1);
       i += t.to - t.from;
-      if (acc.again() && !warp_wait(acc_empty(acc.s), acc.ph ^ 1, p.err, 123)) {
-        ok = false;
-        break;
-      }
-      for (int k = t.from; k < t.to; ++k, r.next()) {
-        if (!warp_wait(full(r.s), r.ph, p.err, 124)) {
+      for (int from = t.from; from < t.to && ok; from += p.run) {
+        const int to = min(t.to, from + p.run);
+        if (acc.again() && !warp_wait(acc_empty(acc.s), acc.ph ^ 1, p.err, 123)) {
           ok = false;
           break;
         }
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        if (leader) {
-          const uint32_t a = sbase + r.s * stage;
-          const int steps = min(kRows / 16, (t.rows - k * kRows + 15) / 16);
-          for (int j = 0; j < steps; ++j)
-            mma_f16<1>(tmem + acc.s * 128, sdesc_mn(a, kRows * 128) + 128 * j, sdesc_mn(a + kWide, kRows * 128) + 128 * j, idesc,
-                       ((k - t.from) | j) != 0);
-          mma_commit(empty(r.s));
+        for (int k = from; k < to; ++k, r.next()) {
+          if (!warp_wait(full(r.s), r.ph, p.err, 124)) {
+            ok = false;
+            break;
+          }
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          if (leader) {
+            const uint32_t a = sbase + r.s * stage;
+            const int steps = min(kRows / 16, (t.rows - k * kRows + 15) / 16);
+            for (int j = 0; j < steps; ++j)
+              mma_f16<1>(tmem + acc.s * 256, sdesc_mn(a, kRows * 128) + 128 * j, sdesc_mn(a + kWide, kRows * 128) + 128 * j, idesc,
+                         ((k - from) | j) != 0);
+            mma_commit(empty(r.s));
+          }
+          __syncwarp();
         }
-        __syncwarp();
-      }
-      if (ok) {
-        if (leader) mma_commit(acc_full(acc.s));
-        __syncwarp();
-        acc.next();
+        if (ok) {
+          if (leader) mma_commit(acc_full(acc.s));
+          __syncwarp();
+          acc.next();
+        }
       }
     }
     leave(
@@ -219,28 +226,42 @@ outer_kernel(const __grid_constant__ OuterMaps m, const OuterParams p) {
       }
     }
     Turns acc(2);
-    for (long i = i0; i < i1; acc.next()) {
+    bool ok = true;
+    for (long i = i0; i < i1 && ok;) {
       const Piece t = deal.at(i, i1);
       i += t.to - t.from;
-      if (!warp_wait(acc_full(acc.s), acc.ph, p.err, 126)) break;
-      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const int c = t.block * 128 + 32 * q + lane;
       float* part = p.parts + (((size_t)blockIdx.x * 2 + (t.from == 0)) * 128 + 32 * q + lane) * p.r;
-      for (int j = 0; j < p.r16; j += 16) {
-        uint32_t v[16];
-        __syncwarp();
-        tmem_ld16_nowait(tmem + ((uint32_t)(32 * q) << 16) + acc.s * 128 + j, v);
-        tmem_ld_wait<16>(v);
-#pragma unroll
-        for (int k = 0; k < 16; k += 8) {
-          if (c >= p.C[t.which] || j + k >= p.r) continue;
-          if (t.whole()) store16<DT>(p, t, c, j + k, reinterpret_cast<const float*>(v + k));
-          else put8(part + j + k, v + k, false);
+      for (int from = t.from; from < t.to && ok; from += p.run, acc.next()) {
+        if (!warp_wait(acc_full(acc.s), acc.ph, p.err, 126)) {
+          ok = false;
+          break;
         }
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const bool earlier = from > t.from, last = from + p.run >= t.to;   // sums of this piece are in `part`; these end it
+        const uint32_t sums = tmem + ((uint32_t)(32 * q) << 16) + acc.s * 256;
+        for (int j = 0; j < p.r; j += 8) {                // of the first term and of the second, from whole sixteens
+          uint32_t v[16], w[16];
+          __syncwarp();
+          tmem_ld16_nowait(sums + (j & ~15), v);
+          tmem_ld16_nowait(sums + ((p.r + j) & ~15), w);
+          tmem_ld_wait<16>(v);
+          tmem_ld_wait<16>(w);
+          if (c >= p.C[t.which]) continue;
+          const bool vh = j & 8, wh = (p.r + j) & 8;
+          float f[8];
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            f[x] = __uint_as_float(vh ? v[8 + x] : v[x]) + __uint_as_float(wh ? w[8 + x] : w[x]);
+            if (earlier) f[x] += part[j + x];
+          }
+          if (last && t.whole()) store16<DT>(p, t, c, j, f);
+          else put8(part + j, f);
+        }
+        __syncwarp();
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+        mbar_arrive_if(acc_empty(acc.s), lane == 0);
       }
-      __syncwarp();
-      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-      mbar_arrive_if(acc_empty(acc.s), lane == 0);
     }
   }
   griddep_launch_dependents();
@@ -249,7 +270,7 @@ outer_kernel(const __grid_constant__ OuterMaps m, const OuterParams p) {
   if (warp == 1) {
     __syncwarp();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-    tmem_free<1>(tmem, 256);
+    tmem_free<1>(tmem, 512);
   }
 }
 
@@ -313,20 +334,15 @@ cudaError_t launch_dt(const OuterMaps& m, const OuterParams& p, int smem, cudaSt
 
 size_t outer_bytes(int r) { return (size_t)sm_count() * 2 * 128 * r * 4; }
 
-// The tensor cores truncate when they add, 6e-9 of a sum of one sign per element:
-// a tenth of a 16-bit result's last unit after 65,536 (bf16) and 8,192 (f16).
-bool outer_takes(int dtype, int S, int K, int N) {
-  const double rows = (double)S * ((K + 127) / 128 + (N + 127) / 128) / sm_count() + kRows;   // of a CTA
-  return (rows < S ? rows : S) <= (dtype == SITU_DT_BF16 ? 65536 : 8192);
-}
-
 situ_status launch_outer(const OuterArgs& a, cudaStream_t st) {
   OuterParams p = {};
   p.offsets = a.offsets;
   p.S = a.S;
   p.n = a.n;
   p.r = a.r;
-  p.r16 = (a.r + 15) / 16 * 16;
+  // The tensor cores truncate when they add, 6e-9 of a sum of one sign per element:
+  // a tenth of a 16-bit result's last unit after 65,536 (bf16) and 8,192 (f16).
+  p.run = (a.dtype == SITU_DT_BF16 ? 65536 : 8192) / kRows;
   p.C[0] = a.K;
   p.C[1] = a.N;
   p.blocks[0] = (a.K + 127) / 128;
@@ -335,7 +351,7 @@ situ_status launch_outer(const OuterArgs& a, cudaStream_t st) {
   p.out[1] = a.db;
   p.parts = a.parts;
   p.err = a.err;
-  const int stage = kWide + (a.r + 63) / 64 * kRows * 128;
+  const int stage = kWide + (2 * a.r + 63) / 64 * kRows * 128;
   p.stages = (kSmem - 1024) / stage;
   if (p.stages > kMaxStages) p.stages = kMaxStages;
   const CUtensorMapDataType dt = a.dtype == SITU_DT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
@@ -346,7 +362,7 @@ situ_status launch_outer(const OuterArgs& a, cudaStream_t st) {
   bool ok = true;
   for (int i = 0; i < 2 && ok; ++i) {
     const uint64_t dw[2] = {(uint64_t)p.C[i], (uint64_t)a.S}, sw[1] = {(uint64_t)ld[i] * 2};
-    const uint64_t dn[2] = {(uint64_t)a.r, (uint64_t)a.S}, sn[1] = {(uint64_t)a.r * 2};
+    const uint64_t dn[2] = {(uint64_t)a.r * 2, (uint64_t)a.S}, sn[1] = {(uint64_t)a.r * 4};
     ok = make_map_nd(&m.wide[i], dt, wide[i], 2, dw, sw, box) && make_map_nd(&m.wide1[i], dt, wide[i], 2, dw, sw, one) &&
          make_map_nd(&m.narrow[i], dt, narrow[i], 2, dn, sn, box) && make_map_nd(&m.narrow1[i], dt, narrow[i], 2, dn, sn, one);
   }

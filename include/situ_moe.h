@@ -613,7 +613,8 @@ situ_status situ_moe_fp8_gemm(const situ_fp8_gemm_args* args, void* stream);
  * gated activation with its input kept in 8 bits, and low-rank adapters.
  * These operators have no counterpart in the pages; adapters beside this layer
  * are what the FlashInfer 0.6.18 MoE-LoRA notes are about, without a
- * definition.  No kernel of theirs waits on another, so none has a status.
+ * definition.  The adapters' kernels bound their waits as the expert products' do
+ * and share their device_status.
  * --------------------------------------------------------------------- */
 
 /* situ_moe_balance_loss -- over the n tokens whose mask byte is not 0 (all with
@@ -743,8 +744,9 @@ situ_status situ_moe_gated_backward(const situ_gated_args* args, void* stream);
  * overlap it.  base and out are of one type, that of the operands or fp32.
  * Sums are fp32, out is rounded once; on more than a few rows u enters the
  * second product rounded to 16 bits for 16-bit results, with 22 bits or more
- * for fp32 ones.  u (or NULL) receives u [S, r] in the operands' type (zeros
- * without an adapter), which the gradients take.  For experts, an adapter per
+ * for fp32 ones.  u (or NULL) receives u [S, 2, r] in two terms of the operands'
+ * type, the first u rounded, the second what that leaves (zeros without an
+ * adapter), which the gradients take.  For experts, an adapter per
  * (request's adapter, expert) pair is one of n, its rows in any order.
  * Results do not depend on the order of execution, nor on what other rows'
  * adapters hold.  K, N multiples of 8, rows strided by multiples of 8 elements
@@ -766,7 +768,7 @@ typedef struct situ_lora_args {
   int64_t ld_base;
   void* out;                      /* [S, N], rows ldo apart */
   int64_t ldo;
-  void* u;                        /* [S, r], or NULL */
+  void* u;                        /* [S, 2, r], or NULL */
   int32_t* device_status;         /* as for the expert products */
 } situ_lora_args;
 /* of the current device; 0 for few rows, which take none (and for bad arguments) */
@@ -778,9 +780,9 @@ situ_status situ_moe_lora(const situ_lora_args* args, void* workspace, size_t wo
  *   v = scale dy b,  dx = dx0 + v a,  da[e] = v^T x,  db[e] = dy^T u   over e's rows
  * dx0 (or NULL: zeros) is the shared projection's gradient, dx may be it, both
  * of the operands' type or fp32; da [n, r, K] and db [n, N, r] are of the
- * operands' type, zeros for an adapter without rows, products of v and u
- * rounded to it.  The last two are situ_moe_grouped_gemm's, with its
- * device_status.  S == 0 sets da and db to zeros. */
+ * operands' type, rounded once, zeros for an adapter without rows (v is taken in
+ * two terms as u is).  Results do not depend on the order of execution.  S == 0
+ * sets da and db to zeros. */
 typedef struct situ_lora_backward_args {
   int32_t dtype, dx_dtype;
   int32_t S, K, N, r, n;
@@ -792,7 +794,7 @@ typedef struct situ_lora_backward_args {
   const void* b;
   const int32_t* offsets;
   const float* scale;
-  const void* u;                  /* [S, r] */
+  const void* u;                  /* [S, 2, r] */
   const void* dx0;
   int64_t ld_dx0;
   void* dx;

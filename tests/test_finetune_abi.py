@@ -180,7 +180,7 @@ def test_binding_refuses_host_tensors_and_wrong_types():
                  lambda: B.situ_moe_save_mxfp8(h), lambda: B.situ_moe_restore_mxfp8(u8, u8[:, :1]),
                  lambda: B.situ_moe_gated(h, one, one), lambda: B.situ_moe_gated_backward(h[:, :4], u8, u8[:, :2], one, one),
                  lambda: B.situ_moe_lora(None, h, ad, ad, offsets=off),
-                 lambda: B.situ_moe_lora_backward(h, h, ad, ad, off, h)):
+                 lambda: B.situ_moe_lora_backward(h, h, ad, ad, off, h[:, None])):
         with pytest.raises(ValueError, match="CUDA"):
             call()
     for call in (lambda: B.situ_moe_balance_loss(h, ids), lambda: B.situ_moe_balance_loss(f, ids.long()),
