@@ -449,8 +449,9 @@ def _status_word(index: int) -> torch.Tensor:
 
 def situ_moe_gemm_status(device=None, reset: bool = False) -> int:
     """0, or the code of the first bounded wait that a product
-    (situ_moe_grouped_gemm*, situ_moe_fp8*_gemm) on ``device`` gave up; until
-    it is reset the products there do no work.  Waits for the device."""
+    (situ_moe_grouped_gemm*, situ_moe_fp8*_gemm, situ_moe_lora*) on ``device``
+    gave up; until it is reset the products there do no work.  Waits for the
+    device."""
     device = torch.device("cuda" if device is None else device)
     index = torch.cuda.current_device() if device.index is None else device.index
     torch.cuda.synchronize(index)
@@ -795,8 +796,9 @@ def situ_moe_fp8_grouped_gemm(x_q: torch.Tensor, x_scale: torch.Tensor, w_q: tor
 # kept in 8 bits, low-rank adapters
 #
 # Streams, devices and copies are as for the expert products above.  None of
-# these calls waits for the host, except a first situ_moe_lora_backward on a
-# device (the products' status word).
+# these calls waits for the device, except a first situ_moe_lora or
+# situ_moe_lora_backward on it (the products' status word, which they share): that
+# does not belong inside a graph capture.
 # ---------------------------------------------------------------------------
 
 # workspace sizes of shapes already seen: a call into the library less
@@ -1107,7 +1109,7 @@ class _ExpertFfn(torch.autograd.Function):
     def forward(ctx, x, w1, w2, offsets, p0, p1, activation, keep):
         gate_up = situ_moe_grouped_gemm(x, w1, offsets)
         h, q, scale = situ_moe_gated(gate_up, p0, p1, offsets, activation=activation, save=True)
-        kept = situ_moe_save_mxfp8(x) if keep == "mxfp8" and ctx.needs_input_grad[1] else (x, None)
+        kept = (None, None) if not ctx.needs_input_grad[1] else situ_moe_save_mxfp8(x) if keep == "mxfp8" else (x, None)
         ctx.save_for_backward(*kept, q, scale, w1, w2, offsets, p0, p1)
         ctx.activation, ctx.dtype = activation, x.dtype
         return situ_moe_grouped_gemm(h, w2, offsets)
@@ -1274,13 +1276,15 @@ class _LoraLinear(torch.autograd.Function):
         dx = da = db = None
         if any(ctx.needs_input_grad[1:4]):
             dx, da, db = situ_moe_lora_backward(dy.to(x.dtype), x, a, b, offsets, u, scale=scale)
-        return dy, dx, da, db, None, None
+        return dy if ctx.needs_input_grad[0] else None, dx, da, db, None, None
 
 
 def lora_linear(base: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, offsets: torch.Tensor,
                 scale=None) -> torch.Tensor:
     """situ_moe_lora for training, rows sorted by adapter: differentiable in
-    base, x, a and b."""
+    base, x, a and b (up to 1,024 adapters)."""
+    if a.shape[0] > 1024:
+        raise ValueError("the gradients take up to 1024 adapters")
     return _LoraLinear.apply(base, x, a, b, offsets, scale)
 
 

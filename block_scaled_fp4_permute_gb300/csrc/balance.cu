@@ -16,8 +16,8 @@
 // same columns in every row, so the forward's column sums stay in registers too;
 // it issues the next row's loads before it works on the present one.  The
 // gradient's f_e are in shared memory, which leaves room for half as many rows
-// again.  Column sums are fp32 within a CTA (a few hundred rows) and two-sums of
-// fp32 across CTAs, in a fixed order: results do not depend on the order of
+// again.  Column sums are fp32, of 256 rows of a group and then of a CTA's groups, and
+// two-sums of fp32 across CTAs, in a fixed order: results do not depend on the order of
 // execution.
 // Measured (65,536 x 896, top-16): forward 43 us (5.5 TB/s) and 7 for the join,
 // gradient 76 to 81 (6 TB/s).
@@ -38,6 +38,7 @@ constexpr int kMaxExperts = SITU_MAX_LOCAL_EXPERTS;
 constexpr int kFinalCtas = 8;        // of the joining kernel's one cluster
 constexpr int kFinalThreads = 512;
 constexpr int kSms = 152;
+constexpr int kFold = 256;           // rows of a group whose column sums stay in registers
 
 struct BalanceParams {
   const float* logits;
@@ -143,56 +144,61 @@ balance_kernel(BalanceParams p) {
   const long first = (long)blockIdx.x * kGroups + g.id;
   const long rounds = (p.T - (long)blockIdx.x * kGroups + step - 1) / step;
   load_row<L, NV, VEC>(cur, p.logits + (size_t)min(first, (long)p.T - 1) * p.ld, g.lane, p.E, -INFINITY);
-  for (long i = 0; i < rounds; ++i) {
-    const long t = first + i * step;
-    const bool have = t < p.T, keep = have && (!p.mask || p.mask[t] != 0);
-    const int id = keep && g.lane < p.k ? __ldg(p.ids + (size_t)t * p.k + g.lane) : -1;
-    float v[V];
-    float m = -INFINITY;
+  for (long from = 0; from < rounds; from += kFold) {
+    for (long i = from; i < min(rounds, from + kFold); ++i) {
+      const long t = first + i * step;
+      const bool have = t < p.T, keep = have && (!p.mask || p.mask[t] != 0);
+      const int id = keep && g.lane < p.k ? __ldg(p.ids + (size_t)t * p.k + g.lane) : -1;
+      float v[V];
+      float m = -INFINITY;
 #pragma unroll
-    for (int c = 0; c < V; ++c) {
-      v[c] = cur[c];
-      m = fmaxf(m, v[c]);
-    }
-    load_row<L, NV, VEC>(cur, p.logits + (size_t)min(t + step, (long)p.T - 1) * p.ld, g.lane, p.E, -INFINITY);
-    m = g.reduce(m, red[g.id], turn, fmax_op);
-    if (m == -INFINITY) m = 0.f;               // a row of -inf: p = 0
-    float s = 0.f;
+      for (int c = 0; c < V; ++c) {
+        v[c] = cur[c];
+        m = fmaxf(m, v[c]);
+      }
+      load_row<L, NV, VEC>(cur, p.logits + (size_t)min(t + step, (long)p.T - 1) * p.ld, g.lane, p.E, -INFINITY);
+      m = g.reduce(m, red[g.id], turn, fmax_op);
+      if (m == -INFINITY) m = 0.f;               // a row of -inf: p = 0
+      float s = 0.f;
 #pragma unroll
-    for (int c = 0; c < V; ++c) {
-      v[c] = exp2_approx((v[c] - m) * kLog2e);   // 2 ulps, next to the 2^-24 |l - m| of any fp32 softmax
-      s += v[c];
-    }
-    s = g.reduce(s, red[g.id], turn, add_op);
-    const float inv = s == 0.f ? 0.f : 1.f / s;
-    if (have && g.lane == 0) p.stats[t] = make_float2(m, inv);
-    if (keep) {
+      for (int c = 0; c < V; ++c) {
+        v[c] = exp2_approx((v[c] - m) * kLog2e);   // 2 ulps, next to the 2^-24 |l - m| of any fp32 softmax
+        s += v[c];
+      }
+      s = g.reduce(s, red[g.id], turn, add_op);
+      const float inv = s == 0.f ? 0.f : 1.f / s;
+      if (have && g.lane == 0) p.stats[t] = make_float2(m, inv);
+      if (keep) {
 #pragma unroll
-      for (int c = 0; c < V; ++c) acc[c] = fmaf(v[c], inv, acc[c]);
-      mine += g.lane == 0;
+        for (int c = 0; c < V; ++c) acc[c] = fmaf(v[c], inv, acc[c]);
+        mine += g.lane == 0;
+      }
+      if (id >= 0 && id < p.E) atomicAdd(hist + id, 1);
     }
-    if (id >= 0 && id < p.E) atomicAdd(hist + id, 1);
+    // the groups' column sums, in the groups' order
+    if (L < kWarp) {
+#pragma unroll
+      for (int c = 0; c < V; ++c) acc[c] += __shfl_xor_sync(0xffffffffu, acc[c], 16);
+    }
+    constexpr int kTurns = L < kWarp ? kFwdThreads / kWarp : kGroups;
+    for (int w = 0; w < kTurns; ++w) {
+      if (L < kWarp ? (int)threadIdx.x / kWarp == w && (threadIdx.x & 31) < L : g.id == w) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int c = 4 * (g.lane + L * j) + i;
+            if (c < p.E) sum_p[c] += acc[4 * j + i];
+          }
+      }
+      __syncthreads();
+    }
+#pragma unroll
+    for (int c = 0; c < V; ++c) acc[c] = 0.f;
   }
   griddep_launch_dependents();
   if (mine) atomicAdd(&tokens_s, mine);
-  // the groups' column sums, in the groups' order
-  if (L < kWarp) {
-#pragma unroll
-    for (int c = 0; c < V; ++c) acc[c] += __shfl_xor_sync(0xffffffffu, acc[c], 16);
-  }
-  constexpr int kTurns = L < kWarp ? kFwdThreads / kWarp : kGroups;
-  for (int w = 0; w < kTurns; ++w) {
-    if (L < kWarp ? (int)threadIdx.x / kWarp == w && (threadIdx.x & 31) < L : g.id == w) {
-#pragma unroll
-      for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int c = 4 * (g.lane + L * j) + i;
-          if (c < p.E) sum_p[c] += acc[4 * j + i];
-        }
-    }
-    __syncthreads();
-  }
+  __syncthreads();
   if (gridDim.x > 1) {
     const size_t at = (size_t)blockIdx.x * p.pitch;
     for (int e = threadIdx.x; e < p.pitch; e += kFwdThreads) {
@@ -467,7 +473,7 @@ bool bad(const void* q, uintptr_t mask) { return (reinterpret_cast<uintptr_t>(q)
 
 extern "C" size_t situ_moe_balance_loss_workspace_size(int32_t T, int32_t num_experts_total) {
   using namespace situ;
-  if (T < 0 || num_experts_total < 1 || num_experts_total > kMaxExperts) return 0;
+  if (T < 0 || T > SITU_GEMM_MAX_ROWS || num_experts_total < 1 || num_experts_total > kMaxExperts) return 0;
   if (forward_grid(T, num_experts_total) == 1) return 0;   // one CTA writes the result itself
   const size_t grid = (size_t)forward_grid(T, num_experts_total), pitch = (size_t)(num_experts_total + 3) / 4 * 4;
   return (grid * (2 * pitch + 1) * 4 + 15) / 16 * 16;
@@ -478,8 +484,8 @@ extern "C" situ_status situ_moe_balance_loss(const situ_balance_args* a, void* w
   using namespace situ;
   if (!a) return SITU_ERR_NULL_ARG;
   const int E = a->num_experts_total;
-  if (a->T < 0 || E < 1 || E > kMaxExperts || a->top_k < 1 || a->top_k > SITU_MAX_TOP_K || a->top_k > E || a->ld < E ||
-      a->ld > (int64_t)1 << 39)
+  if (a->T < 0 || a->T > SITU_GEMM_MAX_ROWS || E < 1 || E > kMaxExperts || a->top_k < 1 || a->top_k > SITU_MAX_TOP_K ||
+      a->top_k > E || a->ld < E || a->ld > (int64_t)1 << 39)
     return SITU_ERR_BAD_SHAPE;
   const size_t need = situ_moe_balance_loss_workspace_size(a->T, E);
   if (!a->loss || !a->counts || !a->tokens || (need > 0 && !workspace)) return SITU_ERR_NULL_ARG;
@@ -527,8 +533,8 @@ extern "C" situ_status situ_moe_router_backward(const situ_router_backward_args*
   using namespace situ;
   if (!a) return SITU_ERR_NULL_ARG;
   const int E = a->num_experts_total;
-  if (a->T < 0 || E < 1 || E > kMaxExperts || a->top_k < 1 || a->top_k > SITU_MAX_TOP_K || a->top_k > E || a->ld < E ||
-      a->ldo < E || a->ld > (int64_t)1 << 39 || a->ldo > (int64_t)1 << 39)
+  if (a->T < 0 || a->T > SITU_GEMM_MAX_ROWS || E < 1 || E > kMaxExperts || a->top_k < 1 || a->top_k > SITU_MAX_TOP_K ||
+      a->top_k > E || a->ld < E || a->ldo < E || a->ld > (int64_t)1 << 39 || a->ldo > (int64_t)1 << 39)
     return SITU_ERR_BAD_SHAPE;
   if (a->renormalize != 0 && a->renormalize != 1) return SITU_ERR_UNSUPPORTED;
   if (a->T == 0) return SITU_OK;

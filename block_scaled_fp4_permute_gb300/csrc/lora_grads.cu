@@ -284,7 +284,7 @@ outer_join_kernel(const OuterParams p) {
   const Deal deal(p, scan, scan + kMaxGroups + 1);
   const long G = gridDim.x, i0 = first_item(blockIdx.x, deal.total, G), i1 = first_item(blockIdx.x + 1, deal.total, G);
   griddep_wait();
-  if (i0 == i1) return;
+  if (i0 == i1 || *reinterpret_cast<volatile int*>(p.err) != 0) return;   // no parts where a wait was given up
   // the piece that holds the CTA's last item
   Piece t = deal.at(i1 - 1, deal.total);
   if (t.from + 1 == t.chunks || t.from >= i1 - i0) return;   // it ends here, or began before

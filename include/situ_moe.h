@@ -626,9 +626,9 @@ situ_status situ_moe_fp8_gemm(const situ_fp8_gemm_args* args, void* stream);
  * counts[e] = c_e, tokens = n, and per row (masked ones too) its largest logit
  * and 1 / sum exp(l - largest), which the gradient takes.  A row of -inf has
  * p = 0; a NaN or +inf makes its row's p NaN.  What a masked row holds reaches
- * neither loss nor counts.  Sums are fp32 over a few hundred rows and fp64
+ * neither loss nor counts.  Sums are fp32 over a CTA's rows and fp32 pairs
  * beyond, in a fixed order.  T == 0 gives zeros.  E up to
- * SITU_MAX_LOCAL_EXPERTS; rows ld elements apart.
+ * SITU_MAX_LOCAL_EXPERTS, T to SITU_GEMM_MAX_ROWS; rows ld elements apart.
  * Errors: NULL_ARG, BAD_SHAPE, MISALIGNED (row_stats 8 bytes, workspace 16),
  * WORKSPACE_TOO_SMALL, CUDA. */
 typedef struct situ_balance_args {

@@ -244,6 +244,17 @@ def test_router_long_rows_of_tokens():
         assert torch.equal(B.situ_moe_balance_loss(logits, ids)[0], loss)
 
 
+def test_router_many_rows_a_group():
+    # column sums taken out of the registers several times
+    T, E, k = 1_500_001, 20, 2
+    logits, _ = router_case(T, E, k)
+    ids, _ = B.situ_moe_route_topk(logits, k)
+    loss, counts, tokens, _ = B.situ_moe_balance_loss(logits, ids)
+    rl, rc, _, _ = router_ref(logits, ids, None, 1.0, 1.0, None, True)
+    assert torch.equal(counts.long(), rc) and int(tokens) == T
+    assert abs(loss.item() - rl.item()) <= (p_error(logits) + (256 + 32 + 2 * 16) * U) * rl.item()
+
+
 def test_balanced_route_gradients():
     T, E, k = 60, 24, 3
     logits, dw = router_case(T, E, k)
@@ -859,6 +870,57 @@ def test_captured_and_replayed_on_new_inputs():
         graph.replay()
         for a, b in zip(got, want):
             assert torch.equal(a, b)
+
+
+def test_a_training_step_captured_and_replayed():
+    g = gen(5)
+    T, Hd, I, E, r, k = 120, 64, 40, 6, 8, 2
+    x = normal(g, T, Hd)
+    router = (torch.randn(Hd, E, generator=g, device="cuda") * Hd ** -0.5).requires_grad_()
+    w1, w2 = normal(g, E, 2 * I, Hd, std=Hd ** -0.5).requires_grad_(), normal(g, E, Hd, I, std=I ** -0.5).requires_grad_()
+    a, b = normal(g, E, r, Hd, std=Hd ** -0.5).requires_grad_(), normal(g, E, Hd, r, std=0.3).requires_grad_()
+    p0, p1 = torch.full((E,), 1.5, device="cuda"), torch.full((E,), 2.0, device="cuda")
+    dy = normal(g, T * k, Hd, std=0.2)
+
+    def run():
+        ids, w, counts, loss = B.balanced_route(x.float() @ router, k)
+        _, off, slot, _ = B.situ_moe_permute(ids, E, E, 0)
+        rows = x[slot.long() // k]
+        y = B.lora_linear(B.expert_ffn(rows, w1, w2, off, p0, p1), rows, a, b, off)
+        return torch.autograd.grad((y.float() * dy.float()).sum() + loss + (w * w).sum(), (router, w1, w2, a, b))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run()
+    x.copy_(normal(g, T, Hd))
+    graph.replay()
+    for got_, want in zip(got, run()):
+        assert torch.equal(got_, want)
+
+
+def test_no_work_after_a_wait_was_given_up():
+    g = gen(7)
+    S, K, N, r, n = 300, 72, 136, 16, 3
+    c = lora_case(g, S, K, N, r, n, BF16, BF16)
+    off, dy = offsets_of([100] * 3), normal(g, S, N)
+    _, u = B.situ_moe_lora(c["base"], c["x"], c["a"], c["b"], offsets=off, keep=True)
+    want = B.situ_moe_lora_backward(dy, c["x"], c["a"], c["b"], off, u)
+    out, dx = torch.full((S, N), 3.0, dtype=BF16, device="cuda"), torch.full((S, K), 3.0, dtype=BF16, device="cuda")
+    B._status_word(torch.cuda.current_device()).fill_(99)
+    try:
+        B.situ_moe_lora(c["base"], c["x"], c["a"], c["b"], offsets=off, out=out)
+        B.situ_moe_lora_backward(dy, c["x"], c["a"], c["b"], off, u, out=dx)
+        assert (out == 3).all() and (dx == 3).all()
+    finally:
+        assert B.situ_moe_gemm_status(reset=True) == 99
+    for a, b in zip(B.situ_moe_lora_backward(dy, c["x"], c["a"], c["b"], off, u), want):
+        assert torch.equal(a, b)
 
 
 def test_two_graphs_and_eager_calls_in_turn():
