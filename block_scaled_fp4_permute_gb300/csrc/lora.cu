@@ -66,7 +66,7 @@ struct LoraParams {
   void* u16;                       // [S, 2, r] scaled, in two terms of the operands' type, or null
   int stages, w_stage;             // shared memory: stages of w, bytes of one
   int x_stages;                    // shrink: of x
-  int y_stages, u_bytes;           // expand: items of base, bytes of u
+  int y_stages, u_stages, u_bytes; // expand: items of base, tiles of u, bytes of one
   // Rows sorted by adapter, where *mixed (null: never): their numbers, how many
   // have an adapter, and of each row its place among them (-1: none).
   const int32_t *mixed, *perm, *kept, *place;
@@ -100,6 +100,17 @@ __device__ __forceinline__ int adapter_of(const int32_t* ids, const int32_t* off
     else lo = mid + 1;
   }
   return lo <= n ? lo - 1 : -1;
+}
+
+// The same for a whole warp, a row to each lane: up to 31 adapters' offsets in one
+// load where a search takes a load after the other.  Rows from S on have none.
+__device__ __forceinline__ int adapter_of_lane(const int32_t* ids, const int32_t* offsets, int n, int row, int S) {
+  if (ids || n >= 32) return row < S ? adapter_of(ids, offsets, n, row) : -1;
+  const int lane = threadIdx.x & 31, o = lane <= n ? __ldcg(offsets + lane) : 0;
+  int first = n + 1;               // entry beyond row
+  for (int j = n; j >= 0; --j)
+    if (__shfl_sync(0xffffffffu, o, j) > row) first = j;
+  return row < S && first <= n ? first - 1 : -1;
 }
 
 template <int DT>
@@ -233,7 +244,20 @@ struct Adapters {
   int count;
 };
 constexpr int kEpi = 256;   // epilogue threads of either kernel
-__device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+// of T threads at a named barrier; whether all of them came with ok
+template <int T>
+__device__ __forceinline__ void sync_some() {
+  asm volatile("bar.sync 1, %0;" ::"n"(T) : "memory");
+}
+template <int T>
+__device__ __forceinline__ bool all_of(bool ok) {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.and.pred q, 1, %2, p;\n selp.u32 %0, 1, 0, q;\n}"
+               : "=r"(r)
+               : "r"((uint32_t)ok), "n"(T)
+               : "memory");
+  return r != 0;
+}
 // The rows to go through: `count` of them, the i-th is number row(i), S where there
 // is none.
 struct Rows {
@@ -243,71 +267,73 @@ struct Rows {
       : perm(p.mixed && __ldcg(p.mixed) ? p.perm : nullptr), S(p.S), count(perm ? __ldcg(p.kept) : p.S) {}
   __device__ __forceinline__ int row(int i) const { return i >= count ? S : perm ? __ldcg(perm + i) : i; }
 };
-// by the epilogue threads, of which this is number i
+// of row i of a tile, for its thread (whole warps)
+__device__ __forceinline__ int tile_adapter(const LoraParams& p, const Rows& rows, int row0, int i) {
+  return adapter_of_lane(p.ids, p.offsets, p.n, row0 + i < rows.count ? rows.row(row0 + i) : p.S, p.S);
+}
+// By R threads, of which this is number i and has e = tile_adapter.  Where one of
+// them comes without ok (it gave up waiting for the place) nothing is written.
 template <int R>
-__device__ __forceinline__ void find_adapters(Adapters<R>& t, const LoraParams& p, const Rows& rows, int row0, int i) {
-  static_assert(R <= kEpi, "a thread per row");
-  const bool mine = i < R;
-  int e = -1;
-  if (mine) {
-    if (row0 + i < rows.count) e = adapter_of(p.ids, p.offsets, p.n, rows.row(row0 + i));
-    t.of[i] = e;
-    t.halves[i] = 0;
-  }
-  epi_sync();
+__device__ __forceinline__ bool find_adapters(Adapters<R>& t, const Rows& rows, int row0, int i, int e, bool ok) {
+  if (!all_of<R>(ok)) return false;
+  const int lane = i & 31, w = i >> 5;
+  t.of[i] = e;
+  t.halves[i] = 0;
+  sync_some<R>();
   const int e0 = t.of[0];
-  const bool same = __all_sync(0xffffffffu, !mine || e == e0 || row0 + i >= rows.count);
-  if (mine && (i & 31) == 0) t.same[i >> 5] = same;
-  epi_sync();
+  const bool same = __all_sync(0xffffffffu, e == e0 || row0 + i >= rows.count);
+  if (lane == 0) t.same[w] = same;
+  sync_some<R>();
   uint32_t all = 1;
 #pragma unroll
-  for (int w = 0; w < R / 32; ++w) all &= t.same[w];
+  for (int v = 0; v < R / 32; ++v) all &= t.same[v];
   if (all) {
-    if (mine) t.at[i] = e >= 0 ? 0 : -1;
+    t.at[i] = e >= 0 ? 0 : -1;
     if (i == 0) {
       t.list[0] = e0;
       t.halves[0] = rows.count - row0 > 128 ? 3 : 1;
       t.count = e0 >= 0 ? 1 : 0;
     }
-    epi_sync();
-    return;
+    sync_some<R>();
+    return true;
   }
-  int first = i;       // the first row of this one's adapter
-  if (mine && e >= 0) {
-    const int4* of = reinterpret_cast<const int4*>(t.of);
-    for (int j = 0; 4 * j < i; ++j) {
-      const int4 v = of[j];
-      const int f = v.x == e ? 0 : v.y == e ? 1 : v.z == e ? 2 : v.w == e ? 3 : 4;
-      if (f < 4) {
-        first = min(i, 4 * j + f);
+  // the first row of this one's adapter: in its warp, then in those before it, an
+  // adapter at a time
+  const int l0 = __ffs(__match_any_sync(0xffffffffu, e)) - 1;
+  int first = 32 * w + l0;
+  uint32_t lead = __ballot_sync(0xffffffffu, e >= 0 && l0 == lane);
+  for (uint32_t rest = lead; rest; rest &= rest - 1) {
+    const int l = __ffs(rest) - 1, its = __shfl_sync(0xffffffffu, e, l);
+    for (int v = 0; v < w; ++v) {
+      const uint32_t found = __ballot_sync(0xffffffffu, t.of[32 * v + lane] == its);
+      if (found) {
+        if (e == its) first = 32 * v + __ffs(found) - 1;
+        lead &= ~(1u << l);
         break;
       }
     }
   }
-  __syncwarp();
-  const uint32_t lead = __ballot_sync(0xffffffffu, mine && e >= 0 && first == i);
-  if (mine && (i & 31) == 0) t.lead[i >> 5] = lead;
-  epi_sync();
-  if (mine) {
-    int place = __popc(t.lead[first >> 5] & ((1u << (first & 31)) - 1u));
-    for (int w = 0; w < first >> 5; ++w) place += __popc(t.lead[w]);
-    t.at[i] = e >= 0 ? place : -1;
-    if (e >= 0 && first == i) t.list[place] = e;
-    if (e >= 0) atomicOr(&t.halves[place], 1 << (i >> 7));
-    if (i == 0) {
-      int n = 0;
+  if (lane == 0) t.lead[w] = lead;
+  sync_some<R>();
+  int place = __popc(t.lead[first >> 5] & ((1u << (first & 31)) - 1u));
+  for (int v = 0; v < first >> 5; ++v) place += __popc(t.lead[v]);
+  t.at[i] = e >= 0 ? place : -1;
+  if (e >= 0 && first == i) t.list[place] = e;
+  if (e >= 0) atomicOr(&t.halves[place], 1 << (i >> 7));
+  if (i == 0) {
+    int n = 0;
 #pragma unroll
-      for (int w = 0; w < R / 32; ++w) n += __popc(t.lead[w]);
-      t.count = n;
-    }
+    for (int v = 0; v < R / 32; ++v) n += __popc(t.lead[v]);
+    t.count = n;
   }
-  epi_sync();
+  sync_some<R>();
+  return true;
 }
 
 constexpr int kTmemCols = 512;                // of an SM
 constexpr int kShrinkRows = 256;              // of a tile of the shrink: two MMAs share an adapter's weights
 constexpr int kShrinkThreads = 64 + kEpi;     // copies, MMAs; eight epilogue warps
-constexpr int kExpandThreads = 128 + kEpi;    // copies of base and out, MMAs, copies of weights; eight epilogue warps
+constexpr int kExpandThreads = 128 + kEpi + kTile;   // copies of base and out, MMAs, copies of weights; eight epilogue warps; u
 
 // A CTA's items of one tile, `per` items to a tile, and the next tile's.
 struct Segment {
@@ -326,11 +352,6 @@ struct Segment {
   }
 };
 
-__device__ __forceinline__ void prefetch_2d(const CUtensorMap* map, int x, int y) {
-  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(map)), "r"(x),
-               "r"(y)
-               : "memory");
-}
 __device__ __forceinline__ void store_2d(const CUtensorMap* map, uint32_t src, int x, int y) {
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
                    reinterpret_cast<uint64_t>(map)),
@@ -376,11 +397,9 @@ shrink_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
   const long total = (long)((rows.count + kShrinkRows - 1) / kShrinkRows) * p.chunks, G = sharers(total, p.shrink_ctas, p.least);
   const bool shares = blockIdx.x < G;
   const long i0 = shares ? first_item(blockIdx.x, total, G) : 0, i1 = shares ? first_item(blockIdx.x + 1, total, G) : 0;
+  int e_first = -1;                  // of the first tile: on its way while the barriers are set up
+  if (warp >= 2 && i0 < i1) e_first = tile_adapter(p, rows, (int)(i0 / p.chunks) * kShrinkRows, tid - 64);
   if (tid == 0) {
-    for (long i = i0; !rows.perm && i < i1 && i < i0 + p.x_stages; ++i)   // x does not wait for the adapters' list
-      for (int h = 0; h < kShrinkRows; h += kTile)
-        if ((i / p.chunks) * kShrinkRows + h < p.S)
-          prefetch_2d(&map_x, (int)(i % p.chunks) * kChunk, (int)(i / p.chunks) * kShrinkRows + h);
     holder[1] = (uint32_t)*reinterpret_cast<volatile int*>(p.err);   // an earlier launch gave up a wait: no work then
     prefetch_map(&map_w);
     for (int s = 0; s < 4 * kMaxStages; ++s) mbar_init(bar0 + 8 * s, 1);
@@ -399,6 +418,7 @@ shrink_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = holder[0];
   const bool dead = holder[1] != 0;
+  griddep_launch_dependents();       // its CTAs start where these have left, and fetch base
   constexpr int kSumCols = kTmemCols / 2, kHalfCols = kSumCols / 2;   // of a sum's columns, those of 128 rows
   const int per = kHalfCols / p.r16;                    // adapters of a pass
   const uint32_t wbase = sbase + p.x_stages * 2 * kXBytes;
@@ -543,18 +563,18 @@ shrink_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     const int et = tid - 64, q = warp & 3, h = (warp - 2) >> 2, mine = h * kTile + 32 * q + lane;
     Turns l(2), acc(2);
     bool ok = true;
-    auto list = [&](const Segment& g) {                 // of a tile, while the one before is worked on
+    auto list = [&](const Segment& g, int e) {          // of a tile, while the one before is worked on
       if (l.again() && !warp_wait(list_empty(l.s), l.ph ^ 1, p.err, 91)) ok = false;
-      find_adapters(lists[l.s], p, rows, g.tile * kShrinkRows, et);
+      ok = find_adapters(lists[l.s], rows, g.tile * kShrinkRows, et, e, ok);
       mbar_arrive_if(list_full(l.s), et == 0);
       l.next();
     };
     Segment g(i0, i1, p.chunks);
-    if (g.more()) list(g);
+    if (g.more()) list(g, e_first);
     for (int b = 0; g.more(); b ^= 1) {
       Segment n = g;
       n.next();
-      if (n.more()) list(n);
+      if (n.more()) list(n, tile_adapter(p, rows, n.tile * kShrinkRows, et));
       const Adapters<kShrinkRows>& ad = lists[b];
       const int nd = ad.count, at = ad.at[mine], row = g.tile * kShrinkRows + mine;
       const int part = (int)((long)blockIdx.x - cta_of((long)g.tile * p.chunks, total, G));
@@ -595,7 +615,6 @@ shrink_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
       g = n;
     }
   }
-  griddep_launch_dependents();
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   if (warp == 1) {
@@ -614,8 +633,9 @@ shrink_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
 // base loaded and out stored by the epilogue's own instructions, the loads', the
 // sums' and the stores' times added up (403 MB in 116 us).  u stays in shared
 // memory for all the CTA's items of a tile, its 16-bit terms one after the
-// other along the contraction.  The items are dealt out evenly over the CTAs,
-// one per SM.
+// other along the contraction; warps of their own bring the next tile's meanwhile
+// (between two tiles it cost each CTA that has two 13 us of 70).  The items are
+// dealt out evenly over the CTAs, one per SM.
 template <int DT, bool TRANS, bool F32>
 __global__ void __launch_bounds__(kExpandThreads, 1)
 expand_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_base,
@@ -623,8 +643,8 @@ expand_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
   constexpr int kTerms = terms_of(DT, F32), kCols = cols_of(F32), kBoxCols = kCols / 2;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Adapters<kTile> lists[2];
-  __shared__ float back[kTile];      // f16: the power of two that a row's u was divided by
-  __shared__ uint64_t bars[4 * kMaxStages + 10];
+  __shared__ float back[2][kTile];   // f16: the power of two that a row's u was divided by
+  __shared__ uint64_t bars[4 * kMaxStages + 11];
   __shared__ uint32_t holder[2];
   uint8_t* smem = smem_raw + (((saddr(smem_raw) + 1023) & ~1023u) - saddr(smem_raw));
   const uint32_t sbase = saddr(smem);
@@ -638,8 +658,15 @@ expand_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
   auto acc_full = [&](int b) { return tail + 8 * b; };
   auto acc_empty = [&](int b) { return tail + 16 + 8 * b; };
   auto list_full = [&](int b) { return tail + 32 + 8 * b; };
-  auto list_empty = [&](int b) { return tail + 48 + 8 * b; };
-  const uint32_t u_full = tail + 64, drain = tail + 72;
+  auto u_full = [&](int b) { return tail + 48 + 8 * b; };
+  auto tile_empty = [&](int b) { return tail + 64 + 8 * b; };
+  const uint32_t drain = tail + 80;
+  const int blocks = (p.C + kCols - 1) / kCols;
+  const Rows rows(p);
+  const long total = (long)((rows.count + kTile - 1) / kTile) * blocks, G = gridDim.x;
+  const long i0 = first_item(blockIdx.x, total, G), i1 = first_item(blockIdx.x + 1, total, G);
+  int e_first = -1;                  // of the first tile, ahead of the copies of base
+  if (warp >= 12 && i0 < i1) e_first = tile_adapter(p, rows, (int)(i0 / blocks) * kTile, tid - 384);
   if (tid == 0) {
     prefetch_map(&map_w);
     if (p.base) prefetch_map(&map_base);
@@ -654,9 +681,9 @@ expand_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
       mbar_init(acc_full(b), 1);
       mbar_init(acc_empty(b), kEpi / 32);
       mbar_init(list_full(b), 1);
-      mbar_init(list_empty(b), 2);
+      mbar_init(u_full(b), 12);                           // warps of the first tile's; of four, three each
+      mbar_init(tile_empty(b), kEpi / 32 + 2);          // the epilogue, the copies of weights, the MMAs
     }
-    mbar_init(u_full, kEpi / 32);
     mbar_init(drain, 1);
     holder[1] = (uint32_t)*reinterpret_cast<volatile int*>(p.err);   // an earlier call gave up a wait: no work then
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -667,13 +694,122 @@ expand_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = holder[0];
   const bool dead = holder[1] != 0;
-  const int blocks = (p.C + kCols - 1) / kCols;
-  const Rows rows(p);
-  const long total = (long)((rows.count + kTile - 1) / kTile) * blocks, G = gridDim.x;
-  const long i0 = first_item(blockIdx.x, total, G), i1 = first_item(blockIdx.x + 1, total, G);
-  const uint32_t ubase = sbase, wbase = sbase + p.u_bytes, ybase = wbase + p.stages * p.w_stage;
+  const uint32_t wbase = sbase + p.u_stages * p.u_bytes, ybase = wbase + p.stages * p.w_stage;
   const int rboxes = (p.r + 63) / 64, steps = p.r16 / 16;
   const int rrows = min(64, p.r16);                     // TRANS: contraction rows of a box
+
+  // u of a tile in its place ts: what warp `part` of `among` has of it
+  auto stage_u = [&](const Segment& g, int ts, int part, int among) {
+    const long t0 = (long)(g.tile / (kShrinkRows / kTile)) * p.chunks;
+    const long all = (long)((rows.count + kShrinkRows - 1) / kShrinkRows) * p.chunks;
+    const long sharing = sharers(all, p.shrink_ctas, p.least);
+    const int parts = (int)(cta_of(t0 + p.chunks - 1, all, sharing) - cta_of(t0, all, sharing)) + 1;
+    const bool write = p.u16 && g.from == 0;
+    const Adapters<kTile>& ad = lists[ts];
+    uint8_t* us = smem + ts * p.u_bytes;
+    const size_t stride = (size_t)p.S * p.r;
+    // Eight lanes to a row, four columns each of every 32; four rows at a time
+    // and kRows of those together, four parts in flight.
+    auto stage = [&](auto cs) {
+      constexpr int kC = decltype(cs)::value, kRows = 4 / kC;
+      const int c0 = 4 * (lane & 7);
+#pragma unroll 1
+      for (int r0 = 4 * kRows * part; r0 < kTile; r0 += 4 * kRows * among) {
+        float u[kRows][kC][4];
+        const float* src[kRows];
+        int of[kRows];
+        float f[kRows];
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+          const int r = r0 + 4 * i + (lane >> 3);
+          of[i] = ad.of[r];
+          f[i] = of[i] >= 0 && p.scale ? __ldg(p.scale + of[i]) : 1.f;
+          src[i] = p.part + (size_t)(g.tile * kTile + r) * p.r + c0;
+#pragma unroll
+          for (int c = 0; c < kC; ++c) u[i][c][0] = u[i][c][1] = u[i][c][2] = u[i][c][3] = 0.f;
+        }
+        for (int s0 = 0; s0 < parts; s0 += 4) {
+          float4 v[4][kRows][kC];
+#pragma unroll
+          for (int s = 0; s < 4; ++s)
+#pragma unroll
+            for (int i = 0; i < kRows; ++i)
+#pragma unroll
+              for (int c = 0; c < kC; ++c)
+                v[s][i][c] = s0 + s < parts && of[i] >= 0 && c0 + 32 * c < p.r
+                                 ? __ldcg(reinterpret_cast<const float4*>(src[i] + (s0 + s) * stride + 32 * c))
+                                 : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int s = 0; s < 4; ++s)
+#pragma unroll
+            for (int i = 0; i < kRows; ++i)
+#pragma unroll
+              for (int c = 0; c < kC; ++c) {
+                u[i][c][0] += v[s][i][c].x;
+                u[i][c][1] += v[s][i][c].y;
+                u[i][c][2] += v[s][i][c].z;
+                u[i][c][3] += v[s][i][c].w;
+              }
+        }
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+          const int r = r0 + 4 * i + (lane >> 3);
+#pragma unroll
+          for (int c = 0; c < kC; ++c)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) u[i][c][k] = of[i] >= 0 ? u[i][c][k] * f[i] : 0.f;
+          float to = 1.f;
+          if (DT == SITU_DT_F16) {
+            float m = 0.f;
+#pragma unroll
+            for (int c = 0; c < kC; ++c)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) m = fmaxf(m, fabsf(u[i][c][k]));
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            const int k = (int)(__float_as_uint(m) >> 23) - 127;    // m in [2^k, 2^(k + 1))
+            const int ex = m > 0.f && m < INFINITY ? max(-100, min(120, k - 14)) : 0;
+            to = exp2i(-ex);
+            if ((lane & 7) == 0) back[ts][r] = exp2i(ex);
+          }
+          const int row = write ? rows.row(g.tile * kTile + r) : p.S;
+#pragma unroll
+          for (int c = 0; c < kC; ++c) {
+            const int j = c0 + 32 * c;
+            if (row < p.S && j < p.r) {
+              uint2 *o = reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.u16) + (size_t)row * 2 * p.r + j), hi, lo;
+              two_terms<DT>(u[i][c][0], u[i][c][1], hi.x, lo.x);
+              two_terms<DT>(u[i][c][2], u[i][c][3], hi.y, lo.y);
+              o[0] = hi;
+              o[p.r / 4] = lo;
+            }
+#pragma unroll
+            for (int t = 0; t < kTerms; ++t) {
+              uint32_t v[2];
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const float a = u[i][c][2 * k] * (t == 0 ? to : 1.f), b = u[i][c][2 * k + 1] * (t == 0 ? to : 1.f);
+                v[k] = pack16<DT>(a, b);
+                // what the term leaves; an infinity leaves nothing
+                u[i][c][2 * k] = fabsf(a) < INFINITY ? a - lo16<DT>(v[k]) : 0.f;
+                u[i][c][2 * k + 1] = fabsf(b) < INFINITY ? b - hi16<DT>(v[k]) : 0.f;
+              }
+              const int k = t * p.r16 + j;              // along u's terms: 128-byte swizzled rows of 64
+              if (j < p.r16)
+                *reinterpret_cast<uint2*>(us + (k >> 6) * kXBytes + r * 128 + ((((k & 63) >> 3) ^ (r & 7)) << 4) +
+                                          2 * (k & 4)) = make_uint2(v[0], v[1]);
+            }
+          }
+        }
+      }
+    };
+    using std::integral_constant;
+    if (p.r <= 32) stage(integral_constant<int, 1>{});
+    else if (p.r <= 64) stage(integral_constant<int, 2>{});
+    else stage(integral_constant<int, 4>{});
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+  };
 
   if (warp == 0 && !dead) {
     // ---------------- base in, out ----------------
@@ -726,22 +862,18 @@ expand_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
     // ---------------- MMAs ----------------
     const bool leader = elect_one();
     const uint32_t idesc = idesc_of(DT == SITU_DT_BF16, false, TRANS, kCols);
-    Turns w(p.stages), acc(2), l(2);
-    uint32_t seg = 0;
+    Turns w(p.stages), acc(2), tile(p.u_stages);
     bool ok = true;
-    for (Segment g(i0, i1, blocks); g.more() && ok; g.next(), seg ^= 1) {
-      if (!warp_wait(list_full(l.s), l.ph, p.err, 102)) {
+    for (Segment g(i0, i1, blocks); g.more() && ok; g.next(), tile.next()) {
+      if (!warp_wait(u_full(tile.s), tile.ph, p.err, 102)) {
         ok = false;
         break;
       }
-      const int nd = lists[l.s].count;
-      __syncwarp();
-      mbar_arrive_if(list_empty(l.s), lane == 0);
-      l.next();
-      ok = warp_wait(u_full, seg, p.err, 103);
+      const int nd = lists[tile.s].count;
+      const uint32_t ubase = sbase + tile.s * p.u_bytes;
       for (int b = g.from; b < g.to && ok; ++b)
         for (int d = 0; d < nd; ++d, w.next(), acc.next()) {
-          if ((acc.again() && !warp_wait(acc_empty(acc.s), acc.ph ^ 1, p.err, 104)) || !warp_wait(wfull(w.s), w.ph, p.err, 105)) {
+          if ((acc.again() && !warp_wait(acc_empty(acc.s), acc.ph ^ 1, p.err, 113)) || !warp_wait(wfull(w.s), w.ph, p.err, 105)) {
             ok = false;
             break;
           }
@@ -761,6 +893,8 @@ expand_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
           }
           __syncwarp();
         }
+      if (leader) mma_commit(tile_empty(tile.s));
+      __syncwarp();
     }
     leave(
         ok, [&] { return w.last([&](int j, uint32_t ph) { return warp_wait(wempty(j), ph, p.err, 106); }); },
@@ -772,14 +906,14 @@ expand_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
   } else if (warp == 2 && !dead) {
     // ---------------- weights ----------------
     const bool leader = elect_one();
-    Turns w(p.stages), l(2);
+    Turns w(p.stages), tile(p.u_stages);
     bool ok = true;
-    for (Segment g(i0, i1, blocks); g.more() && ok; g.next()) {
-      if (!warp_wait(list_full(l.s), l.ph, p.err, 107)) {
+    for (Segment g(i0, i1, blocks); g.more() && ok; g.next(), tile.next()) {
+      if (!warp_wait(list_full(tile.s), tile.ph, p.err, 107)) {
         ok = false;
         break;
       }
-      const Adapters<kTile>& ad = lists[l.s];
+      const Adapters<kTile>& ad = lists[tile.s];
       const int nd = ad.count;
       for (int b = g.from; b < g.to && ok; ++b)
         for (int d = 0; d < nd; ++d, w.next()) {
@@ -804,8 +938,7 @@ expand_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
           __syncwarp();
         }
       __syncwarp();
-      mbar_arrive_if(list_empty(l.s), lane == 0);
-      l.next();
+      mbar_arrive_if(tile_empty(tile.s), lane == 0);
     }
     leave(
         ok, [&] { return w.last([&](int j, uint32_t ph) { return warp_wait(wempty(j), ph, p.err, 109); }); },
@@ -826,107 +959,40 @@ expand_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
             reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.u16) + (size_t)row * 2 * p.r)[i] = make_uint4(0, 0, 0, 0);
       }
     }
-  } else if (warp >= 4 && !dead) {
-    // ---------------- lists, u, and sums onto base ----------------
-    const int et = tid - 128, q = warp & 3, h = (warp - 4) >> 2;   // this warp's 32 rows, and box of an item
-    Turns l(2), acc(2), y(p.y_stages);
-    bool ok = true;
-    auto list = [&](const Segment& g) {                 // of a tile, while the one before is worked on
-      if (l.again() && !warp_wait(list_empty(l.s), l.ph ^ 1, p.err, 110)) ok = false;
-      find_adapters(lists[l.s], p, rows, g.tile * kTile, et);
-      mbar_arrive_if(list_full(l.s), et == 0);
-      l.next();
-    };
-    // u of a tile: two threads to a row, eight elements of each sixteen each
-    auto stage_u = [&](const Segment& g, const Adapters<kTile>& ad) {
-      const int r = et >> 1, place = g.tile * kTile + r, row = rows.row(place), e = ad.of[r];
-      const float f = e >= 0 && p.scale ? __ldg(p.scale + e) : 1.f;
-      const bool write = p.u16 && g.from == 0 && row < p.S;
-      const long t0 = (long)(g.tile / (kShrinkRows / kTile)) * p.chunks;
-      const long all = (long)((rows.count + kShrinkRows - 1) / kShrinkRows) * p.chunks;
-      const long sharing = sharers(all, p.shrink_ctas, p.least);
-      const int parts = (int)(cta_of(t0 + p.chunks - 1, all, sharing) - cta_of(t0, all, sharing)) + 1;
-      auto sum8 = [&](int j, float (&u)[8]) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) u[k] = 0.f;
-        if (e < 0 || j >= p.r) return;
-#pragma unroll 4
-        for (int s = 0; s < parts; ++s) {
-          const float4* src = reinterpret_cast<const float4*>(p.part + ((size_t)s * p.S + place) * p.r + j);
-          const float4 v = __ldcg(src), z = __ldcg(src + 1);
-          u[0] += v.x;
-          u[1] += v.y;
-          u[2] += v.z;
-          u[3] += v.w;
-          u[4] += z.x;
-          u[5] += z.y;
-          u[6] += z.z;
-          u[7] += z.w;
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) u[k] *= f;
-      };
-      float to = 1.f;
-      if (DT == SITU_DT_F16) {
-        float m = 0.f;
-        for (int j = 8 * (et & 1); j < p.r16; j += 16) {
-          float u[8];
-          sum8(j, u);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) m = fmaxf(m, fabsf(u[k]));
-        }
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        const int k = (int)(__float_as_uint(m) >> 23) - 127;          // m in [2^k, 2^(k + 1))
-        const int ex = m > 0.f && m < INFINITY ? max(-100, min(120, k - 14)) : 0;
-        to = exp2i(-ex);
-        if ((et & 1) == 0) back[r] = exp2i(ex);
-      }
-#pragma unroll 2
-      for (int j = 8 * (et & 1); j < p.r16; j += 16) {
-        float u[8];
-        sum8(j, u);
-        if (write && j < p.r) {
-          uint4 *o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.u16) + (size_t)row * 2 * p.r + j), hi, lo;
-          two_terms<DT>(u[0], u[1], hi.x, lo.x);
-          two_terms<DT>(u[2], u[3], hi.y, lo.y);
-          two_terms<DT>(u[4], u[5], hi.z, lo.z);
-          two_terms<DT>(u[6], u[7], hi.w, lo.w);
-          o[0] = hi;
-          o[p.r / 8] = lo;
-        }
-#pragma unroll
-        for (int t = 0; t < kTerms; ++t) {
-          uint32_t v[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float a = u[2 * k] * (t == 0 ? to : 1.f), b = u[2 * k + 1] * (t == 0 ? to : 1.f);
-            v[k] = pack16<DT>(a, b);
-            // what the term leaves; an infinity leaves nothing
-            u[2 * k] = fabsf(a) < INFINITY ? a - lo16<DT>(v[k]) : 0.f;
-            u[2 * k + 1] = fabsf(b) < INFINITY ? b - hi16<DT>(v[k]) : 0.f;
-          }
-          const int k = t * p.r16 + j;                  // along u's terms: 128-byte swizzled rows of 64
-          *reinterpret_cast<uint4*>(smem + (k >> 6) * kXBytes + r * 128 + ((((k & 63) >> 3) ^ (r & 7)) << 4)) =
-              make_uint4(v[0], v[1], v[2], v[3]);
-        }
-      }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      epi_sync();                             // back[] and, before the arrivals, every lane's u
-      mbar_arrive_if(u_full, lane == 0);
-    };
-    Segment g(i0, i1, blocks);
-    if (g.more()) {
-      list(g);
-      griddep_wait();                                   // the parts are the predecessor's: base and weights come meanwhile
-      stage_u(g, lists[0]);
+  } else if (warp >= 12 && !dead) {
+    // ---------------- lists, and u from its parts ----------------
+    const int st = tid - 384;
+    Turns tile(p.u_stages);
+    bool ok = true, first = true;
+    for (Segment g(i0, i1, blocks); g.more(); g.next(), tile.next(), first = false) {
+      const int e = first ? e_first : tile_adapter(p, rows, g.tile * kTile, st);
+      if (tile.again() && !warp_wait(tile_empty(tile.s), tile.ph ^ 1, p.err, 110)) ok = false;
+      ok = find_adapters(lists[tile.s], rows, g.tile * kTile, st, e, ok);
+      if (!ok) break;
+      mbar_arrive_if(list_full(tile.s), st == 0);
+      if (first) griddep_wait();                          // the parts are the predecessor's: base and weights come meanwhile
+      stage_u(g, tile.s, first ? 8 + warp - 12 : warp - 12, first ? 12 : 4);
+      if (lane == 0) mbar_arrive_n(u_full(tile.s), first ? 1 : 3);
     }
-    for (int lb = 0; g.more(); lb ^= 1) {
-      Segment n = g;
-      n.next();
-      if (n.more()) list(n);
-      const Adapters<kTile>& ad = lists[lb];
+  } else if (warp >= 4 && !dead) {
+    // ---------------- sums onto base ----------------
+    const int q = warp & 3, h = (warp - 4) >> 2;        // this warp's 32 rows, and box of an item
+    Turns acc(2), y(p.y_stages), tile(p.u_stages);
+    bool ok = true;
+    if (i0 < i1) {                                        // u of the first tile together
+      ok = warp_wait(list_full(0), 0, p.err, 104);
+      griddep_wait();
+      if (ok) stage_u(Segment(i0, i1, blocks), 0, warp - 4, 12);
+      mbar_arrive_if(u_full(0), lane == 0);
+    }
+    for (Segment g(i0, i1, blocks); g.more() && ok; g.next(), tile.next()) {
+      if (!warp_wait(u_full(tile.s), tile.ph, p.err, 103)) {
+        ok = false;
+        break;
+      }
+      const Adapters<kTile>& ad = lists[tile.s];
       const int nd = ad.count, at = ad.at[32 * q + lane];
-      const float my_back = DT == SITU_DT_F16 ? back[32 * q + lane] : 1.f;
+      const float my_back = DT == SITU_DT_F16 ? back[tile.s][32 * q + lane] : 1.f;
       const int my_row = rows.perm ? rows.row(g.tile * kTile + 32 * q + lane) : 0;
       for (int b = g.from; b < g.to && ok; ++b, y.next()) {
         uint8_t* mine = smem + (ybase - sbase) + y.s * 2 * kXBytes + h * kXBytes + (32 * q + lane) * 128;
@@ -1002,11 +1068,7 @@ expand_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
         __syncwarp();
         mbar_arrive_if(ydone(y.s), lane == 0);
       }
-      g = n;
-      if (g.more()) {
-        epi_sync();                           // every warp is done with back[], and the MMAs with u
-        stage_u(g, lists[lb ^ 1]);
-      }
+      mbar_arrive_if(tile_empty(tile.s), lane == 0);
     }
   }
   if (dead || i0 == i1) griddep_wait();   // the others have, or wait for a warp that has
@@ -1090,15 +1152,19 @@ cudaError_t launch_pair(const Maps& m, LoraParams s, LoraParams x, cudaStream_t 
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   x.u_bytes = (terms_of(DT, F32) * x.r16 + 63) / 64 * kXBytes;
-  // four items of base and four of weights where they fit (16,384 x 6144 bf16 at
-  // rank 64: 69 us; five and two: 75, three and two: 79), else base first
-  int rest;
-  for (x.stages = 4;; --x.stages) {
-    rest = 1024 + x.u_bytes + x.stages * x.w_stage;
-    x.y_stages = (kExpandSmem - rest) / (2 * kXBytes);
-    if (x.y_stages > 4) x.y_stages = 4;
-    if (x.y_stages >= 3 || x.stages == 2) break;
+  // two tiles of u where three items of base and two of weights fit beside them;
+  // then as many items of base as fit, up to four, and of weights (16,384 x 6144
+  // bf16 at rank 64: four and three 113 us for both kernels, three and four 121)
+  x.u_stages = 1024 + 2 * x.u_bytes + 2 * x.w_stage + 3 * 2 * kXBytes <= kExpandSmem ? 2 : 1;
+  x.y_stages = 0;
+  for (int w = 4; w >= 2; --w) {
+    const int y = (kExpandSmem - 1024 - x.u_stages * x.u_bytes - w * x.w_stage) / (2 * kXBytes);
+    if (x.y_stages < 4 && y > x.y_stages) {
+      x.y_stages = y < 4 ? y : 4;
+      x.stages = w;
+    }
   }
+  const int rest = 1024 + x.u_stages * x.u_bytes + x.stages * x.w_stage;
   const long items = (long)((x.S + kTile - 1) / kTile) * ((x.C + cols_of(F32) - 1) / cols_of(F32));
   return launch_pdl(expand, dim3((unsigned)(items < sms ? items : sms)), dim3(kExpandThreads), rest + x.y_stages * 2 * kXBytes,
                     st, m.other, m.base, m.base1, m.out, x);

@@ -50,6 +50,10 @@ __device__ __forceinline__ uint32_t idesc_of(bool bf16, bool trans_a, bool trans
          ((uint32_t)(128 >> 4) << 24);
 }
 
+__device__ __forceinline__ void mbar_arrive_n(uint32_t a, uint32_t n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(a), "r"(n) : "memory");
+}
+
 // Items dealt out evenly: CTA c of G takes [c T / G, (c + 1) T / G) of T, and
 // item i is CTA ((i + 1) G - 1) / T's.
 __host__ __device__ __forceinline__ long first_item(long c, long T, long G) { return c * T / G; }
