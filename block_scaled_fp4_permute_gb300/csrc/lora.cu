@@ -698,13 +698,15 @@ expand_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
   const int rboxes = (p.r + 63) / 64, steps = p.r16 / 16;
   const int rrows = min(64, p.r16);                     // TRANS: contraction rows of a box
 
-  // u of a tile in its place ts: what warp `part` of `among` has of it
-  auto stage_u = [&](const Segment& g, int ts, int part, int among) {
+  auto parts_of = [&](const Segment& g) {
     const long t0 = (long)(g.tile / (kShrinkRows / kTile)) * p.chunks;
     const long all = (long)((rows.count + kShrinkRows - 1) / kShrinkRows) * p.chunks;
     const long sharing = sharers(all, p.shrink_ctas, p.least);
-    const int parts = (int)(cta_of(t0 + p.chunks - 1, all, sharing) - cta_of(t0, all, sharing)) + 1;
-    const bool write = p.u16 && g.from == 0;
+    return (int)(cta_of(t0 + p.chunks - 1, all, sharing) - cta_of(t0, all, sharing)) + 1;
+  };
+  // u of a tile in its place ts: what warp `part` of `among` has of it
+  auto stage_u = [&](const Segment& g, int ts, int part, int among, int parts) {
+    const bool write = p.u16 && g.from == 0 && parts > 0;
     const Adapters<kTile>& ad = lists[ts];
     uint8_t* us = smem + ts * p.u_bytes;
     const size_t stride = (size_t)p.S * p.r;
@@ -728,7 +730,7 @@ expand_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
 #pragma unroll
           for (int c = 0; c < kC; ++c) u[i][c][0] = u[i][c][1] = u[i][c][2] = u[i][c][3] = 0.f;
         }
-        for (int s0 = 0; s0 < parts; s0 += 4) {
+        for (int s0 = 0; s0 == 0 || s0 < parts; s0 += 4) {
           float4 v[4][kRows][kC];
 #pragma unroll
           for (int s = 0; s < 4; ++s)
@@ -810,6 +812,37 @@ expand_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
   };
+
+  // Lists and u from its parts, by four warps, for the first tile by those of the
+  // epilogue too.  There a round without parts comes first, while the predecessor
+  // ends: it brings the instructions in, which took 3.6 us of the 7 between that
+  // end and the first MMA.
+  bool first_ok = true;
+  if (warp >= 4 && !dead) {
+    const bool all = warp >= 12;
+    const int st = tid - 384;
+    Turns tile(p.u_stages);
+    bool first = true;
+    for (Segment g(i0, i1, blocks); g.more(); g.next(), tile.next(), first = false) {
+      if (all) {
+        const int e = first ? e_first : tile_adapter(p, rows, g.tile * kTile, st);
+        if (tile.again() && !warp_wait(tile_empty(tile.s), tile.ph ^ 1, p.err, 110)) first_ok = false;
+        first_ok = find_adapters(lists[tile.s], rows, g.tile * kTile, st, e, first_ok);
+        if (!first_ok) break;
+        mbar_arrive_if(list_full(tile.s), st == 0);
+      } else {
+        first_ok = warp_wait(list_full(0), 0, p.err, 104);
+      }
+      const int parts = parts_of(g);
+#pragma unroll 1
+      for (int round = first ? 0 : 1; round < 2; ++round) {
+        if (first && round == 1) griddep_wait();          // the parts are the predecessor's: base and weights come meanwhile
+        if (first_ok) stage_u(g, tile.s, first ? warp - 4 : warp - 12, first ? 12 : 4, round == 0 ? 0 : parts);
+      }
+      if (lane == 0) mbar_arrive_n(u_full(tile.s), first ? 1 : 3);
+      if (!all) break;
+    }
+  }
 
   if (warp == 0 && !dead) {
     // ---------------- base in, out ----------------
@@ -959,32 +992,11 @@ expand_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
             reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.u16) + (size_t)row * 2 * p.r)[i] = make_uint4(0, 0, 0, 0);
       }
     }
-  } else if (warp >= 12 && !dead) {
-    // ---------------- lists, and u from its parts ----------------
-    const int st = tid - 384;
-    Turns tile(p.u_stages);
-    bool ok = true, first = true;
-    for (Segment g(i0, i1, blocks); g.more(); g.next(), tile.next(), first = false) {
-      const int e = first ? e_first : tile_adapter(p, rows, g.tile * kTile, st);
-      if (tile.again() && !warp_wait(tile_empty(tile.s), tile.ph ^ 1, p.err, 110)) ok = false;
-      ok = find_adapters(lists[tile.s], rows, g.tile * kTile, st, e, ok);
-      if (!ok) break;
-      mbar_arrive_if(list_full(tile.s), st == 0);
-      if (first) griddep_wait();                          // the parts are the predecessor's: base and weights come meanwhile
-      stage_u(g, tile.s, first ? 8 + warp - 12 : warp - 12, first ? 12 : 4);
-      if (lane == 0) mbar_arrive_n(u_full(tile.s), first ? 1 : 3);
-    }
-  } else if (warp >= 4 && !dead) {
+  } else if (warp >= 4 && warp < 12 && !dead) {
     // ---------------- sums onto base ----------------
     const int q = warp & 3, h = (warp - 4) >> 2;        // this warp's 32 rows, and box of an item
     Turns acc(2), y(p.y_stages), tile(p.u_stages);
-    bool ok = true;
-    if (i0 < i1) {                                        // u of the first tile together
-      ok = warp_wait(list_full(0), 0, p.err, 104);
-      griddep_wait();
-      if (ok) stage_u(Segment(i0, i1, blocks), 0, warp - 4, 12);
-      mbar_arrive_if(u_full(0), lane == 0);
-    }
+    bool ok = first_ok;
     for (Segment g(i0, i1, blocks); g.more() && ok; g.next(), tile.next()) {
       if (!warp_wait(u_full(tile.s), tile.ph, p.err, 103)) {
         ok = false;
