@@ -45,8 +45,8 @@ namespace {
 constexpr int kTile = 128;         // rows of a tile
 constexpr int kChunk = 64;         // contraction elements of a stage (shrink)
 constexpr int kXBytes = kTile * 128;   // a box: 128 bytes of 128 rows
-constexpr int kMaxStages = 8;      // of a ring
-constexpr int kShrinkSmem = 218 * 1024, kExpandSmem = 221 * 1024;   // 227 KB with the static parts
+constexpr int kMaxStages = 16;     // of a ring
+constexpr int kShrinkSmem = 217 * 1024, kExpandSmem = 220 * 1024;   // 227 KB with the static parts
 constexpr int kCluster = 8;        // CTAs of a row
 constexpr int kRowThreads = 256;
 
@@ -1153,9 +1153,10 @@ cudaError_t launch_pair(const Maps& m, LoraParams s, LoraParams x, cudaStream_t 
     if (e != cudaSuccess) return e;
     raised.fetch_or(bit);
   }
-  // five stages of x and seven of weights at ranks up to 64, else four and five:
-  // a tile of several adapters takes more of the latter
-  s.x_stages = s.w_stage <= 8192 ? 5 : 4;
+  // four stages of x, and as many of weights as fit beside them: with five and seven
+  // at rank 64 a tile of two adapters waited for weights (16,384 rows backwards 170
+  // us, four and eleven 165)
+  s.x_stages = 4;
   s.stages = (kShrinkSmem - 1024 - s.x_stages * 2 * kXBytes) / s.w_stage;
   if (s.stages > kMaxStages) s.stages = kMaxStages;
   const long sms = sm_count();
@@ -1196,7 +1197,7 @@ situ_status launch_tiles(int dtype, bool f32, const void* rows, int64_t ld_rows,
   s.run = f32 ? 1024 / kChunk : s.chunks;
   x.chunks = s.chunks;
   const int boxes = (s.r + 63) / 64;
-  s.w_stage = boxes * 8192;
+  s.w_stage = TRANS ? boxes * 8192 : (s.r16 * 128 + 1023) / 1024 * 1024;
   const int rrows = s.r16 < 64 ? s.r16 : 64;
   const int cols = cols_of(f32);
   x.w_stage = TRANS ? boxes * (cols / 64) * rrows * 128 : boxes * cols * 128;
