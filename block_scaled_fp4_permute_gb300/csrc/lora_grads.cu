@@ -275,39 +275,61 @@ outer_kernel(const __grid_constant__ OuterMaps m, const OuterParams p) {
 }
 
 // The tile that begins in CTA blockIdx.x and goes on in later ones: its sums
-// added up in their order.
+// added up in their order, all of a tile's loads of two parts in flight (a few at a
+// time took 6 us).  A round without parts comes first, while the predecessor ends:
+// it brings the instructions in.
+constexpr int kJoinThreads = 512;
 template <int DT>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kJoinThreads)
 outer_join_kernel(const OuterParams p) {
   __shared__ int scan[kScanInts];
-  scan_tiles(p.offsets, p.n, p.S, kRows, scan, scan + kMaxGroups + 1, kThreads);
+  scan_tiles(p.offsets, p.n, p.S, kRows, scan, scan + kMaxGroups + 1, kJoinThreads);
   const Deal deal(p, scan, scan + kMaxGroups + 1);
   const long G = gridDim.x, i0 = first_item(blockIdx.x, deal.total, G), i1 = first_item(blockIdx.x + 1, deal.total, G);
-  griddep_wait();
-  if (i0 == i1 || *reinterpret_cast<volatile int*>(p.err) != 0) return;   // no parts where a wait was given up
+  if (i0 == i1) {
+    griddep_wait();
+    return;
+  }
   // the piece that holds the CTA's last item
-  Piece t = deal.at(i1 - 1, deal.total);
-  if (t.from + 1 == t.chunks || t.from >= i1 - i0) return;   // it ends here, or began before
-  const int last = (int)cta_of(i1 - 1 + (t.chunks - t.from - 1), deal.total, G);
-  for (int i = threadIdx.x; i < 128 * p.r / 8; i += kThreads) {
-    const int c = i * 8 / p.r, j = i * 8 - c * p.r;
-    if (t.block * 128 + c >= p.C[t.which]) continue;
-    float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int k = blockIdx.x; k <= last; ++k) {
-      if (first_item(k, deal.total, G) == first_item(k + 1, deal.total, G)) continue;   // more CTAs than items
-      const float4* v =
-          reinterpret_cast<const float4*>(p.parts + (((size_t)k * 2 + (k == (int)blockIdx.x)) * 128 + c) * p.r + j);
-      const float4 a = __ldcg(v), b = __ldcg(v + 1);
-      s[0] += a.x;
-      s[1] += a.y;
-      s[2] += a.z;
-      s[3] += a.w;
-      s[4] += b.x;
-      s[5] += b.y;
-      s[6] += b.z;
-      s[7] += b.w;
+  const Piece t = deal.at(i1 - 1, deal.total);
+  const bool mine = t.from + 1 != t.chunks && t.from < i1 - i0;   // else it ends here, or began before
+  const int last = mine ? (int)cta_of(i1 - 1 + (t.chunks - t.from - 1), deal.total, G) : -1;
+  for (int round = 0; round < 2; ++round) {
+    if (round == 1) {
+      griddep_wait();
+      if (!mine || *reinterpret_cast<volatile int*>(p.err) != 0) return;   // no parts where a wait was given up
     }
-    store16<DT>(p, t, t.block * 128 + c, j, s);
+    const int end = round == 1 ? last : -1;
+    for (int i = threadIdx.x; i < 128 * p.r / 8; i += kJoinThreads) {
+      const int c = i * 8 / p.r, j = i * 8 - c * p.r;
+      const bool in = t.block * 128 + c < p.C[t.which];
+      float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      for (int k0 = blockIdx.x; k0 == (int)blockIdx.x || k0 <= end; k0 += 2) {
+        float4 v[2][2];
+#pragma unroll
+        for (int d = 0; d < 2; ++d) {
+          const int k = k0 + d;
+          // (more CTAs than items)
+          const bool there = in && k <= end && first_item(k, deal.total, G) != first_item(k + 1, deal.total, G);
+          const float4* q =
+              reinterpret_cast<const float4*>(p.parts + (((size_t)k * 2 + (k == (int)blockIdx.x)) * 128 + c) * p.r + j);
+          v[d][0] = there ? __ldcg(q) : make_float4(0.f, 0.f, 0.f, 0.f);
+          v[d][1] = there ? __ldcg(q + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int d = 0; d < 2; ++d) {
+          s[0] += v[d][0].x;
+          s[1] += v[d][0].y;
+          s[2] += v[d][0].z;
+          s[3] += v[d][0].w;
+          s[4] += v[d][1].x;
+          s[5] += v[d][1].y;
+          s[6] += v[d][1].z;
+          s[7] += v[d][1].w;
+        }
+      }
+      if (in && round == 1) store16<DT>(p, t, t.block * 128 + c, j, s);
+    }
   }
 }
 
@@ -327,7 +349,7 @@ cudaError_t launch_dt(const OuterMaps& m, const OuterParams& p, int smem, cudaSt
   const unsigned grid = (unsigned)sm_count();
   outer_kernel<DT><<<grid, kThreads, smem, st>>>(m, p);
   e = cudaGetLastError();
-  return e != cudaSuccess ? e : launch_pdl(outer_join_kernel<DT>, dim3(grid), dim3(kThreads), 0, st, p);
+  return e != cudaSuccess ? e : launch_pdl(outer_join_kernel<DT>, dim3(grid), dim3(kJoinThreads), 0, st, p);
 }
 
 }  // namespace
