@@ -694,6 +694,7 @@ expand_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = holder[0];
   const bool dead = holder[1] != 0;
+  griddep_launch_dependents();       // of the backward pass: the gradients' CTAs fetch x and dy where these have left
   const uint32_t wbase = sbase + p.u_stages * p.u_bytes, ybase = wbase + p.stages * p.w_stage;
   const int rboxes = (p.r + 63) / 64, steps = p.r16 / 16;
   const int rrows = min(64, p.r16);                     // TRANS: contraction rows of a box

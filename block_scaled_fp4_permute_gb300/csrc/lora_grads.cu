@@ -127,43 +127,53 @@ outer_kernel(const __grid_constant__ OuterMaps m, const OuterParams p) {
   if (warp == 0 && !dead) {
     // ---------------- copies ----------------
     const bool leader = elect_one();
-    Turns r(p.stages);
     bool ok = true;
-    for (long i = i0; i < i1 && ok;) {
-      const Piece t = deal.at(i, i1);
-      i += t.to - t.from;
-      const int c0 = t.block * 128, wboxes = c0 + 64 < p.C[t.which] ? 2 : 1;
-      for (int k = t.from; k < t.to; ++k, r.next()) {
-        if (r.again() && !warp_wait(empty(r.s), r.ph ^ 1, p.err, 121)) {
-          ok = false;
-          break;
-        }
-        const uint32_t to = sbase + r.s * stage;
-        const int left = t.rows - k * kRows, row = t.row0 + k * kRows;
-        if (left >= kRows) {
-          if (leader) {
-            mbar_expect_tx(full(r.s), (wboxes + nboxes) * kRows * 128);
-            for (int h = 0; h < wboxes; ++h) copy_2d<1>(to + h * kRows * 128, &m.wide[t.which], c0 + 64 * h, row, full(r.s));
-            for (int h = 0; h < nboxes; ++h) copy_2d<1>(to + kWide + h * kRows * 128, &m.narrow[t.which], 64 * h, row, full(r.s));
+    // of the chunks [a, b), x or dy and v or u
+    auto copy = [&](long a, long b, Turns& r, bool wide, bool narrow) {
+      for (long i = a; i < b && ok;) {
+        const Piece t = deal.at(i, b);
+        i += t.to - t.from;
+        const int c0 = t.block * 128, wboxes = c0 + 64 < p.C[t.which] ? 2 : 1;
+        for (int k = t.from; k < t.to; ++k, r.next()) {
+          if (r.again() && !warp_wait(empty(r.s), r.ph ^ 1, p.err, 121)) {
+            ok = false;
+            break;
           }
-        } else {
-          const int fours = (left + 15) / 16 * 4, boxes = wboxes + nboxes;
-          if (leader) mbar_expect_tx(full(r.s), boxes * fours * 512);
-          __syncwarp();
-          for (int g = lane; g < boxes * fours; g += 32) {
-            const int box = g / fours, f = 4 * (g - box * fours);
-            int at[4];
+          const uint32_t to = sbase + r.s * stage;
+          const int left = t.rows - k * kRows, row = t.row0 + k * kRows;
+          const int fours = left >= kRows ? kRows / 4 : (left + 15) / 16 * 4;
+          if (leader && wide) mbar_expect_tx(full(r.s), (wboxes + nboxes) * fours * 512);
+          if (left >= kRows) {
+            if (leader) {
+              for (int h = 0; h < wboxes && wide; ++h) copy_2d<1>(to + h * kRows * 128, &m.wide[t.which], c0 + 64 * h, row, full(r.s));
+              for (int h = 0; h < nboxes && narrow; ++h)
+                copy_2d<1>(to + kWide + h * kRows * 128, &m.narrow[t.which], 64 * h, row, full(r.s));
+            }
+          } else {
+            __syncwarp();
+            const int from = wide ? 0 : wboxes, end = wboxes + (narrow ? nboxes : 0);
+            for (int g = from * fours + lane; g < end * fours; g += 32) {
+              const int box = g / fours, f = 4 * (g - box * fours);
+              int at[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) at[j] = f + j < left ? row + f + j : p.S;
-            const bool wide = box < wboxes;
-            copy_rows4<1>(to + (wide ? box : 2 + box - wboxes) * kRows * 128 + f * 128,
-                          wide ? &m.wide1[t.which] : &m.narrow1[t.which], wide ? c0 + 64 * box : 64 * (box - wboxes), at[0], at[1],
-                          at[2], at[3], full(r.s));
+              for (int j = 0; j < 4; ++j) at[j] = f + j < left ? row + f + j : p.S;
+              const bool x = box < wboxes;
+              copy_rows4<1>(to + (x ? box : 2 + box - wboxes) * kRows * 128 + f * 128,
+                            x ? &m.wide1[t.which] : &m.narrow1[t.which], x ? c0 + 64 * box : 64 * (box - wboxes), at[0], at[1],
+                            at[2], at[3], full(r.s));
+            }
           }
+          __syncwarp();
         }
-        __syncwarp();
       }
-    }
+    };
+    // v is the predecessor's: the first round's x and dy come meanwhile
+    const long first = min(i1, i0 + p.stages);
+    Turns ahead(p.stages), r(p.stages);
+    copy(i0, first, ahead, true, false);
+    griddep_wait();
+    copy(i0, first, r, false, true);
+    copy(first, i1, r, true, true);
     leave(
         ok, [&] { return r.last([&](int j, uint32_t ph) { return warp_wait(empty(j), ph, p.err, 122); }); },
         [&] { r.last([&](int j, uint32_t ph) { return drain_wait(full(j), ph); }); });
@@ -264,6 +274,7 @@ outer_kernel(const __grid_constant__ OuterMaps m, const OuterParams p) {
       }
     }
   }
+  if (dead) griddep_wait();
   griddep_launch_dependents();
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
@@ -347,8 +358,7 @@ cudaError_t launch_dt(const OuterMaps& m, const OuterParams& p, int smem, cudaSt
     raised.fetch_or(bit);
   }
   const unsigned grid = (unsigned)sm_count();
-  outer_kernel<DT><<<grid, kThreads, smem, st>>>(m, p);
-  e = cudaGetLastError();
+  e = launch_pdl(outer_kernel<DT>, dim3(grid), dim3(kThreads), smem, st, m, p);
   return e != cudaSuccess ? e : launch_pdl(outer_join_kernel<DT>, dim3(grid), dim3(kJoinThreads), 0, st, p);
 }
 
