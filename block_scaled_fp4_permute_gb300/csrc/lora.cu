@@ -1236,12 +1236,17 @@ situ_status launch_tiles(int dtype, bool f32, const void* rows, int64_t ld_rows,
   return e == cudaSuccess ? SITU_OK : SITU_ERR_CUDA;
 }
 
-// A cluster per row, or tiles.  A row's cluster reads its adapter, about 0.07 us a
-// row at rank 16 (3584 x 6144, four times that at rank 64), whatever the others
-// take; tiles take 15 us or more, and share one adapter's weights but go through
-// each of several: 512 rows at rank 16 of one adapter 37 us by rows and 19 in tiles,
-// of 16 in any order 37 and 48, 128 rows of 16 at rank 64 48 and 57.
-bool by_rows(int S, int r, int n) { return S <= 64 || (long)S * r <= 512l * (n < 16 ? n : 16); }
+// A cluster per row, or tiles.  A row's cluster reads its adapter whatever the
+// others take: 4 us and about 0.07 a row at rank 16, in proportion to the rank above
+// (3584 x 6144).  Tiles take 15 us, and about 1.3 at low ranks and 2.6 at 128 for each
+// adapter that rows of a tile take, in any order at most n of them; up to 48 here, for
+// the more there are the sooner they are sorted.  By rows and in tiles, us: 128 rows
+// at rank 16 of one adapter 14 and 16, 256 20 and 17, 512 of 16 adapters 37 and 52 (30
+// where they come in runs); at rank 64 32 rows of one 14 and 17, 64 22 and 17, 128
+// of 64 48 and 103; at rank 128 64 of one 40 and 21, of 16 39 and 52.
+bool by_rows(int S, int r, int n) {
+  return (long)S * (r < 16 ? 16 : r) <= 2700 + 5l * (n < 48 ? n : 48) * (r + 128) / 2;
+}
 // Whether rows named by ids may be sorted by adapter first: the look at them and
 // the sorting cost 8 to 17 us, which few adapters in any order hardly do.
 bool sortable(const int32_t* ids, int n) { return ids && n > 16 && n <= SITU_MAX_LOCAL_EXPERTS; }

@@ -542,7 +542,9 @@ def lora_bar(y, both, second, K, r, dtype, out_dtype, rows):
 @pytest.mark.parametrize("S,K,N,r,n", [(1, 8, 8, 8, 1), (1, 3584, 768, 16, 3), (5, 264, 1000, 24, 2), (33, 72, 136, 128, 40),
                                        (64, 128, 64, 40, 7), (65, 64, 128, 8, 2), (130, 200, 264, 16, 3), (300, 1032, 72, 32, 300),
                                        (700, 136, 1160, 48, 4), (1000, 520, 520, 64, 11), (257, 2048, 392, 128, 5),
-                                       (2100, 64, 64, 104, 1), (3000, 136, 200, 24, 40), (2049, 520, 1032, 16, 700)])
+                                       (2100, 64, 64, 104, 1), (3000, 136, 200, 24, 40), (2049, 520, 1032, 16, 700),
+                                       (129, 64, 64, 128, 1), (200, 72, 136, 64, 2), (400, 64, 72, 128, 20),
+                                       (60001, 64, 72, 24, 5), (40007, 72, 64, 128, 3), (40000, 64, 136, 16, 30)])
 @pytest.mark.parametrize("dtype,out_dtype", [(BF16, BF16), (F16, F16), (BF16, F32), (F16, F32)])
 @pytest.mark.parametrize("order", ["mixed", "runs"])
 def test_lora(S, K, N, r, n, dtype, out_dtype, order):
