@@ -940,6 +940,23 @@ def situ_moe_router_backward(router_logits: torch.Tensor, topk_ids: torch.Tensor
     return out
 
 
+def _graphed(f, *args):
+    """f(*args) of an autograd function.  torch adds a leaf's gradient on the
+    stream on which the first of its living graphs was built.  A backward pass
+    captured on another stream would draw that one into the capture, which can
+    end the process, so the captured forward pass is refused."""
+    nodes = []
+    if torch.is_grad_enabled():
+        for t in args:
+            if isinstance(t, torch.Tensor) and t.is_cuda and t.requires_grad and t.is_leaf:
+                node, stream = torch.autograd.graph.get_gradient_edge(t).node, _raw_stream(t.get_device())
+                nodes.append(node)   # alive until f's graph holds it
+                if node.metadata.setdefault("situ_moe stream", stream) != stream and torch.cuda.is_current_stream_capturing():
+                    raise RuntimeError("captured on one stream while a graph of the same leaf, built on another, is alive: "
+                                       "drop what holds it (outputs, losses) first")
+    return f(*args)
+
+
 class _BalancedRoute(torch.autograd.Function):
     @staticmethod
     def forward(ctx, router_logits, top_k, renormalize, mask, coef):
@@ -966,7 +983,7 @@ class _BalancedRoute(torch.autograd.Function):
 def balanced_route(router_logits: torch.Tensor, top_k: int, *, renormalize: bool = True, mask=None, coef: float = 0.01):
     """situ_moe_route_topk for training: (topk_ids, topk_weights, counts, loss),
     the weights and the balance loss differentiable in the logits."""
-    return _BalancedRoute.apply(router_logits, top_k, renormalize, mask, coef)
+    return _graphed(_BalancedRoute.apply, router_logits, top_k, renormalize, mask, coef)
 
 
 def situ_moe_save_mxfp8(x: torch.Tensor, *, out=None, stream=None):
@@ -1144,7 +1161,7 @@ def expert_ffn(x: torch.Tensor, w1: torch.Tensor, w2: torch.Tensor, offsets: tor
         raise ValueError('keep must be "mxfp8" or "16bit"')
     if w1.dim() != 3 or w2.dim() != 3:
         raise ValueError("w1 must be [E, 2I, H] and w2 [E, H, I]")
-    return _ExpertFfn.apply(x, w1, w2, offsets, p0, p1, activation, keep)
+    return _graphed(_ExpertFfn.apply, x, w1, w2, offsets, p0, p1, activation, keep)
 
 
 def _adapters(x, a, b, scale, index):
@@ -1285,7 +1302,7 @@ def lora_linear(base: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.T
     base, x, a and b (up to 1,024 adapters)."""
     if a.shape[0] > 1024:
         raise ValueError("the gradients take up to 1024 adapters")
-    return _LoraLinear.apply(base, x, a, b, offsets, scale)
+    return _graphed(_LoraLinear.apply, base, x, a, b, offsets, scale)
 
 
 class Layer:

@@ -24,8 +24,11 @@
 // adapters are many, they are sorted first and copied row by row.
 // (mma.sync gave 266 multiply-adds a clock and SM, a thirtieth of tcgen05's: it held
 // a shrink at rank 32 at 28 us where the bytes take 9.)
-// Measured (bf16, 16,384 rows, 3584 -> 6144, rank 64, four adapters): shrink 36 us
-// (117 MB of x), expand 77 (403 MB; a plain copy 62); backwards 58 and 51.
+// Measured (bf16, 16,384 rows, 3584 -> 6144, rank 64, four adapters): 104 us forwards
+// for 519 MB (5.0 TB/s), 162 backwards with the gradients for 753 MB.  The shrink's
+// CTAs end 29 us after its start (32 where a tile has rows of two adapters) and
+// the expand streams 403 MB in 55; the rest is what begins and ends: first loads,
+// u's parts and the first sums.
 //
 // u enters the second product in 16 bits.  For 16-bit results it is rounded
 // once (half an ulp of u, as y itself is); for fp32 results it goes as a sum of
@@ -1110,8 +1113,8 @@ struct Maps {
 // more adapters than sorted.  Counted over up to kLooked tiles: neighbours that
 // differ, and one, but no more than there are adapters; sorted, a tile takes one
 // and each adapter one more.  Five per tile are as many as the sorted rows' way of
-// copying costs (16,384 rows in any order of 4 adapters 159 us as they are and 207
-// sorted, of 9 309 and 209, of 256 3406 and 246; in runs of 256 150).
+// copying costs (16,384 rows at rank 16 in any order of 4 adapters 159 us as they are
+// and 202 sorted, of 9 311 and 203, of 256 3430 and 239; in runs of 256 150 and 237).
 constexpr int kLooked = 1024;
 __global__ void __launch_bounds__(1024)
 mixed_kernel(const int32_t* ids, int S, int n, int32_t* mixed) {
@@ -1248,7 +1251,10 @@ bool by_rows(int S, int r, int n) {
   return (long)S * (r < 16 ? 16 : r) <= 2700 + 5l * (n < 48 ? n : 48) * (r + 128) / 2;
 }
 // Whether rows named by ids may be sorted by adapter first: the look at them and
-// the sorting cost 8 to 17 us, which few adapters in any order hardly do.
+// the sorting cost 8 to 17 us also where the rows are then taken as they are
+// (16,384 rows in runs of 64 adapters 124 us, 108 without).  With up to 16 adapters,
+// more often in runs than not, they are not looked at: in any order 9 take 311 us and
+// 16 515, where the sort would make it 203.
 bool sortable(const int32_t* ids, int n) { return ids && n > 16 && n <= SITU_MAX_LOCAL_EXPERTS; }
 // its scratch: *mixed; numbers, places; counts, offsets, the permute's own
 size_t sort_ints(int S, int n) { return 1 + 2 * (size_t)S + 2 * (size_t)n + 1 + permute_scratch_bytes(S, 1, n) / 4; }

@@ -746,7 +746,8 @@ situ_status situ_moe_gated_backward(const situ_gated_args* args, void* stream);
  * second product rounded to 16 bits for 16-bit results, with 22 bits or more
  * for fp32 ones.  u (or NULL) receives u [S, 2, r] in two terms of the operands'
  * type, the first u rounded, the second what that leaves (zeros without an
- * adapter), which the gradients take.  For experts, an adapter per
+ * adapter), which the gradients take.  What is written overlaps no other
+ * operand.  For experts, an adapter per
  * (request's adapter, expert) pair is one of n, its rows in any order.
  * Results do not depend on the order of execution, nor on what other rows'
  * adapters hold.  K, N multiples of 8, rows strided by multiples of 8 elements
@@ -781,7 +782,8 @@ situ_status situ_moe_lora(const situ_lora_args* args, void* workspace, size_t wo
  * dx0 (or NULL: zeros) is the shared projection's gradient, dx may be it, both
  * of the operands' type or fp32; da [n, r, K] and db [n, N, r] are of the
  * operands' type, rounded once, zeros for an adapter without rows (v is taken in
- * two terms as u is).  Results do not depend on the order of execution.  S == 0
+ * two terms as u is).  dx overlaps neither dy nor x: these are still read
+ * while it is written.  Results do not depend on the order of execution.  S == 0
  * sets da and db to zeros. */
 typedef struct situ_lora_backward_args {
   int32_t dtype, dx_dtype;

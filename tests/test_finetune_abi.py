@@ -119,7 +119,7 @@ def test_restore_refusals(lib, args, status):
 
 
 def lora(lib, ws=0xf000, nbytes=1 << 30, **over):
-    a = dict(dtype=0, out_dtype=0, S=200, K=64, N=128, r=16, n=4, x=0x1000, ldx=64, a=0x2000, b=0x3000, ids=0x4000,
+    a = dict(dtype=0, out_dtype=0, S=2000, K=64, N=128, r=16, n=4, x=0x1000, ldx=64, a=0x2000, b=0x3000, ids=0x4000,
              offsets=None, scale=None, base=0x5000, ld_base=128, out=0x6000, ldo=128, u=None, device_status=0xd000)
     a.update(over)
     return lib.situ_moe_lora(ctypes.byref(B.SituLoraArgs(**a)), ws, nbytes, None)

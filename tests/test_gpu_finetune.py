@@ -906,6 +906,37 @@ def test_a_training_step_captured_and_replayed():
         assert torch.equal(got_, want)
 
 
+def test_a_capture_beside_a_living_graph_of_the_same_leaves_is_refused():
+    g = gen(6)
+    S, K, N, r = 300, 72, 64, 8
+    x, dy = normal(g, S, K), normal(g, S, N)
+    a, b = normal(g, 2, r, K).requires_grad_(), normal(g, 2, N, r).requires_grad_()
+    off = offsets_of([100, 200])
+
+    def run():
+        a.grad = b.grad = None
+        y = B.lora_linear(torch.zeros(S, N, dtype=BF16, device="cuda"), x, a, b, off)
+        return y, a, b
+
+    y = run()[0]                                    # a living graph, of the current stream
+    again = run()[0]                                # another beside it is fine
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with pytest.raises(RuntimeError, match="alive"):
+        with torch.cuda.graph(graph):
+            run()
+    again.backward(dy)
+    want = a.grad.clone(), b.grad.clone()
+    del y, again
+    a.grad = b.grad = None
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()[0].backward(dy)
+    graph.replay()
+    assert torch.equal(a.grad, want[0]) and torch.equal(b.grad, want[1])
+
+
 def test_no_work_after_a_wait_was_given_up():
     g = gen(7)
     S, K, N, r, n = 300, 72, 136, 16, 3
