@@ -1239,23 +1239,27 @@ situ_status launch_tiles(int dtype, bool f32, const void* rows, int64_t ld_rows,
   return e == cudaSuccess ? SITU_OK : SITU_ERR_CUDA;
 }
 
-// A cluster per row, or tiles.  A row's cluster reads its adapter whatever the
-// others take: 4 us and about 0.07 a row at rank 16, in proportion to the rank above
-// (3584 x 6144).  Tiles take 15 us, and about 1.3 at low ranks and 2.6 at 128 for each
-// adapter that rows of a tile take, in any order at most n of them; up to 48 here, for
-// the more there are the sooner they are sorted.  By rows and in tiles, us: 128 rows
-// at rank 16 of one adapter 14 and 16, 256 20 and 17, 512 of 16 adapters 37 and 52 (30
-// where they come in runs); at rank 64 32 rows of one 14 and 17, 64 22 and 17, 128
-// of 64 48 and 103; at rank 128 64 of one 40 and 21, of 16 39 and 52.
-bool by_rows(int S, int r, int n) {
-  return (long)S * (r < 16 ? 16 : r) <= 2700 + 5l * (n < 48 ? n : 48) * (r + 128) / 2;
-}
+constexpr int kFew = 16;            // adapters
 // Whether rows named by ids may be sorted by adapter first: the look at them and
 // the sorting cost 8 to 17 us also where the rows are then taken as they are
 // (16,384 rows in runs of 64 adapters 124 us, 108 without).  With up to 16 adapters,
 // more often in runs than not, they are not looked at: in any order 9 take 311 us and
 // 16 515, where the sort would make it 203.
-bool sortable(const int32_t* ids, int n) { return ids && n > 16 && n <= SITU_MAX_LOCAL_EXPERTS; }
+bool sortable(const int32_t* ids, int n) { return ids && n > kFew && n <= SITU_MAX_LOCAL_EXPERTS; }
+// A cluster per row, or tiles.  A row's cluster reads its adapter whatever the
+// others take: 4 us and about 0.07 a row at rank 16, in proportion to the rank above
+// (3584 x 6144).  Tiles take 15 us, and about 1.3 at low ranks and 2.6 at 128 for each
+// adapter that rows of a tile take: in any order at most n of them (no more than 48
+// tell), sorted, for 16 us, as many as 256 rows hold.  By rows and in tiles, us: 128
+// rows at rank 16 of one adapter 14 and 16, 256 20 and 17, 512 of 16 adapters 37 and 52
+// (30 where they come in runs), 1,024 of 64 70 and 62; at rank 64 32 rows of one 14
+// and 17, 64 22 and 17, 128 of 64 48 and 103; at rank 128 64 of one 40 and 21, of 16
+// 39 and 52.
+bool by_rows(int S, int r, int n) {
+  const float each = 1.3f * (1.f + r / 128.f), mixed = each * (n < 48 ? n : 48);
+  const float sorted = n > kFew && n <= SITU_MAX_LOCAL_EXPERTS ? 16.f + each * (1.f + 256.f * n / S) : mixed;
+  return 4.f + (float)S * (r < 16 ? 16 : r) / 244.f <= 15.f + (mixed < sorted ? mixed : sorted);
+}
 // its scratch: *mixed; numbers, places; counts, offsets, the permute's own
 size_t sort_ints(int S, int n) { return 1 + 2 * (size_t)S + 2 * (size_t)n + 1 + permute_scratch_bytes(S, 1, n) / 4; }
 
@@ -1279,7 +1283,7 @@ bool bad_sizes(int S, int K, int N, int r, int n) {
 extern "C" size_t situ_moe_lora_workspace_size(int32_t S, int32_t K, int32_t N, int32_t r, int32_t n) {
   using namespace situ;
   if (bad_sizes(S, K, N, r, n) || S == 0 || by_rows(S, r, n)) return 0;
-  return part_bytes(S, K, r) + (n > 16 && n <= SITU_MAX_LOCAL_EXPERTS ? (sort_ints(S, n) * 4 + 31) / 32 * 32 : 0);
+  return part_bytes(S, K, r) + (n > kFew && n <= SITU_MAX_LOCAL_EXPERTS ? (sort_ints(S, n) * 4 + 31) / 32 * 32 : 0);
 }
 
 extern "C" situ_status situ_moe_lora(const situ_lora_args* a, void* workspace, size_t workspace_bytes, void* stream) {
