@@ -34,6 +34,12 @@ namespace {
 
 constexpr int kFwdThreads = 512;     // one CTA per SM, so that there are few partial sums
 constexpr int kBackThreads = 256;    // three CTAs per SM
+// One more of either where rows are short (up to 256 columns: a chain of reductions
+// each) and many: 65,536 x 130, top-6, 30 + 33 us without and 24 + 30 with them;
+// 8,192 x 256 11 + 9 and 12 + 10.
+constexpr int fwd_ctas(int nv) { return nv <= 2 ? 2 : 1; }
+constexpr int back_ctas(int nv) { return nv <= 2 ? 4 : 3; }
+constexpr int kManyRows = 16, kManyBackRows = 8;   // of a group
 constexpr int kMaxExperts = SITU_MAX_LOCAL_EXPERTS;
 constexpr int kFinalCtas = 8;        // of the joining kernel's one cluster
 constexpr int kFinalThreads = 512;
@@ -96,13 +102,27 @@ struct Group {
   }
 };
 
-// Columns 4 (lane + L j) .. + 3 of a row, `none` past its end.
+// Column i of a lane's j-th four: neighbours where rows are read 16 bytes a lane
+// (VEC), else a lane's width apart, so that a load's lanes are neighbours (35,954 x
+// 729, both passes: 81 us with fours, 77 so).
+template <int L, bool VEC>
+__device__ __forceinline__ int column(int lane, int j, int i) {
+  return VEC ? 4 * (lane + L * j) + i : lane + L * (4 * j + i);
+}
+template <int L, bool VEC>
+__device__ __forceinline__ float4 columns(const float* row, int lane, int j) {
+  return VEC ? *reinterpret_cast<const float4*>(row + 4 * (lane + L * j))
+             : make_float4(row[lane + L * 4 * j], row[lane + L * (4 * j + 1)], row[lane + L * (4 * j + 2)],
+                           row[lane + L * (4 * j + 3)]);
+}
+
+// A lane's columns of a row, `none` past its end.
 template <int L, int NV, bool VEC>
 __device__ __forceinline__ void load_row(float (&v)[4 * NV], const float* row, int lane, int E, float none) {
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int c = 4 * (lane + L * j);
     if (VEC) {
+      const int c = column<L, VEC>(lane, j, 0);
       const float4 x = c < E ? __ldg(reinterpret_cast<const float4*>(row + c)) : make_float4(none, none, none, none);
       v[4 * j] = x.x;
       v[4 * j + 1] = x.y;
@@ -110,7 +130,10 @@ __device__ __forceinline__ void load_row(float (&v)[4 * NV], const float* row, i
       v[4 * j + 3] = x.w;
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[4 * j + i] = c + i < E ? __ldg(row + c + i) : none;
+      for (int i = 0; i < 4; ++i) {
+        const int c = column<L, VEC>(lane, j, i);
+        v[4 * j + i] = c < E ? __ldg(row + c) : none;
+      }
     }
   }
 }
@@ -119,7 +142,7 @@ __device__ __forceinline__ float fmax_op(float a, float b) { return fmaxf(a, b);
 __device__ __forceinline__ float add_op(float a, float b) { return a + b; }
 
 template <int L, int NV, bool VEC>
-__global__ void __launch_bounds__(kFwdThreads, 1)
+__global__ void __launch_bounds__(kFwdThreads, fwd_ctas(NV))
 balance_kernel(BalanceParams p) {
   constexpr int kGroups = kFwdThreads / L, V = 4 * NV;
   extern __shared__ float smem[];              // column sums [E], counts [E]
@@ -187,7 +210,7 @@ balance_kernel(BalanceParams p) {
         for (int j = 0; j < NV; ++j)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int c = 4 * (g.lane + L * j) + i;
+            const int c = column<L, VEC>(g.lane, j, i);
             if (c < p.E) sum_p[c] += acc[4 * j + i];
           }
       }
@@ -321,10 +344,10 @@ balance_join_kernel(BalanceParams p, int parts) {
     *p.loss = tok > 0 ? (float)((double)p.coef * p.E * t / (tok * tok * p.k)) : 0.f;
   }
 }
-static_assert(kMaxExperts / 4 / kFinalCtas <= kFinalThreads && kSms <= kFinalThreads, "a thread per four columns, per part");
+static_assert(kMaxExperts / 4 / kFinalCtas <= kFinalThreads && 2 * kSms <= kFinalThreads, "a thread per four columns, per part");
 
 template <int L, int NV, bool VEC>
-__global__ void __launch_bounds__(kBackThreads, 3)
+__global__ void __launch_bounds__(kBackThreads, back_ctas(NV))
 router_back_kernel(RouterBackParams p) {
   constexpr int kGroups = kBackThreads / L, V = 4 * NV, kPitch = 4 * L * NV;
   extern __shared__ float4 smem4[];            // a row of the chosen slots' terms per group, zeros between rows
@@ -342,7 +365,7 @@ router_back_kernel(RouterBackParams p) {
     for (int c = threadIdx.x; c < kPitch; c += kBackThreads) F_s[c] = p.dloss && c < p.E ? (float)p.counts[c] * gl : 0.f;
   }
   __syncthreads();
-  auto F4 = [&](int j) { return *reinterpret_cast<const float4*>(F_s + 4 * (g.lane + L * j)); };
+  auto F4 = [&](int j) { return columns<L, VEC>(F_s, g.lane, j); };
   int turn = 0;
   const long step = (long)gridDim.x * kGroups;
   const long first = (long)blockIdx.x * kGroups + g.id;
@@ -405,22 +428,22 @@ router_back_kernel(RouterBackParams p) {
     }
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = 4 * (g.lane + L * j);
-      float4 x = p.dw ? *reinterpret_cast<const float4*>(mine + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+      float4 x = p.dw ? columns<L, VEC>(mine, g.lane, j) : make_float4(0.f, 0.f, 0.f, 0.f);
       const float4 F = keep ? F4(j) : make_float4(0.f, 0.f, 0.f, 0.f);
       x.x = fmaf(v[4 * j], F.x - sub, x.x);
       x.y = fmaf(v[4 * j + 1], F.y - sub, x.y);
       x.z = fmaf(v[4 * j + 2], F.z - sub, x.z);
       x.w = fmaf(v[4 * j + 3], F.w - sub, x.w);
       if (!have) continue;
+      const int c = column<L, VEC>(g.lane, j, 0);
       float* o = p.out + (size_t)t * p.ldo + c;
       if (VEC) {
         if (c < p.E) *reinterpret_cast<float4*>(o) = x;
       } else {
         if (c < p.E) o[0] = x.x;
-        if (c + 1 < p.E) o[1] = x.y;
-        if (c + 2 < p.E) o[2] = x.z;
-        if (c + 3 < p.E) o[3] = x.w;
+        if (c + L < p.E) o[L] = x.y;
+        if (c + 2 * L < p.E) o[2 * L] = x.z;
+        if (c + 3 * L < p.E) o[3 * L] = x.w;
       }
     }
     if (p.dw) {
@@ -454,15 +477,17 @@ cudaError_t with_shape(int E, bool vec, F&& f) {
 #undef SITU_SHAPE
 }
 
-int grid_of(int T, int E, int threads, int most) {
+// CTAs for T rows: `ctas` to an SM, `more` where E is short and a group would take more than `many` rows
+int grid_of(int T, int E, int threads, int ctas, int more, int many) {
   const int groups = threads / (E <= 128 ? 16 : E <= 1024 ? 32 : 128);
   const long rows = (T + groups - 1) / groups;
+  const long most = kSms * (E <= 256 && rows > (long)many * ctas * kSms ? more : ctas);
   return (int)(rows < 1 ? 1 : rows > most ? most : rows);
 }
 // One CTA does the whole forward up to this many rows per group: a second
 // launch costs about 3 us, as do four rows in turn.
 int forward_grid(int T, int E) {
-  const int g = grid_of(T, E, kFwdThreads, kSms);
+  const int g = grid_of(T, E, kFwdThreads, fwd_ctas(8), fwd_ctas(1), kManyRows);
   return g <= 4 ? 1 : g;
 }
 
@@ -570,7 +595,7 @@ extern "C" situ_status situ_moe_router_backward(const situ_router_backward_args*
       const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
       if (e != cudaSuccess) return e;
     }
-    k<<<grid_of(p.T, E, kBackThreads, 3 * kSms), kBackThreads, kSmem, (cudaStream_t)stream>>>(p);
+    k<<<grid_of(p.T, E, kBackThreads, back_ctas(8), back_ctas(1), kManyBackRows), kBackThreads, kSmem, (cudaStream_t)stream>>>(p);
     return cudaGetLastError();
   });
   return e == cudaSuccess ? SITU_OK : SITU_ERR_CUDA;

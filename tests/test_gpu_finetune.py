@@ -103,7 +103,7 @@ def p_error(logits):
 @pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 8, 2), (32, 8, 8), (3, 3, 2), (70, 64, 4), (257, 65, 5), (300, 128, 16),
                                    (1000, 130, 6), (513, 256, 8), (95, 385, 3), (2000, 512, 2), (129, 770, 16),
                                    (4099, 896, 16), (300, 1024, 10), (77, 1025, 3), (64, 2048, 16), (41, 2052, 7),
-                                   (33, 4096, 16), (9, 4095, 16)])
+                                   (33, 4096, 16), (9, 4095, 16), (40001, 130, 6), (40000, 256, 8), (90000, 37, 3)])
 @pytest.mark.parametrize("renorm", [True, False])
 @pytest.mark.parametrize("masked", [False, True])
 def test_router(T, E, k, renorm, masked):
