@@ -822,11 +822,18 @@ def _size(name, index, *args) -> int:
         return getattr(_lib or lib(), name)(*args)
 
 
-def _scratch(n: int, index: int):
+def _new(index: int):
+    """_empty on GPU ``index``, the device looked at once for several tensors."""
+    if _empty_cuda is not None and _current_device() == index:
+        return _empty_cuda
+    return lambda shape, strides, dtype: torch.empty(shape, dtype=dtype, device=f"cuda:{index}")
+
+
+def _scratch(n: int, new):
     """(tensor or None, pointer or None) of n bytes; the caller keeps the tensor until the call is enqueued."""
     if n == 0:
         return None, None
-    t = _empty((n,), (1,), torch.uint8, index)
+    t = new((n,), (1,), torch.uint8)
     return t, t.data_ptr()
 
 
@@ -887,10 +894,11 @@ def situ_moe_balance_loss(router_logits: torch.Tensor, topk_ids: torch.Tensor, *
     if stream is not None:
         return _on_stream(stream, situ_moe_balance_loss, router_logits, topk_ids, mask=mask, coef=coef)
     logits, ld, ids, mask, index, T, E, k = _router(router_logits, topk_ids, mask)
-    loss, counts = _empty((), (), torch.float32, index), _empty((E,), (1,), torch.int32, index)
-    tokens, stats = _empty((1,), (1,), torch.int32, index), _empty((T, 2), (2, 1), torch.float32, index)
+    new = _new(index)
+    loss, counts = new((), (), torch.float32), new((E,), (1,), torch.int32)
+    tokens, stats = new((1,), (1,), torch.int32), new((T, 2), (2, 1), torch.float32)
     n = _balance_bytes(T, E, index)
-    ws, pws = _scratch(n, index)
+    ws, pws = _scratch(n, new)
     args = SituBalanceArgs(logits.data_ptr(), ld, ids.data_ptr(), None if mask is None else mask.data_ptr(), T, E, k, coef,
                            loss.data_ptr(), counts.data_ptr(), tokens.data_ptr(), stats.data_ptr())
     _enqueue("situ_moe_balance_loss", index, ctypes.byref(args), pws, n)
@@ -1002,7 +1010,8 @@ def situ_moe_save_mxfp8(x: torch.Tensor, *, out=None, stream=None):
     nk = -(-K // 32)
     x, px, ldx = _rows(x, 8)
     if out is None:
-        q, scale = _empty((S, K), (K, 1), torch.uint8, index), _empty((S, nk), (nk, 1), torch.uint8, index)
+        new = _new(index)
+        q, scale = new((S, K), (K, 1), torch.uint8), new((S, nk), (nk, 1), torch.uint8)
     else:
         q, scale = out
         for t, want, what in ((q, (S, K), "q"), (scale, (S, nk), "scale")):
@@ -1074,15 +1083,16 @@ def situ_moe_gated(gate_up: torch.Tensor, p0: torch.Tensor, p1: torch.Tensor, of
     if (S | 2 * I) >> 31:
         raise _too_large(S, 2 * I)
     p0, p1, offsets, poff, E = _caps(p0, p1, offsets, index)
+    new = _new(index)
     x, px, ldx = _rows(gate_up, 8)
     if out is None:
-        h, ldh = _empty((S, I), (I, 1), dtype, index), I
+        h, ldh = new((S, I), (I, 1), dtype), I
     else:
         h, ldh = out, _given(out, (S, I), dtype, index, 8)
     q = scale = pq = ps = None
     if save:
         nb = 2 * -(-I // 32)
-        q, scale = _empty((S, 2 * I), (2 * I, 1), torch.uint8, index), _empty((S, nb), (nb, 1), torch.uint8, index)
+        q, scale = new((S, 2 * I), (2 * I, 1), torch.uint8), new((S, nb), (nb, 1), torch.uint8)
         pq, ps = q.data_ptr(), scale.data_ptr()
     args = SituGatedArgs(_DTYPES[dtype], activation, S, I, E, px, ldx, p0.data_ptr(), p1.data_ptr(), poff, h.data_ptr(),
                          ldh, pq, ps, None, 0, None, 0)
@@ -1108,12 +1118,13 @@ def situ_moe_gated_backward(dh: torch.Tensor, q: torch.Tensor, scale: torch.Tens
         raise _too_large(S, 2 * I)
     q, scale = _kept(q, scale, S, 2 * I, 2 * -(-I // 32), index)
     p0, p1, offsets, poff, E = _caps(p0, p1, offsets, index)
+    new = _new(index)
     dh, pdh, ldh = _rows(dh, 8)
     if out is None:
-        out, ldo = _empty((S, 2 * I), (2 * I, 1), dtype, index), 2 * I
+        out, ldo = new((S, 2 * I), (2 * I, 1), dtype), 2 * I
     else:
         ldo = _given(out, (S, 2 * I), dtype, index, 8)
-    h = _empty((S, I), (I, 1), dtype, index) if want_h else None
+    h = new((S, I), (I, 1), dtype) if want_h else None
     args = SituGatedArgs(_DTYPES[dtype], activation, S, I, E, None, 0, p0.data_ptr(), p1.data_ptr(), poff,
                          None if h is None else h.data_ptr(), I, q.data_ptr(), scale.data_ptr(), pdh, ldh, out.data_ptr(),
                          ldo)
@@ -1165,16 +1176,15 @@ def expert_ffn(x: torch.Tensor, w1: torch.Tensor, w2: torch.Tensor, offsets: tor
 
 
 def _adapters(x, a, b, scale, index):
-    """Checks an adapter set beside x [S, K]: (a, b, scale, S, K, N, r, n)."""
+    """Checks an adapter set beside x [S, K]: (a, b, their pointers, scale, S, K, N, r, n)."""
     dtype = x.dtype
     if dtype is not torch.bfloat16 and dtype is not torch.float16 or a.dtype is not dtype or b.dtype is not dtype:
         raise TypeError("x, a and b must be all bf16 or all f16")
-    if x.dim() != 2 or a.dim() != 3 or b.dim() != 3:
-        raise ValueError("needs x [S, K], a [n, r, K] and b [n, N, r]")
-    S, K = x.shape
-    n, r, Ka = a.shape
-    N = b.shape[1]
-    if Ka != K or b.shape != (n, N, r):
+    try:
+        (S, K), (n, r, Ka), (nb, N, rb) = x.shape, a.shape, b.shape
+    except ValueError:
+        raise ValueError("needs x [S, K], a [n, r, K] and b [n, N, r]") from None
+    if Ka != K or nb != n or rb != r:
         raise ValueError(f"needs a [n, r, {K}] and b [n, N, r], not {tuple(a.shape)} and {tuple(b.shape)}")
     if (S | K | N | n) >> 31:
         raise _too_large(S, K, N, n)
@@ -1182,7 +1192,9 @@ def _adapters(x, a, b, scale, index):
         raise ValueError(f"the operands must be on one CUDA device, not on {x.device}, {a.device} and {b.device}")
     if scale is not None:
         scale = _vector(scale, torch.float32, n, "scale", index)
-    return _packed(a)[0], _packed(b)[0], scale, S, K, N, r, n
+    a, pa = _packed(a)
+    b, pb = _packed(b)
+    return a, b, pa, pb, scale, S, K, N, r, n
 
 
 def _beside(t, shape, dtypes, name, index):
@@ -1206,7 +1218,7 @@ def situ_moe_lora(base, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, *, id
         return _on_stream(stream, lambda x, a, b, base, **kw: situ_moe_lora(base, x, a, b, **kw), x, a, b, base, ids=ids,
                           offsets=offsets, scale=scale, out=out, keep=keep)
     index = x.get_device()
-    a, b, scale, S, K, N, r, n = _adapters(x, a, b, scale, index)
+    a, b, pa, pb, scale, S, K, N, r, n = _adapters(x, a, b, scale, index)
     if (ids is None) == (offsets is None):
         raise ValueError("needs one of ids and offsets")
     dtype, pids, poff = x.dtype, None, None
@@ -1224,15 +1236,16 @@ def situ_moe_lora(base, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, *, id
     if base is not None:
         base, pbase, ld_base = _beside(base, (S, N), (dtype, torch.float32), "base", index)
         out_dtype = base.dtype
+    new = _new(index)
     if out is None:
-        out, ldo = _empty((S, N), (N, 1), out_dtype, index), N
+        out, ldo = new((S, N), (N, 1), out_dtype), N
     else:
         ldo = _given(out, (S, N), out_dtype, index, 4 if out_dtype is torch.float32 else 8)
-    u = _empty((S, 2, r), (2 * r, r, 1), dtype, index) if keep else None
+    u = new((S, 2, r), (2 * r, r, 1), dtype) if keep else None
     size = _lora_bytes(S, K, N, r, n, index)
-    ws, pws = _scratch(size, index)
-    args = SituLoraArgs(_DTYPES[dtype], _DTYPES.get(out_dtype, -1), S, K, N, r, n, px, ldx, a.data_ptr(), b.data_ptr(), pids,
-                        poff, None if scale is None else scale.data_ptr(), pbase, ld_base, out.data_ptr(), ldo,
+    ws, pws = _scratch(size, new)
+    args = SituLoraArgs(_DTYPES[dtype], _DTYPES.get(out_dtype, -1), S, K, N, r, n, px, ldx, pa, pb, pids, poff,
+                        None if scale is None else scale.data_ptr(), pbase, ld_base, out.data_ptr(), ldo,
                         None if u is None else u.data_ptr(), _status_word(index).data_ptr())
     _enqueue("situ_moe_lora", index, ctypes.byref(args), pws, size)
     return (out, u) if keep else out
@@ -1247,7 +1260,7 @@ def situ_moe_lora_backward(dy: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b
     if stream is not None:
         return _on_stream(stream, situ_moe_lora_backward, dy, x, a, b, offsets, u, scale=scale, dx=dx, out=out)
     index = x.get_device()
-    a, b, scale, S, K, N, r, n = _adapters(x, a, b, scale, index)
+    a, b, pa, pb, scale, S, K, N, r, n = _adapters(x, a, b, scale, index)
     dtype = x.dtype
     if dy.dtype is not dtype or u.dtype is not dtype:
         raise TypeError(f"dy and u must be {dtype}, as x")
@@ -1265,15 +1278,16 @@ def situ_moe_lora_backward(dy: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b
     if dx is not None:
         dx, pdx0, ld_dx0 = _beside(dx, (S, K), (dtype, torch.float32), "dx", index)
         dx_dtype = dx.dtype
+    new = _new(index)
     if out is None:
-        out, ldo = _empty((S, K), (K, 1), dx_dtype, index), K
+        out, ldo = new((S, K), (K, 1), dx_dtype), K
     else:
         ldo = _given(out, (S, K), dx_dtype, index, 4 if dx_dtype is torch.float32 else 8)
-    da, db = _empty((n, r, K), (r * K, K, 1), dtype, index), _empty((n, N, r), (N * r, r, 1), dtype, index)
+    da, db = new((n, r, K), (r * K, K, 1), dtype), new((n, N, r), (N * r, r, 1), dtype)
     size = _lora_backward_bytes(S, K, N, r, index)
-    ws, pws = _scratch(size, index)
-    args = SituLoraBackwardArgs(_DTYPES[dtype], _DTYPES.get(dx_dtype, -1), S, K, N, r, n, pdy, ld_dy, px, ldx, a.data_ptr(),
-                                b.data_ptr(), offsets.data_ptr(), None if scale is None else scale.data_ptr(), pu, pdx0,
+    ws, pws = _scratch(size, new)
+    args = SituLoraBackwardArgs(_DTYPES[dtype], _DTYPES.get(dx_dtype, -1), S, K, N, r, n, pdy, ld_dy, px, ldx, pa, pb,
+                                offsets.data_ptr(), None if scale is None else scale.data_ptr(), pu, pdx0,
                                 ld_dx0, out.data_ptr(), ldo, da.data_ptr(), db.data_ptr(), _status_word(index).data_ptr())
     _enqueue("situ_moe_lora_backward", index, ctypes.byref(args), pws, size)
     return out, da, db
