@@ -396,12 +396,6 @@ shrink_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
   auto list_full = [&](int b) { return tail + 32 + 8 * b; };
   auto list_empty = [&](int b) { return tail + 48 + 8 * b; };
   const uint32_t drain = tail + 64;
-  const Rows rows(p);
-  const long total = (long)((rows.count + kShrinkRows - 1) / kShrinkRows) * p.chunks, G = sharers(total, p.shrink_ctas, p.least);
-  const bool shares = blockIdx.x < G;
-  const long i0 = shares ? first_item(blockIdx.x, total, G) : 0, i1 = shares ? first_item(blockIdx.x + 1, total, G) : 0;
-  int e_first = -1;                  // of the first tile: on its way while the barriers are set up
-  if (warp >= 2 && i0 < i1) e_first = tile_adapter(p, rows, (int)(i0 / p.chunks) * kShrinkRows, tid - 64);
   if (tid == 0) {
     holder[1] = (uint32_t)*reinterpret_cast<volatile int*>(p.err);   // an earlier launch gave up a wait: no work then
     prefetch_map(&map_w);
@@ -416,6 +410,13 @@ shrink_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) tmem_alloc<1>(saddr(holder), kTmemCols);
+  if (p.mixed) griddep_wait();       // the rows' order is the predecessor's
+  const Rows rows(p);
+  const long total = (long)((rows.count + kShrinkRows - 1) / kShrinkRows) * p.chunks, G = sharers(total, p.shrink_ctas, p.least);
+  const bool shares = blockIdx.x < G;
+  const long i0 = shares ? first_item(blockIdx.x, total, G) : 0, i1 = shares ? first_item(blockIdx.x + 1, total, G) : 0;
+  int e_first = -1;                  // of the first tile: on its way while the barriers are set up
+  if (warp >= 2 && i0 < i1) e_first = tile_adapter(p, rows, (int)(i0 / p.chunks) * kShrinkRows, tid - 64);
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -1114,31 +1115,99 @@ struct Maps {
 // differ, and one, but no more than there are adapters; sorted, a tile takes one
 // and each adapter one more.  Five per tile are as many as the sorted rows' way of
 // copying costs (16,384 rows at rank 16 in any order of 4 adapters 159 us as they are
-// and 202 sorted, of 9 311 and 203, of 256 3430 and 239; in runs of 256 150 and 237).
+// and 202 sorted, of 9 311 and 205, of 256 3430 and 262; in runs of 256 150 and 237).
 constexpr int kLooked = 1024;
-__global__ void __launch_bounds__(1024)
-mixed_kernel(const int32_t* ids, int S, int n, int32_t* mixed) {
+// by 1,024 threads, the answer in every one
+__device__ __forceinline__ bool is_mixed(const int32_t* ids, int S, int n) {
   __shared__ int found[32];
   const int tiles = (S + kTile - 1) / kTile, step = (tiles + kLooked - 1) / kLooked, looked = (tiles + step - 1) / step;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int sum = 0;
+#pragma unroll 4
   for (int t = warp; t < looked; t += 32) {
     const long r0 = (long)t * step * kTile;
     int changes = 0;
 #pragma unroll
     for (int j = 0; j < kTile / 32; ++j) {
       const long r = r0 + 32 * j + lane;
-      changes += r > r0 && r < S && __ldg(ids + r) != __ldg(ids + r - 1);
+      changes += __popc(__ballot_sync(0xffffffffu, r > r0 && r < S && __ldg(ids + r) != __ldg(ids + r - 1)));
     }
-    sum += min(__reduce_add_sync(0xffffffffu, changes) + 1, n);
+    sum += min(changes + 1, n);
   }
   if (lane == 0) found[warp] = sum;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    long total = 0;
-    for (int w = 0; w < 32; ++w) total += found[w];
-    *mixed = total * tiles / looked > 5l * tiles + n;
+  long total = 0;
+  for (int w = 0; w < 32; ++w) total += found[w];
+  return total * tiles / looked > 5l * tiles + n;
+}
+__global__ void __launch_bounds__(1024)
+mixed_kernel(const int32_t* ids, int S, int n, int32_t* mixed) {
+  const bool yes = is_mixed(ids, S, n);
+  if (threadIdx.x == 0) *mixed = yes;
+}
+
+// The look and, where it says so, the stable sort of up to kSortRows rows by
+// adapter, by one CTA: a warp counts and then places the rows of its share, 32 at
+// a time, in their order.  perm: the rows' numbers; place: of each row, its place
+// (-1: no adapter); *kept: how many have one.
+constexpr int kSortRows = 16384, kSortAdapters = 1024, kSortPitch = 33;   // pitch: of an adapter's counts, a warp each
+__global__ void __launch_bounds__(1024)
+sort_kernel(const int32_t* ids, int S, int n, int32_t* mixed, int32_t* perm, int32_t* place, int32_t* kept) {
+  extern __shared__ int count[];     // [n][kSortPitch], and [n]
+  __shared__ int sums[32];
+  griddep_launch_dependents();
+  int* first = count + n * kSortPitch;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool yes = is_mixed(ids, S, n);
+  if (threadIdx.x == 0) *mixed = yes;
+  if (!yes) return;
+  for (int i = threadIdx.x; i < n * kSortPitch; i += 1024) count[i] = 0;
+  __syncthreads();
+  const int per = (S + 1023) / 1024 * 32, r0 = warp * per, r1 = min(S, r0 + per);
+  auto each = [&](auto&& f) {        // f(row, adapter or -1, lanes of the same one)
+    for (int r = r0; r < r1; r += 32) {
+      const int row = r + lane, id = row < r1 ? __ldg(ids + row) : -1, e = id >= 0 && id < n ? id : -1;
+      f(row, e, __match_any_sync(0xffffffffu, e));
+      __syncwarp();
+    }
+  };
+  each([&](int, int e, uint32_t same) {
+    if (e >= 0 && __ffs(same) - 1 == lane) count[e * kSortPitch + warp] += __popc(same);
+  });
+  __syncthreads();
+  auto scan = [&](int v) {           // of a warp, up to and with this lane
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += u;
+    }
+    return v;
+  };
+  for (int e = warp; e < n; e += 32) {
+    const int v = count[e * kSortPitch + lane], up = scan(v);
+    count[e * kSortPitch + lane] = up - v;
+    if (lane == 31) first[e] = up;
   }
+  __syncthreads();
+  const int mine = (int)threadIdx.x < n ? first[threadIdx.x] : 0, up = scan(mine);   // n is at most 1,024
+  if (lane == 31) sums[warp] = up;
+  __syncthreads();
+  int before = 0, all = 0;
+  for (int w = 0; w < 32; ++w) {
+    before += w < warp ? sums[w] : 0;
+    all += sums[w];
+  }
+  if ((int)threadIdx.x < n) first[threadIdx.x] = before + up - mine;
+  if (threadIdx.x == 0) *kept = all;
+  __syncthreads();
+  each([&](int row, int e, uint32_t same) {
+    int* const at = count + e * kSortPitch + warp;
+    const int to = e >= 0 ? first[e] + *at + __popc(same & ((1u << lane) - 1)) : -1;
+    __syncwarp();
+    if (e >= 0 && __ffs(same) - 1 == lane) *at += __popc(same);
+    if (row < r1) place[row] = to;
+    if (to >= 0) perm[to] = row;
+  });
 }
 
 template <int DT, bool TRANS, bool F32>
@@ -1164,9 +1233,14 @@ cudaError_t launch_pair(const Maps& m, LoraParams s, LoraParams x, cudaStream_t 
   s.stages = (kShrinkSmem - 1024 - s.x_stages * 2 * kXBytes) / s.w_stage;
   if (s.stages > kMaxStages) s.stages = kMaxStages;
   const long sms = sm_count();
-  shrink<<<(unsigned)s.shrink_ctas, kShrinkThreads, 1024 + s.x_stages * 2 * kXBytes + s.stages * s.w_stage, st>>>(m.x, m.x1, m.w,
-                                                                                                               s);
-  e = cudaGetLastError();
+  const dim3 grid((unsigned)s.shrink_ctas), block(kShrinkThreads);
+  const size_t smem = 1024 + s.x_stages * 2 * kXBytes + s.stages * s.w_stage;
+  if (s.mixed) {
+    e = launch_pdl(shrink, grid, block, smem, st, m.x, m.x1, m.w, s);
+  } else {
+    shrink<<<grid, block, smem, st>>>(m.x, m.x1, m.w, s);
+    e = cudaGetLastError();
+  }
   if (e != cudaSuccess) return e;
   x.u_bytes = (terms_of(DT, F32) * x.r16 + 63) / 64 * kXBytes;
   // two tiles of u where three items of base and two of weights fit beside them;
@@ -1239,13 +1313,17 @@ situ_status launch_tiles(int dtype, bool f32, const void* rows, int64_t ld_rows,
   return e == cudaSuccess ? SITU_OK : SITU_ERR_CUDA;
 }
 
-constexpr int kFew = 16;            // adapters
-// Whether rows named by ids may be sorted by adapter first: the look at them and
-// the sorting cost 8 to 17 us also where the rows are then taken as they are
-// (16,384 rows in runs of 64 adapters 124 us, 108 without).  With up to 16 adapters,
-// more often in runs than not, they are not looked at: in any order 9 take 311 us and
-// 16 515, where the sort would make it 203.
-bool sortable(const int32_t* ids, int n) { return ids && n > kFew && n <= SITU_MAX_LOCAL_EXPERTS; }
+// Whether rows named by ids are looked at and, where they are mixed, sorted by
+// adapter first.  The look costs 5 us by one CTA (8 to 17 with the permute's kernels,
+// which run whatever it says) also where the rows come in runs, so with up to 16
+// adapters it is taken only where any order would cost some 100 us more than
+// sorted rows: 16,384 rows at rank 16 of 9 adapters 311 and 205 us, of 16 515 and 211.
+// One CTA sorts up to kSortRows: 16,384 rows of 64 adapters in any order 228 us and in
+// runs 112, with the permute's kernels 213 and 124; half as many, no difference mixed.
+bool sortable(int S, int n) {
+  return n <= SITU_MAX_LOCAL_EXPERTS && (n > 16 || (n > 8 && (long)S * (n - 5) > 60000));
+}
+bool by_one_cta(int S, int n) { return S <= kSortRows && n <= kSortAdapters; }
 // A cluster per row, or tiles.  A row's cluster reads its adapter whatever the
 // others take: 4 us and about 0.07 a row at rank 16, in proportion to the rank above
 // (3584 x 6144).  Tiles take 15 us, and about 1.3 at low ranks and 2.6 at 128 for each
@@ -1257,7 +1335,7 @@ bool sortable(const int32_t* ids, int n) { return ids && n > kFew && n <= SITU_M
 // 39 and 52.
 bool by_rows(int S, int r, int n) {
   const float each = 1.3f * (1.f + r / 128.f), mixed = each * (n < 48 ? n : 48);
-  const float sorted = n > kFew && n <= SITU_MAX_LOCAL_EXPERTS ? 16.f + each * (1.f + 256.f * n / S) : mixed;
+  const float sorted = sortable(S, n) ? 16.f + each * (1.f + 256.f * n / S) : mixed;
   return 4.f + (float)S * (r < 16 ? 16 : r) / 244.f <= 15.f + (mixed < sorted ? mixed : sorted);
 }
 // its scratch: *mixed; numbers, places; counts, offsets, the permute's own
@@ -1283,7 +1361,7 @@ bool bad_sizes(int S, int K, int N, int r, int n) {
 extern "C" size_t situ_moe_lora_workspace_size(int32_t S, int32_t K, int32_t N, int32_t r, int32_t n) {
   using namespace situ;
   if (bad_sizes(S, K, N, r, n) || S == 0 || by_rows(S, r, n)) return 0;
-  return part_bytes(S, K, r) + (n > kFew && n <= SITU_MAX_LOCAL_EXPERTS ? (sort_ints(S, n) * 4 + 31) / 32 * 32 : 0);
+  return part_bytes(S, K, r) + (sortable(S, n) ? (sort_ints(S, n) * 4 + 31) / 32 * 32 : 0);
 }
 
 extern "C" situ_status situ_moe_lora(const situ_lora_args* a, void* workspace, size_t workspace_bytes, void* stream) {
@@ -1339,15 +1417,25 @@ extern "C" situ_status situ_moe_lora(const situ_lora_args* a, void* workspace, s
   s.part = static_cast<float*>(workspace);
   s.scale = a->scale;
   s.err = a->device_status;
-  if (sortable(a->ids, a->n)) {
+  if (a->ids && sortable(a->S, a->n)) {
     int32_t* mixed = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + part_bytes(a->S, a->K, a->r));
     int32_t *perm = mixed + 1, *place = perm + a->S, *counts = place + a->S, *offsets = counts + a->n,
             *scratch = offsets + a->n + 1;
-    mixed_kernel<<<1, 1024, 0, st>>>(a->ids, a->S, a->n, mixed);
-    if (cudaGetLastError() != cudaSuccess ||
-        launch_permute(a->ids, a->S, 1, a->n, 0, 1, counts, offsets, nullptr, nullptr, perm, place, nullptr, scratch, st) !=
-            cudaSuccess)
-      return SITU_ERR_CUDA;
+    bool ok;
+    if (by_one_cta(a->S, a->n)) {
+      const size_t smem = (size_t)a->n * (kSortPitch + 1) * 4;
+      ok = smem <= 40 * 1024 ||      // 48 KB with the static part
+           cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                kSortAdapters * (kSortPitch + 1) * 4) == cudaSuccess;
+      if (ok) sort_kernel<<<1, 1024, smem, st>>>(a->ids, a->S, a->n, mixed, perm, place, offsets + a->n);
+      ok = ok && cudaGetLastError() == cudaSuccess;
+    } else {
+      mixed_kernel<<<1, 1024, 0, st>>>(a->ids, a->S, a->n, mixed);
+      ok = cudaGetLastError() == cudaSuccess &&
+           launch_permute(a->ids, a->S, 1, a->n, 0, 1, counts, offsets, nullptr, nullptr, perm, place, nullptr, scratch, st) ==
+               cudaSuccess;
+    }
+    if (!ok) return SITU_ERR_CUDA;
     s.mixed = mixed;
     s.perm = perm;
     s.place = place;

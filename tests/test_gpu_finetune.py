@@ -544,7 +544,9 @@ def lora_bar(y, both, second, K, r, dtype, out_dtype, rows):
                                        (700, 136, 1160, 48, 4), (1000, 520, 520, 64, 11), (257, 2048, 392, 128, 5),
                                        (2100, 64, 64, 104, 1), (3000, 136, 200, 24, 40), (2049, 520, 1032, 16, 700),
                                        (129, 64, 64, 128, 1), (200, 72, 136, 64, 2), (400, 64, 72, 128, 20),
-                                       (60001, 64, 72, 24, 5), (40007, 72, 64, 128, 3), (40000, 64, 136, 16, 30)])
+                                       (60001, 64, 72, 24, 5), (40007, 72, 64, 128, 3), (40000, 64, 136, 16, 30),
+                                       (6007, 64, 72, 16, 16), (16385, 64, 64, 8, 9), (16384, 64, 64, 8, 1024),
+                                       (9001, 64, 64, 64, 1025)])
 @pytest.mark.parametrize("dtype,out_dtype", [(BF16, BF16), (F16, F16), (BF16, F32), (F16, F32)])
 @pytest.mark.parametrize("order", ["mixed", "runs"])
 def test_lora(S, K, N, r, n, dtype, out_dtype, order):
