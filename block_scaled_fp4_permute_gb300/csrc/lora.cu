@@ -1316,25 +1316,25 @@ situ_status launch_tiles(int dtype, bool f32, const void* rows, int64_t ld_rows,
 // Whether rows named by ids are looked at and, where they are mixed, sorted by
 // adapter first.  The look costs 5 us by one CTA (8 to 17 with the permute's kernels,
 // which run whatever it says) also where the rows come in runs, so with up to 16
-// adapters it is taken only where any order would cost some 100 us more than
+// adapters it is taken only where any order would cost some 70 us more than
 // sorted rows: 16,384 rows at rank 16 of 9 adapters 311 and 205 us, of 16 515 and 211.
 // One CTA sorts up to kSortRows: 16,384 rows of 64 adapters in any order 228 us and in
 // runs 112, with the permute's kernels 213 and 124; half as many, no difference mixed.
 bool sortable(int S, int n) {
-  return n <= SITU_MAX_LOCAL_EXPERTS && (n > 16 || (n > 8 && (long)S * (n - 5) > 60000));
+  return n <= SITU_MAX_LOCAL_EXPERTS && (n > 16 || (n > 8 && (long)S * (n - 5) > 40000));
 }
 bool by_one_cta(int S, int n) { return S <= kSortRows && n <= kSortAdapters; }
 // A cluster per row, or tiles.  A row's cluster reads its adapter whatever the
 // others take: 4 us and about 0.07 a row at rank 16, in proportion to the rank above
 // (3584 x 6144).  Tiles take 15 us, and about 1.3 at low ranks and 2.6 at 128 for each
-// adapter that rows of a tile take: in any order at most n of them (no more than 48
-// tell), sorted, for 16 us, as many as 256 rows hold.  By rows and in tiles, us: 128
-// rows at rank 16 of one adapter 14 and 16, 256 20 and 17, 512 of 16 adapters 37 and 52
-// (30 where they come in runs), 1,024 of 64 70 and 62; at rank 64 32 rows of one 14
-// and 17, 64 22 and 17, 128 of 64 48 and 103; at rank 128 64 of one 40 and 21, of 16
-// 39 and 52.
+// adapter that rows of a tile take: in any order up to n of them, sorted, for 16
+// us, as many as 256 rows hold.  By rows and in tiles, us: 128 rows at rank 16 of one
+// adapter 14 and 16, 256 20 and 17, 512 of 16 adapters 37 and 52 (30 where they come in
+// runs), 1,024 of 64 70 and 62; at rank 64 32 rows of one 14 and 17, 64 22 and 17, 128
+// of 64 48 and 103, 512 of 256 175 and 403; at rank 128 64 of one 40 and 21, of 16 39
+// and 52.
 bool by_rows(int S, int r, int n) {
-  const float each = 1.3f * (1.f + r / 128.f), mixed = each * (n < 48 ? n : 48);
+  const float each = 1.3f * (1.f + r / 128.f), mixed = each * (n < kTile ? n : kTile);
   const float sorted = sortable(S, n) ? 16.f + each * (1.f + 256.f * n / S) : mixed;
   return 4.f + (float)S * (r < 16 ? 16 : r) / 244.f <= 15.f + (mixed < sorted ? mixed : sorted);
 }
