@@ -53,6 +53,16 @@ constexpr int kShrinkSmem = 217 * 1024, kExpandSmem = 220 * 1024;   // 227 KB wi
 constexpr int kCluster = 8;        // CTAs of a row
 constexpr int kRowThreads = 256;
 
+// f16, backwards (lora_common.cuh): u as the forward pass kept it, and what makes it anew
+// where that has lost it.
+struct FarParams {
+  const uint16_t *u, *x, *a;
+  long ldx;
+  int K;
+  float *u32, *row_most;
+  uint32_t* most;                  // null: not this case
+};
+
 struct LoraParams {
   const int32_t *ids, *offsets;
   int S, C, r, n;                  // C: the other extent (contraction or columns)
@@ -66,7 +76,8 @@ struct LoraParams {
   long ld_base;
   void* out;
   long ldo;
-  void* u16;                       // [S, 2, r] scaled, in two terms of the operands' type, or null
+  void* u16;                       // [S, 2, r] scaled, in two terms of the operands' type, or null; f16 backwards: fp32 [S, r]
+  FarParams far;                   // backwards, f16
   int stages, w_stage;             // shared memory: stages of w, bytes of one
   int x_stages;                    // shrink: of x
   int y_stages, u_stages, u_bytes; // expand: items of base, tiles of u, bytes of one
@@ -91,20 +102,6 @@ struct RowParams {
   int S, K, N, r, n;
 };
 
-__device__ __forceinline__ int adapter_of(const int32_t* ids, const int32_t* offsets, int n, int row) {
-  if (ids) {
-    const int e = __ldcg(ids + row);
-    return e >= 0 && e < n ? e : -1;
-  }
-  int lo = 0, hi = n + 1;          // the first entry beyond row lies in [lo, hi]
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldcg(offsets + mid) > row) hi = mid;
-    else lo = mid + 1;
-  }
-  return lo <= n ? lo - 1 : -1;
-}
-
 // The same for a whole warp, a row to each lane: up to 31 adapters' offsets in one
 // load where a search takes a load after the other.  Rows from S on have none.
 __device__ __forceinline__ int adapter_of_lane(const int32_t* ids, const int32_t* offsets, int n, int row, int S) {
@@ -114,17 +111,6 @@ __device__ __forceinline__ int adapter_of_lane(const int32_t* ids, const int32_t
   for (int j = n; j >= 0; --j)
     if (__shfl_sync(0xffffffffu, o, j) > row) first = j;
   return row < S && first <= n ? first - 1 : -1;
-}
-
-template <int DT>
-__device__ __forceinline__ float dot8(const uint4& a, const uint4& b, float acc) {
-  const uint32_t u[4] = {a.x, a.y, a.z, a.w}, v[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    acc = fmaf(lo16<DT>(u[i]), lo16<DT>(v[i]), acc);
-    acc = fmaf(hi16<DT>(u[i]), hi16<DT>(v[i]), acc);
-  }
-  return acc;
 }
 
 // --------------------------------------------------------------------------
@@ -333,6 +319,93 @@ __device__ __forceinline__ bool find_adapters(Adapters<R>& t, const Rows& rows, 
   return true;
 }
 
+// f16, backwards: a row of u anew from x and a, to fp32, by a warp; its largest finite
+// magnitude.
+__device__ __noinline__ float u_anew(const uint4* x, const uint4* a, int pieces, int r, float f, float* out) {
+  const int lane = threadIdx.x & 31;
+  float m = 0.f;
+#pragma unroll 1
+  for (int c = 0; c < r; c += 8) {
+    const uint4* w = a + (size_t)c * pieces;
+    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int d = lane; d < pieces; d += 32) {
+      const uint4 v = __ldg(x + d);
+#pragma unroll
+      for (int t = 0; t < 8; ++t) acc[t] = dot8<SITU_DT_F16>(v, __ldg(w + (size_t)t * pieces + d), acc[t]);
+    }
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) acc[t] += __shfl_xor_sync(0xffffffffu, acc[t], o);
+      acc[t] *= f;
+      m = finite_max(m, acc[t]);
+    }
+    if (lane == 0) put8(out + c, acc);
+  }
+  return m;
+}
+__device__ __forceinline__ bool zeros(const uint4* x, int pieces) {
+  bool any = false;
+  for (int d = threadIdx.x & 31; d < pieces; d += 32) {
+    const uint4 v = __ldg(x + d);
+    any = any || ((v.x | v.y | v.z | v.w) & 0x7FFF7FFFu) != 0;
+  }
+  return !__any_sync(0xffffffffu, any);
+}
+// f16, backwards: each row's largest finite magnitude of u, from the kept terms.  Where
+// those have lost it (an infinity, or nothing from kLeast on, beside which f16's steps
+// are no longer small) u is made anew, which the sign of the largest says.  By a warp.
+constexpr float kLeast = 1.f / 256;      // a step's half is 2^-17 of it
+__device__ __forceinline__ void look_at_u(const LoraParams& p, long unit) {
+  const RowLanes k(p.r, unit);
+  uint2 hi[kRowTurns];
+#pragma unroll
+  for (int i = 0; i < kRowTurns; ++i) {
+    const long row = k.row(i, p.S);
+    hi[i] = row < p.S ? __ldg(reinterpret_cast<const uint2*>(p.far.u + (size_t)row * 2 * p.r + k.j)) : make_uint2(0, 0);
+  }
+  uint32_t lost = 0;                                      // bit i: this lane's row of turn i has been lost
+#pragma unroll
+  for (int i = 0; i < kRowTurns; ++i) {
+    constexpr int kF16 = SITU_DT_F16;
+    const float v[4] = {lo16<kF16>(hi[i].x), hi16<kF16>(hi[i].x), lo16<kF16>(hi[i].y), hi16<kF16>(hi[i].y)};
+    float m = 0.f;
+    bool finite = true;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      m = finite_max(m, v[t]);
+      finite = finite && fabsf(v[t]) < INFINITY;
+    }
+    m = k.largest(m);
+    const long row = k.row(i, p.S);
+    if (row < p.S && (!finite || m < kLeast)) lost |= 1u << i;
+    if (row < p.S && k.j == 0) p.far.row_most[row] = m;
+  }
+  if (!__any_sync(0xffffffffu, lost != 0)) return;
+  for (uint32_t rest = lost; rest; rest &= rest - 1) {    // rows without an adapter are zeros
+    const int i = __ffs(rest) - 1;
+    if (adapter_of(nullptr, p.offsets, p.n, (int)k.row(i, p.S)) < 0) lost &= ~(1u << i);
+  }
+  __syncwarp();
+#pragma unroll 1
+  for (int i = 0; i < kRowTurns; ++i) {
+    const uint32_t lanes = __ballot_sync(0xffffffffu, lost >> i & 1);
+#pragma unroll 1
+    for (int a = 0; a < k.per; ++a) {                     // a row after the other, by all lanes
+      const uint32_t of = (k.q == 32 ? 0xffffffffu : (1u << k.q) - 1) << (a * k.q);
+      if (!(lanes & of)) continue;
+      const long row = k.row0 + (long)i * k.per + a;
+      const int e = adapter_of(nullptr, p.offsets, p.n, (int)row), pieces = p.far.K / 8;
+      const uint4* x = reinterpret_cast<const uint4*>(p.far.x + (size_t)row * p.far.ldx);
+      if (zeros(x, pieces)) continue;                     // kept as they are
+      const float m = u_anew(x, reinterpret_cast<const uint4*>(p.far.a) + (size_t)e * p.r * pieces, pieces, p.r,
+                             p.scale ? __ldg(p.scale + e) : 1.f, p.far.u32 + (size_t)row * p.r);
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) p.far.row_most[row] = -m;
+    }
+  }
+}
+
 constexpr int kTmemCols = 512;                // of an SM
 constexpr int kShrinkRows = 256;              // of a tile of the shrink: two MMAs share an adapter's weights
 constexpr int kShrinkThreads = 64 + kEpi;     // copies, MMAs; eight epilogue warps
@@ -410,6 +483,8 @@ shrink_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) tmem_alloc<1>(saddr(holder), kTmemCols);
+  if (DT == SITU_DT_F16 && TRANS && blockIdx.x == 0)
+    for (int i = tid; i < 2 * p.n; i += kShrinkThreads) p.far.most[i] = 0;
   if (p.mixed) griddep_wait();       // the rows' order is the predecessor's
   const Rows rows(p);
   const long total = (long)((rows.count + kShrinkRows - 1) / kShrinkRows) * p.chunks, G = sharers(total, p.shrink_ctas, p.least);
@@ -575,6 +650,11 @@ shrink_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     };
     Segment g(i0, i1, p.chunks);
     if (g.more()) list(g, e_first);
+    if (DT == SITU_DT_F16 && TRANS) {                     // before the first sums are there
+      constexpr int kWarps = kEpi / 32;
+      for (long unit = (long)blockIdx.x * kWarps + warp - 2; unit * RowLanes::rows(p.r) < p.S; unit += (long)gridDim.x * kWarps)
+        look_at_u(p, unit);
+    }
     for (int b = 0; g.more(); b ^= 1) {
       Segment n = g;
       n.next();
@@ -765,25 +845,31 @@ expand_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
           for (int c = 0; c < kC; ++c)
 #pragma unroll
             for (int k = 0; k < 4; ++k) u[i][c][k] = of[i] >= 0 ? u[i][c][k] * f[i] : 0.f;
+          const int row = write ? rows.row(g.tile * kTile + r) : p.S;
           float to = 1.f;
           if (DT == SITU_DT_F16) {
             float m = 0.f;
 #pragma unroll
             for (int c = 0; c < kC; ++c)
 #pragma unroll
-              for (int k = 0; k < 4; ++k) m = fmaxf(m, fabsf(u[i][c][k]));
+              for (int k = 0; k < 4; ++k) m = finite_max(m, u[i][c][k]);
 #pragma unroll
             for (int o = 1; o < 8; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            const int k = (int)(__float_as_uint(m) >> 23) - 127;    // m in [2^k, 2^(k + 1))
-            const int ex = m > 0.f && m < INFINITY ? max(-100, min(120, k - 14)) : 0;
+            const int ex = power_of(m);
             to = exp2i(-ex);
-            if ((lane & 7) == 0) back[ts][r] = exp2i(ex);
+            if ((lane & 7) == 0) {
+              back[ts][r] = exp2i(ex);
+              if (TRANS && row < p.S && of[i] >= 0) raise_most(p.far.most + of[i], m);
+            }
           }
-          const int row = write ? rows.row(g.tile * kTile + r) : p.S;
 #pragma unroll
           for (int c = 0; c < kC; ++c) {
             const int j = c0 + 32 * c;
-            if (row < p.S && j < p.r) {
+            if (DT == SITU_DT_F16 && TRANS) {               // v as it is: its terms wait for the largest
+              if (row < p.S && j < p.r)
+                *reinterpret_cast<float4*>(static_cast<float*>(p.u16) + (size_t)row * p.r + j) =
+                    make_float4(u[i][c][0], u[i][c][1], u[i][c][2], u[i][c][3]);
+            } else if (row < p.S && j < p.r) {
               uint2 *o = reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.u16) + (size_t)row * 2 * p.r + j), hi, lo;
               two_terms<DT>(u[i][c][0], u[i][c][1], hi.x, lo.x);
               two_terms<DT>(u[i][c][2], u[i][c][3], hi.y, lo.y);
@@ -995,6 +1081,19 @@ expand_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
         if (p.u16)
           for (int i = lane; i < p.r / 4; i += 32)
             reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.u16) + (size_t)row * 2 * p.r)[i] = make_uint4(0, 0, 0, 0);
+      }
+    }
+  } else if (DT == SITU_DT_F16 && TRANS && warp == 3 && !dead) {
+    // ---------------- the adapters' largest u ----------------
+    griddep_wait();
+    for (long r0 = (long)blockIdx.x * 32; r0 < p.S; r0 += G * 32) {
+      const int e = adapter_of_lane(nullptr, p.offsets, p.n, (int)min(r0 + lane, (long)p.S), p.S);
+      const float m = e >= 0 ? fabsf(__ldcg(p.far.row_most + r0 + lane)) : 0.f;
+      if (__all_sync(0xffffffffu, e == __shfl_sync(0xffffffffu, e, 0))) {
+        const uint32_t all = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
+        if (lane == 0 && e >= 0) raise_most(p.far.most + p.n + e, __uint_as_float(all));
+      } else if (e >= 0) {
+        raise_most(p.far.most + p.n + e, m);
       }
     }
   } else if (warp >= 4 && warp < 12 && !dead) {
@@ -1348,6 +1447,10 @@ size_t shared_bytes(int S, int N, int r) {
   const size_t a = part_bytes(S, N, r), b = outer_bytes(r);
   return a > b ? a : b;
 }
+// behind them v, and for f16 u, its rows' largest and the adapters' largest of both
+size_t kept_bytes(int S, int r) { return (size_t)S * r * 4 + 32; }
+size_t row_bytes(int S) { return ((size_t)S * 4 + 31) / 32 * 32; }
+constexpr size_t kMostBytes = 2 * SITU_GEMM_MAX_GROUPS * 4;
 
 bool bad_extent(int C) { return C < 8 || C % 8 != 0 || C > SITU_GEMM_MAX_DIM; }
 bool bad_sizes(int S, int K, int N, int r, int n) {
@@ -1455,7 +1558,7 @@ extern "C" situ_status situ_moe_lora(const situ_lora_args* a, void* workspace, s
 extern "C" size_t situ_moe_lora_backward_workspace_size(int32_t S, int32_t K, int32_t N, int32_t r) {
   using namespace situ;
   if (bad_sizes(S, K, N, r, 1)) return 0;
-  return shared_bytes(S, N, r) + (size_t)S * r * 4 + 16;
+  return shared_bytes(S, N, r) + 2 * kept_bytes(S, r) + row_bytes(S) + kMostBytes;
 }
 
 extern "C" situ_status situ_moe_lora_backward(const situ_lora_backward_args* a, void* workspace, size_t workspace_bytes,
@@ -1477,26 +1580,18 @@ extern "C" situ_status situ_moe_lora_backward(const situ_lora_backward_args* a, 
   if (bad(a->offsets, 3) || bad(a->scale, 3) || bad(a->device_status, 3)) return SITU_ERR_MISALIGNED;
   if (workspace_bytes < situ_moe_lora_backward_workspace_size(a->S, a->K, a->N, a->r)) return SITU_ERR_WORKSPACE_TOO_SMALL;
   uint8_t* v = static_cast<uint8_t*>(workspace) + shared_bytes(a->S, a->N, a->r);
-  if (a->S > 0) {
-    LoraParams s = {};
-    s.offsets = a->offsets;
-    s.S = a->S;
-    s.r = a->r;
-    s.n = a->n;
-    s.part = static_cast<float*>(workspace);
-    s.scale = a->scale;
-    s.err = a->device_status;
-    LoraParams x = s;
-    s.C = a->N;
-    x.C = a->K;
-    x.base = a->dx0;
-    x.ld_base = (long)a->ld_dx0;
-    x.out = a->dx;
-    x.ldo = (long)a->ld_dx;
-    x.u16 = v;
-    const situ_status t =
-        launch_tiles<true>(a->dtype, f32 != 0, a->dy, a->ld_dy, a->b, a->a, s, x, (cudaStream_t)stream);
-    if (t != SITU_OK) return t;
+  FarParams far = {};
+  if (a->dtype == SITU_DT_F16) {
+    uint8_t* u32 = v + kept_bytes(a->S, a->r);
+    uint8_t* row_most = u32 + kept_bytes(a->S, a->r);
+    far.u = static_cast<const uint16_t*>(a->u);
+    far.x = static_cast<const uint16_t*>(a->x);
+    far.a = static_cast<const uint16_t*>(a->a);
+    far.ldx = (long)a->ldx;
+    far.K = a->K;
+    far.u32 = reinterpret_cast<float*>(u32);
+    far.row_most = reinterpret_cast<float*>(row_most);
+    far.most = reinterpret_cast<uint32_t*>(row_most + row_bytes(a->S));
   }
   OuterArgs o;
   o.dtype = a->dtype;
@@ -1509,6 +1604,9 @@ extern "C" situ_status situ_moe_lora_backward(const situ_lora_backward_args* a, 
   o.dy = a->dy;
   o.v = v;
   o.u = a->u;
+  o.u32 = far.u32;
+  o.row_most = far.row_most;
+  o.most = far.most;
   o.ldx = a->ldx;
   o.ld_dy = a->ld_dy;
   o.offsets = a->offsets;
@@ -1516,7 +1614,28 @@ extern "C" situ_status situ_moe_lora_backward(const situ_lora_backward_args* a, 
   o.db = a->db;
   o.parts = static_cast<float*>(workspace);             // u's parts have been read
   o.err = a->device_status;
-  if (a->S > 0) return launch_outer(o, (cudaStream_t)stream);
+  if (a->S > 0) {
+    LoraParams s = {};
+    s.offsets = a->offsets;
+    s.S = a->S;
+    s.r = a->r;
+    s.n = a->n;
+    s.part = static_cast<float*>(workspace);
+    s.scale = a->scale;
+    s.err = a->device_status;
+    s.far = far;
+    LoraParams x = s;
+    s.C = a->N;
+    x.C = a->K;
+    x.base = a->dx0;
+    x.ld_base = (long)a->ld_dx0;
+    x.out = a->dx;
+    x.ldo = (long)a->ld_dx;
+    x.u16 = v;
+    const situ_status t =
+        launch_tiles<true>(a->dtype, f32 != 0, a->dy, a->ld_dy, a->b, a->a, s, x, (cudaStream_t)stream);
+    return t != SITU_OK ? t : launch_outer(o, (cudaStream_t)stream);
+  }
   const bool zero = cudaMemsetAsync(a->da, 0, (size_t)a->n * a->r * a->K * 2, (cudaStream_t)stream) == cudaSuccess &&
                     cudaMemsetAsync(a->db, 0, (size_t)a->n * a->N * a->r * 2, (cudaStream_t)stream) == cudaSuccess;
   return zero ? SITU_OK : SITU_ERR_CUDA;

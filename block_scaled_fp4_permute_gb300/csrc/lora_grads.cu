@@ -6,7 +6,10 @@
 // the columns of a narrow one on its N side, rows along the contraction (both
 // operands MN-major).  u and v come in two 16-bit terms, side by side on the N side:
 // rounded to one, the gradients would be off by as much again as their own
-// rounding.  Bound by the bytes of x and dy: r operations a byte.  The
+// rounding.  In f16 the terms are those of u and v under a power of two per adapter,
+// which its sums are multiplied by again: v of a fine-tuning run's first steps lies
+// far below f16's smallest step.  The kernels that make v look at u as well and leave
+// the adapters' largest; terms_kernel makes the terms.  Bound by the bytes of x and dy: r operations a byte.  The
 // general products over groups (situ_moe_grouped_gemm) give whole tiles to CTAs, and
 // four adapters of 3584 x 6144 make 56 and 96 tiles for 152 SMs.  Here the
 // chunks of 64 rows of all tiles of both gradients are dealt out evenly over one CTA
@@ -36,6 +39,7 @@ struct OuterParams {
   int S, n, r;
   int C[2], blocks[2];                   // of x and dy: columns, tiles of 128
   void* out[2];                          // da, db
+  const uint32_t* most;                  // f16: [2][n], the bits of each adapter's largest v and u
   float* parts;                          // [CTA][2][128][r]
   int stages, run;                       // run: chunks of a sum in tensor memory
   int* err;
@@ -75,9 +79,19 @@ struct Deal {
   }
 };
 
+// f16: what v or u of a piece's adapter was divided by
+template <int DT>
+__device__ __forceinline__ float factor_of(const OuterParams& p, const Piece& t) {
+  return DT == SITU_DT_F16 ? exp2i(power_of(__uint_as_float(__ldcg(p.most + t.which * p.n + t.e)))) : 1.f;
+}
+
 // Sums of column c of a tile to the gradient, rounded: da is [j][c], db [c][j].
 template <int DT>
-__device__ __forceinline__ void store16(const OuterParams& p, const Piece& t, int c, int j, const float* v) {
+__device__ __forceinline__ void store16(const OuterParams& p, const Piece& t, float f, int c, int j, float* v) {
+  if (DT == SITU_DT_F16) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] *= f;
+  }
   uint16_t* out = static_cast<uint16_t*>(p.out[t.which]);
   if (t.which == 0) {
     out += ((size_t)t.e * p.r + j) * p.C[0] + c;
@@ -236,12 +250,14 @@ outer_kernel(const __grid_constant__ OuterMaps m, const OuterParams p) {
         for (long i = (long)blockIdx.x * 128 + tid - 128; i < pieces; i += (long)gridDim.x * 128) out[i] = make_uint4(0, 0, 0, 0);
       }
     }
+    griddep_wait();                       // `most` is the predecessors'
     Turns acc(2);
     bool ok = true;
     for (long i = i0; i < i1 && ok;) {
       const Piece t = deal.at(i, i1);
       i += t.to - t.from;
       const int c = t.block * 128 + 32 * q + lane;
+      const float back = factor_of<DT>(p, t);
       float* part = p.parts + (((size_t)blockIdx.x * 2 + (t.from == 0)) * 128 + 32 * q + lane) * p.r;
       for (int from = t.from; from < t.to && ok; from += p.run, acc.next()) {
         if (!warp_wait(acc_full(acc.s), acc.ph, p.err, 126)) {
@@ -266,7 +282,7 @@ outer_kernel(const __grid_constant__ OuterMaps m, const OuterParams p) {
             f[x] = __uint_as_float(vh ? v[8 + x] : v[x]) + __uint_as_float(wh ? w[8 + x] : w[x]);
             if (earlier) f[x] += part[j + x];
           }
-          if (last && t.whole()) store16<DT>(p, t, c, j, f);
+          if (last && t.whole()) store16<DT>(p, t, back, c, j, f);
           else put8(part + j, f);
         }
         __syncwarp();
@@ -312,6 +328,7 @@ outer_join_kernel(const OuterParams p) {
       if (!mine || *reinterpret_cast<volatile int*>(p.err) != 0) return;   // no parts where a wait was given up
     }
     const int end = round == 1 ? last : -1;
+    const float back = round == 1 ? factor_of<DT>(p, t) : 1.f;
     for (int i = threadIdx.x; i < 128 * p.r / 8; i += kJoinThreads) {
       const int c = i * 8 / p.r, j = i * 8 - c * p.r;
       const bool in = t.block * 128 + c < p.C[t.which];
@@ -340,8 +357,63 @@ outer_join_kernel(const OuterParams p) {
           s[7] += v[d][1].w;
         }
       }
-      if (in && round == 1) store16<DT>(p, t, t.block * 128 + c, j, s);
+      if (in && round == 1) store16<DT>(p, t, back, t.block * 128 + c, j, s);
     }
+  }
+}
+
+// f16: v and u to two terms under their adapters' powers of two.
+constexpr int kTermWarps = 8;
+struct TermsParams {
+  const uint16_t* u;
+  float *v, *u32;
+  const float* row_most;
+  int S, r, n;
+  const int32_t* offsets;
+  const uint32_t* most;
+};
+__global__ void __launch_bounds__(32 * kTermWarps)
+terms_kernel(const TermsParams p) {
+  constexpr int kF16 = SITU_DT_F16;
+  griddep_launch_dependents();
+  const RowLanes k(p.r, (long)blockIdx.x * kTermWarps + (threadIdx.x >> 5));
+  const int which = blockIdx.y;
+  float* const to = which ? p.u32 : p.v;
+  int e[kRowTurns];
+  float4 v[kRowTurns];
+#pragma unroll
+  for (int i = 0; i < kRowTurns; ++i) {
+    const long row = k.row(i, p.S);
+    e[i] = row < p.S ? adapter_of(nullptr, p.offsets, p.n, (int)row) : -1;
+    v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (which && row < p.S) {
+      const uint2 hi = __ldg(reinterpret_cast<const uint2*>(p.u + (size_t)row * 2 * p.r + k.j));
+      const uint2 lo = __ldg(reinterpret_cast<const uint2*>(p.u + ((size_t)row * 2 + 1) * p.r + k.j));
+      v[i] = make_float4(lo16<kF16>(hi.x) + lo16<kF16>(lo.x), hi16<kF16>(hi.x) + hi16<kF16>(lo.x),
+                         lo16<kF16>(hi.y) + lo16<kF16>(lo.y), hi16<kF16>(hi.y) + hi16<kF16>(lo.y));
+    }
+  }
+  griddep_wait();
+  uint32_t m[kRowTurns];
+#pragma unroll
+  for (int i = 0; i < kRowTurns; ++i) {
+    const long row = k.row(i, p.S);
+    m[i] = e[i] >= 0 ? __ldcg(p.most + which * p.n + e[i]) : 0;
+    if (row < p.S && (which == 0 || (__float_as_uint(__ldcg(p.row_most + row)) >> 31) != 0))
+      v[i] = __ldcg(reinterpret_cast<const float4*>(to + (size_t)row * p.r + k.j));
+  }
+  __syncwarp();                            // all of a row is read before any of it is written
+#pragma unroll
+  for (int i = 0; i < kRowTurns; ++i) {
+    const long row = k.row(i, p.S);
+    if (row >= p.S) continue;
+    const float f = exp2i(-power_of(__uint_as_float(m[i])));
+    uint2 hi, lo;
+    two_terms<kF16>(v[i].x * f, v[i].y * f, hi.x, lo.x);
+    two_terms<kF16>(v[i].z * f, v[i].w * f, hi.y, lo.y);
+    uint16_t* o = reinterpret_cast<uint16_t*>(to + (size_t)row * p.r) + k.j;
+    *reinterpret_cast<uint2*>(o) = hi;
+    *reinterpret_cast<uint2*>(o + p.r) = lo;
   }
 }
 
@@ -384,12 +456,21 @@ situ_status launch_outer(const OuterArgs& a, cudaStream_t st) {
   p.out[1] = a.db;
   p.parts = a.parts;
   p.err = a.err;
+  p.most = a.most;
+  const bool f16 = a.dtype == SITU_DT_F16;
+  if (f16) {
+    const TermsParams t = {static_cast<const uint16_t*>(a.u), static_cast<float*>(a.v), a.u32, a.row_most, a.S, a.r, a.n, a.offsets,
+                           a.most};
+    const long rows = kTermWarps * RowLanes::rows(a.r);   // of a block
+    if (launch_pdl(terms_kernel, dim3((unsigned)((a.S + rows - 1) / rows), 2), dim3(32 * kTermWarps), 0, st, t) != cudaSuccess)
+      return SITU_ERR_CUDA;
+  }
   const int stage = kWide + (2 * a.r + 63) / 64 * kRows * 128;
   p.stages = (kSmem - 1024) / stage;
   if (p.stages > kMaxStages) p.stages = kMaxStages;
   const CUtensorMapDataType dt = a.dtype == SITU_DT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   OuterMaps m;
-  const void *wide[2] = {a.x, a.dy}, *narrow[2] = {a.v, a.u};
+  const void *wide[2] = {a.x, a.dy}, *narrow[2] = {a.v, f16 ? a.u32 : a.u};
   const int64_t ld[2] = {a.ldx, a.ld_dy};
   const uint32_t box[2] = {64, kRows}, one[2] = {64, 1};
   bool ok = true;
@@ -401,7 +482,7 @@ situ_status launch_outer(const OuterArgs& a, cudaStream_t st) {
   }
   if (!ok) return SITU_ERR_CUDA;
   const int smem = 1024 + p.stages * stage;
-  const cudaError_t e = a.dtype == SITU_DT_BF16 ? launch_dt<SITU_DT_BF16>(m, p, smem, st) : launch_dt<SITU_DT_F16>(m, p, smem, st);
+  const cudaError_t e = !f16 ? launch_dt<SITU_DT_BF16>(m, p, smem, st) : launch_dt<SITU_DT_F16>(m, p, smem, st);
   return e == cudaSuccess ? SITU_OK : SITU_ERR_CUDA;
 }
 

@@ -746,9 +746,9 @@ situ_status situ_moe_gated_backward(const situ_gated_args* args, void* stream);
  * second product rounded to 16 bits for 16-bit results, with 22 bits or more
  * for fp32 ones.  u (or NULL) receives u [S, 2, r] in two terms of the operands'
  * type, the first u rounded, the second what that leaves (zeros without an
- * adapter), which the gradients take.  What is written overlaps no other
- * operand.  For experts, an adapter per
- * (request's adapter, expert) pair is one of n, its rows in any order.
+ * adapter; as far as that type's range goes), which the gradients take.  What is
+ * written overlaps no other operand.  For experts, an adapter per (request's
+ * adapter, expert) pair is one of n, its rows in any order.
  * Results do not depend on the order of execution, nor on what other rows'
  * adapters hold.  K, N multiples of 8, rows strided by multiples of 8 elements
  * (fp32: 4), pointers 16-byte aligned, ids, offsets, scale 4.
@@ -781,10 +781,14 @@ situ_status situ_moe_lora(const situ_lora_args* args, void* workspace, size_t wo
  *   v = scale dy b,  dx = dx0 + v a,  da[e] = v^T x,  db[e] = dy^T u   over e's rows
  * dx0 (or NULL: zeros) is the shared projection's gradient, dx may be it, both
  * of the operands' type or fp32; da [n, r, K] and db [n, N, r] are of the
- * operands' type, rounded once, zeros for an adapter without rows (v is taken in
- * two terms as u is).  dx overlaps neither dy nor x: these are still read
- * while it is written.  Results do not depend on the order of execution.  S == 0
- * sets da and db to zeros. */
+ * operands' type, rounded once, zeros for an adapter without rows.  v and u are
+ * taken in two terms of the operands' type, in f16 under a power of two per
+ * adapter (22 bits, or all of a value down to 2^-39 of the adapter's largest), so
+ * that neither vanishes nor overflows.  A row of u that f16 could not keep (an
+ * infinity, or nothing from 2^-8 on) is made anew from x and a, which is slow where
+ * all rows are such; the others are exact to 2^-17 of their largest.  dx overlaps
+ * neither dy nor x: these are still read while it is written.  Results do not
+ * depend on the order of execution.  S == 0 sets da and db to zeros. */
 typedef struct situ_lora_backward_args {
   int32_t dtype, dx_dtype;
   int32_t S, K, N, r, n;
