@@ -7,17 +7,22 @@
 //   SWIGLU_BIAS   h = g sigmoid(a g) (u + c)
 // With E0 = e^-g, E1 = e^(-2g/b), E2 = e^(-2u/bl) and d_i = 1 + E_i,
 //   sigmoid(g) = 1/d0,  tanh(g/b) = (1 - E1)/d1,  its derivative by g times b = 4 E1/d1^2,
-//   d/dg [b tanh(g/b) sigmoid(g)] = 1/d0 (4 E1/d1^2 + b tanh(g/b) E0/d0):
-// no difference of nearly equal numbers, and one reciprocal, of d0 d1 d2, for
-// all three.  Exponents are clamped at 25 (SWIGLU_BIAS: 80), where the factors
-// are at their limits to 1.4e-11, so that the product stays finite; NaN passes.
+//   d/dg [b tanh(g/b) sigmoid(g)] = 1/d0 (4 E1/d1^2 + b tanh(g/b) E0/d0)
+// and one reciprocal, of d0 d1 d2, for all three.  1 - E1 is a difference of nearly
+// equal numbers where g is small beside b.  So the factor is g tanh(y)/y with
+// y = max(|g/b|, 2^-7.5): tanh(y)/y is off by y^2/3 < 2^-16.5 below that, and the
+// difference by 2^-15.5 at most above (its derivative's 1 - tanh^2 by 2^-15).  A result
+// is rounded once, whatever the cap.
+// Where the product could overflow, each factor has a reciprocal of its own: E1 and E2
+// are taken of magnitudes, and a sigmoid below 2^-126 is zero.  NaN passes.
 //
 // Bound by memory: per pair of gate and up, the forward reads 4 bytes and
 // writes 2 (h) and 2 1/16 (the kept form); the backward reads 2 1/16 and 2 (dh)
 // and writes 4 and, with h, 2 more.  Power-of-two scales make what is restored
 // exact in 16 bits, so that the gradients' 16-bit products take it as it is.
-// Measured (bf16, 32,768 rows of 2,048, 32 experts): forward 93 us (5.8 TB/s),
-// backward 118 (5.7), held by issue slots as much as by memory.
+// Measured (bf16, 32,768 rows of 2,048, 32 experts): forward 101 us (5.4 TB/s),
+// backward 123 (5.5), held by issue slots as much as by memory (with the factors as
+// they stand above, 91 and 115; SWIGLU_BIAS 83 and 109).
 //
 // Two neighbouring lanes hold a block of 32 columns, 16 each: the row's expert
 // and its constants are then a small part of a thread's work (with eight columns
@@ -113,6 +118,11 @@ __device__ __forceinline__ F2 operator*(F2 a, F2 b) {
 __device__ __forceinline__ F2 operator+(F2 a, F2 b) {
   F2 r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 operator-(F2 a, F2 b) {
+  F2 r;
+  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
   return r;
 }
 __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
@@ -264,7 +274,31 @@ __device__ __forceinline__ void restore8(uint32_t lo, uint32_t hi, float s, floa
   }
 }
 
-__device__ __forceinline__ float exp25(float z) { return exp2_approx(min_nan(z, 25.f * kLog2e)); }
+constexpr float kSmall = 1.f / 181;      // 2^-7.5 of a cap, below which its factor counts as the argument
+
+// b tanh(x / b) and its derivative; k = -2 log2(e) / b, 0 without a cap
+struct Tanh {
+  float t, dt;
+  __device__ __forceinline__ Tanh(float x, float b, float k) : t(x), dt(1.f) {
+    if (k < 0.f) {
+      const float e = exp2_approx(-fabsf(k * x)), r = rcp_approx(1.f + e);
+      if (!(fabsf(x) < kSmall * b)) t = copysignf(b * (1.f - e) * r, x);
+      dt = 4.f * e * r * r;
+    }
+  }
+};
+// sigmoid(v) and, from v brought into where that is no subnormal, sigmoid(-v)
+__device__ __forceinline__ float sigmoid(float v) { return rcp_approx(1.f + exp2_approx(-kLog2e * v)); }
+struct Sigmoid {
+  float v, s, c;
+  __device__ __forceinline__ explicit Sigmoid(float a) {
+    constexpr float kMost = 87.f;
+    v = max_nan(min_nan(a, kMost), -kMost);
+    const float e = exp2_approx(-kLog2e * v), r = rcp_approx(1.f + e);
+    s = a < -kMost ? 0.f : r;
+    c = e * r;
+  }
+};
 
 // The activation of one row's expert and its derivatives.
 template <int ACT>
@@ -272,67 +306,70 @@ struct Act {
   float b, bl, k0, k1;   // SITU: caps and -2 log2(e) / cap, 0 without one; SWIGLU_BIAS: b = a, bl = c
   __device__ __forceinline__ Act(float p0, float p1) : b(p0), bl(p1), k0(0.f), k1(0.f) {
     if (ACT == SITU_ACT_FN_SITU) {
-      k0 = p0 > 0.f ? -2.f * kLog2e * rcp_approx(p0) : 0.f;
-      k1 = p1 > 0.f ? -2.f * kLog2e * rcp_approx(p1) : 0.f;
+      constexpr float kLeast = -3e38f;         // finite beside caps below fp32's normal numbers
+      k0 = p0 > 0.f ? fmaxf(-2.f * kLog2e * rcp_approx(p0), kLeast) : 0.f;
+      k1 = p1 > 0.f ? fmaxf(-2.f * kLog2e * rcp_approx(p1), kLeast) : 0.f;
     }
   }
-  __device__ __forceinline__ float swiglu_exp(float g) const {
-    return exp2_approx(max_nan(min_nan(-kLog2e * b * g, 80.f * kLog2e), -80.f * kLog2e));
-  }
   __device__ __forceinline__ float value(float g, float u) const {
-    if (ACT == SITU_ACT_FN_SWIGLU_BIAS) return g * (u + bl) * rcp_approx(1.f + swiglu_exp(g));
-    const float e0 = exp25(-kLog2e * g), e1 = exp25(k0 * g), e2 = exp25(k1 * u);
-    const float ng = k0 < 0.f ? b * (1.f - e1) : g, dg = k0 < 0.f ? 1.f + e1 : 1.f;
-    const float nu = k1 < 0.f ? bl * (1.f - e2) : u, du = k1 < 0.f ? 1.f + e2 : 1.f;
-    return ng * nu * rcp_approx((1.f + e0) * dg * du);
+    if (ACT == SITU_ACT_FN_SWIGLU_BIAS) return g * sigmoid(b * g) * (u + bl);
+    return Tanh(g, b, k0).t * sigmoid(g) * Tanh(u, bl, k1).t;
   }
   // h and its derivatives by g and u
   __device__ __forceinline__ float all(float g, float u, float& hg, float& hu) const {
     if (ACT == SITU_ACT_FN_SWIGLU_BIAS) {
-      const float e0 = swiglu_exp(g), s = rcp_approx(1.f + e0), up = u + bl;
-      hu = g * s;
-      hg = s * fmaf(b * hu, e0, 1.f) * up;
+      const float up = u + bl;
+      const Sigmoid s(b * g);
+      hu = g * s.s;
+      hg = s.s * fmaf(s.v, s.c, 1.f) * up;
       return hu * up;
     }
-    const float e0 = exp25(-kLog2e * g), e1 = exp25(k0 * g), e2 = exp25(k1 * u);
-    const float d0 = 1.f + e0, d1 = 1.f + e1, d2 = 1.f + e2;
-    const float d12 = d1 * d2, r = rcp_approx(d0 * d12);
-    const float r0 = r * d12, r12 = r * d0, r1 = r12 * d2, r2 = r12 * d1;
-    const float t = k0 < 0.f ? b * (1.f - e1) * r1 : g, dt = k0 < 0.f ? 4.f * e1 * r1 * r1 : 1.f;
-    const float up = k1 < 0.f ? bl * (1.f - e2) * r2 : u, dup = k1 < 0.f ? 4.f * e2 * r2 * r2 : 1.f;
-    const float gate = t * r0;
-    hg = r0 * fmaf(gate, e0, dt) * up;
-    hu = gate * dup;
-    return gate * up;
+    const Tanh t(g, b, k0), up(u, bl, k1);
+    const Sigmoid s(g);
+    const float gate = t.t * s.s;
+    hg = s.s * fmaf(t.t, s.c, t.dt) * up.t;
+    hu = gate * up.dt;
+    return gate * up.t;
   }
 };
 
 // SITU with both caps, on pairs, where no exponential or product of them can
-// overflow: the exponents' sum is below 2^124 for the thread's largest gate and
-// up (so there is no clamp, and no NaN or infinity among them).  One at a time the
-// kernels were bound by issue slots (52 instructions a pair: forward 141 us).
+// overflow: the exponents' sum is below 120 for the thread's largest gate and up (so
+// there is no NaN or infinity among them).  One at a time the kernels
+// were bound by issue slots (52 instructions a pair: forward 141 us).
 struct Situ2 {
-  F2 nb, b, nbl, bl, k, k0, k1;
+  F2 k, k0, k1;
   float most_g, most_u;   // exponents per unit of |g| and |u|
   bool capped;
   __device__ __forceinline__ explicit Situ2(const Act<SITU_ACT_FN_SITU>& a)
-      : nb(f2(-a.b)), b(f2(a.b)), nbl(f2(-a.bl)), bl(f2(a.bl)), k(f2(-kLog2e)), k0(f2(a.k0)), k1(f2(a.k1)),
+      : k(f2(-kLog2e)), k0(f2(a.k0)), k1(f2(a.k1)),
         most_g(kLog2e - a.k0), most_u(-a.k1), capped(a.k0 < 0.f && a.k1 < 0.f) {}
   __device__ __forceinline__ bool fits(float amax_g, float amax_u) const {
     return capped && amax_g * most_g + amax_u * most_u < 120.f;   // false for NaN
   }
+  // cap tanh(x / cap) = x (1 - E) / (y (1 + E)), y = max(|x / cap|, kSmall), E = e^-2y: z = -2 y log2(e) takes y's
+  // place, with the constants that leaves in the sigmoid's denominator
   __device__ __forceinline__ F2 value(F2 g, F2 u) const {
-    const F2 one = f2(1.f), e0 = exp2_pair(g * k), e1 = exp2_pair(g * k0), e2 = exp2_pair(u * k1);
-    return fma2(e1, nb, b) * fma2(e2, nbl, bl) * rcp_pair((e0 + one) * (e1 + one) * (e2 + one));
+    const F2 one = f2(1.f), c = f2(0.25f / (kLog2e * kLog2e)), z1 = away(g * k0), z2 = away(u * k1);
+    const F2 e0 = exp2_pair(g * k), e1 = exp2_pair(z1), e2 = exp2_pair(z2);
+    return (g * (one - e1)) * (u * (one - e2)) * rcp_pair(fma2(e0, c, c) * fma2(e1, z1, z1) * fma2(e2, z2, z2));
   }
-  __device__ __forceinline__ F2 all(F2 g, F2 u, F2& hg, F2& hu) const {
-    const F2 one = f2(1.f), four = f2(4.f), e0 = exp2_pair(g * k), e1 = exp2_pair(g * k0), e2 = exp2_pair(u * k1);
-    const F2 d0 = e0 + one, d1 = e1 + one, d2 = e2 + one, d12 = d1 * d2, r = rcp_pair(d0 * d12);
-    const F2 r0 = r * d12, r12 = r * d0, r1 = r12 * d2, r2 = r12 * d1;
-    const F2 dt = (four * e1 * r1) * r1, up = fma2(e2, nbl, bl) * r2, dup = (four * e2 * r2) * r2;
-    const F2 gate = fma2(e1, nb, b) * r1 * r0;
+  static __device__ __forceinline__ F2 away(F2 z) {
+    const float2 a = both(z);
+    constexpr float kMost = -2.f * kLog2e * kSmall;
+    return f2(fminf(-fabsf(a.x), kMost), fminf(-fabsf(a.y), kMost));
+  }
+  // h, and its derivatives by g and, a 16th of it, by u: gate is a quarter here, up four times
+  __device__ __forceinline__ F2 all(F2 g, F2 u, F2& hg, F2& hu16) const {
+    constexpr float kC = -2.f * kLog2e;      // z / y
+    const F2 one = f2(1.f), z1 = away(g * k0), z2 = away(u * k1);
+    const F2 e0 = exp2_pair(g * k), e1 = exp2_pair(z1), e2 = exp2_pair(z2);
+    const F2 d0 = e0 + one, d1 = fma2(e1, z1, z1), d2 = fma2(e2, z2, z2), d12 = d1 * d2, r = rcp_pair(d0 * d12);
+    const F2 r0 = r * d12, r12 = r * d0, r1 = r12 * d2, r2 = r12 * d1, q1 = z1 * r1, q2 = z2 * r2;
+    const F2 dt = (e1 * q1) * q1, dup = (e2 * q2) * q2;   // a quarter each
+    const F2 gate = (g * fma2(e1, f2(-.25f * kC), f2(.25f * kC))) * r1 * r0, up = (u * fma2(e2, f2(-4.f * kC), f2(4.f * kC))) * r2;
     hg = r0 * fma2(gate, e0, dt) * up;
-    hu = gate * dup;
+    hu16 = gate * dup;
     return gate * up;
   }
 };
@@ -349,7 +386,7 @@ struct Place {
 };
 
 template <int DT, int ACT, bool SAVE>
-__global__ void __launch_bounds__(512, 3)   // 93 us with 42 registers, 102 with 60: more rows' loads at once
+__global__ void __launch_bounds__(256, ACT == SITU_ACT_FN_SITU ? 5 : 6)   // 101 us with 48 registers, 104 with 64 and, spilling, with 40
 gated_kernel(GatedParams p) {
   const Place at;
   const bool first = at.r < p.S && at.c < p.I, second = at.r < p.S && at.c + 16 < p.I;
@@ -412,7 +449,7 @@ gated_kernel(GatedParams p) {
 }
 
 template <int DT, int ACT, bool H>
-__global__ void __launch_bounds__(512, 2)   // 118 us with 64, 161 with 42, which spill
+__global__ void __launch_bounds__(256, 4)   // 123 us with 64 registers, 152 with 48, which spill
 gated_back_kernel(GatedParams p) {
   const Place at;
   const int e = at.r < p.S ? expert_of(p.offsets, p.E, (int)at.r, at.together) : -1;
@@ -444,12 +481,13 @@ gated_back_kernel(GatedParams p) {
       if (fits) {
         if constexpr (ACT == SITU_ACT_FN_SITU) {
           const Situ2 a(act);
+          const F2 sixteen = f2(16.f);
 #pragma unroll
           for (int i = 0; i < 8; i += 2) {
             F2 hg, hu;
             const F2 dd = f2(df[i], df[i + 1]);
             const float2 v = both(a.all(f2(fg[i], fg[i + 1]), f2(fu[i], fu[i + 1]), hg, hu));
-            const float2 x = both(dd * hg), y = both(dd * hu);
+            const float2 x = both(dd * hg), y = both((dd * sixteen) * hu);
             h[i] = v.x;
             h[i + 1] = v.y;
             fg[i] = x.x;
@@ -555,9 +593,12 @@ struct Shape {
 Shape shape_of(int S, int K, int rows = 1) {   // rows of a thread
   const int pieces = (K + 31) / 32 * 2;
   int x, y, parts = 1;
-  if (pieces <= 32) {
+  if (pieces <= 16) {
     x = pieces;
     y = 16;
+  } else if (pieces <= 32) {
+    x = (pieces + 3) / 4 * 4;
+    y = 8;
   } else {
     parts = (pieces + 255) / 256;
     x = ((pieces + parts - 1) / parts + 31) / 32 * 32;

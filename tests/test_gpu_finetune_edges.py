@@ -85,3 +85,83 @@ def test_f16_gradients_of_rows_of_every_size():
         want = p.T @ t
         within(got, want, far_bar(want, p, pa, t, C, kept))
     assert torch.isnan(db[1, :, 3]).all() and torch.isfinite(db[0]).all() and torch.isfinite(da[0]).all()
+# --------------------------------------------------------------------------
+# gated activation near zero, beside large caps and far below it
+# --------------------------------------------------------------------------
+
+def factors(x, cap):
+    """cap tanh(x / cap) and its derivative in 64 bits; x and 1 without a cap."""
+    if cap <= 0:
+        return x, torch.ones_like(x)
+    y = x / cap
+    s = torch.exp(-2 * y.abs())
+    return cap * torch.tanh(y), 4 * s / (1 + s) ** 2
+
+
+# Relative errors.  A factor cap tanh(x / cap): where |x / cap| >= 2^-7.5 the exponential is off by 2^-22 and the
+# difference 1 - e^(-2 x / cap) is at least 2^-6.5, so off by 2^-15.5; below, by the 2^-16.5 that tanh(y)/y is short of
+# 1.  A sigmoid: 2^-22 and 2^-23.4 of its argument's magnitude, below 2^-16.9 for |g| <= 80.  Two factors, a sigmoid and
+# roundings: below 2^-14.  A derivative is off by 2^-15 where x counts as 2^-7.5: a fifth more.
+NEAR = 2.0 ** -14
+CAPS = [0.5, 1.7, 30.0, 2.0 ** 12, 3e6, 1e9, 1e30, 0.0]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("b", CAPS)
+@pytest.mark.parametrize("bl", [0.7, 1e8, -1.0])
+@pytest.mark.parametrize("far", [False, True])
+def test_situ_is_rounded_once(dtype, b, bl, far):
+    # magnitudes from 2^-20 to 4, or to 80; in blocks of mixed and of like size (8 bits keep a block's largest)
+    g = gen(7)
+    S, I = 96, 64
+    size = torch.rand(S, 2 * I, generator=g, device="cuda") * (27.3 if far else 22) - 20
+    size[::3] = size[::3, :1]
+    size = size.clamp(max=6.32 if far else 2.0)
+    x = (torch.exp2(size) * (torch.randint(0, 2, size.shape, generator=g, device="cuda") * 2 - 1)).to(dtype)
+    p0, p1 = torch.tensor([b], device="cuda"), torch.tensor([bl], device="cuda")
+    h, q, s = B.situ_moe_gated(x, p0, p1, save=True)
+    tiny = TINY[dtype] + 2.0 ** -118           # a sigmoid below 2^-126 is zero
+
+    def parts(x):
+        gg, u = x.double().chunk(2, 1)
+        (t, dt), (up, dup) = factors(gg, p0.item()), factors(u, p1.item())
+        sg, cg = torch.sigmoid(gg), torch.sigmoid(-gg)
+        return t * sg, dt * sg, t * sg * cg, up, dup
+
+    gate, _, _, up, _ = parts(x)
+    want = gate * up
+    within(h, want, (H[dtype] + NEAR) * want.abs() + tiny)
+    assert torch.equal(B.situ_moe_gated(x, p0, p1), h)
+    back = B.situ_moe_restore_mxfp8(q.reshape(2 * S, I), s.reshape(2 * S, -1), F32).reshape(S, 2 * I)
+    dh = normal(g, S, I, dtype=dtype)
+    dx, h2 = B.situ_moe_gated_backward(dh, q, s, p0, p1, want_h=True)
+    gate, d0, d1, up, dup = parts(back)
+    within(h2, gate * up, (H[dtype] + NEAR) * (gate * up).abs() + tiny)
+    d = dh.double()
+    want = d * (d0 + d1) * up
+    # the slope's two terms may cancel: their own errors, not their sum's
+    within(dx[:, :I], want, H[dtype] * want.abs() + 1.2 * NEAR * (d * up).abs() * (d0 + d1.abs()) + tiny)
+    want = d * gate * dup
+    within(dx[:, I:], want, (H[dtype] + 1.2 * NEAR) * want.abs() + tiny)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("act", [B.SITU_ACT_FN_SITU, B.SITU_ACT_FN_SWIGLU_BIAS])
+def test_gated_values_do_not_depend_on_their_neighbours(dtype, act):
+    # gates below -25 beside ordinary and beside large ones, each as its limit has it
+    I = 64
+    g = torch.linspace(-80, -20, I, device="cuda")
+    x = torch.stack([torch.cat((g, torch.full((I,), 1.5, device="cuda")))] * 2).to(dtype)
+    x[1, ::16] = 3e4                             # another form of the arithmetic for these lanes' columns
+    for p in ((0.7, 1.9), (0.0, 0.0)) if act == B.SITU_ACT_FN_SITU else ((1.0, 0.5),):
+        p0, p1 = torch.tensor([p[0]], device="cuda"), torch.tensor([p[1]], device="cuda")
+        h = B.situ_moe_gated(x, p0, p1, activation=act)
+        gg = x[:, :I].double()
+        if act == B.SITU_ACT_FN_SITU:
+            want = factors(gg, p[0])[0] * torch.sigmoid(gg) * factors(x[:, I:].double(), p[1])[0]
+        else:
+            want = gg * torch.sigmoid(gg) * (x[:, I:].double() + p[1])
+        same = torch.arange(I, device="cuda") % 16 != 0
+        within(h[:, same], want[:, same], (H[dtype] + NEAR) * want[:, same].abs() + TINY[dtype])
+        assert ((h[0, same].double() - h[1, same].double()).abs() <= (2 * H[dtype] + 2 * NEAR) * want[0, same].abs()
+                + TINY[dtype]).all()
