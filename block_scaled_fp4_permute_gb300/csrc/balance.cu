@@ -389,6 +389,7 @@ router_back_kernel(RouterBackParams p) {
       }
     }
     const bool keep = have && (!p.mask || p.mask[t] != 0);
+    if (!keep && dw == 0.f) w = 0.f;            // a padding token's weight may be NaN
     float dot = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {

@@ -659,8 +659,8 @@ situ_status situ_moe_balance_loss(const situ_balance_args* args, void* workspace
  * several ranks' tokens (f_e is a constant here; the gradient is then that of
  * this rank's tokens in the joint loss).  Terms of an ID that a row names
  * twice are added; IDs outside [0, E) take none.  A masked row without weight
- * gradients gives zeros, whatever its logits hold.  Results do not depend on
- * the order of execution.  Errors: as above, UNSUPPORTED (renormalize). */
+ * gradients (none, or zeros) gives zeros, whatever its logits and weights hold.
+ * Results do not depend on the order of execution.  Errors: as above, UNSUPPORTED (renormalize). */
 typedef struct situ_router_backward_args {
   const float* router_logits;
   int64_t ld;

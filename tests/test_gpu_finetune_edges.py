@@ -165,3 +165,26 @@ def test_gated_values_do_not_depend_on_their_neighbours(dtype, act):
         within(h[:, same], want[:, same], (H[dtype] + NEAR) * want[:, same].abs() + TINY[dtype])
         assert ((h[0, same].double() - h[1, same].double()).abs() <= (2 * H[dtype] + 2 * NEAR) * want[0, same].abs()
                 + TINY[dtype]).all()
+# --------------------------------------------------------------------------
+# router: masked rows whose weights are NaN
+# --------------------------------------------------------------------------
+
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("E", [24, 200, 1500])
+def test_masked_tokens_of_any_logits_get_no_gradient(renorm, E):
+    T, k = 40, 3
+    g = gen(E)
+    logits, mask = torch.randn(T, E, generator=g, device="cuda"), torch.ones(T, dtype=torch.bool, device="cuda")
+    rows = [3, 11, 17, 39]
+    mask[rows] = False
+    dw = torch.randn(T, k, generator=g, device="cuda") * mask[:, None]       # the loss does not see them
+    want = logits.clone().requires_grad_()
+    _, w, _, loss = B.balanced_route(want, k, renormalize=renorm, mask=mask)
+    torch.autograd.backward((w, loss), (dw, torch.ones_like(loss)))
+    bad = logits.clone()
+    bad[3], bad[11], bad[17], bad[39, 5] = -float("inf"), float("inf"), float("nan"), float("nan")
+    leaf = bad.requires_grad_()
+    _, w, _, loss = B.balanced_route(leaf, k, renormalize=renorm, mask=mask)
+    torch.autograd.backward((w, loss), (dw, torch.ones_like(loss)))
+    assert (leaf.grad[rows] == 0).all() and torch.equal(leaf.grad[mask], want.grad[mask])
+    assert torch.isfinite(leaf.grad).all()
