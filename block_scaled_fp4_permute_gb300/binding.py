@@ -107,7 +107,8 @@ class SituLoraBackwardArgs(ctypes.Structure):
         ("dy", ctypes.c_void_p), ("ld_dy", ctypes.c_int64), ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64),
         ("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("offsets", ctypes.c_void_p), ("scale", ctypes.c_void_p),
         ("u", ctypes.c_void_p), ("dx0", ctypes.c_void_p), ("ld_dx0", ctypes.c_int64), ("dx", ctypes.c_void_p),
-        ("ld_dx", ctypes.c_int64), ("da", ctypes.c_void_p), ("db", ctypes.c_void_p), ("device_status", ctypes.c_void_p)]
+        ("ld_dx", ctypes.c_int64), ("da", ctypes.c_void_p), ("db", ctypes.c_void_p), ("device_status", ctypes.c_void_p),
+        ("dy_scale", ctypes.c_void_p)]
 
 
 def library_path() -> str:
@@ -1252,13 +1253,15 @@ def situ_moe_lora(base, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, *, id
 
 
 def situ_moe_lora_backward(dy: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, offsets: torch.Tensor,
-                           u: torch.Tensor, *, scale=None, dx=None, out=None, stream=None):
+                           u: torch.Tensor, *, scale=None, dx=None, out=None, dy_scale=None, stream=None):
     """The gradients of situ_moe_lora with rows sorted by adapter, from dy [S, N]
     and its u: (dx [S, K], da, db).  ``dx`` is what x's gradient is added to
     (that of the shared projection; None: zeros, of x's type), and ``out``,
-    which may be it, receives the sum."""
+    which may be it, receives the sum.  dy counts times ``dy_scale``, one fp32 on
+    the device."""
     if stream is not None:
-        return _on_stream(stream, situ_moe_lora_backward, dy, x, a, b, offsets, u, scale=scale, dx=dx, out=out)
+        return _on_stream(stream, situ_moe_lora_backward, dy, x, a, b, offsets, u, scale=scale, dx=dx, out=out,
+                          dy_scale=dy_scale)
     index = x.get_device()
     a, b, pa, pb, scale, S, K, N, r, n = _adapters(x, a, b, scale, index)
     dtype = x.dtype
@@ -1278,6 +1281,9 @@ def situ_moe_lora_backward(dy: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b
     if dx is not None:
         dx, pdx0, ld_dx0 = _beside(dx, (S, K), (dtype, torch.float32), "dx", index)
         dx_dtype = dx.dtype
+    if dy_scale is not None and (dy_scale.dtype is not torch.float32 or dy_scale.numel() != 1
+                                 or dy_scale.get_device() != index):
+        raise ValueError(f"dy_scale must be one fp32 on cuda:{index}")
     new = _new(index)
     if out is None:
         out, ldo = new((S, K), (K, 1), dx_dtype), K
@@ -1288,9 +1294,19 @@ def situ_moe_lora_backward(dy: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b
     ws, pws = _scratch(size, new)
     args = SituLoraBackwardArgs(_DTYPES[dtype], _DTYPES.get(dx_dtype, -1), S, K, N, r, n, pdy, ld_dy, px, ldx, pa, pb,
                                 offsets.data_ptr(), None if scale is None else scale.data_ptr(), pu, pdx0,
-                                ld_dx0, out.data_ptr(), ldo, da.data_ptr(), db.data_ptr(), _status_word(index).data_ptr())
+                                ld_dx0, out.data_ptr(), ldo, da.data_ptr(), db.data_ptr(), _status_word(index).data_ptr(),
+                                None if dy_scale is None else dy_scale.data_ptr())
     _enqueue("situ_moe_lora_backward", index, ctypes.byref(args), pws, size)
     return out, da, db
+
+
+def _into_f16(t: torch.Tensor):
+    """(t times a power of two, as f16; that power's inverse): the largest
+    magnitude in [2^14, 2^15), all on the device."""
+    most = torch.linalg.vector_norm(t, float("inf"))
+    e = torch.where(torch.isfinite(most), 15 - torch.frexp(most).exponent, 0).clamp(-126, 126).int()
+    power, back = ((127 + e) << 23).view(torch.float32), ((127 - e) << 23).view(torch.float32)
+    return torch.mul(t, power, out=torch.empty(t.shape, dtype=torch.float16, device=t.device)), back
 
 
 class _LoraLinear(torch.autograd.Function):
@@ -1306,14 +1322,20 @@ class _LoraLinear(torch.autograd.Function):
         x, a, b, offsets, u, scale = ctx.saved_tensors
         dx = da = db = None
         if any(ctx.needs_input_grad[1:4]):
-            dx, da, db = situ_moe_lora_backward(dy.to(x.dtype), x, a, b, offsets, u, scale=scale)
+            if dy.dtype is torch.float32 and x.dtype is torch.float16 and dy.numel():
+                d, back = _into_f16(dy)
+            else:
+                d, back = dy.to(x.dtype), None
+            dx, da, db = situ_moe_lora_backward(d, x, a, b, offsets, u, scale=scale, dy_scale=back)
         return dy if ctx.needs_input_grad[0] else None, dx, da, db, None, None
 
 
 def lora_linear(base: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, offsets: torch.Tensor,
                 scale=None) -> torch.Tensor:
     """situ_moe_lora for training, rows sorted by adapter: differentiable in
-    base, x, a and b (up to 1,024 adapters)."""
+    base, x, a and b (up to 1,024 adapters).  Beside an fp32 base the incoming
+    gradient is rounded to the operands' type for those of x, a and b, in f16
+    under a power of two of its largest magnitude; base's is as it came."""
     if a.shape[0] > 1024:
         raise ValueError("the gradients take up to 1024 adapters")
     return _graphed(_LoraLinear.apply, base, x, a, b, offsets, scale)

@@ -72,6 +72,7 @@ struct LoraParams {
   long shrink_ctas, least;         // CTAs that the shrink's chunks are dealt out over, chunks of each at least
   float* part;                     // [parts of a tile][S][r]
   const float* scale;              // [n] or null
+  const float* times;              // [1] or null: what u counts times besides
   const void* base;
   long ld_base;
   void* out;
@@ -792,6 +793,7 @@ expand_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
   // u of a tile in its place ts: what warp `part` of `among` has of it
   auto stage_u = [&](const Segment& g, int ts, int part, int among, int parts) {
     const bool write = p.u16 && g.from == 0 && parts > 0;
+    const float times = TRANS && p.times ? __ldg(p.times) : 1.f;
     const Adapters<kTile>& ad = lists[ts];
     uint8_t* us = smem + ts * p.u_bytes;
     const size_t stride = (size_t)p.S * p.r;
@@ -810,7 +812,7 @@ expand_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
         for (int i = 0; i < kRows; ++i) {
           const int r = r0 + 4 * i + (lane >> 3);
           of[i] = ad.of[r];
-          f[i] = of[i] >= 0 && p.scale ? __ldg(p.scale + of[i]) : 1.f;
+          f[i] = times * (of[i] >= 0 && p.scale ? __ldg(p.scale + of[i]) : 1.f);
           src[i] = p.part + (size_t)(g.tile * kTile + r) * p.r + c0;
 #pragma unroll
           for (int c = 0; c < kC; ++c) u[i][c][0] = u[i][c][1] = u[i][c][2] = u[i][c][3] = 0.f;
@@ -1577,7 +1579,7 @@ extern "C" situ_status situ_moe_lora_backward(const situ_lora_backward_args* a, 
   for (const void* q : ptrs)
     if (bad(q, 15)) return SITU_ERR_MISALIGNED;
   if (bad(workspace, 31)) return SITU_ERR_MISALIGNED;
-  if (bad(a->offsets, 3) || bad(a->scale, 3) || bad(a->device_status, 3)) return SITU_ERR_MISALIGNED;
+  if (bad(a->offsets, 3) || bad(a->scale, 3) || bad(a->device_status, 3) || bad(a->dy_scale, 3)) return SITU_ERR_MISALIGNED;
   if (workspace_bytes < situ_moe_lora_backward_workspace_size(a->S, a->K, a->N, a->r)) return SITU_ERR_WORKSPACE_TOO_SMALL;
   uint8_t* v = static_cast<uint8_t*>(workspace) + shared_bytes(a->S, a->N, a->r);
   FarParams far = {};
@@ -1607,6 +1609,7 @@ extern "C" situ_status situ_moe_lora_backward(const situ_lora_backward_args* a, 
   o.u32 = far.u32;
   o.row_most = far.row_most;
   o.most = far.most;
+  o.dy_scale = a->dy_scale;
   o.ldx = a->ldx;
   o.ld_dy = a->ld_dy;
   o.offsets = a->offsets;
@@ -1624,6 +1627,7 @@ extern "C" situ_status situ_moe_lora_backward(const situ_lora_backward_args* a, 
     s.scale = a->scale;
     s.err = a->device_status;
     s.far = far;
+    s.times = a->dy_scale;
     LoraParams x = s;
     s.C = a->N;
     x.C = a->K;

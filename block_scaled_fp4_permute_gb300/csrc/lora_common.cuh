@@ -188,6 +188,7 @@ struct OuterArgs {
   float* u32;
   const float* row_most;
   const uint32_t* most;
+  const float* dy_scale;                 // [1] or null: what dy counts times (v has it already)
   int64_t ldx, ld_dy;
   const int32_t* offsets;
   void *da, *db;

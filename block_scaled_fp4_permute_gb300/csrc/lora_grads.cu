@@ -40,6 +40,7 @@ struct OuterParams {
   int C[2], blocks[2];                   // of x and dy: columns, tiles of 128
   void* out[2];                          // da, db
   const uint32_t* most;                  // f16: [2][n], the bits of each adapter's largest v and u
+  const float* dy_scale;
   float* parts;                          // [CTA][2][128][r]
   int stages, run;                       // run: chunks of a sum in tensor memory
   int* err;
@@ -79,19 +80,19 @@ struct Deal {
   }
 };
 
-// f16: what v or u of a piece's adapter was divided by
+// What a piece's sums count times: what dy does, and in f16 what v or u of its adapter
+// was divided by.
 template <int DT>
 __device__ __forceinline__ float factor_of(const OuterParams& p, const Piece& t) {
-  return DT == SITU_DT_F16 ? exp2i(power_of(__uint_as_float(__ldcg(p.most + t.which * p.n + t.e)))) : 1.f;
+  const float f = DT == SITU_DT_F16 ? exp2i(power_of(__uint_as_float(__ldcg(p.most + t.which * p.n + t.e)))) : 1.f;
+  return t.which && p.dy_scale ? f * __ldg(p.dy_scale) : f;
 }
 
 // Sums of column c of a tile to the gradient, rounded: da is [j][c], db [c][j].
 template <int DT>
 __device__ __forceinline__ void store16(const OuterParams& p, const Piece& t, float f, int c, int j, float* v) {
-  if (DT == SITU_DT_F16) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] *= f;
-  }
+  for (int i = 0; i < 8; ++i) v[i] *= f;
   uint16_t* out = static_cast<uint16_t*>(p.out[t.which]);
   if (t.which == 0) {
     out += ((size_t)t.e * p.r + j) * p.C[0] + c;
@@ -457,6 +458,7 @@ situ_status launch_outer(const OuterArgs& a, cudaStream_t st) {
   p.parts = a.parts;
   p.err = a.err;
   p.most = a.most;
+  p.dy_scale = a.dy_scale;
   const bool f16 = a.dtype == SITU_DT_F16;
   if (f16) {
     const TermsParams t = {static_cast<const uint16_t*>(a.u), static_cast<float*>(a.v), a.u32, a.row_most, a.S, a.r, a.n, a.offsets,

@@ -779,6 +779,8 @@ situ_status situ_moe_lora(const situ_lora_args* args, void* workspace, size_t wo
 /* situ_moe_lora_backward -- from dy [S, N] and the forward's u, rows sorted by
  * adapter (offsets; n up to SITU_GEMM_MAX_GROUPS):
  *   v = scale dy b,  dx = dx0 + v a,  da[e] = v^T x,  db[e] = dy^T u   over e's rows
+ * where dy counts times *dy_scale (one fp32 on the device, or NULL: 1), so that a
+ * gradient out of f16's range can be brought into it.
  * dx0 (or NULL: zeros) is the shared projection's gradient, dx may be it, both
  * of the operands' type or fp32; da [n, r, K] and db [n, N, r] are of the
  * operands' type, rounded once, zeros for an adapter without rows.  v and u are
@@ -808,6 +810,7 @@ typedef struct situ_lora_backward_args {
   void* da;
   void* db;
   int32_t* device_status;
+  const float* dy_scale;          /* [1] on the device, or NULL: 1 */
 } situ_lora_backward_args;
 size_t situ_moe_lora_backward_workspace_size(int32_t S, int32_t K, int32_t N, int32_t r);
 situ_status situ_moe_lora_backward(const situ_lora_backward_args* args, void* workspace, size_t workspace_bytes,

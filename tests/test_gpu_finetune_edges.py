@@ -188,3 +188,65 @@ def test_masked_tokens_of_any_logits_get_no_gradient(renorm, E):
     torch.autograd.backward((w, loss), (dw, torch.ones_like(loss)))
     assert (leaf.grad[rows] == 0).all() and torch.equal(leaf.grad[mask], want.grad[mask])
     assert torch.isfinite(leaf.grad).all()
+
+
+# --------------------------------------------------------------------------
+# adapters beside an fp32 projection
+# --------------------------------------------------------------------------
+
+@pytest.mark.parametrize("size", [1e-30, 1e-9, 1.0, 1e7])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_fp32_gradients_beside_16_bit_operands(dtype, size):
+    g = gen(11)
+    counts, K, N, r = [60, 0, 41], 136, 72, 8
+    S, n, off = sum(counts), len(counts), offsets_of(counts)
+    inv = 1.0 / size                                    # brings the results back into f16's range where it can
+    x = normal(g, S, K, std=min(inv, 3e3), dtype=dtype)
+    a, b = normal(g, n, r, K, std=0.1, dtype=dtype), normal(g, n, N, r, std=min(inv, 1e3), dtype=dtype)
+    leaves = [t.requires_grad_() for t in (torch.randn(S, N, generator=g, device="cuda"), x, a, b)]
+    dy = torch.randn(S, N, generator=g, device="cuda") * size
+    B.lora_linear(*leaves, off).backward(dy)
+    assert torch.equal(leaves[0].grad, dy)
+    x, a, b = (t.detach() for t in leaves[1:])
+    most = dy.abs().max().double() if dtype is F16 else 0.0
+    # dy rounded to the operands' type, in f16 under a power of two (half a subnormal's step, 2^-25, beside 2^14); what
+    # the two terms leave (bf16 2^-17, f16 2^-22); the rest as above
+    terms16 = 2.0 ** -17 if dtype is BF16 else 2.0 ** -22
+    for e, (v, va, xe), (ue, ua, de) in gradients(dy, x, a, b, counts, torch.ones(n, device="cuda")):
+        if not counts[e]:
+            assert (leaves[2].grad[e] == 0).all() and (leaves[3].grad[e] == 0).all()
+            continue
+        L = counts[e]
+        want, terms = v.T @ xe, v.abs().T @ xe.abs()
+        within(leaves[2].grad[e], want, 1.1 * H[dtype] * want.abs() + (H[dtype] + (2 * L + 2 * N + 80) * U) * (va.T @ xe.abs())
+               + terms16 * terms + 2.0 ** -39 * (most * b[e].double().abs().sum(0) + v.abs().max())[:, None] * xe.abs().sum(0)
+               + TINY[dtype] / 2)
+        want, terms = de.T @ ue, de.abs().T @ ue.abs()
+        within(leaves[3].grad[e], want, 1.1 * H[dtype] * want.abs() + (H[dtype] + terms16 + 2 * L * U) * terms
+               + (2 * K + 80) * U * (de.abs().T @ ua) + 2.0 ** -39 * most * ue.abs().sum(0)
+               + (2.0 ** -25 + 2.0 ** -39 * ue.abs().max()) * de.abs().sum(0)[:, None] + TINY[dtype] / 2)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_dy_scale(dtype):
+    # a power of two changes no bit beside dy that has it
+    g = gen(12)
+    counts, K, N, r = [300, 41], 136, 264, 16
+    S, off = sum(counts), offsets_of(counts)
+    x, dy = normal(g, S, K, dtype=dtype), normal(g, S, N, dtype=dtype)
+    a, b = normal(g, 2, r, K, std=0.1, dtype=dtype), normal(g, 2, N, r, std=0.3, dtype=dtype)
+    scale = torch.tensor([0.7, -1.3], device="cuda")
+    _, u = B.situ_moe_lora(None, x, a, b, offsets=off, scale=scale, keep=True)
+    for f in (0.125, 4.0, -1.0):
+        t = torch.tensor([f], device="cuda")
+        for p, q in zip(B.situ_moe_lora_backward(dy, x, a, b, off, u, scale=scale, dy_scale=t),
+                        B.situ_moe_lora_backward(dy * f, x, a, b, off, u, scale=scale)):
+            assert torch.equal(p, q)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    p = B.situ_moe_lora_backward(dy, x, a, b, off, u, scale=scale, dy_scale=t, stream=s)
+    s.synchronize()
+    assert all(torch.equal(i, j) for i, j in zip(p, B.situ_moe_lora_backward(dy * f, x, a, b, off, u, scale=scale)))
+    for bad in (torch.ones(2, device="cuda"), torch.ones(1), torch.ones(1, device="cuda", dtype=dtype)):
+        with pytest.raises(ValueError, match="dy_scale"):
+            B.situ_moe_lora_backward(dy, x, a, b, off, u, dy_scale=bad)
