@@ -949,6 +949,13 @@ def situ_moe_router_backward(router_logits: torch.Tensor, topk_ids: torch.Tensor
     return out
 
 
+def _constant(**tensors) -> None:
+    """Refuses what a gradient is asked for and none is made of."""
+    for name, t in tensors.items():
+        if t is not None and t.requires_grad and torch.is_grad_enabled():
+            raise ValueError(f"{name} gets no gradient here: detach it, or clear its requires_grad")
+
+
 def _graphed(f, *args):
     """f(*args) of an autograd function.  torch adds a leaf's gradient on the
     stream on which the first of its living graphs was built.  A backward pass
@@ -1168,11 +1175,12 @@ def expert_ffn(x: torch.Tensor, w1: torch.Tensor, w2: torch.Tensor, offsets: tor
     expert, differentiable in x [S, H], w1 [E, 2I, H] and w2 [E, H, I].  For the
     backward pass it keeps the gate/up columns in 8 bits, x in 8 bits
     (``keep`` "mxfp8") or as it is ("16bit"), and no h: 2 I + H bytes a row and
-    a 32nd, where 16 bits take 6 I + 2 H."""
+    a 32nd, where 16 bits take 6 I + 2 H.  p0 and p1 are constants."""
     if keep not in ("mxfp8", "16bit"):
         raise ValueError('keep must be "mxfp8" or "16bit"')
     if w1.dim() != 3 or w2.dim() != 3:
         raise ValueError("w1 must be [E, 2I, H] and w2 [E, H, I]")
+    _constant(p0=p0, p1=p1)
     return _graphed(_ExpertFfn.apply, x, w1, w2, offsets, p0, p1, activation, keep)
 
 
@@ -1335,9 +1343,11 @@ def lora_linear(base: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.T
     """situ_moe_lora for training, rows sorted by adapter: differentiable in
     base, x, a and b (up to 1,024 adapters).  Beside an fp32 base the incoming
     gradient is rounded to the operands' type for those of x, a and b, in f16
-    under a power of two of its largest magnitude; base's is as it came."""
+    under a power of two of its largest magnitude; base's is as it came.
+    ``scale`` is a constant."""
     if a.shape[0] > 1024:
         raise ValueError("the gradients take up to 1024 adapters")
+    _constant(scale=scale)
     return _graphed(_LoraLinear.apply, base, x, a, b, offsets, scale)
 
 

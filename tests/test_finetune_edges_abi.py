@@ -1,9 +1,24 @@
 """Refusals of the fine-tuning operators' entry points that came later (no GPU needed)."""
 import pytest
+import torch
 
+from block_scaled_fp4_permute_gb300 import binding as B
 from test_finetune_abi import lib, lora_back  # noqa: F401
 
 
 @pytest.mark.parametrize("over,status", [(dict(dy_scale=0xb002), 6), (dict(dy_scale=0xb001, S=0), 6)])
 def test_dy_scale_refusals(lib, over, status):  # noqa: F811
     assert lora_back(lib, **over) == status
+
+
+def test_constants_that_ask_for_a_gradient_are_refused():
+    # None came back for them without a word
+    h, ad, off = torch.zeros(4, 8, dtype=torch.bfloat16), torch.zeros(2, 8, 8, dtype=torch.bfloat16), torch.tensor([0, 4, 4])
+    one, leaf = torch.ones(2), torch.ones(2, requires_grad=True)
+    for name, call in (("p0", lambda: B.expert_ffn(h, ad, ad, off, leaf, one)), ("p1", lambda: B.expert_ffn(h, ad, ad, off, one, leaf)),
+                       ("scale", lambda: B.lora_linear(h, h, ad, ad, off, leaf))):
+        with pytest.raises(ValueError, match=name + " gets no gradient"):
+            call()
+        with torch.no_grad(), pytest.raises((TypeError, ValueError)) as e:   # goes on to the devices' check
+            call()
+        assert "gradient" not in str(e.value)
