@@ -720,7 +720,8 @@ shrink_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
 // memory for all the CTA's items of a tile, its 16-bit terms one after the
 // other along the contraction; warps of their own bring the next tile's meanwhile
 // (between two tiles it cost each CTA that has two 13 us of 70).  The items are
-// dealt out evenly over the CTAs, one per SM.
+// dealt out evenly over the CTAs, one per SM.  Waits are bounded from where they begin,
+// so those for what comes of u begin when the shrink, however long, has ended.
 template <int DT, bool TRANS, bool F32>
 __global__ void __launch_bounds__(kExpandThreads, 1)
 expand_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_base,
@@ -966,6 +967,7 @@ expand_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
       ++next;
     };
     for (int j = 0; j < p.y_stages - 1 && next < i1; ++j) load();
+    griddep_wait();
     for (long i = i0; i < i1; ++i, out.next()) {
       if (!warp_wait(ydone(out.s), out.ph, p.err, 101)) {
         ok = false;
@@ -990,6 +992,7 @@ expand_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
     const uint32_t idesc = idesc_of(DT == SITU_DT_BF16, false, TRANS, kCols);
     Turns w(p.stages), acc(2), tile(p.u_stages);
     bool ok = true;
+    griddep_wait();
     for (Segment g(i0, i1, blocks); g.more() && ok; g.next(), tile.next()) {
       if (!warp_wait(u_full(tile.s), tile.ph, p.err, 102)) {
         ok = false;
@@ -1043,9 +1046,10 @@ expand_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
       const int nd = ad.count;
       for (int b = g.from; b < g.to && ok; ++b)
         for (int d = 0; d < nd; ++d, w.next()) {
-          if (w.again() && !warp_wait(wempty(w.s), w.ph ^ 1, p.err, 108)) {
-            ok = false;
-            break;
+          if (w.again()) {
+            griddep_wait();
+            ok = warp_wait(wempty(w.s), w.ph ^ 1, p.err, 108);
+            if (!ok) break;
           }
           if (leader) {
             const uint32_t to = wbase + w.s * p.w_stage;

@@ -199,6 +199,7 @@ outer_kernel(const __grid_constant__ OuterMaps m, const OuterParams p) {
     const uint32_t idesc = idesc_of(DT == SITU_DT_BF16, true, true, 2 * p.r);
     Turns r(p.stages), acc(2);
     bool ok = true;
+    griddep_wait();                       // bounded waits for what comes of v begin here
     for (long i = i0; i < i1 && ok;) {
       const Piece t = deal.at(i, i1);
       i += t.to - t.from;
