@@ -1070,6 +1070,7 @@ expand_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__
       __syncwarp();
       mbar_arrive_if(tile_empty(tile.s), lane == 0);
     }
+    griddep_wait();
     leave(
         ok, [&] { return w.last([&](int j, uint32_t ph) { return warp_wait(wempty(j), ph, p.err, 109); }); },
         [&] { w.last([&](int j, uint32_t ph) { return drain_wait(wfull(j), ph); }); });

@@ -37,3 +37,8 @@ def test_sums_wait_after_u_has_been_staged():
     text = open(os.path.join(build.CSRC, "lora.cu")).read()
     text = text[text.index("\nexpand_kernel("):]
     assert text.index("if (first && round == 1) griddep_wait();") < text.index("// ---------------- sums onto base")
+
+
+def test_weights_leave_after_the_predecessor():
+    text = role("lora.cu", "expand_kernel", "weights")
+    assert "griddep_wait();" in text[:text.index("leave(")].splitlines()[-2]

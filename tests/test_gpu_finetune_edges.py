@@ -250,3 +250,24 @@ def test_dy_scale(dtype):
     for bad in (torch.ones(2, device="cuda"), torch.ones(1), torch.ones(1, device="cuda", dtype=dtype)):
         with pytest.raises(ValueError, match="dy_scale"):
             B.situ_moe_lora_backward(dy, x, a, b, off, u, dy_scale=bad)
+
+
+@pytest.mark.parametrize("order", ["mixed", "runs"])
+def test_adapters_beyond_those_that_are_sorted(order):
+    # more adapters than any sort here takes: tiles of as many adapters as rows
+    g = gen(21)
+    S, K, N, r, n = 3001, 72, 136, 8, 5000
+    x, a, b = normal(g, S, K), normal(g, n, r, K, std=0.1), normal(g, n, N, r, std=0.3)
+    base, ids = normal(g, S, N), torch.randint(-3, n + 3, (S,), generator=g, device="cuda").int()
+    if order == "runs":
+        ids = ids.sort().values
+    y = B.situ_moe_lora(base, x, a, b, ids=ids)
+    none = (ids < 0) | (ids >= n)
+    e = ids.clamp(0, n - 1).long()
+    xd, ad, bd = x.double(), a[e].double(), b[e].double()
+    u = torch.einsum("sk,srk->sr", xd, ad)
+    want = torch.einsum("sr,snr->sn", u, bd) * ~none[:, None] + base.double()
+    both = torch.einsum("sr,snr->sn", torch.einsum("sk,srk->sr", xd.abs(), ad.abs()), bd.abs())
+    second = torch.einsum("sr,snr->sn", u.abs(), bd.abs())
+    within(y, want, H[BF16] * want.abs() + (2 * K + 40) * U * both + (H[BF16] + (6 * r + 8) * U) * second + TINY[BF16])
+    assert torch.equal(y[none], base[none])
