@@ -959,17 +959,19 @@ def _constant(**tensors) -> None:
 def _graphed(f, *args):
     """f(*args) of an autograd function.  torch adds a leaf's gradient on the
     stream on which the first of its living graphs was built.  A backward pass
-    captured on another stream would draw that one into the capture, which can
-    end the process, so the captured forward pass is refused."""
+    captured elsewhere draws that stream into the capture, which is fine but for
+    the legacy default stream: that can end the process, so the captured forward
+    pass is refused."""
     nodes = []
     if torch.is_grad_enabled():
         for t in args:
             if isinstance(t, torch.Tensor) and t.is_cuda and t.requires_grad and t.is_leaf:
                 node, stream = torch.autograd.graph.get_gradient_edge(t).node, _raw_stream(t.get_device())
                 nodes.append(node)   # alive until f's graph holds it
-                if node.metadata.setdefault("situ_moe stream", stream) != stream and torch.cuda.is_current_stream_capturing():
-                    raise RuntimeError("captured on one stream while a graph of the same leaf, built on another, is alive: "
-                                       "drop what holds it (outputs, losses) first")
+                if node.metadata.setdefault("situ_moe stream", stream) == 0 != stream and torch.cuda.is_current_stream_capturing():
+                    raise RuntimeError("captured while a graph of the same leaf, built on the default stream, is alive: drop what "
+                                       "holds it (outputs, losses), or build it under a side stream, as a wrapper that keeps "
+                                       "its leaves' nodes has to be")
     return f(*args)
 
 

@@ -271,3 +271,34 @@ def test_adapters_beyond_those_that_are_sorted(order):
     second = torch.einsum("sr,snr->sn", u.abs(), bd.abs())
     within(y, want, H[BF16] * want.abs() + (2 * K + 40) * U * both + (H[BF16] + (6 * r + 8) * U) * second + TINY[BF16])
     assert torch.equal(y[none], base[none])
+
+
+# --------------------------------------------------------------------------
+# captures
+# --------------------------------------------------------------------------
+
+def test_a_capture_beside_nodes_kept_from_a_side_stream():
+    # the usual recipe: a warm-up on a side stream, a wrapper that keeps the leaves' nodes, and a graph on its own stream
+    g = gen(31)
+    S, K, N, r = 300, 72, 64, 8
+    x, dy = normal(g, S, K), normal(g, S, N)
+    a, b = normal(g, 2, r, K).requires_grad_(), normal(g, 2, N, r).requires_grad_()
+    off, base = offsets_of([100, 200]), torch.zeros(S, N, dtype=BF16, device="cuda")
+    B.lora_linear(base, x, a, b, off).backward(dy)
+    want, a.grad, b.grad = (a.grad.clone(), b.grad.clone()), None, None
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        kept = [t.expand_as(t).grad_fn.next_functions[0][0] for t in (a, b)]
+        for _ in range(2):
+            B.lora_linear(base, x, a, b, off).backward(dy)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    a.grad = b.grad = None
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        B.lora_linear(base, x, a, b, off).backward(dy)
+    x.mul_(2.0)                                  # a power of two, through every rounding
+    for _ in range(2):
+        graph.replay()
+    assert torch.equal(a.grad, 2 * want[0]) and torch.equal(b.grad, 2 * want[1]) and len(kept) == 2
