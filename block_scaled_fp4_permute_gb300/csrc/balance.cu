@@ -22,7 +22,7 @@
 // Measured (65,536 x 896, top-16): forward 43 us (5.5 TB/s) and 7 for the join,
 // gradient 76 to 81 (6 TB/s).
 #include "../../include/situ_moe.h"
-#include "situ_internal.h"
+#include "gemm_groups.cuh"
 
 #include <cooperative_groups.h>
 
@@ -43,7 +43,7 @@ constexpr int kManyRows = 16, kManyBackRows = 8;   // of a group
 constexpr int kMaxExperts = SITU_MAX_LOCAL_EXPERTS;
 constexpr int kFinalCtas = 8;        // of the joining kernel's one cluster
 constexpr int kFinalThreads = 512;
-constexpr int kSms = 152;
+constexpr int kMostSms = 256;        // that grids are sized for
 constexpr int kFold = 256;           // rows of a group whose column sums stay in registers
 
 struct BalanceParams {
@@ -344,7 +344,9 @@ balance_join_kernel(BalanceParams p, int parts) {
     *p.loss = tok > 0 ? (float)((double)p.coef * p.E * t / (tok * tok * p.k)) : 0.f;
   }
 }
-static_assert(kMaxExperts / 4 / kFinalCtas <= kFinalThreads && 2 * kSms <= kFinalThreads, "a thread per four columns, per part");
+static_assert(kMaxExperts / 4 / kFinalCtas <= kFinalThreads &&
+                  fwd_ctas(1) * kMostSms <= kFinalThreads,
+              "a thread per four columns, per part");
 
 template <int L, int NV, bool VEC>
 __global__ void __launch_bounds__(kBackThreads, back_ctas(NV))
@@ -478,11 +480,16 @@ cudaError_t with_shape(int E, bool vec, F&& f) {
 #undef SITU_SHAPE
 }
 
+// of the current device; without one, those that the sizes are asked for
+int sms() {
+  const int n = gg::sm_count();
+  return n < 1 ? 152 : n < kMostSms ? n : kMostSms;
+}
 // CTAs for T rows: `ctas` to an SM, `more` where E is short and a group would take more than `many` rows
 int grid_of(int T, int E, int threads, int ctas, int more, int many) {
   const int groups = threads / (E <= 128 ? 16 : E <= 1024 ? 32 : 128);
   const long rows = (T + groups - 1) / groups;
-  const long most = kSms * (E <= 256 && rows > (long)many * ctas * kSms ? more : ctas);
+  const long n = sms(), most = n * (E <= 256 && rows > many * ctas * n ? more : ctas);
   return (int)(rows < 1 ? 1 : rows > most ? most : rows);
 }
 // One CTA does the whole forward up to this many rows per group: a second

@@ -1,8 +1,11 @@
 """Refusals of the fine-tuning operators' entry points that came later (no GPU needed)."""
+import os
+import re
+
 import pytest
 import torch
 
-from block_scaled_fp4_permute_gb300 import binding as B
+from block_scaled_fp4_permute_gb300 import binding as B, build
 from test_finetune_abi import lib, lora_back  # noqa: F401
 
 
@@ -22,3 +25,13 @@ def test_constants_that_ask_for_a_gradient_are_refused():
         with torch.no_grad(), pytest.raises((TypeError, ValueError)) as e:   # goes on to the devices' check
             call()
         assert "gradient" not in str(e.value)
+
+
+def test_the_routers_grids_follow_the_devices_sm_count():
+    # a constant of 152 put a second wave on a GPU of 148
+    text = re.sub(r"//.*", "", open(os.path.join(build.CSRC, "balance.cu")).read())
+    assert "sm_count()" in text and not re.search(r"kSms\s*=", text)
+
+
+def test_the_router_needs_a_workspace_without_a_device_too(lib):  # noqa: F811
+    assert lib.situ_moe_balance_loss_workspace_size(65536, 896) >= 152 * (2 * 896 + 1) * 4
