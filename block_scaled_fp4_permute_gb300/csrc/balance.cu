@@ -264,7 +264,8 @@ struct Sum {
 
 // Joins `parts` CTAs' sums: one cluster of CTAS, a share of the columns per CTA,
 // four columns a thread, their parts in up to 32 slices; the loss's terms meet in
-// CTA 0.  One CTA where that is no more than 256 KB to read.
+// CTA 0.  One CTA where that is no more than 256 KB to read, up to kJoinPitch columns.
+constexpr int kJoinPitch = 4 * kFinalThreads;
 template <int CTAS>
 __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kFinalThreads)
 balance_join_kernel(BalanceParams p, int parts) {
@@ -280,7 +281,7 @@ balance_join_kernel(BalanceParams p, int parts) {
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = CTAS > 1 ? (int)cluster.block_rank() : 0;
   const int quads = p.pitch / 4, cols = (quads + CTAS - 1) / CTAS, c0 = rank * cols, width = max(0, min(cols, quads - c0));
-  const int slices = min(32, kFinalThreads / cols);      // cols <= 128
+  const int slices = min(32, kFinalThreads / cols);      // at least one: cols <= kFinalThreads
   const int c = threadIdx.x % cols, s = threadIdx.x / cols;
   Sum a[4];
   int n[4] = {0, 0, 0, 0};
@@ -344,7 +345,7 @@ balance_join_kernel(BalanceParams p, int parts) {
     *p.loss = tok > 0 ? (float)((double)p.coef * p.E * t / (tok * tok * p.k)) : 0.f;
   }
 }
-static_assert(kMaxExperts / 4 / kFinalCtas <= kFinalThreads &&
+static_assert(kMaxExperts / 4 / kFinalCtas <= kFinalThreads && kJoinPitch / 4 <= kFinalThreads &&
                   fwd_ctas(1) * kMostSms <= kFinalThreads,
               "a thread per four columns, per part");
 
@@ -547,7 +548,7 @@ extern "C" situ_status situ_moe_balance_loss(const situ_balance_args* a, void* w
   p.part_c = reinterpret_cast<int32_t*>(p.part_p + (size_t)grid * p.pitch);
   p.part_n = p.part_c + (size_t)grid * p.pitch;
   auto join = [&](int parts) {
-    return (size_t)parts * p.pitch * 8 <= 256 * 1024 && p.pitch <= 4 * kFinalThreads
+    return (size_t)parts * p.pitch * 8 <= 256 * 1024 && p.pitch <= kJoinPitch
                ? launch_pdl(balance_join_kernel<1>, dim3(1), dim3(kFinalThreads), 0, st, p, parts)
                : launch_pdl(balance_join_kernel<kFinalCtas>, dim3(kFinalCtas), dim3(kFinalThreads), 0, st, p, parts);
   };
