@@ -302,3 +302,32 @@ def test_a_capture_beside_nodes_kept_from_a_side_stream():
     for _ in range(2):
         graph.replay()
     assert torch.equal(a.grad, 2 * want[0]) and torch.equal(b.grad, 2 * want[1]) and len(kept) == 2
+
+
+def test_a_captured_step_of_f16_adapters_beside_an_fp32_base():
+    g = gen(33)
+    S, K, N, r = 200, 72, 64, 8
+    x, base, dy = normal(g, S, K, dtype=F16), normal(g, S, N, dtype=F32), normal(g, S, N, std=1e-9, dtype=F32)
+    a, b = normal(g, 2, r, K, dtype=F16).requires_grad_(), normal(g, 2, N, r, std=100.0, dtype=F16).requires_grad_()
+    off = offsets_of([120, 80])
+
+    def run():
+        return torch.autograd.grad(B.lora_linear(base, x, a, b, off), (a, b), dy)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run()
+    for size in (1e-6, 1e3, 0.0):
+        dy.copy_(normal(g, S, N, std=size, dtype=F32))
+        graph.replay()
+        want = run()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        # dB has a deviation of size 72^0.5 120^0.5 = 93 size: at 1e3 many of its elements are beyond f16
+        true = torch.stack([dy[q].double().T @ (x[q].double() @ a[e].double().T) for e, q in ((0, slice(0, 120)), (1, slice(120, 200)))])
+        assert torch.isfinite(got[1][true.abs() < 6e4]).all() and (got[1].abs().max() > 0) == (size > 0)
