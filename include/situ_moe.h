@@ -748,7 +748,9 @@ situ_status situ_moe_gated_backward(const situ_gated_args* args, void* stream);
  * type, the first u rounded, the second what that leaves (zeros without an
  * adapter; as far as that type's range goes), which the gradients take.  What is
  * written overlaps no other operand.  For experts, an adapter per (request's
- * adapter, expert) pair is one of n, its rows in any order.
+ * adapter, expert) pair is one of n, its rows in any order; of more than
+ * SITU_MAX_LOCAL_EXPERTS adapters rows are not sorted here, and take a pass of a
+ * tile for each adapter in it, so that rows in runs are much faster.
  * Results do not depend on the order of execution, nor on what other rows'
  * adapters hold.  K, N multiples of 8, rows strided by multiples of 8 elements
  * (fp32: 4), pointers 16-byte aligned, ids, offsets, scale 4.
