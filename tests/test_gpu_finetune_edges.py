@@ -28,7 +28,8 @@ def gradients(dy, x, a, b, counts, scale):
         rows = slice(at, at + n)
         at += n
         f, ae, be, xe, de = scale[e].double(), a[e].double(), b[e].double(), x[rows].double(), dy[rows].double()
-        yield e, (f * (de @ be), f * (de.abs() @ be.abs()), xe), (f * (xe @ ae.T), f * (xe.abs() @ ae.abs().T), de)
+        yield (e, (f * (de @ be), f.abs() * (de.abs() @ be.abs()), xe),
+               (f * (xe @ ae.T), f.abs() * (xe.abs() @ ae.abs().T), de))
 
 
 # A sum p^T t over L rows: p itself a sum of C terms (2 (C + 40) U of their magnitudes), taken in two terms of f16 under
